@@ -6,4 +6,4 @@ a C ABI declared in ``include/ssdc.h``). ``ssdc`` is the thin ctypes binding;
 nothing: the library is opened on first use, and a missing library is an error.
 """
 
-__all__ = ["inputs", "ssdc"]
+__all__ = ["block", "inputs", "ssdc"]

@@ -33,7 +33,7 @@ def _stale(lib, srcs):
         return True
     t = os.path.getmtime(lib)
     deps = srcs + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-    deps.append(os.path.join(HERE, "..", "include", "ssdc.h"))
+    deps += glob.glob(os.path.join(HERE, "..", "include", "*.h"))
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 

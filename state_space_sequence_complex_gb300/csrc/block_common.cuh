@@ -1,0 +1,57 @@
+// Device helpers of the operators around the scan: element types, gates, e4m3.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+namespace ssdc {
+namespace block {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// s = sigmoid(z) and r = sigmoid(-z) = 1 - s from one exponential and one reciprocal:
+// with e = exp(-|z|) in (0, 1], sigmoid(|z|) = 1 / (1 + e) and sigmoid(-|z|) = e / (1 + e),
+// so neither loses digits where the other is near one. The fast exponential's relative
+// error, about |z| 1e-7, is the largest here.
+__device__ __forceinline__ void sigmoid_pair(float z, float& s, float& r) {
+    const float e = __expf(-fabsf(z));
+    const float inv = __fdividef(1.0f, 1.0f + e);
+    const float small = e * inv;
+    s = z >= 0.0f ? inv : small;
+    r = z >= 0.0f ? small : inv;
+    if (z != z) s = r = z;
+}
+
+// The scale of a group and an element's e4m3 value. Both divisions are the rounded ones:
+// an element that lies midway between two e4m3 values must round as x / scale does.
+__device__ __forceinline__ float group_scale(float amax) { return fmaxf(amax, 7.88860905e-31f /* 2^-100 */) / 448.0f; }
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint8_t e4m3(float v) { return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
+
+template <int kWidth = 32>
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = kWidth / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <int kWidth = 32>
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = kWidth / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+}  // namespace block
+}  // namespace ssdc

@@ -1,0 +1,390 @@
+// Host side of the C ABI declared in include/ssdc_block.h: argument checks, then one
+// launch sequence per call on the caller's stream. Nothing is allocated.
+#include <atomic>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "block_kernels.h"
+#include "ssdc_kernels.h"
+
+namespace {
+
+using namespace ssdc::block;
+
+constexpr int64_t kBig = int64_t(1) << 40;  // most elements of one array
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_device_ok[kMaxDevices];
+
+int check_device() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SSDC_ERR_CUDA;
+    if (g_device_ok[dev].load(std::memory_order_acquire)) return SSDC_OK;
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+        return SSDC_ERR_CUDA;
+    if (major != 10 || minor != 3) return SSDC_ERR_DEVICE;
+    g_device_ok[dev].store(1, std::memory_order_release);
+    return SSDC_OK;
+}
+
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+size_t type_bytes(int type) { return type == SSD_TYPE_F32 ? 4 : type == SSD_TYPE_BF16 ? 2 : 1; }
+
+// A three-level array: `outer` rows of `mid` rows of `inner` contiguous elements. Dense
+// arrays and rows are special cases. lo, hi: the bytes it spans.
+struct Array {
+    const void* p;
+    int64_t outer, mid, inner, s_outer, s_mid;
+    size_t elem;
+    uintptr_t lo() const { return reinterpret_cast<uintptr_t>(p); }
+    uintptr_t hi() const {
+        return lo() + (uintptr_t)((outer - 1) * s_outer + (mid - 1) * s_mid + inner) * elem;
+    }
+    bool operator==(const Array& o) const {
+        return p == o.p && s_outer == o.s_outer && s_mid == o.s_mid && elem == o.elem;
+    }
+};
+
+Array seq(const void* p, int64_t sb, int64_t st, const ssd_gated_dims& d) {
+    return Array{p, d.B, d.T, d.D, sb, st, type_bytes(d.type)};
+}
+Array rows(const void* p, int64_t ld, int64_t M, int64_t D, size_t elem) { return Array{p, 1, M, D, 0, ld, elem}; }
+Array dense(const void* p, int64_t n, size_t elem = 4) { return Array{p, 1, 1, n, 0, 0, elem}; }
+
+// Whether two arrays may share a byte. Arrays whose spans meet are still apart where they
+// have the same strides and element size and their columns are apart in every row (slices
+// of one wider array).
+bool overlaps(const Array& a, const Array& b) {
+    if (a.p == nullptr || b.p == nullptr || a.hi() <= b.lo() || b.hi() <= a.lo()) return false;
+    if (a.elem != b.elem || a.s_mid != b.s_mid || (a.s_outer != b.s_outer && a.outer > 1)) return true;
+    // the stride that separates the rows; every other stride is a multiple of it
+    int64_t step = a.mid > 1 ? a.s_mid : 0;
+    if (a.outer > 1 && (step == 0 || a.s_outer < step)) step = a.s_outer;
+    if (step <= 0 || (a.mid > 1 && a.s_mid % step) || (a.outer > 1 && a.s_outer % step)) return true;
+    const uintptr_t d = a.lo() > b.lo() ? a.lo() - b.lo() : b.lo() - a.lo();
+    const bool a_after = a.lo() > b.lo();
+    if (d % a.elem) return true;
+    const int64_t off = (int64_t)(d / a.elem) % step;  // where the later one's columns start in the earlier's rows
+    const int64_t first = a_after ? b.inner : a.inner, second = a_after ? a.inner : b.inner;
+    return !(off >= first && off + second <= step);
+}
+
+// An output's rows must be apart from each other.
+bool self_apart(const Array& a) {
+    const bool m = a.mid > 1, o = a.outer > 1;
+    if (m && a.s_mid < a.inner) return false;
+    if (o && a.s_outer < a.inner) return false;
+    if (!m || !o) return true;
+    return a.s_outer >= (a.mid - 1) * a.s_mid + a.inner || a.s_mid >= (a.outer - 1) * a.s_outer + a.inner;
+}
+
+bool in_range(const Array& a) {
+    return a.s_outer >= 0 && a.s_mid >= 0 && a.s_outer <= kBig && a.s_mid <= kBig &&
+           (double)(a.outer - 1) * (double)a.s_outer + (double)(a.mid - 1) * (double)a.s_mid + (double)a.inner <=
+               (double)kBig;
+}
+
+// Inputs, outputs and the pairs that may be one array (an output updated in place).
+struct Args {
+    Array in[10], out[6];
+    int n_in = 0, n_out = 0;
+    int rc = SSDC_OK;
+    void fail(int code) {
+        if (rc == SSDC_OK) rc = code;
+    }
+    void check(const Array& a) {
+        if (!in_range(a)) return fail(SSDC_ERR_INVALID);
+        if (!aligned_to(a.p, a.elem)) fail(SSDC_ERR_ALIGN);
+    }
+    void input(const Array& a, bool needed = true) {
+        if (a.p == nullptr) {
+            if (needed) fail(SSDC_ERR_INVALID);
+            return;
+        }
+        check(a);
+        in[n_in++] = a;
+    }
+    // same: an input that this output may be
+    void output(const Array& a, bool needed = true, const void* same1 = nullptr, const void* same2 = nullptr) {
+        if (a.p == nullptr) {
+            if (needed) fail(SSDC_ERR_INVALID);
+            return;
+        }
+        check(a);
+        if (rc != SSDC_OK) return;
+        if (!self_apart(a)) return fail(SSDC_ERR_INVALID);
+        for (int k = 0; k < n_in; ++k) {
+            const bool same = (same1 != nullptr && in[k].p == same1) || (same2 != nullptr && in[k].p == same2);
+            if (!(same && in[k] == a) && overlaps(a, in[k])) return fail(SSDC_ERR_INVALID);
+        }
+        for (int k = 0; k < n_out; ++k)
+            if (overlaps(a, out[k])) return fail(SSDC_ERR_INVALID);
+        out[n_out++] = a;
+    }
+};
+
+int check_gated(const ssd_gated_dims& d) {
+    if (d.B <= 0 || d.T <= 0 || d.D <= 0) return SSDC_ERR_INVALID;
+    if (d.type != SSD_TYPE_F32 && d.type != SSD_TYPE_BF16) return SSDC_ERR_INVALID;
+    if (d.B > INT32_MAX || d.D > INT32_MAX || d.B > INT32_MAX / d.D || d.T > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
+    if ((double)d.B * (double)d.T * (double)d.D > (double)kBig) return SSDC_ERR_UNSUPPORTED;
+    return SSDC_OK;
+}
+
+int64_t state_rows(const ssd_gated_dims& d) {
+    return (d.T + SSD_GATED_STATE_TOKENS - 1) / SSD_GATED_STATE_TOKENS;
+}
+
+int done(int launches) {
+    if (launches < 0) return launches;
+    if (cudaGetLastError() != cudaSuccess) return SSDC_ERR_CUDA;
+    ssdc::set_last_launch_count(launches);
+    return SSDC_OK;
+}
+
+Gated gated_problem(const ssd_seq_in& x, const ssd_seq_in& f, const ssd_seq_in& i, const ssd_gated_dims& d) {
+    Gated p = {};
+    p.x = x.p; p.x_b = x.stride_b; p.x_t = x.stride_t;
+    p.f = f.p; p.f_b = f.stride_b; p.f_t = f.stride_t;
+    p.i = i.p; p.i_b = i.stride_b; p.i_t = i.stride_t;
+    p.T = d.T; p.B = (int)d.B; p.D = (int)d.D;
+    p.bf16 = d.type == SSD_TYPE_BF16;
+    return p;
+}
+
+int check_rows(int64_t M, int64_t D, int type) {
+    if (M <= 0 || D <= 0) return SSDC_ERR_INVALID;
+    if (type != SSD_TYPE_F32 && type != SSD_TYPE_BF16) return SSDC_ERR_INVALID;
+    if (D > 32768 || M > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
+    return SSDC_OK;
+}
+
+int64_t groups(int64_t n) { return (n + SSD_FP8_GROUP - 1) / SSD_FP8_GROUP; }
+
+// A row of 8-bit values: a whole number of 16-byte units, as the copies into shared memory need.
+int check_fp8_rows(const void* p, int64_t ld, int64_t cols) {
+    if (p == nullptr) return SSDC_OK;
+    if (ld < cols) return SSDC_ERR_INVALID;
+    if (ld % 16 != 0 || !aligned_to(p, 16)) return SSDC_ERR_ALIGN;
+    return SSDC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssd_gated_scan_states_bytes(ssd_gated_dims dims) {
+    if (check_gated(dims) != SSDC_OK) return 0;
+    return (size_t)(dims.B * state_rows(dims) * dims.D) * sizeof(float);
+}
+
+int ssd_gated_scan_fwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* h0, const uint8_t* reset,
+                       ssd_gated_dims d, ssd_seq_out h, float* h_last, float* states, cudaStream_t stream) {
+    int rc = check_gated(d);
+    if (rc != SSDC_OK) return rc;
+    Args a;
+    a.input(seq(x.p, x.stride_b, x.stride_t, d));
+    a.input(seq(f.p, f.stride_b, f.stride_t, d));
+    a.input(seq(i.p, i.stride_b, i.stride_t, d), false);
+    a.input(dense(h0, d.B * d.D), false);
+    a.input(dense(reset, d.B * d.T, 1), false);
+    a.output(seq(h.p, h.stride_b, h.stride_t, d));
+    a.output(dense(h_last, d.B * d.D), true, h0);
+    a.output(dense(states, d.B * state_rows(d) * d.D), false);
+    if (a.rc != SSDC_OK) return a.rc;
+    rc = check_device();
+    if (rc != SSDC_OK) return rc;
+    Gated p = gated_problem(x, f, i, d);
+    p.h0 = h0; p.reset = reset;
+    p.h = h.p; p.h_b = h.stride_b; p.h_t = h.stride_t;
+    p.h_last = h_last; p.states = states;
+    (void)cudaGetLastError();
+    return done(gated_fwd_launch(p, stream));
+}
+
+int ssd_gated_scan_step(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* state_in, int64_t B, int64_t D,
+                        int32_t type, ssd_seq_out h, float* state_out, cudaStream_t stream) {
+    const ssd_gated_dims d = {B, 1, D, type};
+    int rc = check_gated(d);
+    if (rc != SSDC_OK) return rc;
+    Args a;
+    a.input(seq(x.p, x.stride_b, 0, d));
+    a.input(seq(f.p, f.stride_b, 0, d));
+    a.input(seq(i.p, i.stride_b, 0, d), false);
+    a.input(dense(state_in, B * D));
+    a.output(seq(h.p, h.stride_b, 0, d));
+    a.output(dense(state_out, B * D), true, state_in);
+    if (a.rc != SSDC_OK) return a.rc;
+    rc = check_device();
+    if (rc != SSDC_OK) return rc;
+    Gated p = gated_problem(x, f, i, d);
+    p.h0 = state_in; p.h = h.p; p.h_b = h.stride_b; p.h_last = state_out;
+    (void)cudaGetLastError();
+    return done(gated_step_launch(p, stream));
+}
+
+int ssd_gated_scan_bwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* states, const uint8_t* reset,
+                       ssd_seq_in dh, const float* dh_last, ssd_gated_dims d, ssd_seq_out dx, ssd_seq_out df,
+                       ssd_seq_out di, float* dh0, cudaStream_t stream) {
+    int rc = check_gated(d);
+    if (rc != SSDC_OK) return rc;
+    if ((i.p == nullptr) != (di.p == nullptr)) return SSDC_ERR_INVALID;
+    Args a;
+    a.input(seq(x.p, x.stride_b, x.stride_t, d));
+    a.input(seq(f.p, f.stride_b, f.stride_t, d));
+    a.input(seq(i.p, i.stride_b, i.stride_t, d), false);
+    a.input(dense(states, d.B * state_rows(d) * d.D));
+    a.input(dense(reset, d.B * d.T, 1), false);
+    a.input(seq(dh.p, dh.stride_b, dh.stride_t, d));
+    a.input(dense(dh_last, d.B * d.D), false);
+    a.output(seq(dx.p, dx.stride_b, dx.stride_t, d));
+    a.output(seq(df.p, df.stride_b, df.stride_t, d));
+    a.output(seq(di.p, di.stride_b, di.stride_t, d), false);
+    a.output(dense(dh0, d.B * d.D), false, dh_last);
+    if (a.rc != SSDC_OK) return a.rc;
+    rc = check_device();
+    if (rc != SSDC_OK) return rc;
+    Gated p = gated_problem(x, f, i, d);
+    p.in_states = states; p.reset = reset;
+    p.dh = dh.p; p.dh_b = dh.stride_b; p.dh_t = dh.stride_t; p.dh_last = dh_last;
+    p.dx = dx.p; p.dx_b = dx.stride_b; p.dx_t = dx.stride_t;
+    p.df = df.p; p.df_b = df.stride_b; p.df_t = df.stride_t;
+    p.di = di.p; p.di_b = di.stride_b; p.di_t = di.stride_t;
+    p.dh0 = dh0;
+    (void)cudaGetLastError();
+    return done(gated_bwd_launch(p, stream));
+}
+
+int ssd_residual_norm_fwd(ssd_rows_in x, ssd_rows_in residual, const float* w, float eps, int64_t M, int64_t D,
+                          int32_t type, ssd_rows_out r, int32_t out_type, ssd_rows_out y, float* scale, float* rstd,
+                          cudaStream_t stream) {
+    int rc = check_rows(M, D, type);
+    if (rc != SSDC_OK) return rc;
+    if (out_type != SSD_TYPE_F32 && out_type != SSD_TYPE_BF16 && out_type != SSD_TYPE_E4M3) return SSDC_ERR_INVALID;
+    if (!(eps >= 0.0f)) return SSDC_ERR_INVALID;
+    const bool fp8 = out_type == SSD_TYPE_E4M3;
+    if (fp8 != (scale != nullptr)) return SSDC_ERR_INVALID;
+    if (fp8 && (rc = check_fp8_rows(y.p, y.ld, D)) != SSDC_OK) return rc;
+    Args a;
+    a.input(rows(x.p, x.ld, M, D, type_bytes(type)));
+    a.input(rows(residual.p, residual.ld, M, D, type_bytes(type)), false);
+    a.input(dense(w, D), false);
+    a.output(rows(r.p, r.ld, M, D, type_bytes(type)), false, x.p, residual.p);
+    a.output(rows(y.p, y.ld, M, D, type_bytes(out_type)));
+    a.output(dense(scale, M * groups(D)), fp8);
+    a.output(dense(rstd, M), false);
+    if (a.rc != SSDC_OK) return a.rc;
+    rc = check_device();
+    if (rc != SSDC_OK) return rc;
+    Norm p = {};
+    p.x = x.p; p.x_ld = x.ld; p.res = residual.p; p.res_ld = residual.ld;
+    p.w = w; p.eps = eps; p.M = M; p.D = (int)D; p.bf16 = type == SSD_TYPE_BF16;
+    p.r = r.p; p.r_ld = r.ld; p.out_type = out_type; p.y = y.p; p.y_ld = y.ld;
+    p.scale = scale; p.rstd = rstd;
+    (void)cudaGetLastError();
+    return done(norm_fwd_launch(p, stream));
+}
+
+size_t ssd_residual_norm_bwd_workspace_bytes(int64_t M, int64_t D) {
+    if (check_rows(M, D, SSD_TYPE_F32) != SSDC_OK) return 0;
+    return (size_t)norm_bwd_parts(M, D) * (size_t)D * sizeof(float);
+}
+
+int ssd_residual_norm_bwd(ssd_rows_in dy, ssd_rows_in dr, ssd_rows_in r, const float* w, const float* rstd, int64_t M,
+                          int64_t D, int32_t type, ssd_rows_out dx, float* dw, void* workspace, size_t ws_bytes,
+                          cudaStream_t stream) {
+    int rc = check_rows(M, D, type);
+    if (rc != SSDC_OK) return rc;
+    const size_t e = type_bytes(type), need = ssd_residual_norm_bwd_workspace_bytes(M, D);
+    if (dw != nullptr && (workspace == nullptr || !aligned_to(workspace, 256) || ws_bytes < need))
+        return SSDC_ERR_WORKSPACE;
+    Args a;
+    a.input(rows(dy.p, dy.ld, M, D, e));
+    a.input(rows(dr.p, dr.ld, M, D, e), false);
+    a.input(rows(r.p, r.ld, M, D, e));
+    a.input(dense(w, D), false);
+    a.input(dense(rstd, M));
+    a.output(rows(dx.p, dx.ld, M, D, e), true, dy.p, dr.p);
+    a.output(dense(dw, D), false);
+    if (dw != nullptr) a.output(dense(workspace, (int64_t)(need / 4)));
+    if (a.rc != SSDC_OK) return a.rc;
+    rc = check_device();
+    if (rc != SSDC_OK) return rc;
+    NormBwd p = {};
+    p.dy = dy.p; p.dy_ld = dy.ld; p.dr = dr.p; p.dr_ld = dr.ld; p.r = r.p; p.r_ld = r.ld;
+    p.w = w; p.rstd = rstd; p.M = M; p.D = (int)D; p.bf16 = type == SSD_TYPE_BF16;
+    p.dx = dx.p; p.dx_ld = dx.ld; p.dw = dw; p.partial = static_cast<float*>(workspace);
+    (void)cudaGetLastError();
+    return done(norm_bwd_launch(p, stream));
+}
+
+int ssd_fp8_quantize(ssd_rows_in x, int64_t M, int64_t K, int32_t type, int32_t scales, ssd_rows_out q, float* scale,
+                     ssd_rows_out qt, float* scale_t, cudaStream_t stream) {
+    if (M <= 0 || K <= 0) return SSDC_ERR_INVALID;
+    if (type != SSD_TYPE_F32 && type != SSD_TYPE_BF16) return SSDC_ERR_INVALID;
+    if (scales != SSD_SCALE_ROWS && scales != SSD_SCALE_BLOCKS) return SSDC_ERR_INVALID;
+    if (M > INT32_MAX - 128 || K > INT32_MAX - 128) return SSDC_ERR_UNSUPPORTED;
+    if (q.p == nullptr && qt.p == nullptr) return SSDC_ERR_INVALID;
+    if ((q.p == nullptr) != (scale == nullptr) || (qt.p == nullptr) != (scale_t == nullptr)) return SSDC_ERR_INVALID;
+    int rc;
+    if ((rc = check_fp8_rows(q.p, q.ld, K)) != SSDC_OK || (rc = check_fp8_rows(qt.p, qt.ld, M)) != SSDC_OK) return rc;
+    const bool blocks = scales == SSD_SCALE_BLOCKS;
+    Args a;
+    a.input(rows(x.p, x.ld, M, K, type_bytes(type)));
+    a.output(rows(q.p, q.ld, M, K, 1), false);
+    a.output(dense(scale, blocks ? groups(M) * groups(K) : M * groups(K)), false);
+    a.output(rows(qt.p, qt.ld, K, M, 1), false);
+    a.output(dense(scale_t, blocks ? groups(M) * groups(K) : K * groups(M)), false);
+    if (a.rc != SSDC_OK) return a.rc;
+    rc = check_device();
+    if (rc != SSDC_OK) return rc;
+    Quant p = {};
+    p.x = x.p; p.x_ld = x.ld; p.M = M; p.K = K; p.bf16 = type == SSD_TYPE_BF16; p.blocks = blocks;
+    p.q = static_cast<uint8_t*>(q.p); p.q_ld = q.ld; p.scale = scale;
+    p.qt = static_cast<uint8_t*>(qt.p); p.qt_ld = qt.ld; p.scale_t = scale_t;
+    (void)cudaGetLastError();
+    return done(quantize_launch(p, stream));
+}
+
+size_t ssd_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0 || K <= 0 || M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256) return 0;
+    return matmul_workspace(M, N, K);
+}
+
+int ssd_fp8_matmul(ssd_rows_in a8, const float* a_scale, ssd_rows_in b8, const float* b_scale, int32_t b_scales,
+                   int64_t M, int64_t N, int64_t K, int32_t out_type, ssd_rows_out c, void* workspace,
+                   size_t ws_bytes, cudaStream_t stream) {
+    if (M <= 0 || N <= 0 || K <= 0) return SSDC_ERR_INVALID;
+    if (out_type != SSD_TYPE_F32 && out_type != SSD_TYPE_BF16) return SSDC_ERR_INVALID;
+    if (b_scales != SSD_SCALE_ROWS && b_scales != SSD_SCALE_BLOCKS) return SSDC_ERR_INVALID;
+    if (M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256) return SSDC_ERR_UNSUPPORTED;
+    int rc;
+    if ((rc = check_fp8_rows(a8.p, a8.ld, K)) != SSDC_OK || (rc = check_fp8_rows(b8.p, b8.ld, K)) != SSDC_OK) return rc;
+    const size_t need = matmul_workspace(M, N, K);
+    if (workspace == nullptr || !aligned_to(workspace, 256) || ws_bytes < need) return SSDC_ERR_WORKSPACE;
+    const bool blocks = b_scales == SSD_SCALE_BLOCKS;
+    Args a;
+    a.input(rows(a8.p, a8.ld, M, K, 1));
+    a.input(dense(a_scale, M * groups(K)));
+    a.input(rows(b8.p, b8.ld, N, K, 1));
+    a.input(dense(b_scale, blocks ? groups(N) * groups(K) : N * groups(K)));
+    a.output(rows(c.p, c.ld, M, N, type_bytes(out_type)));
+    a.output(dense(workspace, (int64_t)(need / 4)));
+    if (a.rc != SSDC_OK) return a.rc;
+    rc = check_device();
+    if (rc != SSDC_OK) return rc;
+    Matmul p = {};
+    p.a = static_cast<const uint8_t*>(a8.p); p.a_ld = a8.ld; p.a_scale = a_scale;
+    p.b = static_cast<const uint8_t*>(b8.p); p.b_ld = b8.ld; p.b_scale = b_scale; p.b_blocks = blocks;
+    p.M = M; p.N = N; p.K = K; p.out_bf16 = out_type == SSD_TYPE_BF16;
+    p.c = c.p; p.c_ld = c.ld;
+    p.status = static_cast<int*>(workspace);
+    p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
+    (void)cudaGetLastError();
+    return done(matmul_launch(p, stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,192 @@
+"""Host-only checks of the operators around the scan: the symbols that the header
+declares, and the arguments that each entry point refuses before anything reaches a
+GPU. Every call here fails a host check, so the addresses are never used."""
+import os
+import re
+
+import pytest
+
+from state_space_sequence_complex_gb300 import block, ssdc
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INVALID, UNSUPPORTED, ALIGN, WORKSPACE = (ssdc.SSDC_ERR_INVALID, ssdc.SSDC_ERR_UNSUPPORTED, ssdc.SSDC_ERR_ALIGN,
+                                          ssdc.SSDC_ERR_WORKSPACE)
+BASE = 1 << 40
+
+
+def at(k):
+    """Addresses 64 GB apart."""
+    return BASE + (k << 36)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from state_space_sequence_complex_gb300 import build
+    build.build()
+    return block.load()
+
+
+def test_exports_every_declared_symbol(lib):
+    text = open(os.path.join(ROOT, "include", "ssdc_block.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = sorted(set(re.findall(r"\b(ssd_\w+)\s*\(", text)))
+    assert sorted(block.EXPORTS) == names
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+SEQ = lambda p, sb=6400, st=64: block.ssd_seq(p, sb, st)
+NONE = block.ssd_seq(None, 0, 0)
+
+
+def fwd(lib, **k):
+    a = dict(x=SEQ(at(1)), f=SEQ(at(2)), i=SEQ(at(3)), h0=at(4), reset=at(5), dims=(2, 100, 64, 1), h=SEQ(at(6)),
+             h_last=at(7), states=at(8))
+    a.update(k)
+    return lib.ssd_gated_scan_fwd(a["x"], a["f"], a["i"], a["h0"], a["reset"], block.ssd_gated_dims(*a["dims"]), a["h"],
+                                  a["h_last"], a["states"], None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(dims=(0, 100, 64, 1)), INVALID), (dict(dims=(2, 0, 64, 1)), INVALID), (dict(dims=(2, 100, -1, 1)), INVALID),
+    (dict(dims=(2, 100, 64, 2)), INVALID), (dict(dims=(2, 100, 64, 7)), INVALID),
+    (dict(dims=(1 << 31, 100, 64, 1)), UNSUPPORTED), (dict(dims=(1 << 20, 1, 1 << 20, 1)), UNSUPPORTED),
+    (dict(x=NONE), INVALID), (dict(f=NONE), INVALID), (dict(h=NONE), INVALID), (dict(h_last=None), INVALID),
+    (dict(x=SEQ(at(1) + 1)), ALIGN), (dict(h=SEQ(at(6) + 1)), ALIGN), (dict(h0=at(4) + 2), ALIGN),
+    (dict(x=SEQ(at(1), -1)), INVALID), (dict(x=SEQ(at(1), 6400, -64)), INVALID),
+    (dict(x=SEQ(at(1), 1 << 50)), INVALID),
+    (dict(h=SEQ(at(1))), INVALID), (dict(h=SEQ(at(3) + 2)), INVALID),         # over an input
+    (dict(h=SEQ(at(6), 0)), INVALID), (dict(h=SEQ(at(6), 6400, 63)), INVALID),  # rows on top of each other
+    (dict(h=SEQ(at(6), 640, 64)), INVALID),
+    (dict(h_last=at(2)), INVALID), (dict(h_last=at(4) + 4), INVALID), (dict(states=at(6)), INVALID),
+    (dict(states=at(7)), INVALID),
+    # slices of one array, 192 wide: the output's columns reach into the gate's
+    (dict(x=SEQ(at(1), 19200, 192), f=SEQ(at(1) + 128, 19200, 192), h=SEQ(at(1) + 254, 19200, 192)), INVALID),
+    (dict(x=SEQ(at(1), 19200, 192), f=SEQ(at(1) + 128, 19200, 192), h=SEQ(at(1) + 258, 19200, 192)), INVALID),
+])
+def test_scan_refuses(lib, change, want):
+    assert fwd(lib, **change) == want
+
+
+def bwd(lib, **k):
+    a = dict(x=SEQ(at(1)), f=SEQ(at(2)), i=SEQ(at(3)), states=at(4), reset=None, dh=SEQ(at(5)), dh_last=at(6),
+             dx=SEQ(at(7)), df=SEQ(at(8)), di=SEQ(at(9)), dh0=at(10))
+    a.update(k)
+    return lib.ssd_gated_scan_bwd(a["x"], a["f"], a["i"], a["states"], a["reset"], a["dh"], a["dh_last"],
+                                  block.ssd_gated_dims(2, 100, 64, 1), a["dx"], a["df"], a["di"], a["dh0"], None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(states=None), dict(dh=NONE), dict(dx=NONE), dict(df=NONE), dict(di=NONE), dict(i=NONE),
+    dict(dx=SEQ(at(1))), dict(df=SEQ(at(5))), dict(df=SEQ(at(7))), dict(dh0=at(4)), dict(dh0=at(6) + 4)])
+def test_scan_backward_refuses(lib, change):
+    assert bwd(lib, **change) == INVALID
+
+
+@pytest.mark.parametrize("change", [dict(state=None), dict(out=None), dict(out=at(4) + 4), dict(h=at(1)), dict(B=0),
+                                    dict(D=0), dict(type=2)])
+def test_step_refuses(lib, change):
+    a = dict(state=at(4), out=at(5), h=at(6), B=8, D=64, type=1)
+    a.update(change)
+    assert lib.ssd_gated_scan_step(SEQ(at(1), 64, 0), SEQ(at(2), 64, 0), NONE, a["state"], a["B"], a["D"], a["type"],
+                                   SEQ(a["h"], 64, 0), a["out"], None) == INVALID
+
+
+ROWS = lambda p, ld=256: block.ssd_rows(p, ld)
+
+
+def norm(lib, **k):
+    a = dict(x=ROWS(at(1)), res=ROWS(at(2)), w=at(3), eps=1e-5, M=10, D=256, type=1, r=ROWS(at(4)), out=2, y=ROWS(at(5)),
+             scale=at(6), rstd=at(7))
+    a.update(k)
+    return lib.ssd_residual_norm_fwd(a["x"], a["res"], a["w"], a["eps"], a["M"], a["D"], a["type"], a["r"], a["out"],
+                                     a["y"], a["scale"], a["rstd"], None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(M=0), INVALID), (dict(D=0), INVALID), (dict(type=2), INVALID), (dict(out=3), INVALID),
+    (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(D=32769), UNSUPPORTED),
+    (dict(M=1 << 31), UNSUPPORTED), (dict(x=ROWS(None)), INVALID), (dict(y=ROWS(None)), INVALID),
+    (dict(scale=None), INVALID), (dict(out=1), INVALID),  # a scale exactly with 8 bits
+    (dict(y=ROWS(at(5), 255)), INVALID), (dict(y=ROWS(at(5), 264)), ALIGN), (dict(y=ROWS(at(5) + 8)), ALIGN),
+    (dict(r=ROWS(at(1), 512)), INVALID), (dict(r=ROWS(at(1) + 2)), INVALID), (dict(y=ROWS(at(2))), INVALID),
+    (dict(rstd=at(3)), INVALID), (dict(w=at(3) + 2), ALIGN), (dict(r=ROWS(at(4), 255)), INVALID)])
+def test_norm_refuses(lib, change, want):
+    assert norm(lib, **change) == want
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(dw=at(6), ws=None), WORKSPACE), (dict(ws=at(7) + 4), WORKSPACE), (dict(ws_bytes=16), WORKSPACE),
+    (dict(rstd=None), INVALID), (dict(r=ROWS(None)), INVALID), (dict(dx=ROWS(at(3))), INVALID),
+    (dict(dx=ROWS(at(1), 300)), INVALID), (dict(dw=at(4)), INVALID), (dict(dw=at(7)), INVALID)])
+def test_norm_backward_refuses(lib, change, want):
+    need = lib.ssd_residual_norm_bwd_workspace_bytes(10, 256)
+    assert need > 0 and lib.ssd_residual_norm_bwd_workspace_bytes(0, 256) == 0
+    a = dict(dy=ROWS(at(1)), dr=ROWS(at(2)), r=ROWS(at(3)), rstd=at(4), dx=ROWS(at(5)), dw=at(6), ws=at(7), ws_bytes=need)
+    a.update(change)
+    assert lib.ssd_residual_norm_bwd(a["dy"], a["dr"], a["r"], None, a["rstd"], 10, 256, 1, a["dx"], a["dw"], a["ws"],
+                                     a["ws_bytes"], None) == want
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(M=0), INVALID), (dict(scales=2), INVALID), (dict(type=2), INVALID), (dict(q=ROWS(None), qt=ROWS(None)), INVALID),
+    (dict(scale=None), INVALID), (dict(scale_t=None), INVALID), (dict(q=ROWS(at(2), 250)), INVALID),
+    (dict(q=ROWS(at(2), 260)), ALIGN), (dict(qt=ROWS(at(4) + 1, 16)), ALIGN), (dict(q=ROWS(at(1))), INVALID),
+    (dict(qt=ROWS(at(2), 16)), INVALID)])
+def test_quantize_refuses(lib, change, want):
+    a = dict(M=10, K=256, type=1, scales=0, q=ROWS(at(2)), scale=at(3), qt=ROWS(at(4), 16), scale_t=at(5))
+    a.update(change)
+    assert lib.ssd_fp8_quantize(ROWS(at(1)), a["M"], a["K"], a["type"], a["scales"], a["q"], a["scale"], a["qt"],
+                                a["scale_t"], None) == want
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(M=0), INVALID), (dict(N=0), INVALID), (dict(K=-5), INVALID), (dict(out=2), INVALID), (dict(scales=2), INVALID),
+    (dict(M=(1 << 31) - 2), UNSUPPORTED), (dict(a=ROWS(None)), INVALID), (dict(b_scale=None), INVALID),
+    (dict(a=ROWS(at(1), 200)), INVALID), (dict(a=ROWS(at(1), 264)), ALIGN), (dict(b=ROWS(at(3) + 8)), ALIGN),
+    (dict(c=ROWS(None)), INVALID), (dict(c=ROWS(at(5), 63)), INVALID), (dict(c=ROWS(at(1), 64)), INVALID),
+    (dict(c=ROWS(at(2), 64)), INVALID), (dict(c=ROWS(at(6), 64)), INVALID), (dict(ws=None), WORKSPACE),
+    (dict(ws=at(6) + 128), WORKSPACE), (dict(ws_bytes=0), WORKSPACE)])
+def test_product_refuses(lib, change, want):
+    a = dict(M=10, N=64, K=256, out=1, scales=1, a=ROWS(at(1)), a_scale=at(2), b=ROWS(at(3)), b_scale=at(4),
+             c=ROWS(at(5), 64), ws=at(6), ws_bytes=1 << 30)
+    a.update(change)
+    assert lib.ssd_fp8_matmul(a["a"], a["a_scale"], a["b"], a["b_scale"], a["scales"], a["M"], a["N"], a["K"], a["out"],
+                              a["c"], a["ws"], a["ws_bytes"], None) == want
+
+
+def test_plans_refuse(lib):
+    for make in (lambda: block.GatedScan(0, 4, 4, device="cpu"), lambda: block.GatedScan(1, 4, 4, "fp16", device="cpu"),
+                 lambda: block.ResidualNorm(4, 4, out="int8", device="cpu"),
+                 lambda: block.Fp8Product(4, 4, 4, b_scales="columns", device="cpu"),
+                 lambda: block.Fp8Quantize(4, 4, direct=False, device="cpu"),
+                 lambda: block.GatedScanStep(1, -2, device="cpu")):
+        with pytest.raises(ValueError):
+            make()
+    with pytest.raises(ssdc.SSDCError):
+        block.ResidualNorm(4, 40000, device="cpu")
+
+
+def test_calls_check_their_tensors(lib):
+    import torch
+    scan = block.GatedScan(2, 3, 4, device="cpu")
+    t = torch.zeros(2, 3, 4, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="input gate"):
+        scan(t, t)
+    with pytest.raises(TypeError, match="x must be"):
+        scan(t.float(), t, t)
+    with pytest.raises(ValueError, match="shape"):
+        scan(t, t[:, :2], t)
+    with pytest.raises(ValueError, match="contiguous channels"):
+        scan(t, t, torch.zeros(2, 4, 3, dtype=torch.bfloat16).transpose(1, 2))
+    with pytest.raises(ValueError, match="h0 must be contiguous"):
+        scan(t, t, t, h0=torch.zeros(2, 8)[:, ::2])
+    with pytest.raises(TypeError, match="reset"):
+        scan(t, t, t, reset=torch.zeros(2, 3))
+    product = block.Fp8Product(4, 8, 16, device="cpu")
+    q = torch.zeros(4, 16, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    with pytest.raises(ValueError, match="a_scale"):
+        product(q, torch.zeros(4, 1), q, torch.zeros(1, 1))
+    norm = block.ResidualNorm(4, 16, device="cpu")
+    with pytest.raises(ValueError, match="w must have"):
+        norm(torch.zeros(4, 16, dtype=torch.bfloat16), None, torch.zeros(15))
