@@ -9,8 +9,8 @@
 // A pair of CTAs works on a tile of 256 rows x BN columns (cta_group::2): each CTA
 // stages half of A's rows and half of B's, which halves the operand bytes an SM takes in
 // for its part of the product. Roles: warp 0 loads (TMA, a ring of stages of one group),
-// warps 1 and 2 of the even CTA issue the MMAs of every other group, warps 4 .. 19 scale, add and store; each of
-// those owns 32 rows x BN / 4 columns in registers, and takes registers that the first
+// warps 1 and 2 of the even CTA issue the MMAs of every other group, warp 3 fetches the
+// scales, warps 4 .. 19 scale, add and store; each of those owns 32 rows x BN / 4 columns in registers, and takes registers that the first
 // four warps give up. (The issue of an MMA returns shortly before it is done, so a single
 // issuer's waits between two groups left the tensor cores idle for as long as they worked.)
 #include <cuda.h>
@@ -29,8 +29,8 @@ namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;  // wait limit
 constexpr int kAddWarps = 16, kThreads = 128 + 32 * kAddWarps;
-// Registers a thread: 96 x 640 = 61440 at launch = 32 x 128 + 112 x 512 after the split
-constexpr int kCtlRegs = 32, kAddRegs = 112;
+// Registers a thread: 96 x 640 = 61440 at launch, 56 x 128 + 104 x 512 = 60416 after the split
+constexpr int kCtlRegs = 56, kAddRegs = 104;
 constexpr int kGroup = SSD_FP8_GROUP;
 
 struct Product {
@@ -56,19 +56,21 @@ template <int BN>
 struct Shape {
     static constexpr uint32_t kA = 128 * kGroup, kB = BN / 2 * kGroup, kStage = kA + kB;
     static constexpr int kCols = BN / 4;  // columns of one warp
-    // per adding warp: its columns' scales of two groups, and 32 rows of 32 values of C, a
-    // bank apart, for rows of C that start unaligned
-    static constexpr uint32_t kScales = 2 * kCols * 4, kPitch = 33 * 4, kOut = 32 * kPitch;
-    static constexpr uint32_t kWarp = kScales + kOut;
+    // Scales, a ring of groups: 128 rows' for each of B's two blocks (already multiplied), or 128
+    // rows' and then the columns'
+    static constexpr int kRing = 8, kSlot = 128 + 256;
+    static constexpr uint32_t kScales = kRing * kSlot * 4;
+    // per adding warp: 32 rows of 32 values of C, a bank apart, for rows that start unaligned
+    static constexpr uint32_t kOut = 32 * 33 * 4;
     static constexpr int kStages = BN == 256 ? 4 : 5;
-    static constexpr uint32_t kBytes = 1024 + kStages * kStage + kAddWarps * kWarp;
+    static constexpr uint32_t kBytes = 1024 + kStages * kStage + kScales + kAddWarps * kOut;
 };
 
 // 32 consecutive values of each of a warp's 32 rows to C, one row a lane. Rows aligned to
 // 32 bytes take whole sectors straight from registers; others go through shared memory, a
 // row at a time. Columns from n on; rows and columns outside C are left out.
 template <typename T>
-__device__ __forceinline__ void store_rows(const Product& p, char* stage, const float* v, int64_t m0, int64_t n, int lane) {
+__device__ __forceinline__ void store_rows(const Product& p, char* stage, const float2* v, int64_t m0, int64_t n, int lane) {
     T* c = static_cast<T*>(p.c) + n;
     const int cols = (int)min((int64_t)32, p.N - n), rows = (int)min((int64_t)32, p.M - m0);
     if (p.aligned && cols == 32) {
@@ -80,7 +82,7 @@ __device__ __forceinline__ void store_rows(const Product& p, char* stage, const 
                     uint32_t w[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const __nv_bfloat162 t = __floats2bfloat162_rn(v[e + 2 * k], v[e + 2 * k + 1]);
+                        const __nv_bfloat162 t = __float22bfloat162_rn(v[e / 2 + k]);
                         w[k] = *reinterpret_cast<const uint32_t*>(&t);
                     }
                     ptx::st_global_v8(to + e, w);
@@ -90,7 +92,7 @@ __device__ __forceinline__ void store_rows(const Product& p, char* stage, const 
                 for (int e = 0; e < 32; e += 8) {
                     uint32_t w[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[e + k]);
+                    for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(k & 1 ? v[(e + k) / 2].y : v[(e + k) / 2].x);
                     ptx::st_global_v8(to + e, w);
                 }
             }
@@ -99,7 +101,10 @@ __device__ __forceinline__ void store_rows(const Product& p, char* stage, const 
         float* st = reinterpret_cast<float*>(stage);
         __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) st[lane * 33 + e] = v[e];
+        for (int e = 0; e < 16; ++e) {
+            st[lane * 33 + 2 * e] = v[e].x;
+            st[lane * 33 + 2 * e + 1] = v[e].y;
+        }
         __syncwarp();
         if (lane < cols)
             for (int r = 0; r < rows; ++r) c[(m0 + r) * p.c_ld + lane] = from_f32<T>(st[r * 33 + lane]);
@@ -124,7 +129,7 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             ptx::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            ptx::mbar_init(&tfull[b], 1);
+            ptx::mbar_init(&tfull[b], 2);  // the product, and its scales
             ptx::mbar_init(&tempty[b], 2 * kAddWarps);
         }
         ptx::fence_mbar_init();
@@ -140,6 +145,7 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     ptx::cluster_sync();  // the peer's barriers are initialised
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    float* scales = reinterpret_cast<float*>(smem + S::kStages * S::kStage);
     bool ok = true;
 
     if (warp < 4) {
@@ -189,48 +195,95 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 }
             }
         }
+        if (warp == 3) {
+            // The scales of every group, for the adding warps of this CTA: loaded two groups ahead
+            // (under load they take longer than a group's product), put into the ring once the
+            // product two groups back is complete. That one was begun when every adding warp had
+            // read the one before it, so none still uses the ring's slots from five groups back.
+            constexpr int kB = kBlocks ? BN / 128 : BN / 32;  // scales of B a lane holds
+            const float *sa_at = nullptr, *sb_at = nullptr;
+            int rows_in = 0, cols_in = 0, idx = pair, g = 0;  // the group to load next
+            float sa[2][4], sb[2][kB];
+            auto load = [&](float (&a)[4], float (&b)[kB]) {
+                if (idx >= tiles) return;
+                if (g == 0) {
+                    int mt, nt;
+                    tile_at(p, idx, mt, nt);
+                    const int64_t m = min((int64_t)mt * 256 + rank * 128, p.M - 1), n = (int64_t)nt * BN;
+                    sa_at = p.a_scale + m;
+                    rows_in = (int)min((int64_t)128, p.M - m) - 1;
+                    sb_at = kBlocks ? p.b_scale + n / kGroup * p.KB : p.b_scale + n;
+                    cols_in = (int)min((int64_t)BN, p.N - n) - 1;
+                }
+                // rows and columns outside C take the last one's
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = __ldg(sa_at + min(lane + 32 * i, rows_in));
+#pragma unroll
+                for (int i = 0; i < kB; ++i)
+                    b[i] = __ldg(sb_at + (kBlocks ? min(i, cols_in / kGroup) * p.KB : min(lane + 32 * i, cols_in)));
+                sa_at += p.M;
+                sb_at += kBlocks ? 1 : p.N;
+                if (++g == p.KB) {
+                    g = 0;
+                    idx += pairs;
+                }
+            };
+            load(sa[0], sb[0]);
+            load(sa[1], sb[1]);
+            const uint32_t total = (uint32_t)((tiles - pair + pairs - 1) / pairs) * p.KB;
+            uint32_t phase = 1;
+            for (uint32_t it = 0; it < total && ok; it += 2) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (it + k >= total) break;
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&tfull[k], phase, kWaitNs));
+                    if (!ok) break;
+                    float* slot = scales + (it + k) % S::kRing * S::kSlot;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (kBlocks) {
+#pragma unroll
+                            for (int j = 0; j < kB; ++j) slot[128 * j + 32 * i + lane] = sa[k][i] * sb[k][j];
+                        } else {
+                            slot[32 * i + lane] = sa[k][i];
+                        }
+                    }
+                    if (!kBlocks) {
+#pragma unroll
+                        for (int j = 0; j < kB; ++j) slot[128 + 32 * j + lane] = sb[k][j];
+                    }
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&tfull[k]);
+                    load(sa[k], sb[k]);
+                }
+                phase ^= 1;
+            }
+        }
     } else {
         ptx::regs_inc<kAddRegs>();
         constexpr int kCols = S::kCols;
         const int quad = warp % 4, part = (warp - 4) / 4;
         const uint32_t taddr = tmem + ((uint32_t)(32 * quad) << 16) + part * kCols;
-        char* mine = smem + S::kStages * S::kStage + (warp - 4) * S::kWarp;
-        float* sn = reinterpret_cast<float*>(mine);
+        char* stage = smem + S::kStages * S::kStage + S::kScales + (warp - 4) * S::kOut;
+        // this lane's row's scale in a slot, and the warp's columns'
+        const int row_at = 32 * quad + lane + (kBlocks ? part * kCols / kGroup * 128 : 0), col_at = 128 + part * kCols;
+        const uint32_t tempty_at = ptx::mapa(ptx::smem_addr(&tempty[0]), 0);
         uint32_t it = 0;
         for (int idx = pair; idx < tiles && ok; idx += pairs) {
             int mt, nt;
             tile_at(p, idx, mt, nt);
-            const int64_t m0 = (int64_t)mt * 256 + rank * 128 + 32 * quad, m = m0 + lane;
+            const int64_t m0 = (int64_t)mt * 256 + rank * 128 + 32 * quad;
             const int64_t n0 = (int64_t)nt * BN + part * kCols;
-            const bool row_in = m < p.M;
-            // the scales of B for these columns: one of a block, or one a column (two a lane)
-            const float* sb_at = kBlocks ? p.b_scale + (n0 < p.N ? n0 / kGroup : 0) * p.KB : p.b_scale + n0 + lane;
-            float acc[kCols];
+            float2 acc[kCols / 2];
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
-            float sa = 0.0f, sb[kCols / 32];
-            auto load_scales = [&](int g) {
-                sa = row_in ? __ldg(p.a_scale + (int64_t)g * p.M + m) : 0.0f;
-                if (kBlocks) {
-                    sb[0] = __ldg(sb_at + g);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kCols / 32; ++j)
-                        sb[j] = n0 + 32 * j + lane < p.N ? __ldg(sb_at + (int64_t)g * p.N + 32 * j) : 0.0f;
-                }
-            };
-            load_scales(0);
+            for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
             for (int g = 0; g < p.KB; ++g, ++it) {
-                const float s = kBlocks ? sa * sb[0] : sa;
                 const uint32_t b = it & 1;
-                if (!kBlocks) {
-#pragma unroll
-                    for (int j = 0; j < kCols / 32; ++j) sn[b * kCols + 32 * j + lane] = sb[j];
-                    __syncwarp();
-                }
-                if (g + 1 < p.KB) load_scales(g + 1);  // while this group's product is computed
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(&tfull[b], (it >> 1) & 1, kWaitNs));
                 if (!ok) break;
+                const float* slot = scales + it % S::kRing * S::kSlot;
+                const float s = slot[row_at];
+                const float2 ss = make_float2(s, s);
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < kCols / 32; ++j) {
@@ -240,27 +293,26 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     if (j == kCols / 32 - 1) {  // read: the next product but one may take its place
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_remote_relaxed(ptx::mapa(ptx::smem_addr(&tempty[b]), 0));
+                        if (lane == 0) ptx::mbar_arrive_remote_relaxed(tempty_at + 8 * b);
                     }
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        if (kBlocks) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) acc[32 * j + e + k] = fmaf(v[e + k], s, acc[32 * j + e + k]);
-                        } else {
-                            const float4 w = *reinterpret_cast<const float4*>(sn + b * kCols + 32 * j + e);
-                            acc[32 * j + e] = fmaf(v[e] * w.x, s, acc[32 * j + e]);
-                            acc[32 * j + e + 1] = fmaf(v[e + 1] * w.y, s, acc[32 * j + e + 1]);
-                            acc[32 * j + e + 2] = fmaf(v[e + 2] * w.z, s, acc[32 * j + e + 2]);
-                            acc[32 * j + e + 3] = fmaf(v[e + 3] * w.w, s, acc[32 * j + e + 3]);
+                        float2* to = acc + 16 * j + e / 2;
+                        float2 lo = make_float2(v[e], v[e + 1]), hi = make_float2(v[e + 2], v[e + 3]);
+                        if (!kBlocks) {
+                            const float4 w = *reinterpret_cast<const float4*>(slot + col_at + 32 * j + e);
+                            lo = ptx::mul2(lo, make_float2(w.x, w.y));
+                            hi = ptx::mul2(hi, make_float2(w.z, w.w));
                         }
+                        to[0] = ptx::fma2(lo, ss, to[0]);
+                        to[1] = ptx::fma2(hi, ss, to[1]);
                     }
                 }
             }
             if (!ok) break;
 #pragma unroll
             for (int j = 0; j < kCols / 32; ++j)
-                if (n0 + 32 * j < p.N) store_rows<T>(p, mine + S::kScales, acc + 32 * j, m0, n0 + 32 * j, lane);
+                if (n0 + 32 * j < p.N) store_rows<T>(p, stage, acc + 16 * j, m0, n0 + 32 * j, lane);
         }
     }
     if (!ok) {
