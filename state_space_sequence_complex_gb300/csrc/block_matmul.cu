@@ -10,7 +10,7 @@
 // stages half of A's rows and half of B's, which halves the operand bytes an SM takes in
 // for its part of the product. Roles: warp 0 loads (TMA, a ring of stages of one group),
 // warps 1 and 2 of the even CTA issue the MMAs of every other group, warp 3 fetches the
-// scales, warps 4 .. 19 scale, add and store; each of those owns 32 rows x BN / 4 columns in registers, and takes registers that the first
+// scales, the others scale, add and store; each of those owns 32 rows x BN / 2 columns in registers, and takes registers that the first
 // four warps give up. (The issue of an MMA returns shortly before it is done, so a single
 // issuer's waits between two groups left the tensor cores idle for as long as they worked.)
 #include <cuda.h>
@@ -28,9 +28,6 @@ namespace block {
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;  // wait limit
-constexpr int kAddWarps = 16, kThreads = 128 + 32 * kAddWarps;
-// Registers a thread: 96 x 640 = 61440 at launch, 56 x 128 + 104 x 512 = 60416 after the split
-constexpr int kCtlRegs = 56, kAddRegs = 104;
 constexpr int kGroup = SSD_FP8_GROUP;
 
 struct Product {
@@ -38,7 +35,7 @@ struct Product {
     int64_t M, N, c_ld;
     int KB, m_tiles, n_tiles;
     void* c;
-    bool aligned;  // every row of c starts at a multiple of 32 bytes
+    bool tma_out;  // c's rows start at multiples of 16 bytes: stored by TMA
     int* status;
 };
 
@@ -55,69 +52,91 @@ __device__ __forceinline__ void tile_at(const Product& p, int idx, int& mt, int&
 template <int BN>
 struct Shape {
     static constexpr uint32_t kA = 128 * kGroup, kB = BN / 2 * kGroup, kStage = kA + kB;
-    static constexpr int kCols = BN / 4;  // columns of one warp
+    static constexpr int kBufs = 512 / BN;  // tensor-memory buffers
+    // adding warps: four quarters of the rows x two halves of the columns
+    static constexpr int kCols = BN / 2, kAddWarps = 8, kThreads = 128 + 32 * kAddWarps;
+    // Registers a thread: 384 x 168 at launch = 128 x 56 + 256 x 224 after the split
+    static constexpr int kCtlRegs = 56, kAddRegs = 224;
     // Scales, a ring of groups: 128 rows' for each of B's two blocks (already multiplied), or 128
     // rows' and then the columns'
-    static constexpr int kRing = 8, kSlot = 128 + 256;
+    static constexpr int kRing = 4 * kBufs, kSlot = 128 + 256;
     static constexpr uint32_t kScales = kRing * kSlot * 4;
-    // per adding warp: 32 rows of 32 values of C, a bank apart, for rows that start unaligned
-    static constexpr uint32_t kOut = 32 * 33 * 4;
+    // per adding warp: twice 32 rows of 128 bytes of C (of 132 where they are stored one by one)
+    static constexpr uint32_t kOut = 8 * 1024;
     static constexpr int kStages = BN == 256 ? 4 : 5;
-    static constexpr uint32_t kBytes = 1024 + kStages * kStage + kScales + kAddWarps * kOut;
+    static constexpr uint32_t kBytes = 1024 + kStages * kStage + kAddWarps * kOut + kScales;
 };
 
-// 32 consecutive values of each of a warp's 32 rows to C, one row a lane. Rows aligned to
-// 32 bytes take whole sectors straight from registers; others go through shared memory, a
-// row at a time. Columns from n on; rows and columns outside C are left out.
+__device__ __forceinline__ uint32_t bf16_pair(float2 v) {
+    const __nv_bfloat162 t = __float22bfloat162_rn(v);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// 128 bytes (64 bfloat16 or 32 fp32 values) of each of a warp's 32 rows, one row a lane, to C
+// from row m0 and column n on, through the warp's staging rows.
 template <typename T>
-__device__ __forceinline__ void store_rows(const Product& p, char* stage, const float2* v, int64_t m0, int64_t n, int lane) {
-    T* c = static_cast<T*>(p.c) + n;
-    const int cols = (int)min((int64_t)32, p.N - n), rows = (int)min((int64_t)32, p.M - m0);
-    if (p.aligned && cols == 32) {
-        if (lane < rows) {
-            T* to = c + (m0 + lane) * p.c_ld;
-            if constexpr (sizeof(T) == 2) {
+__device__ __forceinline__ void store_piece(const Product& p, const CUtensorMap* map_c, char* stage, int half,
+                                            const float2* v, int64_t m0, int64_t n, int lane) {
+    constexpr bool kHalf = sizeof(T) == 2;
+    constexpr int kPiece = 128 / sizeof(T);
+    auto word = [&](int e) {  // the e-th of the row's 32 words
+        if constexpr (kHalf) return bf16_pair(v[e]);
+        else return __float_as_uint(e & 1 ? v[e / 2].y : v[e / 2].x);
+    };
+    if (p.tma_out) {
+        // asynchronous: the warp goes on to the next tile while the rows are copied out; rows and
+        // columns outside C are left out by the copy
+        if (lane == 0) ptx::bulk_wait_read<1>();  // of the two, the half copied out before the last
+        __syncwarp();
 #pragma unroll
-                for (int e = 0; e < 32; e += 16) {
-                    uint32_t w[8];
+        for (int e = 0; e < 32; e += 4)  // (the 128-byte swizzle of the tensor map)
+            *reinterpret_cast<uint4*>(stage + 4096 * half + lane * 128 + (((e / 4) ^ (lane & 7)) << 4)) =
+                make_uint4(word(e), word(e + 1), word(e + 2), word(e + 3));
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            ptx::tma_store_2d(map_c, stage + 4096 * half, (int)n, (int)m0);
+            ptx::bulk_commit();
+        }
+        return;
+    }
+    // Rows that start anywhere: word by word, a row a store. A row of bfloat16 that starts between
+    // two words is shifted by one value, its first and last values stored alone.
+    uint32_t* st = reinterpret_cast<uint32_t*>(stage);
+    __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const __nv_bfloat162 t = __float22bfloat162_rn(v[e / 2 + k]);
-                        w[k] = *reinterpret_cast<const uint32_t*>(&t);
-                    }
-                    ptx::st_global_v8(to + e, w);
-                }
+    for (int e = 0; e < 32; ++e) st[lane * 33 + e] = word(e);
+    __syncwarp();
+    const int cols = (int)min((int64_t)kPiece, p.N - n), rows = (int)min((int64_t)32, p.M - m0);
+    for (int r = 0; r < rows; ++r) {
+        T* c = static_cast<T*>(p.c) + (m0 + r) * p.c_ld + n;
+        const uint32_t w = st[r * 33 + lane];
+        if constexpr (kHalf) {
+            if ((reinterpret_cast<uintptr_t>(c) & 2) == 0) {
+                if (2 * lane + 1 < cols) reinterpret_cast<uint32_t*>(c)[lane] = w;
+                else if (2 * lane < cols) reinterpret_cast<uint16_t*>(c)[2 * lane] = (uint16_t)w;
             } else {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(k & 1 ? v[(e + k) / 2].y : v[(e + k) / 2].x);
-                    ptx::st_global_v8(to + e, w);
-                }
+                const uint32_t next = st[r * 33 + min(lane + 1, 31)];
+                if (lane == 0) reinterpret_cast<uint16_t*>(c)[0] = (uint16_t)w;
+                if (2 * lane + 2 < cols)
+                    *reinterpret_cast<uint32_t*>(c + 2 * lane + 1) = __byte_perm(w, next, 0x5432);
+                else if (2 * lane + 1 < cols) reinterpret_cast<uint16_t*>(c)[2 * lane + 1] = (uint16_t)(w >> 16);
             }
+        } else {
+            if (lane < cols) reinterpret_cast<uint32_t*>(c)[lane] = w;
         }
-    } else {
-        float* st = reinterpret_cast<float*>(stage);
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            st[lane * 33 + 2 * e] = v[e].x;
-            st[lane * 33 + 2 * e + 1] = v[e].y;
-        }
-        __syncwarp();
-        if (lane < cols)
-            for (int r = 0; r < rows; ++r) c[(m0 + r) * p.c_ld + lane] = from_f32<T>(st[r * 33 + lane]);
     }
 }
 
 template <int BN, bool kBlocks, typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Product p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<BN>::kThreads, 1)
+product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+             const __grid_constant__ CUtensorMap map_c, const Product p) {
     using S = Shape<BN>;
+    constexpr int kBufs = S::kBufs;
     extern __shared__ char smem_raw[];
     char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t full[S::kStages], empty[S::kStages], tfull[2], tempty[2];
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], tfull[kBufs], tempty[kBufs];
     __shared__ uint32_t tmem_slot;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank();
@@ -128,9 +147,9 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kBufs; ++b) {
             ptx::mbar_init(&tfull[b], 2);  // the product, and its scales
-            ptx::mbar_init(&tempty[b], 2 * kAddWarps);
+            ptx::mbar_init(&tempty[b], 2 * S::kAddWarps);
         }
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&map_a);
@@ -145,11 +164,12 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     ptx::cluster_sync();  // the peer's barriers are initialised
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    float* scales = reinterpret_cast<float*>(smem + S::kStages * S::kStage);
+    char* out = smem + S::kStages * S::kStage;
+    float* scales = reinterpret_cast<float*>(out + S::kAddWarps * S::kOut);
     bool ok = true;
 
     if (warp < 4) {
-        ptx::regs_dec<kCtlRegs>();
+        ptx::regs_dec<S::kCtlRegs>();
         if (warp == 0 && lane == 0) {
             uint32_t it = 0;
             for (int idx = pair; idx < tiles && ok; idx += pairs) {
@@ -172,14 +192,15 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 ok = ptx::mbar_wait(&empty[k % S::kStages], (k / S::kStages) & 1, kWaitNs);
         }
         if ((warp == 1 || warp == 2) && lane == 0 && rank == 0) {
-            // one issuer for each tensor-memory buffer
+            // two issuers, each of every other group
             constexpr uint32_t idesc = ptx::idesc_e4m3(256, BN);
-            const uint32_t b = warp - 1, d = tmem + b * BN;
             const uint64_t base = ptx::smem_desc_sw128(ptx::smem_addr(smem), 16, 1024);
             const uint32_t total = (uint32_t)((tiles - pair + pairs - 1) / pairs) * p.KB;
-            uint32_t s = b, s_phase = 0, b_phase = 1;
-            for (uint32_t it = b; it < total; it += 2) {
-                ok = ptx::mbar_wait(&tempty[b], b_phase, kWaitNs) && ptx::mbar_wait(&full[s], s_phase, kWaitNs);
+            uint32_t s = warp - 1, s_phase = 0;
+            for (uint32_t it = warp - 1; it < total; it += 2) {
+                const uint32_t b = it % kBufs, b_phase = it / kBufs & 1 ^ 1, d = tmem + b * BN;
+                // (the operands come early: waited for first, the buffer's release is acted on at once)
+                ok = ptx::mbar_wait(&full[s], s_phase, kWaitNs) && ptx::mbar_wait(&tempty[b], b_phase, kWaitNs);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const uint64_t da = base + s * (S::kStage / 16), db = da + S::kA / 16;
@@ -187,7 +208,6 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 for (int k = 0; k < 4; ++k) ptx::mma_f8_ss_pair(d, da + 2 * k, db + 2 * k, idesc, k > 0);
                 ptx::mma_commit_pair(&tfull[b]);
                 ptx::mma_commit_pair(&empty[s]);
-                b_phase ^= 1;
                 s += 2;
                 if (s >= S::kStages) {
                     s -= S::kStages;
@@ -198,13 +218,14 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         if (warp == 3) {
             // The scales of every group, for the adding warps of this CTA: loaded two groups ahead
             // (under load they take longer than a group's product), put into the ring once the
-            // product two groups back is complete. That one was begun when every adding warp had
-            // read the one before it, so none still uses the ring's slots from five groups back.
+            // product kBufs groups back is complete. That one was begun when every adding warp had
+            // read the one in its buffer before, 2 kBufs groups back, and so had done with all
+            // earlier ones: of a ring of more than 2 kBufs slots the oldest is free.
             constexpr int kB = kBlocks ? BN / 128 : BN / 32;  // scales of B a lane holds
             const float *sa_at = nullptr, *sb_at = nullptr;
             int rows_in = 0, cols_in = 0, idx = pair, g = 0;  // the group to load next
             float sa[2][4], sb[2][kB];
-            auto load = [&](float (&a)[4], float (&b)[kB]) {
+            auto load = [&](float (&a)[4], float (&c)[kB]) {
                 if (idx >= tiles) return;
                 if (g == 0) {
                     int mt, nt;
@@ -220,7 +241,7 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 for (int i = 0; i < 4; ++i) a[i] = __ldg(sa_at + min(lane + 32 * i, rows_in));
 #pragma unroll
                 for (int i = 0; i < kB; ++i)
-                    b[i] = __ldg(sb_at + (kBlocks ? min(i, cols_in / kGroup) * p.KB : min(lane + 32 * i, cols_in)));
+                    c[i] = __ldg(sb_at + (kBlocks ? min(i, cols_in / kGroup) * p.KB : min(lane + 32 * i, cols_in)));
                 sa_at += p.M;
                 sb_at += kBlocks ? 1 : p.N;
                 if (++g == p.KB) {
@@ -231,12 +252,12 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             load(sa[0], sb[0]);
             load(sa[1], sb[1]);
             const uint32_t total = (uint32_t)((tiles - pair + pairs - 1) / pairs) * p.KB;
-            uint32_t phase = 1;
             for (uint32_t it = 0; it < total && ok; it += 2) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (it + k >= total) break;
-                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&tfull[k], phase, kWaitNs));
+                    const uint32_t b = (it + k) % kBufs, phase = (it + k) / kBufs & 1 ^ 1;
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&tfull[b], phase, kWaitNs));
                     if (!ok) break;
                     float* slot = scales + (it + k) % S::kRing * S::kSlot;
 #pragma unroll
@@ -253,22 +274,37 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         for (int j = 0; j < kB; ++j) slot[128 + 32 * j + lane] = sb[k][j];
                     }
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&tfull[k]);
+                    if (lane == 0) ptx::mbar_arrive(&tfull[b]);
                     load(sa[k], sb[k]);
                 }
-                phase ^= 1;
             }
         }
     } else {
-        ptx::regs_inc<kAddRegs>();
+        ptx::regs_inc<S::kAddRegs>();
         constexpr int kCols = S::kCols;
         const int quad = warp % 4, part = (warp - 4) / 4;
         const uint32_t taddr = tmem + ((uint32_t)(32 * quad) << 16) + part * kCols;
-        char* stage = smem + S::kStages * S::kStage + S::kScales + (warp - 4) * S::kOut;
+        char* stage = out + (warp - 4) * S::kOut;
         // this lane's row's scale in a slot, and the warp's columns'
         const int row_at = 32 * quad + lane + (kBlocks ? part * kCols / kGroup * 128 : 0), col_at = 128 + part * kCols;
         const uint32_t tempty_at = ptx::mapa(ptx::smem_addr(&tempty[0]), 0);
-        uint32_t it = 0;
+        // Pieces of 32 columns are read while the one before is added, and the first of a group
+        // while the last of the group before is: waits on shared-memory barriers take 200 cycles
+        // while operands stream through it, and must not stand between two pieces.
+        float v[2][32], s = 0.0f;
+        const uint32_t total = (uint32_t)((tiles - pair + pairs - 1) / pairs) * p.KB;
+        uint32_t it = 0;  // the group that begin() reads next
+        bool ready = false;
+        auto begin = [&]() {
+            const uint32_t b = it % kBufs, phase = it / kBufs & 1;
+            ok = __all_sync(0xffffffffu, ready || ptx::mbar_wait(&tfull[b], phase, kWaitNs));
+            if (!ok) return;
+            ptx::tc_fence_after();
+            ptx::tmem_ld32(taddr + b * BN, v[0]);
+            s = scales[it % S::kRing * S::kSlot + row_at];
+            ++it;
+        };
+        begin();
         for (int idx = pair; idx < tiles && ok; idx += pairs) {
             int mt, nt;
             tile_at(p, idx, mt, nt);
@@ -277,28 +313,27 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             float2 acc[kCols / 2];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
-            for (int g = 0; g < p.KB; ++g, ++it) {
-                const uint32_t b = it & 1;
-                ok = __all_sync(0xffffffffu, ptx::mbar_wait(&tfull[b], (it >> 1) & 1, kWaitNs));
-                if (!ok) break;
-                const float* slot = scales + it % S::kRing * S::kSlot;
-                const float s = slot[row_at];
+            for (int g = 0; g < p.KB && ok; ++g) {
+                const uint32_t b = (it - 1) % kBufs;
+                const float* slot = scales + (it - 1) % S::kRing * S::kSlot;
                 const float2 ss = make_float2(s, s);
-                ptx::tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < kCols / 32; ++j) {
-                    float v[32];
-                    ptx::tmem_ld32(taddr + b * BN + 32 * j, v);
                     ptx::tmem_wait_ld();
-                    if (j == kCols / 32 - 1) {  // read: the next product but one may take its place
+                    if (j == kCols / 32 - 2) ready = ptx::mbar_test_wait(&tfull[it % kBufs], it / kBufs & 1);
+                    if (j + 1 < kCols / 32) {
+                        ptx::tmem_ld32(taddr + b * BN + 32 * (j + 1), v[(j + 1) & 1]);
+                    } else {  // read: the next product but kBufs - 1 may take its place
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive_remote_relaxed(tempty_at + 8 * b);
+                        if (it < total) begin();
                     }
+                    const float* u = v[j & 1];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         float2* to = acc + 16 * j + e / 2;
-                        float2 lo = make_float2(v[e], v[e + 1]), hi = make_float2(v[e + 2], v[e + 3]);
+                        float2 lo = make_float2(u[e], u[e + 1]), hi = make_float2(u[e + 2], u[e + 3]);
                         if (!kBlocks) {
                             const float4 w = *reinterpret_cast<const float4*>(slot + col_at + 32 * j + e);
                             lo = ptx::mul2(lo, make_float2(w.x, w.y));
@@ -310,10 +345,13 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 }
             }
             if (!ok) break;
+            constexpr int kPiece = 128 / sizeof(T);
 #pragma unroll
-            for (int j = 0; j < kCols / 32; ++j)
-                if (n0 + 32 * j < p.N) store_rows<T>(p, stage, acc + 16 * j, m0, n0 + 32 * j, lane);
+            for (int j = 0; j < kCols / kPiece; ++j)
+                if (m0 < p.M && n0 + kPiece * j < p.N)
+                    store_piece<T>(p, &map_c, stage, j & 1, acc + kPiece / 2 * j, m0, n0 + kPiece * j, lane);
         }
+        if (lane == 0) ptx::bulk_wait_all();
     }
     if (!ok) {
         // a wait gave up: report it, and leave copies and products in flight the time to end
@@ -339,17 +377,23 @@ int device_sms() {
 
 template <int BN, bool kBlocks, typename T>
 int launch_pair(const Matmul& p, Product q, int sms, cudaStream_t stream) {
-    CUtensorMap ma, mb;
-    if (!tc::encode_tiled_u8(&ma, p.a, p.K, p.M, p.a_ld, 128) || !tc::encode_tiled_u8(&mb, p.b, p.K, p.N, p.b_ld, BN / 2))
+    using S = Shape<BN>;
+    CUtensorMap ma, mb, mc;
+    if (!tc::encode_tiled_2d(&ma, p.a, 1, p.K, p.M, p.a_ld, 128) || !tc::encode_tiled_2d(&mb, p.b, 1, p.K, p.N, p.b_ld, BN / 2))
         return SSDC_ERR_CUDA;
+    if (q.tma_out) {
+        if (!tc::encode_tiled_2d(&mc, p.c, sizeof(T), p.N, p.M, p.c_ld * (int64_t)sizeof(T), 32)) return SSDC_ERR_CUDA;
+    } else {
+        mc = ma;  // not used
+    }
     q.n_tiles = (int)((p.N + BN - 1) / BN);
     const int64_t tiles = (int64_t)q.m_tiles * q.n_tiles;
-    if (tiles > INT32_MAX / 2) return SSDC_ERR_UNSUPPORTED;
+    if (tiles * q.KB > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
     const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
     auto* k = product_pair<BN, kBlocks, T>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<BN>::kBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes) != cudaSuccess)
         return SSDC_ERR_CUDA;
-    k<<<2 * pairs, kThreads, Shape<BN>::kBytes, stream>>>(ma, mb, q);
+    k<<<2 * pairs, S::kThreads, S::kBytes, stream>>>(ma, mb, mc, q);
     return 1;
 }
 
@@ -376,14 +420,14 @@ int matmul_launch(const Matmul& p, cudaStream_t stream) {
     q.m_tiles = (int)((p.M + 255) / 256);
     q.c = p.c;
     const size_t e = p.out_bf16 ? 2 : 4;
-    q.aligned = (reinterpret_cast<uintptr_t>(p.c) | (uintptr_t)(p.c_ld * e)) % 32 == 0;
+    q.tma_out = (reinterpret_cast<uintptr_t>(p.c) | (uintptr_t)(p.c_ld * e)) % 16 == 0;
     q.status = p.status;
     // The tile width whose rounds over the SM pairs cover fewer columns in all
     auto rounds = [&](int bn) {
         const int64_t tiles = (int64_t)q.m_tiles * ((p.N + bn - 1) / bn);
         return (tiles + sms / 2 - 1) / (sms / 2) * bn;
     };
-    return rounds(128) < rounds(256) ? launch_pair_types<128>(p, q, sms, stream)
+    return 1.4 * rounds(128) < rounds(256) ? launch_pair_types<128>(p, q, sms, stream)
                                      : launch_pair_types<256>(p, q, sms, stream);
 }
 

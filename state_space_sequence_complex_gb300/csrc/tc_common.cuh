@@ -134,8 +134,9 @@ bool encode_feature_map_bf16(CUtensorMap* m, const void* base, int F, int H, int
 // strides[i] is the byte stride of dimension i + 1.
 bool encode_tiled_f32(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
                       const cuuint32_t* box);
-// Host: rows of bytes, boxes of 128 columns x box_rows with the 128-byte swizzle and zero fill.
-bool encode_tiled_u8(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
+// Host: rows of 1-, 2- (bfloat16) or 4-byte (fp32) elements, `pitch` bytes apart; boxes of 128
+// bytes x box_rows with the 128-byte swizzle and zero fill.
+bool encode_tiled_2d(CUtensorMap* m, const void* base, int elem, int64_t cols, int64_t rows, int64_t pitch, int box_rows);
 
 }  // namespace tc
 }  // namespace ssdc
