@@ -21,15 +21,16 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 
 // s = sigmoid(z) and r = sigmoid(-z) = 1 - s from one exponential and one reciprocal:
 // with e = exp(-|z|) in (0, 1], sigmoid(|z|) = 1 / (1 + e) and sigmoid(-|z|) = e / (1 + e),
-// so neither loses digits where the other is near one. The fast exponential's relative
-// error, about |z| 1e-7, is the largest here.
+// so neither loses digits where the other is near one. The hardware's approximations of
+// 2^y and 1 / y: the largest relative error, about |z| 1e-7 from rounding y = -|z| log2(e),
+// is in the smaller of the two. A NaN gives NaNs.
 __device__ __forceinline__ void sigmoid_pair(float z, float& s, float& r) {
-    const float e = __expf(-fabsf(z));
-    const float inv = __fdividef(1.0f, 1.0f + e);
+    float e, inv;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-fabsf(z) * 1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(1.0f + e));
     const float small = e * inv;
     s = z >= 0.0f ? inv : small;
     r = z >= 0.0f ? small : inv;
-    if (z != z) s = r = z;
 }
 
 // The scale of a group and an element's e4m3 value. Both divisions are the rounded ones:
