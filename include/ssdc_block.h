@@ -69,12 +69,17 @@ typedef struct {
  *   states    output for the backward pass, or NULL:
  *             ssd_gated_scan_states_bytes() bytes, the state entering every
  *             SSD_GATED_STATE_TOKENS-th token, (B, ceil(T / that), D) fp32
+ *   status    a device word, or NULL. The CTAs of a cluster wait for one another for
+ *             two seconds at most; a wait that gives up sets the word to
+ *             SSDC_ERR_TIMEOUT, and the results are NaN. The caller zeroes it once
+ *             (ssd_complex_status() reads it)
  * One launch. Results do not depend on timing: sums run in a fixed order.
  */
 #define SSD_GATED_STATE_TOKENS 64
 size_t ssd_gated_scan_states_bytes(ssd_gated_dims dims);
 int ssd_gated_scan_fwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float *h0, const uint8_t *reset,
-                       ssd_gated_dims dims, ssd_seq_out h, float *h_last, float *states, cudaStream_t stream);
+                       ssd_gated_dims dims, ssd_seq_out h, float *h_last, float *states, int32_t *status,
+                       cudaStream_t stream);
 
 /*
  * One token for every batch row (the forward pass at T = 1, for generation):
@@ -94,12 +99,12 @@ int ssd_gated_scan_step(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float *s
  *   states    what the forward pass kept for the same inputs (h0 is in it)
  *   dh        gradient of h;  dh_last (B, D) fp32, or NULL: zero
  *   di        given exactly with i;  dh0: (B, D) fp32, or NULL: not written; it
- *             may be dh_last
+ *             may be dh_last;  status: as for the forward pass
  * The states inside a chunk are recomputed in fp32 from `states`. One launch.
  */
 int ssd_gated_scan_bwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float *states, const uint8_t *reset,
                        ssd_seq_in dh, const float *dh_last, ssd_gated_dims dims, ssd_seq_out dx, ssd_seq_out df,
-                       ssd_seq_out di, float *dh0, cudaStream_t stream);
+                       ssd_seq_out di, float *dh0, int32_t *status, cudaStream_t stream);
 
 /*
  * Residual norm over M rows of D features:

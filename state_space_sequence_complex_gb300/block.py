@@ -66,9 +66,9 @@ def load() -> ctypes.CDLL:
     q, r, d = ssd_seq, ssd_rows, ssd_gated_dims
     for name, res, args in (
             ("ssd_gated_scan_states_bytes", sz, [d]),
-            ("ssd_gated_scan_fwd", i32, [q, q, q, vp, vp, d, q, vp, vp, vp]),
+            ("ssd_gated_scan_fwd", i32, [q, q, q, vp, vp, d, q, vp, vp, vp, vp]),
             ("ssd_gated_scan_step", i32, [q, q, q, vp, i64, i64, i32, q, vp, vp]),
-            ("ssd_gated_scan_bwd", i32, [q, q, q, vp, vp, q, vp, d, q, q, q, vp, vp]),
+            ("ssd_gated_scan_bwd", i32, [q, q, q, vp, vp, q, vp, d, q, q, q, vp, vp, vp]),
             ("ssd_residual_norm_fwd", i32, [r, r, vp, f32, i64, i64, i32, r, i32, r, vp, vp, vp]),
             ("ssd_residual_norm_bwd_workspace_bytes", sz, [i64, i64]),
             ("ssd_residual_norm_bwd", i32, [r, r, r, vp, vp, i64, i64, i32, r, vp, vp, sz, vp]),
@@ -193,6 +193,7 @@ class GatedScan:
         self.states = None
         if keep_states:
             self.states = torch.empty((B, -(-T // STATE_TOKENS), D), dtype=torch.float32, device=self.device)
+        self.workspace = torch.zeros(64, dtype=torch.int32, device=self.device)
         self._h = _seq("h", self.h, self.shape, self.dtype, self.device)
 
     def __call__(self, x, f, i=None, h0=None, reset=None, out=None, stream=None):
@@ -207,10 +208,13 @@ class GatedScan:
             _dense("h0", h0, self.state_shape, torch.float32, self.device),
             _dense("reset", reset, self.mark_shape, torch.uint8, self.device), self.dims, h_out,
             self.h_last.data_ptr(), None if self.states is None else self.states.data_ptr(),
-            _stream(stream, self.device))
+            self.workspace.data_ptr(), _stream(stream, self.device))
         if rc:
             _raise(rc, "ssd_gated_scan_fwd")
         return h, self.h_last
+
+    def status(self, stream=None) -> int:
+        return ssdc.ssd_complex_status(self.workspace, stream)
 
 
 class GatedScanBackward:
@@ -230,6 +234,7 @@ class GatedScanBackward:
         self.states_shape = (B, -(-T // STATE_TOKENS), D)
         names = ("dx", "df", "di") if input_gate else ("dx", "df")
         self.grads = {k: torch.empty(self.shape, dtype=self.dtype, device=self.device) for k in names}
+        self.workspace = torch.zeros(64, dtype=torch.int32, device=self.device)
         self.grads["dh0"] = torch.empty(self.state_shape, dtype=torch.float32, device=self.device)
 
     def __call__(self, x, f, i, states, dh, dh_last=None, reset=None, stream=None):
@@ -241,10 +246,14 @@ class GatedScanBackward:
             _dense("states", states, self.states_shape, torch.float32, d),
             _dense("reset", reset, self.mark_shape, torch.uint8, d), _seq("dh", dh, *a),
             _dense("dh_last", dh_last, self.state_shape, torch.float32, d), self.dims, _seq("dx", g["dx"], *a),
-            _seq("df", g["df"], *a), _seq("di", g.get("di"), *a), g["dh0"].data_ptr(), _stream(stream, d))
+            _seq("df", g["df"], *a), _seq("di", g.get("di"), *a), g["dh0"].data_ptr(),
+            self.workspace.data_ptr(), _stream(stream, d))
         if rc:
             _raise(rc, "ssd_gated_scan_bwd")
         return dict(g)
+
+    def status(self, stream=None) -> int:
+        return ssdc.ssd_complex_status(self.workspace, stream)
 
 
 class GatedScanStep:

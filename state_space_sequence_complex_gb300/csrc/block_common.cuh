@@ -33,6 +33,14 @@ __device__ __forceinline__ void sigmoid_pair(float z, float& s, float& r) {
     r = z >= 0.0f ? small : inv;
 }
 
+// sigmoid(z) alone: 1 / (1 + exp(-z)), to zero where the exponential overflows.
+__device__ __forceinline__ float sigmoid(float z) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
+}
+
 // The scale of a group and an element's e4m3 value. Both divisions are the rounded ones:
 // an element that lies midway between two e4m3 values must round as x / scale does.
 __device__ __forceinline__ float group_scale(float amax) { return fmaxf(amax, 7.88860905e-31f /* 2^-100 */) / 448.0f; }

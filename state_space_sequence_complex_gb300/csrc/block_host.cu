@@ -182,7 +182,8 @@ size_t ssd_gated_scan_states_bytes(ssd_gated_dims dims) {
 }
 
 int ssd_gated_scan_fwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* h0, const uint8_t* reset,
-                       ssd_gated_dims d, ssd_seq_out h, float* h_last, float* states, cudaStream_t stream) {
+                       ssd_gated_dims d, ssd_seq_out h, float* h_last, float* states, int32_t* status,
+                       cudaStream_t stream) {
     int rc = check_gated(d);
     if (rc != SSDC_OK) return rc;
     Args a;
@@ -194,13 +195,14 @@ int ssd_gated_scan_fwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* h0
     a.output(seq(h.p, h.stride_b, h.stride_t, d));
     a.output(dense(h_last, d.B * d.D), true, h0);
     a.output(dense(states, d.B * state_rows(d) * d.D), false);
+    a.output(dense(status, 1), false);
     if (a.rc != SSDC_OK) return a.rc;
     rc = check_device();
     if (rc != SSDC_OK) return rc;
     Gated p = gated_problem(x, f, i, d);
     p.h0 = h0; p.reset = reset;
     p.h = h.p; p.h_b = h.stride_b; p.h_t = h.stride_t;
-    p.h_last = h_last; p.states = states;
+    p.h_last = h_last; p.states = states; p.status = status;
     (void)cudaGetLastError();
     return done(gated_fwd_launch(p, stream));
 }
@@ -228,7 +230,7 @@ int ssd_gated_scan_step(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* s
 
 int ssd_gated_scan_bwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* states, const uint8_t* reset,
                        ssd_seq_in dh, const float* dh_last, ssd_gated_dims d, ssd_seq_out dx, ssd_seq_out df,
-                       ssd_seq_out di, float* dh0, cudaStream_t stream) {
+                       ssd_seq_out di, float* dh0, int32_t* status, cudaStream_t stream) {
     int rc = check_gated(d);
     if (rc != SSDC_OK) return rc;
     if ((i.p == nullptr) != (di.p == nullptr)) return SSDC_ERR_INVALID;
@@ -244,6 +246,7 @@ int ssd_gated_scan_bwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* st
     a.output(seq(df.p, df.stride_b, df.stride_t, d));
     a.output(seq(di.p, di.stride_b, di.stride_t, d), false);
     a.output(dense(dh0, d.B * d.D), false, dh_last);
+    a.output(dense(status, 1), false);
     if (a.rc != SSDC_OK) return a.rc;
     rc = check_device();
     if (rc != SSDC_OK) return rc;
@@ -253,7 +256,7 @@ int ssd_gated_scan_bwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* st
     p.dx = dx.p; p.dx_b = dx.stride_b; p.dx_t = dx.stride_t;
     p.df = df.p; p.df_b = df.stride_b; p.df_t = df.stride_t;
     p.di = di.p; p.di_b = di.stride_b; p.di_t = di.stride_t;
-    p.dh0 = dh0;
+    p.dh0 = dh0; p.status = status;
     (void)cudaGetLastError();
     return done(gated_bwd_launch(p, stream));
 }

@@ -32,6 +32,7 @@ struct Gated {
     void *dx, *df, *di;
     int64_t dx_b, dx_t, df_b, df_t, di_b, di_t;
     float* dh0;
+    int* status;  // or null
 };
 int gated_fwd_launch(const Gated& p, cudaStream_t stream);
 int gated_bwd_launch(const Gated& p, cudaStream_t stream);

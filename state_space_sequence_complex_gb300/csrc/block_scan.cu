@@ -7,7 +7,9 @@
 // registers; 8 warps a CTA, a tile of 64 tokens, joined through shared memory; and R tiles
 // a cluster, joined through distributed shared memory. A cluster walks its channels'
 // sequence R tiles at a time, the running state in registers, and every input is read
-// once. All joins run in the order of the tokens, so results do not depend on timing.
+// once. All joins run in the order of the tokens, so results do not depend on timing. The
+// tiles' totals travel by st.async, counted on an mbarrier of the CTA that takes them: a
+// cluster barrier's release would wait for the last tile's rows to reach memory.
 //
 // A lane owns two adjacent channels (one where the arrays do not allow it), a warp 64: a row
 // of a warp is one 128-byte line of bfloat16. Bound by HBM: 8 bytes an element (bfloat16
@@ -34,9 +36,15 @@ constexpr int kMaxCluster = kWarps;  // one warp sends to each CTA of the cluste
 constexpr float kStop = -0.0f;
 __device__ __forceinline__ bool stops(float A) { return __float_as_uint(A) == 0x80000000u; }
 // The state behind a run, from the one before it.
-__device__ __forceinline__ float through(float A, float H, float h) { return stops(A) ? H : fmaf(A, h, H); }
+template <bool kReset>
+__device__ __forceinline__ float through(float A, float H, float h) {
+    return kReset && stops(A) ? H : fmaf(A, h, H);
+}
 // The factor of two runs, the first one first.
-__device__ __forceinline__ float both(float A1, float A2) { return stops(A1) || stops(A2) ? kStop : A1 * A2; }
+template <bool kReset>
+__device__ __forceinline__ float both(float A1, float A2) {
+    return kReset && (stops(A1) || stops(A2)) ? kStop : A1 * A2;
+}
 
 // kVec adjacent channels of one token, as they are in memory.
 template <typename T, int kVec>
@@ -82,52 +90,82 @@ __device__ __forceinline__ void store(float* p, const float (&v)[kVec]) {
 }
 
 // The totals of the cluster's tiles, by tile, for this CTA's channels: A and H of each of a
-// lane's channels. Two of them: a CTA may be a round ahead of another.
+// lane's channels. Two of them, with a barrier each, by the parity of the round: a CTA that
+// sends its total of round i + 2 has taken every CTA's of round i + 1, which each sent when
+// it had used round i's.
 template <int kVec>
 struct Totals {
     float v[2][kMaxCluster][32][2 * kVec];
+    uint64_t full[2];
 };
+constexpr uint64_t kWaitNs = 2000000000ull;  // wait limit
 
-// This CTA's total to every CTA of the cluster (one warp each), then the first half of the
-// cluster's barrier.
 template <int kVec>
-__device__ __forceinline__ void send_total(Totals<kVec>& t, int parity, uint32_t rank, uint32_t R, int warp, int lane,
-                                           const float (&A)[kVec], const float (&H)[kVec]) {
-    if (warp < (int)R) {
-        const uint32_t to = ptx::mapa(ptx::smem_addr(t.v[parity][rank][lane]), warp);
-        if constexpr (kVec == 2)
-            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(A[0]), "f"(A[1]), "f"(H[0]),
-                         "f"(H[1])
-                         : "memory");
-        else
-            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(A[0]), "f"(H[0]) : "memory");
+__device__ __forceinline__ void totals_init(Totals<kVec>& t, uint32_t R) {
+    if (R == 1) return;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(&t.full[0], 1);
+        ptx::mbar_init(&t.full[1], 1);
+        ptx::fence_mbar_init();
     }
+    // (a CTA's shared memory may be written to once it runs and its barriers are there)
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
 
-// The second half, then: `carry` through the tiles before this one (in), and through all (carry).
+// This CTA's total to every CTA of the cluster, its own too: one warp each.
 template <int kVec>
-__device__ __forceinline__ void receive_totals(const Totals<kVec>& t, int parity, uint32_t rank, uint32_t R, int lane,
-                                               float (&carry)[kVec], float (&in)[kVec]) {
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+__device__ __forceinline__ void send_total(Totals<kVec>& t, int64_t round, uint32_t rank, uint32_t R, int warp, int lane,
+                                           const float (&A)[kVec], const float (&H)[kVec]) {
+    if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    const int parity = (int)(round & 1);
+    if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&t.full[parity], R * 32 * 8 * kVec);
+    if (warp < (int)R) {
+        const uint32_t to = ptx::mapa(ptx::smem_addr(t.v[parity][rank][lane]), warp);
+        const uint32_t bar = ptx::mapa(ptx::smem_addr(&t.full[parity]), warp);
+        if constexpr (kVec == 2) ptx::st_async_v4(to, make_float4(A[0], A[1], H[0], H[1]), bar);
+        else ptx::st_async_v2(to, make_float2(A[0], H[0]), bar);
+    }
+}
+
+// `carry` through the tiles before this one (in), and through all (carry).
+// A wait that gives up makes the results NaN from there on, and later waits give up at once.
+template <int kVec, bool kReset>
+__device__ __forceinline__ void receive_totals(Totals<kVec>& t, int64_t round, uint32_t rank, uint32_t R, int lane,
+                                               float (&carry)[kVec], float (&in)[kVec], bool& ok) {
+    const int parity = (int)(round & 1);
+    ok = ptx::mbar_wait(&t.full[parity], (uint32_t)(round >> 1) & 1, ok ? kWaitNs : 0) && ok;
+    if (!ok) {
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) carry[c] = __int_as_float(0x7fffffff);
+    }
 #pragma unroll
     for (int c = 0; c < kVec; ++c) in[c] = carry[c];
     for (uint32_t r = 0; r < R; ++r) {
         const float* v = t.v[parity][r][lane];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
-            carry[c] = through(v[c], v[kVec + c], carry[c]);
+            carry[c] = through<kReset>(v[c], v[kVec + c], carry[c]);
             if (r < rank) in[c] = carry[c];
         }
     }
 }
 
-template <typename T, int kVec, bool kGate>
-__global__ void __launch_bounds__(kThreads, 2) gated_fwd(const Gated p) {
+// No CTA leaves while another may still send to it (where a wait gave up).
+__device__ __forceinline__ void leave(uint32_t R, bool ok, int* status) {
+    if (!ok && status) atomicCAS(status, SSDC_OK, SSDC_ERR_TIMEOUT);
+    if (R > 1) {
+        ptx::cluster_arrive_relaxed();
+        ptx::cluster_wait();
+    }
+}
+
+template <typename T, int kVec, bool kGate, bool kReset>
+__global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const Gated p) {
     __shared__ Totals<kVec> totals;
     __shared__ float part[2][kWarps][32][2 * kVec];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
+    totals_init(totals, R);
     const int64_t groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
     const int b = (int)(group / groups), d = (int)(group % groups) * 32 * kVec + lane * kVec;
     const bool in_d = d < p.D;
@@ -136,40 +174,44 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd(const Gated p) {
     const T* f = static_cast<const T*>(p.f) + b * p.f_b + d;
     const T* g = kGate ? static_cast<const T*>(p.i) + b * p.i_b + d : nullptr;
     T* h = static_cast<T*>(p.h) + b * p.h_b + d;
-    const uint8_t* reset = p.reset ? p.reset + (int64_t)b * p.T : nullptr;
+    const uint8_t* reset = kReset ? p.reset + (int64_t)b * p.T : nullptr;
 
-    // (a CTA's shared memory may be written to once the CTA runs)
-    if (R > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     float carry[kVec];
 #pragma unroll
     for (int c = 0; c < kVec; ++c) carry[c] = p.h0 && in_d ? p.h0[(int64_t)b * p.D + d + c] : 0.0f;
 
     Raw<T, kVec> rx[kTok], rf[kTok], rg[kTok];
-    uint32_t stop = 0;
+    int n = 0;          // tokens of this warp, the same for all lanes
+    uint32_t stop = 0;  // those at which a document starts
     auto load = [&](int64_t tile) {
         const int64_t t0 = tile * kTile + warp * kTok;
+        n = (int)max((int64_t)0, min((int64_t)kTok, p.T - t0));
         stop = 0;
+        if (kReset) {
+            const uint32_t mark = lane < n ? __ldg(reset + t0 + lane) : 0;
+            stop = __ballot_sync(0xffffffffu, mark != 0);
+        }
+        const T *px = x + t0 * p.x_t, *pf = f + t0 * p.f_t, *pg = kGate ? g + t0 * p.i_t : nullptr;
 #pragma unroll
         for (int k = 0; k < kTok; ++k) {
-            const int64_t t = t0 + k;
             rx[k].zero();
             rf[k].zero();
             if (kGate) rg[k].zero();
-            if (t < p.T) {
-                if (in_d) {
-                    rx[k].load(x + t * p.x_t);
-                    rf[k].load(f + t * p.f_t);
-                    if (kGate) rg[k].load(g + t * p.i_t);
-                }
-                if (reset && __ldg(reset + t)) stop |= 1u << k;
+            if (in_d && k < n) {
+                rx[k].load(px + k * p.x_t);
+                rf[k].load(pf + k * p.f_t);
+                if (kGate) rg[k].load(pg + k * p.i_t);
             }
         }
     };
     load(rank);
-    int parity = 0;
-    for (int64_t tile0 = 0; tile0 < tiles; tile0 += R, parity ^= 1) {
-        const int64_t tile = tile0 + rank, t0 = tile * kTile + warp * kTok;
-        const int n = (int)max((int64_t)0, min((int64_t)kTok, p.T - t0));  // tokens of this warp
+    bool ok = true;
+    int64_t round = 0;
+    for (int64_t tile = rank; tile - rank < tiles; tile += R, ++round) {
+        const int parity = (int)(round & 1);
+        const int rows = n;
+        // a warp whose tokens are all there and start no document takes the short way
+        const bool plain = rows == kTok && (!kReset || stop == 0);
         float C[kTok][kVec], v[kTok][kVec], A[kVec], H[kVec];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
@@ -180,17 +222,40 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd(const Gated p) {
         for (int k = 0; k < kTok; ++k)
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
-                float a, r, u;
-                sigmoid_pair(rf[k].get(c), a, r);
-                u = r;
-                if (kGate) sigmoid_pair(rg[k].get(c), u, r);
-                // tokens past the end leave the state as it is
-                C[k][c] = k >= n ? 1.0f : (stop >> k & 1) ? kStop : a;
-                v[k][c] = k >= n ? 0.0f : u * rx[k].get(c);
-                H[c] = through(C[k][c], v[k][c], H[c]);
-                A[c] = both(A[c], C[k][c]);
+                float u;
+                if (kGate) {
+                    C[k][c] = sigmoid(rf[k].get(c));
+                    u = sigmoid(rg[k].get(c));
+                } else {
+                    sigmoid_pair(rf[k].get(c), C[k][c], u);
+                }
+                v[k][c] = u * rx[k].get(c);
             }
-        if (tile0 + R < tiles) load(tile + R);
+        if (plain) {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k)
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    H[c] = fmaf(C[k][c], H[c], v[k][c]);
+                    A[c] *= C[k][c];
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k)
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    // tokens past the end leave the state as it is
+                    if (k >= rows) {
+                        C[k][c] = 1.0f;
+                        v[k][c] = 0.0f;
+                    } else if (kReset && (stop >> k & 1)) {
+                        C[k][c] = kStop;
+                    }
+                    H[c] = through<kReset>(C[k][c], v[k][c], H[c]);
+                    A[c] = both<kReset>(A[c], C[k][c]);
+                }
+        }
+        if (tile - rank + R < tiles) load(tile + R);
         float* mine = part[parity][warp][lane];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
@@ -208,26 +273,28 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd(const Gated p) {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float* o = part[parity][w][lane];
+            if (w == warp) {
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                if (w == warp) {
+                for (int c = 0; c < kVec; ++c) {
                     preA[c] = A[c];
                     preH[c] = H[c];
                 }
-                H[c] = through(o[c], o[kVec + c], H[c]);
-                A[c] = both(A[c], o[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                H[c] = through<kReset>(o[c], o[kVec + c], H[c]);
+                A[c] = both<kReset>(A[c], o[c]);
             }
         }
         float in[kVec];
         if (R > 1) {
-            if (tile0 == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-            send_total<kVec>(totals, parity, rank, R, warp, lane, A, H);
-            receive_totals<kVec>(totals, parity, rank, R, lane, carry, in);
+            send_total<kVec>(totals, round, rank, R, warp, lane, A, H);
+            receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
         } else {
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
                 in[c] = carry[c];
-                carry[c] = through(A[c], H[c], carry[c]);
+                carry[c] = through<kReset>(A[c], H[c], carry[c]);
             }
         }
         if (p.states && warp == 0 && in_d && tile < tiles) {
@@ -236,32 +303,44 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd(const Gated p) {
             for (int c = 0; c < kVec; ++c) s[c] = in[c];
         }
 #pragma unroll
-        for (int c = 0; c < kVec; ++c) in[c] = through(preA[c], preH[c], in[c]);
+        for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(preA[c], preH[c], in[c]);
+        T* ph = h + (tile * kTile + warp * kTok) * p.h_t;
+        if (plain) {
 #pragma unroll
-        for (int k = 0; k < kTok; ++k) {
+            for (int k = 0; k < kTok; ++k) {
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) in[c] = through(C[k][c], v[k][c], in[c]);
-            if (k < n && in_d) store<kVec>(h + (t0 + k) * p.h_t, in);
+                for (int c = 0; c < kVec; ++c) in[c] = fmaf(C[k][c], in[c], v[k][c]);
+                if (in_d) store<kVec>(ph + k * p.h_t, in);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) {
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(C[k][c], v[k][c], in[c]);
+                if (k < rows && in_d) store<kVec>(ph + k * p.h_t, in);
+            }
         }
     }
     if (rank == 0 && warp == 0 && in_d) {
 #pragma unroll
         for (int c = 0; c < kVec; ++c) p.h_last[(int64_t)b * p.D + d + c] = carry[c];
     }
+    leave(R, ok, p.status);
 }
 
 // Backward, from the last tile to the first: with k_t = c_{t+1} g_{t+1} the gradient that enters
 // token t from its right, g_t = dh_t + k_t and k_{t-1} = c_t g_t, so a run of tokens maps
 // k -> A k + G with the same A as forward. Each tile's states are recomputed from the one
-// that the forward pass kept for it.
-template <typename T, int kVec, bool kGate>
+// that the forward pass kept for it. The next tile's rows are fetched into L2 meanwhile.
+template <typename T, int kVec, bool kGate, bool kReset>
 __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
     __shared__ Totals<kVec> totals;
-    __shared__ float part[2][kWarps][32][3 * kVec];
+    __shared__ float part[2][kWarps][32][4 * kVec];  // A, G, H of a lane's channels
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
+    totals_init(totals, R);
     const int64_t groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
-    const int b = (int)(group / groups), d = (int)(group % groups) * 32 * kVec + lane * kVec;
+    const int b = (int)(group / groups), d0 = (int)(group % groups) * 32 * kVec, d = d0 + lane * kVec;
     const bool in_d = d < p.D;
     const int64_t tiles = (p.T + kTile - 1) / kTile;
     const T* x = static_cast<const T*>(p.x) + b * p.x_b + d;
@@ -271,42 +350,58 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
     T* dx = static_cast<T*>(p.dx) + b * p.dx_b + d;
     T* df = static_cast<T*>(p.df) + b * p.df_b + d;
     T* di = kGate ? static_cast<T*>(p.di) + b * p.di_b + d : nullptr;
-    const uint8_t* reset = p.reset ? p.reset + (int64_t)b * p.T : nullptr;
+    const uint8_t* reset = kReset ? p.reset + (int64_t)b * p.T : nullptr;
+    // the row that this lane fetches for its warp: one of 8 tokens of one of the 4 arrays
+    const int fetch = lane / kTok;
+    const T* fetch_at = (fetch == 0 ? x : fetch == 1 ? f : fetch == 2 ? dh : kGate ? g : x) - lane * kVec;
+    const int64_t fetch_t = fetch == 0 ? p.x_t : fetch == 1 ? p.f_t : fetch == 2 ? p.dh_t : kGate ? p.i_t : p.x_t;
 
-    // (a CTA's shared memory may be written to once the CTA runs)
-    if (R > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     float carry[kVec];
 #pragma unroll
     for (int c = 0; c < kVec; ++c) carry[c] = p.dh_last && in_d ? p.dh_last[(int64_t)b * p.D + d + c] : 0.0f;
 
-    int parity = 0;
-    for (int64_t back0 = 0; back0 < tiles; back0 += R, parity ^= 1) {
-        const int64_t tile = tiles - 1 - (back0 + rank), t0 = tile * kTile + warp * kTok;
+    bool ok = true;
+    int64_t round = 0;
+    for (int64_t back = rank; back - rank < tiles; back += R, ++round) {
+        const int parity = (int)(round & 1);
+        const int64_t tile = tiles - 1 - back, t0 = tile * kTile + warp * kTok;
         const int n = tile < 0 ? 0 : (int)max((int64_t)0, min((int64_t)kTok, p.T - t0));
-        Raw<T, kVec> rx[kTok], rf[kTok], rg[kTok], rh[kTok];
         uint32_t stop = 0;
+        if (kReset) {
+            const uint32_t mark = lane < n ? __ldg(reset + t0 + lane) : 0;
+            stop = __ballot_sync(0xffffffffu, mark != 0);
+        }
+        Raw<T, kVec> rx[kTok], rf[kTok], rg[kTok], rh[kTok];
         float s[kVec];
 #pragma unroll
         for (int c = 0; c < kVec; ++c)
             s[c] = tile >= 0 && in_d ? __ldg(p.in_states + ((int64_t)b * tiles + tile) * p.D + d + c) : 0.0f;
+        {
+            const T *px = x + t0 * p.x_t, *pf = f + t0 * p.f_t, *ph = dh + t0 * p.dh_t, *pg = kGate ? g + t0 * p.i_t : nullptr;
 #pragma unroll
-        for (int k = 0; k < kTok; ++k) {
-            const int64_t t = t0 + k;
-            rx[k].zero();
-            rf[k].zero();
-            rh[k].zero();
-            if (kGate) rg[k].zero();
-            if (k < n) {
-                if (in_d) {
-                    rf[k].load(f + t * p.f_t);
-                    if (kGate) rg[k].load(g + t * p.i_t);
-                    rx[k].load(x + t * p.x_t);
-                    rh[k].load(dh + t * p.dh_t);
+            for (int k = 0; k < kTok; ++k) {
+                rx[k].zero();
+                rf[k].zero();
+                rh[k].zero();
+                if (kGate) rg[k].zero();
+                if (in_d && k < n) {
+                    rf[k].load(pf + k * p.f_t);
+                    if (kGate) rg[k].load(pg + k * p.i_t);
+                    rx[k].load(px + k * p.x_t);
+                    rh[k].load(ph + k * p.dh_t);
                 }
-                if (reset && __ldg(reset + t)) stop |= 1u << k;
+            }
+            // (a tile before this one is full)
+            const int64_t next = tile - R;
+            if (next >= 0) {
+                const T* q = fetch_at + (next * kTile + warp * kTok + lane % kTok) * fetch_t;
+                ptx::prefetch_l2(q);
+                if (sizeof(T) * kVec * 32 > 128 && d0 + 32 < p.D) ptx::prefetch_l2(q + 32);
             }
         }
-        // C, the factors' derivatives, and the run's A, H (states) and G (gradients)
+        const bool plain = n == kTok && (!kReset || stop == 0);
+        // a token's factor C, its input's factor u and both factors' derivatives (ca; cu with x
+        // in it), and the run's A, H (states) and G (gradients)
         float C[kTok][kVec], ca[kTok][kVec], u[kTok][kVec], cu[kTok][kVec], A[kVec], H[kVec], G[kVec];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
@@ -317,32 +412,52 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
         for (int k = 0; k < kTok; ++k)
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
-                float a, na, nu;
-                sigmoid_pair(rf[k].get(c), a, na);
-                ca[k][c] = a * na;
+                float na, nu;
+                sigmoid_pair(rf[k].get(c), C[k][c], na);
+                ca[k][c] = C[k][c] * na;
                 u[k][c] = na;
                 if (kGate) {
                     sigmoid_pair(rg[k].get(c), u[k][c], nu);
-                    cu[k][c] = u[k][c] * nu;
+                    cu[k][c] = rx[k].get(c) * (u[k][c] * nu);
                 }
-                C[k][c] = k >= n ? 1.0f : (stop >> k & 1) ? kStop : a;
-                H[c] = through(C[k][c], k >= n ? 0.0f : u[k][c] * rx[k].get(c), H[c]);
-                A[c] = both(A[c], C[k][c]);
             }
+        if (plain) {
 #pragma unroll
-        for (int k = kTok - 1; k >= 0; --k)
+            for (int k = 0; k < kTok; ++k)
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) G[c] = through(C[k][c], 0.0f, rh[k].get(c) + G[c]);
+                for (int c = 0; c < kVec; ++c) {
+                    H[c] = fmaf(C[k][c], H[c], u[k][c] * rx[k].get(c));
+                    A[c] *= C[k][c];
+                }
+#pragma unroll
+            for (int k = kTok - 1; k >= 0; --k)
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) G[c] = C[k][c] * (rh[k].get(c) + G[c]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k)
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    // tokens past the end change nothing (their rows are zero)
+                    if (k >= n) C[k][c] = 1.0f;
+                    else if (kReset && (stop >> k & 1)) C[k][c] = kStop;
+                    H[c] = through<kReset>(C[k][c], u[k][c] * rx[k].get(c), H[c]);
+                    A[c] = both<kReset>(A[c], C[k][c]);
+                }
+#pragma unroll
+            for (int k = kTok - 1; k >= 0; --k)
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) G[c] = through<kReset>(C[k][c], 0.0f, rh[k].get(c) + G[c]);
+        }
         float* mine = part[parity][warp][lane];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
             mine[c] = A[c];
-            mine[kVec + c] = H[c];
-            mine[2 * kVec + c] = G[c];
+            mine[kVec + c] = G[c];
+            mine[2 * kVec + c] = H[c];
         }
         __syncthreads();
-        // the state behind the tile's warps before this one; the gradient's run through those after
-        // it (suf), and through all
+        // the gradient's run through the tile's warps after this one (suf), and through all
         float sufA[kVec], sufG[kVec];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
@@ -352,62 +467,63 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
 #pragma unroll
         for (int w = kWarps - 1; w >= 0; --w) {
             const float* o = part[parity][w][lane];
+            if (w == warp) {
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                if (w == warp) {
+                for (int c = 0; c < kVec; ++c) {
                     sufA[c] = A[c];
                     sufG[c] = G[c];
                 }
-                G[c] = through(o[c], o[2 * kVec + c], G[c]);
-                A[c] = both(A[c], o[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                G[c] = through<kReset>(o[c], o[kVec + c], G[c]);
+                A[c] = both<kReset>(A[c], o[c]);
             }
         }
-        if (R > 1) {
-            if (back0 == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-            send_total<kVec>(totals, parity, rank, R, warp, lane, A, G);
+        if (R > 1) send_total<kVec>(totals, round, rank, R, warp, lane, A, G);
+        // the state behind the tile's warps before this one, then token by token: what enters a
+        // token (nothing at a reset) makes its gate's gradient
+        for (int w = 0; w < warp; ++w) {
+            const float* o = part[parity][w][lane];
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) s[c] = through<kReset>(o[c], o[2 * kVec + c], s[c]);
         }
-#pragma unroll
-        for (int w = 0; w < kWarps - 1; ++w)
-            if (w < warp) {
-                const float* o = part[parity][w][lane];
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) s[c] = through(o[c], o[kVec + c], s[c]);
-            }
-        float before[kTok][kVec];  // the state that enters each token (0 at a reset)
 #pragma unroll
         for (int k = 0; k < kTok; ++k)
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
-                before[k][c] = stops(C[k][c]) ? 0.0f : s[c];
-                s[c] = through(C[k][c], u[k][c] * rx[k].get(c), s[c]);
+                const float xv = rx[k].get(c), before = kReset && stops(C[k][c]) ? 0.0f : s[c];
+                ca[k][c] *= kGate ? before : before - xv;
+                s[c] = through<kReset>(C[k][c], u[k][c] * xv, s[c]);
             }
         float in[kVec];
         if (R > 1) {
-            receive_totals<kVec>(totals, parity, rank, R, lane, carry, in);
+            receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
         } else {
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
                 in[c] = carry[c];
-                carry[c] = through(A[c], G[c], carry[c]);
+                carry[c] = through<kReset>(A[c], G[c], carry[c]);
             }
         }
 #pragma unroll
-        for (int c = 0; c < kVec; ++c) in[c] = through(sufA[c], sufG[c], in[c]);
+        for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(sufA[c], sufG[c], in[c]);
+        T *px = dx + t0 * p.dx_t, *pf = df + t0 * p.df_t, *pi = kGate ? di + t0 * p.di_t : nullptr;
 #pragma unroll
         for (int k = kTok - 1; k >= 0; --k) {
             float ox[kVec], of[kVec], oi[kVec];
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
-                const float gr = rh[k].get(c) + in[c], xv = rx[k].get(c);
+                const float gr = rh[k].get(c) + in[c];
                 ox[c] = u[k][c] * gr;
-                of[c] = ca[k][c] * gr * (kGate ? before[k][c] : before[k][c] - xv);
-                if (kGate) oi[c] = xv * cu[k][c] * gr;
-                if (k < n) in[c] = stops(C[k][c]) ? 0.0f : C[k][c] * gr;
+                of[c] = ca[k][c] * gr;
+                if (kGate) oi[c] = cu[k][c] * gr;
+                in[c] = kReset && stops(C[k][c]) ? 0.0f : C[k][c] * gr;
             }
-            if (k < n && in_d) {
-                store<kVec>(dx + (t0 + k) * p.dx_t, ox);
-                store<kVec>(df + (t0 + k) * p.df_t, of);
-                if (kGate) store<kVec>(di + (t0 + k) * p.di_t, oi);
+            if (in_d && k < n) {
+                store<kVec>(px + k * p.dx_t, ox);
+                store<kVec>(pf + k * p.df_t, of);
+                if (kGate) store<kVec>(pi + k * p.di_t, oi);
             }
         }
     }
@@ -415,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
 #pragma unroll
         for (int c = 0; c < kVec; ++c) p.dh0[(int64_t)b * p.D + d + c] = carry[c];
     }
+    leave(R, ok, p.status);
 }
 
 // One token: a thread a channel pair (or channel). Bound by the launch.
@@ -474,8 +591,10 @@ int launch_cluster(K kernel, const Gated& p, int vec, cudaStream_t stream) {
 
 template <typename T, int kVec, bool kGate>
 int launch(const Gated& p, int what, cudaStream_t stream) {
-    if (what == 0) return launch_cluster(gated_fwd<T, kVec, kGate>, p, kVec, stream);
-    if (what == 1) return launch_cluster(gated_bwd<T, kVec, kGate>, p, kVec, stream);
+    if (what == 0 && p.reset) return launch_cluster(gated_fwd<T, kVec, kGate, true>, p, kVec, stream);
+    if (what == 0) return launch_cluster(gated_fwd<T, kVec, kGate, false>, p, kVec, stream);
+    if (what == 1 && p.reset) return launch_cluster(gated_bwd<T, kVec, kGate, true>, p, kVec, stream);
+    if (what == 1) return launch_cluster(gated_bwd<T, kVec, kGate, false>, p, kVec, stream);
     const int64_t n = (int64_t)p.B * ((p.D + kVec - 1) / kVec);
     gated_step<T, kVec, kGate><<<(unsigned)((n + 127) / 128), 128, 0, stream>>>(p);
     return 1;

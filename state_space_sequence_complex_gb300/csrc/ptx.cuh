@@ -164,6 +164,16 @@ __device__ __forceinline__ void st_async_v4(uint32_t dst_cluster, float4 v, uint
                  : "memory");
 }
 
+// The same with 8 bytes.
+__device__ __forceinline__ void st_async_v2(uint32_t dst_cluster, float2 v, uint32_t mbar_cluster) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(dst_cluster),
+                 "f"(v.x), "f"(v.y), "r"(mbar_cluster)
+                 : "memory");
+}
+
+// Fetch the line of a global address into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 // Wait until every committed bulk operation has completed (writes visible).

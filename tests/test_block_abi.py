@@ -41,10 +41,10 @@ NONE = block.ssd_seq(None, 0, 0)
 
 def fwd(lib, **k):
     a = dict(x=SEQ(at(1)), f=SEQ(at(2)), i=SEQ(at(3)), h0=at(4), reset=at(5), dims=(2, 100, 64, 1), h=SEQ(at(6)),
-             h_last=at(7), states=at(8))
+             h_last=at(7), states=at(8), status=at(9))
     a.update(k)
     return lib.ssd_gated_scan_fwd(a["x"], a["f"], a["i"], a["h0"], a["reset"], block.ssd_gated_dims(*a["dims"]), a["h"],
-                                  a["h_last"], a["states"], None)
+                                  a["h_last"], a["states"], a["status"], None)
 
 
 @pytest.mark.parametrize("change,want", [
@@ -59,7 +59,7 @@ def fwd(lib, **k):
     (dict(h=SEQ(at(6), 0)), INVALID), (dict(h=SEQ(at(6), 6400, 63)), INVALID),  # rows on top of each other
     (dict(h=SEQ(at(6), 640, 64)), INVALID),
     (dict(h_last=at(2)), INVALID), (dict(h_last=at(4) + 4), INVALID), (dict(states=at(6)), INVALID),
-    (dict(states=at(7)), INVALID),
+    (dict(states=at(7)), INVALID), (dict(status=at(1)), INVALID), (dict(status=at(9) + 2), ALIGN),
     # slices of one array, 192 wide: the output's columns reach into the gate's
     (dict(x=SEQ(at(1), 19200, 192), f=SEQ(at(1) + 128, 19200, 192), h=SEQ(at(1) + 254, 19200, 192)), INVALID),
     (dict(x=SEQ(at(1), 19200, 192), f=SEQ(at(1) + 128, 19200, 192), h=SEQ(at(1) + 258, 19200, 192)), INVALID),
@@ -73,7 +73,7 @@ def bwd(lib, **k):
              dx=SEQ(at(7)), df=SEQ(at(8)), di=SEQ(at(9)), dh0=at(10))
     a.update(k)
     return lib.ssd_gated_scan_bwd(a["x"], a["f"], a["i"], a["states"], a["reset"], a["dh"], a["dh_last"],
-                                  block.ssd_gated_dims(2, 100, 64, 1), a["dx"], a["df"], a["di"], a["dh0"], None)
+                                  block.ssd_gated_dims(2, 100, 64, 1), a["dx"], a["df"], a["di"], a["dh0"], None, None)
 
 
 @pytest.mark.parametrize("change", [
