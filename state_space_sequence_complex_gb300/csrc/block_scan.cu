@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps, kTok = 8, kTile = kWarps * kTok;
 static_assert(kTile == SSD_GATED_STATE_TOKENS, "a state is kept for every tile");
-constexpr int kMaxCluster = kWarps;  // one warp sends to each CTA of the cluster
+constexpr int kMaxCluster = 8;
 
 // A reset stops everything that comes before it, an infinity or a NaN too, so it is not the
 // factor 0 but a mark of its own in A: the value -0, which no product of gates takes.
@@ -102,7 +102,6 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // wait limit
 
 template <int kVec>
 __device__ __forceinline__ void totals_init(Totals<kVec>& t, uint32_t R) {
-    if (R == 1) return;
     if (threadIdx.x == 0) {
         ptx::mbar_init(&t.full[0], 1);
         ptx::mbar_init(&t.full[1], 1);
@@ -112,22 +111,20 @@ __device__ __forceinline__ void totals_init(Totals<kVec>& t, uint32_t R) {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
 
-// This CTA's total to every CTA of the cluster, its own too: one warp each.
+// This CTA's total to every CTA of the cluster, its own too; by one warp.
 template <int kVec>
-__device__ __forceinline__ void send_total(Totals<kVec>& t, int64_t round, uint32_t rank, uint32_t R, int warp, int lane,
+__device__ __forceinline__ void send_total(Totals<kVec>& t, int64_t round, uint32_t rank, uint32_t R, int lane,
                                            const float (&A)[kVec], const float (&H)[kVec]) {
-    if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     const int parity = (int)(round & 1);
-    if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&t.full[parity], R * 32 * 8 * kVec);
-    if (warp < (int)R) {
-        const uint32_t to = ptx::mapa(ptx::smem_addr(t.v[parity][rank][lane]), warp);
-        const uint32_t bar = ptx::mapa(ptx::smem_addr(&t.full[parity]), warp);
+    if (lane == 0) ptx::mbar_arrive_expect_tx(&t.full[parity], R * 32 * 8 * kVec);
+    const uint32_t at = ptx::smem_addr(t.v[parity][rank][lane]), full = ptx::smem_addr(&t.full[parity]);
+    for (uint32_t r = 0; r < R; ++r) {
+        const uint32_t to = ptx::mapa(at, r), bar = ptx::mapa(full, r);
         if constexpr (kVec == 2) ptx::st_async_v4(to, make_float4(A[0], A[1], H[0], H[1]), bar);
         else ptx::st_async_v2(to, make_float2(A[0], H[0]), bar);
     }
 }
 
-// `carry` through the tiles before this one (in), and through all (carry).
 // A wait that gives up makes the results NaN from there on, and later waits give up at once.
 template <int kVec, bool kReset>
 __device__ __forceinline__ void receive_totals(Totals<kVec>& t, int64_t round, uint32_t rank, uint32_t R, int lane,
@@ -163,17 +160,21 @@ template <typename T, int kVec, bool kGate, bool kReset>
 __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const Gated p) {
     __shared__ Totals<kVec> totals;
     __shared__ float part[2][kWarps][32][2 * kVec];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // (the warp's index from a shuffle: what depends on it alone is then computed once a warp)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
     totals_init(totals, R);
     const int64_t groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
     const int b = (int)(group / groups), d = (int)(group % groups) * 32 * kVec + lane * kVec;
     const bool in_d = d < p.D;
     const int64_t tiles = (p.T + kTile - 1) / kTile;
-    const T* x = static_cast<const T*>(p.x) + b * p.x_b + d;
-    const T* f = static_cast<const T*>(p.f) + b * p.f_b + d;
-    const T* g = kGate ? static_cast<const T*>(p.i) + b * p.i_b + d : nullptr;
-    T* h = static_cast<T*>(p.h) + b * p.h_b + d;
+    // rows of the batch row b; a lane's channels (a valid lane's where it is past the last) are
+    // added as a 32-bit offset
+    const T* x = static_cast<const T*>(p.x) + b * p.x_b;
+    const T* f = static_cast<const T*>(p.f) + b * p.f_b;
+    const T* g = kGate ? static_cast<const T*>(p.i) + b * p.i_b : nullptr;
+    T* h = static_cast<T*>(p.h) + b * p.h_b;
+    const uint32_t dl = in_d ? d : p.D - kVec;
     const uint8_t* reset = kReset ? p.reset + (int64_t)b * p.T : nullptr;
 
     float carry[kVec];
@@ -192,15 +193,24 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
             stop = __ballot_sync(0xffffffffu, mark != 0);
         }
         const T *px = x + t0 * p.x_t, *pf = f + t0 * p.f_t, *pg = kGate ? g + t0 * p.i_t : nullptr;
+        if (n == kTok) {
 #pragma unroll
-        for (int k = 0; k < kTok; ++k) {
-            rx[k].zero();
-            rf[k].zero();
-            if (kGate) rg[k].zero();
-            if (in_d && k < n) {
-                rx[k].load(px + k * p.x_t);
-                rf[k].load(pf + k * p.f_t);
-                if (kGate) rg[k].load(pg + k * p.i_t);
+            for (int k = 0; k < kTok; ++k) {
+                rf[k].load(pf + k * p.f_t + dl);
+                if (kGate) rg[k].load(pg + k * p.i_t + dl);
+                rx[k].load(px + k * p.x_t + dl);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) {
+                rx[k].zero();
+                rf[k].zero();
+                if (kGate) rg[k].zero();
+                if (k < n) {
+                    rf[k].load(pf + k * p.f_t + dl);
+                    if (kGate) rg[k].load(pg + k * p.i_t + dl);
+                    rx[k].load(px + k * p.x_t + dl);
+                }
             }
         }
     };
@@ -263,40 +273,33 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
             mine[kVec + c] = H[c];
         }
         __syncthreads();
-        // the tile's warps before this one, and all of them
+        // the tile's warps before this one; the last warp adds its own and has the tile's total
         float preA[kVec], preH[kVec];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
-            A[c] = preA[c] = 1.0f;
-            H[c] = preH[c] = 0.0f;
+            preA[c] = 1.0f;
+            preH[c] = 0.0f;
         }
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+#pragma unroll 1
+        for (int w = 0; w < warp; ++w) {
             const float* o = part[parity][w][lane];
-            if (w == warp) {
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) {
-                    preA[c] = A[c];
-                    preH[c] = H[c];
-                }
-            }
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
-                H[c] = through<kReset>(o[c], o[kVec + c], H[c]);
-                A[c] = both<kReset>(A[c], o[c]);
+                preH[c] = through<kReset>(o[c], o[kVec + c], preH[c]);
+                preA[c] = both<kReset>(preA[c], o[c]);
             }
+        }
+        if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        if (warp == kWarps - 1) {
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                H[c] = through<kReset>(A[c], H[c], preH[c]);
+                A[c] = both<kReset>(preA[c], A[c]);
+            }
+            send_total<kVec>(totals, round, rank, R, lane, A, H);
         }
         float in[kVec];
-        if (R > 1) {
-            send_total<kVec>(totals, round, rank, R, warp, lane, A, H);
-            receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
-        } else {
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                in[c] = carry[c];
-                carry[c] = through<kReset>(A[c], H[c], carry[c]);
-            }
-        }
+        receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
         if (p.states && warp == 0 && in_d && tile < tiles) {
             float* s = p.states + ((int64_t)b * tiles + tile) * p.D + d;
 #pragma unroll
@@ -310,14 +313,14 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
             for (int k = 0; k < kTok; ++k) {
 #pragma unroll
                 for (int c = 0; c < kVec; ++c) in[c] = fmaf(C[k][c], in[c], v[k][c]);
-                if (in_d) store<kVec>(ph + k * p.h_t, in);
+                if (in_d) store<kVec>(ph + k * p.h_t + dl, in);
             }
         } else {
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
 #pragma unroll
                 for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(C[k][c], v[k][c], in[c]);
-                if (k < rows && in_d) store<kVec>(ph + k * p.h_t, in);
+                if (k < rows && in_d) store<kVec>(ph + k * p.h_t + dl, in);
             }
         }
     }
@@ -336,24 +339,26 @@ template <typename T, int kVec, bool kGate, bool kReset>
 __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
     __shared__ Totals<kVec> totals;
     __shared__ float part[2][kWarps][32][4 * kVec];  // A, G, H of a lane's channels
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // (the warp's index from a shuffle: what depends on it alone is then computed once a warp)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
     totals_init(totals, R);
     const int64_t groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
     const int b = (int)(group / groups), d0 = (int)(group % groups) * 32 * kVec, d = d0 + lane * kVec;
     const bool in_d = d < p.D;
     const int64_t tiles = (p.T + kTile - 1) / kTile;
-    const T* x = static_cast<const T*>(p.x) + b * p.x_b + d;
-    const T* f = static_cast<const T*>(p.f) + b * p.f_b + d;
-    const T* g = kGate ? static_cast<const T*>(p.i) + b * p.i_b + d : nullptr;
-    const T* dh = static_cast<const T*>(p.dh) + b * p.dh_b + d;
-    T* dx = static_cast<T*>(p.dx) + b * p.dx_b + d;
-    T* df = static_cast<T*>(p.df) + b * p.df_b + d;
-    T* di = kGate ? static_cast<T*>(p.di) + b * p.di_b + d : nullptr;
+    const T* x = static_cast<const T*>(p.x) + b * p.x_b;
+    const T* f = static_cast<const T*>(p.f) + b * p.f_b;
+    const T* g = kGate ? static_cast<const T*>(p.i) + b * p.i_b : nullptr;
+    const T* dh = static_cast<const T*>(p.dh) + b * p.dh_b;
+    T* dx = static_cast<T*>(p.dx) + b * p.dx_b;
+    T* df = static_cast<T*>(p.df) + b * p.df_b;
+    T* di = kGate ? static_cast<T*>(p.di) + b * p.di_b : nullptr;
+    const uint32_t dl = in_d ? d : p.D - kVec;
     const uint8_t* reset = kReset ? p.reset + (int64_t)b * p.T : nullptr;
     // the row that this lane fetches for its warp: one of 8 tokens of one of the 4 arrays
     const int fetch = lane / kTok;
-    const T* fetch_at = (fetch == 0 ? x : fetch == 1 ? f : fetch == 2 ? dh : kGate ? g : x) - lane * kVec;
+    const T* fetch_at = (fetch == 0 ? x : fetch == 1 ? f : fetch == 2 ? dh : kGate ? g : x) + d0;
     const int64_t fetch_t = fetch == 0 ? p.x_t : fetch == 1 ? p.f_t : fetch == 2 ? p.dh_t : kGate ? p.i_t : p.x_t;
 
     float carry[kVec];
@@ -378,17 +383,27 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
             s[c] = tile >= 0 && in_d ? __ldg(p.in_states + ((int64_t)b * tiles + tile) * p.D + d + c) : 0.0f;
         {
             const T *px = x + t0 * p.x_t, *pf = f + t0 * p.f_t, *ph = dh + t0 * p.dh_t, *pg = kGate ? g + t0 * p.i_t : nullptr;
+            if (n == kTok) {
 #pragma unroll
-            for (int k = 0; k < kTok; ++k) {
-                rx[k].zero();
-                rf[k].zero();
-                rh[k].zero();
-                if (kGate) rg[k].zero();
-                if (in_d && k < n) {
-                    rf[k].load(pf + k * p.f_t);
-                    if (kGate) rg[k].load(pg + k * p.i_t);
-                    rx[k].load(px + k * p.x_t);
-                    rh[k].load(ph + k * p.dh_t);
+                for (int k = 0; k < kTok; ++k) {
+                    rf[k].load(pf + k * p.f_t + dl);
+                    if (kGate) rg[k].load(pg + k * p.i_t + dl);
+                    rx[k].load(px + k * p.x_t + dl);
+                    rh[k].load(ph + k * p.dh_t + dl);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kTok; ++k) {
+                    rx[k].zero();
+                    rf[k].zero();
+                    rh[k].zero();
+                    if (kGate) rg[k].zero();
+                    if (k < n) {
+                        rf[k].load(pf + k * p.f_t + dl);
+                        if (kGate) rg[k].load(pg + k * p.i_t + dl);
+                        rx[k].load(px + k * p.x_t + dl);
+                        rh[k].load(ph + k * p.dh_t + dl);
+                    }
                 }
             }
             // (a tile before this one is full)
@@ -457,32 +472,35 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
             mine[2 * kVec + c] = H[c];
         }
         __syncthreads();
-        // the gradient's run through the tile's warps after this one (suf), and through all
+        // the gradient's run through the tile's warps after this one; the first warp adds its own
+        // and has the tile's total
         float sufA[kVec], sufG[kVec];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
-            A[c] = sufA[c] = 1.0f;
-            G[c] = sufG[c] = 0.0f;
+            sufA[c] = 1.0f;
+            sufG[c] = 0.0f;
         }
-#pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
+#pragma unroll 1
+        for (int w = kWarps - 1; w > warp; --w) {
             const float* o = part[parity][w][lane];
-            if (w == warp) {
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) {
-                    sufA[c] = A[c];
-                    sufG[c] = G[c];
-                }
-            }
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
-                G[c] = through<kReset>(o[c], o[kVec + c], G[c]);
-                A[c] = both<kReset>(A[c], o[c]);
+                sufG[c] = through<kReset>(o[c], o[kVec + c], sufG[c]);
+                sufA[c] = both<kReset>(sufA[c], o[c]);
             }
         }
-        if (R > 1) send_total<kVec>(totals, round, rank, R, warp, lane, A, G);
+        if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        if (warp == 0) {
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                G[c] = through<kReset>(A[c], G[c], sufG[c]);
+                A[c] = both<kReset>(sufA[c], A[c]);
+            }
+            send_total<kVec>(totals, round, rank, R, lane, A, G);
+        }
         // the state behind the tile's warps before this one, then token by token: what enters a
         // token (nothing at a reset) makes its gate's gradient
+#pragma unroll 1
         for (int w = 0; w < warp; ++w) {
             const float* o = part[parity][w][lane];
 #pragma unroll
@@ -497,15 +515,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
                 s[c] = through<kReset>(C[k][c], u[k][c] * xv, s[c]);
             }
         float in[kVec];
-        if (R > 1) {
-            receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
-        } else {
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                in[c] = carry[c];
-                carry[c] = through<kReset>(A[c], G[c], carry[c]);
-            }
-        }
+        receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
 #pragma unroll
         for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(sufA[c], sufG[c], in[c]);
         T *px = dx + t0 * p.dx_t, *pf = df + t0 * p.df_t, *pi = kGate ? di + t0 * p.di_t : nullptr;
@@ -521,9 +531,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
                 in[c] = kReset && stops(C[k][c]) ? 0.0f : C[k][c] * gr;
             }
             if (in_d && k < n) {
-                store<kVec>(px + k * p.dx_t, ox);
-                store<kVec>(pf + k * p.df_t, of);
-                if (kGate) store<kVec>(pi + k * p.di_t, oi);
+                store<kVec>(px + k * p.dx_t + dl, ox);
+                store<kVec>(pf + k * p.df_t + dl, of);
+                if (kGate) store<kVec>(pi + k * p.di_t + dl, oi);
             }
         }
     }
