@@ -44,7 +44,8 @@ extern "C" {
  * states are fp32. A sequence array is given by its first element and the
  * element strides of batch rows and tokens; channels are contiguous. So the
  * three inputs may be column slices of one projection's output, and either
- * order of batch and time works. Input strides may be zero (broadcast rows).
+ * order of batch and time works. Input strides may be zero (broadcast rows); a
+ * token stride of 2^31 bytes or more is SSDC_ERR_UNSUPPORTED.
  */
 typedef struct {
     const void *p;

@@ -2,6 +2,7 @@
 // launch sequence per call on the caller's stream. Nothing is allocated.
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 
 #include <cuda_runtime.h>
 
@@ -145,6 +146,13 @@ int done(int launches) {
     return SSDC_OK;
 }
 
+// The kernels step from token to token in 32 bits.
+int check_token_strides(const ssd_gated_dims& d, std::initializer_list<int64_t> strides) {
+    for (int64_t s : strides)
+        if (s >= (int64_t(1) << 31) / (int64_t)type_bytes(d.type)) return SSDC_ERR_UNSUPPORTED;
+    return SSDC_OK;
+}
+
 Gated gated_problem(const ssd_seq_in& x, const ssd_seq_in& f, const ssd_seq_in& i, const ssd_gated_dims& d) {
     Gated p = {};
     p.x = x.p; p.x_b = x.stride_b; p.x_t = x.stride_t;
@@ -197,7 +205,8 @@ int ssd_gated_scan_fwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* h0
     a.output(dense(states, d.B * state_rows(d) * d.D), false);
     a.output(dense(status, 1), false);
     if (a.rc != SSDC_OK) return a.rc;
-    rc = check_device();
+    rc = check_token_strides(d, {x.stride_t, f.stride_t, i.stride_t, h.stride_t});
+    if (rc == SSDC_OK) rc = check_device();
     if (rc != SSDC_OK) return rc;
     Gated p = gated_problem(x, f, i, d);
     p.h0 = h0; p.reset = reset;
@@ -248,7 +257,8 @@ int ssd_gated_scan_bwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* st
     a.output(dense(dh0, d.B * d.D), false, dh_last);
     a.output(dense(status, 1), false);
     if (a.rc != SSDC_OK) return a.rc;
-    rc = check_device();
+    rc = check_token_strides(d, {x.stride_t, f.stride_t, i.stride_t, dh.stride_t, dx.stride_t, df.stride_t, di.stride_t});
+    if (rc == SSDC_OK) rc = check_device();
     if (rc != SSDC_OK) return rc;
     Gated p = gated_problem(x, f, i, d);
     p.in_states = states; p.reset = reset;

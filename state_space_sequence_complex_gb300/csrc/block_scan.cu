@@ -89,13 +89,29 @@ __device__ __forceinline__ void store(float* p, const float (&v)[kVec]) {
     else *p = v[0];
 }
 
+// A run of tokens for a lane's channels, as it goes through shared memory.
+template <int kVec>
+struct alignas(8 * kVec) Run {
+    float A[kVec], H[kVec];
+};
+template <int kVec>
+struct alignas(4 * kVec) Lane {
+    float v[kVec];
+};
+
+// Row k of a few, from the first: the token stride in bytes has 32 bits, so that this is one instruction.
+template <typename T>
+__device__ __forceinline__ T* row(T* first, int k, int32_t stride) {
+    return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(first) + (int64_t)k * stride);
+}
+
 // The totals of the cluster's tiles, by tile, for this CTA's channels: A and H of each of a
 // lane's channels. Two of them, with a barrier each, by the parity of the round: a CTA that
 // sends its total of round i + 2 has taken every CTA's of round i + 1, which each sent when
 // it had used round i's.
 template <int kVec>
 struct Totals {
-    float v[2][kMaxCluster][32][2 * kVec];
+    Run<kVec> v[2][kMaxCluster][32];
     uint64_t full[2];
 };
 constexpr uint64_t kWaitNs = 2000000000ull;  // wait limit
@@ -117,7 +133,7 @@ __device__ __forceinline__ void send_total(Totals<kVec>& t, int64_t round, uint3
                                            const float (&A)[kVec], const float (&H)[kVec]) {
     const int parity = (int)(round & 1);
     if (lane == 0) ptx::mbar_arrive_expect_tx(&t.full[parity], R * 32 * 8 * kVec);
-    const uint32_t at = ptx::smem_addr(t.v[parity][rank][lane]), full = ptx::smem_addr(&t.full[parity]);
+    const uint32_t at = ptx::smem_addr(&t.v[parity][rank][lane]), full = ptx::smem_addr(&t.full[parity]);
     for (uint32_t r = 0; r < R; ++r) {
         const uint32_t to = ptx::mapa(at, r), bar = ptx::mapa(full, r);
         if constexpr (kVec == 2) ptx::st_async_v4(to, make_float4(A[0], A[1], H[0], H[1]), bar);
@@ -138,10 +154,10 @@ __device__ __forceinline__ void receive_totals(Totals<kVec>& t, int64_t round, u
 #pragma unroll
     for (int c = 0; c < kVec; ++c) in[c] = carry[c];
     for (uint32_t r = 0; r < R; ++r) {
-        const float* v = t.v[parity][r][lane];
+        const Run<kVec> o = t.v[parity][r][lane];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
-            carry[c] = through<kReset>(v[c], v[kVec + c], carry[c]);
+            carry[c] = through<kReset>(o.A[c], o.H[c], carry[c]);
             if (r < rank) in[c] = carry[c];
         }
     }
@@ -159,7 +175,7 @@ __device__ __forceinline__ void leave(uint32_t R, bool ok, int* status) {
 template <typename T, int kVec, bool kGate, bool kReset>
 __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const Gated p) {
     __shared__ Totals<kVec> totals;
-    __shared__ float part[2][kWarps][32][2 * kVec];
+    __shared__ Run<kVec> part[2][kWarps][32];
     // (the warp's index from a shuffle: what depends on it alone is then computed once a warp)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
@@ -168,8 +184,9 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
     const int b = (int)(group / groups), d = (int)(group % groups) * 32 * kVec + lane * kVec;
     const bool in_d = d < p.D;
     const int64_t tiles = (p.T + kTile - 1) / kTile;
-    // rows of the batch row b; a lane's channels (a valid lane's where it is past the last) are
-    // added as a 32-bit offset
+    // rows of the batch row b; dl: this lane's channels, or the last ones where there are none
+    constexpr int32_t e = sizeof(T);
+    const int32_t st_x = (int32_t)p.x_t * e, st_f = (int32_t)p.f_t * e, st_i = (int32_t)p.i_t * e, st_h = (int32_t)p.h_t * e;
     const T* x = static_cast<const T*>(p.x) + b * p.x_b;
     const T* f = static_cast<const T*>(p.f) + b * p.f_b;
     const T* g = kGate ? static_cast<const T*>(p.i) + b * p.i_b : nullptr;
@@ -192,13 +209,13 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
             const uint32_t mark = lane < n ? __ldg(reset + t0 + lane) : 0;
             stop = __ballot_sync(0xffffffffu, mark != 0);
         }
-        const T *px = x + t0 * p.x_t, *pf = f + t0 * p.f_t, *pg = kGate ? g + t0 * p.i_t : nullptr;
+        const T *px = x + t0 * p.x_t + dl, *pf = f + t0 * p.f_t + dl, *pg = kGate ? g + t0 * p.i_t + dl : nullptr;
         if (n == kTok) {
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
-                rf[k].load(pf + k * p.f_t + dl);
-                if (kGate) rg[k].load(pg + k * p.i_t + dl);
-                rx[k].load(px + k * p.x_t + dl);
+                rf[k].load(row(pf, k, st_f));
+                if (kGate) rg[k].load(row(pg, k, st_i));
+                rx[k].load(row(px, k, st_x));
             }
         } else {
 #pragma unroll
@@ -207,9 +224,9 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
                 rf[k].zero();
                 if (kGate) rg[k].zero();
                 if (k < n) {
-                    rf[k].load(pf + k * p.f_t + dl);
-                    if (kGate) rg[k].load(pg + k * p.i_t + dl);
-                    rx[k].load(px + k * p.x_t + dl);
+                    rf[k].load(row(pf, k, st_f));
+                    if (kGate) rg[k].load(row(pg, k, st_i));
+                    rx[k].load(row(px, k, st_x));
                 }
             }
         }
@@ -266,12 +283,13 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
                 }
         }
         if (tile - rank + R < tiles) load(tile + R);
-        float* mine = part[parity][warp][lane];
+        Run<kVec> mine;
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
-            mine[c] = A[c];
-            mine[kVec + c] = H[c];
+            mine.A[c] = A[c];
+            mine.H[c] = H[c];
         }
+        part[parity][warp][lane] = mine;
         __syncthreads();
         // the tile's warps before this one; the last warp adds its own and has the tile's total
         float preA[kVec], preH[kVec];
@@ -282,11 +300,11 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
         }
 #pragma unroll 1
         for (int w = 0; w < warp; ++w) {
-            const float* o = part[parity][w][lane];
+            const Run<kVec> o = part[parity][w][lane];
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
-                preH[c] = through<kReset>(o[c], o[kVec + c], preH[c]);
-                preA[c] = both<kReset>(preA[c], o[c]);
+                preH[c] = through<kReset>(o.A[c], o.H[c], preH[c]);
+                preA[c] = both<kReset>(preA[c], o.A[c]);
             }
         }
         if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -307,20 +325,20 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
         }
 #pragma unroll
         for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(preA[c], preH[c], in[c]);
-        T* ph = h + (tile * kTile + warp * kTok) * p.h_t;
+        T* ph = h + (tile * kTile + warp * kTok) * p.h_t + dl;
         if (plain) {
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
 #pragma unroll
                 for (int c = 0; c < kVec; ++c) in[c] = fmaf(C[k][c], in[c], v[k][c]);
-                if (in_d) store<kVec>(ph + k * p.h_t + dl, in);
+                if (in_d) store<kVec>(row(ph, k, st_h), in);
             }
         } else {
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
 #pragma unroll
                 for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(C[k][c], v[k][c], in[c]);
-                if (k < rows && in_d) store<kVec>(ph + k * p.h_t + dl, in);
+                if (k < rows && in_d) store<kVec>(row(ph, k, st_h), in);
             }
         }
     }
@@ -338,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
 template <typename T, int kVec, bool kGate, bool kReset>
 __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
     __shared__ Totals<kVec> totals;
-    __shared__ float part[2][kWarps][32][4 * kVec];  // A, G, H of a lane's channels
+    __shared__ Run<kVec> part[2][kWarps][32];        // A and G
+    __shared__ Lane<kVec> part_h[2][kWarps][32];     // H
     // (the warp's index from a shuffle: what depends on it alone is then computed once a warp)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
@@ -350,6 +369,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
     const T* x = static_cast<const T*>(p.x) + b * p.x_b;
     const T* f = static_cast<const T*>(p.f) + b * p.f_b;
     const T* g = kGate ? static_cast<const T*>(p.i) + b * p.i_b : nullptr;
+    constexpr int32_t e = sizeof(T);
+    const int32_t st_x = (int32_t)p.x_t * e, st_f = (int32_t)p.f_t * e, st_i = (int32_t)p.i_t * e, st_dh = (int32_t)p.dh_t * e;
+    const int32_t st_dx = (int32_t)p.dx_t * e, st_df = (int32_t)p.df_t * e, st_di = (int32_t)p.di_t * e;
     const T* dh = static_cast<const T*>(p.dh) + b * p.dh_b;
     T* dx = static_cast<T*>(p.dx) + b * p.dx_b;
     T* df = static_cast<T*>(p.df) + b * p.df_b;
@@ -382,14 +404,15 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
         for (int c = 0; c < kVec; ++c)
             s[c] = tile >= 0 && in_d ? __ldg(p.in_states + ((int64_t)b * tiles + tile) * p.D + d + c) : 0.0f;
         {
-            const T *px = x + t0 * p.x_t, *pf = f + t0 * p.f_t, *ph = dh + t0 * p.dh_t, *pg = kGate ? g + t0 * p.i_t : nullptr;
+            const T *px = x + t0 * p.x_t + dl, *pf = f + t0 * p.f_t + dl, *ph = dh + t0 * p.dh_t + dl;
+            const T* pg = kGate ? g + t0 * p.i_t + dl : nullptr;
             if (n == kTok) {
 #pragma unroll
                 for (int k = 0; k < kTok; ++k) {
-                    rf[k].load(pf + k * p.f_t + dl);
-                    if (kGate) rg[k].load(pg + k * p.i_t + dl);
-                    rx[k].load(px + k * p.x_t + dl);
-                    rh[k].load(ph + k * p.dh_t + dl);
+                    rf[k].load(row(pf, k, st_f));
+                    if (kGate) rg[k].load(row(pg, k, st_i));
+                    rx[k].load(row(px, k, st_x));
+                    rh[k].load(row(ph, k, st_dh));
                 }
             } else {
 #pragma unroll
@@ -399,10 +422,10 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
                     rh[k].zero();
                     if (kGate) rg[k].zero();
                     if (k < n) {
-                        rf[k].load(pf + k * p.f_t + dl);
-                        if (kGate) rg[k].load(pg + k * p.i_t + dl);
-                        rx[k].load(px + k * p.x_t + dl);
-                        rh[k].load(ph + k * p.dh_t + dl);
+                        rf[k].load(row(pf, k, st_f));
+                        if (kGate) rg[k].load(row(pg, k, st_i));
+                        rx[k].load(row(px, k, st_x));
+                        rh[k].load(row(ph, k, st_dh));
                     }
                 }
             }
@@ -464,13 +487,16 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
 #pragma unroll
                 for (int c = 0; c < kVec; ++c) G[c] = through<kReset>(C[k][c], 0.0f, rh[k].get(c) + G[c]);
         }
-        float* mine = part[parity][warp][lane];
+        Run<kVec> mine;
+        Lane<kVec> mine_h;
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
-            mine[c] = A[c];
-            mine[kVec + c] = G[c];
-            mine[2 * kVec + c] = H[c];
+            mine.A[c] = A[c];
+            mine.H[c] = G[c];
+            mine_h.v[c] = H[c];
         }
+        part[parity][warp][lane] = mine;
+        part_h[parity][warp][lane] = mine_h;
         __syncthreads();
         // the gradient's run through the tile's warps after this one; the first warp adds its own
         // and has the tile's total
@@ -482,11 +508,11 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
         }
 #pragma unroll 1
         for (int w = kWarps - 1; w > warp; --w) {
-            const float* o = part[parity][w][lane];
+            const Run<kVec> o = part[parity][w][lane];
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
-                sufG[c] = through<kReset>(o[c], o[kVec + c], sufG[c]);
-                sufA[c] = both<kReset>(sufA[c], o[c]);
+                sufG[c] = through<kReset>(o.A[c], o.H[c], sufG[c]);
+                sufA[c] = both<kReset>(sufA[c], o.A[c]);
             }
         }
         if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -502,9 +528,10 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
         // token (nothing at a reset) makes its gate's gradient
 #pragma unroll 1
         for (int w = 0; w < warp; ++w) {
-            const float* o = part[parity][w][lane];
+            const Run<kVec> o = part[parity][w][lane];
+            const Lane<kVec> oh = part_h[parity][w][lane];
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) s[c] = through<kReset>(o[c], o[2 * kVec + c], s[c]);
+            for (int c = 0; c < kVec; ++c) s[c] = through<kReset>(o.A[c], oh.v[c], s[c]);
         }
 #pragma unroll
         for (int k = 0; k < kTok; ++k)
@@ -518,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
         receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
 #pragma unroll
         for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(sufA[c], sufG[c], in[c]);
-        T *px = dx + t0 * p.dx_t, *pf = df + t0 * p.df_t, *pi = kGate ? di + t0 * p.di_t : nullptr;
+        T *px = dx + t0 * p.dx_t + dl, *pf = df + t0 * p.df_t + dl, *pi = kGate ? di + t0 * p.di_t + dl : nullptr;
 #pragma unroll
         for (int k = kTok - 1; k >= 0; --k) {
             float ox[kVec], of[kVec], oi[kVec];
@@ -531,9 +558,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
                 in[c] = kReset && stops(C[k][c]) ? 0.0f : C[k][c] * gr;
             }
             if (in_d && k < n) {
-                store<kVec>(px + k * p.dx_t + dl, ox);
-                store<kVec>(pf + k * p.df_t + dl, of);
-                if (kGate) store<kVec>(pi + k * p.di_t + dl, oi);
+                store<kVec>(row(px, k, st_dx), ox);
+                store<kVec>(row(pf, k, st_df), of);
+                if (kGate) store<kVec>(row(pi, k, st_di), oi);
             }
         }
     }

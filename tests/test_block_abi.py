@@ -54,7 +54,7 @@ def fwd(lib, **k):
     (dict(x=NONE), INVALID), (dict(f=NONE), INVALID), (dict(h=NONE), INVALID), (dict(h_last=None), INVALID),
     (dict(x=SEQ(at(1) + 1)), ALIGN), (dict(h=SEQ(at(6) + 1)), ALIGN), (dict(h0=at(4) + 2), ALIGN),
     (dict(x=SEQ(at(1), -1)), INVALID), (dict(x=SEQ(at(1), 6400, -64)), INVALID),
-    (dict(x=SEQ(at(1), 1 << 50)), INVALID),
+    (dict(x=SEQ(at(1), 1 << 50)), INVALID), (dict(x=SEQ(1 << 45, 64, 1 << 30)), UNSUPPORTED),
     (dict(h=SEQ(at(1))), INVALID), (dict(h=SEQ(at(3) + 2)), INVALID),         # over an input
     (dict(h=SEQ(at(6), 0)), INVALID), (dict(h=SEQ(at(6), 6400, 63)), INVALID),  # rows on top of each other
     (dict(h=SEQ(at(6), 640, 64)), INVALID),
