@@ -19,6 +19,7 @@
 
 #include "block_common.cuh"
 #include "block_kernels.h"
+#include "block_scan.cuh"
 #include "ptx.cuh"
 #include "ssdc_kernels.h"
 
@@ -27,24 +28,10 @@ namespace block {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps, kTok = 8, kTile = kWarps * kTok;
-static_assert(kTile == SSD_GATED_STATE_TOKENS, "a state is kept for every tile");
-constexpr int kMaxCluster = 8;
+using namespace gated;
 
-// A reset stops everything that comes before it, an infinity or a NaN too, so it is not the
-// factor 0 but a mark of its own in A: the value -0, which no product of gates takes.
-constexpr float kStop = -0.0f;
-__device__ __forceinline__ bool stops(float A) { return __float_as_uint(A) == 0x80000000u; }
-// The state behind a run, from the one before it.
-template <bool kReset>
-__device__ __forceinline__ float through(float A, float H, float h) {
-    return kReset && stops(A) ? H : fmaf(A, h, H);
-}
-// The factor of two runs, the first one first.
-template <bool kReset>
-__device__ __forceinline__ float both(float A1, float A2) {
-    return kReset && (stops(A1) || stops(A2)) ? kStop : A1 * A2;
-}
+constexpr int kTok = 8, kTile = kWarps * kTok;
+static_assert(kTile == SSD_GATED_STATE_TOKENS, "a state is kept for every tile");
 
 // kVec adjacent channels of one token, as they are in memory.
 template <typename T, int kVec>
@@ -89,87 +76,10 @@ __device__ __forceinline__ void store(float* p, const float (&v)[kVec]) {
     else *p = v[0];
 }
 
-// A run of tokens for a lane's channels, as it goes through shared memory.
-template <int kVec>
-struct alignas(8 * kVec) Run {
-    float A[kVec], H[kVec];
-};
-template <int kVec>
-struct alignas(4 * kVec) Lane {
-    float v[kVec];
-};
-
 // Row k of a few, from the first: the token stride in bytes has 32 bits, so that this is one instruction.
 template <typename T>
 __device__ __forceinline__ T* row(T* first, int k, int32_t stride) {
     return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(first) + (int64_t)k * stride);
-}
-
-// The totals of the cluster's tiles, by tile, for this CTA's channels: A and H of each of a
-// lane's channels. Two of them, with a barrier each, by the parity of the round: a CTA that
-// sends its total of round i + 2 has taken every CTA's of round i + 1, which each sent when
-// it had used round i's.
-template <int kVec>
-struct Totals {
-    Run<kVec> v[2][kMaxCluster][32];
-    uint64_t full[2];
-};
-constexpr uint64_t kWaitNs = 2000000000ull;  // wait limit
-
-template <int kVec>
-__device__ __forceinline__ void totals_init(Totals<kVec>& t, uint32_t R) {
-    if (threadIdx.x == 0) {
-        ptx::mbar_init(&t.full[0], 1);
-        ptx::mbar_init(&t.full[1], 1);
-        ptx::fence_mbar_init();
-    }
-    // (a CTA's shared memory may be written to once it runs and its barriers are there)
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-
-// This CTA's total to every CTA of the cluster, its own too; by one warp.
-template <int kVec>
-__device__ __forceinline__ void send_total(Totals<kVec>& t, int64_t round, uint32_t rank, uint32_t R, int lane,
-                                           const float (&A)[kVec], const float (&H)[kVec]) {
-    const int parity = (int)(round & 1);
-    if (lane == 0) ptx::mbar_arrive_expect_tx(&t.full[parity], R * 32 * 8 * kVec);
-    const uint32_t at = ptx::smem_addr(&t.v[parity][rank][lane]), full = ptx::smem_addr(&t.full[parity]);
-    for (uint32_t r = 0; r < R; ++r) {
-        const uint32_t to = ptx::mapa(at, r), bar = ptx::mapa(full, r);
-        if constexpr (kVec == 2) ptx::st_async_v4(to, make_float4(A[0], A[1], H[0], H[1]), bar);
-        else ptx::st_async_v2(to, make_float2(A[0], H[0]), bar);
-    }
-}
-
-// A wait that gives up makes the results NaN from there on, and later waits give up at once.
-template <int kVec, bool kReset>
-__device__ __forceinline__ void receive_totals(Totals<kVec>& t, int64_t round, uint32_t rank, uint32_t R, int lane,
-                                               float (&carry)[kVec], float (&in)[kVec], bool& ok) {
-    const int parity = (int)(round & 1);
-    ok = ptx::mbar_wait(&t.full[parity], (uint32_t)(round >> 1) & 1, ok ? kWaitNs : 0) && ok;
-    if (!ok) {
-#pragma unroll
-        for (int c = 0; c < kVec; ++c) carry[c] = __int_as_float(0x7fffffff);
-    }
-#pragma unroll
-    for (int c = 0; c < kVec; ++c) in[c] = carry[c];
-    for (uint32_t r = 0; r < R; ++r) {
-        const Run<kVec> o = t.v[parity][r][lane];
-#pragma unroll
-        for (int c = 0; c < kVec; ++c) {
-            carry[c] = through<kReset>(o.A[c], o.H[c], carry[c]);
-            if (r < rank) in[c] = carry[c];
-        }
-    }
-}
-
-// No CTA leaves while another may still send to it (where a wait gave up).
-__device__ __forceinline__ void leave(uint32_t R, bool ok, int* status) {
-    if (!ok && status) atomicCAS(status, SSDC_OK, SSDC_ERR_TIMEOUT);
-    if (R > 1) {
-        ptx::cluster_arrive_relaxed();
-        ptx::cluster_wait();
-    }
 }
 
 template <typename T, int kVec, bool kGate, bool kReset>
@@ -205,10 +115,7 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
         const int64_t t0 = tile * kTile + warp * kTok;
         n = (int)max((int64_t)0, min((int64_t)kTok, p.T - t0));
         stop = 0;
-        if (kReset) {
-            const uint32_t mark = lane < n ? __ldg(reset + t0 + lane) : 0;
-            stop = __ballot_sync(0xffffffffu, mark != 0);
-        }
+        if (kReset) stop = marks(reset, t0, n, lane);
         const T *px = x + t0 * p.x_t + dl, *pf = f + t0 * p.f_t + dl, *pg = kGate ? g + t0 * p.i_t + dl : nullptr;
         if (n == kTok) {
 #pragma unroll
@@ -394,10 +301,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
         const int64_t tile = tiles - 1 - back, t0 = tile * kTile + warp * kTok;
         const int n = tile < 0 ? 0 : (int)max((int64_t)0, min((int64_t)kTok, p.T - t0));
         uint32_t stop = 0;
-        if (kReset) {
-            const uint32_t mark = lane < n ? __ldg(reset + t0 + lane) : 0;
-            stop = __ballot_sync(0xffffffffu, mark != 0);
-        }
+        if (kReset) stop = marks(reset, t0, n, lane);
         Raw<T, kVec> rx[kTok], rf[kTok], rg[kTok], rh[kTok];
         float s[kVec];
 #pragma unroll
@@ -599,31 +503,10 @@ bool pairs_ok(const void* q, int64_t sb, int64_t st, size_t elem) {
     return q == nullptr || (reinterpret_cast<uintptr_t>(q) % (2 * elem) == 0 && sb % 2 == 0 && st % 2 == 0);
 }
 
-// Tiles a cluster takes at a time: enough CTAs to fill the GPU's SMs several times over with
-// as few exchanges as that allows.
-int cluster_size(const Gated& p, int64_t groups) {
-    const int64_t tiles = (p.T + kTile - 1) / kTile;
-    int R = 1;
-    while (R < kMaxCluster && R < tiles && groups * R < 152 * 3) R *= 2;
-    return R;
-}
-
 template <typename K>
 int launch_cluster(K kernel, const Gated& p, int vec, cudaStream_t stream) {
     const int64_t groups = (int64_t)p.B * ((p.D + 32 * vec - 1) / (32 * vec));
-    const int R = cluster_size(p, groups);
-    if (groups * R > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(groups * R));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = R;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? 1 : SSDC_ERR_CUDA;
+    return launch_clusters(kernel, groups, cluster_size((p.T + kTile - 1) / kTile, groups, 152 * 3), 0, stream, p);
 }
 
 template <typename T, int kVec, bool kGate>
@@ -654,8 +537,14 @@ int launch_scan(const Gated& p, int what, cudaStream_t stream) {
 
 }  // namespace
 
-int gated_fwd_launch(const Gated& p, cudaStream_t stream) { return launch_scan(p, 0, stream); }
-int gated_bwd_launch(const Gated& p, cudaStream_t stream) { return launch_scan(p, 1, stream); }
+int gated_fwd_launch(const Gated& p, cudaStream_t stream) {
+    const int n = gated::tma_fwd_launch(p, stream);
+    return n != 0 ? n : launch_scan(p, 0, stream);
+}
+int gated_bwd_launch(const Gated& p, cudaStream_t stream) {
+    const int n = gated::tma_bwd_launch(p, stream);
+    return n != 0 ? n : launch_scan(p, 1, stream);
+}
 int gated_step_launch(const Gated& p, cudaStream_t stream) { return launch_scan(p, 2, stream); }
 
 }  // namespace block

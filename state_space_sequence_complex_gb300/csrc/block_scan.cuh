@@ -1,0 +1,152 @@
+// What the gated scan's kernels share (block_scan.cu, block_scan_tma.cu): how runs of tokens
+// are joined, within a tile and across the tiles of a cluster.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "block_common.cuh"
+#include "block_kernels.h"
+#include "ptx.cuh"
+
+namespace ssdc {
+namespace block {
+namespace gated {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kMaxCluster = 8;
+
+// A reset stops everything that comes before it, an infinity or a NaN too, so it is not the
+// factor 0 but a mark of its own in A: the value -0, which no product of gates takes.
+constexpr float kStop = -0.0f;
+__device__ __forceinline__ bool stops(float A) { return __float_as_uint(A) == 0x80000000u; }
+// The state behind a run, from the one before it.
+template <bool kReset>
+__device__ __forceinline__ float through(float A, float H, float h) {
+    return kReset && stops(A) ? H : fmaf(A, h, H);
+}
+// The factor of two runs, the first one first.
+template <bool kReset>
+__device__ __forceinline__ float both(float A1, float A2) {
+    return kReset && (stops(A1) || stops(A2)) ? kStop : A1 * A2;
+}
+
+// A run of tokens for a lane's channels, as it goes through shared memory.
+template <int kVec>
+struct alignas(8 * kVec) Run {
+    float A[kVec], H[kVec];
+};
+template <int kVec>
+struct alignas(4 * kVec) Lane {
+    float v[kVec];
+};
+
+// The totals of the cluster's tiles, by tile, for this CTA's channels: A and H of each of a
+// lane's channels. Two of them, with a barrier each, by the parity of the round: a CTA that
+// sends its total of round i + 2 has taken every CTA's of round i + 1, which each sent when
+// it had used round i's.
+template <int kVec>
+struct Totals {
+    Run<kVec> v[2][kMaxCluster][32];
+    uint64_t full[2];
+};
+constexpr uint64_t kWaitNs = 2000000000ull;  // wait limit
+
+template <int kVec>
+__device__ __forceinline__ void totals_init(Totals<kVec>& t, uint32_t R) {
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(&t.full[0], 1);
+        ptx::mbar_init(&t.full[1], 1);
+        ptx::fence_mbar_init();
+    }
+    // (a CTA's shared memory may be written to once it runs and its barriers are there)
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+
+// This CTA's total to every CTA of the cluster, its own too; by one warp.
+template <int kVec>
+__device__ __forceinline__ void send_total(Totals<kVec>& t, int64_t round, uint32_t rank, uint32_t R, int lane,
+                                           const float (&A)[kVec], const float (&H)[kVec]) {
+    const int parity = (int)(round & 1);
+    if (lane == 0) ptx::mbar_arrive_expect_tx(&t.full[parity], R * 32 * 8 * kVec);
+    const uint32_t at = ptx::smem_addr(&t.v[parity][rank][lane]), full = ptx::smem_addr(&t.full[parity]);
+    for (uint32_t r = 0; r < R; ++r) {
+        const uint32_t to = ptx::mapa(at, r), bar = ptx::mapa(full, r);
+        if constexpr (kVec == 2) ptx::st_async_v4(to, make_float4(A[0], A[1], H[0], H[1]), bar);
+        else ptx::st_async_v2(to, make_float2(A[0], H[0]), bar);
+    }
+}
+
+// A wait that gives up makes the results NaN from there on, and later waits give up at once.
+template <int kVec, bool kReset>
+__device__ __forceinline__ void receive_totals(Totals<kVec>& t, int64_t round, uint32_t rank, uint32_t R, int lane,
+                                               float (&carry)[kVec], float (&in)[kVec], bool& ok) {
+    const int parity = (int)(round & 1);
+    ok = ptx::mbar_wait(&t.full[parity], (uint32_t)(round >> 1) & 1, ok ? kWaitNs : 0) && ok;
+    if (!ok) {
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) carry[c] = __int_as_float(0x7fffffff);
+    }
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) in[c] = carry[c];
+    for (uint32_t r = 0; r < R; ++r) {
+        const Run<kVec> o = t.v[parity][r][lane];
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+            carry[c] = through<kReset>(o.A[c], o.H[c], carry[c]);
+            if (r < rank) in[c] = carry[c];
+        }
+    }
+}
+
+// No CTA leaves while another may still send to it (where a wait gave up).
+__device__ __forceinline__ void leave(uint32_t R, bool ok, int* status) {
+    if (!ok && status) atomicCAS(status, SSDC_OK, SSDC_ERR_TIMEOUT);
+    if (R > 1) {
+        ptx::cluster_arrive_relaxed();
+        ptx::cluster_wait();
+    }
+}
+
+// The marks of a warp's tokens that start a document, one bit each: the lane's token is marked.
+__device__ __forceinline__ uint32_t marks(const uint8_t* reset, int64_t t0, int n, int lane) {
+    const uint32_t mark = lane < n ? __ldg(reset + t0 + lane) : 0;
+    return __ballot_sync(0xffffffffu, mark != 0);
+}
+
+// Tiles that a cluster takes at a time: enough CTAs to fill the GPU's SMs several times over
+// with as few exchanges as that allows.
+inline int cluster_size(int64_t tiles, int64_t groups, int ctas) {
+    int R = 1;
+    while (R < kMaxCluster && R < tiles && groups * R < ctas) R *= 2;
+    return R;
+}
+
+// A kernel on `groups` clusters of R CTAs.
+template <typename... KArgs, typename... Args>
+inline int launch_clusters(void (*kernel)(KArgs...), int64_t groups, int R, size_t smem, cudaStream_t stream,
+                           const Args&... args) {
+    if (groups * R > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(groups * R));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = R;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 1 : SSDC_ERR_CUDA;
+}
+
+// The forward and backward passes by TMA copies (block_scan_tma.cu): the launches, or 0 where
+// the arrays or sizes do not allow it.
+int tma_fwd_launch(const Gated& p, cudaStream_t stream);
+int tma_bwd_launch(const Gated& p, cudaStream_t stream);
+
+}  // namespace gated
+}  // namespace block
+}  // namespace ssdc

@@ -1,0 +1,546 @@
+// Gated scan by TMA copies: the forward and backward passes of block_scan.cu, joined the same
+// way, for arrays that tensor maps can describe (rows and strides of whole 16-byte units).
+//
+// The scan costs about as many instructions as HBM allows it: 2.9 elements a cycle and SM at
+// 8 bytes an element leave 44 of them each. A thread that loads its rows itself spends a
+// third of those on addresses. Here a warp's rows come and go as one copy for each array:
+// an element is then read from shared memory at a constant offset, its result is written
+// over it and copied out from there, and the next rows are on their way meanwhile.
+//
+// Every warp copies its own tokens and waits for them alone; the CTA meets once a tile.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "block_common.cuh"
+#include "block_kernels.h"
+#include "block_scan.cuh"
+#include "ptx.cuh"
+#include "ssdc_kernels.h"
+#include "tc_common.cuh"
+
+namespace ssdc {
+namespace block {
+namespace gated {
+
+namespace {
+
+constexpr int kStages = 2;
+
+struct FwdMaps {
+    CUtensorMap x, f, i, h;
+};
+struct BwdMaps {
+    CUtensorMap x, f, i, dh, dx, df, di;
+};
+
+// A lane's word of a row in shared memory: two bfloat16 channels or one fp32.
+template <typename T>
+struct Word;
+template <>
+struct Word<__nv_bfloat16> {
+    static constexpr int kVec = 2;
+    static __device__ __forceinline__ void get(const char* at, float (&v)[2]) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(at);
+        v[0] = ptx::bf16_lo(w);
+        v[1] = ptx::bf16_hi(w);
+    }
+    static __device__ __forceinline__ void put(char* at, const float (&v)[2]) {
+        *reinterpret_cast<__nv_bfloat162*>(at) = __floats2bfloat162_rn(v[0], v[1]);
+    }
+};
+template <>
+struct Word<float> {
+    static constexpr int kVec = 1;
+    static __device__ __forceinline__ void get(const char* at, float (&v)[1]) { v[0] = *reinterpret_cast<const float*>(at); }
+    static __device__ __forceinline__ void put(char* at, const float (&v)[1]) { *reinterpret_cast<float*>(at) = v[0]; }
+};
+
+// Copies in flight get the time to end before a CTA leaves after a wait that gave up.
+__device__ __forceinline__ void pause_if(bool failed) {
+    if (!failed) return;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - t0 < 2000000) {
+    }
+}
+
+// Shared memory of a CTA: for every stage and warp the rows of each array, 128 bytes a row.
+template <int kTok, int kArrays>
+constexpr uint32_t warp_bytes() { return kTok * 128 * kArrays; }
+template <int kTok, int kArrays>
+constexpr uint32_t smem_bytes() { return kStages * kWarps * warp_bytes<kTok, kArrays>() + 128; }
+
+constexpr int kFwdTok = 16, kBwdTok = 8;
+
+template <typename T, bool kGate, bool kReset>
+__global__ void __launch_bounds__(kThreads, 2) gated_fwd_tma(const __grid_constant__ FwdMaps maps, const Gated p) {
+    constexpr int kVec = Word<T>::kVec, kTok = kFwdTok, kTile = kWarps * kTok, kArrays = kGate ? 3 : 2;
+    constexpr uint32_t kWarp = warp_bytes<kTok, kArrays>(), kArray = kTok * 128;
+    extern __shared__ char smem_raw[];
+    char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    __shared__ Totals<kVec> totals;
+    __shared__ Run<kVec> part[2][kWarps][32];
+    __shared__ uint64_t full[kStages][kWarps];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
+    if (lane == 0)
+        for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s][warp], 1);
+    totals_init(totals, R);  // (and its fence)
+    const int groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
+    const int b = group / groups, d0 = group % groups * 32 * kVec, d = d0 + lane * kVec;
+    const bool in_d = d < p.D;
+    const int T_ = (int)p.T, tiles = (T_ + kTile - 1) / kTile;
+    const int64_t state_at = (int64_t)b * p.D + d, state_rows = (p.T + SSD_GATED_STATE_TOKENS - 1) / SSD_GATED_STATE_TOKENS;
+    const uint8_t* reset = kReset ? p.reset + (int64_t)b * p.T : nullptr;
+
+    float carry[kVec];
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) carry[c] = p.h0 && in_d ? p.h0[state_at + c] : 0.0f;
+
+    // the copies of this warp's rows of the CTA's tile of a round (none where they are all past the end: the barrier's phase passes all the same)
+    auto fetch = [&](int round) {
+        const int t0 = (round * (int)R + (int)rank) * kTile + warp * kTok;
+        uint64_t* bar = &full[round % kStages][warp];
+        if (t0 >= T_) return ptx::mbar_arrive(bar);
+        char* at = smem + (round % kStages * kWarps + warp) * kWarp;
+        ptx::mbar_arrive_expect_tx(bar, kWarp);
+        ptx::tma_load_3d(at, &maps.x, bar, d0, t0, b);
+        ptx::tma_load_3d(at + kArray, &maps.f, bar, d0, t0, b);
+        if (kGate) ptx::tma_load_3d(at + 2 * kArray, &maps.i, bar, d0, t0, b);
+    };
+    __syncwarp();
+    if (lane == 0) fetch(0);
+    bool ok = true;
+    const int rounds = (tiles + (int)R - 1) / (int)R;
+    uint32_t stop_next = kReset ? marks(reset, (int64_t)rank * kTile + warp * kTok, min(kTok, T_ - ((int)rank * kTile + warp * kTok)), lane) : 0;
+    for (int round = 0; round < rounds; ++round) {
+        const int parity = round & 1, t0 = (round * (int)R + (int)rank) * kTile + warp * kTok, n = min(kTok, T_ - t0);
+        const uint32_t stop = stop_next;
+        if (lane == 0 && round + 1 < rounds) {
+            ptx::bulk_wait_read<0>();  // the rows of the round before last have been copied out
+            fetch(round + 1);
+        }
+        __syncwarp();
+        ok = ptx::mbar_wait(&full[round % kStages][warp], round / kStages & 1, ok ? kWaitNs : 0) && ok;
+        char* at = smem + (round % kStages * kWarps + warp) * kWarp + lane * 4;
+        if (kReset && round + 1 < rounds) {
+            const int t1 = t0 + (int)R * kTile;
+            stop_next = marks(reset, t1, min(kTok, T_ - t1), lane);
+        }
+        // a warp whose tokens are all there and start no document takes the short way
+        const bool plain = n == kTok && (!kReset || stop == 0);
+        float C[kTok][kVec], v[kTok][kVec], A[kVec], H[kVec];
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+            A[c] = 1.0f;
+            H[c] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < kTok; ++k) {
+            float x[kVec], f[kVec], g[kVec];
+            Word<T>::get(at + k * 128, x);
+            Word<T>::get(at + kArray + k * 128, f);
+            if (kGate) Word<T>::get(at + 2 * kArray + k * 128, g);
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                float u;
+                if (kGate) {
+                    C[k][c] = sigmoid(f[c]);
+                    u = sigmoid(g[c]);
+                } else {
+                    sigmoid_pair(f[c], C[k][c], u);
+                }
+                v[k][c] = u * x[c];
+            }
+        }
+        if (plain) {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k)
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    H[c] = fmaf(C[k][c], H[c], v[k][c]);
+                    A[c] *= C[k][c];
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k)
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    // tokens past the end leave the state as it is
+                    if (k >= n) {
+                        C[k][c] = 1.0f;
+                        v[k][c] = 0.0f;
+                    } else if (kReset && (stop >> k & 1)) {
+                        C[k][c] = kStop;
+                    }
+                    H[c] = through<kReset>(C[k][c], v[k][c], H[c]);
+                    A[c] = both<kReset>(A[c], C[k][c]);
+                }
+        }
+        Run<kVec> mine;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+            mine.A[c] = A[c];
+            mine.H[c] = H[c];
+        }
+        part[parity][warp][lane] = mine;
+        __syncthreads();
+        // the tile's warps before this one; the last warp adds its own and has the tile's total
+        float preA[kVec], preH[kVec];
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+            preA[c] = 1.0f;
+            preH[c] = 0.0f;
+        }
+#pragma unroll 1
+        for (int w = 0; w < warp; ++w) {
+            const Run<kVec> o = part[parity][w][lane];
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                preH[c] = through<kReset>(o.A[c], o.H[c], preH[c]);
+                preA[c] = both<kReset>(preA[c], o.A[c]);
+            }
+        }
+        if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        if (warp == kWarps - 1) {
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                H[c] = through<kReset>(A[c], H[c], preH[c]);
+                A[c] = both<kReset>(preA[c], A[c]);
+            }
+            send_total<kVec>(totals, round, rank, R, lane, A, H);
+        }
+        float in[kVec];
+        receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(preA[c], preH[c], in[c]);
+        if (p.states && t0 % SSD_GATED_STATE_TOKENS == 0 && n > 0 && in_d) {
+            float* s = p.states + ((int64_t)b * state_rows + t0 / SSD_GATED_STATE_TOKENS) * p.D + d;
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) s[c] = in[c];
+        }
+        // h over x (rows past the end are not copied out)
+        if (plain) {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) {
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) in[c] = fmaf(C[k][c], in[c], v[k][c]);
+                Word<T>::put(at + k * 128, in);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k) {
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(C[k][c], v[k][c], in[c]);
+                Word<T>::put(at + k * 128, in);
+            }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && n > 0) {
+            ptx::tma_store_3d(&maps.h, at, d0, t0, b);
+            ptx::bulk_commit();
+        }
+    }
+    if (rank == 0 && warp == 0 && in_d) {
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) p.h_last[state_at + c] = carry[c];
+    }
+    if (lane == 0) ptx::bulk_wait_all();
+    pause_if(!ok);
+    leave(R, ok, p.status);
+}
+
+template <typename T, bool kGate, bool kReset>
+__global__ void __launch_bounds__(kThreads, 2) gated_bwd_tma(const __grid_constant__ BwdMaps maps, const Gated p) {
+    constexpr int kVec = Word<T>::kVec, kTok = kBwdTok, kTile = kWarps * kTok, kArrays = kGate ? 4 : 3;
+    static_assert(kTile == SSD_GATED_STATE_TOKENS, "a state is kept for every tile");
+    constexpr uint32_t kWarp = warp_bytes<kTok, kArrays>(), kArray = kTok * 128;
+    extern __shared__ char smem_raw[];
+    char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    __shared__ Totals<kVec> totals;
+    __shared__ Run<kVec> part[2][kWarps][32];     // A and G
+    __shared__ Lane<kVec> part_h[2][kWarps][32];  // H
+    __shared__ uint64_t full[kStages][kWarps];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
+    if (lane == 0)
+        for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s][warp], 1);
+    totals_init(totals, R);
+    const int groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
+    const int b = group / groups, d0 = group % groups * 32 * kVec, d = d0 + lane * kVec;
+    const bool in_d = d < p.D;
+    const int T_ = (int)p.T, tiles = (T_ + kTile - 1) / kTile;
+    const int64_t state_at = (int64_t)b * p.D + d;
+    const uint8_t* reset = kReset ? p.reset + (int64_t)b * p.T : nullptr;
+
+    float carry[kVec];
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) carry[c] = p.dh_last && in_d ? p.dh_last[state_at + c] : 0.0f;
+
+    // the first token of this warp in a round, counted from the last tile; negative: none
+    auto first = [&](int round) { return (tiles - 1 - (round * (int)R + (int)rank)) * kTile + warp * kTok; };
+    auto has = [&](int t0) { return t0 >= warp * kTok && t0 < T_; };
+    float s_next[kVec];
+    uint32_t stop_next = 0;
+    auto fetch = [&](int round) {
+        const int t0 = first(round);
+        uint64_t* bar = &full[round % kStages][warp];
+        if (!has(t0)) return ptx::mbar_arrive(bar);
+        char* at = smem + (round % kStages * kWarps + warp) * kWarp;
+        ptx::mbar_arrive_expect_tx(bar, kWarp);
+        ptx::tma_load_3d(at + kArray, &maps.f, bar, d0, t0, b);
+        if (kGate) ptx::tma_load_3d(at + 3 * kArray, &maps.i, bar, d0, t0, b);
+        ptx::tma_load_3d(at, &maps.x, bar, d0, t0, b);
+        ptx::tma_load_3d(at + 2 * kArray, &maps.dh, bar, d0, t0, b);
+    };
+    auto load_ahead = [&](int round) {  // the tile's state and marks
+        const int t0 = first(round), tile = tiles - 1 - (round * (int)R + (int)rank);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c)
+            s_next[c] = tile >= 0 && in_d ? __ldg(p.in_states + ((int64_t)b * tiles + tile) * p.D + d + c) : 0.0f;
+        if (kReset) stop_next = marks(reset, t0, has(t0) ? min(kTok, T_ - t0) : 0, lane);
+    };
+    __syncwarp();
+    if (lane == 0) fetch(0);
+    load_ahead(0);
+    bool ok = true;
+    const int rounds = (tiles + (int)R - 1) / (int)R;
+    for (int round = 0; round < rounds; ++round) {
+        const int parity = round & 1, t0 = first(round), n = has(t0) ? min(kTok, T_ - t0) : 0;
+        const uint32_t stop = stop_next;
+        float s[kVec];
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) s[c] = s_next[c];
+        if (lane == 0 && round + 1 < rounds) {
+            ptx::bulk_wait_read<0>();
+            fetch(round + 1);
+        }
+        __syncwarp();
+        ok = ptx::mbar_wait(&full[round % kStages][warp], round / kStages & 1, ok ? kWaitNs : 0) && ok;
+        // x, f, dh and i in, dx, df and di out
+        char *at = smem + (round % kStages * kWarps + warp) * kWarp + lane * 4, *at_f = at + kArray, *at_h = at + 2 * kArray,
+             *at_i = at + 3 * kArray;
+        if (round + 1 < rounds) load_ahead(round + 1);
+        const bool plain = n == kTok && (!kReset || stop == 0);
+        // a token's factor C, its input's factor u and both factors' derivatives (ca; cu with x
+        // in it), and the run's A, H (states) and G (gradients)
+        float C[kTok][kVec], ca[kTok][kVec], u[kTok][kVec], cu[kTok][kVec], v[kTok][kVec], A[kVec], H[kVec], G[kVec];
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+            A[c] = 1.0f;
+            H[c] = G[c] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < kTok; ++k) {
+            float x[kVec], f[kVec], g[kVec];
+            Word<T>::get(at + k * 128, x);
+            Word<T>::get(at_f + k * 128, f);
+            if (kGate) Word<T>::get(at_i + k * 128, g);
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                float na, nu;
+                sigmoid_pair(f[c], C[k][c], na);
+                ca[k][c] = C[k][c] * na;
+                u[k][c] = na;
+                if (kGate) sigmoid_pair(g[c], u[k][c], nu);
+                v[k][c] = u[k][c] * x[c];
+                if (kGate) cu[k][c] = v[k][c] * nu;
+                else cu[k][c] = x[c];
+            }
+        }
+        if (plain) {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k)
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    H[c] = fmaf(C[k][c], H[c], v[k][c]);
+                    A[c] *= C[k][c];
+                }
+#pragma unroll
+            for (int k = kTok - 1; k >= 0; --k) {
+                float dh[kVec];
+                Word<T>::get(at_h + k * 128, dh);
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) G[c] = C[k][c] * (dh[c] + G[c]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k)
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    // tokens past the end change nothing
+                    if (k >= n) {
+                        C[k][c] = 1.0f;
+                        v[k][c] = 0.0f;
+                    } else if (kReset && (stop >> k & 1)) {
+                        C[k][c] = kStop;
+                    }
+                    H[c] = through<kReset>(C[k][c], v[k][c], H[c]);
+                    A[c] = both<kReset>(A[c], C[k][c]);
+                }
+#pragma unroll
+            for (int k = kTok - 1; k >= 0; --k) {
+                float dh[kVec];
+                Word<T>::get(at_h + k * 128, dh);
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) G[c] = through<kReset>(C[k][c], 0.0f, k < n ? dh[c] + G[c] : G[c]);
+            }
+        }
+        Run<kVec> mine;
+        Lane<kVec> mine_h;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+            mine.A[c] = A[c];
+            mine.H[c] = G[c];
+            mine_h.v[c] = H[c];
+        }
+        part[parity][warp][lane] = mine;
+        part_h[parity][warp][lane] = mine_h;
+        __syncthreads();
+        // the gradient's run through the tile's warps after this one; the first warp adds its own
+        // and has the tile's total
+        float sufA[kVec], sufG[kVec];
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+            sufA[c] = 1.0f;
+            sufG[c] = 0.0f;
+        }
+#pragma unroll 1
+        for (int w = kWarps - 1; w > warp; --w) {
+            const Run<kVec> o = part[parity][w][lane];
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                sufG[c] = through<kReset>(o.A[c], o.H[c], sufG[c]);
+                sufA[c] = both<kReset>(sufA[c], o.A[c]);
+            }
+        }
+        if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        if (warp == 0) {
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                G[c] = through<kReset>(A[c], G[c], sufG[c]);
+                A[c] = both<kReset>(sufA[c], A[c]);
+            }
+            send_total<kVec>(totals, round, rank, R, lane, A, G);
+        }
+        // the state behind the tile's warps before this one, then token by token: what enters a
+        // token (nothing at a reset) makes its gate's gradient
+#pragma unroll 1
+        for (int w = 0; w < warp; ++w) {
+            const Run<kVec> o = part[parity][w][lane];
+            const Lane<kVec> oh = part_h[parity][w][lane];
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) s[c] = through<kReset>(o.A[c], oh.v[c], s[c]);
+        }
+#pragma unroll
+        for (int k = 0; k < kTok; ++k)
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                const float before = kReset && stops(C[k][c]) ? 0.0f : s[c];
+                ca[k][c] *= kGate ? before : before - cu[k][c];
+                s[c] = through<kReset>(C[k][c], v[k][c], s[c]);
+            }
+        float in[kVec];
+        receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(sufA[c], sufG[c], in[c]);
+#pragma unroll
+        for (int k = kTok - 1; k >= 0; --k) {
+            float dh[kVec], ox[kVec], of[kVec], oi[kVec];
+            Word<T>::get(at_h + k * 128, dh);
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                // (rows past the end were filled with zeros)
+                const float gr = dh[c] + in[c];
+                ox[c] = u[k][c] * gr;
+                of[c] = ca[k][c] * gr;
+                oi[c] = cu[k][c] * gr;
+                in[c] = kReset && stops(C[k][c]) ? 0.0f : C[k][c] * gr;
+            }
+            Word<T>::put(at + k * 128, ox);
+            Word<T>::put(at_f + k * 128, of);
+            if (kGate) Word<T>::put(at_i + k * 128, oi);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && n > 0) {
+            ptx::tma_store_3d(&maps.dx, at, d0, t0, b);
+            ptx::tma_store_3d(&maps.df, at_f, d0, t0, b);
+            if (kGate) ptx::tma_store_3d(&maps.di, at_i, d0, t0, b);
+            ptx::bulk_commit();
+        }
+    }
+    if (p.dh0 && rank == 0 && warp == 0 && in_d) {
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) p.dh0[state_at + c] = carry[c];
+    }
+    if (lane == 0) ptx::bulk_wait_all();
+    pause_if(!ok);
+    leave(R, ok, p.status);
+}
+
+// Whether a map can describe an array, and the map.
+bool make_map(CUtensorMap* m, const void* q, int64_t sb, int64_t st, const Gated& p, int rows) {
+    const int64_t e = p.bf16 ? 2 : 4;
+    if (p.B == 1) sb = st * p.T;  // not used
+    if (reinterpret_cast<uintptr_t>(q) % 16 || st * e % 16 || sb * e % 16 || st < p.D || sb < st) return false;
+    return tc::encode_rows_3d(m, q, (int)e, p.D, p.T, p.B, st * e, sb * e, rows);
+}
+
+template <typename K, typename M>
+int launch(K kernel, const M& maps, const Gated& p, int tile, uint32_t smem, cudaStream_t stream) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return SSDC_ERR_CUDA;
+    const int per = p.bf16 ? 64 : 32;
+    const int64_t groups = (int64_t)p.B * ((p.D + per - 1) / per);
+    return launch_clusters(kernel, groups, cluster_size((p.T + tile - 1) / tile, groups, 152 * 2), smem, stream, maps, p);
+}
+
+// Fewer tokens than this are one tile of the other kernels, which start sooner.
+constexpr int64_t kMinTokens = 65;
+
+template <typename T, bool kGate>
+int fwd(const FwdMaps& m, const Gated& p, cudaStream_t stream) {
+    constexpr uint32_t smem = smem_bytes<kFwdTok, kGate ? 3 : 2>();
+    return p.reset ? launch(gated_fwd_tma<T, kGate, true>, m, p, kWarps * kFwdTok, smem, stream)
+                   : launch(gated_fwd_tma<T, kGate, false>, m, p, kWarps * kFwdTok, smem, stream);
+}
+template <typename T, bool kGate>
+int bwd(const BwdMaps& m, const Gated& p, cudaStream_t stream) {
+    constexpr uint32_t smem = smem_bytes<kBwdTok, kGate ? 4 : 3>();
+    return p.reset ? launch(gated_bwd_tma<T, kGate, true>, m, p, kWarps * kBwdTok, smem, stream)
+                   : launch(gated_bwd_tma<T, kGate, false>, m, p, kWarps * kBwdTok, smem, stream);
+}
+
+}  // namespace
+
+int tma_fwd_launch(const Gated& p, cudaStream_t stream) {
+    if (p.T < kMinTokens || p.T > INT32_MAX - 4096) return 0;
+    FwdMaps m;
+    if (!make_map(&m.x, p.x, p.x_b, p.x_t, p, kFwdTok) || !make_map(&m.f, p.f, p.f_b, p.f_t, p, kFwdTok) ||
+        !make_map(&m.h, p.h, p.h_b, p.h_t, p, kFwdTok))
+        return 0;
+    m.i = m.x;
+    if (p.i && !make_map(&m.i, p.i, p.i_b, p.i_t, p, kFwdTok)) return 0;
+    if (p.bf16) return p.i ? fwd<__nv_bfloat16, true>(m, p, stream) : fwd<__nv_bfloat16, false>(m, p, stream);
+    return p.i ? fwd<float, true>(m, p, stream) : fwd<float, false>(m, p, stream);
+}
+
+int tma_bwd_launch(const Gated& p, cudaStream_t stream) {
+    if (p.T < kMinTokens || p.T > INT32_MAX - 4096) return 0;
+    BwdMaps m;
+    if (!make_map(&m.x, p.x, p.x_b, p.x_t, p, kBwdTok) || !make_map(&m.f, p.f, p.f_b, p.f_t, p, kBwdTok) ||
+        !make_map(&m.dh, p.dh, p.dh_b, p.dh_t, p, kBwdTok) || !make_map(&m.dx, p.dx, p.dx_b, p.dx_t, p, kBwdTok) ||
+        !make_map(&m.df, p.df, p.df_b, p.df_t, p, kBwdTok))
+        return 0;
+    m.i = m.x;
+    m.di = m.dx;
+    if (p.i && (!make_map(&m.i, p.i, p.i_b, p.i_t, p, kBwdTok) || !make_map(&m.di, p.di, p.di_b, p.di_t, p, kBwdTok)))
+        return 0;
+    if (p.bf16) return p.i ? bwd<__nv_bfloat16, true>(m, p, stream) : bwd<__nv_bfloat16, false>(m, p, stream);
+    return p.i ? bwd<float, true>(m, p, stream) : bwd<float, false>(m, p, stream);
+}
+
+}  // namespace gated
+}  // namespace block
+}  // namespace ssdc

@@ -435,6 +435,18 @@ bool encode_tiled_2d(CUtensorMap* m, const void* base, int elem, int64_t cols, i
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_rows_3d(CUtensorMap* m, const void* base, int elem, int64_t D, int64_t T, int64_t B, int64_t t_bytes,
+                    int64_t b_bytes, int box_rows) {
+    if (!get_encoder()) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)B};
+    const cuuint64_t strides[2] = {(cuuint64_t)t_bytes, (cuuint64_t)b_bytes};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / elem), (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+    return g_encode(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                    const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 bool make_feature_map(CUtensorMap* m, const float* base, int F, int H, int64_t T, int B) {

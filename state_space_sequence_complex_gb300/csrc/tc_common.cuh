@@ -137,6 +137,10 @@ bool encode_tiled_f32(CUtensorMap* m, const void* base, int rank, const cuuint64
 // Host: rows of 1-, 2- (bfloat16) or 4-byte (fp32) elements, `pitch` bytes apart; boxes of 128
 // bytes x box_rows with the 128-byte swizzle and zero fill.
 bool encode_tiled_2d(CUtensorMap* m, const void* base, int elem, int64_t cols, int64_t rows, int64_t pitch, int box_rows);
+// Host: a (B, T, D) array of 2- (bfloat16) or 4-byte (fp32) elements; boxes of 128 bytes of
+// channels x box_rows tokens, unswizzled, with zero fill.
+bool encode_rows_3d(CUtensorMap* m, const void* base, int elem, int64_t D, int64_t T, int64_t B, int64_t t_bytes,
+                    int64_t b_bytes, int box_rows);
 
 }  // namespace tc
 }  // namespace ssdc
