@@ -30,7 +30,7 @@ namespace {
 
 using namespace gated;
 
-constexpr int kTok = 8, kTile = kWarps * kTok;
+constexpr int kWarps = 8, kThreads = 32 * kWarps, kTok = 8, kTile = kWarps * kTok;
 static_assert(kTile == SSD_GATED_STATE_TOKENS, "a state is kept for every tile");
 
 // kVec adjacent channels of one token, as they are in memory.
@@ -506,7 +506,7 @@ bool pairs_ok(const void* q, int64_t sb, int64_t st, size_t elem) {
 template <typename K>
 int launch_cluster(K kernel, const Gated& p, int vec, cudaStream_t stream) {
     const int64_t groups = (int64_t)p.B * ((p.D + 32 * vec - 1) / (32 * vec));
-    return launch_clusters(kernel, groups, cluster_size((p.T + kTile - 1) / kTile, groups, 152 * 3), 0, stream, p);
+    return launch_clusters(kernel, groups, cluster_size((p.T + kTile - 1) / kTile, groups, 152 * 3), kThreads, 0, stream, p);
 }
 
 template <typename T, int kVec, bool kGate>

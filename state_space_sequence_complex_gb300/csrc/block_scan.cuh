@@ -14,7 +14,6 @@ namespace ssdc {
 namespace block {
 namespace gated {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kMaxCluster = 8;
 
 // A reset stops everything that comes before it, an infinity or a NaN too, so it is not the
@@ -123,14 +122,14 @@ inline int cluster_size(int64_t tiles, int64_t groups, int ctas) {
     return R;
 }
 
-// A kernel on `groups` clusters of R CTAs.
+// A kernel on `groups` clusters of R CTAs of so many threads.
 template <typename... KArgs, typename... Args>
-inline int launch_clusters(void (*kernel)(KArgs...), int64_t groups, int R, size_t smem, cudaStream_t stream,
+inline int launch_clusters(void (*kernel)(KArgs...), int64_t groups, int R, int threads, size_t smem, cudaStream_t stream,
                            const Args&... args) {
     if (groups * R > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(groups * R));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

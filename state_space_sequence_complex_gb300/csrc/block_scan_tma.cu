@@ -66,14 +66,22 @@ __device__ __forceinline__ void pause_if(bool failed) {
 // Shared memory of a CTA: for every stage and warp the rows of each array, 128 bytes a row.
 template <int kTok, int kArrays>
 constexpr uint32_t warp_bytes() { return kTok * 128 * kArrays; }
-template <int kTok, int kArrays>
+template <int kWarps, int kTok, int kArrays>
 constexpr uint32_t smem_bytes() { return kStages * kWarps * warp_bytes<kTok, kArrays>() + 128; }
 
-constexpr int kFwdTok = 16, kBwdTok = 8;
+// Warps of a CTA, and tokens that a thread holds in registers
+constexpr int kFwdWarps = 8, kFwdTok = 16;
+// Backward a token takes twice the registers. Two bfloat16 channels a lane: four warps of 16
+// tokens (B 16 T 2048 D 1024: 94 us; eight of 8: 106 us); one fp32 channel: eight of 8
+// (167 us; four of 16: 187 us).
+template <typename T>
+constexpr int bwd_warps() { return sizeof(T) == 2 ? 4 : 8; }
+template <typename T>
+constexpr int bwd_tok() { return 64 / bwd_warps<T>(); }
 
 template <typename T, bool kGate, bool kReset>
-__global__ void __launch_bounds__(kThreads, 2) gated_fwd_tma(const __grid_constant__ FwdMaps maps, const Gated p) {
-    constexpr int kVec = Word<T>::kVec, kTok = kFwdTok, kTile = kWarps * kTok, kArrays = kGate ? 3 : 2;
+__global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(const __grid_constant__ FwdMaps maps, const Gated p) {
+    constexpr int kVec = Word<T>::kVec, kWarps = kFwdWarps, kTok = kFwdTok, kTile = kWarps * kTok, kArrays = kGate ? 3 : 2;
     constexpr uint32_t kWarp = warp_bytes<kTok, kArrays>(), kArray = kTok * 128;
     extern __shared__ char smem_raw[];
     char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -82,9 +90,11 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_tma(const __grid_consta
     __shared__ uint64_t full[kStages][kWarps];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
-    if (lane == 0)
+    if (lane == 0) {
         for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s][warp], 1);
-    totals_init(totals, R);  // (and its fence)
+        ptx::fence_mbar_init();
+    }
+    if (R > 1) totals_init(totals, R);
     const int groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
     const int b = group / groups, d0 = group % groups * 32 * kVec, d = d0 + lane * kVec;
     const bool in_d = d < p.D;
@@ -184,33 +194,40 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_tma(const __grid_consta
         }
         part[parity][warp][lane] = mine;
         __syncthreads();
-        // the tile's warps before this one; the last warp adds its own and has the tile's total
-        float preA[kVec], preH[kVec];
+        // the tile's warps before this one (pre); and all of them, in every warp or, where the
+        // total goes to the cluster's CTAs, in the last one
+        float preA[kVec], preH[kVec], allA[kVec], allH[kVec];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
-            preA[c] = 1.0f;
-            preH[c] = 0.0f;
+            allA[c] = preA[c] = 1.0f;
+            allH[c] = preH[c] = 0.0f;
         }
-#pragma unroll 1
-        for (int w = 0; w < warp; ++w) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w > warp && R > 1) break;
             const Run<kVec> o = part[parity][w][lane];
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
-                preH[c] = through<kReset>(o.A[c], o.H[c], preH[c]);
-                preA[c] = both<kReset>(preA[c], o.A[c]);
+                if (w == warp) {
+                    preA[c] = allA[c];
+                    preH[c] = allH[c];
+                }
+                allH[c] = through<kReset>(o.A[c], o.H[c], allH[c]);
+                allA[c] = both<kReset>(allA[c], o.A[c]);
             }
-        }
-        if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-        if (warp == kWarps - 1) {
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                H[c] = through<kReset>(A[c], H[c], preH[c]);
-                A[c] = both<kReset>(preA[c], A[c]);
-            }
-            send_total<kVec>(totals, round, rank, R, lane, A, H);
         }
         float in[kVec];
-        receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
+        if (R > 1) {
+            if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            if (warp == kWarps - 1) send_total<kVec>(totals, round, rank, R, lane, allA, allH);
+            receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
+        } else {
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                in[c] = carry[c];
+                carry[c] = through<kReset>(allA[c], allH[c], carry[c]);
+            }
+        }
 #pragma unroll
         for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(preA[c], preH[c], in[c]);
         if (p.states && t0 % SSD_GATED_STATE_TOKENS == 0 && n > 0 && in_d) {
@@ -251,8 +268,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_tma(const __grid_consta
 }
 
 template <typename T, bool kGate, bool kReset>
-__global__ void __launch_bounds__(kThreads, 2) gated_bwd_tma(const __grid_constant__ BwdMaps maps, const Gated p) {
-    constexpr int kVec = Word<T>::kVec, kTok = kBwdTok, kTile = kWarps * kTok, kArrays = kGate ? 4 : 3;
+__global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __grid_constant__ BwdMaps maps, const Gated p) {
+    constexpr int kVec = Word<T>::kVec, kWarps = bwd_warps<T>(), kTok = bwd_tok<T>(), kTile = kWarps * kTok, kArrays = kGate ? 4 : 3;
     static_assert(kTile == SSD_GATED_STATE_TOKENS, "a state is kept for every tile");
     constexpr uint32_t kWarp = warp_bytes<kTok, kArrays>(), kArray = kTok * 128;
     extern __shared__ char smem_raw[];
@@ -263,9 +280,11 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_tma(const __grid_consta
     __shared__ uint64_t full[kStages][kWarps];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
-    if (lane == 0)
+    if (lane == 0) {
         for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s][warp], 1);
-    totals_init(totals, R);
+        ptx::fence_mbar_init();
+    }
+    if (R > 1) totals_init(totals, R);
     const int groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
     const int b = group / groups, d0 = group % groups * 32 * kVec, d = d0 + lane * kVec;
     const bool in_d = d < p.D;
@@ -397,40 +416,41 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_tma(const __grid_consta
         part[parity][warp][lane] = mine;
         part_h[parity][warp][lane] = mine_h;
         __syncthreads();
-        // the gradient's run through the tile's warps after this one; the first warp adds its own
-        // and has the tile's total
-        float sufA[kVec], sufG[kVec];
+        // the gradient's run through the tile's warps after this one (suf); and through all, in
+        // every warp or, where the total goes to the cluster's CTAs, in the first one
+        float sufA[kVec], sufG[kVec], allA[kVec], allG[kVec];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
-            sufA[c] = 1.0f;
-            sufG[c] = 0.0f;
+            allA[c] = sufA[c] = 1.0f;
+            allG[c] = sufG[c] = 0.0f;
         }
-#pragma unroll 1
-        for (int w = kWarps - 1; w > warp; --w) {
+#pragma unroll
+        for (int w = kWarps - 1; w >= 0; --w) {
+            if (w < warp && R > 1) break;
             const Run<kVec> o = part[parity][w][lane];
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
-                sufG[c] = through<kReset>(o.A[c], o.H[c], sufG[c]);
-                sufA[c] = both<kReset>(sufA[c], o.A[c]);
+                if (w == warp) {
+                    sufA[c] = allA[c];
+                    sufG[c] = allG[c];
+                }
+                allG[c] = through<kReset>(o.A[c], o.H[c], allG[c]);
+                allA[c] = both<kReset>(allA[c], o.A[c]);
             }
         }
-        if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-        if (warp == 0) {
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                G[c] = through<kReset>(A[c], G[c], sufG[c]);
-                A[c] = both<kReset>(sufA[c], A[c]);
-            }
-            send_total<kVec>(totals, round, rank, R, lane, A, G);
+        if (R > 1) {
+            if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            if (warp == 0) send_total<kVec>(totals, round, rank, R, lane, allA, allG);
         }
         // the state behind the tile's warps before this one, then token by token: what enters a
         // token (nothing at a reset) makes its gate's gradient
-#pragma unroll 1
-        for (int w = 0; w < warp; ++w) {
+#pragma unroll
+        for (int w = 0; w < kWarps - 1; ++w) {
             const Run<kVec> o = part[parity][w][lane];
             const Lane<kVec> oh = part_h[parity][w][lane];
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) s[c] = through<kReset>(o.A[c], oh.v[c], s[c]);
+            for (int c = 0; c < kVec; ++c)
+                if (w < warp) s[c] = through<kReset>(o.A[c], oh.v[c], s[c]);
         }
 #pragma unroll
         for (int k = 0; k < kTok; ++k)
@@ -441,7 +461,15 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_tma(const __grid_consta
                 s[c] = through<kReset>(C[k][c], v[k][c], s[c]);
             }
         float in[kVec];
-        receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
+        if (R > 1) {
+            receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
+        } else {
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                in[c] = carry[c];
+                carry[c] = through<kReset>(allA[c], allG[c], carry[c]);
+            }
+        }
 #pragma unroll
         for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(sufA[c], sufG[c], in[c]);
 #pragma unroll
@@ -488,12 +516,12 @@ bool make_map(CUtensorMap* m, const void* q, int64_t sb, int64_t st, const Gated
 }
 
 template <typename K, typename M>
-int launch(K kernel, const M& maps, const Gated& p, int tile, uint32_t smem, cudaStream_t stream) {
+int launch(K kernel, const M& maps, const Gated& p, int warps, int tile, uint32_t smem, cudaStream_t stream) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return SSDC_ERR_CUDA;
     const int per = p.bf16 ? 64 : 32;
     const int64_t groups = (int64_t)p.B * ((p.D + per - 1) / per);
-    return launch_clusters(kernel, groups, cluster_size((p.T + tile - 1) / tile, groups, 152 * 2), smem, stream, maps, p);
+    return launch_clusters(kernel, groups, cluster_size((p.T + tile - 1) / tile, groups, 152), 32 * warps, smem, stream, maps, p);
 }
 
 // Fewer tokens than this are one tile of the other kernels, which start sooner.
@@ -501,15 +529,15 @@ constexpr int64_t kMinTokens = 65;
 
 template <typename T, bool kGate>
 int fwd(const FwdMaps& m, const Gated& p, cudaStream_t stream) {
-    constexpr uint32_t smem = smem_bytes<kFwdTok, kGate ? 3 : 2>();
-    return p.reset ? launch(gated_fwd_tma<T, kGate, true>, m, p, kWarps * kFwdTok, smem, stream)
-                   : launch(gated_fwd_tma<T, kGate, false>, m, p, kWarps * kFwdTok, smem, stream);
+    constexpr uint32_t smem = smem_bytes<kFwdWarps, kFwdTok, kGate ? 3 : 2>();
+    return p.reset ? launch(gated_fwd_tma<T, kGate, true>, m, p, kFwdWarps, kFwdWarps * kFwdTok, smem, stream)
+                   : launch(gated_fwd_tma<T, kGate, false>, m, p, kFwdWarps, kFwdWarps * kFwdTok, smem, stream);
 }
 template <typename T, bool kGate>
 int bwd(const BwdMaps& m, const Gated& p, cudaStream_t stream) {
-    constexpr uint32_t smem = smem_bytes<kBwdTok, kGate ? 4 : 3>();
-    return p.reset ? launch(gated_bwd_tma<T, kGate, true>, m, p, kWarps * kBwdTok, smem, stream)
-                   : launch(gated_bwd_tma<T, kGate, false>, m, p, kWarps * kBwdTok, smem, stream);
+    constexpr uint32_t smem = smem_bytes<bwd_warps<T>(), bwd_tok<T>(), kGate ? 4 : 3>();
+    return p.reset ? launch(gated_bwd_tma<T, kGate, true>, m, p, bwd_warps<T>(), 64, smem, stream)
+                   : launch(gated_bwd_tma<T, kGate, false>, m, p, bwd_warps<T>(), 64, smem, stream);
 }
 
 }  // namespace
@@ -528,14 +556,15 @@ int tma_fwd_launch(const Gated& p, cudaStream_t stream) {
 
 int tma_bwd_launch(const Gated& p, cudaStream_t stream) {
     if (p.T < kMinTokens || p.T > INT32_MAX - 4096) return 0;
+    const int rows = p.bf16 ? bwd_tok<__nv_bfloat16>() : bwd_tok<float>();
     BwdMaps m;
-    if (!make_map(&m.x, p.x, p.x_b, p.x_t, p, kBwdTok) || !make_map(&m.f, p.f, p.f_b, p.f_t, p, kBwdTok) ||
-        !make_map(&m.dh, p.dh, p.dh_b, p.dh_t, p, kBwdTok) || !make_map(&m.dx, p.dx, p.dx_b, p.dx_t, p, kBwdTok) ||
-        !make_map(&m.df, p.df, p.df_b, p.df_t, p, kBwdTok))
+    if (!make_map(&m.x, p.x, p.x_b, p.x_t, p, rows) || !make_map(&m.f, p.f, p.f_b, p.f_t, p, rows) ||
+        !make_map(&m.dh, p.dh, p.dh_b, p.dh_t, p, rows) || !make_map(&m.dx, p.dx, p.dx_b, p.dx_t, p, rows) ||
+        !make_map(&m.df, p.df, p.df_b, p.df_t, p, rows))
         return 0;
     m.i = m.x;
     m.di = m.dx;
-    if (p.i && (!make_map(&m.i, p.i, p.i_b, p.i_t, p, kBwdTok) || !make_map(&m.di, p.di, p.di_b, p.di_t, p, kBwdTok)))
+    if (p.i && (!make_map(&m.i, p.i, p.i_b, p.i_t, p, rows) || !make_map(&m.di, p.di, p.di_b, p.di_t, p, rows)))
         return 0;
     if (p.bf16) return p.i ? bwd<__nv_bfloat16, true>(m, p, stream) : bwd<__nv_bfloat16, false>(m, p, stream);
     return p.i ? bwd<float, true>(m, p, stream) : bwd<float, false>(m, p, stream);
