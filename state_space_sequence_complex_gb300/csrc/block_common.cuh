@@ -49,6 +49,22 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 }
 __device__ __forceinline__ uint8_t e4m3(float v) { return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
 
+// kN e4m3 values to kN bytes (an address of a multiple of kN).
+template <int kN>
+__device__ __forceinline__ void store_e4m3(uint8_t* p, const float* q) {
+    static_assert(kN == 1 || kN == 4 || kN == 8 || kN == 16, "");
+    if constexpr (kN == 1) {
+        *p = e4m3(q[0]);
+    } else {
+        uint32_t w[kN / 4];
+#pragma unroll
+        for (int i = 0; i < kN / 4; ++i) w[i] = e4m3x2(q[4 * i], q[4 * i + 1]) | e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16;
+        if constexpr (kN == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
+        else if constexpr (kN == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 template <int kWidth = 32>
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

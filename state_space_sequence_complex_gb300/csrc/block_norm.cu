@@ -1,183 +1,400 @@
-// Residual norm, its gradients, and the 8-bit quantiser (include/ssdc_block.h).
+// Residual norm and its gradients (include/ssdc_block.h).
+//
+//   r = x + residual,  rstd = 1 / sqrt(mean(r^2) + eps),  y = r rstd w
+//
+// Bound by HBM. A row is read once and stays in registers between the sum of squares and
+// the output: a warp holds 1024 features, 32 a lane, and up to 32 warps share a row. A
+// lane's features are vectors of 16 bytes (bfloat16: 8, so that a group of 128 features is
+// half a warp; fp32: 4, a whole one), or, for rows that do not start at multiples of 16
+// bytes, single features 32 apart.
 #include <cuda_runtime.h>
 
 #include "block_common.cuh"
 #include "block_kernels.h"
+#include "ptx.cuh"
+#include "ssdc_kernels.h"
 
 namespace ssdc {
 namespace block {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kVals = 32, kWarpSpan = 32 * kVals;  // features of a lane and of a warp
 
-__device__ float block_sum(float v) {
-    __shared__ float part[kWarps];
+// Which features a lane holds: value i of lane l is feature base + at(i, l). A run is kRun
+// adjacent features, one load.
+template <typename T, bool kAligned>
+struct Layout {
+    static constexpr int kRun = kAligned ? 16 / (int)sizeof(T) : 1;
+    static constexpr int kRuns = kVals / kRun;
+    static constexpr int kGroupRuns = kAligned ? 1 : 4;              // runs of a lane in a group of 128
+    static constexpr int kGroupLanes = 128 / (kRun * kGroupRuns);    // lanes that share a group
+    static __device__ __forceinline__ int run_at(int run, int lane) { return (run * 32 + lane) * kRun; }
+};
+
+// kRun values at a feature inside the row, as floats.
+template <typename T, bool kAligned>
+__device__ __forceinline__ void load_run(const T* p, float* v) {
+    if constexpr (!kAligned) {
+        v[0] = to_f32(*p);
+    } else if constexpr (sizeof(T) == 2) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = ptx::bf16_lo(u[i]);
+            v[2 * i + 1] = ptx::bf16_hi(u[i]);
+        }
+    } else {
+        const float4 w = *reinterpret_cast<const float4*>(p);
+        v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+    }
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+// kN values to an array of T (kN is a run of the input's type; the output's may be another).
+template <typename T, int kN>
+__device__ __forceinline__ void store_run(T* p, const float* v) {
+    if constexpr (kN == 1) {
+        *p = from_f32<T>(v[0]);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < kN; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else if constexpr (kN == 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                  pack_bf16(v[6], v[7]));
+    } else {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    }
+}
+template <int kN>
+__device__ __forceinline__ void load_w(const float* w, float* v) {
+    if constexpr (kN == 1) {
+        v[0] = __ldg(w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kN; i += 4) {
+            const float4 t = __ldg(reinterpret_cast<const float4*>(w + i));
+            v[i] = t.x; v[i + 1] = t.y; v[i + 2] = t.z; v[i + 3] = t.w;
+        }
+    }
+}
+
+// 1 / sqrt(m) to within a unit of its last place: the hardware's approximation and one step of
+// Newton's method, the residual 1 - m y^2 formed with the product's rounding error.
+__device__ __forceinline__ float rsqrt_refined(float m) {
+    const float y = rsqrtf(m), h = m * y, l = fmaf(m, y, -h);
+    const float e = fmaf(-h, y, 1.0f) - l * y;
+    const float r = fmaf(0.5f * y, e, y);
+    return isfinite(r) ? r : y;  // (m infinite or zero)
+}
+
+// The sum over the warps of a row (`row` of the CTA's kRows, kRowWarps each); every warp of the
+// CTA takes part. `slot` alternates between calls.
+template <int kRowWarps>
+__device__ __forceinline__ float row_sum(float v, float (*part)[32], int slot, int warp) {
     v = warp_sum(v);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    if constexpr (kRowWarps == 1) return v;
+    if (threadIdx.x % 32 == 0) part[slot][warp] = v;
     __syncthreads();
     float s = 0.0f;
-    for (int k = 0; k < kWarps; ++k) s += part[k];
+    const int first = warp / kRowWarps * kRowWarps;
+#pragma unroll
+    for (int k = 0; k < kRowWarps; ++k) s += part[slot][first + k];
     return s;
 }
 
-// One CTA a row; a warp owns whole groups of 128 features.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_fwd(Norm p) {
-    const int64_t m = blockIdx.x;
-    const T* x = static_cast<const T*>(p.x) + m * p.x_ld;
-    const T* res = p.res ? static_cast<const T*>(p.res) + m * p.res_ld : nullptr;
-    T* r = p.r ? static_cast<T*>(p.r) + m * p.r_ld : nullptr;
-    float sq = 0.0f;
-    for (int d = threadIdx.x; d < p.D; d += kThreads) {
-        const float v = to_f32(x[d]) + (res ? to_f32(res[d]) : 0.0f);
-        sq = fmaf(v, v, sq);
-    }
-    const float rstd = rsqrtf(block_sum(sq) / (float)p.D + p.eps);
-    if (p.rstd && threadIdx.x == 0) p.rstd[m] = rstd;
+template <int kRowWarps>
+constexpr int cta_warps() { return kRowWarps > 8 ? kRowWarps : 8; }
+
+template <typename T, typename TO, bool kFp8, int kRowWarps, bool kAligned>
+__global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1 : 4) norm_fwd(const Norm p) {
+    using L = Layout<T, kAligned>;
+    constexpr int kWarps = cta_warps<kRowWarps>(), kRun = L::kRun;
+    __shared__ float part[1][32];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int d0 = warp * 128; d0 < p.D; d0 += kWarps * 128) {
-        float y[4], amax = 0.0f;
-        for (int j = 0; j < 4; ++j) {
-            const int d = d0 + lane + 32 * j;
-            y[j] = 0.0f;
-            if (d < p.D) {
-                const float v = to_f32(x[d]) + (res ? to_f32(res[d]) : 0.0f);
-                if (r) r[d] = from_f32<T>(v);
-                y[j] = v * rstd * (p.w ? p.w[d] : 1.0f);
-                if (p.out_type == SSD_TYPE_F32) static_cast<float*>(p.y)[m * p.y_ld + d] = y[j];
-                if (p.out_type == SSD_TYPE_BF16)
-                    static_cast<__nv_bfloat16*>(p.y)[m * p.y_ld + d] = __float2bfloat16_rn(y[j]);
+    const int64_t m = (int64_t)blockIdx.x * (kWarps / kRowWarps) + warp / kRowWarps;
+    const int base = warp % kRowWarps * kWarpSpan;
+    const bool in = m < p.M;
+    const T* x = static_cast<const T*>(p.x) + m * p.x_ld + base;
+    const T* res = static_cast<const T*>(p.res) + m * p.res_ld + base;
+    float v[kVals];
+#pragma unroll
+    for (int i = 0; i < L::kRuns; ++i) {
+        const int at = L::run_at(i, lane);
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) v[i * kRun + e] = 0.0f;
+        if (in && base + at < p.D) load_run<T, kAligned>(x + at, v + i * kRun);
+    }
+    if (p.res) {
+#pragma unroll
+        for (int i = 0; i < L::kRuns; ++i) {
+            const int at = L::run_at(i, lane);
+            if (in && base + at < p.D) {
+                float u[kRun];
+                load_run<T, kAligned>(res + at, u);
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) v[i * kRun + e] += u[e];
             }
-            amax = fmaxf(amax, fabsf(y[j]));
         }
-        if (p.out_type == SSD_TYPE_E4M3) {
-            const float s = group_scale(warp_max(amax));
-            if (lane == 0) p.scale[(int64_t)(d0 / 128) * p.M + m] = s;
-            for (int j = 0; j < 4; ++j) {
-                const int d = d0 + lane + 32 * j;
-                if (d < p.D) static_cast<uint8_t*>(p.y)[m * p.y_ld + d] = e4m3(y[j] / s);
+    }
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) sq = fmaf(v[i], v[i], sq);
+    sq = row_sum<kRowWarps>(sq, part, 0, warp);
+    if (!in) return;
+    const float rstd = rsqrt_refined(sq / (float)p.D + p.eps);
+    if (p.rstd && lane == 0 && base == 0) p.rstd[m] = rstd;
+    if (p.r) {
+        T* r = static_cast<T*>(p.r) + m * p.r_ld + base;
+#pragma unroll
+        for (int i = 0; i < L::kRuns; ++i) {
+            const int at = L::run_at(i, lane);
+            if (base + at < p.D) store_run<T, kRun>(r + at, v + i * kRun);
+        }
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < L::kRuns; i0 += L::kGroupRuns) {
+        float lo[kRun * L::kGroupRuns];  // what rounding the two products left out of y
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = i0; i < i0 + L::kGroupRuns; ++i) {
+            const int at = L::run_at(i, lane);
+            float w[kRun];
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) w[e] = 1.0f;
+            if (p.w && base + at < p.D) load_w<kRun>(p.w + base + at, w);
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) {
+                float& t = v[i * kRun + e];
+                const float n = t * rstd, y = n * w[e];
+                if (kFp8) {
+                    lo[(i - i0) * kRun + e] = fmaf(fmaf(t, rstd, -n), w[e], fmaf(n, w[e], -y));
+                    amax = fmaxf(amax, fabsf(y));
+                }
+                t = y;
+            }
+            if (!kFp8 && base + at < p.D)
+                store_run<TO, kRun>(static_cast<TO*>(p.y) + m * p.y_ld + base + at, v + i * kRun);
+        }
+        if (kFp8) {
+            amax = warp_max<L::kGroupLanes>(amax);
+            const float s = group_scale(amax), inv = 1.0f / s;
+            const int first = base + L::run_at(i0, lane);  // in the same group for all its lanes and runs
+            if (lane % L::kGroupLanes == 0 && first < p.D) p.scale[(int64_t)(first / SSD_FP8_GROUP) * p.M + m] = s;
+#pragma unroll
+            for (int i = i0; i < i0 + L::kGroupRuns; ++i) {
+                const int at = L::run_at(i, lane);
+                float q[kRun];
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) q[e] = fmaf(lo[(i - i0) * kRun + e], inv, v[i * kRun + e] / s);
+                if (base + at < p.D) store_e4m3<kRun>(static_cast<uint8_t*>(p.y) + m * p.y_ld + base + at, q);
             }
         }
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_bwd(NormBwd p) {
-    const int64_t m = blockIdx.x;
-    const T* dy = static_cast<const T*>(p.dy) + m * p.dy_ld;
-    const T* dr = p.dr ? static_cast<const T*>(p.dr) + m * p.dr_ld : nullptr;
-    const T* r = static_cast<const T*>(p.r) + m * p.r_ld;
-    T* dx = static_cast<T*>(p.dx) + m * p.dx_ld;
-    const float rstd = p.rstd[m];
-    float s = 0.0f;
-    for (int d = threadIdx.x; d < p.D; d += kThreads)
-        s += to_f32(dy[d]) * (p.w ? p.w[d] : 1.0f) * (to_f32(r[d]) * rstd);
-    const float mean = block_sum(s) / (float)p.D;
-    for (int d = threadIdx.x; d < p.D; d += kThreads) {
-        const float xh = to_f32(r[d]) * rstd, gy = to_f32(dy[d]) * (p.w ? p.w[d] : 1.0f);
-        dx[d] = from_f32<T>((dr ? to_f32(dr[d]) : 0.0f) + rstd * (gy - xh * mean));
+// Gradients. A warp walks rows kRows apart and adds up its share of dw in registers; the CTA's
+// warps that hold the same features join theirs at the end, one row of `partial` a CTA.
+template <typename T, int kRowWarps, bool kAligned>
+__global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1 : 2) norm_bwd(const NormBwd p) {
+    using L = Layout<T, kAligned>;
+    constexpr int kWarps = cta_warps<kRowWarps>(), kRun = L::kRun, kRows = kWarps / kRowWarps;
+    __shared__ float part[2][32];
+    __shared__ float join[kRows > 1 ? kWarps - kRowWarps : 1][kRows > 1 ? kWarpSpan / 4 : 1];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int base = warp % kRowWarps * kWarpSpan;
+    float dw[kVals];
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) dw[i] = 0.0f;
+    int slot = 0;
+    for (int64_t m0 = (int64_t)blockIdx.x * kRows; m0 < p.M; m0 += (int64_t)gridDim.x * kRows, slot ^= 1) {
+        const int64_t m = m0 + warp / kRowWarps;
+        const bool in = m < p.M;
+        const T* dy = static_cast<const T*>(p.dy) + m * p.dy_ld + base;
+        const T* r = static_cast<const T*>(p.r) + m * p.r_ld + base;
+        const T* dr = static_cast<const T*>(p.dr) + m * p.dr_ld + base;
+        const float rstd = in ? __ldg(p.rstd + m) : 0.0f;
+        float g[kVals], xh[kVals], s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < L::kRuns; ++i) {
+            const int at = L::run_at(i, lane);
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) g[i * kRun + e] = xh[i * kRun + e] = 0.0f;
+            if (in && base + at < p.D) {
+                load_run<T, kAligned>(dy + at, g + i * kRun);
+                load_run<T, kAligned>(r + at, xh + i * kRun);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < L::kRuns; ++i) {
+            const int at = L::run_at(i, lane);
+            float w[kRun];
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) w[e] = 1.0f;
+            if (p.w && base + at < p.D) load_w<kRun>(p.w + base + at, w);
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) {
+                const int j = i * kRun + e;
+                xh[j] *= rstd;
+                dw[j] = fmaf(g[j], xh[j], dw[j]);
+                g[j] *= w[e];
+                s = fmaf(g[j], xh[j], s);
+            }
+        }
+        const float mean = row_sum<kRowWarps>(s, part, slot, warp) / (float)p.D;
+        if (!in) continue;
+        T* dx = static_cast<T*>(p.dx) + m * p.dx_ld + base;
+#pragma unroll
+        for (int i = 0; i < L::kRuns; ++i) {
+            const int at = L::run_at(i, lane);
+            if (base + at < p.D) {
+                float o[kRun];
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) o[e] = 0.0f;
+                if (p.dr) load_run<T, kAligned>(dr + at, o);
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) {
+                    const int j = i * kRun + e;
+                    o[e] = fmaf(rstd, fmaf(-xh[j], mean, g[j]), o[e]);
+                }
+                store_run<T, kRun>(dx + at, o);
+            }
+        }
+    }
+    if (!p.dw) return;
+    float* to = p.partial + (int64_t)blockIdx.x * p.D + base;
+    if constexpr (kRows > 1) {
+        // a quarter of the lanes' values at a time, so that the rows' shares fit into shared memory
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            __syncthreads();
+            if (warp >= kRowWarps)
+#pragma unroll
+                for (int i = 0; i < kVals / 4; ++i) join[warp - kRowWarps][i * 32 + lane] = dw[q * (kVals / 4) + i];
+            __syncthreads();
+            if (warp < kRowWarps)
+#pragma unroll
+                for (int i = 0; i < kVals / 4; ++i)
+                    for (int k = 1; k < kRows; ++k) dw[q * (kVals / 4) + i] += join[k * kRowWarps + warp - kRowWarps][i * 32 + lane];
+        }
+        if (warp >= kRowWarps) return;
+    }
+#pragma unroll
+    for (int i = 0; i < L::kRuns; ++i) {
+        const int at = L::run_at(i, lane);
+        if (base + at < p.D)
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) to[at + e] = dw[i * kRun + e];
     }
 }
 
-// dw: one CTA for 32 features and one part of the rows, before dx may overwrite dy.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_bwd_dw(NormBwd p, int parts) {
-    const int d = blockIdx.x * 32 + threadIdx.x % 32;
-    const int64_t per = (p.M + parts - 1) / parts, m0 = blockIdx.y * per;
-    const int64_t m1 = m0 + per < p.M ? m0 + per : p.M;
-    __shared__ float part[kWarps][32];
+// dw from the CTAs' shares, in their order: a CTA sums 32 features, 8 warps an eighth of the shares each.
+__global__ void __launch_bounds__(256) norm_bwd_sum(const float* partial, float* dw, int D, int parts) {
+    __shared__ float join[8][32];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, d = blockIdx.x * 32 + lane;
+    grid_dependency_wait();
     float s = 0.0f;
-    if (d < p.D)
-        for (int64_t m = m0 + threadIdx.x / 32; m < m1; m += kWarps)
-            s += to_f32(static_cast<const T*>(p.dy)[m * p.dy_ld + d]) *
-                 (to_f32(static_cast<const T*>(p.r)[m * p.r_ld + d]) * p.rstd[m]);
-    part[threadIdx.x / 32][threadIdx.x % 32] = s;
+    const int per = (parts + 7) / 8;
+    if (d < D) {
+#pragma unroll 8
+        for (int k = warp * per; k < min((warp + 1) * per, parts); ++k) s += partial[(int64_t)k * D + d];
+    }
+    join[warp][lane] = s;
     __syncthreads();
-    if (threadIdx.x < 32 && d < p.D) {
+    if (warp == 0 && d < D) {
         s = 0.0f;
-        for (int k = 0; k < kWarps; ++k) s += part[k][threadIdx.x];
-        p.partial[(int64_t)blockIdx.y * p.D + d] = s;
+        for (int k = 0; k < 8; ++k) s += join[k][lane];
+        dw[d] = s;
     }
 }
 
-__global__ void __launch_bounds__(kThreads) norm_bwd_sum(NormBwd p, int parts) {
-    const int d = blockIdx.x * kThreads + threadIdx.x;
-    if (d >= p.D) return;
-    float s = 0.0f;
-    for (int k = 0; k < parts; ++k) s += p.partial[(int64_t)k * p.D + d];
-    p.dw[d] = s;
+// Warps of a row: a power of two.
+int row_warps(int64_t D) {
+    int w = 1;
+    while (w * kWarpSpan < D) w *= 2;
+    return w;
 }
 
-// One CTA a tile of 128 x 128; threads re-read the tile.
+bool rows16(const void* q, int64_t ld, size_t elem) {
+    return q == nullptr || (reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * (int64_t)elem % 16 == 0);
+}
+
+template <typename T, typename TO, bool kFp8, int W>
+void fwd(const Norm& p, bool aligned, cudaStream_t stream) {
+    constexpr int rows = cta_warps<W>() / W, threads = 32 * cta_warps<W>();
+    const unsigned grid = (unsigned)((p.M + rows - 1) / rows);
+    if (aligned) norm_fwd<T, TO, kFp8, W, true><<<grid, threads, 0, stream>>>(p);
+    else norm_fwd<T, TO, kFp8, W, false><<<grid, threads, 0, stream>>>(p);
+}
+template <typename T, typename TO, bool kFp8>
+void fwd_rows(const Norm& p, bool aligned, cudaStream_t stream) {
+    switch (row_warps(p.D)) {
+        case 1: return fwd<T, TO, kFp8, 1>(p, aligned, stream);
+        case 2: return fwd<T, TO, kFp8, 2>(p, aligned, stream);
+        case 4: return fwd<T, TO, kFp8, 4>(p, aligned, stream);
+        case 8: return fwd<T, TO, kFp8, 8>(p, aligned, stream);
+        case 16: return fwd<T, TO, kFp8, 16>(p, aligned, stream);
+        default: return fwd<T, TO, kFp8, 32>(p, aligned, stream);
+    }
+}
 template <typename T>
-__global__ void __launch_bounds__(128) quantize(Quant p) {
-    __shared__ float amax[128];
-    const int64_t m0 = (int64_t)blockIdx.y * 128, k0 = (int64_t)blockIdx.x * 128;
-    const int t = threadIdx.x;
-    const int64_t MB = (p.M + 127) / 128, KB = (p.K + 127) / 128;
-    auto at = [&](int64_t m, int64_t k) {
-        return m < p.M && k < p.K ? to_f32(static_cast<const T*>(p.x)[m * p.x_ld + k]) : 0.0f;
-    };
-    float by_row = 0.0f, by_col = 0.0f;
-    for (int j = 0; j < 128; ++j) {
-        by_row = fmaxf(by_row, fabsf(at(m0 + t, k0 + j)));
-        by_col = fmaxf(by_col, fabsf(at(m0 + j, k0 + t)));
-    }
-    if (p.blocks) {
-        amax[t] = by_row;
-        __syncthreads();
-        for (int j = 0; j < 128; ++j) by_row = fmaxf(by_row, amax[j]);
-        by_col = by_row;
-    }
-    const float sr = group_scale(by_row), sc = group_scale(by_col);
-    if (p.q) {
-        if (p.blocks && t == 0) p.scale[blockIdx.y * KB + blockIdx.x] = sr;
-        if (!p.blocks && m0 + t < p.M) p.scale[blockIdx.x * p.M + m0 + t] = sr;
-        for (int j = 0; j < 128; ++j)
-            if (m0 + t < p.M && k0 + j < p.K) p.q[(m0 + t) * p.q_ld + k0 + j] = e4m3(at(m0 + t, k0 + j) / sr);
-    }
-    if (p.qt) {
-        if (p.blocks && t == 0) p.scale_t[blockIdx.x * MB + blockIdx.y] = sc;
-        if (!p.blocks && k0 + t < p.K) p.scale_t[blockIdx.y * p.K + k0 + t] = sc;
-        for (int j = 0; j < 128; ++j)
-            if (m0 + j < p.M && k0 + t < p.K) p.qt[(k0 + t) * p.qt_ld + m0 + j] = e4m3(at(m0 + j, k0 + t) / sc);
+void fwd_types(const Norm& p, bool aligned, cudaStream_t stream) {
+    if (p.out_type == SSD_TYPE_E4M3) fwd_rows<T, T, true>(p, aligned, stream);
+    else if (p.out_type == SSD_TYPE_BF16) fwd_rows<T, __nv_bfloat16, false>(p, aligned, stream);
+    else fwd_rows<T, float, false>(p, aligned, stream);
+}
+
+template <typename T, int W>
+void bwd(const NormBwd& p, bool aligned, int grid, cudaStream_t stream) {
+    if (aligned) norm_bwd<T, W, true><<<grid, 32 * cta_warps<W>(), 0, stream>>>(p);
+    else norm_bwd<T, W, false><<<grid, 32 * cta_warps<W>(), 0, stream>>>(p);
+}
+template <typename T>
+void bwd_rows(const NormBwd& p, bool aligned, int grid, cudaStream_t stream) {
+    switch (row_warps(p.D)) {
+        case 1: return bwd<T, 1>(p, aligned, grid, stream);
+        case 2: return bwd<T, 2>(p, aligned, grid, stream);
+        case 4: return bwd<T, 4>(p, aligned, grid, stream);
+        case 8: return bwd<T, 8>(p, aligned, grid, stream);
+        case 16: return bwd<T, 16>(p, aligned, grid, stream);
+        default: return bwd<T, 32>(p, aligned, grid, stream);
     }
 }
 
 }  // namespace
 
 int norm_fwd_launch(const Norm& p, cudaStream_t stream) {
-    if (p.bf16) norm_fwd<__nv_bfloat16><<<(unsigned)p.M, kThreads, 0, stream>>>(p);
-    else norm_fwd<float><<<(unsigned)p.M, kThreads, 0, stream>>>(p);
+    const size_t e = p.bf16 ? 2 : 4, eo = p.out_type == SSD_TYPE_F32 ? 4 : p.out_type == SSD_TYPE_BF16 ? 2 : 1;
+    const bool aligned = p.D % (16 / (int)e) == 0 && rows16(p.x, p.x_ld, e) && rows16(p.res, p.res_ld, e) &&
+                         rows16(p.r, p.r_ld, e) && rows16(p.y, p.y_ld, eo) && rows16(p.w, 0, 4);
+    if (p.bf16) fwd_types<__nv_bfloat16>(p, aligned, stream);
+    else fwd_types<float>(p, aligned, stream);
     return 1;
 }
 
-int norm_bwd_parts(int64_t M, int64_t) { return (int)(M < 1024 ? 1 : M / 1024 < 64 ? M / 1024 : 64); }
+// The CTAs that walk the rows: two an SM, fewer for few rows and (their shares of dw being written
+// and read again) for wide ones.
+int norm_bwd_parts(int64_t M, int64_t D) {
+    const int w = row_warps(D), rows = w > 8 ? 1 : 8 / w;
+    const int64_t ctas = (M + rows - 1) / rows, most = D <= 2048 ? 304 : 152;
+    return (int)(ctas < most ? ctas : most);
+}
 
 int norm_bwd_launch(const NormBwd& p, cudaStream_t stream) {
-    int launches = 1;
-    if (p.dw) {
-        const int parts = norm_bwd_parts(p.M, p.D);
-        const dim3 grid((p.D + 31) / 32, parts);
-        if (p.bf16) norm_bwd_dw<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(p, parts);
-        else norm_bwd_dw<float><<<grid, kThreads, 0, stream>>>(p, parts);
-        norm_bwd_sum<<<(p.D + kThreads - 1) / kThreads, kThreads, 0, stream>>>(p, parts);
-        launches += 2;
-    }
-    if (p.bf16) norm_bwd<__nv_bfloat16><<<(unsigned)p.M, kThreads, 0, stream>>>(p);
-    else norm_bwd<float><<<(unsigned)p.M, kThreads, 0, stream>>>(p);
-    return launches;
-}
-
-int quantize_launch(const Quant& p, cudaStream_t stream) {
-    const dim3 grid((unsigned)((p.K + 127) / 128), (unsigned)((p.M + 127) / 128));
-    if (grid.y > 65535) return SSDC_ERR_UNSUPPORTED;
-    if (p.bf16) quantize<__nv_bfloat16><<<grid, 128, 0, stream>>>(p);
-    else quantize<float><<<grid, 128, 0, stream>>>(p);
-    return 1;
+    const size_t e = p.bf16 ? 2 : 4;
+    const bool aligned = p.D % (16 / (int)e) == 0 && rows16(p.dy, p.dy_ld, e) && rows16(p.dr, p.dr_ld, e) &&
+                         rows16(p.r, p.r_ld, e) && rows16(p.dx, p.dx_ld, e) && rows16(p.w, 0, 4);
+    const int parts = norm_bwd_parts(p.M, p.D);
+    if (p.bf16) bwd_rows<__nv_bfloat16>(p, aligned, parts, stream);
+    else bwd_rows<float>(p, aligned, parts, stream);
+    if (!p.dw) return 1;
+    if (launch_dependent(norm_bwd_sum, dim3((p.D + 31) / 32), dim3(256), 0, stream, (const float*)p.partial, p.dw, p.D, parts) !=
+        cudaSuccess)
+        return SSDC_ERR_CUDA;
+    return 2;
 }
 
 }  // namespace block
