@@ -41,9 +41,24 @@ __device__ __forceinline__ float sigmoid(float z) {
     return s;
 }
 
-// The scale of a group and an element's e4m3 value. Both divisions are the rounded ones:
-// an element that lies midway between two e4m3 values must round as x / scale does.
-__device__ __forceinline__ float group_scale(float amax) { return fmaxf(amax, 7.88860905e-31f /* 2^-100 */) / 448.0f; }
+// The scale of a group, rounded to nearest, and a quotient by it. An element that lies midway
+// between two e4m3 values must round as x / scale does, so the quotient is the rounded one: the
+// product with the rounded reciprocal, corrected by its exact remainder (Markstein's method; a
+// division for each element took as long as its memory). An infinite scale gives NaNs.
+struct Scale {
+    float s, inv;
+    __device__ __forceinline__ explicit Scale(float amax)
+        : s(fmaxf(amax, 7.88860905e-31f /* 2^-100 */) / 448.0f), inv(1.0f / s) {}
+    // (x + lo) / s for a small lo
+    __device__ __forceinline__ float quotient(float x) const {
+        const float q = x * inv;
+        return fmaf(fmaf(-q, s, x), inv, q);
+    }
+    __device__ __forceinline__ float quotient(float x, float lo) const {
+        const float q = x * inv;
+        return fmaf(fmaf(-q, s, x) + lo, inv, q);
+    }
+};
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }

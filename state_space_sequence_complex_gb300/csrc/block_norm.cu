@@ -181,15 +181,15 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
         }
         if (kFp8) {
             amax = warp_max<L::kGroupLanes>(amax);
-            const float s = group_scale(amax), inv = 1.0f / s;
+            const Scale s(amax);
             const int first = base + L::run_at(i0, lane);  // in the same group for all its lanes and runs
-            if (lane % L::kGroupLanes == 0 && first < p.D) p.scale[(int64_t)(first / SSD_FP8_GROUP) * p.M + m] = s;
+            if (lane % L::kGroupLanes == 0 && first < p.D) p.scale[(int64_t)(first / SSD_FP8_GROUP) * p.M + m] = s.s;
 #pragma unroll
             for (int i = i0; i < i0 + L::kGroupRuns; ++i) {
                 const int at = L::run_at(i, lane);
                 float q[kRun];
 #pragma unroll
-                for (int e = 0; e < kRun; ++e) q[e] = fmaf(lo[(i - i0) * kRun + e], inv, v[i * kRun + e] / s);
+                for (int e = 0; e < kRun; ++e) q[e] = s.quotient(v[i * kRun + e], lo[(i - i0) * kRun + e]);
                 if (base + at < p.D) store_e4m3<kRun>(static_cast<uint8_t*>(p.y) + m * p.y_ld + base + at, q);
             }
         }
@@ -217,6 +217,14 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
         const T* r = static_cast<const T*>(p.r) + m * p.r_ld + base;
         const T* dr = static_cast<const T*>(p.dr) + m * p.dr_ld + base;
         const float rstd = in ? __ldg(p.rstd + m) : 0.0f;
+        // the next row's lines on their way into L2 (a lane a line of each array)
+        const int64_t next = (int64_t)gridDim.x * kRows;
+        const int ahead = lane * (128 / (int)sizeof(T));
+        if (m + next < p.M && ahead < kWarpSpan && base + ahead < p.D) {
+            ptx::prefetch_l2(dy + next * p.dy_ld + ahead);
+            ptx::prefetch_l2(r + next * p.r_ld + ahead);
+            if (p.dr) ptx::prefetch_l2(dr + next * p.dr_ld + ahead);
+        }
         float g[kVals], xh[kVals], s = 0.0f;
 #pragma unroll
         for (int i = 0; i < L::kRuns; ++i) {

@@ -80,11 +80,11 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
     if (p.q) {
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            const float s = group_scale(row_amax[r]);
+            const Scale s(row_amax[r]);
             if (r < rows && cols > 0) {
                 float q[kCols];
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) q[c] = v[r][c] / s;
+                for (int c = 0; c < kCols; ++c) q[c] = s.quotient(v[r][c]);
                 uint8_t* to = p.q + (m0 + r) * p.q_ld + k0;
                 if (cols == kCols) {
                     store_e4m3<kCols>(to, q);
@@ -94,8 +94,8 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
                         if (c < cols) to[c] = e4m3(q[c]);
                 }
                 if (lane == 0) {
-                    if (!kBlocks) p.scale[tk * p.M + m0 + r] = s;
-                    else if (t == 0 && r == 0) p.scale[tm * tiles_k + tk] = s;
+                    if (!kBlocks) p.scale[tk * p.M + m0 + r] = s.s;
+                    else if (t == 0 && r == 0) p.scale[tm * tiles_k + tk] = s.s;
                 }
             }
         }
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
     if (kBlocks) {
 #pragma unroll
         for (int c = 0; c < kCols; ++c) col_amax[c] = row_amax[0];
-        if (t == 0) p.scale_t[tk * tiles_m + tm] = group_scale(row_amax[0]);
+        if (t == 0) p.scale_t[tk * tiles_m + tm] = Scale(row_amax[0]).s;
     } else {
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
@@ -120,17 +120,17 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
 #pragma unroll
             for (int k = 0; k < kThreads / kLanes; ++k) a = fmaxf(a, col_max[k][lane * kCols + c]);
             col_amax[c] = a;
-            if (strip == 0 && c < cols) p.scale_t[tm * p.K + k0 + c] = group_scale(a);
+            if (strip == 0 && c < cols) p.scale_t[tm * p.K + k0 + c] = Scale(a).s;
         }
     }
     // a column's kRows bytes as one piece; pieces of a column exchanged by the column's thread
     constexpr int kPieces = kTile / kRows;
 #pragma unroll
     for (int c = 0; c < kCols; ++c) {
-        const float s = group_scale(col_amax[c]);
+        const Scale s(col_amax[c]);
         float q[kRows];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) q[r] = v[r][c] / s;
+        for (int r = 0; r < kRows; ++r) q[r] = s.quotient(v[r][c]);
         store_e4m3<kRows>(&tile[lane * kCols + c][(strip ^ (lane % kPieces)) * kRows], q);
     }
     __syncthreads();
