@@ -47,8 +47,13 @@ __device__ __forceinline__ float sigmoid(float z) {
 // division for each element took as long as its memory). An infinite scale gives NaNs.
 struct Scale {
     float s, inv;
-    __device__ __forceinline__ explicit Scale(float amax)
-        : s(fmaxf(amax, 7.88860905e-31f /* 2^-100 */) / 448.0f), inv(1.0f / s) {}
+    Scale() = default;
+    __device__ __forceinline__ explicit Scale(float amax) {
+        constexpr float k = 1.0f / 448.0f;
+        const float a = fmaxf(amax, 7.88860905e-31f /* 2^-100 */), q = a * k;
+        s = isinf(a) ? a : fmaf(fmaf(-q, 448.0f, a), k, q);
+        inv = __frcp_rn(s);
+    }
     // (x + lo) / s for a small lo
     __device__ __forceinline__ float quotient(float x) const {
         const float q = x * inv;

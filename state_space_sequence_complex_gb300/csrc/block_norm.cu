@@ -3,10 +3,12 @@
 //   r = x + residual,  rstd = 1 / sqrt(mean(r^2) + eps),  y = r rstd w
 //
 // Bound by HBM. A row is read once and stays in registers between the sum of squares and
-// the output: a warp holds 1024 features, 32 a lane, and up to 32 warps share a row. A
+// the output: a lane holds 8 to 32 features (kVals), and up to 32 warps share a row. A
 // lane's features are vectors of 16 bytes (bfloat16: 8, so that a group of 128 features is
 // half a warp; fp32: 4, a whole one), or, for rows that do not start at multiples of 16
 // bytes, single features 32 apart.
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "block_common.cuh"
@@ -19,12 +21,11 @@ namespace block {
 
 namespace {
 
-constexpr int kVals = 32, kWarpSpan = 32 * kVals;  // features of a lane and of a warp
-
 // Which features a lane holds: value i of lane l is feature base + at(i, l). A run is kRun
 // adjacent features, one load.
-template <typename T, bool kAligned>
+template <typename T, bool kAligned, int kVals>
 struct Layout {
+    static constexpr int kWarpSpan = 32 * kVals;  // features of a warp
     static constexpr int kRun = kAligned ? 16 / (int)sizeof(T) : 1;
     static constexpr int kRuns = kVals / kRun;
     static constexpr int kGroupRuns = kAligned ? 1 : 4;              // runs of a lane in a group of 128
@@ -106,13 +107,16 @@ __device__ __forceinline__ float row_sum(float v, float (*part)[32], int slot, i
     return s;
 }
 
+// CTAs of the gradients' kernel an SM takes (its registers), by a lane's features.
+constexpr int bwd_ctas(int vals) { return vals == 32 ? 2 : vals == 16 ? 3 : 4; }
+
 template <int kRowWarps>
 constexpr int cta_warps() { return kRowWarps > 8 ? kRowWarps : 8; }
 
-template <typename T, typename TO, bool kFp8, int kRowWarps, bool kAligned>
+template <typename T, typename TO, bool kFp8, int kVals, int kRowWarps, bool kAligned>
 __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1 : 4) norm_fwd(const Norm p) {
-    using L = Layout<T, kAligned>;
-    constexpr int kWarps = cta_warps<kRowWarps>(), kRun = L::kRun;
+    using L = Layout<T, kAligned, kVals>;
+    constexpr int kWarps = cta_warps<kRowWarps>(), kRun = L::kRun, kWarpSpan = L::kWarpSpan;
     __shared__ float part[1][32];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t m = (int64_t)blockIdx.x * (kWarps / kRowWarps) + warp / kRowWarps;
@@ -198,10 +202,10 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
 
 // Gradients. A warp walks rows kRows apart and adds up its share of dw in registers; the CTA's
 // warps that hold the same features join theirs at the end, one row of `partial` a CTA.
-template <typename T, int kRowWarps, bool kAligned>
-__global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1 : 2) norm_bwd(const NormBwd p) {
-    using L = Layout<T, kAligned>;
-    constexpr int kWarps = cta_warps<kRowWarps>(), kRun = L::kRun, kRows = kWarps / kRowWarps;
+template <typename T, int kVals, int kRowWarps, bool kAligned>
+__global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1 : bwd_ctas(kVals)) norm_bwd(const NormBwd p) {
+    using L = Layout<T, kAligned, kVals>;
+    constexpr int kWarps = cta_warps<kRowWarps>(), kRun = L::kRun, kRows = kWarps / kRowWarps, kWarpSpan = L::kWarpSpan;
     __shared__ float part[2][32];
     __shared__ float join[kRows > 1 ? kWarps - kRowWarps : 1][kRows > 1 ? kWarpSpan / 4 : 1];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -319,57 +323,85 @@ __global__ void __launch_bounds__(256) norm_bwd_sum(const float* partial, float*
     }
 }
 
-// Warps of a row: a power of two.
-int row_warps(int64_t D) {
-    int w = 1;
-    while (w * kWarpSpan < D) w *= 2;
-    return w;
-}
-
 bool rows16(const void* q, int64_t ld, size_t elem) {
     return q == nullptr || (reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * (int64_t)elem % 16 == 0);
 }
 
-template <typename T, typename TO, bool kFp8, int W>
-void fwd(const Norm& p, bool aligned, cudaStream_t stream) {
-    constexpr int rows = cta_warps<W>() / W, threads = 32 * cta_warps<W>();
-    const unsigned grid = (unsigned)((p.M + rows - 1) / rows);
-    if (aligned) norm_fwd<T, TO, kFp8, W, true><<<grid, threads, 0, stream>>>(p);
-    else norm_fwd<T, TO, kFp8, W, false><<<grid, threads, 0, stream>>>(p);
+// Features a lane holds, and warps of a row (a power of two). Rows in 16-byte loads: 32 bfloat16
+// (M 32768 D 1024, 8-bit output: 44 us; 16: 52 us) or 16 fp32 (M 3001 D 1536: 12.6 us; 32: 14.8 us),
+// which is four or eight loads under way. Rows in single loads: 8, for more warps to a row
+// (M 3001 D 1537 fp32: 17 us; 32: 35 us). The widest rows need 32 either way.
+int lane_vals(int64_t D, bool bf16, bool aligned) {
+    const int v = !aligned ? 8 : bf16 ? 32 : 16;
+    return D <= 32 * 32 * v ? v : 32;
 }
-template <typename T, typename TO, bool kFp8>
-void fwd_rows(const Norm& p, bool aligned, cudaStream_t stream) {
-    switch (row_warps(p.D)) {
-        case 1: return fwd<T, TO, kFp8, 1>(p, aligned, stream);
-        case 2: return fwd<T, TO, kFp8, 2>(p, aligned, stream);
-        case 4: return fwd<T, TO, kFp8, 4>(p, aligned, stream);
-        case 8: return fwd<T, TO, kFp8, 8>(p, aligned, stream);
-        case 16: return fwd<T, TO, kFp8, 16>(p, aligned, stream);
-        default: return fwd<T, TO, kFp8, 32>(p, aligned, stream);
-    }
-}
-template <typename T>
-void fwd_types(const Norm& p, bool aligned, cudaStream_t stream) {
-    if (p.out_type == SSD_TYPE_E4M3) fwd_rows<T, T, true>(p, aligned, stream);
-    else if (p.out_type == SSD_TYPE_BF16) fwd_rows<T, __nv_bfloat16, false>(p, aligned, stream);
-    else fwd_rows<T, float, false>(p, aligned, stream);
+int row_warps(int64_t D, int vals) {
+    int w = 1;
+    while (w * 32 * vals < D) w *= 2;
+    return w;
 }
 
-template <typename T, int W>
-void bwd(const NormBwd& p, bool aligned, int grid, cudaStream_t stream) {
-    if (aligned) norm_bwd<T, W, true><<<grid, 32 * cta_warps<W>(), 0, stream>>>(p);
-    else norm_bwd<T, W, false><<<grid, 32 * cta_warps<W>(), 0, stream>>>(p);
+// Calls f.template operator()<kVals, kRowWarps, kAligned>() for a row of D features.
+template <typename T, typename F>
+void by_row(int64_t D, bool aligned, const F& f) {
+    const int vals = lane_vals(D, sizeof(T) == 2, aligned), w = row_warps(D, vals);
+    auto warps = [&](auto v, auto al) {
+        constexpr int kVals = decltype(v)::value;
+        constexpr bool kAligned = decltype(al)::value;
+        constexpr bool kWide = kVals == 32 && !(kAligned && sizeof(T) == 2);  // taken for the widest rows only
+        if constexpr (!kWide) {
+            switch (w) {
+                case 1: return f.template run<kVals, 1, kAligned>();
+                case 2: return f.template run<kVals, 2, kAligned>();
+                case 4: return f.template run<kVals, 4, kAligned>();
+                case 8: return f.template run<kVals, 8, kAligned>();
+                default: break;
+            }
+        }
+        return w <= 16 ? f.template run<kVals, 16, kAligned>() : f.template run<kVals, 32, kAligned>();
+    };
+    using std::integral_constant;
+    constexpr int kOwn = sizeof(T) == 2 ? 32 : 16;
+    if (aligned && vals == kOwn) warps(integral_constant<int, kOwn>{}, std::true_type{});
+    else if (aligned) warps(integral_constant<int, 32>{}, std::true_type{});
+    else if (vals == 8) warps(integral_constant<int, 8>{}, std::false_type{});
+    else warps(integral_constant<int, 32>{}, std::false_type{});
+}
+
+template <typename T, typename TO, bool kFp8>
+struct Fwd {
+    const Norm& p;
+    cudaStream_t stream;
+    template <int kVals, int W, bool kAligned>
+    void run() const {
+        constexpr int rows = cta_warps<W>() / W;
+        norm_fwd<T, TO, kFp8, kVals, W, kAligned>
+            <<<(unsigned)((p.M + rows - 1) / rows), 32 * cta_warps<W>(), 0, stream>>>(p);
+    }
+};
+template <typename T>
+void fwd(const Norm& p, bool aligned, cudaStream_t stream) {
+    if (p.out_type == SSD_TYPE_E4M3) by_row<T>(p.D, aligned, Fwd<T, T, true>{p, stream});
+    else if (p.out_type == SSD_TYPE_BF16) by_row<T>(p.D, aligned, Fwd<T, __nv_bfloat16, false>{p, stream});
+    else by_row<T>(p.D, aligned, Fwd<T, float, false>{p, stream});
 }
 template <typename T>
-void bwd_rows(const NormBwd& p, bool aligned, int grid, cudaStream_t stream) {
-    switch (row_warps(p.D)) {
-        case 1: return bwd<T, 1>(p, aligned, grid, stream);
-        case 2: return bwd<T, 2>(p, aligned, grid, stream);
-        case 4: return bwd<T, 4>(p, aligned, grid, stream);
-        case 8: return bwd<T, 8>(p, aligned, grid, stream);
-        case 16: return bwd<T, 16>(p, aligned, grid, stream);
-        default: return bwd<T, 32>(p, aligned, grid, stream);
+struct Bwd {
+    const NormBwd& p;
+    int ctas;
+    cudaStream_t stream;
+    template <int kVals, int W, bool kAligned>
+    void run() const {
+        norm_bwd<T, kVals, W, kAligned><<<ctas, 32 * cta_warps<W>(), 0, stream>>>(p);
     }
+};
+
+// The CTAs that walk the rows: as many as the SMs hold, fewer for few rows and (their shares of dw
+// being written and read again) for wide ones.
+int bwd_parts(int64_t M, int64_t D, bool bf16, bool aligned) {
+    const int vals = lane_vals(D, bf16, aligned), w = row_warps(D, vals), rows = w > 8 ? 1 : 8 / w;
+    const int64_t ctas = (M + rows - 1) / rows, most = D <= 2048 ? 152 * bwd_ctas(vals) : 152;
+    return (int)(ctas < most ? ctas : most);
 }
 
 }  // namespace
@@ -378,26 +410,27 @@ int norm_fwd_launch(const Norm& p, cudaStream_t stream) {
     const size_t e = p.bf16 ? 2 : 4, eo = p.out_type == SSD_TYPE_F32 ? 4 : p.out_type == SSD_TYPE_BF16 ? 2 : 1;
     const bool aligned = p.D % (16 / (int)e) == 0 && rows16(p.x, p.x_ld, e) && rows16(p.res, p.res_ld, e) &&
                          rows16(p.r, p.r_ld, e) && rows16(p.y, p.y_ld, eo) && rows16(p.w, 0, 4);
-    if (p.bf16) fwd_types<__nv_bfloat16>(p, aligned, stream);
-    else fwd_types<float>(p, aligned, stream);
+    if (p.bf16) fwd<__nv_bfloat16>(p, aligned, stream);
+    else fwd<float>(p, aligned, stream);
     return 1;
 }
 
-// The CTAs that walk the rows: two an SM, fewer for few rows and (their shares of dw being written
-// and read again) for wide ones.
-int norm_bwd_parts(int64_t M, int64_t D) {
-    const int w = row_warps(D), rows = w > 8 ? 1 : 8 / w;
-    const int64_t ctas = (M + rows - 1) / rows, most = D <= 2048 ? 304 : 152;
-    return (int)(ctas < most ? ctas : most);
+int norm_bwd_parts(int64_t M, int64_t D) {  // for any type and alignment
+    int most = 0;
+    for (int k = 0; k < 4; ++k) {
+        const int n = bwd_parts(M, D, (k & 1) != 0, (k & 2) != 0);
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 int norm_bwd_launch(const NormBwd& p, cudaStream_t stream) {
     const size_t e = p.bf16 ? 2 : 4;
     const bool aligned = p.D % (16 / (int)e) == 0 && rows16(p.dy, p.dy_ld, e) && rows16(p.dr, p.dr_ld, e) &&
                          rows16(p.r, p.r_ld, e) && rows16(p.dx, p.dx_ld, e) && rows16(p.w, 0, 4);
-    const int parts = norm_bwd_parts(p.M, p.D);
-    if (p.bf16) bwd_rows<__nv_bfloat16>(p, aligned, parts, stream);
-    else bwd_rows<float>(p, aligned, parts, stream);
+    const int parts = bwd_parts(p.M, p.D, p.bf16, aligned);
+    if (p.bf16) by_row<__nv_bfloat16>(p.D, aligned, Bwd<__nv_bfloat16>{p, parts, stream});
+    else by_row<float>(p.D, aligned, Bwd<float>{p, parts, stream});
     if (!p.dw) return 1;
     if (launch_dependent(norm_bwd_sum, dim3((p.D + 31) / 32), dim3(256), 0, stream, (const float*)p.partial, p.dw, p.D, parts) !=
         cudaSuccess)

@@ -25,39 +25,38 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
     constexpr int kCols = 16 / sizeof(T), kLanes = kTile / kCols, kRows = kTile * kLanes / kThreads;
     __shared__ __align__(16) uint8_t tile[kTile][kTile];
     __shared__ float col_max[kThreads / kLanes][kTile];
+    __shared__ Scale col_scale[kTile];
     const int t = threadIdx.x, lane = t % kLanes, strip = t / kLanes;  // columns kCols lane .., rows kRows strip ..
     const int64_t tiles_k = (p.K + kTile - 1) / kTile, tiles_m = (p.M + kTile - 1) / kTile;
     const int64_t tk = blockIdx.x % tiles_k, tm = blockIdx.x / tiles_k;
     const int64_t m0 = tm * kTile + strip * kRows, k0 = tk * kTile + lane * kCols;
     const int cols = (int)max((int64_t)0, min((int64_t)kCols, p.K - k0)), rows = (int)max((int64_t)0, min((int64_t)kRows, p.M - m0));
     float v[kRows][kCols];
+    const T* x = static_cast<const T*>(p.x) + m0 * p.x_ld + k0;
+    if (kAligned && rows == kRows && cols == kCols) {
+        uint4 w[kRows];  // all on their way before the first is used
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        const T* x = static_cast<const T*>(p.x) + (m0 + r) * p.x_ld + k0;
+        for (int r = 0; r < kRows; ++r) w[r] = __ldg(reinterpret_cast<const uint4*>(x + r * p.x_ld));
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) v[r][c] = 0.0f;
-        if (r < rows) {
-            if (kAligned && cols == kCols) {
+        for (int r = 0; r < kRows; ++r) {
+            const uint32_t u[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 if constexpr (sizeof(T) == 2) {
-                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(x));
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[r][2 * i] = ptx::bf16_lo(u[i]);
-                        v[r][2 * i + 1] = ptx::bf16_hi(u[i]);
-                    }
+                    v[r][2 * i] = ptx::bf16_lo(u[i]);
+                    v[r][2 * i + 1] = ptx::bf16_hi(u[i]);
                 } else {
-                    const float4 w = __ldg(reinterpret_cast<const float4*>(x));
-                    v[r][0] = w.x; v[r][1] = w.y; v[r][2] = w.z; v[r][3] = w.w;
+                    v[r][i] = __uint_as_float(u[i]);
                 }
-            } else {
-#pragma unroll
-                for (int c = 0; c < kCols; ++c)
-                    if (c < cols) v[r][c] = to_f32(x[c]);
             }
         }
+    } else {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) v[r][c] = r < rows && c < cols ? to_f32(x[r * p.x_ld + c]) : 0.0f;
     }
-    float row_amax[kRows], col_amax[kCols];
+    float row_amax[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
         row_amax[r] = 0.0f;
@@ -101,10 +100,11 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
         }
     }
     if (!p.qt) return;
+    Scale cs[kCols];
     if (kBlocks) {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) col_amax[c] = row_amax[0];
-        if (t == 0) p.scale_t[tk * tiles_m + tm] = Scale(row_amax[0]).s;
+        for (int c = 0; c < kCols; ++c) cs[c] = Scale(row_amax[0]);
+        if (t == 0) p.scale_t[tk * tiles_m + tm] = cs[0].s;
     } else {
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
@@ -114,23 +114,25 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
             col_max[strip][lane * kCols + c] = a;
         }
         __syncthreads();
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) {
+        if (t < kTile) {  // one thread a column
             float a = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kThreads / kLanes; ++k) a = fmaxf(a, col_max[k][lane * kCols + c]);
-            col_amax[c] = a;
-            if (strip == 0 && c < cols) p.scale_t[tm * p.K + k0 + c] = Scale(a).s;
+            for (int k = 0; k < kThreads / kLanes; ++k) a = fmaxf(a, col_max[k][t]);
+            const Scale s(a);
+            col_scale[t] = s;
+            if (tk * kTile + t < p.K) p.scale_t[tm * p.K + tk * kTile + t] = s.s;
         }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) cs[c] = col_scale[lane * kCols + c];
     }
     // a column's kRows bytes as one piece; pieces of a column exchanged by the column's thread
     constexpr int kPieces = kTile / kRows;
 #pragma unroll
     for (int c = 0; c < kCols; ++c) {
-        const Scale s(col_amax[c]);
         float q[kRows];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) q[r] = s.quotient(v[r][c]);
+        for (int r = 0; r < kRows; ++r) q[r] = cs[c].quotient(v[r][c]);
         store_e4m3<kRows>(&tile[lane * kCols + c][(strip ^ (lane % kPieces)) * kRows], q);
     }
     __syncthreads();
