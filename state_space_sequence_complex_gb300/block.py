@@ -417,7 +417,8 @@ class Fp8Product:
     (ceil(K / 128), M), b (N, K) with block scales (ceil(N / 128), ceil(K / 128)), or
     with row scales (ceil(K / 128), N) where ``b_scales`` is ``"rows"``. Operand rows
     start 16-byte aligned (``fp8_empty``, ``Fp8Quantize``, ``ResidualNorm``). Returns
-    C (M, N) in ``out`` (``"bf16"`` or ``"fp32"``)."""
+    C (M, N) in ``out`` (``"bf16"`` or ``"fp32"``); its rows start 16-byte aligned too,
+    so it is not contiguous where N is no multiple of 8 (bf16) or 4 (fp32)."""
 
     def __init__(self, M, N, K, out="bf16", b_scales="blocks", device="cuda"):
         _sizes(M=M, N=N, K=K)
@@ -432,9 +433,10 @@ class Fp8Product:
         KB = fp8_groups(K)
         self.a_shape, self.a_scale_shape, self.b_shape = (M, K), (KB, M), (N, K)
         self.b_scale_shape = (fp8_groups(N), KB) if self.b_scales else (KB, N)
-        self.c = torch.empty((M, N), dtype=_DTYPES[out], device=self.device)
+        per = 8 if out == "bf16" else 4
+        self.c = torch.empty((M, -(-N // per) * per), dtype=_DTYPES[out], device=self.device)[:, :N]
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-        self._c, self._ws = ssd_rows(self.c.data_ptr(), N), self.workspace.data_ptr()
+        self._c, self._ws = ssd_rows(self.c.data_ptr(), self.c.stride(0)), self.workspace.data_ptr()
 
     def __call__(self, a, a_scale, b, b_scale, stream=None):
         d, f8, f32 = self.device, torch.float8_e4m3fn, torch.float32
@@ -551,5 +553,6 @@ class _Fp8Linear(torch.autograd.Function):
 
 
 def fp8_linear(x, w):
-    """Differentiable x w^T in 8-bit products (``Fp8Linear``): returns a new (M, N) tensor."""
+    """Differentiable x w^T in 8-bit products (``Fp8Linear``): returns a new (M, N) tensor
+    (laid out as ``Fp8Product``'s)."""
     return _Fp8Linear.apply(x, w)

@@ -108,6 +108,32 @@ __device__ __forceinline__ void store_piece(const Product& p, const CUtensorMap*
     for (int e = 0; e < 32; ++e) st[lane * 33 + e] = word(e);
     __syncwarp();
     const int cols = (int)min((int64_t)kPiece, p.N - n), rows = (int)min((int64_t)32, p.M - m0);
+    if (kHalf && cols == kPiece) {
+        // many rows under way at a time; a row is shifted by none or one of its values
+        constexpr int kAtOnce = 8;
+        char* c = reinterpret_cast<char*>(static_cast<T*>(p.c) + m0 * p.c_ld + n) + 4 * lane;
+        const int64_t pitch = p.c_ld * (int64_t)sizeof(T);
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
+            uint32_t w[kAtOnce], next[kAtOnce];
+#pragma unroll
+            for (int r = 0; r < kAtOnce; ++r) {
+                w[r] = st[(r0 + r) * 33 + lane];
+                next[r] = st[(r0 + r) * 33 + lane + 1];  // (the 33rd word of a row is not used)
+            }
+#pragma unroll
+            for (int r = 0; r < kAtOnce; ++r) {
+                char* row = c + (r0 + r) * pitch;
+                if (r0 + r < rows) {
+                    const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(row) >> 1) & 1;
+                    if (!odd || lane < 31) *reinterpret_cast<uint32_t*>(row + 2 * odd) = __funnelshift_r(w[r], next[r], 16 * odd);
+                    else *reinterpret_cast<uint16_t*>(row + 2) = (uint16_t)(w[r] >> 16);
+                    if (odd && lane == 0) *reinterpret_cast<uint16_t*>(row) = (uint16_t)w[r];
+                }
+            }
+        }
+        return;
+    }
     for (int r = 0; r < rows; ++r) {
         T* c = static_cast<T*>(p.c) + (m0 + r) * p.c_ld + n;
         const uint32_t w = st[r * 33 + lane];
@@ -427,7 +453,7 @@ int matmul_launch(const Matmul& p, cudaStream_t stream) {
         const int64_t tiles = (int64_t)q.m_tiles * ((p.N + bn - 1) / bn);
         return (tiles + sms / 2 - 1) / (sms / 2) * bn;
     };
-    return 1.4 * rounds(128) < rounds(256) ? launch_pair_types<128>(p, q, sms, stream)
+    return 1.2 * rounds(128) < rounds(256) ? launch_pair_types<128>(p, q, sms, stream)
                                      : launch_pair_types<256>(p, q, sms, stream);
 }
 

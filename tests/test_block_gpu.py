@@ -489,6 +489,27 @@ def test_product_padding_is_not_read():
     assert torch.equal(block.Fp8Product(M, N, K, out="fp32")(dirty(a), a_s, dirty(b), b_s), c)
 
 
+@pytest.mark.parametrize("M,N,pitch,at", [(5, 33, 33, 0), (70, 255, 255, 1), (300, 513, 513, 0), (129, 190, 203, 3), (33, 64, 65, 0)])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_product_rows_that_start_anywhere(M, N, pitch, at, out):
+    """C in rows of any pitch from any element: the same values, and nothing written beside them."""
+    K = 384
+    a, a_s, _ = operand(M, K, seed=1)
+    b, b_s, _ = operand(N, K, seed=2, blocks=True)
+    plan = block.Fp8Product(M, N, K, out=out)
+    want = plan(a, a_s, b, b_s).clone()
+    store = torch.full((M * pitch + at + 64,), 7.0, dtype=DT[out], device="cuda")
+    c = store[at:at + M * pitch].view(M, pitch)[:, :N]
+    rows = lambda t: block.ssd_rows(t.data_ptr(), t.stride(0))
+    rc = block.load().ssd_fp8_matmul(rows(a), a_s.data_ptr(), rows(b), b_s.data_ptr(), 1, M, N, K, 1 if out == "bf16" else 0,
+                                     block.ssd_rows(c.data_ptr(), pitch), plan.workspace.data_ptr(), plan.workspace.numel(),
+                                     torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    assert torch.equal(c, want)
+    c.fill_(7.0)
+    assert (store == 7.0).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(64, 128, 128), (300, 257, 520), (1000, 640, 384)])
 def test_linear_step(M, N, K):
     """y, dx and dw against the products of the quantised values in 64 bits."""
