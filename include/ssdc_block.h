@@ -190,6 +190,22 @@ int ssd_fp8_matmul(ssd_rows_in a, const float *a_scale, ssd_rows_in b, const flo
                    int64_t M, int64_t N, int64_t K, int32_t out_type, ssd_rows_out c, void *workspace,
                    size_t ws_bytes, cudaStream_t stream);
 
+/*
+ * Any of the calls above that launch work, from its arguments as 64-bit words: in
+ * order, structures member by member, integers sign-extended, eps as the bits of a
+ * float in the low half. For bindings in which passing twenty arguments takes
+ * longer than launching the kernel. The checks and results are those of the call;
+ * an unknown call is SSDC_ERR_INVALID.
+ */
+#define SSD_CALL_GATED_SCAN_FWD 0      /* 21 words */
+#define SSD_CALL_GATED_SCAN_STEP 1     /* 17 words */
+#define SSD_CALL_GATED_SCAN_BWD 2      /* 30 words */
+#define SSD_CALL_RESIDUAL_NORM_FWD 3   /* 16 words */
+#define SSD_CALL_RESIDUAL_NORM_BWD 4   /* 16 words */
+#define SSD_CALL_FP8_QUANTIZE 5        /* 12 words */
+#define SSD_CALL_FP8_MATMUL 6          /* 15 words */
+int ssd_block_call(int32_t call, const int64_t *words, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,7 @@ it by the caller, as for any kernel.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -37,7 +38,7 @@ _DTYPES = {"fp32": torch.float32, "bf16": torch.bfloat16}
 
 EXPORTS = ("ssd_gated_scan_states_bytes", "ssd_gated_scan_fwd", "ssd_gated_scan_step", "ssd_gated_scan_bwd",
            "ssd_residual_norm_fwd", "ssd_residual_norm_bwd_workspace_bytes", "ssd_residual_norm_bwd",
-           "ssd_fp8_quantize", "ssd_fp8_matmul_workspace_bytes", "ssd_fp8_matmul")
+           "ssd_fp8_quantize", "ssd_fp8_matmul_workspace_bytes", "ssd_fp8_matmul", "ssd_block_call")
 
 
 class ssd_seq(ctypes.Structure):
@@ -52,7 +53,6 @@ class ssd_gated_dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64), ("type", ctypes.c_int32)]
 
 
-_NO_SEQ, _NO_ROWS = ssd_seq(None, 0, 0), ssd_rows(None, 0)
 _lib = None
 
 
@@ -74,7 +74,8 @@ def load() -> ctypes.CDLL:
             ("ssd_residual_norm_bwd", i32, [r, r, r, vp, vp, i64, i64, i32, r, vp, vp, sz, vp]),
             ("ssd_fp8_quantize", i32, [r, i64, i64, i32, i32, r, vp, r, vp, vp]),
             ("ssd_fp8_matmul_workspace_bytes", sz, [i64, i64, i64]),
-            ("ssd_fp8_matmul", i32, [r, vp, r, vp, i32, i64, i64, i64, i32, r, vp, sz, vp])):
+            ("ssd_fp8_matmul", i32, [r, vp, r, vp, i32, i64, i64, i64, i32, r, vp, sz, vp]),
+            ("ssd_block_call", i32, [i32, vp, vp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
     _lib = lib
@@ -96,49 +97,80 @@ def _sizes(**sizes):
             raise ValueError(f"{k} must be positive, not {v}")
 
 
-def _check(name, t, shape, dtype, device):
+# What a call's tensors have to be is kept as (dtype, shape, device index) and compared as a whole;
+# for one token or a few these checks are as long as the launch.
+
+
+def _refuse(name, t, like):
+    dtype, shape, index = like
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    want = "the CPU" if index < 0 else f"cuda:{index}"
+    raise ValueError(f"{name} must be on {want}, not {t.device}")
 
 
-def _dense(name, t, shape, dtype, device):
-    """The address of a dense tensor, or None."""
+def _dense(name, t, like):
+    """The address of a dense tensor, or 0 for None."""
     if t is None:
-        return None
-    _check(name, t, shape, dtype, device)
+        return 0
+    if (t.dtype, t.shape, t.get_device()) != like:
+        _refuse(name, t, like)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _seq(name, t, shape, dtype, device):
-    """A (B, T, D) tensor whose channels are contiguous."""
+def _rows(name, t, like):
+    """The address and row stride of a matrix with contiguous rows; zeros for None."""
     if t is None:
-        return _NO_SEQ
-    _check(name, t, shape, dtype, device)
-    sb, st, sd = t.stride()
-    if sd != 1 and shape[2] != 1:
-        raise ValueError(f"{name} must have contiguous channels")
-    return ssd_seq(t.data_ptr(), sb, st)
-
-
-def _rows(name, t, shape, dtype, device):
-    """An (M, D) tensor whose rows are contiguous."""
-    if t is None:
-        return _NO_ROWS
-    _check(name, t, shape, dtype, device)
-    ld, sd = t.stride()
-    if sd != 1 and shape[1] != 1:
+        return 0, 0
+    if (t.dtype, t.shape, t.get_device()) != like:
+        _refuse(name, t, like)
+    ld, one = t.stride()
+    if one != 1 and like[1][1] != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return ssd_rows(t.data_ptr(), ld)
+    return t.data_ptr(), ld
 
 
-def _stream(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+def _seq(name, t, like):
+    """The address and the batch and token strides of a (B, T, D) tensor with contiguous channels; zeros for None."""
+    if t is None:
+        return 0, 0, 0
+    if (t.dtype, t.shape, t.get_device()) != like:
+        _refuse(name, t, like)
+    sb, st, one = t.stride()
+    if one != 1 and like[1][2] != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    return t.data_ptr(), sb, st
+
+
+class _Call:
+    """One of the library's calls with its arguments as a block of words (``ssd_block_call``)."""
+
+    __slots__ = ("name", "number", "fn", "pack", "block", "at", "index")
+
+    def __init__(self, name, number, words, index):
+        self.name, self.number, self.index = name, number, index
+        self.fn = load().ssd_block_call
+        self.block = ctypes.create_string_buffer(8 * words)
+        self.at = ctypes.addressof(self.block)
+        self.pack = struct.Struct(f"{words}q").pack_into
+
+    def __call__(self, stream, *words):
+        self.pack(self.block, 0, *words)
+        if stream is not None:
+            stream = stream.cuda_stream
+        elif self.index >= 0:
+            stream = torch._C._cuda_getCurrentRawStream(self.index)
+        rc = self.fn(self.number, self.at, stream)
+        if rc:
+            _raise(rc, self.name)
+
+
+def _index(device):
+    return -1 if device.type == "cpu" else device.index
 
 
 def _device(device):
@@ -194,23 +226,23 @@ class GatedScan:
         if keep_states:
             self.states = torch.empty((B, -(-T // STATE_TOKENS), D), dtype=torch.float32, device=self.device)
         self.workspace = torch.zeros(64, dtype=torch.int32, device=self.device)
-        self._h = _seq("h", self.h, self.shape, self.dtype, self.device)
+        self._like = self.dtype, torch.Size(self.shape), _index(self.device)
+        self._state = torch.float32, torch.Size(self.state_shape), self._like[2]
+        self._marks = torch.uint8, torch.Size(self.mark_shape), self._like[2]
+        self._dims = B, T, D, self.dims.type
+        self._h = _seq("h", self.h, self._like)
+        self._kept = (self.h_last.data_ptr(), 0 if self.states is None else self.states.data_ptr(), self.workspace.data_ptr())
+        self._call = _Call("ssd_gated_scan_fwd", 0, 21, self._like[2])
 
     def __call__(self, x, f, i=None, h0=None, reset=None, out=None, stream=None):
         """``out``: where h goes instead of this object's ``h``, a (B, T, D) tensor
         with contiguous channels that shares no element with an input."""
         if (i is not None) != self.input_gate:
             raise ValueError("i must be given exactly when the plan has an input gate")
-        a = self.shape, self.dtype, self.device
-        h, h_out = (self.h, self._h) if out is None else (out, _seq("out", out, *a))
-        rc = load().ssd_gated_scan_fwd(
-            _seq("x", x, *a), _seq("f", f, *a), _seq("i", i, *a),
-            _dense("h0", h0, self.state_shape, torch.float32, self.device),
-            _dense("reset", reset, self.mark_shape, torch.uint8, self.device), self.dims, h_out,
-            self.h_last.data_ptr(), None if self.states is None else self.states.data_ptr(),
-            self.workspace.data_ptr(), _stream(stream, self.device))
-        if rc:
-            _raise(rc, "ssd_gated_scan_fwd")
+        like = self._like
+        h, h_out = (self.h, self._h) if out is None else (out, _seq("out", out, like))
+        self._call(stream, *_seq("x", x, like), *_seq("f", f, like), *_seq("i", i, like),
+                   _dense("h0", h0, self._state), _dense("reset", reset, self._marks), *self._dims, *h_out, *self._kept)
         return h, self.h_last
 
     def status(self, stream=None) -> int:
@@ -236,21 +268,24 @@ class GatedScanBackward:
         self.grads = {k: torch.empty(self.shape, dtype=self.dtype, device=self.device) for k in names}
         self.workspace = torch.zeros(64, dtype=torch.int32, device=self.device)
         self.grads["dh0"] = torch.empty(self.state_shape, dtype=torch.float32, device=self.device)
+        self._like = self.dtype, torch.Size(self.shape), _index(self.device)
+        self._state = torch.float32, torch.Size(self.state_shape), self._like[2]
+        self._states = torch.float32, torch.Size(self.states_shape), self._like[2]
+        self._marks = torch.uint8, torch.Size(self.mark_shape), self._like[2]
+        self._dims = B, T, D, self.dims.type
+        g = self.grads
+        self._out = (*_seq("dx", g["dx"], self._like), *_seq("df", g["df"], self._like),
+                     *_seq("di", g.get("di"), self._like), g["dh0"].data_ptr(), self.workspace.data_ptr())
+        self._call = _Call("ssd_gated_scan_bwd", 2, 30, self._like[2])
 
     def __call__(self, x, f, i, states, dh, dh_last=None, reset=None, stream=None):
         if (i is not None) != self.input_gate:
             raise ValueError("i must be given exactly when the plan has an input gate")
-        a, g, d = (self.shape, self.dtype, self.device), self.grads, self.device
-        rc = load().ssd_gated_scan_bwd(
-            _seq("x", x, *a), _seq("f", f, *a), _seq("i", i, *a),
-            _dense("states", states, self.states_shape, torch.float32, d),
-            _dense("reset", reset, self.mark_shape, torch.uint8, d), _seq("dh", dh, *a),
-            _dense("dh_last", dh_last, self.state_shape, torch.float32, d), self.dims, _seq("dx", g["dx"], *a),
-            _seq("df", g["df"], *a), _seq("di", g.get("di"), *a), g["dh0"].data_ptr(),
-            self.workspace.data_ptr(), _stream(stream, d))
-        if rc:
-            _raise(rc, "ssd_gated_scan_bwd")
-        return dict(g)
+        like = self._like
+        self._call(stream, *_seq("x", x, like), *_seq("f", f, like), *_seq("i", i, like),
+                   _dense("states", states, self._states), _dense("reset", reset, self._marks), *_seq("dh", dh, like),
+                   _dense("dh_last", dh_last, self._state), *self._dims, *self._out)
+        return dict(self.grads)
 
     def status(self, stream=None) -> int:
         return ssdc.ssd_complex_status(self.workspace, stream)
@@ -271,30 +306,19 @@ class GatedScanStep:
         self.shape = (B, D)
         self.h = torch.empty(self.shape, dtype=self.dtype, device=self.device)
         self.state = torch.empty(self.shape, dtype=torch.float32, device=self.device)
-        self._h = ssd_seq(self.h.data_ptr(), D, 0)
-
-    def _row(self, name, t):
-        if t is None:
-            return _NO_SEQ
-        _check(name, t, self.shape, self.dtype, self.device)
-        sb, sd = t.stride()
-        if sd != 1 and self.shape[1] != 1:
-            raise ValueError(f"{name} must have contiguous channels")
-        return ssd_seq(t.data_ptr(), sb, 0)
+        self._like = self.dtype, torch.Size(self.shape), _index(self.device)
+        self._state = torch.float32, torch.Size(self.shape), self._like[2]
+        self._rest, self._own = (B, D, self.type, self.h.data_ptr(), D, 0), self.state.data_ptr()
+        self._call = _Call("ssd_gated_scan_step", 1, 17, self._like[2])
 
     def __call__(self, x, f, i, state, state_out=None, stream=None):
         if (i is not None) != self.input_gate:
             raise ValueError("i must be given exactly when the plan has an input gate")
-        out = self.state if state_out is None else state_out
-        B, D = self.shape
-        f32 = torch.float32
-        rc = load().ssd_gated_scan_step(
-            self._row("x", x), self._row("f", f), self._row("i", i), _dense("state", state, self.shape, f32, self.device),
-            B, D, self.type, self._h, _dense("state_out", out, self.shape, f32, self.device),
-            _stream(stream, self.device))
-        if rc:
-            _raise(rc, "ssd_gated_scan_step")
-        return self.h, out
+        like = self._like
+        to = self._own if state_out is None else _dense("state_out", state_out, self._state)
+        self._call(stream, *_rows("x", x, like), 0, *_rows("f", f, like), 0, *_rows("i", i, like), 0,
+                   _dense("state", state, self._state), *self._rest, to)
+        return self.h, self.state if state_out is None else state_out
 
 
 # ---- residual norm
@@ -326,18 +350,19 @@ class ResidualNorm:
             self.scale = torch.empty((fp8_groups(D), M), dtype=torch.float32, device=self.device)
         else:
             self.y = torch.empty(self.shape, dtype=_DTYPES[out], device=self.device)
-        self._r, self._y = ssd_rows(self.r.data_ptr(), D), ssd_rows(self.y.data_ptr(), self.y.stride(0))
+        self._like = self.dtype, torch.Size(self.shape), _index(self.device)
+        self._weights = torch.float32, torch.Size((D,)), self._like[2]
+        self._rest = (struct.unpack("I", struct.pack("f", self.eps))[0], M, D, self.type, self.r.data_ptr(), D,
+                      self.out_type, self.y.data_ptr(), self.y.stride(0),
+                      0 if self.scale is None else self.scale.data_ptr(), self.rstd.data_ptr())
+        self._result = (self.r, self.y) if self.scale is None else (self.r, self.y, self.scale)
+        self._call = _Call("ssd_residual_norm_fwd", 3, 16, self._like[2])
 
     def __call__(self, x, residual=None, w=None, stream=None):
-        M, D = self.shape
-        a = self.shape, self.dtype, self.device
-        rc = load().ssd_residual_norm_fwd(
-            _rows("x", x, *a), _rows("residual", residual, *a), _dense("w", w, (D,), torch.float32, self.device),
-            self.eps, M, D, self.type, self._r, self.out_type, self._y,
-            None if self.scale is None else self.scale.data_ptr(), self.rstd.data_ptr(), _stream(stream, self.device))
-        if rc:
-            _raise(rc, "ssd_residual_norm_fwd")
-        return (self.r, self.y) if self.scale is None else (self.r, self.y, self.scale)
+        like = self._like
+        self._call(stream, *_rows("x", x, like), *_rows("residual", residual, like), _dense("w", w, self._weights),
+                   *self._rest)
+        return self._result
 
 
 class ResidualNormBackward:
@@ -356,17 +381,15 @@ class ResidualNormBackward:
         self.dx = torch.empty(self.shape, dtype=self.dtype, device=self.device)
         self.dw = torch.empty(D, dtype=torch.float32, device=self.device)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        self._dx = ssd_rows(self.dx.data_ptr(), D)
+        self._like = self.dtype, torch.Size(self.shape), _index(self.device)
+        self._weights, self._rstd = (torch.float32, torch.Size((D,)), self._like[2]), (torch.float32, torch.Size((M,)), self._like[2])
+        self._rest = (M, D, self.type, self.dx.data_ptr(), D, self.dw.data_ptr(), self.workspace.data_ptr(), nbytes)
+        self._call = _Call("ssd_residual_norm_bwd", 4, 16, self._like[2])
 
     def __call__(self, dy, r, w, rstd, dr=None, stream=None):
-        M, D = self.shape
-        a, f32 = (self.shape, self.dtype, self.device), torch.float32
-        rc = load().ssd_residual_norm_bwd(
-            _rows("dy", dy, *a), _rows("dr", dr, *a), _rows("r", r, *a), _dense("w", w, (D,), f32, self.device),
-            _dense("rstd", rstd, (M,), f32, self.device), M, D, self.type, self._dx, self.dw.data_ptr(),
-            self.workspace.data_ptr(), self.workspace.numel(), _stream(stream, self.device))
-        if rc:
-            _raise(rc, "ssd_residual_norm_bwd")
+        like = self._like
+        self._call(stream, *_rows("dy", dy, like), *_rows("dr", dr, like), *_rows("r", r, like),
+                   _dense("w", w, self._weights), _dense("rstd", rstd, self._rstd), *self._rest)
         return self.dx, self.dw
 
 
@@ -399,17 +422,16 @@ class Fp8Quantize:
         if transposed:
             self.qt = fp8_empty(K, M, self.device)
             self.scale_t = torch.empty((KB, MB) if self.scales else (MB, K), **f32)
-        rows = lambda t: _NO_ROWS if t is None else ssd_rows(t.data_ptr(), t.stride(0))
-        ptr = lambda t: None if t is None else t.data_ptr()
-        self._out = rows(self.q), ptr(self.scale), rows(self.qt), ptr(self.scale_t)
+        self._like = self.dtype, torch.Size(self.shape), _index(self.device)
+        rows = lambda t: (0, 0) if t is None else (t.data_ptr(), t.stride(0))
+        ptr = lambda t: 0 if t is None else t.data_ptr()
+        self._rest = (M, K, self.type, self.scales, *rows(self.q), ptr(self.scale), *rows(self.qt), ptr(self.scale_t))
+        self._result = tuple(t for t in (self.q, self.scale, self.qt, self.scale_t) if t is not None)
+        self._call = _Call("ssd_fp8_quantize", 5, 12, self._like[2])
 
     def __call__(self, x, stream=None):
-        M, K = self.shape
-        rc = load().ssd_fp8_quantize(_rows("x", x, self.shape, self.dtype, self.device), M, K, self.type, self.scales,
-                                     *self._out, _stream(stream, self.device))
-        if rc:
-            _raise(rc, "ssd_fp8_quantize")
-        return tuple(t for t in (self.q, self.scale, self.qt, self.scale_t) if t is not None)
+        self._call(stream, *_rows("x", x, self._like), *self._rest)
+        return self._result
 
 
 class Fp8Product:
@@ -436,16 +458,16 @@ class Fp8Product:
         per = 8 if out == "bf16" else 4
         self.c = torch.empty((M, -(-N // per) * per), dtype=_DTYPES[out], device=self.device)[:, :N]
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-        self._c, self._ws = ssd_rows(self.c.data_ptr(), self.c.stride(0)), self.workspace.data_ptr()
+        index, f8, f32 = _index(self.device), torch.float8_e4m3fn, torch.float32
+        size = torch.Size
+        self._a, self._b = (f8, size(self.a_shape), index), (f8, size(self.b_shape), index)
+        self._a_scale, self._b_scale = (f32, size(self.a_scale_shape), index), (f32, size(self.b_scale_shape), index)
+        self._rest = (self.b_scales, M, N, K, self.type, self.c.data_ptr(), self.c.stride(0), self.workspace.data_ptr(), nbytes)
+        self._call = _Call("ssd_fp8_matmul", 6, 15, index)
 
     def __call__(self, a, a_scale, b, b_scale, stream=None):
-        d, f8, f32 = self.device, torch.float8_e4m3fn, torch.float32
-        rc = load().ssd_fp8_matmul(
-            _rows("a", a, self.a_shape, f8, d), _dense("a_scale", a_scale, self.a_scale_shape, f32, d),
-            _rows("b", b, self.b_shape, f8, d), _dense("b_scale", b_scale, self.b_scale_shape, f32, d),
-            self.b_scales, *self.sizes, self.type, self._c, self._ws, self.workspace.numel(), _stream(stream, d))
-        if rc:
-            _raise(rc, "ssd_fp8_matmul")
+        self._call(stream, *_rows("a", a, self._a), _dense("a_scale", a_scale, self._a_scale), *_rows("b", b, self._b),
+                   _dense("b_scale", b_scale, self._b_scale), *self._rest)
         return self.c
 
     def status(self, stream=None) -> int:

@@ -2,6 +2,7 @@
 // launch sequence per call on the caller's stream. Nothing is allocated.
 #include <atomic>
 #include <cstdint>
+#include <cstring>
 #include <initializer_list>
 
 #include <cuda_runtime.h>
@@ -15,7 +16,7 @@ using namespace ssdc::block;
 
 constexpr int64_t kBig = int64_t(1) << 40;  // most elements of one array
 constexpr int kMaxDevices = 64;
-std::atomic<int> g_device_ok[kMaxDevices];
+std::atomic<int> g_device_ok[kMaxDevices];  // an sm_103 device's SMs
 
 int check_device() {
     int dev = 0;
@@ -26,7 +27,9 @@ int check_device() {
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
         return SSDC_ERR_CUDA;
     if (major != 10 || minor != 3) return SSDC_ERR_DEVICE;
-    g_device_ok[dev].store(1, std::memory_order_release);
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2) return SSDC_ERR_CUDA;
+    g_device_ok[dev].store(sms, std::memory_order_release);
     return SSDC_OK;
 }
 
@@ -181,6 +184,12 @@ int check_fp8_rows(const void* p, int64_t ld, int64_t cols) {
 }
 
 }  // namespace
+
+int ssdc::block::device_sms() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    return g_device_ok[dev].load(std::memory_order_acquire);
+}
 
 extern "C" {
 
@@ -398,6 +407,97 @@ int ssd_fp8_matmul(ssd_rows_in a8, const float* a_scale, ssd_rows_in b8, const f
     p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
     (void)cudaGetLastError();
     return done(matmul_launch(p, stream));
+}
+
+int ssd_block_call(int32_t call, const int64_t* words, cudaStream_t stream) {
+    if (words == nullptr) return SSDC_ERR_INVALID;
+    const int64_t* w = words;
+    auto ptr = [&] { return reinterpret_cast<void*>(*w++); };
+    auto f32 = [&] { return static_cast<float*>(ptr()); };
+    auto i64 = [&] { return *w++; };
+    auto i32 = [&] { return (int32_t)*w++; };
+    auto seq_in = [&] { ssd_seq_in a; a.p = ptr(); a.stride_b = i64(); a.stride_t = i64(); return a; };
+    auto seq_out = [&] { ssd_seq_out a; a.p = ptr(); a.stride_b = i64(); a.stride_t = i64(); return a; };
+    auto rows_in = [&] { ssd_rows_in a; a.p = ptr(); a.ld = i64(); return a; };
+    auto rows_out = [&] { ssd_rows_out a; a.p = ptr(); a.ld = i64(); return a; };
+    auto dims = [&] { ssd_gated_dims d; d.B = i64(); d.T = i64(); d.D = i64(); d.type = i32(); return d; };
+    switch (call) {
+        case SSD_CALL_GATED_SCAN_FWD: {
+            const ssd_seq_in x = seq_in(), f = seq_in(), i = seq_in();
+            const float* h0 = f32();
+            const uint8_t* reset = static_cast<const uint8_t*>(ptr());
+            const ssd_gated_dims d = dims();
+            const ssd_seq_out h = seq_out();
+            float *h_last = f32(), *states = f32();
+            return ssd_gated_scan_fwd(x, f, i, h0, reset, d, h, h_last, states, static_cast<int32_t*>(ptr()), stream);
+        }
+        case SSD_CALL_GATED_SCAN_STEP: {
+            const ssd_seq_in x = seq_in(), f = seq_in(), i = seq_in();
+            const float* state = f32();
+            const int64_t B = i64(), D = i64();
+            const int32_t type = i32();
+            const ssd_seq_out h = seq_out();
+            return ssd_gated_scan_step(x, f, i, state, B, D, type, h, f32(), stream);
+        }
+        case SSD_CALL_GATED_SCAN_BWD: {
+            const ssd_seq_in x = seq_in(), f = seq_in(), i = seq_in();
+            const float* states = f32();
+            const uint8_t* reset = static_cast<const uint8_t*>(ptr());
+            const ssd_seq_in dh = seq_in();
+            const float* dh_last = f32();
+            const ssd_gated_dims d = dims();
+            const ssd_seq_out dx = seq_out(), df = seq_out(), di = seq_out();
+            float* dh0 = f32();
+            return ssd_gated_scan_bwd(x, f, i, states, reset, dh, dh_last, d, dx, df, di, dh0, static_cast<int32_t*>(ptr()),
+                                      stream);
+        }
+        case SSD_CALL_RESIDUAL_NORM_FWD: {
+            const ssd_rows_in x = rows_in(), res = rows_in();
+            const float* weights = f32();
+            const uint32_t bits = (uint32_t)i64();
+            float eps;
+            std::memcpy(&eps, &bits, sizeof eps);
+            const int64_t M = i64(), D = i64();
+            const int32_t type = i32();
+            const ssd_rows_out r = rows_out();
+            const int32_t out_type = i32();
+            const ssd_rows_out y = rows_out();
+            float* scale = f32();
+            return ssd_residual_norm_fwd(x, res, weights, eps, M, D, type, r, out_type, y, scale, f32(), stream);
+        }
+        case SSD_CALL_RESIDUAL_NORM_BWD: {
+            const ssd_rows_in dy = rows_in(), dr = rows_in(), r = rows_in();
+            const float *weights = f32(), *rstd = f32();
+            const int64_t M = i64(), D = i64();
+            const int32_t type = i32();
+            const ssd_rows_out dx = rows_out();
+            float* dw = f32();
+            void* ws = ptr();
+            return ssd_residual_norm_bwd(dy, dr, r, weights, rstd, M, D, type, dx, dw, ws, (size_t)i64(), stream);
+        }
+        case SSD_CALL_FP8_QUANTIZE: {
+            const ssd_rows_in x = rows_in();
+            const int64_t M = i64(), K = i64();
+            const int32_t type = i32(), scales = i32();
+            const ssd_rows_out q = rows_out();
+            float* scale = f32();
+            const ssd_rows_out qt = rows_out();
+            return ssd_fp8_quantize(x, M, K, type, scales, q, scale, qt, f32(), stream);
+        }
+        case SSD_CALL_FP8_MATMUL: {
+            const ssd_rows_in a = rows_in();
+            const float* a_scale = f32();
+            const ssd_rows_in b = rows_in();
+            const float* b_scale = f32();
+            const int32_t b_scales = i32();
+            const int64_t M = i64(), N = i64(), K = i64();
+            const int32_t out_type = i32();
+            const ssd_rows_out c = rows_out();
+            void* ws = ptr();
+            return ssd_fp8_matmul(a, a_scale, b, b_scale, b_scales, M, N, K, out_type, c, ws, (size_t)i64(), stream);
+        }
+        default: return SSDC_ERR_INVALID;
+    }
 }
 
 }  // extern "C"

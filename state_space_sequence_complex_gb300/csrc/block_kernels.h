@@ -2,6 +2,7 @@
 // operators around the scan: gated scan, residual norm, 8-bit quantiser and product.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -10,6 +11,22 @@
 
 namespace ssdc {
 namespace block {
+
+// A kernel's dynamic shared memory, allowed once on each device.
+template <typename K>
+inline cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+// The current device's SMs, asked once (0: an error).
+int device_sms();
 
 // One gated-scan call. Strides in elements; reset, h0, h_last, states may be null.
 struct Gated {

@@ -393,14 +393,6 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     if (warp == 1) ptx::tmem_dealloc_pair(tmem, 512);
 }
 
-int device_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms;
-}
-
 template <int BN, bool kBlocks, typename T>
 int launch_pair(const Matmul& p, Product q, int sms, cudaStream_t stream) {
     using S = Shape<BN>;
@@ -417,8 +409,8 @@ int launch_pair(const Matmul& p, Product q, int sms, cudaStream_t stream) {
     if (tiles * q.KB > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
     const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
     auto* k = product_pair<BN, kBlocks, T>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes) != cudaSuccess)
-        return SSDC_ERR_CUDA;
+    static std::atomic<uint64_t> allowed;
+    if (allow_smem(k, (int)S::kBytes, allowed) != cudaSuccess) return SSDC_ERR_CUDA;
     k<<<2 * pairs, S::kThreads, S::kBytes, stream>>>(ma, mb, mc, q);
     return 1;
 }

@@ -515,13 +515,13 @@ bool make_map(CUtensorMap* m, const void* q, int64_t sb, int64_t st, const Gated
     return tc::encode_rows_3d(m, q, (int)e, p.D, p.T, p.B, st * e, sb * e, rows);
 }
 
-template <typename K, typename M>
-int launch(K kernel, const M& maps, const Gated& p, int warps, int tile, uint32_t smem, cudaStream_t stream) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return SSDC_ERR_CUDA;
+template <auto kKernel, typename M>
+int launch(const M& maps, const Gated& p, int warps, int tile, uint32_t smem, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed;
+    if (allow_smem(kKernel, (int)smem, allowed) != cudaSuccess) return SSDC_ERR_CUDA;
     const int per = p.bf16 ? 64 : 32;
     const int64_t groups = (int64_t)p.B * ((p.D + per - 1) / per);
-    return launch_clusters(kernel, groups, cluster_size((p.T + tile - 1) / tile, groups, 152), 32 * warps, smem, stream, maps, p);
+    return launch_clusters(kKernel, groups, cluster_size((p.T + tile - 1) / tile, groups, 152), 32 * warps, smem, stream, maps, p);
 }
 
 // Fewer tokens than this are one tile of the other kernels, which start sooner.
@@ -530,14 +530,14 @@ constexpr int64_t kMinTokens = 65;
 template <typename T, bool kGate>
 int fwd(const FwdMaps& m, const Gated& p, cudaStream_t stream) {
     constexpr uint32_t smem = smem_bytes<kFwdWarps, kFwdTok, kGate ? 3 : 2>();
-    return p.reset ? launch(gated_fwd_tma<T, kGate, true>, m, p, kFwdWarps, kFwdWarps * kFwdTok, smem, stream)
-                   : launch(gated_fwd_tma<T, kGate, false>, m, p, kFwdWarps, kFwdWarps * kFwdTok, smem, stream);
+    return p.reset ? launch<gated_fwd_tma<T, kGate, true>>(m, p, kFwdWarps, kFwdWarps * kFwdTok, smem, stream)
+                   : launch<gated_fwd_tma<T, kGate, false>>(m, p, kFwdWarps, kFwdWarps * kFwdTok, smem, stream);
 }
 template <typename T, bool kGate>
 int bwd(const BwdMaps& m, const Gated& p, cudaStream_t stream) {
     constexpr uint32_t smem = smem_bytes<bwd_warps<T>(), bwd_tok<T>(), kGate ? 4 : 3>();
-    return p.reset ? launch(gated_bwd_tma<T, kGate, true>, m, p, bwd_warps<T>(), 64, smem, stream)
-                   : launch(gated_bwd_tma<T, kGate, false>, m, p, bwd_warps<T>(), 64, smem, stream);
+    return p.reset ? launch<gated_bwd_tma<T, kGate, true>>(m, p, bwd_warps<T>(), 64, smem, stream)
+                   : launch<gated_bwd_tma<T, kGate, false>>(m, p, bwd_warps<T>(), 64, smem, stream);
 }
 
 }  // namespace
