@@ -25,6 +25,27 @@ inline cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) 
     return e;
 }
 
+// A kernel on `groups` clusters of R CTAs of so many threads, as a programmatic dependent.
+template <typename... KArgs, typename... Args>
+inline int launch_clusters(void (*kernel)(KArgs...), int64_t groups, int R, int threads, size_t smem, cudaStream_t stream,
+                           const Args&... args) {
+    if (groups * R > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(groups * R));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = R;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 1 : SSDC_ERR_CUDA;
+}
+
 // The current device's SMs, asked once (0: an error).
 int device_sms();
 
@@ -112,6 +133,9 @@ struct Matmul {
 };
 size_t matmul_workspace(int64_t M, int64_t N, int64_t K);
 int matmul_launch(const Matmul& p, cudaStream_t stream);
+// The same for few rows of A (block_matmul_few.cu), and whether it is taken.
+bool matmul_is_few(int64_t M, int64_t N, int64_t K);
+int matmul_few_launch(const Matmul& p, cudaStream_t stream);
 
 }  // namespace block
 }  // namespace ssdc

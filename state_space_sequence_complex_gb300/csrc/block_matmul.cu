@@ -155,7 +155,7 @@ __device__ __forceinline__ void store_piece(const Product& p, const CUtensorMap*
 }
 
 template <int BN, bool kBlocks, typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<BN>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<BN>::kThreads, 1)
 product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
              const __grid_constant__ CUtensorMap map_c, const Product p) {
     using S = Shape<BN>;
@@ -189,6 +189,8 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     __syncthreads();
     ptx::cluster_sync();  // the peer's barriers are initialised
     ptx::tc_fence_after();
+    launch_dependents();
+    grid_dependency_wait();
     const uint32_t tmem = tmem_slot;
     char* out = smem + S::kStages * S::kStage;
     float* scales = reinterpret_cast<float*>(out + S::kAddWarps * S::kOut);
@@ -411,8 +413,7 @@ int launch_pair(const Matmul& p, Product q, int sms, cudaStream_t stream) {
     auto* k = product_pair<BN, kBlocks, T>;
     static std::atomic<uint64_t> allowed;
     if (allow_smem(k, (int)S::kBytes, allowed) != cudaSuccess) return SSDC_ERR_CUDA;
-    k<<<2 * pairs, S::kThreads, S::kBytes, stream>>>(ma, mb, mc, q);
-    return 1;
+    return launch_clusters(k, pairs, 2, S::kThreads, S::kBytes, stream, ma, mb, mc, q);
 }
 
 template <int BN>
@@ -431,6 +432,7 @@ size_t matmul_workspace(int64_t, int64_t, int64_t) { return 256; }
 int matmul_launch(const Matmul& p, cudaStream_t stream) {
     const int sms = device_sms();
     if (sms < 2) return SSDC_ERR_CUDA;
+    if (matmul_is_few(p.M, p.N, p.K)) return matmul_few_launch(p, stream);
     Product q = {};
     q.a_scale = p.a_scale; q.b_scale = p.b_scale;
     q.M = p.M; q.N = p.N; q.c_ld = p.c_ld;

@@ -118,6 +118,8 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
     using L = Layout<T, kAligned, kVals>;
     constexpr int kWarps = cta_warps<kRowWarps>(), kRun = L::kRun, kWarpSpan = L::kWarpSpan;
     __shared__ float part[1][32];
+    launch_dependents();
+    grid_dependency_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t m = (int64_t)blockIdx.x * (kWarps / kRowWarps) + warp / kRowWarps;
     const int base = warp % kRowWarps * kWarpSpan;
@@ -210,6 +212,8 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
     __shared__ float join[kRows > 1 ? kWarps - kRowWarps : 1][kRows > 1 ? kWarpSpan / 4 : 1];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int base = warp % kRowWarps * kWarpSpan;
+    launch_dependents();
+    grid_dependency_wait();
     float dw[kVals];
 #pragma unroll
     for (int i = 0; i < kVals; ++i) dw[i] = 0.0f;
@@ -375,8 +379,8 @@ struct Fwd {
     template <int kVals, int W, bool kAligned>
     void run() const {
         constexpr int rows = cta_warps<W>() / W;
-        norm_fwd<T, TO, kFp8, kVals, W, kAligned>
-            <<<(unsigned)((p.M + rows - 1) / rows), 32 * cta_warps<W>(), 0, stream>>>(p);
+        launch_dependent(norm_fwd<T, TO, kFp8, kVals, W, kAligned>, dim3((unsigned)((p.M + rows - 1) / rows)),
+                         dim3(32 * cta_warps<W>()), 0, stream, p);
     }
 };
 template <typename T>
@@ -392,7 +396,7 @@ struct Bwd {
     cudaStream_t stream;
     template <int kVals, int W, bool kAligned>
     void run() const {
-        norm_bwd<T, kVals, W, kAligned><<<ctas, 32 * cta_warps<W>(), 0, stream>>>(p);
+        launch_dependent(norm_bwd<T, kVals, W, kAligned>, dim3(ctas), dim3(32 * cta_warps<W>()), 0, stream, p);
     }
 };
 

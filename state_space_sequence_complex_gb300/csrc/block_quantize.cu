@@ -12,6 +12,7 @@
 #include "block_common.cuh"
 #include "block_kernels.h"
 #include "ptx.cuh"
+#include "ssdc_kernels.h"
 
 namespace ssdc {
 namespace block {
@@ -26,6 +27,8 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
     __shared__ __align__(16) uint8_t tile[kTile][kTile];
     __shared__ float col_max[kThreads / kLanes][kTile];
     __shared__ Scale col_scale[kTile];
+    launch_dependents();
+    grid_dependency_wait();
     const int t = threadIdx.x, lane = t % kLanes, strip = t / kLanes;  // columns kCols lane .., rows kRows strip ..
     const int64_t tiles_k = (p.K + kTile - 1) / kTile, tiles_m = (p.M + kTile - 1) / kTile;
     const int64_t tk = blockIdx.x % tiles_k, tm = blockIdx.x / tiles_k;
@@ -165,8 +168,7 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
 
 template <typename T, bool kBlocks>
 void launch(const Quant& p, bool aligned, unsigned grid, cudaStream_t stream) {
-    if (aligned) quantize<T, kBlocks, true><<<grid, kThreads, 0, stream>>>(p);
-    else quantize<T, kBlocks, false><<<grid, kThreads, 0, stream>>>(p);
+    launch_dependent(aligned ? quantize<T, kBlocks, true> : quantize<T, kBlocks, false>, dim3(grid), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace

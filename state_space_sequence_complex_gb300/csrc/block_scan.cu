@@ -104,6 +104,8 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
     const uint32_t dl = in_d ? d : p.D - kVec;
     const uint8_t* reset = kReset ? p.reset + (int64_t)b * p.T : nullptr;
 
+    launch_dependents();
+    grid_dependency_wait();
     float carry[kVec];
 #pragma unroll
     for (int c = 0; c < kVec; ++c) carry[c] = p.h0 && in_d ? p.h0[(int64_t)b * p.D + d + c] : 0.0f;
@@ -290,6 +292,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
     const T* fetch_at = (fetch == 0 ? x : fetch == 1 ? f : fetch == 2 ? dh : kGate ? g : x) + d0;
     const int64_t fetch_t = fetch == 0 ? p.x_t : fetch == 1 ? p.f_t : fetch == 2 ? p.dh_t : kGate ? p.i_t : p.x_t;
 
+    launch_dependents();
+    grid_dependency_wait();
     float carry[kVec];
 #pragma unroll
     for (int c = 0; c < kVec; ++c) carry[c] = p.dh_last && in_d ? p.dh_last[(int64_t)b * p.D + d + c] : 0.0f;
@@ -478,6 +482,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
 // One token: a thread a channel pair (or channel). Bound by the launch.
 template <typename T, int kVec, bool kGate>
 __global__ void __launch_bounds__(128) gated_step(const Gated p) {
+    launch_dependents();
+    grid_dependency_wait();
     const int64_t per = (p.D + kVec - 1) / kVec, i = (int64_t)blockIdx.x * 128 + threadIdx.x;
     if (i >= p.B * per) return;
     const int64_t b = i / per, d = (i - b * per) * kVec;
@@ -516,8 +522,9 @@ int launch(const Gated& p, int what, cudaStream_t stream) {
     if (what == 1 && p.reset) return launch_cluster(gated_bwd<T, kVec, kGate, true>, p, kVec, stream);
     if (what == 1) return launch_cluster(gated_bwd<T, kVec, kGate, false>, p, kVec, stream);
     const int64_t n = (int64_t)p.B * ((p.D + kVec - 1) / kVec);
-    gated_step<T, kVec, kGate><<<(unsigned)((n + 127) / 128), 128, 0, stream>>>(p);
-    return 1;
+    return launch_dependent(gated_step<T, kVec, kGate>, dim3((unsigned)((n + 127) / 128)), dim3(128), 0, stream, p) == cudaSuccess
+               ? 1
+               : SSDC_ERR_CUDA;
 }
 
 template <typename T>

@@ -122,25 +122,6 @@ inline int cluster_size(int64_t tiles, int64_t groups, int ctas) {
     return R;
 }
 
-// A kernel on `groups` clusters of R CTAs of so many threads.
-template <typename... KArgs, typename... Args>
-inline int launch_clusters(void (*kernel)(KArgs...), int64_t groups, int R, int threads, size_t smem, cudaStream_t stream,
-                           const Args&... args) {
-    if (groups * R > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(groups * R));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = R;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 1 : SSDC_ERR_CUDA;
-}
-
 // The forward and backward passes by TMA copies (block_scan_tma.cu): the launches, or 0 where
 // the arrays or sizes do not allow it.
 int tma_fwd_launch(const Gated& p, cudaStream_t stream);

@@ -102,6 +102,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
     const int64_t state_at = (int64_t)b * p.D + d, state_rows = (p.T + SSD_GATED_STATE_TOKENS - 1) / SSD_GATED_STATE_TOKENS;
     const uint8_t* reset = kReset ? p.reset + (int64_t)b * p.T : nullptr;
 
+    launch_dependents();
+    grid_dependency_wait();
     float carry[kVec];
 #pragma unroll
     for (int c = 0; c < kVec; ++c) carry[c] = p.h0 && in_d ? p.h0[state_at + c] : 0.0f;
@@ -292,6 +294,8 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
     const int64_t state_at = (int64_t)b * p.D + d;
     const uint8_t* reset = kReset ? p.reset + (int64_t)b * p.T : nullptr;
 
+    launch_dependents();
+    grid_dependency_wait();
     float carry[kVec];
 #pragma unroll
     for (int c = 0; c < kVec; ++c) carry[c] = p.dh_last && in_d ? p.dh_last[state_at + c] : 0.0f;

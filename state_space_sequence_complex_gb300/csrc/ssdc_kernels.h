@@ -174,6 +174,11 @@ int fused2_launch(const Problem& p, const Workspace& ws, cudaStream_t stream, bo
 // Launched the ordinary way, the wait returns at once.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The other side: lets the next kernel of the stream, if it is launched this way, be scheduled once
+// every CTA of this one has come here. It still waits for this kernel's end in its own
+// grid_dependency_wait().
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                                     cudaStream_t stream, Args... args) {
