@@ -179,12 +179,14 @@ int ssd_fp8_quantize(ssd_rows_in x, int64_t M, int64_t K, int32_t type, int32_t 
  *   a, a_scale   (M, K), SSD_SCALE_ROWS
  *   b, b_scale   (N, K), b_scales = SSD_SCALE_BLOCKS (weights) or SSD_SCALE_ROWS
  *   c            output rows of `out_type` (F32 or BF16), ld elements apart
- *   workspace    ssd_fp8_matmul_workspace_bytes() bytes, 256-byte aligned. Its
- *                first word is a status that a wait that gave up sets
- *                (ssd_complex_status() reads it); the caller zeroes that word
- *                once, before the first call
+ *   workspace    ssd_fp8_matmul_workspace_bytes() bytes, 256-byte aligned, for one
+ *                call at a time. Its first word is a status that a wait that gave
+ *                up sets (ssd_complex_status() reads it). The caller zeroes its
+ *                first SSD_FP8_MATMUL_ZEROED bytes, or all of it if it has fewer,
+ *                once, before the first call, and again after such a status
  * a.p and b.p are 16-byte aligned.
  */
+#define SSD_FP8_MATMUL_ZEROED 16384
 size_t ssd_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
 int ssd_fp8_matmul(ssd_rows_in a, const float *a_scale, ssd_rows_in b, const float *b_scale, int32_t b_scales,
                    int64_t M, int64_t N, int64_t K, int32_t out_type, ssd_rows_out c, void *workspace,

@@ -26,9 +26,10 @@ inline cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) 
 }
 
 // A kernel on `groups` clusters of R CTAs of so many threads, as a programmatic dependent.
+// `together`: all of them at the same time or not at all (they wait for one another).
 template <typename... KArgs, typename... Args>
-inline int launch_clusters(void (*kernel)(KArgs...), int64_t groups, int R, int threads, size_t smem, cudaStream_t stream,
-                           const Args&... args) {
+inline int launch_clusters(void (*kernel)(KArgs...), int64_t groups, int R, bool together, int threads, size_t smem,
+                           cudaStream_t stream, const Args&... args) {
     if (groups * R > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(groups * R));
@@ -39,8 +40,13 @@ inline int launch_clusters(void (*kernel)(KArgs...), int64_t groups, int R, int 
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = R;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    if (together) {
+        attr[1].id = cudaLaunchAttributeCooperative;
+        attr[1].val.cooperative = 1;
+    } else {
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 1 : SSDC_ERR_CUDA;

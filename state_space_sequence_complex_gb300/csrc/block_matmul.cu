@@ -37,6 +37,45 @@ struct Product {
     void* c;
     bool tma_out;  // c's rows start at multiples of 16 bytes: stored by TMA
     int* status;
+    int whole;       // tiles that pairs take whole, in turn; the others' groups are dealt out evenly
+    int* flags;      // a pair's warps' marks that their sums of a tile's end are in `sums`
+    float4* sums;
+};
+
+constexpr int kFlags = 16;  // of a pair: 8 adding warps of two CTAs
+
+// What a pair works on, one piece after another: groups g0 .. g1 of a tile. First the tiles that
+// it takes whole. Then its even share of the other tiles' groups, which may begin inside a
+// tile and end inside one. A tile's first part is always some pair's last piece and its later
+// parts are other pairs' first pieces: the one with the first part waits for the others'
+// sums, adds them in the order of K and stores the tile.
+struct Walk {
+    const Product& p;
+    int pair, pairs, tile;
+    int64_t at, end;
+    __device__ __forceinline__ Walk(const Product& q, int pr, int prs) : p(q), pair(pr), pairs(prs), tile(pr), at(first(pr)), end(first(pr + 1)) {}
+    __device__ __forceinline__ int64_t first(int pr) const {
+        return (int64_t)(p.m_tiles * p.n_tiles - p.whole) * p.KB * pr / pairs;
+    }
+    __device__ __forceinline__ uint32_t groups() const {
+        return (uint32_t)((tile < p.whole ? (p.whole - tile + pairs - 1) / pairs : 0) * p.KB + (int)(end - at));
+    }
+    __device__ __forceinline__ bool next(int& idx, int& g0, int& g1) {
+        if (tile < p.whole) {
+            idx = tile;
+            g0 = 0;
+            g1 = p.KB;
+            tile += pairs;
+            return true;
+        }
+        if (at >= end) return false;
+        const int t = (int)(at / p.KB);
+        idx = p.whole + t;
+        g0 = (int)(at - (int64_t)t * p.KB);
+        g1 = (int)min((int64_t)p.KB, g0 + (end - at));
+        at += g1 - g0;
+        return true;
+    }
 };
 
 // Tiles are walked in bands of 8 row tiles, so that the pairs at work at one time share
@@ -166,7 +205,8 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     __shared__ uint32_t tmem_slot;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank();
-    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2, tiles = p.m_tiles * p.n_tiles;
+    Walk walk(p, blockIdx.x / 2, gridDim.x / 2);
+    const uint32_t total = walk.groups();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
@@ -200,10 +240,11 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         ptx::regs_dec<S::kCtlRegs>();
         if (warp == 0 && lane == 0) {
             uint32_t it = 0;
-            for (int idx = pair; idx < tiles && ok; idx += pairs) {
+            int idx, g0, g1;
+            while (ok && walk.next(idx, g0, g1)) {
                 int mt, nt;
                 tile_at(p, idx, mt, nt);
-                for (int g = 0; g < p.KB; ++g, ++it) {
+                for (int g = g0; g < g1; ++g, ++it) {
                     const uint32_t s = it % S::kStages;
                     ok = ptx::mbar_wait(&empty[s], ((it / S::kStages) & 1) ^ 1, kWaitNs);
                     if (!ok) break;
@@ -223,7 +264,6 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             // two issuers, each of every other group
             constexpr uint32_t idesc = ptx::idesc_e4m3(256, BN);
             const uint64_t base = ptx::smem_desc_sw128(ptx::smem_addr(smem), 16, 1024);
-            const uint32_t total = (uint32_t)((tiles - pair + pairs - 1) / pairs) * p.KB;
             uint32_t s = warp - 1, s_phase = 0;
             for (uint32_t it = warp - 1; it < total; it += 2) {
                 const uint32_t b = it % kBufs, b_phase = it / kBufs & 1 ^ 1, d = tmem + b * BN;
@@ -251,17 +291,17 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             // earlier ones: of a ring of more than 2 kBufs slots the oldest is free.
             constexpr int kB = kBlocks ? BN / 128 : BN / 32;  // scales of B a lane holds
             const float *sa_at = nullptr, *sb_at = nullptr;
-            int rows_in = 0, cols_in = 0, idx = pair, g = 0;  // the group to load next
+            int rows_in = 0, cols_in = 0, g = 0, g_end = 0;  // the group to load next, of a piece that ends before g_end
             float sa[2][4], sb[2][kB];
             auto load = [&](float (&a)[4], float (&c)[kB]) {
-                if (idx >= tiles) return;
-                if (g == 0) {
-                    int mt, nt;
+                if (g == g_end) {
+                    int idx, mt, nt;
+                    if (!walk.next(idx, g, g_end)) return;
                     tile_at(p, idx, mt, nt);
                     const int64_t m = min((int64_t)mt * 256 + rank * 128, p.M - 1), n = (int64_t)nt * BN;
-                    sa_at = p.a_scale + m;
+                    sa_at = p.a_scale + g * p.M + m;
                     rows_in = (int)min((int64_t)128, p.M - m) - 1;
-                    sb_at = kBlocks ? p.b_scale + n / kGroup * p.KB : p.b_scale + n;
+                    sb_at = kBlocks ? p.b_scale + n / kGroup * p.KB + g : p.b_scale + g * p.N + n;
                     cols_in = (int)min((int64_t)BN, p.N - n) - 1;
                 }
                 // rows and columns outside C take the last one's
@@ -272,14 +312,10 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     c[i] = __ldg(sb_at + (kBlocks ? min(i, cols_in / kGroup) * p.KB : min(lane + 32 * i, cols_in)));
                 sa_at += p.M;
                 sb_at += kBlocks ? 1 : p.N;
-                if (++g == p.KB) {
-                    g = 0;
-                    idx += pairs;
-                }
+                ++g;
             };
             load(sa[0], sb[0]);
             load(sa[1], sb[1]);
-            const uint32_t total = (uint32_t)((tiles - pair + pairs - 1) / pairs) * p.KB;
             for (uint32_t it = 0; it < total && ok; it += 2) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -316,11 +352,23 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         // this lane's row's scale in a slot, and the warp's columns'
         const int row_at = 32 * quad + lane + (kBlocks ? part * kCols / kGroup * 128 : 0), col_at = 128 + part * kCols;
         const uint32_t tempty_at = ptx::mapa(ptx::smem_addr(&tempty[0]), 0);
-        // Pieces of 32 columns are read while the one before is added, and the first of a group
-        // while the last of the group before is: waits on shared-memory barriers take 200 cycles
-        // while operands stream through it, and must not stand between two pieces.
-        float v[2][32], s = 0.0f;
-        const uint32_t total = (uint32_t)((tiles - pair + pairs - 1) / pairs) * p.KB;
+        // Pieces of kP columns are read while the one before is added, and the first of a group
+        // while the last of the group before is: accesses to shared memory and its barriers take
+        // 200 cycles while operands stream through it, and must not stand between two pieces. With
+        // a scale for every column (as many loads of scales as of sums) the pieces are smaller,
+        // for the registers.
+        constexpr int kP = kBlocks ? 32 : 16, kPieces = kCols / kP;
+        float v[2][kP], s = 0.0f;
+        float4 w[2][kBlocks ? 1 : kP / 4];
+        auto read = [&](int j, uint32_t b, const float* slot) {  // piece j
+            if constexpr (kBlocks) {
+                ptx::tmem_ld32(taddr + b * BN + kP * j, v[j & 1]);
+            } else {
+                ptx::tmem_ld16(taddr + b * BN + kP * j, v[j & 1]);
+#pragma unroll
+                for (int e = 0; e < kP / 4; ++e) w[j & 1][e] = *reinterpret_cast<const float4*>(slot + col_at + kP * j + 4 * e);
+            }
+        };
         uint32_t it = 0;  // the group that begin() reads next
         bool ready = false;
         auto begin = [&]() {
@@ -328,12 +376,16 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             ok = __all_sync(0xffffffffu, ready || ptx::mbar_wait(&tfull[b], phase, kWaitNs));
             if (!ok) return;
             ptx::tc_fence_after();
-            ptx::tmem_ld32(taddr + b * BN, v[0]);
-            s = scales[it % S::kRing * S::kSlot + row_at];
+            const float* slot = scales + it % S::kRing * S::kSlot;
+            read(0, b, slot);
+            s = slot[row_at];
             ++it;
         };
         begin();
-        for (int idx = pair; idx < tiles && ok; idx += pairs) {
+        const int flag_at = (int)rank * 8 + warp - 4;  // this warp among its pair's, and its sums
+        const int64_t sums_at = (int64_t)flag_at * (kCols / 4) * 32 + lane, sums_pair = (int64_t)kFlags * (kCols / 4) * 32;
+        int idx, g0, g1;
+        while (ok && walk.next(idx, g0, g1)) {
             int mt, nt;
             tile_at(p, idx, mt, nt);
             const int64_t m0 = (int64_t)mt * 256 + rank * 128 + 32 * quad;
@@ -341,16 +393,16 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             float2 acc[kCols / 2];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
-            for (int g = 0; g < p.KB && ok; ++g) {
+            for (int g = g0; g < g1 && ok; ++g) {
                 const uint32_t b = (it - 1) % kBufs;
                 const float* slot = scales + (it - 1) % S::kRing * S::kSlot;
                 const float2 ss = make_float2(s, s);
 #pragma unroll
-                for (int j = 0; j < kCols / 32; ++j) {
+                for (int j = 0; j < kPieces; ++j) {
                     ptx::tmem_wait_ld();
-                    if (j == kCols / 32 - 2) ready = ptx::mbar_test_wait(&tfull[it % kBufs], it / kBufs & 1);
-                    if (j + 1 < kCols / 32) {
-                        ptx::tmem_ld32(taddr + b * BN + 32 * (j + 1), v[(j + 1) & 1]);
+                    if (j == kPieces - 2) ready = ptx::mbar_test_wait(&tfull[it % kBufs], it / kBufs & 1);
+                    if (j + 1 < kPieces) {
+                        read(j + 1, b, slot);
                     } else {  // read: the next product but kBufs - 1 may take its place
                         ptx::tc_fence_before();
                         __syncwarp();
@@ -359,18 +411,46 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     }
                     const float* u = v[j & 1];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        float2* to = acc + 16 * j + e / 2;
+                    for (int e = 0; e < kP; e += 4) {
+                        float2* to = acc + (kP * j + e) / 2;
                         float2 lo = make_float2(u[e], u[e + 1]), hi = make_float2(u[e + 2], u[e + 3]);
-                        if (!kBlocks) {
-                            const float4 w = *reinterpret_cast<const float4*>(slot + col_at + 32 * j + e);
-                            lo = ptx::mul2(lo, make_float2(w.x, w.y));
-                            hi = ptx::mul2(hi, make_float2(w.z, w.w));
+                        if constexpr (!kBlocks) {
+                            const float4 c = w[j & 1][e / 4];
+                            lo = ptx::mul2(lo, make_float2(c.x, c.y));
+                            hi = ptx::mul2(hi, make_float2(c.z, c.w));
                         }
                         to[0] = ptx::fma2(lo, ss, to[0]);
                         to[1] = ptx::fma2(hi, ss, to[1]);
                     }
                 }
+            }
+            if (!ok) break;
+            if (g0 > 0) {  // a later part of a tile: the sums for the pair that has the first
+                float4* to = p.sums + walk.pair * sums_pair + sums_at;
+#pragma unroll
+                for (int j = 0; j < kCols / 4; ++j)
+                    __stcg(to + j * 32, make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y));
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) ptx::st_release(p.flags + walk.pair * kFlags + flag_at, 1);
+                continue;
+            }
+            for (int q = walk.pair + 1; g1 < p.KB; ++q) {  // the first part: the others' sums
+                int* flag = p.flags + q * kFlags + flag_at;
+                ok = __all_sync(0xffffffffu, lane != 0 || ptx::wait_flag(flag, 1, kWaitNs));
+                if (!ok) break;
+                const float4* from = p.sums + q * sums_pair + sums_at;
+#pragma unroll
+                for (int j = 0; j < kCols / 4; ++j) {
+                    const float4 w = __ldcg(from + j * 32);
+                    acc[2 * j].x += w.x;
+                    acc[2 * j].y += w.y;
+                    acc[2 * j + 1].x += w.z;
+                    acc[2 * j + 1].y += w.w;
+                }
+                __syncwarp();
+                if (lane == 0) *flag = 0;  // for the next call
+                g1 += (int)min((int64_t)(p.KB - g1), walk.first(q + 1) - walk.first(q));
             }
             if (!ok) break;
             constexpr int kPiece = 128 / sizeof(T);
@@ -395,8 +475,41 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     if (warp == 1) ptx::tmem_dealloc_pair(tmem, 512);
 }
 
+// How a product is dealt out over the pairs of SMs.
+constexpr int kPairs = 76;
+struct Plan {
+    int width, pairs, whole;
+    int64_t tiles;
+    bool split;  // tiles are shared between pairs
+};
+
+// By estimated time, in a wide tile's group (0.41 us at M 9728 N 8192 K 8192; a narrow tile's takes
+// 0.6 of that): rounds of whole tiles, wide or narrow; or, wide, all full rounds but one of whole
+// tiles and the rest's groups dealt evenly, with 14 for the exchange of sums and 8 for each more
+// that a tile takes. M 5136 N 1024 K 4096 (84 wide tiles): 50 us narrow, 34 us dealt evenly.
+Plan plan_for(int64_t M, int64_t N, int64_t K, int64_t most, bool may_split = true) {
+    const int64_t KB = (K + kGroup - 1) / kGroup, mt = (M + 255) / 256;
+    const int64_t wide = mt * ((N + 255) / 256), narrow = mt * ((N + 127) / 128);
+    auto rounds = [&](int64_t tiles) { return (tiles + most - 1) / most; };
+    const double by_wide = (double)(rounds(wide) * KB), by_narrow = 0.6 * (double)(rounds(narrow) * KB);
+    Plan plan = by_narrow < by_wide ? Plan{128, (int)(narrow < most ? narrow : most), 0, narrow, false}
+                                    : Plan{256, (int)(wide < most ? wide : most), 0, wide, false};
+    plan.whole = (int)(plan.tiles < INT32_MAX ? plan.tiles : INT32_MAX);
+    if (!may_split || wide % most == 0 || wide * KB > INT32_MAX) return plan;
+    const int64_t before = wide < most ? 0 : wide / most - 1, rest = wide - before * most;
+    int64_t pairs = most;
+    if (wide < most) {
+        pairs = wide * KB / 8;  // 8 groups each at least
+        pairs = pairs < wide ? wide : pairs > most ? most : pairs;
+    }
+    const double share = (double)(rest * KB) / (double)pairs;
+    const double by_share = (double)(before * KB) + share + 14.0 + 8.0 * (share < (double)KB ? (double)KB / share - 1.0 : 0.0);
+    if (by_share < (by_narrow < by_wide ? by_narrow : by_wide)) return Plan{256, (int)pairs, (int)(before * most), wide, true};
+    return plan;
+}
+
 template <int BN, bool kBlocks, typename T>
-int launch_pair(const Matmul& p, Product q, int sms, cudaStream_t stream) {
+int launch_pair(const Matmul& p, Product q, const Plan& plan, cudaStream_t stream) {
     using S = Shape<BN>;
     CUtensorMap ma, mb, mc;
     if (!tc::encode_tiled_2d(&ma, p.a, 1, p.K, p.M, p.a_ld, 128) || !tc::encode_tiled_2d(&mb, p.b, 1, p.K, p.N, p.b_ld, BN / 2))
@@ -407,27 +520,33 @@ int launch_pair(const Matmul& p, Product q, int sms, cudaStream_t stream) {
         mc = ma;  // not used
     }
     q.n_tiles = (int)((p.N + BN - 1) / BN);
-    const int64_t tiles = (int64_t)q.m_tiles * q.n_tiles;
-    if (tiles * q.KB > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
-    const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
+    q.whole = plan.whole;
+    const int pairs = plan.pairs;
     auto* k = product_pair<BN, kBlocks, T>;
     static std::atomic<uint64_t> allowed;
     if (allow_smem(k, (int)S::kBytes, allowed) != cudaSuccess) return SSDC_ERR_CUDA;
-    return launch_clusters(k, pairs, 2, S::kThreads, S::kBytes, stream, ma, mb, mc, q);
+    return launch_clusters(k, pairs, 2, plan.split, S::kThreads, S::kBytes, stream, ma, mb, mc, q);
 }
 
 template <int BN>
-int launch_pair_types(const Matmul& p, const Product& q, int sms, cudaStream_t stream) {
+int launch_pair_types(const Matmul& p, const Product& q, const Plan& plan, cudaStream_t stream) {
     if (p.b_blocks)
-        return p.out_bf16 ? launch_pair<BN, true, __nv_bfloat16>(p, q, sms, stream)
-                          : launch_pair<BN, true, float>(p, q, sms, stream);
-    return p.out_bf16 ? launch_pair<BN, false, __nv_bfloat16>(p, q, sms, stream)
-                      : launch_pair<BN, false, float>(p, q, sms, stream);
+        return p.out_bf16 ? launch_pair<BN, true, __nv_bfloat16>(p, q, plan, stream)
+                          : launch_pair<BN, true, float>(p, q, plan, stream);
+    return p.out_bf16 ? launch_pair<BN, false, __nv_bfloat16>(p, q, plan, stream)
+                      : launch_pair<BN, false, float>(p, q, plan, stream);
 }
 
 }  // namespace
 
-size_t matmul_workspace(int64_t, int64_t, int64_t) { return 256; }
+// The workspace: the status word, the flags, the sums.
+constexpr size_t kHead = 16384, kSumsOfPair = (size_t)kFlags * 32 * 32 * sizeof(float4);
+
+size_t matmul_workspace(int64_t M, int64_t N, int64_t K) {
+    if (matmul_is_few(M, N, K)) return 256;
+    const Plan plan = plan_for(M, N, K, kPairs);
+    return plan.split ? kHead + plan.pairs * kSumsOfPair : 256;
+}
 
 int matmul_launch(const Matmul& p, cudaStream_t stream) {
     const int sms = device_sms();
@@ -442,13 +561,13 @@ int matmul_launch(const Matmul& p, cudaStream_t stream) {
     const size_t e = p.out_bf16 ? 2 : 4;
     q.tma_out = (reinterpret_cast<uintptr_t>(p.c) | (uintptr_t)(p.c_ld * e)) % 16 == 0;
     q.status = p.status;
-    // The tile width whose rounds over the SM pairs cover fewer columns in all
-    auto rounds = [&](int bn) {
-        const int64_t tiles = (int64_t)q.m_tiles * ((p.N + bn - 1) / bn);
-        return (tiles + sms / 2 - 1) / (sms / 2) * bn;
-    };
-    return 1.2 * rounds(128) < rounds(256) ? launch_pair_types<128>(p, q, sms, stream)
-                                     : launch_pair_types<256>(p, q, sms, stream);
+    char* ws = reinterpret_cast<char*>(p.status);
+    q.flags = reinterpret_cast<int*>(ws + 256);
+    q.sums = reinterpret_cast<float4*>(ws + kHead);
+    Plan plan = plan_for(p.M, p.N, p.K, kPairs);
+    if (sms / 2 < kPairs) plan = plan_for(p.M, p.N, p.K, sms / 2, false);
+    if (plan.tiles * q.KB > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
+    return plan.width == 128 ? launch_pair_types<128>(p, q, plan, stream) : launch_pair_types<256>(p, q, plan, stream);
 }
 
 }  // namespace block

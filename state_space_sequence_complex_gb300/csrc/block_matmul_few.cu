@@ -220,7 +220,7 @@ int launch(const Matmul& p, const Few& q, cudaStream_t stream) {
     auto* k = product_few<kRows, kBlocks, T>;
     static std::atomic<uint64_t> allowed;
     if (allow_smem(k, (int)S::kBytes, allowed) != cudaSuccess) return SSDC_ERR_CUDA;
-    return launch_clusters(k, (p.N + 127) / 128, (int)q.cluster, kThreads, S::kBytes, stream, ma, mb, q);
+    return launch_clusters(k, (p.N + 127) / 128, (int)q.cluster, false, kThreads, S::kBytes, stream, ma, mb, q);
 }
 
 template <int kRows>

@@ -512,7 +512,7 @@ bool pairs_ok(const void* q, int64_t sb, int64_t st, size_t elem) {
 template <typename K>
 int launch_cluster(K kernel, const Gated& p, int vec, cudaStream_t stream) {
     const int64_t groups = (int64_t)p.B * ((p.D + 32 * vec - 1) / (32 * vec));
-    return launch_clusters(kernel, groups, cluster_size((p.T + kTile - 1) / kTile, groups, 152 * 3), kThreads, 0, stream, p);
+    return launch_clusters(kernel, groups, cluster_size((p.T + kTile - 1) / kTile, groups, 152 * 3), false, kThreads, 0, stream, p);
 }
 
 template <typename T, int kVec, bool kGate>

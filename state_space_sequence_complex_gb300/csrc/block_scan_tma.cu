@@ -525,7 +525,7 @@ int launch(const M& maps, const Gated& p, int warps, int tile, uint32_t smem, cu
     if (allow_smem(kKernel, (int)smem, allowed) != cudaSuccess) return SSDC_ERR_CUDA;
     const int per = p.bf16 ? 64 : 32;
     const int64_t groups = (int64_t)p.B * ((p.D + per - 1) / per);
-    return launch_clusters(kKernel, groups, cluster_size((p.T + tile - 1) / tile, groups, 152), 32 * warps, smem, stream, maps, p);
+    return launch_clusters(kKernel, groups, cluster_size((p.T + tile - 1) / tile, groups, 152), false, 32 * warps, smem, stream, maps, p);
 }
 
 // Fewer tokens than this are one tile of the other kernels, which start sooner.

@@ -201,6 +201,21 @@ __device__ __forceinline__ void named_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// A word in global memory that one CTA sets behind its stores and another waits for, for at most
+// `limit_ns` nanoseconds (false if it gave up).
+__device__ __forceinline__ void st_release(int* p, int v) {
+    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ bool wait_flag(const int* p, int v, uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        int w;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(w) : "l"(p) : "memory");
+        if (w == v) return true;
+        if (globaltimer_ns() - t0 > limit_ns) return false;
+    }
+}
+
 // Two fp32 multiply-adds, or products, as one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;

@@ -412,7 +412,8 @@ def operand(rows, cols, seed, blocks=False, std=1.0):
 
 PRODUCT = [(1, 1, 1), (1, 128, 128), (1, 5136, 1024), (3, 130, 127), (8, 257, 1000), (16, 640, 4096), (17, 64, 129),
            (33, 1000, 384), (64, 2049, 512), (65, 256, 256), (127, 129, 2048), (128, 128, 128), (129, 257, 640),
-           (300, 999, 1111), (1021, 1537, 200), (2000, 1024, 1024), (520, 4096, 96)]
+           (300, 999, 1111), (1021, 1537, 200), (2000, 1024, 1024), (520, 4096, 96),
+           (300, 999, 8192), (130, 100, 16000), (5136, 1024, 4096), (2300, 2100, 3300)]  # (tiles shared between SMs)
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCT)
