@@ -456,14 +456,24 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
             for (int c = 0; c < kVec; ++c)
                 if (w < warp) s[c] = through<kReset>(o.A[c], oh.v[c], s[c]);
         }
+        if (plain) {
 #pragma unroll
-        for (int k = 0; k < kTok; ++k)
+            for (int k = 0; k < kTok; ++k)
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                const float before = kReset && stops(C[k][c]) ? 0.0f : s[c];
-                ca[k][c] *= kGate ? before : before - cu[k][c];
-                s[c] = through<kReset>(C[k][c], v[k][c], s[c]);
-            }
+                for (int c = 0; c < kVec; ++c) {
+                    ca[k][c] *= kGate ? s[c] : s[c] - cu[k][c];
+                    s[c] = fmaf(C[k][c], s[c], v[k][c]);
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTok; ++k)
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    const float before = kReset && stops(C[k][c]) ? 0.0f : s[c];
+                    ca[k][c] *= kGate ? before : before - cu[k][c];
+                    s[c] = through<kReset>(C[k][c], v[k][c], s[c]);
+                }
+        }
         float in[kVec];
         if (R > 1) {
             receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
@@ -487,7 +497,8 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
                 ox[c] = u[k][c] * gr;
                 of[c] = ca[k][c] * gr;
                 oi[c] = cu[k][c] * gr;
-                in[c] = kReset && stops(C[k][c]) ? 0.0f : C[k][c] * gr;
+                in[c] = C[k][c] * gr;
+                if (kReset && !plain && stops(C[k][c])) in[c] = 0.0f;
             }
             Word<T>::put(at + k * 128, ox);
             Word<T>::put(at_f + k * 128, of);
