@@ -59,21 +59,33 @@ Array rows(const void* p, int64_t ld, int64_t M, int64_t D, size_t elem) { retur
 Array dense(const void* p, int64_t n, size_t elem = 4) { return Array{p, 1, 1, n, 0, 0, elem}; }
 
 // Whether two arrays may share a byte. Arrays whose spans meet are still apart where they
-// have the same strides and element size and their columns are apart in every row (slices
-// of one wider array).
+// have the same strides and element size and, in every period of the smaller stride, their
+// columns are apart (slices of one wider array) or, in every period of the larger one, the
+// blocks below it are (planes of one array for each sequence).
 bool overlaps(const Array& a, const Array& b) {
     if (a.p == nullptr || b.p == nullptr || a.hi() <= b.lo() || b.hi() <= a.lo()) return false;
     if (a.elem != b.elem || a.s_mid != b.s_mid || (a.s_outer != b.s_outer && a.outer > 1)) return true;
-    // the stride that separates the rows; every other stride is a multiple of it
+    const uintptr_t d = a.lo() > b.lo() ? a.lo() - b.lo() : b.lo() - a.lo();
+    if (d % a.elem) return true;
+    const bool a_after = a.lo() > b.lo();
+    // apart: whether the later array's `second` elements lie after the earlier one's `first` in every period of `step`
+    auto apart = [&](int64_t step, int64_t first, int64_t second) {
+        const int64_t off = (int64_t)(d / a.elem) % step;
+        return off >= first && off + second <= step;
+    };
+    const Array &early = a_after ? b : a, &late = a_after ? a : b;
+    // the larger stride, if there are two
+    if (a.outer > 1 && a.mid > 1) {
+        const bool outer = a.s_outer >= a.s_mid;
+        const int64_t step = outer ? a.s_outer : a.s_mid;
+        auto block = [&](const Array& r) { return (outer ? (r.mid - 1) * r.s_mid : (r.outer - 1) * r.s_outer) + r.inner; };
+        if (step > 0 && apart(step, block(early), block(late))) return false;
+    }
+    // the smaller stride; every other stride has to be a multiple of it
     int64_t step = a.mid > 1 ? a.s_mid : 0;
     if (a.outer > 1 && (step == 0 || a.s_outer < step)) step = a.s_outer;
     if (step <= 0 || (a.mid > 1 && a.s_mid % step) || (a.outer > 1 && a.s_outer % step)) return true;
-    const uintptr_t d = a.lo() > b.lo() ? a.lo() - b.lo() : b.lo() - a.lo();
-    const bool a_after = a.lo() > b.lo();
-    if (d % a.elem) return true;
-    const int64_t off = (int64_t)(d / a.elem) % step;  // where the later one's columns start in the earlier's rows
-    const int64_t first = a_after ? b.inner : a.inner, second = a_after ? a.inner : b.inner;
-    return !(off >= first && off + second <= step);
+    return !apart(step, early.inner, late.inner);
 }
 
 // An output's rows must be apart from each other.

@@ -1,6 +1,7 @@
 """Host-only checks of the operators around the scan: the symbols that the header
 declares, and the arguments that each entry point refuses before anything reaches a
 GPU. Every call here fails a host check, so the addresses are never used."""
+import ctypes
 import os
 import re
 
@@ -190,3 +191,24 @@ def test_calls_check_their_tensors(lib):
     norm = block.ResidualNorm(4, 16, device="cpu")
     with pytest.raises(ValueError, match="w must have"):
         norm(torch.zeros(4, 16, dtype=torch.bfloat16), None, torch.zeros(15))
+
+
+@pytest.mark.parametrize("call,words", [(0, 21), (1, 17), (2, 30), (3, 16), (4, 16), (5, 12), (6, 15)])
+def test_word_block_calls_refuse_what_the_calls_refuse(lib, call, words):
+    none = (ctypes.c_int64 * words)()      # null addresses, zero sizes
+    assert lib.ssd_block_call(call, none, None) == INVALID
+    assert lib.ssd_block_call(call, None, None) == INVALID
+
+
+@pytest.mark.parametrize("call", [-1, 7, 1 << 20])
+def test_word_block_of_no_call(lib, call):
+    assert lib.ssd_block_call(call, (ctypes.c_int64 * 30)(), None) == INVALID
+
+
+@pytest.mark.parametrize("dims,stride_b,stride_t,off", [
+    ((2, 100, 64, 1), 25600, 64, 6399), ((2, 100, 64, 1), 25600, 64, 25600 - 6399),     # planes (B, 4, T, D)
+    ((2, 100, 64, 1), 64, 512, 127), ((2, 100, 64, 1), 64, 512, 512 - 127),             # planes (T, 4, B, D)
+    ((2, 100, 64, 1), 25600, 256, 63), ((2, 100, 64, 1), 25600, 256, 256 - 63)])        # slices (B, T, 4 D)
+def test_scan_output_that_cuts_into_an_input(lib, dims, stride_b, stride_t, off):
+    x = SEQ(at(1), stride_b, stride_t)
+    assert fwd(lib, dims=dims, x=x, h=SEQ(at(1) + 2 * off, stride_b, stride_t)) == INVALID

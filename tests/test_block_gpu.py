@@ -574,3 +574,102 @@ def test_graph_capture():
     torch.cuda.synchronize()
     got = h.clone()
     assert torch.equal(chain(), got)
+
+
+# ---- tensors past 2^31 elements, or with strides past 2^32 bytes: the far end against a small call there
+
+
+def test_scan_far_along():
+    D, tail = 1024, 700
+    T = (1 << 21) + tail
+    x, f, dh = (torch.empty(1, T, D, dtype=torch.bfloat16, device="cuda").normal_() for _ in range(3))
+    reset = torch.zeros(1, T, dtype=torch.uint8, device="cuda")
+    reset[0, -tail] = 1
+    plan = block.GatedScan(1, T, D, input_gate=False, keep_states=True)
+    h, last = plan(x, f, reset=reset)
+    grads = block.GatedScanBackward(1, T, D, input_gate=False)(x, f, None, plan.states, dh, reset=reset)
+    xs, fs, dhs, rs = (t[:, -tail:] for t in (x, f, dh, reset))
+    want, want_last, g = scan_ref(xs, fs, None, None, rs, dh=dhs)
+    close(h[:, -tail:], want, "h")
+    close(last, want_last, "h_last")
+    close(grads["dx"][:, -tail:], g["dx"], "dx")
+    close(grads["df"][:, -tail:], g["df"], "df")
+    first = scan_ref(x[:, :200], f[:, :200], None, None, None)[0]
+    close(h[:, :200], first, "the first tokens")
+
+
+@pytest.mark.parametrize("T", [40, 500])
+def test_scan_far_apart(T):
+    """Sequences more than 2^32 bytes from one another."""
+    B, D, far = 2, 64, (1 << 31) + 128
+    store = torch.zeros(far + 4 * T * D, dtype=torch.bfloat16, device="cuda")
+    x, f, i, h = (store[k * T * D:].as_strided((B, T, D), (far, D, 1)) for k in range(4))
+    for k, t in enumerate((x, f, i)):
+        t.copy_(randn(B, T, D, seed=k, dtype=torch.bfloat16))
+    h0 = randn(B, D, seed=7)
+    _, last = block.GatedScan(B, T, D)(x, f, i, h0=h0, out=h)
+    want, want_last = scan_ref(x, f, i, h0, None)
+    close(h, want, "h")
+    close(last, want_last, "h_last")
+
+
+def test_norm_and_quantiser_far_along():
+    D, tail = 1024, 130
+    M = (1 << 21) + tail
+    x, res, dy = (torch.empty(M, D, dtype=torch.bfloat16, device="cuda").normal_() for _ in range(3))
+    w = randn(D, seed=5)
+    plan = block.ResidualNorm(M, D, out="bf16")
+    r, y = plan(x, res, w)
+    r_want = x[-tail:].double() + res[-tail:].double()
+    rstd = (r_want.pow(2).mean(1) + 1e-5).rsqrt()
+    close(r[-tail:], r_want, "r")
+    close(y[-tail:], r_want * rstd[:, None] * w.double(), "y")
+    dx, _ = block.ResidualNormBackward(M, D)(dy, r, w, plan.rstd)
+    rt, g = r[-tail:].double(), dy[-tail:].double() * w.double()
+    rstd = plan.rstd[-tail:].double()[:, None]
+    close(dx[-tail:], rstd * (g - rt * rstd * (g * rt * rstd).mean(1, keepdim=True)), "dx")
+    _, q, s = block.ResidualNorm(M, D)(x, res, w)
+    _, q1, s1 = block.ResidualNorm(tail, D)(x[-tail:], res[-tail:], w)
+    assert torch.equal(s[:, -tail:], s1) and torch.equal(q[-tail:].view(torch.uint8), q1.view(torch.uint8))
+    q, s, qt, st = block.Fp8Quantize(M, D, transposed=True)(x)
+    at = M // 128 * 128                   # where the last 128 rows that share a transposed scale begin
+    q1, s1, qt1, st1 = block.Fp8Quantize(M - at, D, transposed=True)(x[at:])
+    assert torch.equal(q[at:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[:, at:], s1)
+    assert torch.equal(qt[:, at:].view(torch.uint8), qt1.view(torch.uint8)) and torch.equal(st[-1:], st1)
+
+
+@pytest.mark.parametrize("M,N,K", [(45056, 50257, 130), (270, 1300, 1 << 21), (5, 1300, (1 << 21) + 16)])
+def test_product_far_along(M, N, K):
+    """C, or B, past 2^31 elements."""
+    a, b = block.fp8_empty(M, K), block.fp8_empty(N, K)
+    for t in (a, b):
+        wide = t.as_strided((t.shape[0], t.stride(0)), (t.stride(0), 1)).view(torch.uint8)
+        wide.random_(0, 0x78)             # positive finite values
+    KB = -(-K // 128)
+    sa = torch.rand(KB, M, device="cuda") + 0.5
+    sb = torch.rand(-(-N // 128), KB, device="cuda") + 0.5
+    c = block.Fp8Product(M, N, K, out="fp32")(a, sa, b, sb)
+    m, n = min(M, 100), min(N, 77)
+    value = lambda q, s: q.float().double() * s.repeat_interleave(128, 1)[:, :K].double()
+    bn = sb.repeat_interleave(128, 0)[:N]
+    want = value(a[-m:], sa.t()[-m:]) @ value(b[-n:], bn[-n:]).t()
+    close(c[-m:, -n:], want, "C")
+
+
+@pytest.mark.parametrize("order", [(0, 1, 2, 3), (1, 0, 2, 3), (2, 0, 1, 3), (0, 2, 1, 3)])
+@pytest.mark.parametrize("T", [30, 200])
+def test_scan_planes_of_one_array(order, T):
+    """x, f, i and h as planes of one array, (B, 4, T, D), (4, B, T, D), (T, B, 4, D) and (B, T, 4, D)."""
+    B, D = 3, 72
+    sizes = {(0, 1, 2, 3): (B, 4, T, D), (1, 0, 2, 3): (4, B, T, D), (2, 0, 1, 3): (T, B, 4, D), (0, 2, 1, 3): (B, T, 4, D)}
+    store = torch.zeros(sizes[order], dtype=torch.bfloat16, device="cuda")
+    planes = store.permute(*(order.index(k) for k in (1, 0, 2, 3)))     # (4, B, T, D)
+    assert planes.shape == (4, B, T, D)
+    for k in range(3):
+        planes[k].copy_(randn(B, T, D, seed=k, dtype=torch.bfloat16))
+    kept = planes[:3].clone()
+    _, last = block.GatedScan(B, T, D)(*planes[:3], out=planes[3])
+    want, want_last = scan_ref(*kept, None, None)
+    close(planes[3], want, "h")
+    close(last, want_last, "h_last")
+    assert torch.equal(planes[:3], kept)
