@@ -565,13 +565,22 @@ def residual_norm(x, residual=None, w=None, eps=1e-5):
 class _Fp8Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w):
-        plan = Fp8Linear(x.shape[0], w.shape[0], x.shape[1], _dtype_name(x), device=x.device)
-        ctx.plan = plan
-        return plan.forward(x, w)
+        (M, K), N, name = x.shape, w.shape[0], _dtype_name(x)
+        x_q, x_s, x_qt, x_st = Fp8Quantize(M, K, name, transposed=True, device=x.device)(x)
+        w_q, w_s, w_qt, w_st = Fp8Quantize(N, K, name, scales="blocks", transposed=True, device=x.device)(w)
+        ctx.save_for_backward(x_qt, x_st, w_qt, w_st)
+        ctx.sizes = M, N, K, name
+        return Fp8Product(M, N, K, name, device=x.device)(x_q, x_s, w_q, w_s)
 
     @staticmethod
     def backward(ctx, dy):
-        return ctx.plan.backward(_unit_last(dy))
+        x_qt, x_st, w_qt, w_st = ctx.saved_tensors
+        M, N, K, name = ctx.sizes
+        with_x, with_w = ctx.needs_input_grad
+        grads = Fp8Quantize(M, N, name, direct=with_x, transposed=with_w, device=dy.device)(_unit_last(dy))
+        dx = Fp8Product(M, K, N, name, device=dy.device)(*grads[:2], w_qt, w_st) if with_x else None
+        dw = Fp8Product(N, K, M, name, b_scales="rows", device=dy.device)(*grads[-2:], x_qt, x_st) if with_w else None
+        return dx, dw
 
 
 def fp8_linear(x, w):
