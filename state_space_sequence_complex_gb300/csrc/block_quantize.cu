@@ -1,12 +1,18 @@
 // 8-bit operands of a matrix (include/ssdc_block.h): e4m3 values with a scale for each row and
 // 128 columns, or for each block of 128 x 128, as the matrix stands and transposed.
 //
-// Bound by HBM: a CTA reads a tile of 128 x 128 once, holds it in registers, and writes both
-// operands' tiles. A thread owns kCols adjacent columns (one 16-byte load) of kRows adjacent
-// rows, so that a group of 128 along a row is half a warp (bfloat16) or one (fp32), and the
-// transposed tile's bytes go to shared memory kRows at a time: a column there is 128
-// bytes, its pieces exchanged by an exclusive or with the column's thread, which spreads both
-// the writes by column and the reads by row over the banks.
+// A CTA reads a tile of 128 x 128 once, holds it in registers, and writes both operands' tiles.
+// A thread owns kCols adjacent columns (one 16-byte load) of kRows adjacent rows, so that a group
+// of 128 along a row is half a warp (bfloat16) or one (fp32), and the transposed tile's bytes go
+// to shared memory kRows at a time: a column there is 128 bytes, its pieces exchanged by an
+// exclusive or with the column's thread, which spreads both the writes by column and the reads by
+// row over the banks.
+//
+// Measured, 32768 x 1024 bfloat16: row scales one way 20 us (5.0 TB/s), both ways 32 us (4.3 TB/s),
+// a block's scale both ways 32 us; fp32 both ways 37 us (5.5 TB/s). Between memory and issue slots:
+// 17 instructions a value both ways, nearly half of all slots, in two CTAs an SM. Quotients two at
+// a time and one scale a lane took it from 35 us to 32; the next tile's loads ahead of this
+// one's work, or three or four CTAs with fewer registers, gained nothing.
 #include <cuda_runtime.h>
 
 #include "block_common.cuh"
@@ -65,7 +71,6 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
         row_amax[r] = 0.0f;
 #pragma unroll
         for (int c = 0; c < kCols; ++c) row_amax[r] = fmaxf(row_amax[r], fabsf(v[r][c]));
-        if (!kBlocks) row_amax[r] = warp_max<kLanes>(row_amax[r]);
     }
     if (kBlocks) {
         float a = 0.0f;
@@ -79,14 +84,42 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
 #pragma unroll
         for (int r = 0; r < kRows; ++r) row_amax[r] = a;
     }
+    Scale mine;
+    if (kBlocks) {
+        mine = Scale(row_amax[0]);
+        if (p.q && t == 0) p.scale[tm * tiles_k + tk] = mine.s;
+    } else if (p.q) {
+        // Each step leaves a lane half the rows, of twice the columns, so that each two lanes end
+        // with one row's maximum (row lane / 2) and make its scale.
+        int o = kLanes / 2;
+#pragma unroll
+        for (int n = kRows / 2; n > 0; n /= 2, o /= 2) {
+            const bool upper = lane & o;
+#pragma unroll
+            for (int k = 0; k < n; ++k) {
+                const float other = __shfl_xor_sync(0xffffffffu, upper ? row_amax[k] : row_amax[k + n], o);
+                row_amax[k] = fmaxf(upper ? row_amax[k + n] : row_amax[k], other);
+            }
+        }
+        mine = Scale(fmaxf(row_amax[0], __shfl_xor_sync(0xffffffffu, row_amax[0], 1)));
+        if (lane % 2 == 0 && lane / 2 < rows) p.scale[tk * p.M + m0 + lane / 2] = mine.s;
+    }
     if (p.q) {
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            const Scale s(row_amax[r]);
+            Scale s = mine;
+            if (!kBlocks) {
+                s.s = __shfl_sync(0xffffffffu, mine.s, 2 * r, kLanes);
+                s.inv = __shfl_sync(0xffffffffu, mine.inv, 2 * r, kLanes);
+            }
             if (r < rows && cols > 0) {
                 float q[kCols];
 #pragma unroll
-                for (int c = 0; c < kCols; ++c) q[c] = s.quotient(v[r][c]);
+                for (int c = 0; c < kCols; c += 2) {
+                    const float2 u = s.quotient(make_float2(v[r][c], v[r][c + 1]));
+                    q[c] = u.x;
+                    q[c + 1] = u.y;
+                }
                 uint8_t* to = p.q + (m0 + r) * p.q_ld + k0;
                 if (cols == kCols) {
                     store_e4m3<kCols>(to, q);
@@ -95,10 +128,6 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
                     for (int c = 0; c < kCols; ++c)
                         if (c < cols) to[c] = e4m3(q[c]);
                 }
-                if (lane == 0) {
-                    if (!kBlocks) p.scale[tk * p.M + m0 + r] = s.s;
-                    else if (t == 0 && r == 0) p.scale[tm * tiles_k + tk] = s.s;
-                }
             }
         }
     }
@@ -106,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
     Scale cs[kCols];
     if (kBlocks) {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) cs[c] = Scale(row_amax[0]);
+        for (int c = 0; c < kCols; ++c) cs[c] = mine;
         if (t == 0) p.scale_t[tk * tiles_m + tm] = cs[0].s;
     } else {
 #pragma unroll
@@ -135,7 +164,11 @@ __global__ void __launch_bounds__(kThreads, 2) quantize(const Quant p) {
     for (int c = 0; c < kCols; ++c) {
         float q[kRows];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) q[r] = cs[c].quotient(v[r][c]);
+        for (int r = 0; r < kRows; r += 2) {
+            const float2 u = cs[c].quotient(make_float2(v[r][c], v[r + 1][c]));
+            q[r] = u.x;
+            q[r + 1] = u.y;
+        }
         store_e4m3<kRows>(&tile[lane * kCols + c][(strip ^ (lane % kPieces)) * kRows], q);
     }
     __syncthreads();
