@@ -112,12 +112,11 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
 
     Raw<T, kVec> rx[kTok], rf[kTok], rg[kTok];
     int n = 0;          // tokens of this warp, the same for all lanes
-    uint32_t stop = 0;  // those at which a document starts
+    uint32_t first = 0;  // whether a document starts at the lane's token
     auto load = [&](int64_t tile) {
         const int64_t t0 = tile * kTile + warp * kTok;
         n = (int)max((int64_t)0, min((int64_t)kTok, p.T - t0));
-        stop = 0;
-        if (kReset) stop = marks(reset, t0, n, lane);
+        if (kReset) first = mark(reset, t0, n, lane);
         const T *px = x + t0 * p.x_t + dl, *pf = f + t0 * p.f_t + dl, *pg = kGate ? g + t0 * p.i_t + dl : nullptr;
         if (n == kTok) {
 #pragma unroll
@@ -146,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
     for (int64_t tile = rank; tile - rank < tiles; tile += R, ++round) {
         const int parity = (int)(round & 1);
         const int rows = n;
+        const uint32_t stop = kReset ? marked(first) : 0;
         // a warp whose tokens are all there and start no document takes the short way
         const bool plain = rows == kTok && (!kReset || stop == 0);
         float C[kTok][kVec], v[kTok][kVec], A[kVec], H[kVec];
@@ -304,8 +304,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
         const int parity = (int)(round & 1);
         const int64_t tile = tiles - 1 - back, t0 = tile * kTile + warp * kTok;
         const int n = tile < 0 ? 0 : (int)max((int64_t)0, min((int64_t)kTok, p.T - t0));
-        uint32_t stop = 0;
-        if (kReset) stop = marks(reset, t0, n, lane);
+        const uint32_t first = kReset ? mark(reset, t0, n, lane) : 0;
         Raw<T, kVec> rx[kTok], rf[kTok], rg[kTok], rh[kTok];
         float s[kVec];
 #pragma unroll
@@ -345,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
                 if (sizeof(T) * kVec * 32 > 128 && d0 + 32 < p.D) ptx::prefetch_l2(q + 32);
             }
         }
+        const uint32_t stop = kReset ? marked(first) : 0;
         const bool plain = n == kTok && (!kReset || stop == 0);
         // a token's factor C, its input's factor u and both factors' derivatives (ca; cu with x
         // in it), and the run's A, H (states) and G (gradients)

@@ -8,6 +8,8 @@
 // over it and copied out from there, and the next rows are on their way meanwhile.
 //
 // Every warp copies its own tokens and waits for them alone; the CTA meets once a tile.
+#include <type_traits>
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -87,6 +89,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
     char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     __shared__ Totals<kVec> totals;
     __shared__ Run<kVec> part[2][kWarps][32];
+    __shared__ bool stopped[2][kWarps];  // whether a warp's tokens hold a reset
     __shared__ uint64_t full[kStages][kWarps];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
@@ -123,10 +126,9 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
     if (lane == 0) fetch(0);
     bool ok = true;
     const int rounds = (tiles + (int)R - 1) / (int)R;
-    uint32_t stop_next = kReset ? marks(reset, (int64_t)rank * kTile + warp * kTok, min(kTok, T_ - ((int)rank * kTile + warp * kTok)), lane) : 0;
+    uint32_t mark_next = kReset ? mark(reset, (int64_t)rank * kTile + warp * kTok, min(kTok, T_ - ((int)rank * kTile + warp * kTok)), lane) : 0;
     for (int round = 0; round < rounds; ++round) {
         const int parity = round & 1, t0 = (round * (int)R + (int)rank) * kTile + warp * kTok, n = min(kTok, T_ - t0);
-        const uint32_t stop = stop_next;
         if (lane == 0 && round + 1 < rounds) {
             ptx::bulk_wait_read<0>();  // the rows of the round before last have been copied out
             fetch(round + 1);
@@ -134,12 +136,6 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
         __syncwarp();
         ok = ptx::mbar_wait(&full[round % kStages][warp], round / kStages & 1, ok ? kWaitNs : 0) && ok;
         char* at = smem + (round % kStages * kWarps + warp) * kWarp + lane * 4;
-        if (kReset && round + 1 < rounds) {
-            const int t1 = t0 + (int)R * kTile;
-            stop_next = marks(reset, t1, min(kTok, T_ - t1), lane);
-        }
-        // a warp whose tokens are all there and start no document takes the short way
-        const bool plain = n == kTok && (!kReset || stop == 0);
         float C[kTok][kVec], v[kTok][kVec], A[kVec], H[kVec];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) {
@@ -164,6 +160,14 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
                 v[k][c] = u * x[c];
             }
         }
+        // (the vote waits for the load, a round ahead)
+        const uint32_t stop = kReset ? marked(mark_next) : 0;
+        if (kReset && round + 1 < rounds) {
+            const int t1 = t0 + (int)R * kTile;
+            mark_next = mark(reset, t1, min(kTok, T_ - t1), lane);
+        }
+        // a warp whose tokens are all there and start no document takes the short way
+        const bool plain = n == kTok && (!kReset || stop == 0);
         if (plain) {
 #pragma unroll
             for (int k = 0; k < kTok; ++k)
@@ -195,6 +199,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
             mine.H[c] = H[c];
         }
         part[parity][warp][lane] = mine;
+        if (kReset && lane == 0) stopped[parity][warp] = stop != 0;
         __syncthreads();
         // the tile's warps before this one (pre); and all of them, in every warp or, where the
         // total goes to the cluster's CTAs, in the last one
@@ -204,20 +209,26 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
             allA[c] = preA[c] = 1.0f;
             allH[c] = preH[c] = 0.0f;
         }
+        const bool whole = !kReset || !__any_sync(0xffffffffu, stopped[parity][lane % kWarps]);
+        auto join = [&](auto with_resets) {
+            constexpr bool kStops = decltype(with_resets)::value;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w > warp && R > 1) break;
-            const Run<kVec> o = part[parity][w][lane];
+            for (int w = 0; w < kWarps; ++w) {
+                if (w > warp && R > 1) break;
+                const Run<kVec> o = part[parity][w][lane];
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                if (w == warp) {
-                    preA[c] = allA[c];
-                    preH[c] = allH[c];
+                for (int c = 0; c < kVec; ++c) {
+                    if (w == warp) {
+                        preA[c] = allA[c];
+                        preH[c] = allH[c];
+                    }
+                    allH[c] = through<kStops>(o.A[c], o.H[c], allH[c]);
+                    allA[c] = both<kStops>(allA[c], o.A[c]);
                 }
-                allH[c] = through<kReset>(o.A[c], o.H[c], allH[c]);
-                allA[c] = both<kReset>(allA[c], o.A[c]);
             }
-        }
+        };
+        if (whole) join(std::false_type());
+        else join(std::true_type());
         float in[kVec];
         if (R > 1) {
             if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -279,6 +290,7 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
     __shared__ Totals<kVec> totals;
     __shared__ Run<kVec> part[2][kWarps][32];     // A and G
     __shared__ Lane<kVec> part_h[2][kWarps][32];  // H
+    __shared__ bool stopped[2][kWarps];           // whether a warp's tokens hold a reset
     __shared__ uint64_t full[kStages][kWarps];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
@@ -304,7 +316,7 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
     auto first = [&](int round) { return (tiles - 1 - (round * (int)R + (int)rank)) * kTile + warp * kTok; };
     auto has = [&](int t0) { return t0 >= warp * kTok && t0 < T_; };
     float s_next[kVec];
-    uint32_t stop_next = 0;
+    uint32_t mark_next = 0;
     auto fetch = [&](int round) {
         const int t0 = first(round);
         uint64_t* bar = &full[round % kStages][warp];
@@ -316,21 +328,21 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
         ptx::tma_load_3d(at, &maps.x, bar, d0, t0, b);
         ptx::tma_load_3d(at + 2 * kArray, &maps.dh, bar, d0, t0, b);
     };
-    auto load_ahead = [&](int round) {  // the tile's state and marks
+    auto load_ahead = [&](int round) {  // the tile's state
         const int t0 = first(round), tile = tiles - 1 - (round * (int)R + (int)rank);
 #pragma unroll
         for (int c = 0; c < kVec; ++c)
             s_next[c] = tile >= 0 && in_d ? __ldg(p.in_states + ((int64_t)b * tiles + tile) * p.D + d + c) : 0.0f;
-        if (kReset) stop_next = marks(reset, t0, has(t0) ? min(kTok, T_ - t0) : 0, lane);
     };
     __syncwarp();
     if (lane == 0) fetch(0);
     load_ahead(0);
+    if (kReset) mark_next = mark(reset, first(0), has(first(0)) ? min(kTok, T_ - first(0)) : 0, lane);
     bool ok = true;
     const int rounds = (tiles + (int)R - 1) / (int)R;
     for (int round = 0; round < rounds; ++round) {
         const int parity = round & 1, t0 = first(round), n = has(t0) ? min(kTok, T_ - t0) : 0;
-        const uint32_t stop = stop_next;
+
         float s[kVec];
 #pragma unroll
         for (int c = 0; c < kVec; ++c) s[c] = s_next[c];
@@ -344,7 +356,6 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
         char *at = smem + (round % kStages * kWarps + warp) * kWarp + lane * 4, *at_f = at + kArray, *at_h = at + 2 * kArray,
              *at_i = at + 3 * kArray;
         if (round + 1 < rounds) load_ahead(round + 1);
-        const bool plain = n == kTok && (!kReset || stop == 0);
         // a token's factor C, its input's factor u and both factors' derivatives (ca; cu with x
         // in it), and the run's A, H (states) and G (gradients)
         float C[kTok][kVec], ca[kTok][kVec], u[kTok][kVec], cu[kTok][kVec], v[kTok][kVec], A[kVec], H[kVec], G[kVec];
@@ -371,6 +382,13 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
                 else cu[k][c] = x[c];
             }
         }
+        // (the vote waits for the load, a round ahead)
+        const uint32_t stop = kReset ? marked(mark_next) : 0;
+        if (kReset && round + 1 < rounds) {
+            const int t1 = first(round + 1);
+            mark_next = mark(reset, t1, has(t1) ? min(kTok, T_ - t1) : 0, lane);
+        }
+        const bool plain = n == kTok && (!kReset || stop == 0);
         if (plain) {
 #pragma unroll
             for (int k = 0; k < kTok; ++k)
@@ -418,6 +436,7 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
             mine_h.v[c] = H[c];
         }
         part[parity][warp][lane] = mine;
+        if (kReset && lane == 0) stopped[parity][warp] = stop != 0;
         part_h[parity][warp][lane] = mine_h;
         __syncthreads();
         // the gradient's run through the tile's warps after this one (suf); and through all, in
@@ -428,34 +447,40 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
             allA[c] = sufA[c] = 1.0f;
             allG[c] = sufG[c] = 0.0f;
         }
+        const bool whole = !kReset || !__any_sync(0xffffffffu, stopped[parity][lane % kWarps]);
+        auto join = [&](auto with_resets) {
+            constexpr bool kStops = decltype(with_resets)::value;
 #pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-            if (w < warp && R > 1) break;
-            const Run<kVec> o = part[parity][w][lane];
+            for (int w = kWarps - 1; w >= 0; --w) {
+                if (w < warp && R > 1) break;
+                const Run<kVec> o = part[parity][w][lane];
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                if (w == warp) {
-                    sufA[c] = allA[c];
-                    sufG[c] = allG[c];
+                for (int c = 0; c < kVec; ++c) {
+                    if (w == warp) {
+                        sufA[c] = allA[c];
+                        sufG[c] = allG[c];
+                    }
+                    allG[c] = through<kStops>(o.A[c], o.H[c], allG[c]);
+                    allA[c] = both<kStops>(allA[c], o.A[c]);
                 }
-                allG[c] = through<kReset>(o.A[c], o.H[c], allG[c]);
-                allA[c] = both<kReset>(allA[c], o.A[c]);
             }
-        }
+            // the state behind the tile's warps before this one
+#pragma unroll
+            for (int w = 0; w < kWarps - 1; ++w) {
+                const Run<kVec> o = part[parity][w][lane];
+                const Lane<kVec> oh = part_h[parity][w][lane];
+#pragma unroll
+                for (int c = 0; c < kVec; ++c)
+                    if (w < warp) s[c] = through<kStops>(o.A[c], oh.v[c], s[c]);
+            }
+        };
+        if (whole) join(std::false_type());
+        else join(std::true_type());
         if (R > 1) {
             if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
             if (warp == 0) send_total<kVec>(totals, round, rank, R, lane, allA, allG);
         }
-        // the state behind the tile's warps before this one, then token by token: what enters a
-        // token (nothing at a reset) makes its gate's gradient
-#pragma unroll
-        for (int w = 0; w < kWarps - 1; ++w) {
-            const Run<kVec> o = part[parity][w][lane];
-            const Lane<kVec> oh = part_h[parity][w][lane];
-#pragma unroll
-            for (int c = 0; c < kVec; ++c)
-                if (w < warp) s[c] = through<kReset>(o.A[c], oh.v[c], s[c]);
-        }
+        // token by token: what enters a token (nothing at a reset) makes its gate's gradient
         if (plain) {
 #pragma unroll
             for (int k = 0; k < kTok; ++k)
