@@ -203,7 +203,14 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
 }
 
 // Gradients. A warp walks rows kRows apart and adds up its share of dw in registers; the CTA's
-// warps that hold the same features join theirs at the end, one row of `partial` a CTA.
+// warps that hold the same features join theirs at the end, one row of `partial` a CTA. The next
+// row is on its way meanwhile: into shared memory where it fits, each lane copying what it will
+// itself read, else into L2.
+template <typename T, int kVals, int kRowWarps, bool kAligned>
+constexpr int bwd_smem() {  // two rows of three arrays a warp
+    constexpr int bytes = cta_warps<kRowWarps>() * 2 * 3 * 32 * kVals * (int)sizeof(T);
+    return kAligned && bytes <= 200 * 1024 ? bytes : 0;
+}
 template <typename T, int kVals, int kRowWarps, bool kAligned>
 __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1 : bwd_ctas(kVals)) norm_bwd(const NormBwd p) {
     using L = Layout<T, kAligned, kVals>;
@@ -217,21 +224,48 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
     float dw[kVals];
 #pragma unroll
     for (int i = 0; i < kVals; ++i) dw[i] = 0.0f;
+    constexpr bool kStaged = bwd_smem<T, kVals, kRowWarps, kAligned>() > 0;
+    extern __shared__ __align__(16) char staged[];
+    T* rows = reinterpret_cast<T*>(staged) + warp * 6 * kWarpSpan;
+    auto copy = [&](int64_t m, int stage) {  // this lane's runs of a row of dy, r and dr
+        if (m < p.M)
+#pragma unroll
+            for (int i = 0; i < L::kRuns; ++i) {
+                const int at = L::run_at(i, lane);
+                if (base + at < p.D) {
+                    T* to = rows + 3 * stage * kWarpSpan + at;
+                    ptx::cp_async_16(to, static_cast<const T*>(p.dy) + m * p.dy_ld + base + at);
+                    ptx::cp_async_16(to + kWarpSpan, static_cast<const T*>(p.r) + m * p.r_ld + base + at);
+                    if (p.dr) ptx::cp_async_16(to + 2 * kWarpSpan, static_cast<const T*>(p.dr) + m * p.dr_ld + base + at);
+                }
+            }
+        ptx::cp_async_commit();
+    };
     int slot = 0;
+    float rstd_next = (int64_t)blockIdx.x * kRows + warp / kRowWarps < p.M ? __ldg(p.rstd + (int64_t)blockIdx.x * kRows + warp / kRowWarps) : 0.0f;
+    if constexpr (kStaged) copy((int64_t)blockIdx.x * kRows + warp / kRowWarps, 0);
     for (int64_t m0 = (int64_t)blockIdx.x * kRows; m0 < p.M; m0 += (int64_t)gridDim.x * kRows, slot ^= 1) {
         const int64_t m = m0 + warp / kRowWarps;
         const bool in = m < p.M;
         const T* dy = static_cast<const T*>(p.dy) + m * p.dy_ld + base;
         const T* r = static_cast<const T*>(p.r) + m * p.r_ld + base;
         const T* dr = static_cast<const T*>(p.dr) + m * p.dr_ld + base;
-        const float rstd = in ? __ldg(p.rstd + m) : 0.0f;
-        // the next row's lines on their way into L2 (a lane a line of each array)
         const int64_t next = (int64_t)gridDim.x * kRows;
-        const int ahead = lane * (128 / (int)sizeof(T));
-        if (m + next < p.M && ahead < kWarpSpan && base + ahead < p.D) {
-            ptx::prefetch_l2(dy + next * p.dy_ld + ahead);
-            ptx::prefetch_l2(r + next * p.r_ld + ahead);
-            if (p.dr) ptx::prefetch_l2(dr + next * p.dr_ld + ahead);
+        const float rstd = rstd_next;
+        rstd_next = m + next < p.M ? __ldg(p.rstd + m + next) : 0.0f;
+        if constexpr (kStaged) {
+            copy(m + next, slot ^ 1);
+            ptx::cp_async_wait<1>();
+            dy = rows + 3 * slot * kWarpSpan;
+            r = dy + kWarpSpan;
+            dr = r + kWarpSpan;
+        } else {  // a lane a line of each array
+            const int ahead = lane * (128 / (int)sizeof(T));
+            if (m + next < p.M && ahead < kWarpSpan && base + ahead < p.D) {
+                ptx::prefetch_l2(dy + next * p.dy_ld + ahead);
+                ptx::prefetch_l2(r + next * p.r_ld + ahead);
+                if (p.dr) ptx::prefetch_l2(dr + next * p.dr_ld + ahead);
+            }
         }
         float g[kVals], xh[kVals], s = 0.0f;
 #pragma unroll
@@ -307,22 +341,25 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
     }
 }
 
-// dw from the CTAs' shares, in their order: a CTA sums 32 features, 8 warps an eighth of the shares each.
-__global__ void __launch_bounds__(256) norm_bwd_sum(const float* partial, float* dw, int D, int parts) {
-    __shared__ float join[8][32];
+// dw from the CTAs' shares, in a fixed order: a CTA sums 32 features, each of its warps its part of
+// the shares, with all loads under way at once (304 shares: 10 a warp).
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps) norm_bwd_sum(const float* partial, float* dw, int D, int parts) {
+    __shared__ float join[kSumWarps][32];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, d = blockIdx.x * 32 + lane;
     grid_dependency_wait();
     float s = 0.0f;
-    const int per = (parts + 7) / 8;
+    const int per = (parts + kSumWarps - 1) / kSumWarps;
     if (d < D) {
-#pragma unroll 8
+#pragma unroll 10
         for (int k = warp * per; k < min((warp + 1) * per, parts); ++k) s += partial[(int64_t)k * D + d];
     }
     join[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && d < D) {
         s = 0.0f;
-        for (int k = 0; k < 8; ++k) s += join[k][lane];
+#pragma unroll
+        for (int k = 0; k < kSumWarps; ++k) s += join[k][lane];
         dw[d] = s;
     }
 }
@@ -362,7 +399,10 @@ void by_row(int64_t D, bool aligned, const F& f) {
                 default: break;
             }
         }
-        return w <= 16 ? f.template run<kVals, 16, kAligned>() : f.template run<kVals, 32, kAligned>();
+        if constexpr (!kWide || !kAligned) {
+            if (w <= 16) return f.template run<kVals, 16, kAligned>();
+        }
+        f.template run<kVals, 32, kAligned>();
     };
     using std::integral_constant;
     constexpr int kOwn = sizeof(T) == 2 ? 32 : 16;
@@ -396,7 +436,11 @@ struct Bwd {
     cudaStream_t stream;
     template <int kVals, int W, bool kAligned>
     void run() const {
-        launch_dependent(norm_bwd<T, kVals, W, kAligned>, dim3(ctas), dim3(32 * cta_warps<W>()), 0, stream, p);
+        constexpr int smem = bwd_smem<T, kVals, W, kAligned>();
+        auto* k = norm_bwd<T, kVals, W, kAligned>;
+        static std::atomic<uint64_t> allowed;
+        if (smem > 0 && allow_smem(k, smem, allowed) != cudaSuccess) return;  // (left for the caller to see)
+        launch_dependent(k, dim3(ctas), dim3(32 * cta_warps<W>()), smem, stream, p);
     }
 };
 
@@ -436,7 +480,7 @@ int norm_bwd_launch(const NormBwd& p, cudaStream_t stream) {
     if (p.bf16) by_row<__nv_bfloat16>(p.D, aligned, Bwd<__nv_bfloat16>{p, parts, stream});
     else by_row<float>(p.D, aligned, Bwd<float>{p, parts, stream});
     if (!p.dw) return 1;
-    if (launch_dependent(norm_bwd_sum, dim3((p.D + 31) / 32), dim3(256), 0, stream, (const float*)p.partial, p.dw, p.D, parts) !=
+    if (launch_dependent(norm_bwd_sum, dim3((p.D + 31) / 32), dim3(32 * kSumWarps), 0, stream, (const float*)p.partial, p.dw, p.D, parts) !=
         cudaSuccess)
         return SSDC_ERR_CUDA;
     return 2;
