@@ -7,6 +7,9 @@
 // lane's features are vectors of 16 bytes (bfloat16: 8, so that a group of 128 features is
 // half a warp; fp32: 4, a whole one), or, for rows that do not start at multiples of 16
 // bytes, single features 32 apart.
+//
+// Measured: M 32768 D 1024 bfloat16 to 8 bits with a residual 41 us (5.7 TB/s), gradients 53 us
+// (5.0 TB/s, the sum of dw's shares in it); M 3001 D 1537 fp32 16 us (4.6 TB/s, half of it in L2).
 #include <type_traits>
 
 #include <cuda_runtime.h>

@@ -116,8 +116,8 @@ __device__ __forceinline__ uint32_t mark(const uint8_t* reset, int64_t t0, int n
 }
 __device__ __forceinline__ uint32_t marked(uint32_t mark) { return __ballot_sync(0xffffffffu, mark != 0); }
 
-// Tiles that a cluster takes at a time: enough CTAs to fill the GPU's SMs several times over
-// with as few exchanges as that allows.
+// Tiles that a cluster takes at a time: so many that the clusters reach `ctas` CTAs, which each
+// kernel's launch gives, with as few exchanges as that allows.
 inline int cluster_size(int64_t tiles, int64_t groups, int ctas) {
     int R = 1;
     while (R < kMaxCluster && R < tiles && groups * R < ctas) R *= 2;

@@ -8,6 +8,11 @@
 // over it and copied out from there, and the next rows are on their way meanwhile.
 //
 // Every warp copies its own tokens and waits for them alone; the CTA meets once a tile.
+//
+// Measured, bfloat16 with an input gate, B 16 T 2048 D 1024: forward 49 us (5.5 TB/s; 50 with
+// resets), backward 95 us (5.0 TB/s; 108 with resets); B 4 T 65536: 409 us (5.2 TB/s) and 830 us.
+// Four in ten issue slots are taken, in the 16 (8 backward) warps that the registers allow: what
+// is left is waits for shared memory and for the special-function unit between dependent steps.
 #include <type_traits>
 
 #include <cuda.h>
@@ -71,7 +76,9 @@ constexpr uint32_t warp_bytes() { return kTok * 128 * kArrays; }
 template <int kWarps, int kTok, int kArrays>
 constexpr uint32_t smem_bytes() { return kStages * kWarps * warp_bytes<kTok, kArrays>() + 128; }
 
-// Warps of a CTA, and tokens that a thread holds in registers
+// Warps of a CTA, and tokens that a thread holds in registers. Forward (B 16 T 2048 / B 2 T 2048 /
+// B 1 T 65536, D 1024, bfloat16): eight warps 49 / 11 / 205 us, four (twice the exchanges, half
+// the waits for each other) 59 / 13 / 277 us.
 constexpr int kFwdWarps = 8, kFwdTok = 16;
 // Backward a token takes twice the registers. Two bfloat16 channels a lane: four warps of 16
 // tokens (B 16 T 2048 D 1024: 94 us; eight of 8: 106 us); one fp32 channel: eight of 8
@@ -561,10 +568,12 @@ int launch(const M& maps, const Gated& p, int warps, int tile, uint32_t smem, cu
     if (allow_smem(kKernel, (int)smem, allowed) != cudaSuccess) return SSDC_ERR_CUDA;
     const int per = p.bf16 ? 64 : 32;
     const int64_t groups = (int64_t)p.B * ((p.D + per - 1) / per);
+    // (B 8 T 2048 D 1024, forward / backward: clusters up to 76 CTAs 46 / 91 us, 152: 28 / 53 us, 304: 33 / 60 us)
     return launch_clusters(kKernel, groups, cluster_size((p.T + tile - 1) / tile, groups, 152), false, 32 * warps, smem, stream, maps, p);
 }
 
-// Fewer tokens than this are one tile of the other kernels, which start sooner.
+// Fewer tokens than this are one tile of the other kernels, which start sooner: B 8 T 64 D 1024,
+// calls one after another, forward 6.9 us there and 7.5 here, backward 8.0 and 8.4.
 constexpr int64_t kMinTokens = 65;
 
 template <typename T, bool kGate>
