@@ -5,8 +5,10 @@
 // Bound by HBM. A row is read once and stays in registers between the sum of squares and
 // the output: a lane holds 8 to 32 features (kVals), and up to 32 warps share a row. A
 // lane's features are vectors of 16 bytes (bfloat16: 8, so that a group of 128 features is
-// half a warp; fp32: 4, a whole one), or, for rows that do not start at multiples of 16
-// bytes, single features 32 apart.
+// half a warp; fp32: 4, a whole one). Rows that do not start at multiples of 16 bytes, but at the
+// same place in 16 bytes in every array, are held the same way from the multiple before their
+// start on, shifted by up to 7 features: rows 8 apart are then shifted alike, so a CTA takes such
+// rows. Other rows are held as single features 32 apart.
 //
 // Measured: M 32768 D 1024 bfloat16 to 8 bits with a residual 41 us (5.7 TB/s), gradients 53 us
 // (5.0 TB/s, the sum of dw's shares in it); M 3001 D 1537 fp32 16 us (4.6 TB/s, half of it in L2).
@@ -26,20 +28,19 @@ namespace {
 
 // Which features a lane holds: value i of lane l is feature base + at(i, l). A run is kRun
 // adjacent features, one load.
-template <typename T, bool kAligned, int kVals>
+enum { kSingle, kAligned, kShifted };
+template <typename T, int kAlign, int kVals>
 struct Layout {
     static constexpr int kWarpSpan = 32 * kVals;  // features of a warp
-    static constexpr int kRun = kAligned ? 16 / (int)sizeof(T) : 1;
+    static constexpr int kRun = kAlign != kSingle ? 16 / (int)sizeof(T) : 1;
     static constexpr int kRuns = kVals / kRun;
-    static constexpr int kGroupRuns = kAligned ? 1 : 4;              // runs of a lane in a group of 128
-    static constexpr int kGroupLanes = 128 / (kRun * kGroupRuns);    // lanes that share a group
     static __device__ __forceinline__ int run_at(int run, int lane) { return (run * 32 + lane) * kRun; }
 };
 
 // kRun values at a feature inside the row, as floats.
-template <typename T, bool kAligned>
+template <typename T, int kAlign>
 __device__ __forceinline__ void load_run(const T* p, float* v) {
-    if constexpr (!kAligned) {
+    if constexpr (kAlign == kSingle) {
         v[0] = to_f32(*p);
     } else if constexpr (sizeof(T) == 2) {
         const uint4 w = *reinterpret_cast<const uint4*>(p);
@@ -86,6 +87,59 @@ __device__ __forceinline__ void load_w(const float* w, float* v) {
     }
 }
 
+// A shifted row's run from feature f on may begin before the row or end behind it: what of it lies
+// inside is then loaded and stored singly, the rest is zeros and stays as it is.
+template <int kRun>
+__device__ __forceinline__ bool whole(int f, int D) { return f >= 0 && f + kRun <= D; }
+template <typename T, int kAlign, int kRun>
+__device__ __forceinline__ void load_part(const T* p, int f, int D, float* v) {
+    if (kAlign != kShifted || whole<kRun>(f, D)) {
+        load_run<T, kAlign>(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) v[e] = f + e >= 0 && f + e < D ? to_f32(p[e]) : 0.0f;
+    }
+}
+template <typename T, int kAlign, int kRun>
+__device__ __forceinline__ void store_part(T* p, int f, int D, const float* v) {
+    if (kAlign != kShifted || whole<kRun>(f, D)) {
+        store_run<T, kRun>(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kRun; ++e)
+            if (f + e >= 0 && f + e < D) p[e] = from_f32<T>(v[e]);
+    }
+}
+
+// The weights as a shifted row's features lie, in shared memory.
+__device__ __forceinline__ void shift_weights(float* to, const float* w, int shift, int D, int n) {
+    for (int k = threadIdx.x; k < n; k += blockDim.x)
+        to[k] = k < shift || k - shift >= D ? 0.0f : w ? __ldg(w + k - shift) : 1.0f;
+    __syncthreads();
+}
+
+// kBy of the steps that take a warp's values from a shifted layout to the one from the row's start
+// on: every value moves that many places towards the first. `next`: the first values of the
+// row's next warp.
+template <int kBy, int kRun, int kRuns>
+__device__ __forceinline__ void move_down(float* v, float* next, int lane) {
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+        float in[kBy];
+#pragma unroll
+        for (int e = 0; e < kBy; ++e) {
+            const float after = i + 1 < kRuns ? v[(i + 1) % kRuns * kRun + e] : next[e];
+            in[e] = __shfl_sync(0xffffffffu, lane == 0 ? after : v[i * kRun + e], (lane + 1) % 32);
+        }
+#pragma unroll
+        for (int e = 0; e < kRun - kBy; ++e) v[i * kRun + e] = v[i * kRun + e + kBy];
+#pragma unroll
+        for (int e = 0; e < kBy; ++e) v[i * kRun + kRun - kBy + e] = in[e];
+    }
+#pragma unroll
+    for (int e = 0; e < kRun - kBy; ++e) next[e] = next[e + kBy];
+}
+
 // 1 / sqrt(m) to within a unit of its last place: the hardware's approximation and one step of
 // Newton's method, the residual 1 - m y^2 formed with the product's rounding error.
 __device__ __forceinline__ float rsqrt_refined(float m) {
@@ -116,17 +170,26 @@ constexpr int bwd_ctas(int vals) { return vals == 32 ? 2 : vals == 16 ? 3 : 4; }
 template <int kRowWarps>
 constexpr int cta_warps() { return kRowWarps > 8 ? kRowWarps : 8; }
 
-template <typename T, typename TO, bool kFp8, int kVals, int kRowWarps, bool kAligned>
+template <typename T, typename TO, bool kFp8, int kVals, int kRowWarps, int kAlign>
 __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1 : 4) norm_fwd(const Norm p) {
-    using L = Layout<T, kAligned, kVals>;
+    using L = Layout<T, kAlign, kVals>;
     constexpr int kWarps = cta_warps<kRowWarps>(), kRun = L::kRun, kWarpSpan = L::kWarpSpan;
+    constexpr int kRows = kWarps / kRowWarps;
+    constexpr int kGroupRuns = kAlign != kSingle ? 1 : 4;              // runs of a lane in a group of 128
+    constexpr int kGroupLanes = SSD_FP8_GROUP / (kRun * kGroupRuns);   // lanes that share a group
     __shared__ float part[1][32];
+    constexpr bool kWeights = kAlign == kShifted && !kFp8, kMoved = kAlign == kShifted && kFp8;
+    __shared__ __align__(16) float weights[kWeights ? kRowWarps * kWarpSpan : 4];
+    __shared__ float firsts[kMoved ? kWarps + 1 : 1][8];
     launch_dependents();
     grid_dependency_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t m = (int64_t)blockIdx.x * (kWarps / kRowWarps) + warp / kRowWarps;
-    const int base = warp % kRowWarps * kWarpSpan;
+    const int64_t m = kAlign == kShifted ? ((int64_t)(blockIdx.x / 8) * kRows + warp / kRowWarps) * 8 + blockIdx.x % 8
+                                         : (int64_t)blockIdx.x * kRows + warp / kRowWarps;
     const bool in = m < p.M;
+    // (the same for all rows of the CTA)
+    const int shift = kAlign == kShifted ? (int)(reinterpret_cast<uintptr_t>(static_cast<const T*>(p.x) + m * p.x_ld) / sizeof(T) % kRun) : 0;
+    int base = warp % kRowWarps * kWarpSpan - shift;
     const T* x = static_cast<const T*>(p.x) + m * p.x_ld + base;
     const T* res = static_cast<const T*>(p.res) + m * p.res_ld + base;
     float v[kVals];
@@ -135,7 +198,7 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
         const int at = L::run_at(i, lane);
 #pragma unroll
         for (int e = 0; e < kRun; ++e) v[i * kRun + e] = 0.0f;
-        if (in && base + at < p.D) load_run<T, kAligned>(x + at, v + i * kRun);
+        if (in && base + at < p.D) load_part<T, kAlign, kRun>(x + at, base + at, p.D, v + i * kRun);
     }
     if (p.res) {
 #pragma unroll
@@ -143,11 +206,17 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
             const int at = L::run_at(i, lane);
             if (in && base + at < p.D) {
                 float u[kRun];
-                load_run<T, kAligned>(res + at, u);
+                load_part<T, kAlign, kRun>(res + at, base + at, p.D, u);
 #pragma unroll
                 for (int e = 0; e < kRun; ++e) v[i * kRun + e] += u[e];
             }
         }
+    }
+    if constexpr (kWeights) shift_weights(weights, p.w, shift, p.D, kRowWarps * kWarpSpan);
+    if constexpr (kMoved && kRowWarps > 1) {  // (there before the row's sum is)
+        if (lane == 0)
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) firsts[warp][e] = v[e];
     }
     float sq = 0.0f;
 #pragma unroll
@@ -155,26 +224,45 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
     sq = row_sum<kRowWarps>(sq, part, 0, warp);
     if (!in) return;
     const float rstd = rsqrt_refined(sq / (float)p.D + p.eps);
-    if (p.rstd && lane == 0 && base == 0) p.rstd[m] = rstd;
+    if (p.rstd && lane == 0 && warp % kRowWarps == 0) p.rstd[m] = rstd;
     if (p.r) {
         T* r = static_cast<T*>(p.r) + m * p.r_ld + base;
 #pragma unroll
         for (int i = 0; i < L::kRuns; ++i) {
             const int at = L::run_at(i, lane);
-            if (base + at < p.D) store_run<T, kRun>(r + at, v + i * kRun);
+            if (base + at < p.D) store_part<T, kAlign, kRun>(r + at, base + at, p.D, v + i * kRun);
         }
     }
+    if constexpr (kMoved) {
+        // groups of 128 and 8-bit values count from the row's start
+        float next[kRun];
 #pragma unroll
-    for (int i0 = 0; i0 < L::kRuns; i0 += L::kGroupRuns) {
-        float lo[kRun * L::kGroupRuns];  // what rounding the two products left out of y
+        for (int e = 0; e < kRun; ++e) next[e] = kRowWarps > 1 && warp % kRowWarps + 1 < kRowWarps ? firsts[warp + 1][e] : 0.0f;
+        if constexpr (kRun == 8)
+            if (shift & 4) move_down<4, kRun, L::kRuns>(v, next, lane);
+        if (shift & 2) move_down<2, kRun, L::kRuns>(v, next, lane);
+        if (shift & 1) move_down<1, kRun, L::kRuns>(v, next, lane);
+        base += shift;
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < L::kRuns; i0 += kGroupRuns) {
+        float lo[kRun * kGroupRuns];  // what rounding the two products left out of y
         float amax = 0.0f;
 #pragma unroll
-        for (int i = i0; i < i0 + L::kGroupRuns; ++i) {
+        for (int i = i0; i < i0 + kGroupRuns; ++i) {
             const int at = L::run_at(i, lane);
-            float w[kRun];
+            __align__(16) float w[kRun];
 #pragma unroll
             for (int e = 0; e < kRun; ++e) w[e] = 1.0f;
-            if (p.w && base + at < p.D) load_w<kRun>(p.w + base + at, w);
+            if constexpr (kWeights) {
+#pragma unroll
+                for (int e = 0; e < kRun; e += 4) *reinterpret_cast<float4*>(w + e) = *reinterpret_cast<const float4*>(weights + base + shift + at + e);
+            } else if (p.w && base + at < p.D) {
+                if (!kMoved || base + at + kRun <= p.D) load_w<kRun>(p.w + base + at, w);
+                else
+#pragma unroll
+                    for (int e = 0; e < kRun; ++e) w[e] = base + at + e < p.D ? __ldg(p.w + base + at + e) : 0.0f;
+            }
 #pragma unroll
             for (int e = 0; e < kRun; ++e) {
                 float& t = v[i * kRun + e];
@@ -186,20 +274,27 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
                 t = y;
             }
             if (!kFp8 && base + at < p.D)
-                store_run<TO, kRun>(static_cast<TO*>(p.y) + m * p.y_ld + base + at, v + i * kRun);
+                store_part<TO, kAlign, kRun>(static_cast<TO*>(p.y) + m * p.y_ld + base + at, base + at, p.D, v + i * kRun);
         }
         if (kFp8) {
-            amax = warp_max<L::kGroupLanes>(amax);
+            amax = warp_max<kGroupLanes>(amax);
             const Scale s(amax);
             const int first = base + L::run_at(i0, lane);  // in the same group for all its lanes and runs
-            if (lane % L::kGroupLanes == 0 && first < p.D) p.scale[(int64_t)(first / SSD_FP8_GROUP) * p.M + m] = s.s;
+            if (lane % kGroupLanes == 0 && first < p.D) p.scale[(int64_t)(first / SSD_FP8_GROUP) * p.M + m] = s.s;
 #pragma unroll
-            for (int i = i0; i < i0 + L::kGroupRuns; ++i) {
+            for (int i = i0; i < i0 + kGroupRuns; ++i) {
                 const int at = L::run_at(i, lane);
                 float q[kRun];
 #pragma unroll
                 for (int e = 0; e < kRun; ++e) q[e] = s.quotient(v[i * kRun + e], lo[(i - i0) * kRun + e]);
-                if (base + at < p.D) store_e4m3<kRun>(static_cast<uint8_t*>(p.y) + m * p.y_ld + base + at, q);
+                uint8_t* to = static_cast<uint8_t*>(p.y) + m * p.y_ld + base + at;
+                if (kMoved ? base + at + kRun <= p.D : base + at < p.D) {
+                    store_e4m3<kRun>(to, q);
+                } else if (kMoved) {
+#pragma unroll
+                    for (int e = 0; e < kRun; ++e)
+                        if (base + at + e < p.D) to[e] = e4m3(q[e]);
+                }
             }
         }
     }
@@ -209,27 +304,46 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
 // warps that hold the same features join theirs at the end, one row of `partial` a CTA. The next
 // row is on its way meanwhile: into shared memory where it fits, each lane copying what it will
 // itself read, else into L2.
-template <typename T, int kVals, int kRowWarps, bool kAligned>
-constexpr int bwd_smem() {  // two rows of three arrays a warp
+template <typename T, int kVals, int kRowWarps, int kAlign>
+constexpr int bwd_staging() {  // bytes: two rows of three arrays a warp
     constexpr int bytes = cta_warps<kRowWarps>() * 2 * 3 * 32 * kVals * (int)sizeof(T);
-    return kAligned && bytes <= 200 * 1024 ? bytes : 0;
+    return kAlign == kAligned && bytes <= 200 * 1024 || kAlign == kShifted && kRowWarps <= 2 ? bytes : 0;
 }
-template <typename T, int kVals, int kRowWarps, bool kAligned>
+template <typename T, int kVals, int kRowWarps, int kAlign>
+constexpr int bwd_smem() {  // and, for shifted rows, the weights
+    return bwd_staging<T, kVals, kRowWarps, kAlign>() + (kAlign == kShifted ? kRowWarps * 32 * kVals * 4 : 0);
+}
+template <typename T, int kVals, int kRowWarps, int kAlign>
 __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1 : bwd_ctas(kVals)) norm_bwd(const NormBwd p) {
-    using L = Layout<T, kAligned, kVals>;
+    using L = Layout<T, kAlign, kVals>;
     constexpr int kWarps = cta_warps<kRowWarps>(), kRun = L::kRun, kRows = kWarps / kRowWarps, kWarpSpan = L::kWarpSpan;
     __shared__ float part[2][32];
     __shared__ float join[kRows > 1 ? kWarps - kRowWarps : 1][kRows > 1 ? kWarpSpan / 4 : 1];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int base = warp % kRowWarps * kWarpSpan;
+    // Rows: kRows at a time. Shifted ones are 8 apart, and gridDim.x is a multiple of 8.
+    constexpr int kApart = kAlign == kShifted ? 8 : 1;
+    const int64_t row0 = kAlign == kShifted ? (int64_t)(blockIdx.x / 8) * kRows * 8 + blockIdx.x % 8 : (int64_t)blockIdx.x * kRows;
+    const int in_cta = warp / kRowWarps * kApart;
+    const int shift = kAlign == kShifted ? (int)(reinterpret_cast<uintptr_t>(static_cast<const T*>(p.dy) + row0 * p.dy_ld) / sizeof(T) % kRun) : 0;
+    const int base = warp % kRowWarps * kWarpSpan - shift;
     launch_dependents();
     grid_dependency_wait();
     float dw[kVals];
 #pragma unroll
     for (int i = 0; i < kVals; ++i) dw[i] = 0.0f;
-    constexpr bool kStaged = bwd_smem<T, kVals, kRowWarps, kAligned>() > 0;
+    constexpr int kStaging = bwd_staging<T, kVals, kRowWarps, kAlign>();
+    constexpr bool kStaged = kStaging > 0;
     extern __shared__ __align__(16) char staged[];
     T* rows = reinterpret_cast<T*>(staged) + warp * 6 * kWarpSpan;
+    float* weights = reinterpret_cast<float*>(staged + kStaging);
+    auto fetch = [&](T* to, const T* from, int f) {
+        if (kAlign != kShifted || whole<kRun>(f, p.D)) {
+            ptx::cp_async_16(to, from);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) to[e] = f + e >= 0 && f + e < p.D ? from[e] : from_f32<T>(0.0f);
+        }
+    };
     auto copy = [&](int64_t m, int stage) {  // this lane's runs of a row of dy, r and dr
         if (m < p.M)
 #pragma unroll
@@ -237,18 +351,19 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
                 const int at = L::run_at(i, lane);
                 if (base + at < p.D) {
                     T* to = rows + 3 * stage * kWarpSpan + at;
-                    ptx::cp_async_16(to, static_cast<const T*>(p.dy) + m * p.dy_ld + base + at);
-                    ptx::cp_async_16(to + kWarpSpan, static_cast<const T*>(p.r) + m * p.r_ld + base + at);
-                    if (p.dr) ptx::cp_async_16(to + 2 * kWarpSpan, static_cast<const T*>(p.dr) + m * p.dr_ld + base + at);
+                    fetch(to, static_cast<const T*>(p.dy) + m * p.dy_ld + base + at, base + at);
+                    fetch(to + kWarpSpan, static_cast<const T*>(p.r) + m * p.r_ld + base + at, base + at);
+                    if (p.dr) fetch(to + 2 * kWarpSpan, static_cast<const T*>(p.dr) + m * p.dr_ld + base + at, base + at);
                 }
             }
         ptx::cp_async_commit();
     };
     int slot = 0;
-    float rstd_next = (int64_t)blockIdx.x * kRows + warp / kRowWarps < p.M ? __ldg(p.rstd + (int64_t)blockIdx.x * kRows + warp / kRowWarps) : 0.0f;
-    if constexpr (kStaged) copy((int64_t)blockIdx.x * kRows + warp / kRowWarps, 0);
-    for (int64_t m0 = (int64_t)blockIdx.x * kRows; m0 < p.M; m0 += (int64_t)gridDim.x * kRows, slot ^= 1) {
-        const int64_t m = m0 + warp / kRowWarps;
+    float rstd_next = row0 + in_cta < p.M ? __ldg(p.rstd + row0 + in_cta) : 0.0f;
+    if constexpr (kStaged) copy(row0 + in_cta, 0);
+    if constexpr (kAlign == kShifted) shift_weights(weights, p.w, shift, p.D, kRowWarps * kWarpSpan);
+    for (int64_t m0 = row0; m0 < p.M; m0 += (int64_t)gridDim.x * kRows, slot ^= 1) {
+        const int64_t m = m0 + in_cta;
         const bool in = m < p.M;
         const T* dy = static_cast<const T*>(p.dy) + m * p.dy_ld + base;
         const T* r = static_cast<const T*>(p.r) + m * p.r_ld + base;
@@ -263,13 +378,17 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
             r = dy + kWarpSpan;
             dr = r + kWarpSpan;
         } else {  // a lane a line of each array
-            const int ahead = lane * (128 / (int)sizeof(T));
+            const int ahead = lane * (128 / (int)sizeof(T)) + shift;
             if (m + next < p.M && ahead < kWarpSpan && base + ahead < p.D) {
                 ptx::prefetch_l2(dy + next * p.dy_ld + ahead);
                 ptx::prefetch_l2(r + next * p.r_ld + ahead);
                 if (p.dr) ptx::prefetch_l2(dr + next * p.dr_ld + ahead);
             }
         }
+        auto load = [&](const T* from, int f, float* to) {
+            if constexpr (kStaged) load_run<T, kAlign>(from, to);
+            else load_part<T, kAlign, kRun>(from, f, p.D, to);
+        };
         float g[kVals], xh[kVals], s = 0.0f;
 #pragma unroll
         for (int i = 0; i < L::kRuns; ++i) {
@@ -277,17 +396,22 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
 #pragma unroll
             for (int e = 0; e < kRun; ++e) g[i * kRun + e] = xh[i * kRun + e] = 0.0f;
             if (in && base + at < p.D) {
-                load_run<T, kAligned>(dy + at, g + i * kRun);
-                load_run<T, kAligned>(r + at, xh + i * kRun);
+                load(dy + at, base + at, g + i * kRun);
+                load(r + at, base + at, xh + i * kRun);
             }
         }
 #pragma unroll
         for (int i = 0; i < L::kRuns; ++i) {
             const int at = L::run_at(i, lane);
-            float w[kRun];
+            __align__(16) float w[kRun];
 #pragma unroll
             for (int e = 0; e < kRun; ++e) w[e] = 1.0f;
-            if (p.w && base + at < p.D) load_w<kRun>(p.w + base + at, w);
+            if constexpr (kAlign == kShifted) {
+#pragma unroll
+                for (int e = 0; e < kRun; e += 4) *reinterpret_cast<float4*>(w + e) = *reinterpret_cast<const float4*>(weights + base + shift + at + e);
+            } else if (p.w && base + at < p.D) {
+                load_w<kRun>(p.w + base + at, w);
+            }
 #pragma unroll
             for (int e = 0; e < kRun; ++e) {
                 const int j = i * kRun + e;
@@ -307,13 +431,13 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
                 float o[kRun];
 #pragma unroll
                 for (int e = 0; e < kRun; ++e) o[e] = 0.0f;
-                if (p.dr) load_run<T, kAligned>(dr + at, o);
+                if (p.dr) load(dr + at, base + at, o);
 #pragma unroll
                 for (int e = 0; e < kRun; ++e) {
                     const int j = i * kRun + e;
                     o[e] = fmaf(rstd, fmaf(-xh[j], mean, g[j]), o[e]);
                 }
-                store_run<T, kRun>(dx + at, o);
+                store_part<T, kAlign, kRun>(dx + at, base + at, p.D, o);
             }
         }
     }
@@ -340,7 +464,8 @@ __global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1
         const int at = L::run_at(i, lane);
         if (base + at < p.D)
 #pragma unroll
-            for (int e = 0; e < kRun; ++e) to[at + e] = dw[i * kRun + e];
+            for (int e = 0; e < kRun; ++e)
+                if (kAlign != kShifted || (base + at + e >= 0 && base + at + e < p.D)) to[at + e] = dw[i * kRun + e];
     }
 }
 
@@ -367,16 +492,33 @@ __global__ void __launch_bounds__(32 * kSumWarps) norm_bwd_sum(const float* part
     }
 }
 
-bool rows16(const void* q, int64_t ld, size_t elem) {
-    return q == nullptr || (reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * (int64_t)elem % 16 == 0);
-}
+// How the rows of a call's arrays lie: all from multiples of 16 bytes on; all from the same place in
+// 16 bytes on, row by row; or otherwise.
+struct Rows {
+    size_t elem;
+    bool start = true, alike = true;
+    uintptr_t at = 0;
+    int64_t ld = 0;
+    bool any = false;
+    void add(const void* q, int64_t q_ld) {
+        if (q == nullptr) return;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(q) % 16;
+        const int64_t l = q_ld % (int64_t)(16 / elem);
+        start = start && a == 0 && l == 0;
+        if (any) alike = alike && a == at && l == ld;
+        any = true;
+        at = a;
+        ld = l;
+    }
+};
+bool words16(const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
 
 // Features a lane holds, and warps of a row (a power of two). Rows in 16-byte loads: 32 bfloat16
 // (M 32768 D 1024, 8-bit output: 44 us; 16: 52 us) or 16 fp32 (M 3001 D 1536: 12.6 us; 32: 14.8 us),
 // which is four or eight loads under way. Rows in single loads: 8, for more warps to a row
 // (M 3001 D 1537 fp32: 17 us; 32: 35 us). The widest rows need 32 either way.
-int lane_vals(int64_t D, bool bf16, bool aligned) {
-    const int v = !aligned ? 8 : bf16 ? 32 : 16;
+int lane_vals(int64_t D, bool bf16, int align) {
+    const int v = align == kSingle ? 8 : bf16 ? 32 : 16;
     return D <= 32 * 32 * v ? v : 32;
 }
 int row_warps(int64_t D, int vals) {
@@ -384,104 +526,147 @@ int row_warps(int64_t D, int vals) {
     while (w * 32 * vals < D) w *= 2;
     return w;
 }
+int64_t spread(int64_t D, bool bf16, int align) { return align == kShifted ? D + (bf16 ? 7 : 3) : D; }
+// Rows that are held shifted: of up to 8 warps (their weights are in shared memory), that take no
+// more lanes so than in single loads. Backward, bfloat16 (single / shifted): M 18000 D 901 63 / 49 us,
+// M 10000 D 1601 86 / 41 us, M 4000 D 4001 132 / 58 us; but M 40000 D 417, in twice the lanes,
+// 75 / 83 us. fp32: M 4000 D 3001 102 / 50 us, M 18000 D 901 66 / 73 us. Forward, bfloat16: to 8 bits
+// M 10000 D 1601 56 / 49 us, M 4000 D 4001 51 / 42 us, but M 16384 D 1022 41 / 70 us, in twice the
+// lanes; to bfloat16 M 4000 D 4001 36 / 39 us, and M 2000 D 5501, 32 warps in single loads, 52 /
+// 35 us. fp32 forward M 4000 D 3001 41 / 45 us: in single loads.
+bool may_shift(int64_t D, bool bf16) {
+    const int vals = bf16 ? 32 : 16, w = row_warps(spread(D, bf16, kShifted), vals);
+    return w <= 8 && w * vals == 8 * row_warps(D, 8);
+}
+bool shift_fwd(const Norm& p) { return p.bf16 && may_shift(p.D, true) && (p.out_type == SSD_TYPE_E4M3 || p.D > 4096); }
+bool shift_bwd(int64_t D, bool bf16) { return may_shift(D, bf16) && (bf16 || D > 1024); }
 
-// Calls f.template operator()<kVals, kRowWarps, kAligned>() for a row of D features.
-template <typename T, typename F>
-void by_row(int64_t D, bool aligned, const F& f) {
-    const int vals = lane_vals(D, sizeof(T) == 2, aligned), w = row_warps(D, vals);
+// Calls f.template run<kVals, kRowWarps, kAlign>() for a row of D features. kLeast: the fewest warps
+// of a shifted row (0: rows are not held so).
+template <typename T, int kLeast, typename F>
+void by_row(int64_t D, int align, const F& f) {
+    const int vals = lane_vals(D, sizeof(T) == 2, align), w = row_warps(spread(D, sizeof(T) == 2, align), vals);
     auto warps = [&](auto v, auto al) {
-        constexpr int kVals = decltype(v)::value;
-        constexpr bool kAligned = decltype(al)::value;
-        constexpr bool kWide = kVals == 32 && !(kAligned && sizeof(T) == 2);  // taken for the widest rows only
+        constexpr int kVals = decltype(v)::value, kAlign = decltype(al)::value;
+        constexpr bool kWide = kVals == 32 && !(kAlign != kSingle && sizeof(T) == 2);  // taken for the widest rows only
         if constexpr (!kWide) {
-            switch (w) {
-                case 1: return f.template run<kVals, 1, kAligned>();
-                case 2: return f.template run<kVals, 2, kAligned>();
-                case 4: return f.template run<kVals, 4, kAligned>();
-                case 8: return f.template run<kVals, 8, kAligned>();
-                default: break;
+            constexpr int kFrom = kAlign == kShifted ? kLeast : 1;
+            if constexpr (kFrom <= 1) {
+                if (w == 1) return f.template run<kVals, 1, kAlign>();
             }
+            if constexpr (kFrom <= 2) {
+                if (w == 2) return f.template run<kVals, 2, kAlign>();
+            }
+            if constexpr (kFrom <= 4) {
+                if (w == 4) return f.template run<kVals, 4, kAlign>();
+            }
+            if (w == 8) return f.template run<kVals, 8, kAlign>();
         }
-        if constexpr (!kWide || !kAligned) {
-            if (w <= 16) return f.template run<kVals, 16, kAligned>();
+        if constexpr (kAlign != kShifted) {
+            if constexpr (!kWide || kAlign == kSingle) {
+                if (w <= 16) return f.template run<kVals, 16, kAlign>();
+            }
+            f.template run<kVals, 32, kAlign>();
         }
-        f.template run<kVals, 32, kAligned>();
     };
     using std::integral_constant;
     constexpr int kOwn = sizeof(T) == 2 ? 32 : 16;
-    if (aligned && vals == kOwn) warps(integral_constant<int, kOwn>{}, std::true_type{});
-    else if (aligned) warps(integral_constant<int, 32>{}, std::true_type{});
-    else if (vals == 8) warps(integral_constant<int, 8>{}, std::false_type{});
-    else warps(integral_constant<int, 32>{}, std::false_type{});
+    if constexpr (kLeast > 0) {
+        if (align == kShifted) return warps(integral_constant<int, kOwn>{}, integral_constant<int, kShifted>{});
+    }
+    if (align == kAligned && vals == kOwn) warps(integral_constant<int, kOwn>{}, integral_constant<int, kAligned>{});
+    else if (align == kAligned) warps(integral_constant<int, 32>{}, integral_constant<int, kAligned>{});
+    else if (vals == 8) warps(integral_constant<int, 8>{}, integral_constant<int, kSingle>{});
+    else warps(integral_constant<int, 32>{}, integral_constant<int, kSingle>{});
 }
 
 template <typename T, typename TO, bool kFp8>
 struct Fwd {
     const Norm& p;
     cudaStream_t stream;
-    template <int kVals, int W, bool kAligned>
+    template <int kVals, int W, int kAlign>
     void run() const {
-        constexpr int rows = cta_warps<W>() / W;
-        launch_dependent(norm_fwd<T, TO, kFp8, kVals, W, kAligned>, dim3((unsigned)((p.M + rows - 1) / rows)),
+        constexpr int rows = cta_warps<W>() / W * (kAlign == kShifted ? 8 : 1), ctas = kAlign == kShifted ? 8 : 1;
+        launch_dependent(norm_fwd<T, TO, kFp8, kVals, W, kAlign>, dim3((unsigned)((p.M + rows - 1) / rows * ctas)),
                          dim3(32 * cta_warps<W>()), 0, stream, p);
     }
 };
 template <typename T>
-void fwd(const Norm& p, bool aligned, cudaStream_t stream) {
-    if (p.out_type == SSD_TYPE_E4M3) by_row<T>(p.D, aligned, Fwd<T, T, true>{p, stream});
-    else if (p.out_type == SSD_TYPE_BF16) by_row<T>(p.D, aligned, Fwd<T, __nv_bfloat16, false>{p, stream});
-    else by_row<T>(p.D, aligned, Fwd<T, float, false>{p, stream});
+void fwd(const Norm& p, int align, cudaStream_t stream) {
+    constexpr bool kHalf = sizeof(T) == 2;
+    if (p.out_type == SSD_TYPE_E4M3) by_row<T, kHalf ? 1 : 0>(p.D, align, Fwd<T, T, true>{p, stream});
+    else if (p.out_type == SSD_TYPE_BF16) by_row<T, kHalf ? 8 : 0>(p.D, align, Fwd<T, __nv_bfloat16, false>{p, stream});
+    else by_row<T, 0>(p.D, align, Fwd<T, float, false>{p, stream});
 }
 template <typename T>
 struct Bwd {
     const NormBwd& p;
     int ctas;
     cudaStream_t stream;
-    template <int kVals, int W, bool kAligned>
+    template <int kVals, int W, int kAlign>
     void run() const {
-        constexpr int smem = bwd_smem<T, kVals, W, kAligned>();
-        auto* k = norm_bwd<T, kVals, W, kAligned>;
+        constexpr int smem = bwd_smem<T, kVals, W, kAlign>();
+        auto* k = norm_bwd<T, kVals, W, kAlign>;
         static std::atomic<uint64_t> allowed;
         if (smem > 0 && allow_smem(k, smem, allowed) != cudaSuccess) return;  // (left for the caller to see)
         launch_dependent(k, dim3(ctas), dim3(32 * cta_warps<W>()), smem, stream, p);
     }
 };
 
-// The CTAs that walk the rows: as many as the SMs hold, fewer for few rows and (their shares of dw
-// being written and read again) for wide ones.
-int bwd_parts(int64_t M, int64_t D, bool bf16, bool aligned) {
-    const int vals = lane_vals(D, bf16, aligned), w = row_warps(D, vals), rows = w > 8 ? 1 : 8 / w;
-    const int64_t ctas = (M + rows - 1) / rows, most = D <= 2048 ? 152 * bwd_ctas(vals) : 152;
+// The CTAs that walk the rows: as many as the SMs hold, fewer for few rows (M 4000 D 4000 bfloat16:
+// 37 us with two an SM, 47 us with one). Those of shifted rows are a multiple of 8.
+int bwd_parts(int64_t M, int64_t D, bool bf16, int align) {
+    const int vals = lane_vals(D, bf16, align), w = row_warps(spread(D, bf16, align), vals), rows = w > 8 ? 1 : 8 / w;
+    int64_t ctas = (M + rows - 1) / rows;
+    if (align == kShifted) ctas = (M + 8 * rows - 1) / (8 * rows) * 8;
+    const int64_t most = w > 8 ? 152 : 152 * bwd_ctas(vals);
     return (int)(ctas < most ? ctas : most);
 }
 
 }  // namespace
 
 int norm_fwd_launch(const Norm& p, cudaStream_t stream) {
-    const size_t e = p.bf16 ? 2 : 4, eo = p.out_type == SSD_TYPE_F32 ? 4 : p.out_type == SSD_TYPE_BF16 ? 2 : 1;
-    const bool aligned = p.D % (16 / (int)e) == 0 && rows16(p.x, p.x_ld, e) && rows16(p.res, p.res_ld, e) &&
-                         rows16(p.r, p.r_ld, e) && rows16(p.y, p.y_ld, eo) && rows16(p.w, 0, 4);
-    if (p.bf16) fwd<__nv_bfloat16>(p, aligned, stream);
-    else fwd<float>(p, aligned, stream);
+    const bool same = p.out_type == SSD_TYPE_BF16, fp8 = p.out_type == SSD_TYPE_E4M3;
+    const size_t e = p.bf16 ? 2 : 4, eo = fp8 ? 1 : p.out_type == SSD_TYPE_F32 ? 4 : 2;
+    Rows in{e}, out{eo};
+    in.add(p.x, p.x_ld);
+    in.add(p.res, p.res_ld);
+    in.add(p.r, p.r_ld);
+    out.add(p.y, p.y_ld);
+    int align = kSingle;
+    if (p.D % (16 / (int)e) == 0 && in.start && out.start && words16(p.w)) {
+        align = kAligned;
+    } else if (shift_fwd(p) && in.alike) {
+        if (same) in.add(p.y, p.y_ld);
+        if (same ? in.alike : fp8 && out.start && words16(p.w)) align = kShifted;
+    }
+    if (p.bf16) fwd<__nv_bfloat16>(p, align, stream);
+    else fwd<float>(p, align, stream);
     return 1;
 }
 
 int norm_bwd_parts(int64_t M, int64_t D) {  // for any type and alignment
     int most = 0;
-    for (int k = 0; k < 4; ++k) {
-        const int n = bwd_parts(M, D, (k & 1) != 0, (k & 2) != 0);
-        most = n > most ? n : most;
-    }
+    for (int align : {kSingle, kAligned, kShifted})
+        for (bool bf16 : {false, true}) {
+            const int n = align == kShifted && !shift_bwd(D, bf16) ? 0 : bwd_parts(M, D, bf16, align);
+            most = n > most ? n : most;
+        }
     return most;
 }
 
 int norm_bwd_launch(const NormBwd& p, cudaStream_t stream) {
-    const size_t e = p.bf16 ? 2 : 4;
-    const bool aligned = p.D % (16 / (int)e) == 0 && rows16(p.dy, p.dy_ld, e) && rows16(p.dr, p.dr_ld, e) &&
-                         rows16(p.r, p.r_ld, e) && rows16(p.dx, p.dx_ld, e) && rows16(p.w, 0, 4);
-    const int parts = bwd_parts(p.M, p.D, p.bf16, aligned);
-    if (p.bf16) by_row<__nv_bfloat16>(p.D, aligned, Bwd<__nv_bfloat16>{p, parts, stream});
-    else by_row<float>(p.D, aligned, Bwd<float>{p, parts, stream});
+    Rows rows{(size_t)(p.bf16 ? 2 : 4)};
+    rows.add(p.dy, p.dy_ld);
+    rows.add(p.dr, p.dr_ld);
+    rows.add(p.r, p.r_ld);
+    rows.add(p.dx, p.dx_ld);
+    int align = kSingle;
+    if (p.D % (p.bf16 ? 8 : 4) == 0 && rows.start && words16(p.w)) align = kAligned;
+    else if (shift_bwd(p.D, p.bf16) && rows.alike) align = kShifted;
+    const int parts = bwd_parts(p.M, p.D, p.bf16, align);
+    if (p.bf16) by_row<__nv_bfloat16, 1>(p.D, align, Bwd<__nv_bfloat16>{p, parts, stream});
+    else by_row<float, 4>(p.D, align, Bwd<float>{p, parts, stream});
     if (!p.dw) return 1;
     if (launch_dependent(norm_bwd_sum, dim3((p.D + 31) / 32), dim3(32 * kSumWarps), 0, stream, (const float*)p.partial, p.dw, p.D, parts) !=
         cudaSuccess)

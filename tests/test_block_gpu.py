@@ -673,3 +673,94 @@ def test_scan_planes_of_one_array(order, T):
     close(planes[3], want, "h")
     close(last, want_last, "h_last")
     assert torch.equal(planes[:3], kept)
+
+
+# ---- rows that start anywhere in 16 bytes
+
+
+@pytest.mark.parametrize("M,D,pitch,at", [(1, 9, 9, 0), (37, 77, 77, 3), (70, 1017, 1017, 0), (70, 1018, 1018, 1), (19, 1024, 1024, 5),
+                                          (33, 1025, 1031, 2), (9, 2041, 2041, 0), (30, 2047, 2050, 7), (17, 4001, 4001, 0),
+                                          (10, 8185, 8185, 0), (10, 8186, 8187, 4), (3, 8193, 8193, 1), (2500, 250, 251, 1)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "fp8"), ("bf16", "fp32"), ("fp32", "fp32"), ("fp32", "fp8")])
+def test_norm_rows_that_start_anywhere(M, D, pitch, at, dtype, out):
+    """Rows that start at the same place in 16 bytes in every array, and a residual that starts one element later."""
+    lib, st = block.load(), torch.cuda.current_stream().cuda_stream
+    rows = lambda t: block.ssd_rows(t.data_ptr(), t.stride(0))
+    types = {"bf16": block.TYPE_BF16, "fp32": block.TYPE_F32, "fp8": block.TYPE_E4M3}
+
+    def rows_at(fill, dt, k=at):
+        store = torch.full((k + M * pitch + 16,), fill, dtype=dt, device="cuda")
+        return store, store[k:].as_strided((M, D), (pitch, 1))
+
+    w = randn(D, seed=3, mean=1.0)
+    for apart in (0, 1):
+        (_, x), (_, res) = rows_at(0.0, DT[dtype]), rows_at(0.0, DT[dtype], at + apart)
+        x.copy_(randn(M, D, seed=1))
+        res.copy_(randn(M, D, seed=2))
+        r_store, r = rows_at(7.0, DT[dtype])
+        rstd = torch.empty(M, device="cuda")
+        r_want = x.double() + res.double()
+        s_want = (r_want.square().mean(1) + 1e-5).rsqrt()
+        y_want = r_want * s_want[:, None] * w.double()
+        if out == "fp8":
+            y = block.fp8_empty(M, D)
+            y.as_strided((M, y.stride(0)), (y.stride(0), 1)).view(torch.uint8).fill_(0x7f)
+            scale = torch.empty(-(-D // 128), M, device="cuda")
+        else:
+            y_store, y = rows_at(7.0, DT[out])
+            scale = None
+        rc = lib.ssd_residual_norm_fwd(rows(x), rows(res), w.data_ptr(), 1e-5, M, D, types[dtype], rows(r), types[out], rows(y),
+                                       None if scale is None else scale.data_ptr(), rstd.data_ptr(), st)
+        assert rc == 0
+        close(r, r_want, "r")
+        close(rstd, s_want, "rstd")
+        outside = torch.ones_like(r_store, dtype=torch.bool)
+        outside[at:].as_strided((M, D), (pitch, 1)).fill_(False)
+        assert bool((r_store[outside] == 7.0).all())
+        if out == "fp8":
+            pad = y.as_strided((M, y.stride(0)), (y.stride(0), 1)).view(torch.uint8)[:, D:]
+            assert bool((pad == 0x7f).all())
+            groups = torch.nn.functional.pad(y_want.abs(), (0, -D % 128)).unflatten(1, (-1, 128)).amax(2)
+            s_ref = groups.clamp_min(2.0 ** -100) / 448
+            assert float(((scale.t().double() - s_ref).abs() / s_ref).max()) <= 1e-5
+            got = y.float().double() * scale.t().double().repeat_interleave(128, 1)[:, :D]
+            q_ref = (y_want / s_ref.repeat_interleave(128, 1)[:, :D]).float().to(torch.float8_e4m3fn)
+            e = float((y.float().double() - q_ref.float().double()).norm() / q_ref.float().double().norm())
+            assert e <= 4e-3, e
+            assert float((got - y_want).norm() / y_want.norm()) <= 2.0 ** -4
+        else:
+            close(y, y_want, "y")
+            assert bool((y_store[outside] == 7.0).all())
+
+
+@pytest.mark.parametrize("M,D,pitch,at", [(1, 9, 9, 0), (37, 77, 77, 3), (300, 1017, 1017, 0), (70, 1018, 1018, 1), (19, 1024, 1024, 5),
+                                          (33, 1025, 1031, 2), (9, 2041, 2041, 0), (130, 2047, 2050, 7), (67, 4001, 4001, 0),
+                                          (10, 8185, 8185, 0), (10, 8186, 8187, 4), (3, 8193, 8193, 1), (6000, 250, 251, 1)])
+@pytest.mark.parametrize("dtype,with_dr", [("bf16", True), ("bf16", False), ("fp32", True)])
+def test_norm_gradients_of_rows_that_start_anywhere(M, D, pitch, at, dtype, with_dr):
+    lib, st = block.load(), torch.cuda.current_stream().cuda_stream
+    rows = lambda t: block.ssd_rows(0 if t is None else t.data_ptr(), 0 if t is None else t.stride(0))
+
+    def rows_at(seed, k=at):
+        store = torch.full((k + M * pitch + 16,), 7.0, dtype=DT[dtype], device="cuda")
+        t = store[k:].as_strided((M, D), (pitch, 1))
+        if seed:
+            t.copy_(randn(M, D, seed=seed))
+        return store, t
+
+    w, rstd = randn(D, seed=4, mean=1.0), torch.rand(M, generator=torch.Generator().manual_seed(5)).cuda() + 0.5
+    nbytes = lib.ssd_residual_norm_bwd_workspace_bytes(M, D)
+    for apart in (0, 1):
+        (_, dy), (_, r), (_, dr), (store, dx) = rows_at(1), rows_at(2, at + apart), rows_at(3), rows_at(0)
+        dr = dr if with_dr else None
+        dw, ws = torch.empty(D, device="cuda"), torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        assert lib.ssd_residual_norm_bwd(rows(dy), rows(dr), rows(r), w.data_ptr(), rstd.data_ptr(), M, D,
+                                         block._TYPES[dtype], rows(dx), dw.data_ptr(), ws.data_ptr(), nbytes, st) == 0
+        g, xh = dy.double() * w.double(), r.double() * rstd.double()[:, None]
+        want = rstd.double()[:, None] * (g - xh * (g * xh).mean(1, keepdim=True)) + (0 if dr is None else dr.double())
+        close(dx, want, "dx")
+        terms = (dy.double() * xh).abs().sum(0)
+        assert float(((dw.double() - (dy.double() * xh).sum(0)).abs() / terms).max()) <= 1e-5
+        outside = torch.ones_like(store, dtype=torch.bool)
+        outside[at:].as_strided((M, D), (pitch, 1)).fill_(False)
+        assert bool((store[outside] == 7.0).all())
