@@ -764,3 +764,28 @@ def test_norm_gradients_of_rows_that_start_anywhere(M, D, pitch, at, dtype, with
         outside = torch.ones_like(store, dtype=torch.bool)
         outside[at:].as_strided((M, D), (pitch, 1)).fill_(False)
         assert bool((store[outside] == 7.0).all())
+
+
+@pytest.mark.parametrize("D", [601, 1601, 5501])
+def test_norm_in_place_of_rows_that_start_anywhere(D):
+    """r over x or over the residual, dx over dy or over dr: as into arrays of their own."""
+    M, dt = 41, torch.bfloat16
+    lib, st = block.load(), torch.cuda.current_stream().cuda_stream
+    rows = lambda t: block.ssd_rows(t.data_ptr(), t.stride(0))
+    x, res, dr, w = randn(M, D, seed=1, dtype=dt), randn(M, D, seed=2, dtype=dt), randn(M, D, seed=3, dtype=dt), randn(D, seed=4)
+    plan = block.ResidualNorm(M, D)
+    r, q, scale = (t.clone() for t in plan(x, res, w))
+    for over in (0, 1):
+        a = [x.clone(), res.clone()]
+        q1, s1 = block.fp8_empty(M, D), torch.empty_like(scale)
+        assert lib.ssd_residual_norm_fwd(rows(a[0]), rows(a[1]), w.data_ptr(), 1e-5, M, D, block.TYPE_BF16, rows(a[over]),
+                                         block.TYPE_E4M3, rows(q1), s1.data_ptr(), None, st) == 0
+        assert torch.equal(a[over], r) and torch.equal(s1, scale) and torch.equal(q1.view(torch.uint8), q.view(torch.uint8))
+    back = block.ResidualNormBackward(M, D)
+    dx, dw = (t.clone() for t in back(x, r, w, plan.rstd, dr))
+    nbytes = back.workspace.numel()
+    for over in (0, 1):
+        a, dw1 = [x.clone(), dr.clone()], torch.empty_like(dw)
+        assert lib.ssd_residual_norm_bwd(rows(a[0]), rows(a[1]), rows(r), w.data_ptr(), plan.rstd.data_ptr(), M, D, block.TYPE_BF16,
+                                         rows(a[over]), dw1.data_ptr(), back.workspace.data_ptr(), nbytes, st) == 0
+        assert torch.equal(a[over], dx) and torch.equal(dw1, dw)
