@@ -75,12 +75,22 @@ typedef struct {
  *             SSDC_ERR_TIMEOUT, and the results are NaN. The caller zeroes it once
  *             (ssd_complex_status() reads it)
  * One launch. Results do not depend on timing: sums run in a fixed order.
+ *
+ * ssd_gated_scan_fwd_ws: the same with a workspace of ssd_gated_scan_workspace_bytes() (16-byte
+ * aligned; its contents need not be kept). Where sequences are long and too few for the GPU,
+ * those are cut into segments that are walked at the same time, in two launches; elsewhere the
+ * size is 0, and the call is the one above.
  */
 #define SSD_GATED_STATE_TOKENS 64
 size_t ssd_gated_scan_states_bytes(ssd_gated_dims dims);
 int ssd_gated_scan_fwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float *h0, const uint8_t *reset,
                        ssd_gated_dims dims, ssd_seq_out h, float *h_last, float *states, int32_t *status,
                        cudaStream_t stream);
+
+size_t ssd_gated_scan_workspace_bytes(ssd_gated_dims dims);
+int ssd_gated_scan_fwd_ws(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float *h0, const uint8_t *reset,
+                          ssd_gated_dims dims, ssd_seq_out h, float *h_last, float *states, int32_t *status,
+                          void *workspace, size_t ws_bytes, cudaStream_t stream);
 
 /*
  * One token for every batch row (the forward pass at T = 1, for generation):
@@ -206,6 +216,7 @@ int ssd_fp8_matmul(ssd_rows_in a, const float *a_scale, ssd_rows_in b, const flo
 #define SSD_CALL_RESIDUAL_NORM_BWD 4   /* 16 words */
 #define SSD_CALL_FP8_QUANTIZE 5        /* 12 words */
 #define SSD_CALL_FP8_MATMUL 6          /* 15 words */
+#define SSD_CALL_GATED_SCAN_FWD_WS 7   /* 23 words */
 int ssd_block_call(int32_t call, const int64_t *words, cudaStream_t stream);
 
 #ifdef __cplusplus

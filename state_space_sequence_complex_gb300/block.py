@@ -36,7 +36,7 @@ STATE_TOKENS = 64
 _TYPES = {"fp32": TYPE_F32, "bf16": TYPE_BF16, "fp8": TYPE_E4M3}
 _DTYPES = {"fp32": torch.float32, "bf16": torch.bfloat16}
 
-EXPORTS = ("ssd_gated_scan_states_bytes", "ssd_gated_scan_fwd", "ssd_gated_scan_step", "ssd_gated_scan_bwd",
+EXPORTS = ("ssd_gated_scan_states_bytes", "ssd_gated_scan_fwd", "ssd_gated_scan_workspace_bytes", "ssd_gated_scan_fwd_ws", "ssd_gated_scan_step", "ssd_gated_scan_bwd",
            "ssd_residual_norm_fwd", "ssd_residual_norm_bwd_workspace_bytes", "ssd_residual_norm_bwd",
            "ssd_fp8_quantize", "ssd_fp8_matmul_workspace_bytes", "ssd_fp8_matmul", "ssd_block_call")
 
@@ -67,6 +67,8 @@ def load() -> ctypes.CDLL:
     for name, res, args in (
             ("ssd_gated_scan_states_bytes", sz, [d]),
             ("ssd_gated_scan_fwd", i32, [q, q, q, vp, vp, d, q, vp, vp, vp, vp]),
+            ("ssd_gated_scan_workspace_bytes", sz, [d]),
+            ("ssd_gated_scan_fwd_ws", i32, [q, q, q, vp, vp, d, q, vp, vp, vp, vp, sz, vp]),
             ("ssd_gated_scan_step", i32, [q, q, q, vp, i64, i64, i32, q, vp, vp]),
             ("ssd_gated_scan_bwd", i32, [q, q, q, vp, vp, q, vp, d, q, q, q, vp, vp, vp]),
             ("ssd_residual_norm_fwd", i32, [r, r, vp, f32, i64, i64, i32, r, i32, r, vp, vp, vp]),
@@ -203,7 +205,7 @@ def fp8_empty(rows: int, cols: int, device="cuda"):
 
 
 class GatedScan:
-    """h_t = c_t h_{t-1} + v_t for every channel (``ssd_gated_scan_fwd``), with
+    """h_t = c_t h_{t-1} + v_t for every channel (``ssd_gated_scan_fwd_ws``), with
     a_t = sigmoid(f_t), c_t = a_t (0 where ``reset`` marks the first token of a
     document), v_t = sigmoid(i_t) x_t, or (1 - a_t) x_t with ``input_gate`` False.
     ``__call__`` takes (B, T, D) tensors with contiguous channels, an optional
@@ -226,13 +228,16 @@ class GatedScan:
         if keep_states:
             self.states = torch.empty((B, -(-T // STATE_TOKENS), D), dtype=torch.float32, device=self.device)
         self.workspace = torch.zeros(64, dtype=torch.int32, device=self.device)
+        nbytes = load().ssd_gated_scan_workspace_bytes(self.dims)
+        self.joints = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
         self._like = self.dtype, torch.Size(self.shape), _index(self.device)
         self._state = torch.float32, torch.Size(self.state_shape), self._like[2]
         self._marks = torch.uint8, torch.Size(self.mark_shape), self._like[2]
         self._dims = B, T, D, self.dims.type
         self._h = _seq("h", self.h, self._like)
-        self._kept = (self.h_last.data_ptr(), 0 if self.states is None else self.states.data_ptr(), self.workspace.data_ptr())
-        self._call = _Call("ssd_gated_scan_fwd", 0, 21, self._like[2])
+        self._kept = (self.h_last.data_ptr(), 0 if self.states is None else self.states.data_ptr(), self.workspace.data_ptr(),
+                      0 if self.joints is None else self.joints.data_ptr(), nbytes)
+        self._call = _Call("ssd_gated_scan_fwd_ws", 7, 23, self._like[2])
 
     def __call__(self, x, f, i=None, h0=None, reset=None, out=None, stream=None):
         """``out``: where h goes instead of this object's ``h``, a (B, T, D) tensor

@@ -210,11 +210,25 @@ size_t ssd_gated_scan_states_bytes(ssd_gated_dims dims) {
     return (size_t)(dims.B * state_rows(dims) * dims.D) * sizeof(float);
 }
 
+size_t ssd_gated_scan_workspace_bytes(ssd_gated_dims d) {
+    if (check_gated(d) != SSDC_OK) return 0;
+    const int segments = gated_segments(d.B, d.T, d.D, d.type == SSD_TYPE_BF16);
+    return segments > 1 ? (size_t)(d.B * segments * d.D) * sizeof(float2) : 0;
+}
+
 int ssd_gated_scan_fwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* h0, const uint8_t* reset,
                        ssd_gated_dims d, ssd_seq_out h, float* h_last, float* states, int32_t* status,
                        cudaStream_t stream) {
+    return ssd_gated_scan_fwd_ws(x, f, i, h0, reset, d, h, h_last, states, status, nullptr, 0, stream);
+}
+
+int ssd_gated_scan_fwd_ws(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* h0, const uint8_t* reset,
+                          ssd_gated_dims d, ssd_seq_out h, float* h_last, float* states, int32_t* status,
+                          void* workspace, size_t ws_bytes, cudaStream_t stream) {
     int rc = check_gated(d);
     if (rc != SSDC_OK) return rc;
+    const size_t need = workspace ? ssd_gated_scan_workspace_bytes(d) : 0;
+    if (workspace != nullptr && (ws_bytes < need || !aligned_to(workspace, 16))) return SSDC_ERR_WORKSPACE;
     Args a;
     a.input(seq(x.p, x.stride_b, x.stride_t, d));
     a.input(seq(f.p, f.stride_b, f.stride_t, d));
@@ -225,6 +239,7 @@ int ssd_gated_scan_fwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* h0
     a.output(dense(h_last, d.B * d.D), true, h0);
     a.output(dense(states, d.B * state_rows(d) * d.D), false);
     a.output(dense(status, 1), false);
+    if (need > 0) a.output(dense(workspace, (int64_t)(need / 4)));
     if (a.rc != SSDC_OK) return a.rc;
     rc = check_token_strides(d, {x.stride_t, f.stride_t, i.stride_t, h.stride_t});
     if (rc == SSDC_OK) rc = check_device();
@@ -233,6 +248,7 @@ int ssd_gated_scan_fwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* h0
     p.h0 = h0; p.reset = reset;
     p.h = h.p; p.h_b = h.stride_b; p.h_t = h.stride_t;
     p.h_last = h_last; p.states = states; p.status = status;
+    p.joints = need > 0 ? static_cast<float2*>(workspace) : nullptr;
     (void)cudaGetLastError();
     return done(gated_fwd_launch(p, stream));
 }
@@ -442,6 +458,17 @@ int ssd_block_call(int32_t call, const int64_t* words, cudaStream_t stream) {
             const ssd_seq_out h = seq_out();
             float *h_last = f32(), *states = f32();
             return ssd_gated_scan_fwd(x, f, i, h0, reset, d, h, h_last, states, static_cast<int32_t*>(ptr()), stream);
+        }
+        case SSD_CALL_GATED_SCAN_FWD_WS: {
+            const ssd_seq_in x = seq_in(), f = seq_in(), i = seq_in();
+            const float* h0 = f32();
+            const uint8_t* reset = static_cast<const uint8_t*>(ptr());
+            const ssd_gated_dims d = dims();
+            const ssd_seq_out h = seq_out();
+            float *h_last = f32(), *states = f32();
+            int32_t* status = static_cast<int32_t*>(ptr());
+            void* ws = ptr();
+            return ssd_gated_scan_fwd_ws(x, f, i, h0, reset, d, h, h_last, states, status, ws, (size_t)i64(), stream);
         }
         case SSD_CALL_GATED_SCAN_STEP: {
             const ssd_seq_in x = seq_in(), f = seq_in(), i = seq_in();

@@ -68,6 +68,10 @@ struct Gated {
     void* h;
     int64_t h_b, h_t;
     float *h_last, *states;
+    // a sequence in segments of `segment` tokens, walked by CTAs of their own (segments > 1): what takes
+    // the state that enters a segment from the one before, (B, segments, D) pairs
+    float2* joints;
+    int segments, segment;
     // backward
     const float* in_states;
     const void* dh;
@@ -79,6 +83,7 @@ struct Gated {
     int* status;  // or null
 };
 int gated_fwd_launch(const Gated& p, cudaStream_t stream);
+int gated_segments(int64_t B, int64_t T, int64_t D, bool bf16);  // that a call with a workspace takes
 int gated_bwd_launch(const Gated& p, cudaStream_t stream);
 int gated_step_launch(const Gated& p, cudaStream_t stream);
 

@@ -88,7 +88,12 @@ constexpr int bwd_warps() { return sizeof(T) == 2 ? 4 : 8; }
 template <typename T>
 constexpr int bwd_tok() { return 64 / bwd_warps<T>(); }
 
-template <typename T, bool kGate, bool kReset>
+// Few sequences and channels leave most SMs idle, however many CTAs a cluster has. Long sequences are
+// then cut into segments, and two kernels take the place of one: the first reads the segments (but
+// each sequence's last) for their maps (kTotals; nothing else is written), the second walks them
+// all, each from the state that the joints before it make. The inputs are read twice, by many
+// more SMs.
+template <typename T, bool kGate, bool kReset, bool kTotals>
 __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(const __grid_constant__ FwdMaps maps, const Gated p) {
     constexpr int kVec = Word<T>::kVec, kWarps = kFwdWarps, kTok = kFwdTok, kTile = kWarps * kTok, kArrays = kGate ? 3 : 2;
     constexpr uint32_t kWarp = warp_bytes<kTok, kArrays>(), kArray = kTok * 128;
@@ -105,10 +110,13 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
         ptx::fence_mbar_init();
     }
     if (R > 1) totals_init(totals, R);
-    const int groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
+    const int groups = (p.D + 32 * kVec - 1) / (32 * kVec);
+    const int mine_of = p.segments - (kTotals ? 1 : 0);  // segments of a sequence in this launch
+    const int group = blockIdx.x / R / mine_of, segment = blockIdx.x / R % mine_of;
+    const int t_begin = segment * p.segment;
     const int b = group / groups, d0 = group % groups * 32 * kVec, d = d0 + lane * kVec;
     const bool in_d = d < p.D;
-    const int T_ = (int)p.T, tiles = (T_ + kTile - 1) / kTile;
+    const int T_ = p.segments > 1 ? (int)min(p.T, (int64_t)t_begin + p.segment) : (int)p.T, tiles = (T_ - t_begin + kTile - 1) / kTile;
     const int64_t state_at = (int64_t)b * p.D + d, state_rows = (p.T + SSD_GATED_STATE_TOKENS - 1) / SSD_GATED_STATE_TOKENS;
     const uint8_t* reset = kReset ? p.reset + (int64_t)b * p.T : nullptr;
 
@@ -117,10 +125,33 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
     float carry[kVec];
 #pragma unroll
     for (int c = 0; c < kVec; ++c) carry[c] = p.h0 && in_d ? p.h0[state_at + c] : 0.0f;
+    float through_all[kVec];  // kTotals: the factor of all tiles so far
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) through_all[c] = 1.0f;
+    if (p.segments > 1) {
+        float2* joint = p.joints + (int64_t)b * p.segments * p.D + d;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+            if (kTotals) {
+                // (h_last may be h0: the second kernel takes h0 from here)
+                if (segment == 0 && warp == 0 && in_d) joint[c] = make_float2(kStop, carry[c]);
+                carry[c] = 0.0f;
+            } else {
+                carry[c] = 0.0f;
+                if (in_d) {
+#pragma unroll 8
+                    for (int s = 0; s <= segment; ++s) {
+                        const float2 j = joint[(int64_t)s * p.D + c];
+                        carry[c] = through<true>(j.x, j.y, carry[c]);
+                    }
+                }
+            }
+        }
+    }
 
     // the copies of this warp's rows of the CTA's tile of a round (none where they are all past the end: the barrier's phase passes all the same)
     auto fetch = [&](int round) {
-        const int t0 = (round * (int)R + (int)rank) * kTile + warp * kTok;
+        const int t0 = t_begin + (round * (int)R + (int)rank) * kTile + warp * kTok;
         uint64_t* bar = &full[round % kStages][warp];
         if (t0 >= T_) return ptx::mbar_arrive(bar);
         char* at = smem + (round % kStages * kWarps + warp) * kWarp;
@@ -133,9 +164,10 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
     if (lane == 0) fetch(0);
     bool ok = true;
     const int rounds = (tiles + (int)R - 1) / (int)R;
-    uint32_t mark_next = kReset ? mark(reset, (int64_t)rank * kTile + warp * kTok, min(kTok, T_ - ((int)rank * kTile + warp * kTok)), lane) : 0;
+    const int t_first = t_begin + (int)rank * kTile + warp * kTok;
+    uint32_t mark_next = kReset ? mark(reset, t_first, min(kTok, T_ - t_first), lane) : 0;
     for (int round = 0; round < rounds; ++round) {
-        const int parity = round & 1, t0 = (round * (int)R + (int)rank) * kTile + warp * kTok, n = min(kTok, T_ - t0);
+        const int parity = round & 1, t0 = t_begin + (round * (int)R + (int)rank) * kTile + warp * kTok, n = min(kTok, T_ - t0);
         if (lane == 0 && round + 1 < rounds) {
             ptx::bulk_wait_read<0>();  // the rows of the round before last have been copied out
             fetch(round + 1);
@@ -246,41 +278,47 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
             for (int c = 0; c < kVec; ++c) {
                 in[c] = carry[c];
                 carry[c] = through<kReset>(allA[c], allH[c], carry[c]);
+                if (kTotals) through_all[c] = both<kReset>(through_all[c], allA[c]);
             }
         }
+        if constexpr (!kTotals) {
 #pragma unroll
-        for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(preA[c], preH[c], in[c]);
-        if (p.states && t0 % SSD_GATED_STATE_TOKENS == 0 && n > 0 && in_d) {
-            float* s = p.states + ((int64_t)b * state_rows + t0 / SSD_GATED_STATE_TOKENS) * p.D + d;
+            for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(preA[c], preH[c], in[c]);
+            if (p.states && t0 % SSD_GATED_STATE_TOKENS == 0 && n > 0 && in_d) {
+                float* s = p.states + ((int64_t)b * state_rows + t0 / SSD_GATED_STATE_TOKENS) * p.D + d;
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) s[c] = in[c];
-        }
-        // h over x (rows past the end are not copied out)
-        if (plain) {
-#pragma unroll
-            for (int k = 0; k < kTok; ++k) {
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) in[c] = fmaf(C[k][c], in[c], v[k][c]);
-                Word<T>::put(at + k * 128, in);
+                for (int c = 0; c < kVec; ++c) s[c] = in[c];
             }
-        } else {
+            // h over x (rows past the end are not copied out)
+            if (plain) {
 #pragma unroll
-            for (int k = 0; k < kTok; ++k) {
+                for (int k = 0; k < kTok; ++k) {
 #pragma unroll
-                for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(C[k][c], v[k][c], in[c]);
-                Word<T>::put(at + k * 128, in);
+                    for (int c = 0; c < kVec; ++c) in[c] = fmaf(C[k][c], in[c], v[k][c]);
+                    Word<T>::put(at + k * 128, in);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kTok; ++k) {
+#pragma unroll
+                    for (int c = 0; c < kVec; ++c) in[c] = through<kReset>(C[k][c], v[k][c], in[c]);
+                    Word<T>::put(at + k * 128, in);
+                }
             }
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && n > 0) {
-            ptx::tma_store_3d(&maps.h, at, d0, t0, b);
-            ptx::bulk_commit();
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && n > 0) {
+                ptx::tma_store_3d(&maps.h, at, d0, t0, b);
+                ptx::bulk_commit();
+            }
         }
     }
     if (rank == 0 && warp == 0 && in_d) {
 #pragma unroll
-        for (int c = 0; c < kVec; ++c) p.h_last[state_at + c] = carry[c];
+        for (int c = 0; c < kVec; ++c) {
+            if (kTotals) p.joints[((int64_t)b * p.segments + segment + 1) * p.D + d + c] = make_float2(through_all[c], ok ? carry[c] : __int_as_float(0x7fffffff));
+            else if (segment == p.segments - 1) p.h_last[state_at + c] = carry[c];
+        }
     }
     if (lane == 0) ptx::bulk_wait_all();
     pause_if(!ok);
@@ -572,15 +610,36 @@ int launch(const M& maps, const Gated& p, int warps, int tile, uint32_t smem, cu
     return launch_clusters(kKernel, groups, cluster_size((p.T + tile - 1) / tile, groups, 152), false, 32 * warps, smem, stream, maps, p);
 }
 
+// Tokens of a segment: whole tiles.
+int segment_tokens(int64_t T, int64_t segments, int64_t tile) {
+    const int64_t tiles = (T + tile - 1) / tile;
+    return (int)((tiles + segments - 1) / segments * tile);
+}
+
+template <auto kKernel>
+int launch_segments(const FwdMaps& maps, const Gated& p, int segments, uint32_t smem, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed;
+    if (allow_smem(kKernel, (int)smem, allowed) != cudaSuccess) return SSDC_ERR_CUDA;
+    const int per = p.bf16 ? 64 : 32;
+    return launch_clusters(kKernel, (int64_t)p.B * ((p.D + per - 1) / per) * segments, 1, false, 32 * kFwdWarps, smem, stream, maps, p);
+}
+
 // Fewer tokens than this are one tile of the other kernels, which start sooner: B 8 T 64 D 1024,
 // calls one after another, forward 6.9 us there and 7.5 here, backward 8.0 and 8.4.
 constexpr int64_t kMinTokens = 65;
 
-template <typename T, bool kGate>
+template <typename T, bool kGate, bool kReset>
 int fwd(const FwdMaps& m, const Gated& p, cudaStream_t stream) {
     constexpr uint32_t smem = smem_bytes<kFwdWarps, kFwdTok, kGate ? 3 : 2>();
-    return p.reset ? launch<gated_fwd_tma<T, kGate, true>>(m, p, kFwdWarps, kFwdWarps * kFwdTok, smem, stream)
-                   : launch<gated_fwd_tma<T, kGate, false>>(m, p, kFwdWarps, kFwdWarps * kFwdTok, smem, stream);
+    if (p.segments == 1) return launch<gated_fwd_tma<T, kGate, kReset, false>>(m, p, kFwdWarps, kFwdWarps * kFwdTok, smem, stream);
+    const int first = launch_segments<gated_fwd_tma<T, kGate, kReset, true>>(m, p, p.segments - 1, smem, stream);
+    if (first < 0) return first;
+    const int second = launch_segments<gated_fwd_tma<T, kGate, kReset, false>>(m, p, p.segments, smem, stream);
+    return second < 0 ? second : first + second;
+}
+template <typename T, bool kGate>
+int fwd(const FwdMaps& m, const Gated& p, cudaStream_t stream) {
+    return p.reset ? fwd<T, kGate, true>(m, p, stream) : fwd<T, kGate, false>(m, p, stream);
 }
 template <typename T, bool kGate>
 int bwd(const BwdMaps& m, const Gated& p, cudaStream_t stream) {
@@ -591,8 +650,17 @@ int bwd(const BwdMaps& m, const Gated& p, cudaStream_t stream) {
 
 }  // namespace
 
-int tma_fwd_launch(const Gated& p, cudaStream_t stream) {
+int tma_fwd_launch(const Gated& call, cudaStream_t stream) {
+    Gated p = call;
     if (p.T < kMinTokens || p.T > INT32_MAX - 4096) return 0;
+    p.segments = 1;
+    p.segment = 0;
+    const int64_t segments = p.joints ? gated_segments(p.B, p.T, p.D, p.bf16) : 1;
+    if (segments > 1) {
+        constexpr int kTile = kFwdWarps * kFwdTok;  // (a state is kept at multiples of its half)
+        p.segment = segment_tokens(p.T, segments, kTile);
+        p.segments = (int)((p.T + p.segment - 1) / p.segment);
+    }
     FwdMaps m;
     if (!make_map(&m.x, p.x, p.x_b, p.x_t, p, kFwdTok) || !make_map(&m.f, p.f, p.f_b, p.f_t, p, kFwdTok) ||
         !make_map(&m.h, p.h, p.h_b, p.h_t, p, kFwdTok))
@@ -620,5 +688,22 @@ int tma_bwd_launch(const Gated& p, cudaStream_t stream) {
 }
 
 }  // namespace gated
+
+// Segments that fill two places on each SM, for sequences of which even clusters of eight CTAs would
+// leave SMs idle, and long enough to pay for reading the inputs twice. In segments / in
+// clusters, B 1, bfloat16 with an input gate: T 65536 D 64 35 / 158 us, T 65536 D 1024 160 / 208 us,
+// T 16384 D 512 28 / 51 us, T 8192 D 512 18 / 26 us, fp32 T 30000 D 512 77 / 74 us; T 5000 D 1152 21 / 18 us,
+// T 4096 D 64 11.6 / 11.4 us.
+int gated_segments(int64_t B, int64_t T, int64_t D, bool bf16) {
+    constexpr int64_t kTile = gated::kFwdWarps * gated::kFwdTok, kSlots = 2 * 152;
+    const int64_t groups = B * ((D + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32));
+    if (groups * gated::kMaxCluster >= 152 || T < 8192) return 1;
+    int64_t segments = kSlots / groups;
+    const int64_t most = T / kTile < 128 ? T / kTile : 128;
+    segments = segments < most ? segments : most;
+    const int64_t tokens = gated::segment_tokens(T, segments, kTile);
+    return (int)((T + tokens - 1) / tokens);
+}
+
 }  // namespace block
 }  // namespace ssdc

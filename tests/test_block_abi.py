@@ -193,14 +193,14 @@ def test_calls_check_their_tensors(lib):
         norm(torch.zeros(4, 16, dtype=torch.bfloat16), None, torch.zeros(15))
 
 
-@pytest.mark.parametrize("call,words", [(0, 21), (1, 17), (2, 30), (3, 16), (4, 16), (5, 12), (6, 15)])
+@pytest.mark.parametrize("call,words", [(0, 21), (1, 17), (2, 30), (3, 16), (4, 16), (5, 12), (6, 15), (7, 23)])
 def test_word_block_calls_refuse_what_the_calls_refuse(lib, call, words):
     none = (ctypes.c_int64 * words)()      # null addresses, zero sizes
     assert lib.ssd_block_call(call, none, None) == INVALID
     assert lib.ssd_block_call(call, None, None) == INVALID
 
 
-@pytest.mark.parametrize("call", [-1, 7, 1 << 20])
+@pytest.mark.parametrize("call", [-1, 8, 1 << 20])
 def test_word_block_of_no_call(lib, call):
     assert lib.ssd_block_call(call, (ctypes.c_int64 * 30)(), None) == INVALID
 
@@ -212,3 +212,18 @@ def test_word_block_of_no_call(lib, call):
 def test_scan_output_that_cuts_into_an_input(lib, dims, stride_b, stride_t, off):
     x = SEQ(at(1), stride_b, stride_t)
     assert fwd(lib, dims=dims, x=x, h=SEQ(at(1) + 2 * off, stride_b, stride_t)) == INVALID
+
+
+def test_scan_workspace_size_and_refusals(lib):
+    dims = lambda *a: block.ssd_gated_dims(*a)
+    size = lib.ssd_gated_scan_workspace_bytes
+    assert size(dims(0, 100, 64, 1)) == 0 and size(dims(1, 100, 64, 5)) == 0
+    assert size(dims(16, 65536, 1024, 1)) == 0 and size(dims(1, 1000, 64, 1)) == 0     # enough sequences; a short one
+    need = size(dims(1, 65536, 64, 1))
+    assert need > 0 and need % (64 * 8) == 0
+    d = dims(1, 65536, 64, 1)
+    for ws, n in ((at(10), need - 1), (at(10) + 8, need)):
+        assert lib.ssd_gated_scan_fwd_ws(SEQ(at(1)), SEQ(at(2)), SEQ(at(3)), at(4), None, d, SEQ(at(6)), at(7), None, at(9), ws, n,
+                                         None) == WORKSPACE
+    assert lib.ssd_gated_scan_fwd_ws(SEQ(at(1)), SEQ(at(2)), SEQ(at(3)), at(4), None, d, SEQ(at(6)), at(7), None, at(9), at(6) + 64, need,
+                                     None) == INVALID      # over h

@@ -789,3 +789,52 @@ def test_norm_in_place_of_rows_that_start_anywhere(D):
         assert lib.ssd_residual_norm_bwd(rows(a[0]), rows(a[1]), rows(r), w.data_ptr(), plan.rstd.data_ptr(), M, D, block.TYPE_BF16,
                                          rows(a[over]), dw1.data_ptr(), back.workspace.data_ptr(), nbytes, st) == 0
         assert torch.equal(a[over], dx) and torch.equal(dw1, dw)
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 8192, 33), (1, 8193, 64), (2, 9000, 100), (3, 9001, 96), (1, 20011, 520)])
+@pytest.mark.parametrize("dtype,gate,docs", [("bf16", True, True), ("fp32", False, False), ("fp32", True, True), ("bf16", False, False)])
+def test_scan_in_segments(B, T, D, dtype, gate, docs):
+    """Few long sequences, in segments, and the same without a workspace; h_last may be h0."""
+    D = -(-D // 8) * 8
+    x, f, i, h0, reset = scan_inputs(B, T, D, dtype, gate, docs, seed=T + D)
+    plan = block.GatedScan(B, T, D, dtype, input_gate=gate, keep_states=True)
+    assert plan.joints is not None
+    plan.joints.fill_(0xff)
+    want, want_last = scan_ref(x, f, i, h0, reset)
+    h, last = plan(x, f, i, h0=h0, reset=reset)
+    close(h, want, "h")
+    close(last, want_last, "h_last")
+    states = torch.cat([h0.double()[:, None], want[:, 63::64]], 1)[:, :plan.states.shape[1]]
+    close(plan.states, states, "states")
+    first, first_last = h.clone(), last.clone()
+    last.copy_(h0)
+    plan(x, f, i, h0=last, reset=reset)
+    assert torch.equal(plan.h, first) and torch.equal(last, first_last)
+    # without an initial state, and without a workspace
+    h, last = plan(x, f, i, reset=reset)
+    want, want_last = scan_ref(x, f, i, None, reset)
+    close(h, want, "h from zero")
+    lib, st = block.load(), torch.cuda.current_stream().cuda_stream
+    seq = lambda t: block.ssd_seq(None, 0, 0) if t is None else block.ssd_seq(t.data_ptr(), t.stride(0), t.stride(1))
+    other = torch.empty_like(h)
+    assert lib.ssd_gated_scan_fwd(seq(x), seq(f), seq(i), None, None if reset is None else reset.data_ptr(), plan.dims, seq(other),
+                                  last.data_ptr(), None, plan.workspace.data_ptr(), st) == 0
+    close(other, want, "h in one launch")
+    assert plan.status() == 0
+
+
+def test_scan_in_segments_stops_bad_values_at_a_reset():
+    """An infinity in a segment reaches the ones after it, up to a reset."""
+    T, D = 8192, 64
+    x, f, i, h0, _ = scan_inputs(1, T, D, "bf16", True, False, seed=3)
+    x[0, 1000] = float("inf")
+    f[0, :, 0] = 20.0        # a gate of nearly one carries it on
+    reset = torch.zeros(1, T, dtype=torch.uint8, device="cuda")
+    reset[0, 6000] = 1
+    plan = block.GatedScan(1, T, D)
+    assert plan.joints is not None
+    h, last = plan(x, f, i, h0=h0, reset=reset)
+    want, want_last = scan_ref(x, f, i, h0, reset)
+    assert bool(torch.isinf(h[0, 5999, 0])) and bool(torch.isfinite(h[0, 6000:]).all()) and bool(torch.isfinite(last).all())
+    close(h[:, 6000:], want[:, 6000:], "after the reset")
+    close(last, want_last, "h_last")
