@@ -592,11 +592,14 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
     leave(R, ok, p.status);
 }
 
-// Whether a map can describe an array, and the map.
+// Whether a map can describe an array, and the map. Rows are whole 16-byte units, not only their pitch: a
+// copy out of shared memory ends at such a unit, so that it would overwrite up to seven values behind a
+// row that ends inside one (seen with D 33 in rows of 40: the last seven were zeros), and a lane's
+// two bfloat16 channels are then always both there.
 bool make_map(CUtensorMap* m, const void* q, int64_t sb, int64_t st, const Gated& p, int rows) {
     const int64_t e = p.bf16 ? 2 : 4;
     if (p.B == 1) sb = st * p.T;  // not used
-    if (reinterpret_cast<uintptr_t>(q) % 16 || st * e % 16 || sb * e % 16 || st < p.D || sb < st) return false;
+    if (reinterpret_cast<uintptr_t>(q) % 16 || p.D * e % 16 || st * e % 16 || sb * e % 16 || st < p.D || sb < st) return false;
     return tc::encode_rows_3d(m, q, (int)e, p.D, p.T, p.B, st * e, sb * e, rows);
 }
 

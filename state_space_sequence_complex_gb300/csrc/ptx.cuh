@@ -294,7 +294,8 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_
         : "memory");
 }
 
-// 3-D tiled store shared -> global (bulk-group completion); elements outside are not written.
+// 3-D tiled store shared -> global (bulk-group completion); elements outside are not written, but
+// for those in the 16 bytes in which a row ends: rows have to be whole 16-byte units.
 __device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                      reinterpret_cast<uint64_t>(tmap)),
