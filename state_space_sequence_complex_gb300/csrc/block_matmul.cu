@@ -125,9 +125,11 @@ __device__ __forceinline__ uint32_t bf16_pair(float2 v) {
 // along, 93 us across (65 us with a scale for each 128 columns, along).
 
 // 128 bytes (64 bfloat16 or 32 fp32 values) of each of a warp's 32 rows to C from row m0 and
-// column n on, through the warp's staging rows.
+// column n on, through the warp's staging rows: piece j of the warp's part of a tile takes half
+// j & 1 of them. A tile's first piece waits until all copies before it have read their rows (the
+// tile before may have ended with either half), a later one until all but the last have.
 template <typename T, bool kAcross>
-__device__ __forceinline__ void store_piece(const Product& p, const CUtensorMap* map_c, char* stage, int half,
+__device__ __forceinline__ void store_piece(const Product& p, const CUtensorMap* map_c, char* stage, int j,
                                             const float2* v, int64_t m0, int64_t n, int lane) {
     constexpr bool kHalf = sizeof(T) == 2;
     constexpr int kPiece = 128 / sizeof(T);
@@ -140,9 +142,12 @@ __device__ __forceinline__ void store_piece(const Product& p, const CUtensorMap*
     if (p.tma_out) {
         // asynchronous: the warp goes on to the next tile while the rows are copied out; rows and
         // columns outside C are left out by the copy
-        if (lane == 0) ptx::bulk_wait_read<1>();  // of the two, the half copied out before the last
+        if (lane == 0) {
+            if (j == 0) ptx::bulk_wait_read<0>();
+            else ptx::bulk_wait_read<1>();
+        }
         __syncwarp();
-        char* to = stage + 4096 * half;  // (with the 128-byte swizzle of the tensor map)
+        char* to = stage + 4096 * (j & 1);  // (with the 128-byte swizzle of the tensor map)
         if constexpr (!kAcross) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
@@ -164,7 +169,7 @@ __device__ __forceinline__ void store_piece(const Product& p, const CUtensorMap*
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            ptx::tma_store_2d(map_c, stage + 4096 * half, (int)n, (int)m0);
+            ptx::tma_store_2d(map_c, to, (int)n, (int)m0);
             ptx::bulk_commit();
         }
         return;
@@ -503,7 +508,7 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
 #pragma unroll
             for (int j = 0; j < kCols / kPiece; ++j)
                 if (m0 < p.M && n0 + kPiece * j < p.N)
-                    store_piece<T, !kBlocks>(p, &map_c, stage, j & 1, acc + kPiece / 2 * j, m0, n0 + kPiece * j, lane);
+                    store_piece<T, !kBlocks>(p, &map_c, stage, j, acc + kPiece / 2 * j, m0, n0 + kPiece * j, lane);
         }
         if (lane == 0) ptx::bulk_wait_all();
     }

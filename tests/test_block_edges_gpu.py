@@ -95,3 +95,48 @@ def test_scan_of_a_product_with_an_odd_number_of_columns():
     close(h, want, "h")
     close(last, want_last, "h_last")
     assert bool((out[..., D:] == GUARD).all())
+
+
+# ---- a product's pairs of SMs with several tiles each, one after another
+
+
+def product_operands(M, N, K, b_scales, seed):
+    """Operands, their values in 64 bits, and the product and the product of the magnitudes."""
+    def operand(rows, scales, seed, std):
+        q, s = block.Fp8Quantize(rows, K, "fp32", scales=scales)(randn(rows, K, seed=seed, std=std))
+        by = s.t() if scales == "rows" else s.repeat_interleave(128, 0)[:rows]
+        return q, s, q.float().double() * by.repeat_interleave(128, 1)[:, :K].double()
+
+    a, a_s, av = operand(M, "rows", seed, 1.0)
+    b, b_s, bv = operand(N, b_scales, seed + 1, 0.1)
+    return (a, a_s, b, b_s), av @ bv.t(), av.abs() @ bv.abs().t()
+
+
+def check_every_value(c, ref, size):
+    """Each value by itself: e4m3 products are exact in fp32; a group's 128 are added with an error of at most 2^-23 of
+    their magnitudes each, then up to two groups: 2^-15 of the magnitudes' sum covers them; bfloat16 rounds once."""
+    err = (c.double() - ref).abs()
+    assert bool((err <= 2.0 ** -15 * size + (2.0 ** -8 * ref.abs() if c.dtype is torch.bfloat16 else 0)).all())
+
+
+# narrow tiles (the first six) and wide ones; the last tile's columns end before, at and behind a multiple of 64 and 128
+ROUNDS = [(32768, 128, 64), (32768, 320, 200), (32768, 272, 256), (50000, 70, 128), (12000, 1100, 130), (32768, 96, 200),
+          (20000, 5136, 128), (9728, 2048, 130), (40000, 200, 100), (30000, 1056, 256), (33000, 448, 96), (20000, 2080, 200)]
+
+
+@pytest.mark.parametrize("M,N,K", ROUNDS)
+@pytest.mark.parametrize("b_scales", ["blocks", "rows"])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_product_in_several_rounds(M, N, K, b_scales, out):
+    """All of C where a pair stores tiles one after another, with little work between two stores, bit for bit again."""
+    args, ref, size = product_operands(M, N, K, b_scales, seed=M % 97)
+    plan = block.Fp8Product(M, N, K, out=out, b_scales=b_scales)
+    c = plan(*args)
+    check_every_value(c, ref, size)
+    first = c.clone()
+    pad = torch.empty(1 << 22, device="cuda")
+    for r in range(8):
+        pad[: (r + 1) * 400000].fill_(float(r))      # (shifts the timing)
+        c.fill_(float("nan"))
+        assert torch.equal(plan(*args), first)
+    assert plan.status() == 0
