@@ -47,6 +47,7 @@ struct Product {
     int whole;       // tiles that pairs take whole, in turn; the others' groups are dealt out evenly
     int* flags;      // a pair's warps' marks that their sums of a tile's end are in `sums`
     float4* sums;
+    int64_t copied;  // (tma_out) the columns that are copied out, whole 16-byte units
 };
 
 constexpr int kFlags = 16;  // of a pair: 8 adding warps of two CTAs
@@ -118,6 +119,9 @@ __device__ __forceinline__ uint32_t bf16_pair(float2 v) {
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 
+// kRest: C's columns are copied out and end inside a 16-byte unit. (An instance of its own: with the test
+// for it in the other, 32768 x 5120 x 1024 bfloat16 took 168 us for 163.)
+
 // Which of a warp's 32 x 16 sums a lane holds. Along: its row's, acc[8 j + e] columns 16 j + 2 e and
 // the next. Across (as the tensor memory gives 8 x 8 blocks to a warp): acc[8 j + 4 i + 2 c + h] is
 // row 16 i + 8 h + lane / 4, columns 16 j + 8 c + 2 (lane % 4) and the next. Where every column has
@@ -128,7 +132,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float2 v) {
 // column n on, through the warp's staging rows: piece j of the warp's part of a tile takes half
 // j & 1 of them. A tile's first piece waits until all copies before it have read their rows (the
 // tile before may have ended with either half), a later one until all but the last have.
-template <typename T, bool kAcross>
+template <typename T, bool kAcross, bool kRest>
 __device__ __forceinline__ void store_piece(const Product& p, const CUtensorMap* map_c, char* stage, int j,
                                             const float2* v, int64_t m0, int64_t n, int lane) {
     constexpr bool kHalf = sizeof(T) == 2;
@@ -140,8 +144,8 @@ __device__ __forceinline__ void store_piece(const Product& p, const CUtensorMap*
     // across: the two values of block c8 (of 8 columns), row 8 k + lane / 4
     auto pair_of = [&](int c8, int k) { return v[8 * (c8 / 2) + 4 * (k / 2) + 2 * (c8 % 2) + k % 2]; };
     if (p.tma_out) {
-        // asynchronous: the warp goes on to the next tile while the rows are copied out; rows and
-        // columns outside C are left out by the copy
+        // asynchronous: the warp goes on to the next tile while the rows are copied out; rows outside C
+        // are left out by the copy, and columns from C's last whole 16-byte unit on
         if (lane == 0) {
             if (j == 0) ptx::bulk_wait_read<0>();
             else ptx::bulk_wait_read<1>();
@@ -168,7 +172,7 @@ __device__ __forceinline__ void store_piece(const Product& p, const CUtensorMap*
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0 && (!kRest || n < p.copied)) {
             ptx::tma_store_2d(map_c, to, (int)n, (int)m0);
             ptx::bulk_commit();
         }
@@ -244,7 +248,23 @@ __device__ __forceinline__ void store_piece(const Product& p, const CUtensorMap*
     }
 }
 
-template <int BN, bool kBlocks, typename T>
+// A copy writes whole 16-byte units: where C's columns end inside one it would overwrite what is behind
+// them. The columns that are no whole unit (from p.copied on) are stored one by one, a row a lane, from
+// the staging rows of a warp's part of a tile, columns n0 on, after its pieces.
+template <typename T>
+__device__ __forceinline__ void store_rest(const Product& p, const char* stage, int64_t m0, int64_t n0, int lane) {
+    constexpr int kPiece = 128 / sizeof(T);
+    if (m0 + lane >= p.M) return;
+    const int first = (int)(p.copied - n0), piece = first / kPiece;
+    const char* row = stage + 4096 * (piece & 1) + lane * 128;
+    T* c = static_cast<T*>(p.c) + (m0 + lane) * p.c_ld + p.copied;
+    for (int k = 0; k < (int)(p.N - p.copied); ++k) {
+        const int at = (first - piece * kPiece + k) * (int)sizeof(T);
+        c[k] = *reinterpret_cast<const T*>(row + (((at / 16) ^ (lane & 7)) << 4) + at % 16);
+    }
+}
+
+template <int BN, bool kBlocks, typename T, bool kRest>
 __global__ void __launch_bounds__(Shape<BN>::kThreads, 1)
 product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
              const __grid_constant__ CUtensorMap map_c, const Product p) {
@@ -508,7 +528,10 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
 #pragma unroll
             for (int j = 0; j < kCols / kPiece; ++j)
                 if (m0 < p.M && n0 + kPiece * j < p.N)
-                    store_piece<T, !kBlocks>(p, &map_c, stage, j, acc + kPiece / 2 * j, m0, n0 + kPiece * j, lane);
+                    store_piece<T, !kBlocks, kRest>(p, &map_c, stage, j, acc + kPiece / 2 * j, m0, n0 + kPiece * j, lane);
+            if constexpr (kRest) {
+                if (n0 <= p.copied && p.copied < n0 + kCols) store_rest<T>(p, stage, m0, n0, lane);
+            }
         }
         if (lane == 0) ptx::bulk_wait_all();
     }
@@ -567,17 +590,20 @@ int launch_pair(const Matmul& p, Product q, const Plan& plan, cudaStream_t strea
     if (!tc::encode_tiled_2d(&ma, p.a, 1, p.K, p.M, p.a_ld, 128) || !tc::encode_tiled_2d(&mb, p.b, 1, p.K, p.N, p.b_ld, BN / 2))
         return SSDC_ERR_CUDA;
     if (q.tma_out) {
-        if (!tc::encode_tiled_2d(&mc, p.c, sizeof(T), p.N, p.M, p.c_ld * (int64_t)sizeof(T), 32)) return SSDC_ERR_CUDA;
+        if (!tc::encode_tiled_2d(&mc, p.c, sizeof(T), q.copied, p.M, p.c_ld * (int64_t)sizeof(T), 32)) return SSDC_ERR_CUDA;
     } else {
         mc = ma;  // not used
     }
     q.n_tiles = (int)((p.N + BN - 1) / BN);
     q.whole = plan.whole;
     const int pairs = plan.pairs;
-    auto* k = product_pair<BN, kBlocks, T>;
-    static std::atomic<uint64_t> allowed;
-    if (allow_smem(k, (int)S::kBytes, allowed) != cudaSuccess) return SSDC_ERR_CUDA;
-    return launch_clusters(k, pairs, 2, plan.split, S::kThreads, S::kBytes, stream, ma, mb, mc, q);
+    auto launch = [&](auto* k, std::atomic<uint64_t>& allowed) {
+        if (allow_smem(k, (int)S::kBytes, allowed) != cudaSuccess) return (int)SSDC_ERR_CUDA;
+        return launch_clusters(k, pairs, 2, plan.split, S::kThreads, S::kBytes, stream, ma, mb, mc, q);
+    };
+    static std::atomic<uint64_t> allowed, allowed_rest;
+    if (q.tma_out && q.copied < p.N) return launch(product_pair<BN, kBlocks, T, true>, allowed_rest);
+    return launch(product_pair<BN, kBlocks, T, false>, allowed);
 }
 
 template <int BN>
@@ -611,7 +637,8 @@ int matmul_launch(const Matmul& p, cudaStream_t stream) {
     q.m_tiles = (int)((p.M + 255) / 256);
     q.c = p.c;
     const size_t e = p.out_bf16 ? 2 : 4;
-    q.tma_out = (reinterpret_cast<uintptr_t>(p.c) | (uintptr_t)(p.c_ld * e)) % 16 == 0;
+    q.copied = p.N / (int64_t)(16 / e) * (int64_t)(16 / e);
+    q.tma_out = (reinterpret_cast<uintptr_t>(p.c) | (uintptr_t)(p.c_ld * e)) % 16 == 0 && q.copied > 0;
     q.status = p.status;
     char* ws = reinterpret_cast<char*>(p.status);
     q.flags = reinterpret_cast<int*>(ws + 256);

@@ -304,7 +304,7 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, 
 }
 
 // 2-D tiled store shared -> global (bulk-group completion); elements outside the tensor are
-// not written.
+// not written, but for those in the 16 bytes in which a row ends.
 __device__ __forceinline__ void tma_store_2d(const void* tmap, const void* src, int c0, int c1) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                      reinterpret_cast<uint64_t>(tmap)),

@@ -140,3 +140,25 @@ def test_product_in_several_rounds(M, N, K, b_scales, out):
         c.fill_(float("nan"))
         assert torch.equal(plan(*args), first)
     assert plan.status() == 0
+
+
+@pytest.mark.parametrize("M,N,pitch", [(100, 257, 264), (100, 130, 192), (300, 33, 40), (300, 1, 8), (40, 70, 72), (8, 45, 48),
+                                       (30000, 132, 136), (20000, 330, 336), (30000, 289, 296), (1021, 1537, 1544)])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("b_scales", ["blocks", "rows"])
+def test_product_columns_that_end_inside_a_unit(M, N, pitch, out, b_scales):
+    """C as columns of wider rows that start at 16 bytes: right, and nothing is written behind its columns."""
+    K = 200
+    (a, a_s, b, b_s), ref, size = product_operands(M, N, K, b_scales, seed=N)
+    lib, st = block.load(), torch.cuda.current_stream().cuda_stream
+    rows = lambda t: block.ssd_rows(t.data_ptr(), t.stride(0))
+    plan = block.Fp8Product(M, N, K, out=out, b_scales=b_scales)
+    store = torch.full((M, pitch), GUARD, dtype=DT[out], device="cuda")
+    c = store[:, :N]
+    for _ in range(3):
+        assert lib.ssd_fp8_matmul(rows(a), a_s.data_ptr(), rows(b), b_s.data_ptr(), plan.b_scales, M, N, K, plan.type, rows(c),
+                                  plan.workspace.data_ptr(), plan.workspace.numel(), st) == 0
+        check_every_value(c, ref, size)
+        assert bool((store[:, N:] == GUARD).all())
+        c.fill_(float("nan"))
+    assert plan.status() == 0
