@@ -510,6 +510,7 @@ product_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 int* flag = p.flags + q * kFlags + flag_at;
                 ok = __all_sync(0xffffffffu, lane != 0 || ptx::wait_flag(flag, 1, kWaitNs));
                 if (!ok) break;
+                __syncwarp();  // (lane 0's acquire is ordered before the other lanes' reads)
                 const float4* from = p.sums + q * sums_pair + sums_at;
 #pragma unroll
                 for (int j = 0; j < kCols / 4; ++j) {

@@ -162,3 +162,28 @@ def test_product_columns_that_end_inside_a_unit(M, N, pitch, out, b_scales):
         assert bool((store[:, N:] == GUARD).all())
         c.fill_(float("nan"))
     assert plan.status() == 0
+
+
+@pytest.mark.parametrize("M,N,K,shared", [(300, 999, 8192, False), (130, 100, 16000, False), (5136, 1024, 4096, True), (2300, 2100, 3300, True),
+                                          (1024, 1024, 9000, False), (1024, 1024, 32768, True), (5136, 4096, 4096, True)])
+@pytest.mark.parametrize("b_scales", ["blocks", "rows"])
+def test_product_of_shared_tiles_repeats(M, N, K, shared, b_scales):
+    """Pairs that add up one tile pass their sums through memory: the same bits every time, whatever runs around."""
+    gen = torch.Generator().manual_seed(K)
+    operand = lambda r: torch.randint(0, 0x78, (r, block.fp8_pitch(K)), dtype=torch.uint8, generator=gen).cuda().view(torch.float8_e4m3fn)[:, :K]
+    KB = block.fp8_groups(K)
+    scale = lambda *s: (torch.rand(*s, generator=gen) + 0.5).cuda()
+    a, b, a_s = operand(M), operand(N), scale(KB, M)
+    b_s = scale(block.fp8_groups(N), KB) if b_scales == "blocks" else scale(KB, N)
+    plan = block.Fp8Product(M, N, K, out="fp32", b_scales=b_scales)
+    assert (plan.workspace.numel() > 16384) == shared      # (room for the sums)
+    first = plan(a, a_s, b, b_s).clone()
+    value = lambda q, s: q.double() * s.double().repeat_interleave(128, 1)[:, :K]
+    ref = value(a[:50], a_s.t()[:50]) @ value(b, b_s.repeat_interleave(128, 0)[:N] if b_scales == "blocks" else b_s.t()).t()
+    close(first[:50], ref, "C")
+    pad = torch.empty(1 << 24, device="cuda")
+    for r in range(20):
+        pad[: 1 + (r * 7919 * 1000) % (1 << 24)].fill_(float(r))
+        plan.c.fill_(float("nan"))
+        assert torch.equal(plan(a, a_s, b, b_s), first)
+    assert plan.status() == 0
