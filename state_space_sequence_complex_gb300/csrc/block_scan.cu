@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
     // (the warp's index from a shuffle: what depends on it alone is then computed once a warp)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
-    totals_init(totals, R);
+    const bool in_place = R > 1 && p.h0 == p.h_last;
+    totals_init(totals, in_place);
     const int64_t groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
     const int b = (int)(group / groups), d = (int)(group % groups) * 32 * kVec + lane * kVec;
     const bool in_d = d < p.D;
@@ -143,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
         }
     };
     load(rank);
+    if (in_place) totals_arrive();
     bool ok = true;
     int64_t round = 0;
     for (int64_t tile = rank; tile - rank < tiles; tile += R, ++round) {
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, kVec == 2 ? 2 : 3) gated_fwd(const G
                 preA[c] = both<kReset>(preA[c], o.A[c]);
             }
         }
-        if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        if (round == 0) totals_wait();
         if (warp == kWarps - 1) {
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {
@@ -273,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
     // (the warp's index from a shuffle: what depends on it alone is then computed once a warp)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = ptx::cluster_ctarank(), R = ptx::cluster_nctarank();
-    totals_init(totals, R);
+    const bool in_place = R > 1 && p.dh0 && p.dh0 == p.dh_last;
+    totals_init(totals, in_place);
     const int64_t groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
     const int b = (int)(group / groups), d0 = (int)(group % groups) * 32 * kVec, d = d0 + lane * kVec;
     const bool in_d = d < p.D;
@@ -347,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
                 if (sizeof(T) * kVec * 32 > 128 && d0 + 32 < p.D) ptx::prefetch_l2(q + 32);
             }
         }
+        if (in_place && round == 0) totals_arrive();
         const uint32_t stop = kReset ? marked(first) : 0;
         const bool plain = n == kTok && (!kReset || stop == 0);
         // a token's factor C, its input's factor u and both factors' derivatives (ca; cu with x
@@ -426,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd(const Gated p) {
                 sufA[c] = both<kReset>(sufA[c], o.A[c]);
             }
         }
-        if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        if (round == 0) totals_wait();
         if (warp == 0) {
 #pragma unroll
             for (int c = 0; c < kVec; ++c) {

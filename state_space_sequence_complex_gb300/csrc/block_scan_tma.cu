@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
         for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s][warp], 1);
         ptx::fence_mbar_init();
     }
-    if (R > 1) totals_init(totals, R);
+    const bool in_place = R > 1 && p.h0 == p.h_last;
+    if (R > 1) totals_init(totals, in_place);
     const int groups = (p.D + 32 * kVec - 1) / (32 * kVec);
     const int mine_of = p.segments - (kTotals ? 1 : 0);  // segments of a sequence in this launch
     const int group = blockIdx.x / R / mine_of, segment = blockIdx.x / R % mine_of;
@@ -166,6 +167,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
     const int rounds = (tiles + (int)R - 1) / (int)R;
     const int t_first = t_begin + (int)rank * kTile + warp * kTok;
     uint32_t mark_next = kReset ? mark(reset, t_first, min(kTok, T_ - t_first), lane) : 0;
+    if (in_place) totals_arrive();
     for (int round = 0; round < rounds; ++round) {
         const int parity = round & 1, t0 = t_begin + (round * (int)R + (int)rank) * kTile + warp * kTok, n = min(kTok, T_ - t0);
         if (lane == 0 && round + 1 < rounds) {
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 16 / kFwdWarps) gated_fwd_tma(
         else join(std::true_type());
         float in[kVec];
         if (R > 1) {
-            if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            if (round == 0) totals_wait();
             if (warp == kWarps - 1) send_total<kVec>(totals, round, rank, R, lane, allA, allH);
             receive_totals<kVec, kReset>(totals, round, rank, R, lane, carry, in, ok);
         } else {
@@ -343,7 +345,8 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
         for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s][warp], 1);
         ptx::fence_mbar_init();
     }
-    if (R > 1) totals_init(totals, R);
+    const bool in_place = R > 1 && p.dh0 && p.dh0 == p.dh_last;
+    if (R > 1) totals_init(totals, in_place);
     const int groups = (p.D + 32 * kVec - 1) / (32 * kVec), group = blockIdx.x / R;
     const int b = group / groups, d0 = group % groups * 32 * kVec, d = d0 + lane * kVec;
     const bool in_d = d < p.D;
@@ -383,6 +386,7 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
     if (lane == 0) fetch(0);
     load_ahead(0);
     if (kReset) mark_next = mark(reset, first(0), has(first(0)) ? min(kTok, T_ - first(0)) : 0, lane);
+    if (in_place) totals_arrive();
     bool ok = true;
     const int rounds = (tiles + (int)R - 1) / (int)R;
     for (int round = 0; round < rounds; ++round) {
@@ -522,7 +526,7 @@ __global__ void __launch_bounds__(32 * bwd_warps<T>(), 2) gated_bwd_tma(const __
         if (whole) join(std::false_type());
         else join(std::true_type());
         if (R > 1) {
-            if (round == 0) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            if (round == 0) totals_wait();
             if (warp == 0) send_total<kVec>(totals, round, rank, R, lane, allA, allG);
         }
         // token by token: what enters a token (nothing at a reset) makes its gate's gradient

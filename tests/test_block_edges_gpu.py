@@ -187,3 +187,31 @@ def test_product_of_shared_tiles_repeats(M, N, K, shared, b_scales):
         plan.c.fill_(float("nan"))
         assert torch.equal(plan(a, a_s, b, b_s), first)
     assert plan.status() == 0
+
+
+# ---- a state updated in place by a cluster
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 512, 64), (2, 300, 128), (1, 1024, 4096), (4, 100, 35), (2, 2048, 96), (1, 400, 1023)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_scan_in_place_of_its_state(B, T, D, dtype):
+    """h_last over h0 and dh0 over dh_last, in one round of a cluster's tiles and in several: as into arrays of their own."""
+    lib, st = block.load(), torch.cuda.current_stream().cuda_stream
+    x, f, i, h0, _ = scan_inputs(B, T, D, dtype, True, False, seed=T + D)
+    dh, dh_last = randn(B, T, D, seed=9, dtype=DT[dtype]), randn(B, D, seed=10)
+    plan = block.GatedScan(B, T, D, dtype, keep_states=True)
+    back = block.GatedScanBackward(B, T, D, dtype)
+    h, last = (t.clone() for t in plan(x, f, i, h0=h0))
+    g = {k: v.clone() for k, v in back(x, f, i, plan.states, dh, dh_last=dh_last).items()}
+    close(last, scan_ref(x, f, i, h0, None)[1], "h_last")
+    dims = block.ssd_gated_dims(B, T, D, block._TYPES[dtype])
+    dx, df, di = (torch.empty_like(x) for _ in range(3))
+    for _ in range(10):
+        plan.h_last.copy_(h0)
+        again = plan(x, f, i, h0=plan.h_last)
+        assert torch.equal(again[0], h) and torch.equal(again[1], last)
+        k = dh_last.clone()
+        assert lib.ssd_gated_scan_bwd(seq(x), seq(f), seq(i), plan.states.data_ptr(), None, seq(dh), k.data_ptr(), dims, seq(dx),
+                                      seq(df), seq(di), k.data_ptr(), None, st) == 0
+        assert torch.equal(dx, g["dx"]) and torch.equal(df, g["df"]) and torch.equal(di, g["di"]) and torch.equal(k, g["dh0"])
+    assert plan.status() == 0 and back.status() == 0
