@@ -5,7 +5,7 @@ runs in libssdc.so's kernels and there is no fallback.
 The classes hold the outputs and workspaces of one problem size, so that a call
 allocates nothing and the next call overwrites the last one's outputs.
 ``gated_scan``, ``residual_norm`` and ``fp8_linear`` are differentiable
-(``torch.autograd``) and allocate their outputs.
+(``torch.autograd``, first derivatives) and allocate their outputs.
 
 A plan's tensors belong to the device it was made for; a call runs on the current
 stream, or on ``stream``. Tensors made on another stream have to be ordered with
@@ -25,6 +25,7 @@ import ctypes
 import struct
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ssdc
 
@@ -505,7 +506,7 @@ class Fp8Linear:
         return dx, self.dw(qt, st, self.x_q.qt, self.x_q.scale_t, stream)
 
 
-# ---- differentiable forms
+# ---- differentiable forms (once: a gradient of a gradient is an error)
 
 
 class _GatedScan(torch.autograd.Function):
@@ -519,6 +520,7 @@ class _GatedScan(torch.autograd.Function):
         return h, last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh, dh_last):
         x, f, i, states, reset = ctx.saved_tensors
         dh = torch.zeros_like(x) if dh is None else _unit_last(dh)
@@ -554,6 +556,7 @@ class _ResidualNorm(torch.autograd.Function):
         return r, y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dr, dy):
         r, w, rstd = ctx.saved_tensors
         dy = torch.zeros_like(r) if dy is None else _unit_last(dy)
@@ -578,6 +581,7 @@ class _Fp8Linear(torch.autograd.Function):
         return Fp8Product(M, N, K, name, device=x.device)(x_q, x_s, w_q, w_s)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x_qt, x_st, w_qt, w_st = ctx.saved_tensors
         M, N, K, name = ctx.sizes

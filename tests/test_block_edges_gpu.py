@@ -215,3 +215,36 @@ def test_scan_in_place_of_its_state(B, T, D, dtype):
                                       seq(df), seq(di), k.data_ptr(), None, st) == 0
         assert torch.equal(dx, g["dx"]) and torch.equal(df, g["df"]) and torch.equal(di, g["di"]) and torch.equal(k, g["dh0"])
     assert plan.status() == 0 and back.status() == 0
+
+
+# ---- the differentiable forms
+
+
+def scan_gradients():
+    x, f, i = (randn(2, 70, 24, seed=k).requires_grad_() for k in range(3))
+    h0 = randn(2, 24, seed=3).requires_grad_()
+    h, last = block.gated_scan(x, f, i, h0)
+    return (h.square().sum() + last.sum()), (x, f, i, h0)
+
+
+def norm_gradients():
+    x, res, w = randn(5, 40, seed=1).requires_grad_(), randn(5, 40, seed=2).requires_grad_(), randn(40, seed=3).requires_grad_()
+    r, y = block.residual_norm(x, res, w)
+    return r.sum() + y.square().sum(), (x, res, w)
+
+
+def linear_gradients():
+    x, w = randn(40, 64, seed=1).requires_grad_(), randn(24, 64, seed=2).requires_grad_()
+    return block.fp8_linear(x, w).square().sum(), (x, w)
+
+
+@pytest.mark.parametrize("make", [scan_gradients, norm_gradients, linear_gradients])
+def test_second_derivatives_are_refused(make):
+    """A gradient of a gradient raises: it would have no part that comes through the operator."""
+    loss, t = make()
+    first = torch.autograd.grad(loss, t, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        sum(g.square().sum() for g in first).backward()
+    loss, t = make()
+    for a, b in zip(torch.autograd.grad(loss, t), first):
+        assert torch.equal(a, b.detach())
