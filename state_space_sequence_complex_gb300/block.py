@@ -7,8 +7,8 @@ allocates nothing and the next call overwrites the last one's outputs.
 ``gated_scan``, ``residual_norm`` and ``fp8_linear`` are differentiable
 (``torch.autograd``, first derivatives) and allocate their outputs.
 
-A plan's tensors belong to the device it was made for; a call runs on the current
-stream, or on ``stream``. Tensors made on another stream have to be ordered with
+A plan's tensors belong to the device it was made for; a call runs there, on that
+device's current stream or on ``stream``, whichever device is current. Tensors made on another stream have to be ordered with
 it by the caller, as for any kernel.
 
     from state_space_sequence_complex_gb300 import block
@@ -152,16 +152,21 @@ def _seq(name, t, like):
 class _Call:
     """One of the library's calls with its arguments as a block of words (``ssd_block_call``)."""
 
-    __slots__ = ("name", "number", "fn", "pack", "block", "at", "index")
+    __slots__ = ("name", "number", "fn", "pack", "block", "at", "index", "several")
 
     def __init__(self, name, number, words, index):
         self.name, self.number, self.index = name, number, index
+        self.several = index >= 0 and torch.cuda.device_count() > 1
         self.fn = load().ssd_block_call
         self.block = ctypes.create_string_buffer(8 * words)
         self.at = ctypes.addressof(self.block)
         self.pack = struct.Struct(f"{words}q").pack_into
 
     def __call__(self, stream, *words):
+        # the library launches on the current device: make it the plan's, whose addresses and stream these are
+        if self.several and torch._C._cuda_getDevice() != self.index:
+            with torch.cuda.device(self.index):
+                return self(stream, *words)
         self.pack(self.block, 0, *words)
         if stream is not None:
             stream = stream.cuda_stream
@@ -181,6 +186,13 @@ def _device(device):
     if device.type == "cuda" and device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     return device
+
+
+def _status(plan, stream):
+    if plan.device.type == "cpu":
+        return ssdc.ssd_complex_status(plan.workspace, stream)
+    with torch.cuda.device(plan.device):
+        return ssdc.ssd_complex_status(plan.workspace, stream)
 
 
 def _raise(rc, what):
@@ -252,7 +264,7 @@ class GatedScan:
         return h, self.h_last
 
     def status(self, stream=None) -> int:
-        return ssdc.ssd_complex_status(self.workspace, stream)
+        return _status(self, stream)
 
 
 class GatedScanBackward:
@@ -294,7 +306,7 @@ class GatedScanBackward:
         return dict(self.grads)
 
     def status(self, stream=None) -> int:
-        return ssdc.ssd_complex_status(self.workspace, stream)
+        return _status(self, stream)
 
 
 class GatedScanStep:
@@ -477,7 +489,7 @@ class Fp8Product:
         return self.c
 
     def status(self, stream=None) -> int:
-        return ssdc.ssd_complex_status(self.workspace, stream)
+        return _status(self, stream)
 
 
 class Fp8Linear:

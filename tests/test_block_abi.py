@@ -227,3 +227,57 @@ def test_scan_workspace_size_and_refusals(lib):
                                          None) == WORKSPACE
     assert lib.ssd_gated_scan_fwd_ws(SEQ(at(1)), SEQ(at(2)), SEQ(at(3)), at(4), None, d, SEQ(at(6)), at(7), None, at(9), at(6) + 64, need,
                                      None) == INVALID      # over h
+
+
+class FakeDevices:
+    """Stands for the CUDA devices: which one is current, and where each call was launched."""
+
+    def __init__(self, monkeypatch, current):
+        import torch
+        self.current, self.calls = current, []
+        fake = self
+
+        class device:
+            def __init__(self, index):
+                self.index = index if isinstance(index, int) else index.index
+
+            def __enter__(self):
+                self.before, fake.current = fake.current, self.index
+
+            def __exit__(self, *_):
+                fake.current = self.before
+
+        monkeypatch.setattr(torch.cuda, "device", device)
+        monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: fake.current, raising=False)
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + index, raising=False)
+
+    def launch(self, number, words, stream):
+        self.calls.append((self.current, number, stream))
+        return 0
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_a_plan_is_launched_on_its_own_device(lib, monkeypatch, current):
+    """The library launches on the current device: it is the plan's around a call, and the caller's again behind it."""
+    fake = FakeDevices(monkeypatch, current)
+    call = block._Call("ssd_residual_norm_fwd", 3, 16, 1)
+    call.fn = fake.launch
+    call(None, *range(16))
+
+    class Stream:
+        cuda_stream = 77
+    call(Stream, *range(16))
+    assert fake.calls == [(1, 3, 1001), (1, 3, 77)]
+    assert fake.current == current
+
+
+def test_the_status_is_read_on_the_plan_s_device(monkeypatch):
+    import torch
+    fake = FakeDevices(monkeypatch, 0)
+
+    class Plan:
+        device, workspace = torch.device("cuda", 1), object()
+    monkeypatch.setattr(ssdc, "ssd_complex_status", lambda workspace, stream: (fake.current, workspace, stream))
+    assert block._status(Plan, None) == (1, Plan.workspace, None)
+    assert fake.current == 0
