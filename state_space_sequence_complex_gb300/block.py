@@ -3,7 +3,8 @@ residual norm, 8-bit product. Argument checks and marshalling only; every step
 runs in libssdc.so's kernels and there is no fallback.
 
 The classes hold the outputs and workspaces of one problem size, so that a call
-allocates nothing and the next call overwrites the last one's outputs.
+allocates nothing and the next call overwrites the last one's outputs: threads that
+call at the same time need a plan each.
 ``gated_scan``, ``residual_norm`` and ``fp8_linear`` are differentiable
 (``torch.autograd``, first derivatives) and allocate their outputs.
 
@@ -150,29 +151,27 @@ def _seq(name, t, like):
 
 
 class _Call:
-    """One of the library's calls with its arguments as a block of words (``ssd_block_call``)."""
+    """One of the library's calls with its arguments as a block of words (``ssd_block_call``), one of its own for
+    each call: the interpreter's lock is given up around the library."""
 
-    __slots__ = ("name", "number", "fn", "pack", "block", "at", "index", "several")
+    __slots__ = ("name", "number", "fn", "pack", "index", "several")
 
     def __init__(self, name, number, words, index):
         self.name, self.number, self.index = name, number, index
         self.several = index >= 0 and torch.cuda.device_count() > 1
         self.fn = load().ssd_block_call
-        self.block = ctypes.create_string_buffer(8 * words)
-        self.at = ctypes.addressof(self.block)
-        self.pack = struct.Struct(f"{words}q").pack_into
+        self.pack = struct.Struct(f"{words}q").pack
 
     def __call__(self, stream, *words):
         # the library launches on the current device: make it the plan's, whose addresses and stream these are
         if self.several and torch._C._cuda_getDevice() != self.index:
             with torch.cuda.device(self.index):
                 return self(stream, *words)
-        self.pack(self.block, 0, *words)
         if stream is not None:
             stream = stream.cuda_stream
         elif self.index >= 0:
             stream = torch._C._cuda_getCurrentRawStream(self.index)
-        rc = self.fn(self.number, self.at, stream)
+        rc = self.fn(self.number, self.pack(*words), stream)
         if rc:
             _raise(rc, self.name)
 

@@ -4,6 +4,7 @@ GPU. Every call here fails a host check, so the addresses are never used."""
 import ctypes
 import os
 import re
+import struct
 
 import pytest
 
@@ -281,3 +282,22 @@ def test_the_status_is_read_on_the_plan_s_device(monkeypatch):
     monkeypatch.setattr(ssdc, "ssd_complex_status", lambda workspace, stream: (fake.current, workspace, stream))
     assert block._status(Plan, None) == (1, Plan.workspace, None)
     assert fake.current == 0
+
+
+def test_a_call_keeps_its_own_words(lib):
+    """The library is called without the interpreter's lock: another thread's call on the same plan, here one from
+    inside, must not change the words that it reads."""
+    call = block._Call("ssd_residual_norm_fwd", 3, 16, -1)
+    seen = []
+
+    def library(number, words, stream):
+        if not seen:
+            seen.append(None)
+            call(None, *range(100, 116))
+        words = words if isinstance(words, bytes) else ctypes.string_at(words, 8 * 16)
+        seen.append(struct.unpack("16q", words))
+        return 0
+
+    call.fn = library
+    call(None, *range(16))
+    assert seen[1:] == [tuple(range(100, 116)), tuple(range(16))]
