@@ -13,7 +13,8 @@
  * Conventions are those of ssdc.h: status codes, no aborts, argument errors
  * found on the host before anything is enqueued, the caller owns every buffer,
  * work is enqueued on `stream`. All pointers are device pointers, aligned to
- * their element (the state, scale and weight arrays are float). Types:
+ * their element (the state, scale and weight arrays are float). A stride that is
+ * never taken (of a single row, token or batch row) may be anything. Types:
  */
 #ifndef SSDC_BLOCK_H
 #define SSDC_BLOCK_H

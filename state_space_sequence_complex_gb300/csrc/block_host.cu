@@ -52,10 +52,13 @@ struct Array {
     }
 };
 
+// A stride that is never taken may be anything (the row stride of a single row): it counts as zero.
+int64_t taken(int64_t stride, int64_t count) { return count > 1 ? stride : 0; }
+
 Array seq(const void* p, int64_t sb, int64_t st, const ssd_gated_dims& d) {
-    return Array{p, d.B, d.T, d.D, sb, st, type_bytes(d.type)};
+    return Array{p, d.B, d.T, d.D, taken(sb, d.B), taken(st, d.T), type_bytes(d.type)};
 }
-Array rows(const void* p, int64_t ld, int64_t M, int64_t D, size_t elem) { return Array{p, 1, M, D, 0, ld, elem}; }
+Array rows(const void* p, int64_t ld, int64_t M, int64_t D, size_t elem) { return Array{p, 1, M, D, 0, taken(ld, M), elem}; }
 Array dense(const void* p, int64_t n, size_t elem = 4) { return Array{p, 1, 1, n, 0, 0, elem}; }
 
 // Whether two arrays may share a byte. Arrays whose spans meet are still apart where they
@@ -164,15 +167,15 @@ int done(int launches) {
 // The kernels step from token to token in 32 bits.
 int check_token_strides(const ssd_gated_dims& d, std::initializer_list<int64_t> strides) {
     for (int64_t s : strides)
-        if (s >= (int64_t(1) << 31) / (int64_t)type_bytes(d.type)) return SSDC_ERR_UNSUPPORTED;
+        if (taken(s, d.T) >= (int64_t(1) << 31) / (int64_t)type_bytes(d.type)) return SSDC_ERR_UNSUPPORTED;
     return SSDC_OK;
 }
 
 Gated gated_problem(const ssd_seq_in& x, const ssd_seq_in& f, const ssd_seq_in& i, const ssd_gated_dims& d) {
     Gated p = {};
-    p.x = x.p; p.x_b = x.stride_b; p.x_t = x.stride_t;
-    p.f = f.p; p.f_b = f.stride_b; p.f_t = f.stride_t;
-    p.i = i.p; p.i_b = i.stride_b; p.i_t = i.stride_t;
+    p.x = x.p; p.x_b = taken(x.stride_b, d.B); p.x_t = taken(x.stride_t, d.T);
+    p.f = f.p; p.f_b = taken(f.stride_b, d.B); p.f_t = taken(f.stride_t, d.T);
+    p.i = i.p; p.i_b = taken(i.stride_b, d.B); p.i_t = taken(i.stride_t, d.T);
     p.T = d.T; p.B = (int)d.B; p.D = (int)d.D;
     p.bf16 = d.type == SSD_TYPE_BF16;
     return p;
@@ -187,11 +190,18 @@ int check_rows(int64_t M, int64_t D, int type) {
 
 int64_t groups(int64_t n) { return (n + SSD_FP8_GROUP - 1) / SSD_FP8_GROUP; }
 
-// A row of 8-bit values: a whole number of 16-byte units, as the copies into shared memory need.
-int check_fp8_rows(const void* p, int64_t ld, int64_t cols) {
+// The row stride that a kernel is given: that of a single row as tensor maps want it, a whole number
+// of 16-byte units that holds the row.
+int64_t row_stride(int64_t ld, int64_t count, int64_t cols, size_t elem) {
+    const int64_t unit = 16 / (int64_t)elem;
+    return count > 1 ? ld : (cols + unit - 1) / unit * unit;
+}
+
+// Rows of 8-bit values: a whole number of 16-byte units, as the copies into shared memory need.
+int check_fp8_rows(const void* p, int64_t ld, int64_t count, int64_t cols) {
     if (p == nullptr) return SSDC_OK;
-    if (ld < cols) return SSDC_ERR_INVALID;
-    if (ld % 16 != 0 || !aligned_to(p, 16)) return SSDC_ERR_ALIGN;
+    if (count > 1 && ld < cols) return SSDC_ERR_INVALID;
+    if (taken(ld, count) % 16 != 0 || !aligned_to(p, 16)) return SSDC_ERR_ALIGN;
     return SSDC_OK;
 }
 
@@ -246,7 +256,7 @@ int ssd_gated_scan_fwd_ws(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float*
     if (rc != SSDC_OK) return rc;
     Gated p = gated_problem(x, f, i, d);
     p.h0 = h0; p.reset = reset;
-    p.h = h.p; p.h_b = h.stride_b; p.h_t = h.stride_t;
+    p.h = h.p; p.h_b = taken(h.stride_b, d.B); p.h_t = taken(h.stride_t, d.T);
     p.h_last = h_last; p.states = states; p.status = status;
     p.joints = need > 0 ? static_cast<float2*>(workspace) : nullptr;
     (void)cudaGetLastError();
@@ -269,7 +279,7 @@ int ssd_gated_scan_step(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* s
     rc = check_device();
     if (rc != SSDC_OK) return rc;
     Gated p = gated_problem(x, f, i, d);
-    p.h0 = state_in; p.h = h.p; p.h_b = h.stride_b; p.h_last = state_out;
+    p.h0 = state_in; p.h = h.p; p.h_b = taken(h.stride_b, B); p.h_last = state_out;
     (void)cudaGetLastError();
     return done(gated_step_launch(p, stream));
 }
@@ -299,10 +309,10 @@ int ssd_gated_scan_bwd(ssd_seq_in x, ssd_seq_in f, ssd_seq_in i, const float* st
     if (rc != SSDC_OK) return rc;
     Gated p = gated_problem(x, f, i, d);
     p.in_states = states; p.reset = reset;
-    p.dh = dh.p; p.dh_b = dh.stride_b; p.dh_t = dh.stride_t; p.dh_last = dh_last;
-    p.dx = dx.p; p.dx_b = dx.stride_b; p.dx_t = dx.stride_t;
-    p.df = df.p; p.df_b = df.stride_b; p.df_t = df.stride_t;
-    p.di = di.p; p.di_b = di.stride_b; p.di_t = di.stride_t;
+    p.dh = dh.p; p.dh_b = taken(dh.stride_b, d.B); p.dh_t = taken(dh.stride_t, d.T); p.dh_last = dh_last;
+    p.dx = dx.p; p.dx_b = taken(dx.stride_b, d.B); p.dx_t = taken(dx.stride_t, d.T);
+    p.df = df.p; p.df_b = taken(df.stride_b, d.B); p.df_t = taken(df.stride_t, d.T);
+    p.di = di.p; p.di_b = taken(di.stride_b, d.B); p.di_t = taken(di.stride_t, d.T);
     p.dh0 = dh0; p.status = status;
     (void)cudaGetLastError();
     return done(gated_bwd_launch(p, stream));
@@ -317,7 +327,7 @@ int ssd_residual_norm_fwd(ssd_rows_in x, ssd_rows_in residual, const float* w, f
     if (!(eps >= 0.0f)) return SSDC_ERR_INVALID;
     const bool fp8 = out_type == SSD_TYPE_E4M3;
     if (fp8 != (scale != nullptr)) return SSDC_ERR_INVALID;
-    if (fp8 && (rc = check_fp8_rows(y.p, y.ld, D)) != SSDC_OK) return rc;
+    if (fp8 && (rc = check_fp8_rows(y.p, y.ld, M, D)) != SSDC_OK) return rc;
     Args a;
     a.input(rows(x.p, x.ld, M, D, type_bytes(type)));
     a.input(rows(residual.p, residual.ld, M, D, type_bytes(type)), false);
@@ -330,9 +340,10 @@ int ssd_residual_norm_fwd(ssd_rows_in x, ssd_rows_in residual, const float* w, f
     rc = check_device();
     if (rc != SSDC_OK) return rc;
     Norm p = {};
-    p.x = x.p; p.x_ld = x.ld; p.res = residual.p; p.res_ld = residual.ld;
+    const size_t e = type_bytes(type), eo = type_bytes(out_type);
+    p.x = x.p; p.x_ld = row_stride(x.ld, M, D, e); p.res = residual.p; p.res_ld = row_stride(residual.ld, M, D, e);
     p.w = w; p.eps = eps; p.M = M; p.D = (int)D; p.bf16 = type == SSD_TYPE_BF16;
-    p.r = r.p; p.r_ld = r.ld; p.out_type = out_type; p.y = y.p; p.y_ld = y.ld;
+    p.r = r.p; p.r_ld = row_stride(r.ld, M, D, e); p.out_type = out_type; p.y = y.p; p.y_ld = row_stride(y.ld, M, D, eo);
     p.scale = scale; p.rstd = rstd;
     (void)cudaGetLastError();
     return done(norm_fwd_launch(p, stream));
@@ -364,9 +375,10 @@ int ssd_residual_norm_bwd(ssd_rows_in dy, ssd_rows_in dr, ssd_rows_in r, const f
     rc = check_device();
     if (rc != SSDC_OK) return rc;
     NormBwd p = {};
-    p.dy = dy.p; p.dy_ld = dy.ld; p.dr = dr.p; p.dr_ld = dr.ld; p.r = r.p; p.r_ld = r.ld;
+    p.dy = dy.p; p.dy_ld = row_stride(dy.ld, M, D, e); p.dr = dr.p; p.dr_ld = row_stride(dr.ld, M, D, e);
+    p.r = r.p; p.r_ld = row_stride(r.ld, M, D, e);
     p.w = w; p.rstd = rstd; p.M = M; p.D = (int)D; p.bf16 = type == SSD_TYPE_BF16;
-    p.dx = dx.p; p.dx_ld = dx.ld; p.dw = dw; p.partial = static_cast<float*>(workspace);
+    p.dx = dx.p; p.dx_ld = row_stride(dx.ld, M, D, e); p.dw = dw; p.partial = static_cast<float*>(workspace);
     (void)cudaGetLastError();
     return done(norm_bwd_launch(p, stream));
 }
@@ -380,7 +392,7 @@ int ssd_fp8_quantize(ssd_rows_in x, int64_t M, int64_t K, int32_t type, int32_t 
     if (q.p == nullptr && qt.p == nullptr) return SSDC_ERR_INVALID;
     if ((q.p == nullptr) != (scale == nullptr) || (qt.p == nullptr) != (scale_t == nullptr)) return SSDC_ERR_INVALID;
     int rc;
-    if ((rc = check_fp8_rows(q.p, q.ld, K)) != SSDC_OK || (rc = check_fp8_rows(qt.p, qt.ld, M)) != SSDC_OK) return rc;
+    if ((rc = check_fp8_rows(q.p, q.ld, M, K)) != SSDC_OK || (rc = check_fp8_rows(qt.p, qt.ld, K, M)) != SSDC_OK) return rc;
     const bool blocks = scales == SSD_SCALE_BLOCKS;
     Args a;
     a.input(rows(x.p, x.ld, M, K, type_bytes(type)));
@@ -392,7 +404,7 @@ int ssd_fp8_quantize(ssd_rows_in x, int64_t M, int64_t K, int32_t type, int32_t 
     rc = check_device();
     if (rc != SSDC_OK) return rc;
     Quant p = {};
-    p.x = x.p; p.x_ld = x.ld; p.M = M; p.K = K; p.bf16 = type == SSD_TYPE_BF16; p.blocks = blocks;
+    p.x = x.p; p.x_ld = row_stride(x.ld, M, K, type_bytes(type)); p.M = M; p.K = K; p.bf16 = type == SSD_TYPE_BF16; p.blocks = blocks;
     p.q = static_cast<uint8_t*>(q.p); p.q_ld = q.ld; p.scale = scale;
     p.qt = static_cast<uint8_t*>(qt.p); p.qt_ld = qt.ld; p.scale_t = scale_t;
     (void)cudaGetLastError();
@@ -412,7 +424,7 @@ int ssd_fp8_matmul(ssd_rows_in a8, const float* a_scale, ssd_rows_in b8, const f
     if (b_scales != SSD_SCALE_ROWS && b_scales != SSD_SCALE_BLOCKS) return SSDC_ERR_INVALID;
     if (M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256) return SSDC_ERR_UNSUPPORTED;
     int rc;
-    if ((rc = check_fp8_rows(a8.p, a8.ld, K)) != SSDC_OK || (rc = check_fp8_rows(b8.p, b8.ld, K)) != SSDC_OK) return rc;
+    if ((rc = check_fp8_rows(a8.p, a8.ld, M, K)) != SSDC_OK || (rc = check_fp8_rows(b8.p, b8.ld, N, K)) != SSDC_OK) return rc;
     const size_t need = matmul_workspace(M, N, K);
     if (workspace == nullptr || !aligned_to(workspace, 256) || ws_bytes < need) return SSDC_ERR_WORKSPACE;
     const bool blocks = b_scales == SSD_SCALE_BLOCKS;
@@ -427,10 +439,10 @@ int ssd_fp8_matmul(ssd_rows_in a8, const float* a_scale, ssd_rows_in b8, const f
     rc = check_device();
     if (rc != SSDC_OK) return rc;
     Matmul p = {};
-    p.a = static_cast<const uint8_t*>(a8.p); p.a_ld = a8.ld; p.a_scale = a_scale;
-    p.b = static_cast<const uint8_t*>(b8.p); p.b_ld = b8.ld; p.b_scale = b_scale; p.b_blocks = blocks;
+    p.a = static_cast<const uint8_t*>(a8.p); p.a_ld = row_stride(a8.ld, M, K, 1); p.a_scale = a_scale;
+    p.b = static_cast<const uint8_t*>(b8.p); p.b_ld = row_stride(b8.ld, N, K, 1); p.b_scale = b_scale; p.b_blocks = blocks;
     p.M = M; p.N = N; p.K = K; p.out_bf16 = out_type == SSD_TYPE_BF16;
-    p.c = c.p; p.c_ld = c.ld;
+    p.c = c.p; p.c_ld = row_stride(c.ld, M, N, type_bytes(out_type));
     p.status = static_cast<int*>(workspace);
     p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
     (void)cudaGetLastError();

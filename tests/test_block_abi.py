@@ -301,3 +301,30 @@ def test_a_call_keeps_its_own_words(lib):
     call.fn = library
     call(None, *range(16))
     assert seen[1:] == [tuple(range(100, 116)), tuple(range(16))]
+
+
+# ---- strides that are never taken: each call still fails, but by its last check
+
+
+def test_stride_of_a_single_row_is_not_checked(lib):
+    scale, x, none = at(3), ROWS(at(1), 3), ROWS(None)
+    # the quantiser: q over x
+    assert lib.ssd_fp8_quantize(x, 1, 256, 1, 0, ROWS(at(1), 257), scale, none, None, None) == INVALID
+    assert lib.ssd_fp8_quantize(x, 256, 1, 1, 0, none, None, ROWS(at(1), 257), scale, None) == INVALID
+    # the product: no workspace
+    for M, N in ((1, 64), (64, 1), (1, 1)):
+        ld = lambda rows: 257 if rows == 1 else 256
+        assert lib.ssd_fp8_matmul(ROWS(at(1), ld(M)), at(2), ROWS(at(3), ld(N)), at(4), 1, M, N, 256, 1, ROWS(at(5), 0 if M == 1 else N),
+                                  None, 0, None) == WORKSPACE
+    # the norm: the scale over the weights
+    assert lib.ssd_residual_norm_fwd(x, none, at(3), 1e-5, 1, 256, 1, none, 2, ROWS(at(5), 257), at(3), None, None) == INVALID
+    # more rows than one are checked
+    assert lib.ssd_fp8_quantize(ROWS(at(1)), 2, 256, 1, 0, ROWS(at(1), 257), scale, none, None, None) == ALIGN
+    assert lib.ssd_fp8_matmul(ROWS(at(1), 257), at(2), ROWS(at(3)), at(4), 1, 2, 64, 256, 1, ROWS(at(5)), None, 0, None) == ALIGN
+
+
+@pytest.mark.parametrize("stride_t", [-1, 1 << 31, 1 << 50])
+def test_token_stride_of_a_single_token_is_not_checked(lib, stride_t):
+    one = (2, 1, 64, 1)
+    assert fwd(lib, dims=one, x=SEQ(at(1), 64, stride_t), h=SEQ(at(6), 64, stride_t), status=at(6)) == INVALID   # the last check
+    assert fwd(lib, dims=(2, 2, 64, 1), x=SEQ(at(1), 64, stride_t)) in (INVALID, UNSUPPORTED)

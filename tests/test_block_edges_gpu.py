@@ -248,3 +248,52 @@ def test_second_derivatives_are_refused(make):
     loss, t = make()
     for a, b in zip(torch.autograd.grad(loss, t), first):
         assert torch.equal(a, b.detach())
+
+
+# ---- a single row, whose stride is never taken
+
+
+@pytest.mark.parametrize("odd", [1, 3, 1001])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_single_rows_of_any_stride(odd, out):
+    """One row as the operand, or as the result, with a stride that no row could have: as a row with an ordinary one."""
+    N, K = 100, 300
+    one = lambda t, ld=odd: t.as_strided(t.shape, (ld, 1))
+    x, w = randn(1, K, seed=1, dtype=torch.bfloat16), randn(N, K, seed=2, dtype=torch.bfloat16)
+    weights = randn(K, seed=3)
+    norm = block.ResidualNorm(1, K)
+    r, q, scale = (t.clone() for t in norm(x, x, weights))
+    r1, q1, scale1 = norm(one(x), one(x), weights)
+    assert torch.equal(r1, r) and torch.equal(q1.view(torch.uint8), q.view(torch.uint8)) and torch.equal(scale1, scale)
+    q = block.fp8_empty(1, K)
+    q.copy_(norm.y)
+    w_q, w_s = block.Fp8Quantize(N, K, scales="blocks")(w)
+    y = block.Fp8Product(1, N, K, out=out)
+    want = y(q, scale, w_q, w_s).clone()
+    assert torch.equal(y(one(q), scale, w_q, w_s), want)
+    row_q, row_s = block.Fp8Quantize(1, K, scales="blocks")(x)
+    a_q, a_s = block.Fp8Quantize(N, K)(w)
+    column = block.Fp8Product(N, 1, K, out=out)
+    want = column(a_q, a_s, row_q, row_s).clone()
+    assert torch.equal(column(a_q, a_s, one(row_q), row_s), want)
+    # C, and r over x, through the C entry points
+    lib, st = block.load(), torch.cuda.current_stream().cuda_stream
+    want, c = y(q, scale, w_q, w_s).clone(), torch.full((1, N + 8), GUARD, dtype=DT[out], device="cuda")
+    rows = lambda t, ld: block.ssd_rows(t.data_ptr(), ld)
+    assert lib.ssd_fp8_matmul(rows(q, odd), scale.data_ptr(), rows(w_q, w_q.stride(0)), w_s.data_ptr(), 1, 1, N, K, y.type, rows(c, odd - 1),
+                              y.workspace.data_ptr(), y.workspace.numel(), st) == 0
+    assert torch.equal(c[:, :N], want) and bool((c[:, N:] == GUARD).all())
+    x1, y1 = x.clone(), torch.empty(1, K, device="cuda")
+    assert lib.ssd_residual_norm_fwd(rows(x1, odd), rows(x, 5), weights.data_ptr(), 1e-5, 1, K, block.TYPE_BF16, rows(x1, 7), block.TYPE_F32,
+                                     rows(y1, 0), None, None, st) == 0
+    assert torch.equal(x1, r)
+
+
+def test_single_token_of_any_stride():
+    B, D = 3, 64
+    x, f, i, h0, _ = scan_inputs(B, 1, D, "bf16", True, False, seed=1)
+    plan = block.GatedScan(B, 1, D)
+    h, last = (t.clone() for t in plan(x, f, i, h0=h0))
+    strange = lambda t, st: t.as_strided(t.shape, (D, st, 1))
+    h1, last1 = plan(strange(x, 1 << 40), strange(f, 0), strange(i, 1 << 31), h0=h0)
+    assert torch.equal(h1, h) and torch.equal(last1, last)
