@@ -164,8 +164,10 @@ __device__ __forceinline__ float row_sum(float v, float (*part)[32], int slot, i
     return s;
 }
 
-// CTAs of the gradients' kernel an SM takes (its registers), by a lane's features.
-constexpr int bwd_ctas(int vals) { return vals == 32 ? 2 : vals == 16 ? 3 : 4; }
+// CTAs of the gradients' kernel an SM takes: two with rows copied ahead (96 KB of shared memory each), else
+// as many as a lane's features leave registers for. (fp32, 16 features, two and three CTAs an SM of which two
+// fit at a time: M 32768 D 1024 93 / 103 us, M 16384 D 1024 54 / 60 us, M 8192 D 4096 93 / 105 us.)
+constexpr int bwd_ctas(int vals, int align) { return vals == 32 || align == kAligned ? 2 : vals == 16 ? 3 : 4; }
 
 template <int kRowWarps>
 constexpr int cta_warps() { return kRowWarps > 8 ? kRowWarps : 8; }
@@ -314,7 +316,7 @@ constexpr int bwd_smem() {  // and, for shifted rows, the weights
     return bwd_staging<T, kVals, kRowWarps, kAlign>() + (kAlign == kShifted ? kRowWarps * 32 * kVals * 4 : 0);
 }
 template <typename T, int kVals, int kRowWarps, int kAlign>
-__global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1 : bwd_ctas(kVals)) norm_bwd(const NormBwd p) {
+__global__ void __launch_bounds__(32 * cta_warps<kRowWarps>(), kRowWarps > 8 ? 1 : bwd_ctas(kVals, kAlign)) norm_bwd(const NormBwd p) {
     using L = Layout<T, kAlign, kVals>;
     constexpr int kWarps = cta_warps<kRowWarps>(), kRun = L::kRun, kRows = kWarps / kRowWarps, kWarpSpan = L::kWarpSpan;
     __shared__ float part[2][32];
@@ -619,7 +621,7 @@ int bwd_parts(int64_t M, int64_t D, bool bf16, int align) {
     const int vals = lane_vals(D, bf16, align), w = row_warps(spread(D, bf16, align), vals), rows = w > 8 ? 1 : 8 / w;
     int64_t ctas = (M + rows - 1) / rows;
     if (align == kShifted) ctas = (M + 8 * rows - 1) / (8 * rows) * 8;
-    const int64_t most = w > 8 ? 152 : 152 * bwd_ctas(vals);
+    const int64_t most = w > 8 ? 152 : 152 * bwd_ctas(vals, align);
     return (int)(ctas < most ? ctas : most);
 }
 
