@@ -297,3 +297,114 @@ def test_single_token_of_any_stride():
     strange = lambda t, st: t.as_strided(t.shape, (D, st, 1))
     h1, last1 = plan(strange(x, 1 << 40), strange(f, 0), strange(i, 1 << 31), h0=h0)
     assert torch.equal(h1, h) and torch.equal(last1, last)
+
+
+# ---- 8-bit values one by one
+
+
+POWERS = torch.tensor([2.0 ** k for k in range(-40, 24)], dtype=torch.float64)
+
+
+def e4m3(v):
+    """The nearest e4m3 value of doubles at or above zero, ties to even, at most 448."""
+    step = POWERS.to(v.device)[(torch.frexp(v)[1].clamp_min(-5) - 4).long() + 40]
+    return (torch.round(v / step) * step).clamp_max(448.0)
+
+
+def check_steps(q, scale, y, bound):
+    """Every value of q is the nearest e4m3 value of |y| / scale moved by at most `bound` of itself; scales likewise.
+    y and scale in 64 bits, scale of each value."""
+    at = y.abs() / scale
+    got = q.float().double()
+    assert bool(((got == 0) | (torch.sign(got) == torch.sign(y))).all())
+    got = got.abs()
+    assert bool((got >= e4m3(at * (1 - bound))).all() and (got <= e4m3(at * (1 + bound))).all())
+
+
+@pytest.mark.parametrize("M,D", [(1000, 1024), (300, 1537), (64, 5136), (7, 129), (20, 32768)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_norm_to_eight_bits_value_by_value(M, D, dtype):
+    """fp32 roundings on the way to a quotient, 2^-24 each: the sum, of a value and of its group's largest; that one's
+    two products; the scale; the quotient. Six of them: less than 2^-21."""
+    x, res = randn(M, D, seed=M, dtype=DT[dtype]), randn(M, D, seed=1, std=2.0)
+    res[:, :: max(1, D // 5)] *= 10.0
+    res, w = res.to(DT[dtype]), randn(D, seed=2, mean=1.0, std=0.2)
+    _, q, scale = block.ResidualNorm(M, D, dtype)(x, res, w)
+    r = x.double() + res.double()
+    y = r / torch.sqrt((r * r).mean(1, keepdim=True) + 1e-5) * w.double()
+    KB = block.fp8_groups(D)
+    largest = torch.nn.functional.pad(y.abs(), (0, KB * 128 - D)).unflatten(1, (KB, 128)).amax(2)
+    s = largest.clamp_min(2.0 ** -100) / 448
+    assert float(((scale.t().double() - s).abs() / s).max()) <= 2.0 ** -20      # (and rstd's, which a quotient does not see)
+    check_steps(q, s.repeat_interleave(128, 1)[:, :D], y, 2.0 ** -21)
+
+
+@pytest.mark.parametrize("M,K", [(1000, 1024), (257, 1000), (130, 5136), (3, 77)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scales", ["rows", "blocks"])
+def test_quantiser_value_by_value(M, K, dtype, scales):
+    """Two roundings of 2^-24 on the way to a quotient, the scale's and its own: at most 2^-23."""
+    x = randn(M, K, seed=M, dtype=DT[dtype])
+    x[:, ::9] *= 30
+    q, s, qt, st = block.Fp8Quantize(M, K, dtype, scales=scales, transposed=True)(x)
+
+    def largest(t, rows):
+        R, C = t.shape
+        RB, CB = -(-R // rows), -(-C // 128)
+        full = torch.zeros(RB * rows, CB * 128, dtype=torch.float64, device="cuda")
+        full[:R, :C] = t.double().abs()
+        by = full.reshape(RB, rows, CB, 128).amax((1, 3)).clamp_min(2.0 ** -100) / 448
+        return by, by.repeat_interleave(rows, 0)[:R].repeat_interleave(128, 1)[:, :C]
+
+    rows = 128 if scales == "blocks" else 1
+    for values, scale, t in ((q, s, x), (qt, st, x.t())):
+        by, each = largest(t, rows)
+        assert torch.equal(scale if rows == 128 else scale.t(), by.float())      # (rounded to nearest)
+        check_steps(values, each, t.double(), 2.0 ** -23)
+
+
+# ---- the same bits every time, whatever runs around
+
+
+def repeating_scan(B, T, D, dtype):
+    x, f, i, h0, reset = scan_inputs(B, T, D, dtype, True, True, seed=T)
+    dh, dh_last = randn(B, T, D, seed=9, dtype=DT[dtype]), randn(B, D, seed=10)
+    plan, back = block.GatedScan(B, T, D, dtype, keep_states=True), block.GatedScanBackward(B, T, D, dtype)
+
+    def call():
+        h, last = plan(x, f, i, h0=h0, reset=reset)
+        return (h, last, plan.states, *back(x, f, i, plan.states, dh, dh_last=dh_last, reset=reset).values())
+    return call, (plan, back)
+
+
+def repeating_norm(M, D, dtype):
+    x, res, dy = (randn(M, D, seed=k, dtype=DT[dtype]) for k in range(3))
+    w = randn(D, seed=3)
+    plan, back = block.ResidualNorm(M, D, dtype), block.ResidualNormBackward(M, D, dtype)
+
+    def call():
+        r, q, scale = plan(x, res, w)
+        return (r, q.view(torch.uint8), scale, *back(dy, r, w, plan.rstd, res))
+    return call, ()
+
+
+def repeating_linear(M, N, K):
+    x, w, dy = randn(M, K, seed=1, dtype=torch.bfloat16), randn(N, K, seed=2, dtype=torch.bfloat16), randn(M, N, seed=3, dtype=torch.bfloat16)
+    plan = block.Fp8Linear(M, N, K)
+    return lambda: (plan.forward(x, w), *plan.backward(dy)), (plan.y, plan.dx, plan.dw)
+
+
+@pytest.mark.parametrize("make,sizes", [
+    (repeating_scan, (2, 2048, 1024, "bf16")), (repeating_scan, (4, 4096, 512, "bf16")), (repeating_scan, (1, 16384, 512, "fp32")),
+    (repeating_scan, (16, 512, 1024, "fp32")), (repeating_scan, (3, 777, 333, "bf16")), (repeating_norm, (3000, 1024, "bf16")),
+    (repeating_norm, (3001, 1537, "fp32")), (repeating_norm, (2000, 1601, "bf16")), (repeating_norm, (5000, 1024, "fp32")),
+    (repeating_linear, (8, 5136, 1024)), (repeating_linear, (4096, 5136, 1024)), (repeating_linear, (1021, 2057, 192))])
+def test_the_same_bits_every_time(make, sizes):
+    call, plans = make(*sizes)
+    first = [t.clone() for t in call()]
+    pad = torch.empty(1 << 24, device="cuda")
+    for r in range(15):
+        pad[: 1 + (r * 7919 * 1000) % (1 << 24)].fill_(float(r))
+        for a, b in zip(call(), first):
+            assert torch.equal(a, b)
+    assert all(p.status() == 0 for p in plans)
