@@ -244,9 +244,10 @@ uint32_t few_cluster(int64_t N, int KB) {
     return r;
 }
 
-// Up to 16 rows always (here / by block_matmul.cu: M 16 N 5136 K 1024 6.1 / 7.0 us, M 16 N 50257
-// K 1024 12 / 17 us); up to 32 where K is dealt over a cluster (M 32 N 1024 K 8192 13 / 23 us; where
-// it is not, M 32 N 5136 K 1024 7.5 / 7.2 us).
+// Up to 16 rows always (M 16, bfloat16, in a graph, here / by block_matmul.cu: N 64 K 64 2.7 / 3.7 us, N 64
+// K 8192 6.6 / 22, N 1024 K 1024 5.7 / 5.9, N 5136 K 1024 5.8 / 6.6, N 20000 K 2048 9.6 / 20, N 50257 K 128
+// 6.0 / 8.7, N 50257 K 4096 42 / 52); up to 32 where K is dealt over a cluster (M 32 N 1024 K 8192 13 / 23 us;
+// where it is not, M 32 N 5136 K 1024 7.5 / 7.2 us).
 bool matmul_is_few(int64_t M, int64_t N, int64_t K) {
     return M <= 16 || (M <= 32 && few_cluster(N, (int)((K + kGroup - 1) / kGroup)) > 1);
 }
