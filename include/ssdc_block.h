@@ -46,7 +46,9 @@ extern "C" {
  * element strides of batch rows and tokens; channels are contiguous. So the
  * three inputs may be column slices of one projection's output, and either
  * order of batch and time works. Input strides may be zero (broadcast rows); a
- * token stride of 2^31 bytes or more is SSDC_ERR_UNSUPPORTED.
+ * token stride of 2^31 bytes or more is SSDC_ERR_UNSUPPORTED. Fastest are arrays
+ * whose rows, strides and first elements are whole 16-byte units and whose batch
+ * rows are further apart than their tokens.
  */
 typedef struct {
     const void *p;
@@ -189,13 +191,17 @@ int ssd_fp8_quantize(ssd_rows_in x, int64_t M, int64_t K, int32_t type, int32_t 
  * of 128 columns are summed on the tensor cores, then scaled and added in fp32.
  *   a, a_scale   (M, K), SSD_SCALE_ROWS
  *   b, b_scale   (N, K), b_scales = SSD_SCALE_BLOCKS (weights) or SSD_SCALE_ROWS
- *   c            output rows of `out_type` (F32 or BF16), ld elements apart
+ *   c            output rows of `out_type` (F32 or BF16), ld elements apart; what
+ *                lies between its rows is not written
  *   workspace    ssd_fp8_matmul_workspace_bytes() bytes, 256-byte aligned, for one
  *                call at a time. Its first word is a status that a wait that gave
- *                up sets (ssd_complex_status() reads it). The caller zeroes its
- *                first SSD_FP8_MATMUL_ZEROED bytes, or all of it if it has fewer,
- *                once, before the first call, and again after such a status
- * a.p and b.p are 16-byte aligned.
+ *                up sets (ssd_complex_status() reads it); C is then incomplete. The
+ *                caller zeroes its first SSD_FP8_MATMUL_ZEROED bytes, or all of it
+ *                if it has fewer, once, before the first call, and again after such
+ *                a status
+ * a.p and b.p are 16-byte aligned. Where CTAs share tiles (the workspace is then
+ * larger than SSD_FP8_MATMUL_ZEROED) all of them have to run at the same time: the
+ * call is SSDC_ERR_CUDA where the device's SMs are not all there for it.
  */
 #define SSD_FP8_MATMUL_ZEROED 16384
 size_t ssd_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
