@@ -6,7 +6,9 @@ The classes hold the outputs and workspaces of one problem size, so that a call
 allocates nothing and the next call overwrites the last one's outputs: threads that
 call at the same time need a plan each.
 ``gated_scan``, ``residual_norm`` and ``fp8_linear`` are differentiable
-(``torch.autograd``, first derivatives) and allocate their outputs.
+(``torch.autograd``, first derivatives) and allocate their outputs. They do not
+read the status of a wait between CTAs that gave up, which a plan's ``status()``
+does: that waits for the GPU.
 
 A plan's tensors belong to the device it was made for; a call runs there, on that
 device's current stream or on ``stream``, whichever device is current. Tensors made on another stream have to be ordered with
