@@ -159,7 +159,7 @@ def run(s):
         if op == "delta_train":
             plan = s["plan"]
             o, last = plan(s["q"], s["k"], s["v"], s["f"], s["b"], h0=s["h0"], reset=s["reset"])
-            g = s["back"](s["q"], s["k"], s["v"], s["f"], s["b"], plan.states, plan.updates, s["do"],
+            g = s["back"](s["q"], s["k"], s["f"], s["b"], plan.states, plan.updates, s["do"],
                           dh_last=s["dh_last"], reset=s["reset"])
             out = {"o": o, "dq": g["dq"], "dk": g["dk"], "dv": g["dv"], "df": g["df"], "db": g["db"]}
             return {**out, "h_last": last, "dh0": g["dh0"]} if s["case"]["state"] else out
