@@ -9,6 +9,11 @@
  *                   in 8 bits and a scale for each 128 features; the gradients
  *   8-bit product   C = A B^T from e4m3 values with a scale for each group or
  *                   block of 128, and the quantisers that make its operands
+ *   delta rule      a matrix state for each head that every token corrects, gated:
+ *                   forward, one token at a time, and the gradients
+ *   gated norm      the norm of every head's features behind a recurrence, times a
+ *                   gate, with a scaled skip connection, an output in 8 bits; the
+ *                   gradients
  *
  * Conventions are those of ssdc.h: status codes, no aborts, argument errors
  * found on the host before anything is enqueued, the caller owns every buffer,
@@ -210,6 +215,113 @@ int ssd_fp8_matmul(ssd_rows_in a, const float *a_scale, ssd_rows_in b, const flo
                    size_t ws_bytes, cudaStream_t stream);
 
 /*
+ * Delta rule. Every batch row and value head h has a state S of K rows and V
+ * columns and takes its queries and keys from the key head g = h / (H / G):
+ *
+ *   a_t = sigmoid(f_t), beta_t = sigmoid(b_t); c_t = a_t, or 0 where reset[b, t] is
+ *         not zero (the first token of a document in a packed row)
+ *   q_t, k_t are taken as K^-1/2 q / sqrt(|q|^2 + 1e-6) and k / sqrt(|k|^2 + 1e-6)
+ *         with `normalize`, else as they are given
+ *   u_t = beta_t (v_t - c_t S_{t-1}^T k_t)
+ *   S_t = c_t S_{t-1} + k_t u_t^T,   S_{-1} = h0 (zero without one)
+ *   o_t = S_t^T q_t
+ *
+ * q, k (B, T, G, K), v (B, T, H, V), f, b (B, T, H) hold `type` (F32 or BF16) values;
+ * gates, sums and states are fp32. They are given by their first element and the
+ * element strides of batch rows, tokens and heads, features contiguous: column slices
+ * of one projection's output work, and any order of batch, time and heads; a stride
+ * may be zero (broadcast). Outputs are dense, in the order of their shapes, and lie
+ * outside the span of every input. Outputs, states and updates are 16-byte aligned.
+ * K and V are multiples of 8 up to 128, G divides H.
+ *
+ * BF16: chunks of 64 tokens on the tensor cores, products with operands in one or two bf16
+ * parts and fp32 sums; states are within 1e-5 of exact ones (relative to their norm)
+ * where |k|^2 beta <= 2, which normalised keys always meet: beyond that the recurrence itself grows
+ * without bound. F32: token by token in fp32. Fastest: BF16, first elements and strides in whole 16 bytes.
+ */
+typedef struct {
+    const void *p;
+    int64_t stride_b, stride_t, stride_h;
+} ssd_heads_in;
+typedef struct {
+    int64_t B, T, H, G, K, V; /* B T H (K + V) up to 2^40, B H up to 2^20, T up to 2^31 - 64 */
+    int32_t type;             /* SSD_TYPE_F32 or SSD_TYPE_BF16 */
+    int32_t normalize;        /* 0 or 1 */
+} ssd_delta_dims;
+
+/*
+ * Forward pass.
+ *   h0        (B, H, K, V) fp32, or NULL: zero
+ *   reset     (B, T) bytes, or NULL
+ *   o         output (B, T, H, V) of `type`
+ *   h_last    output (B, H, K, V) fp32, the state after the last token; it may be h0
+ *   states, updates   outputs for the backward pass, or both NULL: the state that
+ *             enters every SSD_DELTA_STATE_TOKENS-th token,
+ *             (B, H, ceil(T / that), K, V), and u (B, T, H, V), both of `type`
+ * One launch.
+ */
+#define SSD_DELTA_STATE_TOKENS 64
+int ssd_delta_rule_fwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in v, ssd_heads_in f, ssd_heads_in b, const float *h0,
+                       const uint8_t *reset, ssd_delta_dims dims, void *o, float *h_last, void *states, void *updates,
+                       cudaStream_t stream);
+
+/*
+ * One token for every batch row (the forward pass at T = 1, for generation), on
+ * states in place: state_out may be state_in. Token strides are not used, dims.T
+ * is 1. One launch, which reads and writes each state once.
+ */
+int ssd_delta_rule_step(ssd_heads_in q, ssd_heads_in k, ssd_heads_in v, ssd_heads_in f, ssd_heads_in b,
+                        const float *state_in, ssd_delta_dims dims, void *o, float *state_out, cudaStream_t stream);
+
+/*
+ * Backward pass: the gradients of q and k (summed over the value heads that share them),
+ * v, f, b and h0.
+ *   states, updates   what the forward pass kept for the same inputs (h0 is in them)
+ *   d_o       gradient of o;  dh_last (B, H, K, V) fp32, or NULL: zero
+ *   dq, dk (B, T, G, K), dv (B, T, H, V), df, db (B, T, H): outputs of `type`
+ *   dh0       output (B, H, K, V) fp32, or NULL; it may be dh_last
+ *   workspace ssd_delta_rule_bwd_workspace_bytes() bytes, 256-byte aligned, its
+ *             contents need not be kept
+ * df is 0 at a reset. Sums run in a fixed order. Two launches (F32: four).
+ */
+size_t ssd_delta_rule_bwd_workspace_bytes(ssd_delta_dims dims);
+int ssd_delta_rule_bwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in f, ssd_heads_in b, const void *states,
+                       const void *updates, const uint8_t *reset, ssd_heads_in d_o, const float *dh_last,
+                       ssd_delta_dims dims, void *dq, void *dk, void *dv, void *df, void *db, float *dh0,
+                       void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Gated norm over M rows of H heads of D features (D a multiple of 8 up to 256,
+ * H D up to 32768):
+ *   u = x + s v (u = x without v; s: one number for each head),
+ *   y = w u / sqrt(mean over the head's features of u^2 + eps) z sigmoid(z)
+ * in fp32, rounded once.
+ *   x, z, v   rows of H D values of `type`, ld elements apart; v.p may be NULL
+ *   w         (H D) fp32, or NULL: ones
+ *   s         (H) fp32, given exactly with v
+ *   y         output rows of `out_type`: F32, BF16, or E4M3 with scales for each 128
+ *             features as ssd_residual_norm_fwd writes them. It may be x, z or v itself where
+ *             the types are the same
+ * One launch.
+ */
+int ssd_gated_norm_fwd(ssd_rows_in x, ssd_rows_in z, const float *w, ssd_rows_in v, const float *s, float eps, int64_t M,
+                       int64_t H, int64_t D, int32_t type, int32_t out_type, ssd_rows_out y, float *scale,
+                       cudaStream_t stream);
+
+/*
+ * Its gradients, from the forward pass's inputs and dy (rows of `type`):
+ *   dx, dz, dv   output rows of `type`; dv.p exactly with v
+ *   dw           output (H D) fp32, or NULL;  ds: output (H) fp32, exactly with v
+ *   workspace    ssd_gated_norm_bwd_workspace_bytes() bytes, 256-byte aligned, its
+ *                contents need not be kept
+ * dw and ds are summed in a fixed order. Two launches (one without dw and v).
+ */
+size_t ssd_gated_norm_bwd_workspace_bytes(int64_t M, int64_t H, int64_t D);
+int ssd_gated_norm_bwd(ssd_rows_in dy, ssd_rows_in x, ssd_rows_in z, const float *w, ssd_rows_in v, const float *s, float eps,
+                       int64_t M, int64_t H, int64_t D, int32_t type, ssd_rows_out dx, ssd_rows_out dz, ssd_rows_out dv,
+                       float *dw, float *ds, void *workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * Any of the calls above that launch work, from its arguments as 64-bit words: in
  * order, structures member by member, integers sign-extended, eps as the bits of a
  * float in the low half. For bindings in which passing twenty arguments takes
@@ -224,6 +336,11 @@ int ssd_fp8_matmul(ssd_rows_in a, const float *a_scale, ssd_rows_in b, const flo
 #define SSD_CALL_FP8_QUANTIZE 5        /* 12 words */
 #define SSD_CALL_FP8_MATMUL 6          /* 15 words */
 #define SSD_CALL_GATED_SCAN_FWD_WS 7   /* 23 words */
+#define SSD_CALL_DELTA_RULE_FWD 8      /* 34 words */
+#define SSD_CALL_DELTA_RULE_STEP 9     /* 31 words */
+#define SSD_CALL_DELTA_RULE_BWD 10     /* 40 words */
+#define SSD_CALL_GATED_NORM_FWD 11     /* 17 words */
+#define SSD_CALL_GATED_NORM_BWD 12     /* 25 words */
 int ssd_block_call(int32_t call, const int64_t *words, cudaStream_t stream);
 
 #ifdef __cplusplus

@@ -1,11 +1,11 @@
 """Binding of the operators around the scan (include/ssdc_block.h): gated scan,
-residual norm, 8-bit product. Argument checks and marshalling only; every step
+residual norm, 8-bit product, delta rule, gated norm. Argument checks and marshalling only; every step
 runs in libssdc.so's kernels and there is no fallback.
 
 The classes hold the outputs and workspaces of one problem size, so that a call
 allocates nothing and the next call overwrites the last one's outputs: threads that
 call at the same time need a plan each.
-``gated_scan``, ``residual_norm`` and ``fp8_linear`` are differentiable
+``gated_scan``, ``residual_norm``, ``fp8_linear``, ``delta_rule`` and ``gated_norm`` are differentiable
 (``torch.autograd``, first derivatives) and allocate their outputs. They do not
 read the status of a wait between CTAs that gave up, which a plan's ``status()``
 does: that waits for the GPU.
@@ -42,7 +42,9 @@ _DTYPES = {"fp32": torch.float32, "bf16": torch.bfloat16}
 
 EXPORTS = ("ssd_gated_scan_states_bytes", "ssd_gated_scan_fwd", "ssd_gated_scan_workspace_bytes", "ssd_gated_scan_fwd_ws", "ssd_gated_scan_step", "ssd_gated_scan_bwd",
            "ssd_residual_norm_fwd", "ssd_residual_norm_bwd_workspace_bytes", "ssd_residual_norm_bwd",
-           "ssd_fp8_quantize", "ssd_fp8_matmul_workspace_bytes", "ssd_fp8_matmul", "ssd_block_call")
+           "ssd_fp8_quantize", "ssd_fp8_matmul_workspace_bytes", "ssd_fp8_matmul", "ssd_block_call",
+           "ssd_delta_rule_fwd", "ssd_delta_rule_step", "ssd_delta_rule_bwd_workspace_bytes", "ssd_delta_rule_bwd",
+           "ssd_gated_norm_fwd", "ssd_gated_norm_bwd_workspace_bytes", "ssd_gated_norm_bwd")
 
 
 class ssd_seq(ctypes.Structure):
@@ -57,6 +59,14 @@ class ssd_gated_dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64), ("type", ctypes.c_int32)]
 
 
+class ssd_heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
+
+
+class ssd_delta_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in "BTHGKV"] + [("type", ctypes.c_int32), ("normalize", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -67,7 +77,7 @@ def load() -> ctypes.CDLL:
         return _lib
     lib = ssdc.load()
     vp, i64, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
-    q, r, d = ssd_seq, ssd_rows, ssd_gated_dims
+    q, r, d, hd, dd = ssd_seq, ssd_rows, ssd_gated_dims, ssd_heads, ssd_delta_dims
     for name, res, args in (
             ("ssd_gated_scan_states_bytes", sz, [d]),
             ("ssd_gated_scan_fwd", i32, [q, q, q, vp, vp, d, q, vp, vp, vp, vp]),
@@ -81,6 +91,13 @@ def load() -> ctypes.CDLL:
             ("ssd_fp8_quantize", i32, [r, i64, i64, i32, i32, r, vp, r, vp, vp]),
             ("ssd_fp8_matmul_workspace_bytes", sz, [i64, i64, i64]),
             ("ssd_fp8_matmul", i32, [r, vp, r, vp, i32, i64, i64, i64, i32, r, vp, sz, vp]),
+            ("ssd_delta_rule_fwd", i32, [hd, hd, hd, hd, hd, vp, vp, dd, vp, vp, vp, vp, vp]),
+            ("ssd_delta_rule_step", i32, [hd, hd, hd, hd, hd, vp, dd, vp, vp, vp]),
+            ("ssd_delta_rule_bwd_workspace_bytes", sz, [dd]),
+            ("ssd_delta_rule_bwd", i32, [hd, hd, hd, hd, vp, vp, vp, hd, vp, dd, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            ("ssd_gated_norm_fwd", i32, [r, r, vp, r, vp, f32, i64, i64, i64, i32, i32, r, vp, vp]),
+            ("ssd_gated_norm_bwd_workspace_bytes", sz, [i64, i64, i64]),
+            ("ssd_gated_norm_bwd", i32, [r, r, r, vp, r, vp, f32, i64, i64, i64, i32, r, r, r, vp, vp, vp, sz, vp]),
             ("ssd_block_call", i32, [i32, vp, vp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
@@ -150,6 +167,23 @@ def _seq(name, t, like):
     if one != 1 and like[1][2] != 1:
         raise ValueError(f"{name} must have contiguous channels")
     return t.data_ptr(), sb, st
+
+
+def _heads(name, t, like):
+    """The address and the batch, token and head strides of a (B, T, H, D) tensor with contiguous features."""
+    if (t.dtype, t.shape, t.get_device()) != like:
+        _refuse(name, t, like)
+    sb, st, sh, one = t.stride()
+    if one != 1 and like[1][3] != 1:
+        raise ValueError(f"{name} must have contiguous features")
+    return t.data_ptr(), sb, st, sh
+
+
+def _gate(name, t, like):
+    """The same of a (B, T, H) tensor of one value for each head."""
+    if (t.dtype, t.shape, t.get_device()) != like:
+        _refuse(name, t, like)
+    return t.data_ptr(), *t.stride()
 
 
 class _Call:
@@ -519,6 +553,209 @@ class Fp8Linear:
         return dx, self.dw(qt, st, self.x_q.qt, self.x_q.scale_t, stream)
 
 
+# ---- delta rule
+
+
+def _delta_dims(B, T, heads, K, V, dtype, key_heads, normalize, what):
+    key_heads = heads if key_heads is None else key_heads
+    _sizes(B=B, T=T, heads=heads, K=K, V=V, key_heads=key_heads)
+    if heads % key_heads:
+        raise ValueError(f"key_heads must divide heads: {key_heads} and {heads}")
+    dims = ssd_delta_dims(B, T, heads, key_heads, K, V, _type(dtype), int(bool(normalize)))
+    if load().ssd_delta_rule_bwd_workspace_bytes(dims) == 0:
+        _raise(ssdc.SSDC_ERR_UNSUPPORTED, what)
+    return dims, (B, T, heads, key_heads, K, V, dims.type, dims.normalize)
+
+
+class DeltaRule:
+    """The gated delta rule over sequences (``ssd_delta_rule_fwd``): with a_t = sigmoid(f_t), beta_t = sigmoid(b_t),
+    c_t = a_t (0 where ``reset`` marks the first token of a document),
+
+        u_t = beta_t (v_t - c_t S_{t-1}^T k_t),  S_t = c_t S_{t-1} + k_t u_t^T,  o_t = S_t^T q_t
+
+    for a state S of K rows and V columns in each of ``heads`` heads, which share ``key_heads`` heads of q and k
+    (None: one each). With ``normalize`` k is divided by its length, and q by its length and sqrt(K). ``__call__``
+    takes q, k (B, T, key_heads, K), v (B, T, heads, V) with contiguous features, f, b (B, T, heads), an optional
+    state (B, heads, K, V) float32 (this object's own ``h_last`` continues the last call in place) and optional
+    marks (B, T) uint8, and returns ``(o, h_last)``. With ``keep`` a call also fills ``states`` and ``updates``,
+    which the backward pass takes. K and V are multiples of 8 up to 128."""
+
+    def __init__(self, B, T, heads, K, V, dtype="bf16", key_heads=None, normalize=True, keep=False, device="cuda"):
+        self.dims, self._dims = _delta_dims(B, T, heads, K, V, dtype, key_heads, normalize, "DeltaRule")
+        self.device, self.dtype, key_heads = _device(device), _DTYPES[dtype], self.dims.G
+        like = dict(dtype=self.dtype, device=self.device)
+        self.o = torch.empty((B, T, heads, V), **like)
+        self.h_last = torch.empty((B, heads, K, V), dtype=torch.float32, device=self.device)
+        self.states = torch.empty((B, heads, -(-T // STATE_TOKENS), K, V), **like) if keep else None
+        self.updates = torch.empty((B, T, heads, V), **like) if keep else None
+        index = _index(self.device)
+        self._qk, self._v = (self.dtype, torch.Size((B, T, key_heads, K)), index), (self.dtype, self.o.shape, index)
+        self._fb, self._state = (self.dtype, torch.Size((B, T, heads)), index), (torch.float32, self.h_last.shape, index)
+        self._marks = torch.uint8, torch.Size((B, T)), index
+        self._out = (self.o.data_ptr(), self.h_last.data_ptr(),
+                     *((self.states.data_ptr(), self.updates.data_ptr()) if keep else (0, 0)))
+        self._call = _Call("ssd_delta_rule_fwd", 8, 34, index)
+
+    def __call__(self, q, k, v, f, b, h0=None, reset=None, stream=None):
+        self._call(stream, *_heads("q", q, self._qk), *_heads("k", k, self._qk), *_heads("v", v, self._v),
+                   *_gate("f", f, self._fb), *_gate("b", b, self._fb), _dense("h0", h0, self._state),
+                   _dense("reset", reset, self._marks), *self._dims, *self._out)
+        return self.o, self.h_last
+
+
+class DeltaRuleBackward:
+    """The gradients of ``DeltaRule`` (``ssd_delta_rule_bwd``). ``__call__`` takes the forward pass's q, k, f, b, the
+    ``states`` and ``updates`` it kept, ``do`` and optionally ``dh_last``, and returns a dict: ``dq``, ``dk`` (summed
+    over the heads that share them), ``dv``, ``df``, ``db`` and ``dh0``."""
+
+    def __init__(self, B, T, heads, K, V, dtype="bf16", key_heads=None, normalize=True, device="cuda"):
+        self.dims, self._dims = _delta_dims(B, T, heads, K, V, dtype, key_heads, normalize, "DeltaRuleBackward")
+        self.device, self.dtype, key_heads = _device(device), _DTYPES[dtype], self.dims.G
+        index, like = _index(self.device), dict(dtype=self.dtype, device=self.device)
+        shapes = dict(dq=(B, T, key_heads, K), dk=(B, T, key_heads, K), dv=(B, T, heads, V), df=(B, T, heads), db=(B, T, heads))
+        self.grads = {n: torch.empty(s, **like) for n, s in shapes.items()}
+        self.grads["dh0"] = torch.empty((B, heads, K, V), dtype=torch.float32, device=self.device)
+        nbytes = load().ssd_delta_rule_bwd_workspace_bytes(self.dims)
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        g = self.grads
+        self._qk, self._v, self._fb = ((self.dtype, g[n].shape, index) for n in ("dq", "dv", "df"))
+        self._state = torch.float32, g["dh0"].shape, index
+        self._states = self.dtype, torch.Size((B, heads, -(-T // STATE_TOKENS), K, V)), index
+        self._marks = torch.uint8, torch.Size((B, T)), index
+        self._out = (*(g[n].data_ptr() for n in ("dq", "dk", "dv", "df", "db", "dh0")), self.workspace.data_ptr(), nbytes)
+        self._call = _Call("ssd_delta_rule_bwd", 10, 40, index)
+
+    def __call__(self, q, k, f, b, states, updates, do, dh_last=None, reset=None, stream=None):
+        self._call(stream, *_heads("q", q, self._qk), *_heads("k", k, self._qk), *_gate("f", f, self._fb),
+                   *_gate("b", b, self._fb), _dense("states", states, self._states), _dense("updates", updates, self._v),
+                   _dense("reset", reset, self._marks), *_heads("do", do, self._v), _dense("dh_last", dh_last, self._state),
+                   *self._dims, *self._out)
+        return dict(self.grads)
+
+
+class DeltaRuleStep:
+    """One token of B sequences (``ssd_delta_rule_step``). ``__call__`` takes q, k (B, key_heads, K), v (B, heads, V),
+    f, b (B, heads) and the state (B, heads, K, V) float32, and returns ``(o, state)``. The new state goes to this
+    object's ``state``, or to ``state_out``; passing the state itself there updates it in place."""
+
+    def __init__(self, B, heads, K, V, dtype="bf16", key_heads=None, normalize=True, device="cuda"):
+        self.dims, self._dims = _delta_dims(B, 1, heads, K, V, dtype, key_heads, normalize, "DeltaRuleStep")
+        self.device, self.dtype, key_heads = _device(device), _DTYPES[dtype], self.dims.G
+        self.o = torch.empty((B, heads, V), dtype=self.dtype, device=self.device)
+        self.state = torch.empty((B, heads, K, V), dtype=torch.float32, device=self.device)
+        index = _index(self.device)
+        self._qk, self._v = (self.dtype, torch.Size((B, key_heads, K)), index), (self.dtype, self.o.shape, index)
+        self._fb, self._state = (self.dtype, torch.Size((B, heads)), index), (torch.float32, self.state.shape, index)
+        self._rest, self._own = (*self._dims, self.o.data_ptr()), self.state.data_ptr()
+        self._call = _Call("ssd_delta_rule_step", 9, 31, index)
+
+    def __call__(self, q, k, v, f, b, state, state_out=None, stream=None):
+        to = self._own if state_out is None else _dense("state_out", state_out, self._state)
+        self._call(stream, *_token("q", q, self._qk), *_token("k", k, self._qk), *_token("v", v, self._v),
+                   *_token_gate("f", f, self._fb), *_token_gate("b", b, self._fb), _dense("state", state, self._state),
+                   *self._rest, to)
+        return self.o, self.state if state_out is None else state_out
+
+
+def _token(name, t, like):
+    """One token's (B, H, D) tensor with contiguous features, as ``_heads`` gives it."""
+    if (t.dtype, t.shape, t.get_device()) != like:
+        _refuse(name, t, like)
+    sb, sh, one = t.stride()
+    if one != 1 and like[1][2] != 1:
+        raise ValueError(f"{name} must have contiguous features")
+    return t.data_ptr(), sb, 0, sh
+
+
+def _token_gate(name, t, like):
+    if (t.dtype, t.shape, t.get_device()) != like:
+        _refuse(name, t, like)
+    sb, sh = t.stride()
+    return t.data_ptr(), sb, 0, sh
+
+
+# ---- gated norm
+
+
+def _float_bits(v):
+    return struct.unpack("I", struct.pack("f", v))[0]
+
+
+class GatedNorm:
+    """The norm behind a recurrence (``ssd_gated_norm_fwd``) over M rows of ``heads`` heads of D features:
+
+        u = x + s v (with ``skip``; else u = x),  y = w u / sqrt(mean(u^2) + eps) silu(z)
+
+    with a mean for each head. ``out`` is y's type: ``"bf16"``, ``"fp32"`` or ``"fp8"``. ``__call__`` takes x, z and v
+    as (M, heads D) tensors with contiguous rows, the weights w (heads D) float32 (None: ones) and the skip
+    connection's scales s (heads) float32. It returns y, or for ``"fp8"`` ``(q, scale)`` with scale
+    (ceil(heads D / 128), M): the operand that ``Fp8Product`` takes. D is a multiple of 8 up to 256."""
+
+    def __init__(self, M, heads, D, dtype="bf16", out="fp8", eps=1e-5, skip=False, device="cuda"):
+        _sizes(M=M, heads=heads, D=D)
+        self.device, self.skip, self.eps = _device(device), bool(skip), float(eps)
+        self.type, self.dtype, N = _type(dtype), _DTYPES[dtype], heads * D
+        if out not in _TYPES:
+            raise ValueError(f"out must be 'bf16', 'fp32' or 'fp8', not {out!r}")
+        if load().ssd_gated_norm_bwd_workspace_bytes(M, heads, D) == 0:
+            _raise(ssdc.SSDC_ERR_UNSUPPORTED, "GatedNorm")
+        self.scale = None
+        if out == "fp8":
+            self.y = fp8_empty(M, N, self.device)
+            self.scale = torch.empty((fp8_groups(N), M), dtype=torch.float32, device=self.device)
+        else:
+            self.y = torch.empty((M, N), dtype=_DTYPES[out], device=self.device)
+        index = _index(self.device)
+        self._like = self.dtype, torch.Size((M, N)), index
+        self._weights, self._scales = (torch.float32, torch.Size((N,)), index), (torch.float32, torch.Size((heads,)), index)
+        self._rest = (_float_bits(self.eps), M, heads, D, self.type, _TYPES[out], self.y.data_ptr(), self.y.stride(0),
+                      0 if self.scale is None else self.scale.data_ptr())
+        self._result = self.y if self.scale is None else (self.y, self.scale)
+        self._call = _Call("ssd_gated_norm_fwd", 11, 17, index)
+
+    def __call__(self, x, z, w=None, v=None, s=None, stream=None):
+        if (v is not None) != self.skip or (s is not None) != self.skip:
+            raise ValueError("v and s must be given exactly when the plan has a skip connection")
+        like = self._like
+        self._call(stream, *_rows("x", x, like), *_rows("z", z, like), _dense("w", w, self._weights), *_rows("v", v, like),
+                   _dense("s", s, self._scales), *self._rest)
+        return self._result
+
+
+class GatedNormBackward:
+    """The gradients of ``GatedNorm`` (``ssd_gated_norm_bwd``) from the forward pass's inputs. ``__call__`` returns a
+    dict: ``dx``, ``dz``, ``dw``, and with ``skip`` ``dv`` and ``ds``."""
+
+    def __init__(self, M, heads, D, dtype="bf16", eps=1e-5, skip=False, device="cuda"):
+        _sizes(M=M, heads=heads, D=D)
+        self.device, self.skip, self.eps = _device(device), bool(skip), float(eps)
+        self.type, self.dtype, N = _type(dtype), _DTYPES[dtype], heads * D
+        nbytes = load().ssd_gated_norm_bwd_workspace_bytes(M, heads, D)
+        if nbytes == 0:
+            _raise(ssdc.SSDC_ERR_UNSUPPORTED, "GatedNormBackward")
+        self.grads = {n: torch.empty((M, N), dtype=self.dtype, device=self.device) for n in (("dx", "dz", "dv") if skip else ("dx", "dz"))}
+        self.grads["dw"] = torch.empty(N, dtype=torch.float32, device=self.device)
+        if skip:
+            self.grads["ds"] = torch.empty(heads, dtype=torch.float32, device=self.device)
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        index = _index(self.device)
+        self._like = self.dtype, torch.Size((M, N)), index
+        self._weights, self._scales = (torch.float32, torch.Size((N,)), index), (torch.float32, torch.Size((heads,)), index)
+        g = self.grads
+        self._dims = (_float_bits(self.eps), M, heads, D, self.type)
+        self._out = (*_rows("dx", g["dx"], self._like), *_rows("dz", g["dz"], self._like), *_rows("dv", g.get("dv"), self._like),
+                     g["dw"].data_ptr(), g["ds"].data_ptr() if skip else 0, self.workspace.data_ptr(), nbytes)
+        self._call = _Call("ssd_gated_norm_bwd", 12, 25, index)
+
+    def __call__(self, dy, x, z, w=None, v=None, s=None, stream=None):
+        if (v is not None) != self.skip or (s is not None) != self.skip:
+            raise ValueError("v and s must be given exactly when the plan has a skip connection")
+        like = self._like
+        self._call(stream, *_rows("dy", dy, like), *_rows("x", x, like), *_rows("z", z, like), _dense("w", w, self._weights),
+                   *_rows("v", v, like), _dense("s", s, self._scales), *self._dims, *self._out)
+        return dict(self.grads)
+
+
 # ---- differentiable forms (once: a gradient of a gradient is an error)
 
 
@@ -609,3 +846,54 @@ def fp8_linear(x, w):
     """Differentiable x w^T in 8-bit products (``Fp8Linear``): returns a new (M, N) tensor
     (laid out as ``Fp8Product``'s)."""
     return _Fp8Linear.apply(x, w)
+
+
+class _DeltaRule(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, f, b, h0, reset, normalize):
+        (B, T, G, K), (H, V) = q.shape, v.shape[2:]
+        ctx.sizes = B, T, H, K, V, _dtype_name(v), G, normalize
+        ctx.set_materialize_grads(False)
+        plan = DeltaRule(*ctx.sizes, keep=True, device=v.device)
+        o, last = plan(q, k, v, f, b, h0=h0, reset=reset)
+        ctx.save_for_backward(q, k, f, b, plan.states, plan.updates, reset)
+        ctx.with_h0 = h0 is not None
+        return o, last
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do, dh_last):
+        q, k, f, b, states, updates, reset = ctx.saved_tensors
+        do = torch.zeros_like(updates) if do is None else _unit_last(do)  # None: not used
+        plan = DeltaRuleBackward(*ctx.sizes, device=do.device)
+        g = plan(q, k, f, b, states, updates, do, dh_last=None if dh_last is None else dh_last.contiguous(), reset=reset)
+        return g["dq"], g["dk"], g["dv"], g["df"], g["db"], g["dh0"] if ctx.with_h0 else None, None, None
+
+
+def delta_rule(q, k, v, f, b, h0=None, reset=None, normalize=True):
+    """Differentiable ``DeltaRule``: returns new ``(o, h_last)``."""
+    return _DeltaRule.apply(q, k, v, f, b, h0, reset, normalize)
+
+
+class _GatedNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, z, w, v, s, heads, eps):
+        ctx.sizes = x.shape[0], heads, x.shape[1] // heads, _dtype_name(x)
+        ctx.eps, ctx.skip = eps, v is not None
+        ctx.save_for_backward(x, z, w, v, s)
+        return GatedNorm(*ctx.sizes, out=ctx.sizes[3], eps=eps, skip=ctx.skip, device=x.device)(x, z, w, v, s)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, z, w, v, s = ctx.saved_tensors
+        plan = GatedNormBackward(*ctx.sizes, eps=ctx.eps, skip=ctx.skip, device=x.device)
+        g = plan(_unit_last(dy), x, z, w, v, s)
+        return g["dx"], g["dz"], None if w is None else g["dw"], g.get("dv"), g.get("ds"), None, None
+
+
+def gated_norm(x, z, w=None, v=None, s=None, heads=1, eps=1e-5):
+    """Differentiable ``GatedNorm`` of ``heads`` heads in the inputs' type: returns a new (M, heads D) tensor."""
+    if x.shape[1] % heads:
+        raise ValueError(f"heads must divide the {x.shape[1]} features, not {heads}")
+    return _GatedNorm.apply(x, z, w, v, s, heads, eps)

@@ -1,0 +1,329 @@
+// Host side of the delta rule and the gated norm declared in include/ssdc_block.h: argument
+// checks, then one launch sequence per call on the caller's stream. Nothing is allocated.
+#include <cstring>
+
+#include "block_args.h"
+
+namespace {
+
+using namespace ssdc::block;
+
+int check_delta(const ssd_delta_dims& d) {
+    if (d.B <= 0 || d.T <= 0 || d.H <= 0 || d.G <= 0 || d.K <= 0 || d.V <= 0) return SSDC_ERR_INVALID;
+    if (d.type != SSD_TYPE_F32 && d.type != SSD_TYPE_BF16) return SSDC_ERR_INVALID;
+    if (d.normalize != 0 && d.normalize != 1) return SSDC_ERR_INVALID;
+    if (d.H % d.G != 0) return SSDC_ERR_INVALID;
+    if (d.K % 8 != 0 || d.V % 8 != 0 || d.K > 128 || d.V > 128) return SSDC_ERR_UNSUPPORTED;
+    if (d.B > (1 << 20) || d.H > (1 << 20) || d.B * d.H > (1 << 20) || d.T > INT32_MAX - 63) return SSDC_ERR_UNSUPPORTED;
+    if ((double)d.B * (double)d.T * (double)d.H * (double)(d.K + d.V) > (double)kBig) return SSDC_ERR_UNSUPPORTED;
+    return SSDC_OK;
+}
+
+int64_t chunks(const ssd_delta_dims& d) { return (d.T + kDeltaChunk - 1) / kDeltaChunk; }
+
+// The inputs of a call, their spans, and the outputs outside of them. Inputs have three strides: an
+// output is checked against the whole of what an input spans.
+struct Spans {
+    uintptr_t lo[10], hi[10];
+    Array out[10];
+    int n_in = 0, n_out = 0;
+    int rc = SSDC_OK;
+    void fail(int code) {
+        if (rc == SSDC_OK) rc = code;
+    }
+    Heads heads(const ssd_heads_in& a, const ssd_delta_dims& d, int64_t H, int64_t n) {
+        const size_t e = type_bytes(d.type);
+        Heads h = {a.p, taken(a.stride_b, d.B), taken(a.stride_t, d.T), taken(a.stride_h, H)};
+        if (a.p == nullptr) fail(SSDC_ERR_INVALID);
+        const int64_t s[3] = {h.b, h.t, h.h}, m[3] = {d.B - 1, d.T - 1, H - 1};
+        double span = (double)n;
+        for (int i = 0; i < 3; ++i) {
+            if (s[i] < 0 || s[i] > kBig) fail(SSDC_ERR_INVALID);
+            span += (double)s[i] * (double)m[i];
+        }
+        if (span > (double)kBig) fail(SSDC_ERR_INVALID);
+        if (!aligned_to(a.p, e)) fail(SSDC_ERR_ALIGN);
+        if (rc == SSDC_OK) {
+            lo[n_in] = reinterpret_cast<uintptr_t>(a.p);
+            hi[n_in] = lo[n_in] + (uintptr_t)(s[0] * m[0] + s[1] * m[1] + s[2] * m[2] + n) * e;
+            ++n_in;
+        }
+        return h;
+    }
+    void dense_in(const void* p, int64_t n, size_t e, uintptr_t align, bool needed = false) {
+        if (p == nullptr) return needed ? fail(SSDC_ERR_INVALID) : void();
+        if (!aligned_to(p, align)) fail(SSDC_ERR_ALIGN);
+        lo[n_in] = reinterpret_cast<uintptr_t>(p);
+        hi[n_in] = lo[n_in] + (uintptr_t)n * e;
+        ++n_in;
+    }
+    // same: an input that this output may be
+    void output(const void* p, int64_t n, size_t e, bool needed = true, const void* same = nullptr) {
+        if (p == nullptr) return needed ? fail(SSDC_ERR_INVALID) : void();
+        if (!aligned_to(p, 16)) fail(SSDC_ERR_ALIGN);
+        const Array a = dense(p, n, e);
+        for (int k = 0; k < n_in; ++k)
+            if (!(same == p && lo[k] == a.lo() && hi[k] == a.hi()) && a.lo() < hi[k] && lo[k] < a.hi()) fail(SSDC_ERR_INVALID);
+        for (int k = 0; k < n_out; ++k)
+            if (overlaps(a, out[k])) fail(SSDC_ERR_INVALID);
+        out[n_out++] = a;
+    }
+};
+
+Delta problem(const ssd_delta_dims& d) {
+    Delta p = {};
+    p.T = d.T; p.B = (int)d.B; p.H = (int)d.H; p.G = (int)d.G; p.K = (int)d.K; p.V = (int)d.V;
+    p.bf16 = d.type == SSD_TYPE_BF16; p.normalize = d.normalize != 0;
+    return p;
+}
+
+int check_gated_norm(int64_t M, int64_t H, int64_t D, int type) {
+    if (M <= 0 || H <= 0 || D <= 0) return SSDC_ERR_INVALID;
+    if (type != SSD_TYPE_F32 && type != SSD_TYPE_BF16) return SSDC_ERR_INVALID;
+    if (D % 8 != 0 || D > 256 || H > 32768 || H * D > 32768 || M > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
+    return SSDC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ssd_delta_rule_fwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in v, ssd_heads_in f, ssd_heads_in b, const float* h0,
+                       const uint8_t* reset, ssd_delta_dims d, void* o, float* h_last, void* states, void* updates,
+                       cudaStream_t stream) {
+    int rc = check_delta(d);
+    if (rc != SSDC_OK) return rc;
+    if ((states == nullptr) != (updates == nullptr)) return SSDC_ERR_INVALID;
+    const size_t e = type_bytes(d.type);
+    const int64_t state = d.B * d.H * d.K * d.V, rows = d.B * d.T * d.H;
+    Spans a;
+    Delta p = problem(d);
+    p.q = a.heads(q, d, d.G, d.K); p.k = a.heads(k, d, d.G, d.K); p.v = a.heads(v, d, d.H, d.V);
+    p.f = a.heads(f, d, d.H, 1); p.beta = a.heads(b, d, d.H, 1);
+    a.dense_in(h0, state, 4, 16);
+    a.dense_in(reset, d.B * d.T, 1, 1);
+    a.output(o, rows * d.V, e);
+    a.output(h_last, state, 4, true, h0);
+    a.output(states, state * chunks(d), e, false);
+    a.output(updates, rows * d.V, e, false);
+    if (a.rc == SSDC_OK) a.rc = check_device();
+    if (a.rc != SSDC_OK) return a.rc;
+    p.h0 = h0; p.reset = reset; p.o = o; p.h_last = h_last; p.states = states; p.updates = updates;
+    (void)cudaGetLastError();
+    return done(delta_tokens_fwd_launch(p, stream));
+}
+
+int ssd_delta_rule_step(ssd_heads_in q, ssd_heads_in k, ssd_heads_in v, ssd_heads_in f, ssd_heads_in b, const float* state_in,
+                        ssd_delta_dims d, void* o, float* state_out, cudaStream_t stream) {
+    int rc = check_delta(d);
+    if (rc != SSDC_OK) return rc;
+    if (d.T != 1) return SSDC_ERR_INVALID;
+    const int64_t state = d.B * d.H * d.K * d.V;
+    Spans a;
+    Delta p = problem(d);
+    p.q = a.heads(q, d, d.G, d.K); p.k = a.heads(k, d, d.G, d.K); p.v = a.heads(v, d, d.H, d.V);
+    p.f = a.heads(f, d, d.H, 1); p.beta = a.heads(b, d, d.H, 1);
+    a.dense_in(state_in, state, 4, 16, true);
+    a.output(o, d.B * d.H * d.V, type_bytes(d.type));
+    a.output(state_out, state, 4, true, state_in);
+    if (a.rc == SSDC_OK) a.rc = check_device();
+    if (a.rc != SSDC_OK) return a.rc;
+    p.h0 = state_in; p.o = o; p.h_last = state_out;
+    (void)cudaGetLastError();
+    return done(delta_step_launch(p, stream));
+}
+
+size_t ssd_delta_rule_bwd_workspace_bytes(ssd_delta_dims d) {
+    if (check_delta(d) != SSDC_OK) return 0;
+    return delta_bwd_workspace(problem(d));
+}
+
+int ssd_delta_rule_bwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in f, ssd_heads_in b, const void* states, const void* updates,
+                       const uint8_t* reset, ssd_heads_in d_o, const float* dh_last, ssd_delta_dims d, void* dq, void* dk,
+                       void* dv, void* df, void* db, float* dh0, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    int rc = check_delta(d);
+    if (rc != SSDC_OK) return rc;
+    const size_t need = delta_bwd_workspace(problem(d)), e = type_bytes(d.type);
+    if (workspace == nullptr || !aligned_to(workspace, 256) || ws_bytes < need) return SSDC_ERR_WORKSPACE;
+    const int64_t state = d.B * d.H * d.K * d.V, rows = d.B * d.T * d.H, key_rows = d.B * d.T * d.G;
+    Spans a;
+    Delta p = problem(d);
+    p.q = a.heads(q, d, d.G, d.K); p.k = a.heads(k, d, d.G, d.K);
+    p.f = a.heads(f, d, d.H, 1); p.beta = a.heads(b, d, d.H, 1);
+    p.d_o = a.heads(d_o, d, d.H, d.V);
+    a.dense_in(states, state * chunks(d), e, 16, true);
+    a.dense_in(updates, rows * d.V, e, 16, true);
+    a.dense_in(reset, d.B * d.T, 1, 1);
+    a.dense_in(dh_last, state, 4, 16);
+    a.output(dq, key_rows * d.K, e);
+    a.output(dk, key_rows * d.K, e);
+    a.output(dv, rows * d.V, e);
+    a.output(df, rows, e);
+    a.output(db, rows, e);
+    a.output(dh0, state, 4, false, dh_last);
+    a.output(workspace, (int64_t)need, 1);
+    if (a.rc == SSDC_OK) a.rc = check_device();
+    if (a.rc != SSDC_OK) return a.rc;
+    p.in_states = states; p.in_updates = updates; p.reset = reset; p.dh_last = dh_last;
+    p.dq = dq; p.dk = dk; p.dv = dv; p.df = df; p.db = db; p.dh0 = dh0; p.ws = workspace;
+    (void)cudaGetLastError();
+    return done(delta_tokens_bwd_launch(p, stream));
+}
+
+int ssd_gated_norm_fwd(ssd_rows_in x, ssd_rows_in z, const float* w, ssd_rows_in v, const float* s, float eps, int64_t M,
+                       int64_t H, int64_t D, int32_t type, int32_t out_type, ssd_rows_out y, float* scale,
+                       cudaStream_t stream) {
+    int rc = check_gated_norm(M, H, D, type);
+    if (rc != SSDC_OK) return rc;
+    if (out_type != SSD_TYPE_F32 && out_type != SSD_TYPE_BF16 && out_type != SSD_TYPE_E4M3) return SSDC_ERR_INVALID;
+    if (!(eps >= 0.0f) || (v.p == nullptr) != (s == nullptr)) return SSDC_ERR_INVALID;
+    const bool fp8 = out_type == SSD_TYPE_E4M3;
+    const int64_t N = H * D;
+    if (fp8 != (scale != nullptr)) return SSDC_ERR_INVALID;
+    if (fp8 && (rc = check_fp8_rows(y.p, y.ld, M, N)) != SSDC_OK) return rc;
+    const size_t e = type_bytes(type), eo = type_bytes(out_type);
+    Args a;
+    a.input(rows(x.p, x.ld, M, N, e));
+    a.input(rows(z.p, z.ld, M, N, e));
+    a.input(rows(v.p, v.ld, M, N, e), false);
+    a.input(dense(w, N), false);
+    a.input(dense(s, H), false);
+    // a CTA reads all of what it writes over before it writes: y may be any of the three
+    const void* same1 = y.p == v.p ? v.p : x.p;
+    a.output(rows(y.p, y.ld, M, N, eo), true, same1, z.p);
+    a.output(dense(scale, M * groups(N)), fp8);
+    if (a.rc == SSDC_OK) a.rc = check_device();
+    if (a.rc != SSDC_OK) return a.rc;
+    GatedNorm p = {};
+    p.x = x.p; p.x_ld = row_stride(x.ld, M, N, e); p.z = z.p; p.z_ld = row_stride(z.ld, M, N, e);
+    p.v = v.p; p.v_ld = row_stride(v.ld, M, N, e); p.w = w; p.s = s; p.eps = eps;
+    p.M = M; p.H = (int)H; p.D = (int)D; p.bf16 = type == SSD_TYPE_BF16;
+    p.out_type = out_type; p.y = y.p; p.y_ld = row_stride(y.ld, M, N, eo); p.scale = scale;
+    (void)cudaGetLastError();
+    return done(gated_norm_fwd_launch(p, stream));
+}
+
+size_t ssd_gated_norm_bwd_workspace_bytes(int64_t M, int64_t H, int64_t D) {
+    if (check_gated_norm(M, H, D, SSD_TYPE_F32) != SSDC_OK) return 0;
+    return (size_t)gated_norm_bwd_parts(M, H, D) * (size_t)(H * D + H) * sizeof(float);
+}
+
+int ssd_gated_norm_bwd(ssd_rows_in dy, ssd_rows_in x, ssd_rows_in z, const float* w, ssd_rows_in v, const float* s, float eps,
+                       int64_t M, int64_t H, int64_t D, int32_t type, ssd_rows_out dx, ssd_rows_out dz, ssd_rows_out dv,
+                       float* dw, float* ds, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    int rc = check_gated_norm(M, H, D, type);
+    if (rc != SSDC_OK) return rc;
+    if (!(eps >= 0.0f) || (v.p == nullptr) != (s == nullptr) || (v.p == nullptr) != (dv.p == nullptr) ||
+        (v.p == nullptr) != (ds == nullptr))
+        return SSDC_ERR_INVALID;
+    const bool sums = dw != nullptr || ds != nullptr;
+    const size_t e = type_bytes(type), need = ssd_gated_norm_bwd_workspace_bytes(M, H, D);
+    if (sums && (workspace == nullptr || !aligned_to(workspace, 256) || ws_bytes < need)) return SSDC_ERR_WORKSPACE;
+    const int64_t N = H * D;
+    Args a;
+    a.input(rows(dy.p, dy.ld, M, N, e));
+    a.input(rows(x.p, x.ld, M, N, e));
+    a.input(rows(z.p, z.ld, M, N, e));
+    a.input(rows(v.p, v.ld, M, N, e), false);
+    a.input(dense(w, N), false);
+    a.input(dense(s, H), false);
+    a.output(rows(dx.p, dx.ld, M, N, e));
+    a.output(rows(dz.p, dz.ld, M, N, e));
+    a.output(rows(dv.p, dv.ld, M, N, e), false);
+    a.output(dense(dw, N), false);
+    a.output(dense(ds, H), false);
+    if (sums) a.output(dense(workspace, (int64_t)(need / 4)));
+    if (a.rc == SSDC_OK) a.rc = check_device();
+    if (a.rc != SSDC_OK) return a.rc;
+    GatedNorm p = {};
+    p.dy = dy.p; p.dy_ld = row_stride(dy.ld, M, N, e); p.x = x.p; p.x_ld = row_stride(x.ld, M, N, e);
+    p.z = z.p; p.z_ld = row_stride(z.ld, M, N, e); p.v = v.p; p.v_ld = row_stride(v.ld, M, N, e);
+    p.w = w; p.s = s; p.eps = eps; p.M = M; p.H = (int)H; p.D = (int)D; p.bf16 = type == SSD_TYPE_BF16;
+    p.dx = dx.p; p.dx_ld = row_stride(dx.ld, M, N, e); p.dz = dz.p; p.dz_ld = row_stride(dz.ld, M, N, e);
+    p.dv = dv.p; p.dv_ld = row_stride(dv.ld, M, N, e);
+    p.dw = dw; p.ds = ds; p.partial = sums ? static_cast<float*>(workspace) : nullptr;
+    (void)cudaGetLastError();
+    return done(gated_norm_bwd_launch(p, stream));
+}
+
+}  // extern "C"
+
+// The calls of this file by number (ssd_block_call).
+int ssdc::block::delta_call(int32_t call, const int64_t* words, cudaStream_t stream) {
+    const int64_t* w = words;
+    auto ptr = [&] { return reinterpret_cast<void*>(*w++); };
+    auto f32 = [&] { return static_cast<float*>(ptr()); };
+    auto i64 = [&] { return *w++; };
+    auto i32 = [&] { return (int32_t)*w++; };
+    auto real = [&] {
+        const uint32_t bits = (uint32_t)i64();
+        float v;
+        std::memcpy(&v, &bits, sizeof v);
+        return v;
+    };
+    auto heads = [&] { ssd_heads_in a; a.p = ptr(); a.stride_b = i64(); a.stride_t = i64(); a.stride_h = i64(); return a; };
+    auto rows_in = [&] { ssd_rows_in a; a.p = ptr(); a.ld = i64(); return a; };
+    auto rows_out = [&] { ssd_rows_out a; a.p = ptr(); a.ld = i64(); return a; };
+    auto dims = [&] {
+        ssd_delta_dims d;
+        d.B = i64(); d.T = i64(); d.H = i64(); d.G = i64(); d.K = i64(); d.V = i64(); d.type = i32(); d.normalize = i32();
+        return d;
+    };
+    switch (call) {
+        case SSD_CALL_DELTA_RULE_FWD: {
+            const ssd_heads_in q = heads(), k = heads(), v = heads(), f = heads(), b = heads();
+            const float* h0 = f32();
+            const uint8_t* reset = static_cast<const uint8_t*>(ptr());
+            const ssd_delta_dims d = dims();
+            void* o = ptr();
+            float* h_last = f32();
+            void* states = ptr();
+            return ssd_delta_rule_fwd(q, k, v, f, b, h0, reset, d, o, h_last, states, ptr(), stream);
+        }
+        case SSD_CALL_DELTA_RULE_STEP: {
+            const ssd_heads_in q = heads(), k = heads(), v = heads(), f = heads(), b = heads();
+            const float* state = f32();
+            const ssd_delta_dims d = dims();
+            void* o = ptr();
+            return ssd_delta_rule_step(q, k, v, f, b, state, d, o, f32(), stream);
+        }
+        case SSD_CALL_DELTA_RULE_BWD: {
+            const ssd_heads_in q = heads(), k = heads(), f = heads(), b = heads();
+            const void *states = ptr(), *updates = ptr();
+            const uint8_t* reset = static_cast<const uint8_t*>(ptr());
+            const ssd_heads_in d_o = heads();
+            const float* dh_last = f32();
+            const ssd_delta_dims d = dims();
+            void *dq = ptr(), *dk = ptr(), *dv = ptr(), *df = ptr(), *db = ptr();
+            float* dh0 = f32();
+            void* ws = ptr();
+            return ssd_delta_rule_bwd(q, k, f, b, states, updates, reset, d_o, dh_last, d, dq, dk, dv, df, db, dh0, ws,
+                                      (size_t)i64(), stream);
+        }
+        case SSD_CALL_GATED_NORM_FWD: {
+            const ssd_rows_in x = rows_in(), z = rows_in();
+            const float* weights = f32();
+            const ssd_rows_in v = rows_in();
+            const float* s = f32();
+            const float eps = real();
+            const int64_t M = i64(), H = i64(), D = i64();
+            const int32_t type = i32(), out_type = i32();
+            const ssd_rows_out y = rows_out();
+            return ssd_gated_norm_fwd(x, z, weights, v, s, eps, M, H, D, type, out_type, y, f32(), stream);
+        }
+        case SSD_CALL_GATED_NORM_BWD: {
+            const ssd_rows_in dy = rows_in(), x = rows_in(), z = rows_in();
+            const float* weights = f32();
+            const ssd_rows_in v = rows_in();
+            const float* s = f32();
+            const float eps = real();
+            const int64_t M = i64(), H = i64(), D = i64();
+            const int32_t type = i32();
+            const ssd_rows_out dx = rows_out(), dz = rows_out(), dv = rows_out();
+            float *dw = f32(), *ds = f32();
+            void* ws = ptr();
+            return ssd_gated_norm_bwd(dy, x, z, weights, v, s, eps, M, H, D, type, dx, dz, dv, dw, ds, ws, (size_t)i64(), stream);
+        }
+        default: return SSDC_ERR_INVALID;
+    }
+}

@@ -1,0 +1,664 @@
+// The delta rule token by token in fp32: forward, gradients, and one token for serving.
+//
+// A state's columns are independent of each other: u_t = beta (v_t - c S^T k_t) takes a column's
+// dot product with k_t, and S = c S + k_t u_t^T adds to it. So a warp holds 16 columns in registers,
+// 8 lanes to a column that have every 8th group of 4 rows each, and walks the tokens without a barrier
+// inside a tile of them; a CTA has all columns of one state, as the gradients of q and k sum over them.
+#include "block_common.cuh"
+#include "block_kernels.h"
+
+namespace ssdc {
+namespace block {
+namespace {
+
+constexpr int kTile = 8;    // tokens staged at a time
+constexpr int kMaxDim = 128;
+constexpr float kUnitEps = 1e-6f;
+
+template <typename T>
+__device__ __forceinline__ const T* row(const Heads& a, int64_t b, int64_t t, int h) {
+    return static_cast<const T*>(a.p) + b * a.b + t * a.t + h * a.h;
+}
+
+// 1 / (1 + exp(-z)) and its complement, to a few roundings.
+__device__ __forceinline__ float2 gate(float z) {
+    const float e = expf(-fabsf(z)), r = 1.0f / (1.0f + e);
+    return z >= 0.0f ? make_float2(r, e * r) : make_float2(e * r, r);
+}
+
+__device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
+}
+
+// A tile of tokens from t0 into shared memory in fp32, zeros behind the last token and feature.
+template <typename T>
+__device__ void stage(float (*to)[kMaxDim], const Heads& a, int b, int64_t t0, int64_t end, int h, int n) {
+    for (int i = threadIdx.x; i < kTile * kMaxDim; i += blockDim.x) {
+        const int t = i / kMaxDim, d = i % kMaxDim;
+        to[t][d] = t0 + t < end && d < n ? to_f32(row<T>(a, b, t0 + t, h)[d]) : 0.0f;
+    }
+}
+// The same from a dense (B, T, H, n) array.
+template <typename T>
+__device__ void stage_dense(float (*to)[kMaxDim], const void* p, const Delta& d, int b, int64_t t0, int64_t end, int h, int n) {
+    const Heads a = {p, d.T * d.H * n, (int64_t)d.H * n, n};
+    stage<T>(to, a, b, t0, end, h, n);
+}
+
+// Rows divided by their lengths: each warp takes every n-th token.
+__device__ void unit(float (*x)[kMaxDim], float scale) {
+    for (int t = threadIdx.x / 32; t < kTile; t += blockDim.x / 32) {
+        float4* r = reinterpret_cast<float4*>(x[t]) + threadIdx.x % 32;
+        float4 v = *r;
+        const float s = scale / sqrtf(warp_sum(dot4(v, v, 0.0f)) + kUnitEps);
+        *r = make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
+    }
+}
+
+// The decay and beta of a tile's tokens: {c, 1 - a, beta, 1 - beta}.
+template <typename T>
+__device__ void stage_gates(float4* to, const Delta& p, int b, int64_t t0, int64_t end, int h) {
+    const int t = threadIdx.x;
+    if (t < kTile) {
+        float4 g = make_float4(1.0f, 0.0f, 0.0f, 1.0f);
+        if (t0 + t < end) {
+            const float2 a = gate(to_f32(*row<T>(p.f, b, t0 + t, h))), be = gate(to_f32(*row<T>(p.beta, b, t0 + t, h)));
+            const bool first = p.reset != nullptr && p.reset[b * p.T + t0 + t] != 0;
+            g = make_float4(first ? 0.0f : a.x, first ? 0.0f : a.y, be.x, be.y);
+        }
+        to[t] = g;
+    }
+}
+
+template <int KR>
+struct Columns {  // a lane's part of a warp's 16 columns: rows 32 (i / 4) + 4 (lane % 8) + i % 4, 4 columns
+    float s[KR][4];
+    __device__ __forceinline__ static int row(int i) { return (i / 4) * 32 + (threadIdx.x & 7) * 4 + i % 4; }
+    __device__ __forceinline__ static int col() { return (threadIdx.x / 32) * 16 + ((threadIdx.x >> 3) & 3) * 4; }
+    template <typename T>
+    __device__ __forceinline__ void load(const T* p, int K, int V) {
+#pragma unroll
+        for (int i = 0; i < KR; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s[i][j] = p != nullptr && row(i) < K && col() < V ? to_f32(p[(int64_t)row(i) * V + col() + j]) : 0.0f;
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T* p, int K, int V) const {
+#pragma unroll
+        for (int i = 0; i < KR; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (row(i) < K && col() < V) p[(int64_t)row(i) * V + col() + j] = from_f32<T>(s[i][j]);
+    }
+    __device__ __forceinline__ static void vec(float* x, const float* from) {
+#pragma unroll
+        for (int i = 0; i < KR; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(from + row(i));
+            x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+        }
+    }
+    // the columns' dot products with x, in every lane of the columns
+    __device__ __forceinline__ void dots(const float* x, float* d) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            d[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < KR; ++i) d[j] = fmaf(s[i][j], x[i], d[j]);
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) d[j] += __shfl_xor_sync(0xffffffffu, d[j], o);
+        }
+    }
+    // the rows' sums of products with y over the warp's columns, to to[row]
+    __device__ __forceinline__ void sums(const float* y, float* to) const {
+#pragma unroll
+        for (int i = 0; i < KR; i += 4) {
+            float4 r;
+            float* e = reinterpret_cast<float*>(&r);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                float v = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v = fmaf(s[i + n][j], y[j], v);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                e[n] = v + __shfl_xor_sync(0xffffffffu, v, 16);
+            }
+            if ((threadIdx.x & 24) == 0) *reinterpret_cast<float4*>(to + row(i)) = r;
+        }
+    }
+};
+
+// A tile's rows of `n` values to a dense (B, T, H, n) array.
+template <typename T>
+__device__ void flush(void* p, float (*from)[kMaxDim], const Delta& d, int b, int64_t t0, int64_t end, int h, int n) {
+    for (int i = threadIdx.x; i < kTile * n; i += blockDim.x) {
+        const int t = i / n, c = i % n;
+        if (t0 + t < end) static_cast<T*>(p)[((b * d.T + t0 + t) * d.H + h) * n + c] = from_f32<T>(from[t][c]);
+    }
+}
+
+__device__ __forceinline__ void write4(float* to, const float* v) {
+    if ((threadIdx.x & 7) == 0) *reinterpret_cast<float4*>(to + Columns<4>::col()) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+template <typename T, int KR>
+__global__ void __launch_bounds__(256) delta_tokens_fwd(const Delta p) {
+    __shared__ float q[kTile][kMaxDim], k[kTile][kMaxDim], v[kTile][kMaxDim], o[kTile][kMaxDim], u[kTile][kMaxDim];
+    __shared__ float4 gates[kTile];
+    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, g = h / (p.H / p.G);
+    const int64_t chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk, seq = (int64_t)b * p.H + h, size = (int64_t)p.K * p.V;
+    Columns<KR> S;
+    S.load(p.h0 ? p.h0 + seq * size : nullptr, p.K, p.V);
+    for (int64_t t0 = 0; t0 < p.T; t0 += kTile) {
+        __syncthreads();
+        stage<T>(q, p.q, b, t0, p.T, g, p.K);
+        stage<T>(k, p.k, b, t0, p.T, g, p.K);
+        stage<T>(v, p.v, b, t0, p.T, h, p.V);
+        stage_gates<T>(gates, p, b, t0, p.T, h);
+        __syncthreads();
+        if (p.normalize) {
+            unit(q, rsqrtf((float)p.K));
+            unit(k, 1.0f);
+            __syncthreads();
+        }
+        if (p.states != nullptr && t0 % kDeltaChunk == 0)
+            S.store(static_cast<T*>(p.states) + (seq * chunks + t0 / kDeltaChunk) * size, p.K, p.V);
+        const int n = (int)min((int64_t)kTile, p.T - t0);
+        for (int t = 0; t < n; ++t) {
+            const float4 gt = gates[t];
+            float x[KR], d[4];
+            S.vec(x, k[t]);
+            S.dots(x, d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                d[j] = gt.z * fmaf(-gt.x, d[j], v[t][S.col() + j]);
+#pragma unroll
+                for (int i = 0; i < KR; ++i) S.s[i][j] = fmaf(x[i], d[j], gt.x * S.s[i][j]);
+            }
+            if (p.updates != nullptr) write4(u[t], d);
+            S.vec(x, q[t]);
+            S.dots(x, d);
+            write4(o[t], d);
+        }
+        __syncthreads();
+        flush<T>(p.o, o, p, b, t0, p.T, h, p.V);
+        if (p.updates != nullptr) flush<T>(p.updates, u, p, b, t0, p.T, h, p.V);
+    }
+    S.store(p.h_last + seq * size, p.K, p.V);
+}
+
+// What the launches of the backward pass leave for each other, in fp32.
+struct Between {
+    float *dq, *dk;  // (B, T, H, K): gradients of the normalised queries and keys, for each value head
+    float* e;        // (B, T, H): du . u
+    float* behind;   // (B, H, chunks, K, V): the gradient of the state behind each chunk
+};
+__host__ __device__ inline Between between(const Delta& p) {
+    const int64_t rows = p.B * p.T * p.H;
+    Between w;
+    w.behind = static_cast<float*>(p.ws);  // first: K V is a multiple of 64
+    w.dq = w.behind + (int64_t)p.B * p.H * ((p.T + kDeltaChunk - 1) / kDeltaChunk) * p.K * p.V;
+    w.dk = w.dq + rows * p.K;
+    w.e = w.dk + rows * p.K;
+    return w;
+}
+
+// From the last token to the first, with dS the gradient of the state behind a token:
+//   dS += q do^T, du = dS^T k, dv = z = beta du, dk = dS u (so far), dS = c (dS - k z^T).
+template <typename T, int KR>
+__global__ void __launch_bounds__(256) delta_tokens_bwd_reverse(const Delta p) {
+    extern __shared__ float sums[];  // [warps][kTile][kMaxDim]
+    __shared__ float q[kTile][kMaxDim], k[kTile][kMaxDim], d_o[kTile][kMaxDim], u[kTile][kMaxDim], z[kTile][kMaxDim];
+    __shared__ float4 gates[kTile];
+    __shared__ float e[8][kTile];
+    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, g = h / (p.H / p.G);
+    const int warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    const int64_t chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk, seq = (int64_t)b * p.H + h, size = (int64_t)p.K * p.V;
+    const Between w = between(p);
+    Columns<KR> dS;
+    dS.load(p.dh_last ? p.dh_last + seq * size : nullptr, p.K, p.V);
+    for (int64_t t0 = (p.T - 1) / kTile * kTile; t0 >= 0; t0 -= kTile) {
+        __syncthreads();
+        stage<T>(q, p.q, b, t0, p.T, g, p.K);
+        stage<T>(k, p.k, b, t0, p.T, g, p.K);
+        stage<T>(d_o, p.d_o, b, t0, p.T, h, p.V);
+        stage_dense<T>(u, p.in_updates, p, b, t0, p.T, h, p.V);
+        stage_gates<T>(gates, p, b, t0, p.T, h);
+        __syncthreads();
+        if (p.normalize) {
+            unit(q, rsqrtf((float)p.K));
+            unit(k, 1.0f);
+            __syncthreads();
+        }
+        const int n = (int)min((int64_t)kTile, p.T - t0);
+        if (t0 / kDeltaChunk != (t0 + kTile) / kDeltaChunk || t0 + kTile >= p.T)
+            dS.store(w.behind + (seq * chunks + t0 / kDeltaChunk) * size, p.K, p.V);
+        for (int t = n - 1; t >= 0; --t) {
+            const float4 gt = gates[t];
+            float x[KR], d[4], y[4];
+            dS.vec(x, q[t]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[j] = d_o[t][dS.col() + j];
+#pragma unroll
+                for (int i = 0; i < KR; ++i) dS.s[i][j] = fmaf(x[i], y[j], dS.s[i][j]);
+            }
+            dS.vec(x, k[t]);
+            dS.dots(x, d);
+            float du_u = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[j] = u[t][dS.col() + j];
+                du_u = fmaf(d[j], y[j], du_u);
+                d[j] *= gt.z;
+            }
+            dS.sums(y, sums + (warp * kTile + t) * kMaxDim);
+            write4(z[t], d);
+            du_u += __shfl_xor_sync(0xffffffffu, du_u, 8);
+            du_u += __shfl_xor_sync(0xffffffffu, du_u, 16);
+            if (threadIdx.x % 32 == 0) e[warp][t] = du_u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < KR; ++i) dS.s[i][j] = gt.x * fmaf(-x[i], d[j], dS.s[i][j]);
+        }
+        __syncthreads();
+        flush<T>(p.dv, z, p, b, t0, p.T, h, p.V);
+        for (int i = threadIdx.x; i < n * p.K; i += blockDim.x) {
+            const int t = i / p.K, c = i % p.K;
+            float s = 0.0f;
+            for (int r = 0; r < warps; ++r) s += sums[(r * kTile + t) * kMaxDim + c];
+            w.dk[((b * p.T + t0 + t) * p.H + h) * p.K + c] = s;
+        }
+        if (threadIdx.x < n) {
+            float s = 0.0f;
+            for (int r = 0; r < warps; ++r) s += e[r][threadIdx.x];
+            w.e[(b * p.T + t0 + threadIdx.x) * p.H + h] = s;
+        }
+    }
+    if (p.dh0 != nullptr) dS.store(p.dh0 + seq * size, p.K, p.V);
+}
+
+// Forward again through every chunk from its kept state: dq = S_t do, dk -= c S_{t-1} z.
+template <typename T, int KR>
+__global__ void __launch_bounds__(256) delta_tokens_bwd_forward(const Delta p) {
+    extern __shared__ float sums[];  // [2][warps][kTile][kMaxDim]
+    __shared__ float q[kTile][kMaxDim], k[kTile][kMaxDim], d_o[kTile][kMaxDim], u[kTile][kMaxDim], z[kTile][kMaxDim];
+    __shared__ float4 gates[kTile];
+    const int64_t chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk, seq = blockIdx.x / chunks, c0 = blockIdx.x % chunks;
+    const int b = (int)(seq / p.H), h = (int)(seq % p.H), g = h / (p.H / p.G);
+    const int warp = threadIdx.x / 32, warps = blockDim.x / 32, lane = threadIdx.x % 32;
+    const int64_t size = (int64_t)p.K * p.V, end = min(p.T, (c0 + 1) * kDeltaChunk);
+    const Between w = between(p);
+    float* sums_q = sums + warps * kTile * kMaxDim;
+    Columns<KR> S;
+    S.load(static_cast<const T*>(p.in_states) + (seq * chunks + c0) * size, p.K, p.V);
+    for (int64_t t0 = c0 * kDeltaChunk; t0 < end; t0 += kTile) {
+        __syncthreads();
+        stage<T>(q, p.q, b, t0, end, g, p.K);
+        stage<T>(k, p.k, b, t0, end, g, p.K);
+        stage<T>(d_o, p.d_o, b, t0, end, h, p.V);
+        stage_dense<T>(u, p.in_updates, p, b, t0, end, h, p.V);
+        stage_dense<T>(z, p.dv, p, b, t0, end, h, p.V);
+        stage_gates<T>(gates, p, b, t0, end, h);
+        __syncthreads();
+        if (p.normalize) {
+            unit(q, rsqrtf((float)p.K));
+            unit(k, 1.0f);
+            __syncthreads();
+        }
+        const int n = (int)min((int64_t)kTile, end - t0);
+        for (int t = 0; t < n; ++t) {
+            const float4 gt = gates[t];
+            float x[KR], y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = -gt.x * z[t][S.col() + j];
+            S.sums(y, sums + (warp * kTile + t) * kMaxDim);
+            S.vec(x, k[t]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float ut = u[t][S.col() + j];
+                y[j] = d_o[t][S.col() + j];
+#pragma unroll
+                for (int i = 0; i < KR; ++i) S.s[i][j] = fmaf(x[i], ut, gt.x * S.s[i][j]);
+            }
+            S.sums(y, sums_q + (warp * kTile + t) * kMaxDim);
+        }
+        __syncthreads();
+        for (int t = warp; t < n; t += warps) {
+            const int64_t at = ((b * p.T + t0 + t) * p.H + h) * p.K;
+            for (int c = lane; c < p.K; c += 32) {
+                float dk = w.dk[at + c], dq = 0.0f;
+                for (int r = 0; r < warps; ++r) {
+                    dk += sums[(r * kTile + t) * kMaxDim + c];
+                    dq += sums_q[(r * kTile + t) * kMaxDim + c];
+                }
+                w.dk[at + c] = dk;
+                w.dq[at + c] = dq;
+            }
+        }
+    }
+}
+
+// The gradients of f and b for one chunk. That of log a_t is the sum over what crosses t: pairs of a token
+// i >= t and a token j < t, the state in front with i >= t, j < t with the state behind, and both states. Each
+// is a product of its own sign, and none is taken away again, as a difference of two tokens' totals would:
+// where little is kept, totals of one cross by 1e-20.
+//   pair:       D_ij ((q_i.k_j) (do_i.u_j) - (k_i.k_j) (z_i.u_j))
+//   in front:   exp(G_i) (do_i.S0^T q_i - z_i.S0^T k_i)
+//   behind:     exp(G_C - G_j) u_j.dS^T k_j,  both: exp(G_C) <S0, dS>
+constexpr int kPitch = kMaxDim + 4;
+template <typename T, int KR>
+__global__ void __launch_bounds__(256) delta_tokens_bwd_gates(const Delta p) {
+    extern __shared__ float rows[];  // [5][kDeltaChunk][kPitch]: q, k, do, u, z
+    __shared__ float pair[kDeltaChunk][kDeltaChunk + 1], front[kDeltaChunk], behind[kDeltaChunk], part[2][8][kDeltaChunk];
+    __shared__ double sum[kDeltaChunk];
+    __shared__ int doc[kDeltaChunk];
+    __shared__ float both[8];
+    const int64_t chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk, seq = blockIdx.x / chunks, c0 = blockIdx.x % chunks;
+    const int b = (int)(seq / p.H), h = (int)(seq % p.H), g = h / (p.H / p.G), warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    const int64_t size = (int64_t)p.K * p.V, t0 = c0 * kDeltaChunk;
+    const int n = (int)min((int64_t)kDeltaChunk, p.T - t0);
+    const Between w = between(p);
+    constexpr int kRows = kDeltaChunk * kPitch;
+    float *q = rows, *k = q + kRows, *d_o = k + kRows, *u = d_o + kRows, *z = u + kRows;
+    const int64_t dense = (int64_t)p.H * p.V;
+    const Heads from[5] = {p.q, p.k, p.d_o, {p.in_updates, p.T * dense, dense, p.V}, {p.dv, p.T * dense, dense, p.V}};
+    for (int i = threadIdx.x; i < 5 * kDeltaChunk * kMaxDim; i += blockDim.x) {
+        const int a = i / (kDeltaChunk * kMaxDim), t = i / kMaxDim % kDeltaChunk, d = i % kMaxDim;
+        rows[a * kRows + t * kPitch + d] = t < n && d < (a < 2 ? p.K : p.V) ? to_f32(row<T>(from[a], b, t0 + t, a < 2 ? g : h)[d]) : 0.0f;
+    }
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        int r = 0;
+        for (int t = 0; t < n; ++t) {
+            const double f = to_f32(*row<T>(p.f, b, t0 + t, h));
+            s -= f > 0.0 ? log1p(exp(-f)) : log1p(exp(f)) - f;  // log sigmoid(f)
+            r += p.reset != nullptr && p.reset[b * p.T + t0 + t] != 0;
+            sum[t] = s;
+            doc[t] = r;
+        }
+    }
+    __syncthreads();
+    if (p.normalize) {
+        for (int t = warp; t < 2 * kDeltaChunk; t += warps) {
+            float4* r = reinterpret_cast<float4*>((t < kDeltaChunk ? q : k) + t % kDeltaChunk * kPitch) + threadIdx.x % 32;
+            float4 v = *r;
+            const float s = (t < kDeltaChunk ? rsqrtf((float)p.K) : 1.0f) / sqrtf(warp_sum(dot4(v, v, 0.0f)) + kUnitEps);
+            *r = make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
+        }
+        __syncthreads();
+    }
+    Columns<KR> S;
+    auto along = [&](const float* y, const float* d) {  // the columns' part of y.d
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fmaf(y[S.col() + j], d[j], s);
+        s += __shfl_xor_sync(0xffffffffu, s, 8);
+        return s + __shfl_xor_sync(0xffffffffu, s, 16);
+    };
+    float x[KR], d[4];
+    S.load(static_cast<const T*>(p.in_states) + (seq * chunks + c0) * size, p.K, p.V);
+    for (int t = 0; t < n; ++t) {
+        S.vec(x, q + t * kPitch);
+        S.dots(x, d);
+        float s = along(d_o + t * kPitch, d);
+        S.vec(x, k + t * kPitch);
+        S.dots(x, d);
+        s -= along(z + t * kPitch, d);
+        if (threadIdx.x % 32 == 0) part[0][warp][t] = s;
+    }
+    {
+        Columns<KR> dS;
+        dS.load(w.behind + (seq * chunks + c0) * size, p.K, p.V);
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < KR; ++i) {
+                s = fmaf(S.s[i][j], dS.s[i][j], s);
+                S.s[i][j] = dS.s[i][j];
+            }
+        s = warp_sum(s);
+        if (threadIdx.x % 32 == 0) both[warp] = s;
+    }
+    for (int t = 0; t < n; ++t) {
+        S.vec(x, k + t * kPitch);
+        S.dots(x, d);
+        const float s = along(u + t * kPitch, d);
+        if (threadIdx.x % 32 == 0) part[1][warp][t] = s;
+    }
+    for (int at = threadIdx.x; at < kDeltaChunk * kDeltaChunk; at += blockDim.x) {
+        const int i = at / kDeltaChunk, j = at % kDeltaChunk;
+        if (j >= i || i >= n) continue;
+        float qk = 0.0f, kk = 0.0f, ou = 0.0f, zu = 0.0f;
+        for (int c = 0; c < kMaxDim; c += 4) {
+            auto at4 = [&](const float* r, int t) { return *reinterpret_cast<const float4*>(r + t * kPitch + c); };
+            if (c < p.K) {
+                const float4 kj = at4(k, j);
+                qk = dot4(at4(q, i), kj, qk);
+                kk = dot4(at4(k, i), kj, kk);
+            }
+            if (c < p.V) {
+                const float4 uj = at4(u, j);
+                ou = dot4(at4(d_o, i), uj, ou);
+                zu = dot4(at4(z, i), uj, zu);
+            }
+        }
+        pair[i][j] = doc[i] == doc[j] ? expf((float)(sum[i] - sum[j])) * (qk * ou - kk * zu) : 0.0f;
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < n; r += blockDim.x) {
+        float f = 0.0f, e = 0.0f;
+        for (int s = 0; s < warps; ++s) f += part[0][s][r], e += part[1][s][r];
+        front[r] = doc[r] == 0 ? expf((float)sum[r]) * f : 0.0f;
+        behind[r] = doc[r] == doc[n - 1] ? expf((float)(sum[n - 1] - sum[r])) * e : 0.0f;
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < n; r += blockDim.x) {
+        float s = 0.0f;
+        if (doc[n - 1] == 0) {
+            for (int i = 0; i < warps; ++i) s += both[i];
+            s *= expf((float)sum[n - 1]);
+        }
+        for (int j = 0; j < r; ++j) s += behind[j];
+        for (int i = r; i < n; ++i) {
+            s += front[i];
+            for (int j = 0; j < r; ++j) s += pair[i][j];
+        }
+        const int64_t at = (b * p.T + t0 + r) * p.H + h;
+        const bool first = p.reset != nullptr && p.reset[b * p.T + t0 + r] != 0;
+        static_cast<T*>(p.df)[at] = from_f32<T>(first ? 0.0f : s * gate(to_f32(*row<T>(p.f, b, t0 + r, h))).y);
+        static_cast<T*>(p.db)[at] = from_f32<T>(w.e[at] * gate(to_f32(*row<T>(p.beta, b, t0 + r, h))).y);
+    }
+}
+
+// A key head's gradients: its value heads' summed, taken back through the division by the length.
+template <typename T>
+__global__ void __launch_bounds__(128) delta_tokens_bwd_finish(const Delta p) {
+    const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / 32, rows = p.B * p.T * p.G;
+    if (at >= rows) return;
+    const int lane = threadIdx.x % 32, g = (int)(at % p.G), R = p.H / p.G;
+    const int64_t bt = at / p.G, b = bt / p.T, t = bt % p.T;
+    const Between w = between(p);
+    for (int side = 0; side < 2; ++side) {
+        const T* x = row<T>(side ? p.k : p.q, b, t, g);
+        const float* d = (side ? w.dk : w.dq) + (bt * p.H + g * R) * p.K;
+        T* to = static_cast<T*>(side ? p.dk : p.dq) + at * p.K;
+        float v[4], s[4], xx = 0.0f, xs = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = lane + 32 * i;
+            v[i] = s[i] = 0.0f;
+            if (c < p.K) {
+                v[i] = to_f32(x[c]);
+                for (int r = 0; r < R; ++r) s[i] += d[(int64_t)r * p.K + c];
+            }
+            xx = fmaf(v[i], v[i], xx);
+            xs = fmaf(v[i], s[i], xs);
+        }
+        float scale = 1.0f, along = 0.0f;
+        if (p.normalize) {
+            const float inv = 1.0f / sqrtf(warp_sum(xx) + kUnitEps);
+            along = warp_sum(xs) * inv * inv;
+            scale = side ? inv : inv * rsqrtf((float)p.K);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (lane + 32 * i < p.K) to[lane + 32 * i] = from_f32<T>(scale * fmaf(-along, v[i], s[i]));
+    }
+}
+
+// One token. A state's 4 K V bytes are read once into registers (a thread has 4 columns of every
+// n-th row), give S^T k, take the update, give S^T q, and are written once: the kernel is bound by
+// memory, and everything of a CTA's state is in flight at once.
+template <typename T, int CG, int R>
+__global__ void __launch_bounds__(256) delta_step(const Delta p) {
+    constexpr int RG = 256 / CG;  // groups of rows; thread = group * CG + columns / 4
+    __shared__ float q[kMaxDim], k[kMaxDim], norms[2];
+    __shared__ float4 part[8][CG];
+    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, g = h / (p.H / p.G);
+    const int c = threadIdx.x % CG, rg = threadIdx.x / CG, col = 4 * c;
+    const int64_t size = (int64_t)p.K * p.V, seq = blockIdx.x;
+    const float* from = p.h0 + seq * size;
+    float4 s[R];
+    const bool mine = col < p.V;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int r = rg + i * RG;
+        s[i] = mine && r < p.K ? __ldcs(reinterpret_cast<const float4*>(from + (int64_t)r * p.V + col))
+                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    const float a = gate(to_f32(*row<T>(p.f, b, 0, h))).x, beta = gate(to_f32(*row<T>(p.beta, b, 0, h))).x;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (mine) {
+        const T* vp = row<T>(p.v, b, 0, h) + col;
+        v = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
+    }
+    if (threadIdx.x < 64) {  // one warp each for q and k
+        const int side = threadIdx.x / 32, lane = threadIdx.x % 32;
+        const T* x = row<T>(side ? p.k : p.q, b, 0, g);
+        float e[4], ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            e[i] = lane + 32 * i < p.K ? to_f32(x[lane + 32 * i]) : 0.0f;
+            ss = fmaf(e[i], e[i], ss);
+        }
+        float n = 1.0f;
+        if (p.normalize) n = (side ? 1.0f : rsqrtf((float)p.K)) / sqrtf(warp_sum(ss) + kUnitEps);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) (side ? k : q)[lane + 32 * i] = e[i] * n;
+    }
+    // the columns' dot products with x, summed over the groups of rows
+    auto dots = [&](const float* x) {
+        float4 d = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const float e = rg + i * RG < kMaxDim ? x[rg + i * RG] : 0.0f;
+            d.x = fmaf(s[i].x, e, d.x); d.y = fmaf(s[i].y, e, d.y);
+            d.z = fmaf(s[i].z, e, d.z); d.w = fmaf(s[i].w, e, d.w);
+        }
+#pragma unroll
+        for (int o = CG; o < 32; o *= 2) {
+            d.x += __shfl_xor_sync(0xffffffffu, d.x, o); d.y += __shfl_xor_sync(0xffffffffu, d.y, o);
+            d.z += __shfl_xor_sync(0xffffffffu, d.z, o); d.w += __shfl_xor_sync(0xffffffffu, d.w, o);
+        }
+        if (threadIdx.x % 32 < CG) part[threadIdx.x / 32][c] = d;
+        __syncthreads();
+        float4 t = part[0][c];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            const float4 e = part[i][c];
+            t.x += e.x; t.y += e.y; t.z += e.z; t.w += e.w;
+        }
+        return t;
+    };
+    __syncthreads();
+    const float4 held = dots(k);
+    const float4 u = make_float4(beta * fmaf(-a, held.x, v.x), beta * fmaf(-a, held.y, v.y), beta * fmaf(-a, held.z, v.z),
+                                 beta * fmaf(-a, held.w, v.w));
+    float* to = p.h_last + seq * size;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int r = rg + i * RG;
+        const float e = r < kMaxDim ? k[r] : 0.0f;
+        s[i] = make_float4(fmaf(e, u.x, a * s[i].x), fmaf(e, u.y, a * s[i].y), fmaf(e, u.z, a * s[i].z), fmaf(e, u.w, a * s[i].w));
+        if (mine && r < p.K) __stcs(reinterpret_cast<float4*>(to + (int64_t)r * p.V + col), s[i]);
+    }
+    __syncthreads();
+    const float4 o = dots(q);
+    if (mine && rg == 0) {
+        T* op = static_cast<T*>(p.o) + seq * p.V + col;
+        op[0] = from_f32<T>(o.x); op[1] = from_f32<T>(o.y); op[2] = from_f32<T>(o.z); op[3] = from_f32<T>(o.w);
+    }
+}
+
+template <typename T, int CG>
+void step_launch(const Delta& p, cudaStream_t stream) {
+    constexpr int RG = 256 / CG;
+    const int grid = p.B * p.H, rows = (p.K + RG - 1) / RG;
+    if constexpr (128 / RG >= 16)
+        if (rows > 8) return delta_step<T, CG, 16><<<grid, 256, 0, stream>>>(p);
+    if constexpr (128 / RG >= 8)
+        if (rows > 4) return delta_step<T, CG, 8><<<grid, 256, 0, stream>>>(p);
+    if constexpr (128 / RG >= 4)
+        if (rows > 2) return delta_step<T, CG, 4><<<grid, 256, 0, stream>>>(p);
+    delta_step<T, CG, 2><<<grid, 256, 0, stream>>>(p);
+}
+template <typename T>
+void step_launch(const Delta& p, cudaStream_t stream) {
+    if (p.V > 64) step_launch<T, 32>(p, stream);
+    else if (p.V > 32) step_launch<T, 16>(p, stream);
+    else step_launch<T, 8>(p, stream);
+}
+
+template <typename T, int KR>
+int fwd_launch(const Delta& p, cudaStream_t stream) {
+    delta_tokens_fwd<T, KR><<<p.B * p.H, 32 * ((p.V + 15) / 16), 0, stream>>>(p);
+    return 1;
+}
+
+template <typename T, int KR>
+int bwd_launch(const Delta& p, cudaStream_t stream) {
+    const int warps = (p.V + 15) / 16;
+    const int64_t chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk, rows = p.B * p.T * p.G;
+    const size_t one = (size_t)warps * kTile * kMaxDim * sizeof(float);
+    constexpr int kGates = 5 * kDeltaChunk * kPitch * 4;
+    static std::atomic<uint64_t> first{0}, second{0}, third{0};
+    if (allow_smem(delta_tokens_bwd_reverse<T, KR>, 8 * kTile * kMaxDim * 4, first) != cudaSuccess ||
+        allow_smem(delta_tokens_bwd_forward<T, KR>, 16 * kTile * kMaxDim * 4, second) != cudaSuccess ||
+        allow_smem(delta_tokens_bwd_gates<T, KR>, kGates, third) != cudaSuccess)
+        return SSDC_ERR_CUDA;
+    if (p.B * p.H * chunks > INT32_MAX || rows / 4 >= INT32_MAX) return SSDC_ERR_UNSUPPORTED;
+    delta_tokens_bwd_reverse<T, KR><<<p.B * p.H, 32 * warps, one, stream>>>(p);
+    delta_tokens_bwd_forward<T, KR><<<(unsigned)(p.B * p.H * chunks), 32 * warps, 2 * one, stream>>>(p);
+    delta_tokens_bwd_gates<T, KR><<<(unsigned)(p.B * p.H * chunks), 32 * warps, kGates, stream>>>(p);
+    delta_tokens_bwd_finish<T><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(p);
+    return 4;
+}
+
+}  // namespace
+
+int delta_step_launch(const Delta& p, cudaStream_t stream) {
+    if (p.bf16) step_launch<__nv_bfloat16>(p, stream);
+    else step_launch<float>(p, stream);
+    return 1;
+}
+
+int delta_tokens_fwd_launch(const Delta& p, cudaStream_t stream) {
+    if (p.bf16) return p.K > 64 ? fwd_launch<__nv_bfloat16, 16>(p, stream) : fwd_launch<__nv_bfloat16, 8>(p, stream);
+    return p.K > 64 ? fwd_launch<float, 16>(p, stream) : fwd_launch<float, 8>(p, stream);
+}
+
+int delta_tokens_bwd_launch(const Delta& p, cudaStream_t stream) {
+    if (p.bf16) return p.K > 64 ? bwd_launch<__nv_bfloat16, 16>(p, stream) : bwd_launch<__nv_bfloat16, 8>(p, stream);
+    return p.K > 64 ? bwd_launch<float, 16>(p, stream) : bwd_launch<float, 8>(p, stream);
+}
+
+size_t delta_bwd_workspace(const Delta& p) {
+    const int64_t rows = p.B * p.T * p.H, chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk;
+    return (size_t)(rows * (2 * p.K + 1) + p.B * p.H * chunks * p.K * p.V) * sizeof(float);
+}
+
+}  // namespace block
+}  // namespace ssdc

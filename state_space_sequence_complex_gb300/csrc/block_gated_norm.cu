@@ -1,0 +1,338 @@
+// The norm behind a recurrence: u = x + s v, y = w u rstd(u) z sigmoid(z) over every head's D features,
+// and its gradients.
+//
+// Bound by memory: every value is read once and kept in registers, a thread has 8 features in a row.
+// Where D is a power of two, a warp's 256 features hold whole heads and whole groups of 128 (the groups
+// of the 8-bit scales), and both are reduced by shuffles. For other D a CTA has whole heads (and whole
+// groups, where it writes 8 bits), and a head's sum goes through shared memory.
+#include <algorithm>
+
+#include "block_common.cuh"
+#include "block_kernels.h"
+
+namespace ssdc {
+namespace block {
+namespace {
+
+constexpr int kVec = 8;      // features of a thread
+constexpr int kWarps = 8;    // of a CTA whose warps have heads of their own
+
+template <typename T, bool kAligned>
+__device__ __forceinline__ void load8(float* v, const void* base, int64_t at) {
+    const T* p = static_cast<const T*>(base) + at;
+    if constexpr (!kAligned) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] = to_f32(p[i]);
+    } else if constexpr (sizeof(T) == 2) {
+        const uint4 r = __ldcs(reinterpret_cast<const uint4*>(p));
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[2 * i] = ptx::bf16_lo(w[i]), v[2 * i + 1] = ptx::bf16_hi(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 r = __ldcs(reinterpret_cast<const float4*>(p) + i);
+            v[4 * i] = r.x; v[4 * i + 1] = r.y; v[4 * i + 2] = r.z; v[4 * i + 3] = r.w;
+        }
+    }
+}
+
+template <typename T, bool kAligned>
+__device__ __forceinline__ void store8(void* base, int64_t at, const float* v) {
+    T* p = static_cast<T*>(base) + at;
+    if constexpr (!kAligned) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) p[i] = from_f32<T>(v[i]);
+    } else if constexpr (sizeof(T) == 2) {
+        uint4 r;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(p) = r;
+    } else {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// The sum over a head's threads: `n` lanes next to each other (a power of two), or, with shared memory,
+// threads first .. first + n - 1 of the CTA. `buffer`: another one in turn, so that one barrier will do.
+template <bool kWarp>
+__device__ __forceinline__ float head_sum(float v, int n, int first, float* buffer) {
+    if constexpr (kWarp) {
+        for (int o = 1; o < n; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    } else {
+        buffer[threadIdx.x] = v;
+        __syncthreads();
+        float s = 0.0f;
+        for (int i = 0; i < n; ++i) s += buffer[first + i];
+        return s;
+    }
+}
+
+// The features of a thread and its head: `piece` counts the row's parts (256 features, or a CTA's heads).
+struct Place {
+    int feature;  // first of the 8; at least N: none
+    int head, lanes, first;
+};
+template <bool kWarp>
+__device__ __forceinline__ Place place(int piece, int per_piece, int D, int N) {
+    Place a;
+    const int t = kWarp ? threadIdx.x % 32 : threadIdx.x;
+    a.feature = t < per_piece ? (piece * per_piece + t) * kVec : N;
+    a.head = a.feature < N ? a.feature / D : 0;
+    a.lanes = D / kVec;
+    a.first = t < per_piece ? t / a.lanes * a.lanes : 0;
+    return a;
+}
+
+template <typename T, int kOut, bool kWarp, bool kAligned>
+__global__ void __launch_bounds__(512) gated_norm_fwd(const GatedNorm p, int pieces, int per_piece) {
+    __shared__ float buffer[kWarp ? 1 : 512];
+    const int N = p.H * p.D;
+    const int64_t item = kWarp ? (int64_t)blockIdx.x * kWarps + threadIdx.x / 32 : blockIdx.x;
+    const int64_t m = item / pieces;
+    if (m >= p.M) return;  // whole warps, or the whole CTA
+    const Place a = place<kWarp>((int)(item % pieces), per_piece, p.D, N);
+    const bool mine = a.feature < N;
+    float u[kVec] = {}, z[kVec] = {};
+    if (mine) {
+        load8<T, kAligned>(u, p.x, m * p.x_ld + a.feature);
+        load8<T, kAligned>(z, p.z, m * p.z_ld + a.feature);
+        if (p.v != nullptr) {
+            float v[kVec];
+            load8<T, kAligned>(v, p.v, m * p.v_ld + a.feature);
+            const float s = p.s[a.head];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) u[i] = fmaf(s, v[i], u[i]);
+        }
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) ss = fmaf(u[i], u[i], ss);
+    ss = head_sum<kWarp>(ss, a.lanes, a.first, buffer);
+    const float rstd = 1.0f / sqrtf(ss / (float)p.D + p.eps);
+    float y[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const float w = p.w != nullptr && mine ? p.w[a.feature + i] : 1.0f;
+        y[i] = u[i] * rstd * w * (z[i] * sigmoid(z[i]));
+    }
+    if constexpr (kOut == SSD_TYPE_E4M3) {
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) amax = fmaxf(amax, mine ? fabsf(y[i]) : 0.0f);
+        amax = warp_max<16>(amax);
+        const Scale scale(amax);
+        if (mine) {
+            if (a.feature % SSD_FP8_GROUP == 0) p.scale[(int64_t)(a.feature / SSD_FP8_GROUP) * p.M + m] = scale.s;
+            float q[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) q[i] = scale.quotient(y[i]);
+            store_e4m3<kVec>(static_cast<uint8_t*>(p.y) + m * p.y_ld + a.feature, q);
+        }
+    } else if (mine) {
+        if constexpr (kOut == SSD_TYPE_BF16) store8<__nv_bfloat16, kAligned>(p.y, m * p.y_ld + a.feature, y);
+        else store8<float, kAligned>(p.y, m * p.y_ld + a.feature, y);
+    }
+}
+
+// Gradients. With g = z sigmoid(z), n = dy g w: du = rstd (n - u rstd^2 mean(n u)), so both sums of a head
+// (of u u and of n u) are taken at once; dw and ds stay in registers over a thread's rows and are added up
+// in a fixed order: rows of a thread, warps of a CTA, CTAs by gated_norm_dw.
+template <typename T, bool kWarp, bool kAligned, bool kSkip>
+__global__ void __launch_bounds__(kWarp ? 256 : 512) gated_norm_bwd(const GatedNorm p, int pieces, int per_piece, int parts) {
+    __shared__ float buffer[kWarp ? 1 : 4 * 512], sums[kWarp ? kWarps : 1][32][kVec + 1];
+    const int N = p.H * p.D, piece = blockIdx.x % pieces, part = blockIdx.x / pieces;
+    const Place a = place<kWarp>(piece, per_piece, p.D, N);
+    const bool mine = a.feature < N;
+    float w[kVec], dw[kVec] = {}, ds = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) w[i] = !mine ? 0.0f : p.w != nullptr ? p.w[a.feature + i] : 1.0f;
+    const float s = kSkip && mine ? p.s[a.head] : 0.0f, mean = 1.0f / (float)p.D;
+    int turn = 0;
+    for (int64_t m = kWarp ? (int64_t)part * kWarps + threadIdx.x / 32 : part; m < p.M; m += (int64_t)parts * (kWarp ? kWarps : 1)) {
+        float u[kVec] = {}, z[kVec] = {}, dy[kVec] = {}, v[kVec] = {};
+        if (mine) {
+            load8<T, kAligned>(u, p.x, m * p.x_ld + a.feature);
+            load8<T, kAligned>(z, p.z, m * p.z_ld + a.feature);
+            load8<T, kAligned>(dy, p.dy, m * p.dy_ld + a.feature);
+            if constexpr (kSkip) {
+                load8<T, kAligned>(v, p.v, m * p.v_ld + a.feature);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) u[i] = fmaf(s, v[i], u[i]);
+            }
+        }
+        float uu = 0.0f, nu = 0.0f, n[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            float sg, rest;
+            sigmoid_pair(z[i], sg, rest);
+            const float g = z[i] * sg, t = dy[i] * u[i];
+            n[i] = dy[i] * g;                      // times w later
+            z[i] = t * w[i] * fmaf(g, rest, sg);   // dz / rstd
+            dy[i] = t * g;                         // dw's term / rstd
+            uu = fmaf(u[i], u[i], uu);
+            n[i] *= w[i];
+            nu = fmaf(n[i], u[i], nu);
+        }
+        uu = head_sum<kWarp>(uu, a.lanes, a.first, buffer + (turn & 1) * 1024);
+        nu = head_sum<kWarp>(nu, a.lanes, a.first, buffer + (turn & 1) * 1024 + (kWarp ? 0 : 512));
+        ++turn;
+        const float rstd = 1.0f / sqrtf(fmaf(uu, mean, p.eps)), along = nu * mean * rstd * rstd;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            dw[i] = fmaf(dy[i], rstd, dw[i]);
+            z[i] *= rstd;
+            u[i] = rstd * fmaf(-along, u[i], n[i]);
+            if constexpr (kSkip) {
+                ds = fmaf(u[i], v[i], ds);
+                v[i] = s * u[i];
+            }
+        }
+        if (mine) {
+            store8<T, kAligned>(p.dx, m * p.dx_ld + a.feature, u);
+            store8<T, kAligned>(p.dz, m * p.dz_ld + a.feature, z);
+            if constexpr (kSkip) store8<T, kAligned>(p.dv, m * p.dv_ld + a.feature, v);
+        }
+    }
+    if (p.partial == nullptr) return;
+    float* to = p.partial + (int64_t)part * (N + p.H);
+    if constexpr (kWarp) {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sums[warp][lane][i] = dw[i];
+        sums[warp][lane][kVec] = head_sum<true>(ds, a.lanes, a.first, buffer);
+        __syncthreads();
+        for (int i = threadIdx.x; i < 32 * (kVec + 1); i += blockDim.x) {
+            const int l = i / (kVec + 1), e = i % (kVec + 1), feature = (piece * per_piece + l) * kVec;
+            float t = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kWarps; ++r) t += sums[r][l][e];
+            if (feature < N) {
+                if (e < kVec) to[feature + e] = t;
+                else if (feature % p.D == 0) to[N + feature / p.D] = t;
+            }
+        }
+    } else {
+        __syncthreads();
+        ds = head_sum<false>(ds, a.lanes, a.first, buffer);
+        if (mine) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) to[a.feature + i] = dw[i];
+            if (a.feature % p.D == 0) to[N + a.head] = ds;
+        }
+    }
+}
+
+// dw and ds from the CTAs' shares, 8 warps to 32 columns.
+__global__ void __launch_bounds__(256) gated_norm_dw(const GatedNorm p, int parts) {
+    __shared__ float sums[8][32];
+    const int N = p.H * p.D, lane = threadIdx.x % 32, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (c < N + p.H)
+        for (int r = warp; r < parts; r += 8) s += p.partial[(int64_t)r * (N + p.H) + c];
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+        for (int r = 1; r < 8; ++r) s += sums[r][lane];
+        if (c < N) {
+            if (p.dw != nullptr) p.dw[c] = s;
+        } else if (c < N + p.H && p.ds != nullptr) {
+            p.ds[c - N] = s;
+        }
+    }
+}
+
+bool power_of_two(int v) { return (v & (v - 1)) == 0; }
+
+bool rows_aligned(const void* p, int64_t ld, size_t elem) {
+    return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)elem % 16 == 0);
+}
+
+// How a row is dealt out: features of 8 per thread, whole heads to a piece, and with `groups` whole groups of 128.
+struct Split {
+    bool warp;
+    int per_piece, pieces, threads;
+};
+Split split(int H, int D, bool groups) {
+    const int N = H * D, vecs = N / kVec, head = D / kVec;
+    Split s;
+    s.warp = power_of_two(D);
+    if (s.warp) {
+        s.per_piece = 32;
+    } else {
+        int unit = head;
+        if (groups)
+            while (unit % 16 != 0) unit += head;  // at most 31 * 16 = 496
+        s.per_piece = unit * (unit <= 256 ? 256 / unit : 1);
+    }
+    s.pieces = (vecs + s.per_piece - 1) / s.per_piece;
+    s.threads = s.warp ? 32 * kWarps : (std::min(s.per_piece, vecs) + 31) / 32 * 32;
+    return s;
+}
+
+template <typename T, int kOut>
+int fwd_launch(const GatedNorm& p, bool aligned, cudaStream_t stream) {
+    const Split s = split(p.H, p.D, kOut == SSD_TYPE_E4M3);
+    const int64_t items = p.M * s.pieces, ctas = s.warp ? (items + kWarps - 1) / kWarps : items;
+    if (ctas > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
+    auto go = [&](auto kernel) { kernel<<<(unsigned)ctas, s.threads, 0, stream>>>(p, s.pieces, s.per_piece); };
+    if (s.warp) aligned ? go(gated_norm_fwd<T, kOut, true, true>) : go(gated_norm_fwd<T, kOut, true, false>);
+    else aligned ? go(gated_norm_fwd<T, kOut, false, true>) : go(gated_norm_fwd<T, kOut, false, false>);
+    return 1;
+}
+template <typename T>
+int fwd_launch(const GatedNorm& p, cudaStream_t stream) {
+    const size_t out = p.out_type == SSD_TYPE_F32 ? 4 : 2;
+    const bool aligned = rows_aligned(p.x, p.x_ld, sizeof(T)) && rows_aligned(p.z, p.z_ld, sizeof(T)) &&
+                         rows_aligned(p.v, p.v_ld, sizeof(T)) && (p.scale != nullptr || rows_aligned(p.y, p.y_ld, out));
+    if (p.out_type == SSD_TYPE_E4M3) return fwd_launch<T, SSD_TYPE_E4M3>(p, aligned, stream);
+    if (p.out_type == SSD_TYPE_BF16) return fwd_launch<T, SSD_TYPE_BF16>(p, aligned, stream);
+    return fwd_launch<T, SSD_TYPE_F32>(p, aligned, stream);
+}
+
+template <typename T, bool kSkip>
+int bwd_launch(const GatedNorm& p, bool aligned, cudaStream_t stream) {
+    const Split s = split(p.H, p.D, false);
+    const int parts = gated_norm_bwd_parts(p.M, p.H, p.D);
+    auto go = [&](auto kernel) { kernel<<<(unsigned)(s.pieces * parts), s.threads, 0, stream>>>(p, s.pieces, s.per_piece, parts); };
+    if (s.warp) aligned ? go(gated_norm_bwd<T, true, true, kSkip>) : go(gated_norm_bwd<T, true, false, kSkip>);
+    else aligned ? go(gated_norm_bwd<T, false, true, kSkip>) : go(gated_norm_bwd<T, false, false, kSkip>);
+    if (p.partial == nullptr) return 1;
+    gated_norm_dw<<<(p.H * p.D + p.H + 31) / 32, 256, 0, stream>>>(p, parts);
+    return 2;
+}
+template <typename T>
+int bwd_launch(const GatedNorm& p, cudaStream_t stream) {
+    bool aligned = true;
+    const void* rows[] = {p.dy, p.x, p.z, p.v, p.dx, p.dz, p.dv};
+    const int64_t lds[] = {p.dy_ld, p.x_ld, p.z_ld, p.v_ld, p.dx_ld, p.dz_ld, p.dv_ld};
+    for (int i = 0; i < 7; ++i) aligned = aligned && rows_aligned(rows[i], lds[i], sizeof(T));
+    return p.v != nullptr ? bwd_launch<T, true>(p, aligned, stream) : bwd_launch<T, false>(p, aligned, stream);
+}
+
+}  // namespace
+
+int gated_norm_fwd_launch(const GatedNorm& p, cudaStream_t stream) {
+    return p.bf16 ? fwd_launch<__nv_bfloat16>(p, stream) : fwd_launch<float>(p, stream);
+}
+
+int gated_norm_bwd_parts(int64_t M, int64_t H, int64_t D) {
+    const Split s = split((int)H, (int)D, false);
+    // about three CTAs of 256 threads an SM
+    const int64_t want = std::max<int64_t>(1, 456 * 256 / ((int64_t)s.threads * s.pieces));
+    return (int)std::min(want, s.warp ? (M + kWarps - 1) / kWarps : M);
+}
+
+int gated_norm_bwd_launch(const GatedNorm& p, cudaStream_t stream) {
+    return p.bf16 ? bwd_launch<__nv_bfloat16>(p, stream) : bwd_launch<float>(p, stream);
+}
+
+}  // namespace block
+}  // namespace ssdc

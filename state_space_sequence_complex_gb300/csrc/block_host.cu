@@ -412,7 +412,7 @@ int ssd_block_call(int32_t call, const int64_t* words, cudaStream_t stream) {
             void* ws = ptr();
             return ssd_fp8_matmul(a, a_scale, b, b_scale, b_scales, M, N, K, out_type, c, ws, (size_t)i64(), stream);
         }
-        default: return SSDC_ERR_INVALID;
+        default: return delta_call(call, words, stream);
     }
 }
 

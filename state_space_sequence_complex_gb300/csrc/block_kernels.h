@@ -148,5 +148,58 @@ int matmul_launch(const Matmul& p, cudaStream_t stream);
 bool matmul_is_few(int64_t M, int64_t N, int64_t K);
 int matmul_few_launch(const Matmul& p, cudaStream_t stream);
 
+// One delta-rule call. Strides in elements.
+struct Heads {
+    const void* p;
+    int64_t b, t, h;
+};
+struct Delta {
+    Heads q, k, v, f, beta;  // beta: before its sigmoid
+    const uint8_t* reset;
+    int64_t T;
+    int B, H, G, K, V;
+    bool bf16, normalize;
+    // forward
+    const float* h0;
+    void* o;
+    float* h_last;
+    void *states, *updates;  // or null
+    // backward
+    const void *in_states, *in_updates;
+    Heads d_o;
+    const float* dh_last;
+    void *dq, *dk, *dv, *df, *db;
+    float* dh0;
+    void* ws;
+};
+constexpr int kDeltaChunk = SSD_DELTA_STATE_TOKENS;
+int delta_step_launch(const Delta& p, cudaStream_t stream);
+int delta_tokens_fwd_launch(const Delta& p, cudaStream_t stream);
+int delta_tokens_bwd_launch(const Delta& p, cudaStream_t stream);
+size_t delta_bwd_workspace(const Delta& p);
+
+// One gated-norm call; out_type as in the header.
+struct GatedNorm {
+    const void *x, *z, *v, *dy;
+    int64_t x_ld, z_ld, v_ld, dy_ld;
+    const float *w, *s;
+    float eps;
+    int64_t M;
+    int H, D;
+    bool bf16;
+    int out_type;
+    void* y;
+    int64_t y_ld;
+    float* scale;
+    void *dx, *dz, *dv;
+    int64_t dx_ld, dz_ld, dv_ld;
+    float *dw, *ds, *partial;
+};
+int gated_norm_fwd_launch(const GatedNorm& p, cudaStream_t stream);
+int gated_norm_bwd_parts(int64_t M, int64_t H, int64_t D);  // rows of H D + H floats that `partial` holds
+int gated_norm_bwd_launch(const GatedNorm& p, cudaStream_t stream);
+
+int delta_call(int32_t call, const int64_t* words, cudaStream_t stream);  // the calls of block_delta_host.cu, by number
+
 }  // namespace block
 }  // namespace ssdc

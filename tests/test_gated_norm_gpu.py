@@ -1,0 +1,185 @@
+"""Parity of the gated norm with its formula in 64 bits, and of its gradients with automatic differentiation.
+
+Tolerances, relative to the norm of the result. fp32 results: a mean of at most 256 squares, a few products and the
+hardware's exponential, off by |z| 1e-7: 1e-5; dw and ds are sums of such terms over the rows. bfloat16 results are
+those rounded once, by at most 2^-8 of the smallest value of a binade. e4m3 values: a quotient that fp32 moves across
+a rounding boundary is one step (2^-3) off, fewer than 1e-3 of the values: 2^-3 sqrt(1e-3) = 4e-3."""
+import pytest
+import torch
+
+from state_space_sequence_complex_gb300 import block, ssdc
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+TOL = {torch.bfloat16: 2.0 ** -8, torch.float32: 1e-5}
+
+
+def randn(*shape, seed, dtype=torch.float32, mean=0.0, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g, dtype=torch.float64) * std + mean).to(dtype).cuda()
+
+
+def close(got, want, what=""):
+    tol, got, want = TOL[got.dtype], got.double(), want.detach().double()
+    assert got.shape == want.shape and torch.equal(torch.isfinite(got), torch.isfinite(want)), what
+    ok = torch.isfinite(want)
+    e = float((got[ok] - want[ok]).norm() / want[ok].norm().clamp_min(1e-300))
+    assert e <= tol, f"{what}: {e:.3e}"
+
+
+def make(M, H, D, dtype, skip, seed=0):
+    x = dict(x=randn(M, H * D, seed=seed, dtype=DT[dtype], std=2.0), z=randn(M, H * D, seed=seed + 1, dtype=DT[dtype], std=2.0),
+             w=randn(H * D, seed=seed + 2, mean=1.0, std=0.3), v=None, s=None, dy=randn(M, H * D, seed=seed + 3, dtype=DT[dtype]))
+    if skip:
+        x["v"], x["s"] = randn(M, H * D, seed=seed + 4, dtype=DT[dtype]), randn(H, seed=seed + 5)
+    return x
+
+
+def reference(x, H, eps=1e-5):
+    d = {n: x[n].double().requires_grad_() for n in ("x", "z", "w", "v", "s") if x[n] is not None}
+    M, N = x["x"].shape
+    u = d["x"].view(M, H, N // H)
+    if x["v"] is not None:
+        u = u + d["s"][:, None] * d["v"].view(M, H, N // H)
+    y = (u / (u.square().mean(-1, keepdim=True) + eps).sqrt()).flatten(1)
+    y = (y * d["w"] if x["w"] is not None else y) * d["z"] * torch.sigmoid(d["z"])
+    gs = torch.autograd.grad((y * x["dy"].double()).sum(), list(d.values()))
+    return y.detach(), dict(zip(["d" + n for n in d], gs))
+
+
+SHAPES = [(1, 1, 8), (8, 16, 64), (3, 5, 72), (1000, 4, 128), (37, 3, 256), (65, 2, 24), (9, 1, 248), (130, 7, 40), (5, 40, 8),
+          (20, 9, 200), (3, 128, 256), (300, 33, 16)]
+ids = dict(ids=lambda s: "x".join(map(str, s)))
+
+
+@pytest.mark.parametrize("skip", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", SHAPES, **ids)
+def test_forward_and_gradients(shape, dtype, skip):
+    M, H, D = shape
+    x = make(*shape, dtype, skip, seed=sum(shape))
+    want, grads = reference(x, H)
+    for out in ("bf16", "fp32"):
+        close(block.GatedNorm(M, H, D, dtype, out=out, skip=skip)(x["x"], x["z"], x["w"], x["v"], x["s"]), want, out)
+    got = block.GatedNormBackward(M, H, D, dtype, skip=skip)(x["dy"], x["x"], x["z"], x["w"], x["v"], x["s"])
+    assert sorted(got) == sorted(grads)
+    for n in grads:
+        close(got[n], grads[n], n)
+
+
+@pytest.mark.parametrize("skip", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", SHAPES, **ids)
+def test_8_bits(shape, dtype, skip):
+    M, H, D = shape
+    x = make(*shape, dtype, skip, seed=sum(shape) + 1)
+    want, _ = reference(x, H)
+    q, scale = block.GatedNorm(M, H, D, dtype, skip=skip)(x["x"], x["z"], x["w"], x["v"], x["s"])
+    N, NB = H * D, -(-H * D // 128)
+    assert scale.shape == (NB, M)
+    full = torch.nn.functional.pad(want, (0, NB * 128 - N)).reshape(M, NB, 128)
+    close(scale, (full.abs().amax(2).clamp_min(2.0 ** -100) / 448).t(), "scale")
+    quotient = (full / scale.double().t()[..., None]).reshape(M, NB * 128)[:, :N].clamp(-448, 448)
+    ref = quotient.float().to(torch.float8_e4m3fn).double()
+    assert float((q.double() - ref).norm() / ref.norm().clamp_min(1e-300)) <= 4e-3
+
+
+def test_no_weights():
+    x = make(10, 3, 72, "bf16", False)
+    x["w"] = None
+    want, grads = reference(x, 3)
+    close(block.GatedNorm(10, 3, 72, out="bf16")(x["x"], x["z"]), want)
+    got = block.GatedNormBackward(10, 3, 72)(x["dy"], x["x"], x["z"])
+    for n in grads:
+        close(got[n], grads[n], n)
+
+
+@pytest.mark.parametrize("D", [64, 40])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_that_start_anywhere(D, dtype):
+    M, H = 33, 3
+    wide = randn(M, 4 * H * D + 5, seed=3, dtype=DT[dtype])
+    x = make(M, H, D, dtype, True, seed=4)
+    for i, n in enumerate(("x", "z", "v", "dy")):
+        x[n] = wide[:, 1 + i * H * D:1 + (i + 1) * H * D]
+    want, grads = reference(x, H)
+    close(block.GatedNorm(M, H, D, dtype, out=dtype, skip=True)(x["x"], x["z"], x["w"], x["v"], x["s"]), want)
+    q, s = block.GatedNorm(M, H, D, dtype, skip=True)(x["x"], x["z"], x["w"], x["v"], x["s"])
+    q2, s2 = block.GatedNorm(M, H, D, dtype, skip=True)(*(x[n].contiguous() for n in ("x", "z", "w", "v", "s")))
+    assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
+    got = block.GatedNormBackward(M, H, D, dtype, skip=True)(x["dy"], x["x"], x["z"], x["w"], x["v"], x["s"])
+    for n in grads:
+        close(got[n], grads[n], n)
+
+
+@pytest.mark.parametrize("D", [64, 40])
+def test_zeros_infinities_and_nans_stay_in_their_head(D):
+    M, H = 4, 5
+    x = make(M, H, D, "fp32", False, seed=6)
+    clean = block.GatedNorm(M, H, D, "fp32", out="fp32")(x["x"], x["z"], x["w"])
+    x["x"][0] = 0.0
+    x["x"][1, D + 3] = float("inf")
+    x["x"][2, 2 * D] = float("nan")
+    x["z"][3, 5] = float("-inf")
+    y = block.GatedNorm(M, H, D, "fp32", out="fp32")(x["x"], x["z"], x["w"])
+    assert (y[0] == 0).all()
+    assert torch.isnan(y[1, D + 3]) and (y[1, D:D + 3] == 0).all()
+    assert torch.isnan(y[2, 2 * D:3 * D]).all()
+    assert torch.isnan(y[3, 5]) and torch.isfinite(y[3, 6:]).all()
+    assert torch.equal(y[1, :D], clean[1, :D]) and torch.equal(y[2, 3 * D:], clean[2, 3 * D:])
+
+
+def test_repeated_and_captured():
+    x = make(777, 4, 64, "bf16", True, seed=7)
+    args = (x["x"], x["z"], x["w"], x["v"], x["s"])
+    plan, back = block.GatedNorm(777, 4, 64, skip=True), block.GatedNormBackward(777, 4, 64, skip=True)
+    q, s = (t.clone() for t in plan(*args))
+    g = {n: t.clone() for n, t in back(x["dy"], *args).items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q2, s2 = plan(*args)
+        g2 = back(x["dy"], *args)
+    for t in (q2, s2, *g2.values()):
+        t.view(torch.uint8).zero_()
+    graph.replay()
+    assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s2, s)
+    for n in g:
+        assert torch.equal(g2[n], g[n]), n
+
+
+@pytest.mark.parametrize("skip", [False, True])
+def test_differentiable(skip):
+    x = make(50, 3, 32, "fp32", skip, seed=8)
+    _, grads = reference(x, 3)
+    leaves = {n: x[n].requires_grad_() for n in ("x", "z", "w", "v", "s") if x[n] is not None}
+    y = block.gated_norm(**leaves, heads=3)
+    for n, g in zip(leaves, torch.autograd.grad(y, list(leaves.values()), x["dy"])):
+        close(g, grads["d" + n], n)
+
+
+def test_rows_behind_are_left_alone():
+    """Outputs of a plan's rows only: what lies between 8-bit rows stays."""
+    plan = block.GatedNorm(5, 1, 40)
+    whole = plan.y.as_strided((5, 48), (48, 1)).view(torch.uint8)
+    whole.fill_(7)
+    x = make(5, 1, 40, "bf16", False)
+    plan(x["x"], x["z"], x["w"])
+    assert (whole[:, 40:] == 7).all() and not (whole[:, :40] == 7).all()
+
+
+def test_refusals():
+    for H, D in ((2, 12), (1, 264), (200, 256)):
+        with pytest.raises(ssdc.SSDCError):
+            block.GatedNorm(4, H, D)
+    x = make(4, 2, 16, "bf16", True)
+    plan = block.GatedNorm(4, 2, 16)
+    with pytest.raises(ValueError, match="skip"):
+        plan(x["x"], x["z"], x["w"], x["v"], x["s"])
+    with pytest.raises(ValueError, match="skip"):
+        block.GatedNormBackward(4, 2, 16, skip=True)(x["dy"], x["x"], x["z"], x["w"], x["v"])
+    with pytest.raises(TypeError):
+        plan(x["x"].float(), x["z"])
+    with pytest.raises(ValueError, match="divide"):
+        block.gated_norm(x["x"], x["z"], heads=3)
+    with pytest.raises(ValueError, match="out"):
+        block.GatedNorm(4, 2, 16, out="fp16")
