@@ -1,0 +1,232 @@
+// What the delta rule's chunk kernels share: matrix instructions on register fragments, tiles in shared
+// memory, and the preparation of a chunk.
+//
+// Chunks of C = 64 tokens. With G_i the sum of log a up to token i, Gam_i = exp(G_i), gam_j = exp(G_C - G_j),
+// D_ij = exp(G_i - G_j) for i >= j, and q, k scaled to rq q, rk k:
+//   X = v - Gam (k S0) - A U,   U = beta X,   A_ij = D_ij rk_i rk_j k_i.k_j (i > j)
+//   O = Gam q S0 + P U,         P_ij = D_ij rq_i rk_j q_i.k_j (i >= j)
+//   S = Gam_C S0 + k^T gam U
+// U is solved for in four blocks of 16 tokens: U_r = T_r (beta (X_r - sum over c < r of A_rc U_c)) with T_r the
+// inverse of I + beta A_rr, found by substitution in fp32. A reset takes log2 c = -256: 2^-256 is zero in fp32.
+//
+// Matrix instructions are mma.sync m16n8k16 (bf16 operands, fp32 sums): a chain of products of 64 rows whose
+// results are the next one's operands. Sums leave the instruction in the layout in which two neighbouring
+// 8-column tiles are the next one's A operand, so a warp that owns 16 columns of the state runs the whole chain
+// in its registers, without a barrier and without the way through tensor memory, registers and shared memory
+// that a tcgen05 product's result takes to become an operand. Its rate, measured on this GPU, is 1,024
+// multiply-adds a clock and SM (600 TFLOP/s); 21 clocks from operands to sums.
+#pragma once
+
+#include "block_common.cuh"
+#include "block_kernels.h"
+
+namespace ssdc {
+namespace block {
+namespace delta {
+
+constexpr int C = kDeltaChunk;
+constexpr int kPrep = 128;          // threads that prepare chunks
+constexpr float kUnitEps = 1e-6f;
+constexpr float kLog2e = 1.44269504f;
+
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm(uint32_t* r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t* r, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void stsm_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float v) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v));
+    return e;
+}
+
+// Barriers of some of a CTA's warps: those that wait, and those that only say they are there.
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+// Two values as a pair of bf16, the first in the low half.
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// The pair's remainders: with the pair itself 16 bits or more of each value.
+__device__ __forceinline__ uint32_t pack_rest(float lo, float hi, uint32_t p) {
+    return pack(lo - ptx::bf16_lo(p), hi - ptx::bf16_hi(p));
+}
+// Two neighbouring 8-column tiles of sums as an A operand, in two parts.
+struct Split {
+    uint32_t hi[4], lo[4];
+    __device__ __forceinline__ void set(const float* t0, const float* t1) {
+        hi[0] = pack(t0[0], t0[1]); hi[1] = pack(t0[2], t0[3]); hi[2] = pack(t1[0], t1[1]); hi[3] = pack(t1[2], t1[3]);
+        lo[0] = pack_rest(t0[0], t0[1], hi[0]); lo[1] = pack_rest(t0[2], t0[3], hi[1]);
+        lo[2] = pack_rest(t1[0], t1[1], hi[2]); lo[3] = pack_rest(t1[2], t1[3], hi[3]);
+    }
+};
+
+// A tile's 16-byte unit u of row r: units are moved by the row's low bits, so that 8 rows of one unit
+// are in 8 different sets of banks. kPitch: bytes of a row, 128 or 256.
+template <int kPitch>
+__device__ __forceinline__ uint32_t unit_at(uint32_t tile, int r, int u) {
+    return tile + r * kPitch + ((u ^ (r & 7)) << 4);
+}
+// Lane addresses of four 8 x 8 matrices. rows_k: B operand from rows n with k along them, two n-tiles
+// from row n0 and 16 values of k from unit u. cols_k: B operand from rows k (16 from k0) with n along them, units
+// u and u + 1. rows_a: A operand, 16 rows from r0. cols_a: A operand of the transposed tile, 16 columns from unit u as
+// its rows and 16 rows from k0 as its k.
+template <int kPitch>
+__device__ __forceinline__ uint32_t rows_k(uint32_t tile, int n0, int u) {
+    const int l = threadIdx.x % 32, m = l / 8;
+    return unit_at<kPitch>(tile, n0 + 8 * (m / 2) + l % 8, u + m % 2);
+}
+template <int kPitch>
+__device__ __forceinline__ uint32_t cols_k(uint32_t tile, int k0, int u) {
+    const int l = threadIdx.x % 32, m = l / 8;
+    return unit_at<kPitch>(tile, k0 + 8 * (m % 2) + l % 8, u + m / 2);
+}
+template <int kPitch>
+__device__ __forceinline__ uint32_t rows_a(uint32_t tile, int r0, int u) {
+    const int l = threadIdx.x % 32, m = l / 8;
+    return unit_at<kPitch>(tile, r0 + 8 * (m % 2) + l % 8, u + m / 2);
+}
+template <int kPitch>
+__device__ __forceinline__ uint32_t cols_a(uint32_t tile, int k0, int u) {
+    const int l = threadIdx.x % 32, m = l / 8;
+    return unit_at<kPitch>(tile, k0 + 8 * (m / 2) + l % 8, u + m % 2);
+}
+
+// A strip of 16 columns, rows of 32 bytes: unit u (0, 1) of row r.
+__device__ __forceinline__ uint32_t strip_at(uint32_t strip, int r, int u) { return strip + r * 32 + ((u ^ ((r >> 2) & 1)) << 4); }
+// Lane addresses of two 8-row groups from row r0 and both units.
+__device__ __forceinline__ uint32_t strip_rows(uint32_t strip, int r0) {
+    const int l = threadIdx.x % 32, m = l / 8;
+    return strip_at(strip, r0 + 8 * (m / 2) + l % 8, m % 2);
+}
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void store16(uint32_t to, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 load16(uint32_t from) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+    return v;
+}
+__device__ __forceinline__ void stsm(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Eight bf16 of a row that starts anywhere.
+__device__ __forceinline__ uint4 gather8(const __nv_bfloat16* p) {
+    uint4 v;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = (uint32_t)__bfloat16_as_ushort(p[2 * i]) | (uint32_t)__bfloat16_as_ushort(p[2 * i + 1]) << 16;
+    return v;
+}
+
+// Whether every row of an array starts on 16 bytes.
+inline bool whole_units(const Heads& a) {
+    return reinterpret_cast<uintptr_t>(a.p) % 16 == 0 && a.b % 8 == 0 && a.t % 8 == 0 && a.h % 8 == 0;
+}
+
+// 16 bytes of a row to a tile, zeros where `valid` is false (nothing is read then).
+template <bool kUnits>
+__device__ __forceinline__ void fetch(uint32_t to, const __nv_bfloat16* from, bool valid) {
+    if constexpr (kUnits) copy16(to, from, valid);
+    else store16(to, valid ? gather8(from) : make_uint4(0, 0, 0, 0));
+}
+
+__device__ __forceinline__ const __nv_bfloat16* bf16(const void* p) { return static_cast<const __nv_bfloat16*>(p); }
+
+// log2 of sigmoid(f), not below -256.
+__device__ __forceinline__ float log2_sigmoid(float f) {
+    const float s = log1pf(expf(-fabsf(f))), v = f >= 0.0f ? -s : f - s;
+    return v < -177.0f ? -256.0f : v * kLog2e;
+}
+__device__ __forceinline__ float sigmoid_full(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+// What a chunk's tokens have from their gates, in groups of 16. `in`: the decay from the last token of the group
+// before to this one; `out`: from this one to the last of its own group: between two groups a decay is a
+// product of factors below one. sum: log2 of `in`, in units of 2^-40.
+struct Token {
+    long long sum;
+    float in, out;
+};
+struct Factors {
+    float k, q, s, beta;  // Gam rk, Gam rq, gam rk, beta
+};
+
+constexpr float kUnit = 1099511627776.0f, kPerUnit = 9.094947018e-13f;  // 2^40, 2^-40
+
+__device__ __forceinline__ float decay(long long log2_units) { return exp2_fast(__ll2float_rn(log2_units) * kPerUnit); }
+
+// 16 lanes: the entries of a group's tokens, one to a lane. Sums are in units of 2^-40 (they are at most 2^14),
+// which takes integer additions only and rounds nothing but each token's own term; differences keep
+// their digits however large the sums are.
+__device__ __forceinline__ void scan_group(float lg, Token* tab) {
+    const int lane = threadIdx.x % 32;
+    long long s = __float2ll_rn(lg * kUnit);
+#pragma unroll
+    for (int o = 1; o < 16; o *= 2) {
+        const long long t = __shfl_up_sync(0xffffffffu, s, o, 16);
+        if (lane % 16 >= o) s += t;
+    }
+    const long long end = __shfl_sync(0xffffffffu, s, 15, 16);
+    if (lane < 16) tab[lane] = {s, decay(s), decay(end - s)};
+}
+
+// The sum of squares of a tile's row.
+template <int kPitch>
+__device__ __forceinline__ float row_square(uint32_t tile, int r) {
+    float s = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kPitch / 16; ++u) {
+        const uint4 v = load16(unit_at<kPitch>(tile, r, u));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = ptx::bf16_lo(w[i]), b = ptx::bf16_hi(w[i]);
+            s = fmaf(a, a, fmaf(b, b, s));
+        }
+    }
+    return s;
+}
+
+// The inverse of I + N for a strictly lower triangular 16 x 16 N, whose column j is at NT + 20 j in shared
+// memory: lane l has column l % 16 of it in t, by forward substitution, which is as exact as N allows also
+// where powers of N are large. A finished row is taken from all later ones at once: 15 independent steps.
+__device__ __forceinline__ void invert16(const float* NT, float* t) {
+    const int col = threadIdx.x % 16;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[i] = i == col ? 1.0f : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 15; ++j) {
+#pragma unroll
+        for (int i = (j + 1) / 4 * 4; i < 16; i += 4) {
+            const float4 n = *reinterpret_cast<const float4*>(NT + 20 * j + i);
+            const float e[4] = {n.x, n.y, n.z, n.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (i + r > j) t[i + r] = fmaf(-e[r], t[j], t[i + r]);
+        }
+    }
+}
+
+}  // namespace delta
+}  // namespace block
+}  // namespace ssdc

@@ -1,0 +1,689 @@
+// The delta rule's gradients for bfloat16, in chunks on the tensor cores (the forward formulas are in
+// block_delta.cuh).
+//
+// With dS the gradient of the state behind a chunk, and Z the gradient of its X (of v, therefore):
+//   dU = P^T do + gam (k dS),  solved backwards in blocks of 16: Z_r = (T_r beta)^T dU_r, dU_c -= A_rc^T Z_r
+//   dS' = Gam_C dS + (Gam q)^T do - (Gam k)^T Z       (q, k scaled to rq q, rk k throughout)
+// That chain is the first kernel's, which walks a state from the last chunk to the first as the forward one
+// does the other way. It leaves Z = dv and the states dS. All the rest is the second kernel's, chunk by chunk
+// and independent of each other: with M1_ij = D_ij do_i.u_j (i >= j), M2_ij = D_ij z_i.u_j (i > j),
+//   dq_i = Gam_i S do_i + sum_j M1_ij k_j
+//   dk_j = gam_j dS u_j - Gam_j S z_j + sum_i M1_ij q_i - sum_i M2_ij k_i - sum_m M2_jm k_m
+//   db_i = z_i.u_i exp(-b_i)
+//   d log a_t = what crosses t: pairs i >= t > j of e_ij = M1_ij q_i.k_j - M2_ij k_i.k_j, the state in front with
+//   i >= t, j < t with the state behind, and both states with each other
+// Every pair holds a decay of its own, so that nothing that does not cross t is added and taken away again.
+//
+// Operands of the chain are held in two bf16 parts, as dh0 is fp32; those of the second kernel, whose results are
+// rounded to 8 bits, in one: S, dS, u, z as they were written, M1 and M2 rounded.
+#include "block_delta_prepare.cuh"
+
+namespace ssdc {
+namespace block {
+namespace delta {
+namespace {
+
+template <int KP, int NW, bool kUnitRows>
+__device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int h, int w, int col0, int column_threads) {
+    using L = Layout<KP, NW, true>;
+    constexpr int KT = KP / 8;
+    const uint32_t base = ptx::smem_addr(smem);
+    const int lane = threadIdx.x % 32, all = kPrep + column_threads;
+    const int columns = min(16, p.V - col0);
+    const int64_t chunks = (p.T + C - 1) / C, seq = (int64_t)b * p.H + h;
+    const uint32_t strips = base + L::kStripOff + w * 2 * L::kStrip;
+    const int fetch_u = lane % 2, fetch_r = lane / 2;
+    const bool has_unit = 8 * fetch_u < columns;
+    const __nv_bfloat16* row = bf16(p.d_o.p) + b * p.d_o.b + h * p.d_o.h + ((chunks - 1) * C + fetch_r) * p.d_o.t + col0 + (has_unit ? 8 * fetch_u : 0);
+    auto fetch_do = [&](int64_t n) {  // chunks from the last to the first
+        const int left = (int)min((int64_t)C, p.T - (chunks - 1 - n) * C) - fetch_r;
+        const __nv_bfloat16* r = row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            fetch<kUnitRows>(strip_at(strips + (int)(n & 1) * L::kStrip, fetch_r + 16 * i, fetch_u), r, has_unit && 16 * i < left);
+            r += 16 * p.d_o.t;
+        }
+        ptx::cp_async_commit();
+        row -= C * p.d_o.t;
+    };
+    fetch_do(0);
+    float S[KT][4];  // dS, as the forward kernel holds S
+    const int64_t state = seq * p.K * p.V + col0;
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
+            S[i][e] = p.dh_last != nullptr && r < p.K && cl < columns ? p.dh_last[state + (int64_t)r * p.V + cl] : 0.0f;
+        }
+    for (int64_t n = 0; n < chunks; ++n) {
+        const int64_t c = chunks - 1 - n;
+        const int turn = (int)(n & 1);
+        const uint32_t mine = strips + turn * L::kStrip, next = strips + (turn ^ 1) * L::kStrip;
+#pragma unroll
+        for (int i = 0; i < KT; i += 2) {
+            stsm_t(strip_rows(next, 8 * i % C), pack(S[i][0], S[i][1]), pack(S[i][2], S[i][3]), pack(S[i + 1][0], S[i + 1][1]),
+                   pack(S[i + 1][2], S[i + 1][3]));
+            if ((i + 2) % 8 == 0) {
+                const int first = 8 * i / C * C;
+                put_strip(next, static_cast<__nv_bfloat16*>(p.ws) + (seq * chunks + c) * p.K * p.V + (int64_t)first * p.V + col0, p.V,
+                          p.K - first, columns);
+            }
+        }
+        if (n + 1 < chunks) fetch_do(n + 1);
+        else ptx::cp_async_commit();
+        bar_sync(kBarKeys + turn, all);
+        const uint32_t keys = base + (int)(n % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
+        float X[8][4] = {};
+#pragma unroll
+        for (int s = 0; s < KP / 16; ++s) {
+            Split a;
+            a.set(S[2 * s], S[2 * s + 1]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                uint32_t kb[4];
+                ldsm(kb, rows_k<L::kKeyPitch>(keys, 16 * m, 2 * s));
+                mma(X[2 * m], a.hi, kb[0], kb[1]);
+                mma(X[2 * m + 1], a.hi, kb[2], kb[3]);
+                mma(X[2 * m], a.lo, kb[0], kb[1]);
+                mma(X[2 * m + 1], a.lo, kb[2], kb[3]);
+            }
+        }
+        ptx::cp_async_wait<1>();
+        __syncwarp();
+        bar_sync(kBarFull, all);
+        const Factors* factors = reinterpret_cast<const Factors*>(smem + L::kFactorsOff) + turn * C;
+        const uint32_t hi = base + L::kLOff, lo = hi + L::kSquare, ps = lo + L::kSquare, ps2 = ps + L::kSquare;
+        const float gam = reinterpret_cast<const float*>(smem + L::kGamOff)[turn];
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float f = factors[8 * m + 2 * (lane % 4) + e].s;
+                X[m][e] *= f;
+                X[m][e + 2] *= f;
+                // what a reset keeps from the chunks behind is left out, whatever they hold
+                if (gam == 0.0f && f == 0.0f) X[m][e] = X[m][e + 2] = 0.0f;
+            }
+        uint32_t d_o[4][4];  // do^T as A operands
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ldsm_t(d_o[i], strip_rows(mine, 16 * i));
+#pragma unroll
+            for (int j = 0; j <= i; ++j) {
+                uint32_t ph[4], pl[4];
+                ldsm_t(ph, cols_k<L::kPitch>(ps, 16 * i, 2 * j));
+                ldsm_t(pl, cols_k<L::kPitch>(ps2, 16 * i, 2 * j));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma(X[2 * j + e], d_o[i], pl[2 * e], pl[2 * e + 1]);
+                    mma(X[2 * j + e], d_o[i], ph[2 * e], ph[2 * e + 1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 3; r >= 0; --r) {
+            Split a;
+            uint32_t bh[4], bl[4];
+            a.set(X[2 * r], X[2 * r + 1]);
+            ldsm(bh, rows_k<L::kPitch>(hi, 16 * r, 2 * r));
+            ldsm(bl, rows_k<L::kPitch>(lo, 16 * r, 2 * r));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                X[2 * r + e][0] = X[2 * r + e][1] = X[2 * r + e][2] = X[2 * r + e][3] = 0.0f;
+                mma(X[2 * r + e], a.lo, bh[2 * e], bh[2 * e + 1]);
+                mma(X[2 * r + e], a.hi, bl[2 * e], bl[2 * e + 1]);
+                mma(X[2 * r + e], a.hi, bh[2 * e], bh[2 * e + 1]);
+            }
+            a.set(X[2 * r], X[2 * r + 1]);  // Z of this block
+#pragma unroll
+            for (int j = 0; j < r; ++j) {
+                ldsm_t(bh, cols_k<L::kPitch>(hi, 16 * r, 2 * j));
+                ldsm_t(bl, cols_k<L::kPitch>(lo, 16 * r, 2 * j));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma(X[2 * j + e], a.hi, bh[2 * e], bh[2 * e + 1]);
+                    mma(X[2 * j + e], a.lo, bh[2 * e], bh[2 * e + 1]);
+                    mma(X[2 * j + e], a.hi, bl[2 * e], bl[2 * e + 1]);
+                }
+            }
+        }
+        if (n + 1 < chunks) bar_arrive(kBarFree, all);
+#pragma unroll
+        for (int m = 0; m < 8; m += 2)
+            stsm_t(strip_rows(mine, 8 * m), pack(X[m][0], X[m][1]), pack(X[m][2], X[m][3]), pack(X[m + 1][0], X[m + 1][1]),
+                   pack(X[m + 1][2], X[m + 1][3]));
+        const int64_t left = p.T - c * C;
+        put_strip(mine, static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + c * C) * p.H + h) * p.V + col0, (int64_t)p.H * p.V,
+                  left < C ? (int)left : C, columns);
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[i][e] *= gam;
+            if (gam == 0.0f) S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.0f;
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            float g[2][4];  // do of 16 tokens times Gam rq
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = 16 * s + 8 * e + 2 * (lane % 4);
+                const Factors f0 = factors[j], f1 = factors[j + 1];
+                g[e][0] = ptx::bf16_lo(d_o[s][2 * e]) * f0.q; g[e][1] = ptx::bf16_hi(d_o[s][2 * e]) * f1.q;
+                g[e][2] = ptx::bf16_lo(d_o[s][2 * e + 1]) * f0.q; g[e][3] = ptx::bf16_hi(d_o[s][2 * e + 1]) * f1.q;
+                float* x = X[2 * s + e];
+                x[0] *= -f0.k; x[1] *= -f1.k; x[2] *= -f0.k; x[3] *= -f1.k;
+                if (gam == 0.0f) {
+                    if (f0.k == 0.0f) g[e][0] = g[e][2] = x[0] = x[2] = 0.0f;
+                    if (f1.k == 0.0f) g[e][1] = g[e][3] = x[1] = x[3] = 0.0f;
+                }
+            }
+            Split a, z;
+            a.set(g[0], g[1]);
+            z.set(X[2 * s], X[2 * s + 1]);
+#pragma unroll
+            for (int i = 0; i < KT; i += 2) {
+                uint32_t qb[4], kb[4];
+                ldsm_t(qb, cols_k<L::kKeyPitch>(queries, 16 * s, i));
+                ldsm_t(kb, cols_k<L::kKeyPitch>(keys, 16 * s, i));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma(S[i + e], a.hi, qb[2 * e], qb[2 * e + 1]);
+                    mma(S[i + e], a.lo, qb[2 * e], qb[2 * e + 1]);
+                    mma(S[i + e], z.hi, kb[2 * e], kb[2 * e + 1]);
+                    mma(S[i + e], z.lo, kb[2 * e], kb[2 * e + 1]);
+                }
+            }
+        }
+        if (n + 2 < chunks) bar_arrive(kBarStage + turn, all);
+    }
+    if (p.dh0 != nullptr) {
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
+                if (r < p.K && cl < columns) p.dh0[state + (int64_t)r * p.V + cl] = S[i][e];
+            }
+    }
+}
+
+template <int KP, int NW, bool kUnitRows>
+__global__ void __launch_bounds__(kPrep + 32 * NW, KP == 64 && NW == 4 ? 2 : 1) delta_bwd_chain(const __grid_constant__ Delta p) {
+    extern __shared__ __align__(128) char smem[];
+    const int parts = (p.V + 16 * NW - 1) / (16 * NW), item = blockIdx.x / parts, col0 = blockIdx.x % parts * 16 * NW;
+    const int b = item / p.H, h = item % p.H;
+    const int warps = min(NW, (p.V - col0 + 15) / 16);
+    constexpr bool kSplit = KP == 64 || NW == 8;
+    if (threadIdx.x < kPrep) {
+        if constexpr (kSplit) ptx::regs_dec<NW == 8 ? 104 : 96>();
+        prepare_chunks<KP, NW, true, kUnitRows>(p, smem, b, h, 32 * warps);
+    } else {
+        if constexpr (kSplit) ptx::regs_inc<NW == 8 ? 200 : 160>();
+        const int w = threadIdx.x / 32 - kPrep / 32;
+        if (w < warps) walk_back<KP, NW, kUnitRows>(p, smem, b, h, w, col0 + 16 * w, 32 * warps);
+    }
+}
+
+// ---- the second kernel
+
+// A tile of rows of `units` 16-byte units (a power of two), kPitch bytes apart.
+template <int KP, int VP>
+struct Tiles {
+    static constexpr int kKeyPitch = KP * 2, kPitch = VP * 2, kSquarePitch = C * 2;
+    static constexpr int kK = 0, kQ = kK + C * kKeyPitch;
+    static constexpr int kDo = kQ + C * kKeyPitch, kZ = kDo + C * kPitch, kU = kZ + C * kPitch;
+    static constexpr int kS = kU + C * kPitch, kDs = kS + KP * kPitch;
+    // M1 and M2, transposed as they are read, over the states, which have been read by then
+    static constexpr int kM1 = kS, kM2 = kM1 + C * kSquarePitch;
+    static constexpr int kSmall = kDs + KP * kPitch;
+};
+struct Small {
+    Token tab[C];
+    Factors factors[C];
+    float2 lengths[C];
+    float columns[4][C], rows[C], diagonal[C], front[2][C], behind[2][C];
+    float both[8], gate[C], gam, pad[3];
+};
+
+template <int kPitch>
+__device__ __forceinline__ void fetch_rows(uint32_t tile, const __nv_bfloat16* from, int64_t stride, int rows, int have, int n, bool units) {
+    const int per = kPitch / 16;
+    for (int i = threadIdx.x; i < rows * per; i += blockDim.x) {
+        const int r = i / per, u = i % per;
+        const bool valid = r < have && 8 * u < n;
+        const __nv_bfloat16* at = valid ? from + r * stride + 8 * u : from;
+        if (units) fetch<true>(unit_at<kPitch>(tile, r, u), at, valid);
+        else fetch<false>(unit_at<kPitch>(tile, r, u), at, valid);
+    }
+}
+
+// KP / 64 groups of four warps: warp w % 4 has 16 tokens' rows, and of the features of q and k 64 of its group's.
+template <int KP, int VP>
+__global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bwd_chunks(const __grid_constant__ Delta p, bool q_units, bool k_units,
+                                                                                         bool do_units) {
+    using L = Tiles<KP, VP>;
+    extern __shared__ __align__(128) char smem[];
+    const uint32_t base = ptx::smem_addr(smem);
+    Small& sm = *reinterpret_cast<Small*>(smem + L::kSmall);
+    const int tid = threadIdx.x, lane = tid % 32, w = tid / 32 % 4, half = tid / 128;
+    const int64_t chunks = (p.T + C - 1) / C;
+    const int64_t c = blockIdx.x % chunks, bg = blockIdx.x / chunks;
+    const int b = (int)(bg / p.G), g = (int)(bg % p.G), R = p.H / p.G;
+    const int64_t t0 = c * C;
+    const int n_tokens = (int)min((int64_t)C, p.T - t0);
+    const float q_scale = p.normalize ? rsqrtf((float)p.K) : 1.0f;
+    fetch_rows<L::kKeyPitch>(base + L::kK, bf16(p.k.p) + b * p.k.b + t0 * p.k.t + g * p.k.h, p.k.t, C, n_tokens, p.K, k_units);
+    fetch_rows<L::kKeyPitch>(base + L::kQ, bf16(p.q.p) + b * p.q.b + t0 * p.q.t + g * p.q.h, p.q.t, C, n_tokens, p.K, q_units);
+    // rows lane / 4 and 8 more of the warp's 16, features 64 half + 8 i + 2 (lane % 4) and the next
+    float dq[8][4] = {}, dk[8][4] = {};
+    const int row0 = 16 * w + lane / 4;
+    for (int r = 0; r < R; ++r) {
+        const int h = g * R + r;
+        const int64_t seq = (int64_t)b * p.H + h, dense = (int64_t)p.H * p.V, at = ((b * p.T + t0) * p.H + h) * p.V;
+        const int64_t state = (seq * chunks + c) * p.K * p.V;
+        __syncthreads();  // the head before is through with the tiles
+        fetch_rows<L::kPitch>(base + L::kDo, bf16(p.d_o.p) + b * p.d_o.b + t0 * p.d_o.t + h * p.d_o.h, p.d_o.t, C, n_tokens, p.V, do_units);
+        fetch_rows<L::kPitch>(base + L::kZ, bf16(p.dv) + at, dense, C, n_tokens, p.V, true);
+        fetch_rows<L::kPitch>(base + L::kU, bf16(p.in_updates) + at, dense, C, n_tokens, p.V, true);
+        fetch_rows<L::kPitch>(base + L::kS, bf16(p.in_states) + state, p.V, KP, p.K, p.V, true);
+        fetch_rows<L::kPitch>(base + L::kDs, bf16(p.ws) + state, p.V, KP, p.K, p.V, true);
+        ptx::cp_async_commit();
+        float beta_rest = 0.0f;  // exp(-b)
+        if (tid < C) {
+            const int64_t t = t0 + tid;
+            float lg = 0.0f, rest = 0.0f;
+            if (tid < n_tokens) {
+                const float f = to_f32(bf16(p.f.p)[b * p.f.b + t * p.f.t + h * p.f.h]), e = expf(-fabsf(f));
+                const float s = log1pf(e), l = f >= 0.0f ? -s : f - s;
+                const bool first = p.reset != nullptr && p.reset[b * p.T + t] != 0;
+                lg = first || l < -177.0f ? -256.0f : l * kLog2e;
+                rest = first ? 0.0f : (f >= 0.0f ? e : 1.0f) / (1.0f + e);  // 1 - a
+                // where beta is below e^-80 so are u and z, and their product is zero
+                beta_rest = expf(fminf(-to_f32(bf16(p.beta.p)[b * p.beta.b + t * p.beta.t + h * p.beta.h]), 80.0f));
+            }
+            sm.gate[tid] = rest;
+            const int l = lane % 16;
+            long long s = __float2ll_rn(lg * kUnit);
+#pragma unroll
+            for (int o = 1; o < 16; o *= 2) {
+                const long long x = __shfl_up_sync(0xffffffffu, s, o, 16);
+                if (l >= o) s += x;
+            }
+            const long long end = __shfl_sync(0xffffffffu, s, 15, 16);
+            sm.tab[tid] = {s, decay(s), decay(end - s)};
+        }
+        ptx::cp_async_wait<0>();
+        __syncthreads();
+        if (r == 0 && tid < 2 * C) {
+            const float n = p.normalize ? rsqrtf(row_square<L::kKeyPitch>(base + (tid < C ? L::kK : L::kQ), tid % C) + kUnitEps) : 1.0f;
+            reinterpret_cast<float*>(&sm.lengths[tid % C])[tid / C] = tid < C ? n : n * q_scale;
+        }
+        __syncthreads();
+        if (tid < C) {
+            const int group = tid / 16;
+            long long mine = sm.tab[tid].sum, whole = 0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const long long of_m = sm.tab[16 * m + 15].sum;
+                whole += of_m;
+                mine += m < group ? of_m : 0;
+            }
+            const float into = decay(mine);
+            sm.factors[tid] = {into, 0.0f, decay(whole - mine), beta_rest};
+            if (tid == C - 1) sm.gam = into;
+        }
+        __syncthreads();
+        // the states' part
+        const Factors f0 = sm.factors[row0], f1 = sm.factors[row0 + 8];
+        const float2 l0 = sm.lengths[row0], l1 = sm.lengths[row0 + 8];
+        float front[2] = {}, behind[2] = {};
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            if (64 * half + 8 * i >= p.K) break;
+            float so[2][4] = {}, sz[2][4] = {}, su[2][4] = {};
+#pragma unroll
+            for (int s = 0; s < VP / 16; ++s) {
+                uint32_t oa[4], za[4], ua[4], sb[4], db[4];
+                ldsm(oa, rows_a<L::kPitch>(base + L::kDo, 16 * w, 2 * s));
+                ldsm(za, rows_a<L::kPitch>(base + L::kZ, 16 * w, 2 * s));
+                ldsm(ua, rows_a<L::kPitch>(base + L::kU, 16 * w, 2 * s));
+                ldsm(sb, rows_k<L::kPitch>(base + L::kS, 64 * half + 8 * i, 2 * s));
+                ldsm(db, rows_k<L::kPitch>(base + L::kDs, 64 * half + 8 * i, 2 * s));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma(so[e], oa, sb[2 * e], sb[2 * e + 1]);
+                    mma(sz[e], za, sb[2 * e], sb[2 * e + 1]);
+                    mma(su[e], ua, db[2 * e], db[2 * e + 1]);
+                }
+            }
+            uint32_t qv[4], kv[4];  // q and k where the sums are
+            ldsm(qv, rows_a<L::kKeyPitch>(base + L::kQ, 16 * w, 8 * half + i));
+            ldsm(kv, rows_a<L::kKeyPitch>(base + L::kK, 16 * w, 8 * half + i));
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const Factors& f = x < 2 ? f0 : f1;
+                    const uint32_t qp = qv[2 * e + x / 2], kp = kv[2 * e + x / 2];
+                    const float q = x % 2 ? ptx::bf16_hi(qp) : ptx::bf16_lo(qp), k = x % 2 ? ptx::bf16_hi(kp) : ptx::bf16_lo(kp);
+                    // a state that a reset cuts off is left out, whatever it holds
+                    const float o = f.k == 0.0f ? 0.0f : f.k * so[e][x], z = f.k == 0.0f ? 0.0f : f.k * sz[e][x];
+                    const float u = f.s == 0.0f ? 0.0f : f.s * su[e][x];
+                    const float2& l = x < 2 ? l0 : l1;
+                    dq[i + e][x] += o;
+                    dk[i + e][x] += u - z;
+                    front[x / 2] += q * l.y * o - k * l.x * z;
+                    behind[x / 2] += k * l.x * u;
+                }
+        }
+        float both = 0.0f;
+        if (sm.gam != 0.0f) {
+            for (int i = tid; i < KP * (VP / 8); i += blockDim.x) {
+                const uint32_t at_i = i * 16;  // the same place of both tiles
+                const uint4 a = load16(base + L::kS + at_i), d = load16(base + L::kDs + at_i);
+                const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    both = fmaf(ptx::bf16_lo(x[e]), ptx::bf16_lo(y[e]), fmaf(ptx::bf16_hi(x[e]), ptx::bf16_hi(y[e]), both));
+            }
+            both = warp_sum(both);
+        }
+        if (lane == 0) sm.both[tid / 32] = both;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int o = 1; o < 4; o *= 2) {
+                front[x] += __shfl_xor_sync(0xffffffffu, front[x], o);
+                behind[x] += __shfl_xor_sync(0xffffffffu, behind[x], o);
+            }
+            if (lane % 4 == 0) sm.front[half][row0 + 8 * x] = front[x], sm.behind[half][row0 + 8 * x] = behind[x];
+        }
+        __syncthreads();  // the states have been read: M1 and M2 go there
+        // rows of the warp against the tokens up to them
+        float rows[2] = {};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            if (n >= w && half == 0 && lane < 16) sm.columns[w][16 * n + lane] = 0.0f;
+            if (n > w) continue;
+            float pairs[2][4];
+            float qk[2][4] = {}, kk[2][4] = {}, ou[2][4] = {}, zu[2][4] = {};
+#pragma unroll
+            for (int s = 0; s < KP / 16; ++s) {
+                uint32_t qa[4], ka[4], kb[4];
+                ldsm(qa, rows_a<L::kKeyPitch>(base + L::kQ, 16 * w, 2 * s));
+                ldsm(ka, rows_a<L::kKeyPitch>(base + L::kK, 16 * w, 2 * s));
+                ldsm(kb, rows_k<L::kKeyPitch>(base + L::kK, 16 * n, 2 * s));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma(qk[e], qa, kb[2 * e], kb[2 * e + 1]);
+                    mma(kk[e], ka, kb[2 * e], kb[2 * e + 1]);
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < VP / 16; ++s) {
+                uint32_t oa[4], za[4], ub[4];
+                ldsm(oa, rows_a<L::kPitch>(base + L::kDo, 16 * w, 2 * s));
+                ldsm(za, rows_a<L::kPitch>(base + L::kZ, 16 * w, 2 * s));
+                ldsm(ub, rows_k<L::kPitch>(base + L::kU, 16 * n, 2 * s));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma(ou[e], oa, ub[2 * e], ub[2 * e + 1]);
+                    mma(zu[e], za, ub[2 * e], ub[2 * e + 1]);
+                }
+            }
+            const Token i0 = sm.tab[row0], i1 = sm.tab[row0 + 8];
+            long long far = 0;
+            for (int m = n + 1; m < w; ++m) far += sm.tab[16 * m + 15].sum;
+            const float apart = decay(far), in0 = apart * i0.in, in1 = apart * i1.in;
+            uint32_t a1[4], a2[4], m1[4], m2[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = 16 * n + 8 * e + 2 * (lane % 4);
+                const Token j0 = sm.tab[j], j1 = sm.tab[j + 1];
+                const float n0 = sm.lengths[j].x, n1 = sm.lengths[j + 1].x;
+                float d[4], sum[2] = {};
+                if (n < w) {
+                    d[0] = in0 * j0.out, d[1] = in0 * j1.out, d[2] = in1 * j0.out, d[3] = in1 * j1.out;
+                } else {
+                    d[0] = decay(i0.sum - j0.sum), d[1] = decay(i0.sum - j1.sum);
+                    d[2] = decay(i1.sum - j0.sum), d[3] = decay(i1.sum - j1.sum);
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int i = row0 + 8 * (x / 2), jj = j + x % 2;
+                    const float2& l = x < 2 ? l0 : l1;
+                    const float nj = x % 2 ? n1 : n0;
+                    if (n == w && i == jj && half == 0 && i < n_tokens)
+                        static_cast<__nv_bfloat16*>(p.db)[(b * p.T + t0 + i) * p.H + h] = __float2bfloat16_rn(zu[e][x] * sm.factors[i].beta);
+                    const float o = jj > i ? 0.0f : d[x] * ou[e][x], z = jj >= i ? 0.0f : d[x] * zu[e][x];
+                    const float pair = jj >= i ? 0.0f : nj * (o * l.y * qk[e][x] - z * l.x * kk[e][x]);
+                    pairs[e][x] = pair;
+                    sum[x % 2] += pair;
+                    ou[e][x] = o;
+                    zu[e][x] = -z;
+                }
+                a1[2 * e] = pack(ou[e][0] * n0, ou[e][1] * n1);
+                a1[2 * e + 1] = pack(ou[e][2] * n0, ou[e][3] * n1);
+                a2[2 * e] = pack(zu[e][0] * n0, zu[e][1] * n1);
+                a2[2 * e + 1] = pack(zu[e][2] * n0, zu[e][3] * n1);
+                m1[2 * e] = pack(ou[e][0] * l0.y, ou[e][1] * l0.y);
+                m1[2 * e + 1] = pack(ou[e][2] * l1.y, ou[e][3] * l1.y);
+                m2[2 * e] = pack(zu[e][0] * l0.x, zu[e][1] * l0.x);
+                m2[2 * e + 1] = pack(zu[e][2] * l1.x, zu[e][3] * l1.x);
+                if (n < w) {
+                    rows[0] += pairs[e][0] + pairs[e][1];
+                    rows[1] += pairs[e][2] + pairs[e][3];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                        for (int o = 4; o < 32; o *= 2) sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], o);
+                        if (lane < 4 && half == 0) sm.columns[w][j + x] = sum[x];
+                    }
+                }
+            }
+            if (n == w) {
+                // what crosses each token within the block: the sums over j < t by a product with ones, then over i >= t
+                Split a;
+                a.set(pairs[0], pairs[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = 8 * e + lane / 4, j = 2 * (lane % 4);
+                    auto ones = [&](int k) { return (k < t ? 0x3F80u : 0u) | (k + 1 < t ? 0x3F800000u : 0u); };
+                    float sum[4] = {};
+                    mma(sum, a.hi, ones(j), ones(j + 8));
+                    mma(sum, a.lo, ones(j), ones(j + 8));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int at = 8 * e + j + x;
+                        float s = (lane / 4 >= at ? sum[x] : 0.0f) + (lane / 4 + 8 >= at ? sum[x + 2] : 0.0f);
+#pragma unroll
+                        for (int o = 4; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+                        if (lane < 4 && half == 0) sm.diagonal[16 * w + at] = s;
+                    }
+                }
+            }
+            if (half == 0) {
+                stsm(rows_a<L::kSquarePitch>(base + L::kM1, 16 * w, 2 * n), m1[0], m1[1], m1[2], m1[3]);
+                stsm(rows_a<L::kSquarePitch>(base + L::kM2, 16 * w, 2 * n), m2[0], m2[1], m2[2], m2[3]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                uint32_t kb[4];
+                ldsm_t(kb, cols_k<L::kKeyPitch>(base + L::kK, 16 * n, 8 * half + i));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma(dq[i + e], a1, kb[2 * e], kb[2 * e + 1]);
+                    mma(dk[i + e], a2, kb[2 * e], kb[2 * e + 1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int o = 1; o < 4; o *= 2) rows[x] += __shfl_xor_sync(0xffffffffu, rows[x], o);
+            if (lane % 4 == 0 && half == 0) sm.rows[row0 + 8 * x] = rows[x];
+        }
+        __syncthreads();
+        // the columns of the warp's tokens against those from them on
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            if (n < w) continue;
+            uint32_t a1[4], a2[4];
+            ldsm_t(a1, cols_a<L::kSquarePitch>(base + L::kM1, 16 * n, 2 * w));
+            ldsm_t(a2, cols_a<L::kSquarePitch>(base + L::kM2, 16 * n, 2 * w));
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                uint32_t qb[4], kb[4];
+                ldsm_t(qb, cols_k<L::kKeyPitch>(base + L::kQ, 16 * n, 8 * half + i));
+                ldsm_t(kb, cols_k<L::kKeyPitch>(base + L::kK, 16 * n, 8 * half + i));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma(dk[i + e], a1, qb[2 * e], qb[2 * e + 1]);
+                    mma(dk[i + e], a2, kb[2 * e], kb[2 * e + 1]);
+                }
+            }
+        }
+        if (tid < 32) {
+            // Two tokens to a lane. What crosses t, in groups of 16: pairs within t's group; of t's group, rows from
+            // t on with groups before, and columns before t with groups behind; and whole blocks of groups
+            // before and behind. Only sums of what does cross: nothing is taken away from a larger sum.
+            const int group = lane / 8;
+            float f[2], o[2], rows_of[2], columns_of[2], blocks[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                f[i] = sm.front[0][t] + (KP > 64 ? sm.front[1][t] : 0.0f);
+                o[i] = sm.behind[0][t] + (KP > 64 ? sm.behind[1][t] : 0.0f);
+                rows_of[i] = sm.rows[t];
+                columns_of[i] = sm.columns[1][t] + sm.columns[2][t] + sm.columns[3][t];
+            }
+#pragma unroll
+            for (int m = 2; m < 4; ++m) {
+                blocks[m] = sm.columns[m][2 * lane] + sm.columns[m][2 * lane + 1];
+#pragma unroll
+                for (int d = 1; d < 8; d *= 2) blocks[m] += __shfl_xor_sync(0xffffffffu, blocks[m], d);
+            }
+            const float b20 = __shfl_sync(0xffffffffu, blocks[2], 0), b30 = __shfl_sync(0xffffffffu, blocks[3], 0);
+            const float b31 = __shfl_sync(0xffffffffu, blocks[3], 8);
+            const float across = group == 1 ? b20 + b30 : group == 2 ? b30 + b31 : 0.0f;
+            float s = 0.0f;
+            for (int i = 0; i < KP / 16; ++i) s += sm.both[i];
+            s = sm.gam == 0.0f ? across : fmaf(sm.gam, s, across);
+            float from = f[0] + f[1], before = o[0] + o[1], rows_from = rows_of[0] + rows_of[1], columns_to = columns_of[0] + columns_of[1];
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const float x = __shfl_down_sync(0xffffffffu, from, d), y = __shfl_up_sync(0xffffffffu, before, d);
+                if (lane + d < 32) from += x;
+                if (lane >= d) before += y;
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d *= 2) {
+                const float x = __shfl_down_sync(0xffffffffu, rows_from, d, 8), y = __shfl_up_sync(0xffffffffu, columns_to, d, 8);
+                if (lane % 8 + d < 8) rows_from += x;
+                if (lane % 8 >= d) columns_to += y;
+            }
+            // of the lanes behind and before this one
+            float x = __shfl_down_sync(0xffffffffu, from, 1), y = __shfl_up_sync(0xffffffffu, before, 1);
+            s += (lane < 31 ? x : 0.0f) + (lane > 0 ? y : 0.0f);
+            x = __shfl_down_sync(0xffffffffu, rows_from, 1), y = __shfl_up_sync(0xffffffffu, columns_to, 1);
+            s += (lane % 8 < 7 ? x : 0.0f) + (lane % 8 > 0 ? y : 0.0f);
+            const float da[2] = {s + f[0] + f[1] + rows_of[0] + rows_of[1] + sm.diagonal[2 * lane],
+                                 s + f[1] + o[0] + rows_of[1] + columns_of[0] + sm.diagonal[2 * lane + 1]};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 2 * lane + i;
+                if (t < n_tokens) static_cast<__nv_bfloat16*>(p.df)[(b * p.T + t0 + t) * p.H + h] = __float2bfloat16_rn(da[i] * sm.gate[t]);
+            }
+        }
+    }
+    __syncthreads();
+    // back through the division by the length, and out by way of this warp's rows of the q and k tiles
+    const float2 l0 = sm.lengths[row0], l1 = sm.lengths[row0 + 8];
+    float along[4] = {};  // q.dq and k.dk of both rows
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        uint32_t qv[4], kv[4];
+        ldsm(qv, rows_a<L::kKeyPitch>(base + L::kQ, 16 * w, 8 * half + i));
+        ldsm(kv, rows_a<L::kKeyPitch>(base + L::kK, 16 * w, 8 * half + i));
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                along[x] += ptx::bf16_lo(qv[2 * e + x]) * dq[i + e][2 * x] + ptx::bf16_hi(qv[2 * e + x]) * dq[i + e][2 * x + 1];
+                along[2 + x] += ptx::bf16_lo(kv[2 * e + x]) * dk[i + e][2 * x] + ptx::bf16_hi(kv[2 * e + x]) * dk[i + e][2 * x + 1];
+            }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int o = 1; o < 4; o *= 2) along[x] += __shfl_xor_sync(0xffffffffu, along[x], o);
+    if constexpr (KP > 64) {
+        float* sums = reinterpret_cast<float*>(smem + L::kDo);  // [2][C][4]
+        if (lane % 4 == 0) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sums[(half * C + row0 + 8 * (x % 2)) * 4 + x / 2] = along[x];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) along[x] = sums[(row0 + 8 * (x % 2)) * 4 + x / 2] + sums[(C + row0 + 8 * (x % 2)) * 4 + x / 2];
+    }
+    const float unq = p.normalize ? 1.0f / (q_scale * q_scale) : 0.0f, unk = p.normalize ? 1.0f : 0.0f;
+    const float sq[2] = {along[0] * l0.y * l0.y * unq, along[1] * l1.y * l1.y * unq}, sk[2] = {along[2] * l0.x * l0.x * unk, along[3] * l1.x * l1.x * unk};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        uint32_t qv[4], kv[4];
+        const uint32_t qat = rows_a<L::kKeyPitch>(base + L::kQ, 16 * w, 8 * half + i), kat = qat - L::kQ + L::kK;
+        ldsm(qv, qat);
+        ldsm(kv, kat);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float lq = x ? l1.y : l0.y, lk = x ? l1.x : l0.x;
+                uint32_t &q = qv[2 * e + x], &k = kv[2 * e + x];
+                q = pack(lq * (dq[i + e][2 * x] - sq[x] * ptx::bf16_lo(q)), lq * (dq[i + e][2 * x + 1] - sq[x] * ptx::bf16_hi(q)));
+                k = pack(lk * (dk[i + e][2 * x] - sk[x] * ptx::bf16_lo(k)), lk * (dk[i + e][2 * x + 1] - sk[x] * ptx::bf16_hi(k)));
+            }
+        stsm(qat, qv[0], qv[1], qv[2], qv[3]);
+        stsm(kat, kv[0], kv[1], kv[2], kv[3]);
+    }
+    __syncwarp();
+    for (int i = lane; i < 16 * 8; i += 32) {
+        const int r = 16 * w + i / 8, u = 8 * half + i % 8;
+        if (r >= n_tokens || 8 * u >= p.K) continue;
+        const int64_t to = ((b * p.T + t0 + r) * p.G + g) * p.K + 8 * u;
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dq) + to) = load16(unit_at<L::kKeyPitch>(base + L::kQ, r, u));
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dk) + to) = load16(unit_at<L::kKeyPitch>(base + L::kK, r, u));
+    }
+}
+
+template <int KP, int NW>
+int launch(const Delta& p, cudaStream_t stream) {
+    using L = Layout<KP, NW, true>;
+    const bool units = whole_units(p.k) && whole_units(p.q) && whole_units(p.d_o);
+    const auto chain = units ? delta_bwd_chain<KP, NW, true> : delta_bwd_chain<KP, NW, false>;
+    using T = Tiles<KP, 16 * NW>;
+    constexpr int kBytes = T::kSmall + (int)sizeof(Small);
+    static std::atomic<uint64_t> done[3];
+    if (allow_smem(chain, L::kBytes, done[units]) != cudaSuccess || allow_smem(delta_bwd_chunks<KP, 16 * NW>, kBytes, done[2]) != cudaSuccess)
+        return SSDC_ERR_CUDA;
+    const int64_t ctas = (p.T + C - 1) / C * p.B * p.G;
+    if (ctas > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
+    const int parts = (p.V + 16 * NW - 1) / (16 * NW);
+    chain<<<p.B * p.H * parts, kPrep + 32 * NW, L::kBytes, stream>>>(p);
+    delta_bwd_chunks<KP, 16 * NW><<<(unsigned)ctas, 2 * KP, kBytes, stream>>>(p, whole_units(p.q), whole_units(p.k), whole_units(p.d_o));
+    return 2;
+}
+
+}  // namespace
+}  // namespace delta
+
+int delta_bwd_launch(const Delta& p, cudaStream_t stream) {
+    using namespace delta;
+    if (p.K <= 64) return p.V <= 64 ? launch<64, 4>(p, stream) : launch<64, 8>(p, stream);
+    return p.V <= 64 ? launch<128, 4>(p, stream) : launch<128, 8>(p, stream);
+}
+
+}  // namespace block
+}  // namespace ssdc

@@ -110,7 +110,7 @@ int ssd_delta_rule_fwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in v, ssd_heads
     if (a.rc != SSDC_OK) return a.rc;
     p.h0 = h0; p.reset = reset; p.o = o; p.h_last = h_last; p.states = states; p.updates = updates;
     (void)cudaGetLastError();
-    return done(delta_tokens_fwd_launch(p, stream));
+    return done(p.bf16 ? delta_fwd_launch(p, stream) : delta_tokens_fwd_launch(p, stream));
 }
 
 int ssd_delta_rule_step(ssd_heads_in q, ssd_heads_in k, ssd_heads_in v, ssd_heads_in f, ssd_heads_in b, const float* state_in,
@@ -167,7 +167,7 @@ int ssd_delta_rule_bwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in f, ssd_heads
     p.in_states = states; p.in_updates = updates; p.reset = reset; p.dh_last = dh_last;
     p.dq = dq; p.dk = dk; p.dv = dv; p.df = df; p.db = db; p.dh0 = dh0; p.ws = workspace;
     (void)cudaGetLastError();
-    return done(delta_tokens_bwd_launch(p, stream));
+    return done(p.bf16 ? delta_bwd_launch(p, stream) : delta_tokens_bwd_launch(p, stream));
 }
 
 int ssd_gated_norm_fwd(ssd_rows_in x, ssd_rows_in z, const float* w, ssd_rows_in v, const float* s, float eps, int64_t M,

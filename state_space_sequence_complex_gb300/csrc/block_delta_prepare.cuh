@@ -1,0 +1,268 @@
+// The preparation of chunks for the two kernels that walk along a state, forward and backward.
+#pragma once
+
+#include "block_delta.cuh"
+
+namespace ssdc {
+namespace block {
+namespace delta {
+
+enum : int { kBarPrep = 1, kBarKeys = 2 /* and 3 */, kBarStage = 4 /* and 5 */, kBarFull = 6, kBarFree = 7 };
+
+// kBack: from the last chunk to the first, and P in two parts.
+template <int KP, int NW, bool kBack>
+struct Layout {
+    static constexpr int kKeyPitch = KP * 2, kKeyTile = C * kKeyPitch;
+    static constexpr int kStage = 2 * kKeyTile;          // k and q
+    static constexpr int kStages = 3;
+    static constexpr int kStrip = C * 32;                // 64 tokens of 16 columns
+    static constexpr int kPitch = C * 2, kSquare = C * kPitch;
+    static constexpr int kStripOff = kStages * kStage;   // [warp][2] strips of v or do
+    static constexpr int kLOff = kStripOff + NW * 2 * kStrip;  // blocks of -A and (T beta)^T, two parts; P
+    static constexpr int kTabOff = kLOff + (kBack ? 4 : 3) * kSquare;  // [2] Token[64]
+    static constexpr int kFactorsOff = kTabOff + 2 * C * 16; // [2] Factors[64], then [2] Gam_C
+    static constexpr int kGamOff = kFactorsOff + 2 * C * 16;
+    static constexpr int kBetaOff = kGamOff + 16;        // [2] beta of the 64 tokens
+    static constexpr int kLengthOff = kBetaOff + 2 * C * 4;  // rk, rq of the 64 tokens
+    static constexpr int kScratchOff = kLengthOff + C * 8;     // [4 warps] 16 x 20 floats
+    static constexpr int kBytes = kScratchOff + 4 * 16 * 20 * 4;
+};
+
+// What prepares chunks: each of four warps fetches 16 rows of a chunk's keys and queries and takes their lengths,
+// and computes two or three of the ten 16 x 16 blocks on and below the diagonal, one of them on it. While it
+// works on one chunk, the next one's rows are on their way.
+template <int KP, int NW, bool kBack, bool kUnitRows>
+__device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b, int h, int column_threads) {
+    using L = Layout<KP, NW, kBack>;
+    constexpr int kUnits = KP / 8, kRows = 32 / kUnits;  // of a row; rows a warp fetches at once
+    const uint32_t base = ptx::smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = h / (p.H / p.G), all = kPrep + column_threads;
+    const int64_t chunks = (p.T + C - 1) / C;
+    Token* const tabs = reinterpret_cast<Token*>(smem + L::kTabOff);
+    float* const betas_of = reinterpret_cast<float*>(smem + L::kBetaOff);
+    float* const scratch = reinterpret_cast<float*>(smem + L::kScratchOff) + warp * 320;
+    const float q_scale = p.normalize ? rsqrtf((float)p.K) : 1.0f;
+
+    const int fetch_u = lane % kUnits, fetch_r = 16 * warp + lane / kUnits;
+    const bool has_unit = fetch_u * 8 < p.K;
+    // chunks are counted in the order they are taken: the n-th has the tokens from first_token(n)
+    const int64_t step = kBack ? -C : C, first = kBack ? (chunks - 1) * C : 0;
+    auto first_token = [&](int64_t n) { return first + n * step; };
+    const __nv_bfloat16* k_row = bf16(p.k.p) + b * p.k.b + g * p.k.h + (first + fetch_r) * p.k.t + (has_unit ? fetch_u * 8 : 0);
+    const __nv_bfloat16* q_row = bf16(p.q.p) + b * p.q.b + g * p.q.h + (first + fetch_r) * p.q.t + (has_unit ? fetch_u * 8 : 0);
+    auto fetch_keys = [&](int64_t n) {  // in order
+        const uint32_t stage = base + (int)(n % L::kStages) * L::kStage;
+        const int left = (int)min((int64_t)C, p.T - first_token(n)) - fetch_r;
+        const __nv_bfloat16 *k = k_row, *q = q_row;
+#pragma unroll
+        for (int i = 0; i < 16 / kRows; ++i) {
+            const bool valid = has_unit && i * kRows < left;
+            const uint32_t at = unit_at<KP * 2>(stage, fetch_r + i * kRows, fetch_u);
+            fetch<kUnitRows>(at, k, valid);
+            fetch<kUnitRows>(at + L::kKeyTile, q, valid);
+            k += kRows * p.k.t;
+            q += kRows * p.q.t;
+        }
+        ptx::cp_async_commit();
+        k_row += step * p.k.t;
+        q_row += step * p.q.t;
+    };
+    // lanes below 16: the decays' arguments of the warp's tokens, and their marks; the others: beta's. As they are
+    // read: what is made of them waits until they are there.
+    const int gate_r = 16 * warp + lane % 16;
+    const int64_t gate_0 = first + gate_r;
+    const int64_t gate_t = lane < 16 ? p.f.t : p.beta.t;
+    const uint16_t* gates = (lane < 16 ? static_cast<const uint16_t*>(p.f.p) + b * p.f.b + h * p.f.h
+                                       : static_cast<const uint16_t*>(p.beta.p) + b * p.beta.b + h * p.beta.h) + gate_0 * gate_t;
+    const uint8_t* marks = p.reset != nullptr && lane < 16 ? p.reset + b * p.T + gate_0 : nullptr;
+    uint16_t gate;
+    uint8_t mark;
+    auto fetch_gates = [&](int64_t n) {  // in order
+        gate = 0, mark = 0;
+        if (first_token(n) + gate_r < p.T) {
+            gate = *gates;
+            if (marks != nullptr) mark = *marks;
+        }
+        gates += step * gate_t;
+        if (marks != nullptr) marks += step;
+    };
+    // the entries of the warp's tokens of the n-th chunk
+    auto tokens = [&](int64_t n) {
+        const int turn = (int)(n & 1);
+        const bool there = first_token(n) + gate_r < p.T;
+        const float v = __uint_as_float((uint32_t)gate << 16), e = expf(-fabsf(v));
+        // log2 of sigmoid(f), not below -256
+        const float s = log1pf(e), l = v >= 0.0f ? -s : v - s, lg = l < -177.0f ? -256.0f : l * kLog2e;
+        if (lane >= 16) betas_of[turn * C + gate_r] = there ? (v >= 0.0f ? 1.0f : e) / (1.0f + e) : 0.0f;
+        scan_group(!there ? 0.0f : mark != 0 ? -256.0f : lg, tabs + turn * C + 16 * warp);
+        ptx::cp_async_wait<0>();
+    };
+
+    // this warp's blocks: rows bi, columns bj
+    const int bi[3] = {warp, warp < 2 ? warp + 1 : warp, 3}, bj[3] = {warp, warp < 2 ? 0 : warp - 1, warp};
+
+    fetch_gates(0);
+    fetch_keys(0);
+    tokens(0);
+    for (int64_t n = 0; n < chunks; ++n) {
+        const int turn = (int)(n & 1);
+        const uint32_t keys = base + (int)(n % L::kStages) * L::kStage;
+        const Token* tab = tabs + turn * C;
+        const float* betas = betas_of + turn * C;
+        if (n >= 2) bar_sync(kBarStage + turn, all);  // the chunk before the last is through with its stage
+        if (n + 1 < chunks) {
+            fetch_gates(n + 1);
+            fetch_keys(n + 1);
+        }
+        bar_sync(kBarPrep, kPrep);
+        bar_arrive(kBarKeys + turn, all);
+        // pairs of the blocks' entries, rows lane / 4 and 8 more: P, and -A in two parts
+        uint32_t P[3][2][2], P2[3][2][2], A[2][2][2], B[2][2][2], T[8];
+        float2* lengths = reinterpret_cast<float2*>(smem + L::kLengthOff);
+#pragma unroll
+        for (int slot = 0; slot < 3; ++slot) {
+            if (slot == 2 && warp >= 2) break;
+            float kk[2][4] = {}, qk[2][4] = {}, qq[2][4] = {};
+            const uint32_t kb_at = keys + 16 * bj[slot] * L::kKeyPitch, ka_at = keys + 16 * bi[slot] * L::kKeyPitch;
+#pragma unroll
+            for (int s = 0; s < KP / 16; ++s) {
+                uint32_t kb[4], ka[4], qa[4];
+                if (slot > 0) ldsm(kb, rows_k<L::kKeyPitch>(kb_at, 0, 2 * s));
+                ldsm(ka, rows_a<L::kKeyPitch>(ka_at, 0, 2 * s));
+                ldsm(qa, rows_a<L::kKeyPitch>(ka_at + L::kKeyTile, 0, 2 * s));
+                // an A operand's registers are a B operand's of the same rows, in another order
+                if (slot == 0) kb[0] = ka[0], kb[1] = ka[2], kb[2] = ka[1], kb[3] = ka[3];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mma(qk[e], qa, kb[2 * e], kb[2 * e + 1]);
+                    mma(kk[e], ka, kb[2 * e], kb[2 * e + 1]);
+                    if (slot == 0) mma(qq[e], qa, qa[e], qa[e + 2]);
+                }
+            }
+            if (slot == 0) {
+                // the rows' lengths are on the diagonal: row lane / 4 + 8 e in the lane of its own column
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        if (lane / 4 == 2 * (lane % 4) + x)
+                            lengths[16 * warp + 8 * e + lane / 4] =
+                                p.normalize ? make_float2(rsqrtf(kk[e][2 * e + x] + kUnitEps), rsqrtf(qq[e][2 * e + x] + kUnitEps) * q_scale)
+                                            : make_float2(1.0f, 1.0f);
+                bar_sync(kBarPrep, kPrep);
+                if (tid >= kPrep - C) {
+                    const int i = tid - (kPrep - C), group = i / 16;
+                    long long mine = tab[i].sum, all_of_it = 0;
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const long long of_m = tab[16 * m + 15].sum;
+                        all_of_it += of_m;
+                        mine += m < group ? of_m : 0;
+                    }
+                    const float into = decay(mine);
+                    const float2 n = lengths[i];
+                    reinterpret_cast<Factors*>(smem + L::kFactorsOff)[turn * C + i] = {into * n.x, into * n.y, decay(all_of_it - mine) * n.x, betas[i]};
+                    if (i == C - 1) reinterpret_cast<float*>(smem + L::kGamOff)[turn] = into;
+                }
+            }
+            const int row = 16 * bi[slot] + lane / 4;
+            const Token i0 = tab[row], i1 = tab[row + 8];
+            const float2 l0 = lengths[row], l1 = lengths[row + 8];
+            float q0 = l0.y, q1 = l1.y, k0 = l0.x, k1 = l1.x;
+            if (slot > 0) {
+                // whole groups in between
+                long long far = 0;
+                for (int m = bj[slot] + 1; m < bi[slot]; ++m) far += tab[16 * m + 15].sum;
+                const float f = decay(far), d0 = f * i0.in, d1 = f * i1.in;
+                q0 *= d0, q1 *= d1, k0 *= d0, k1 *= d1;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int col = 8 * e + 2 * (lane % 4);
+                const Token j0 = tab[16 * bj[slot] + col], j1 = tab[16 * bj[slot] + col + 1];
+                const float n0 = lengths[16 * bj[slot] + col].x, n1 = lengths[16 * bj[slot] + col + 1].x;
+                float d[4], v[4], a[4];
+                if (slot > 0) {
+                    d[0] = d[2] = j0.out * n0;
+                    d[1] = d[3] = j1.out * n1;
+                } else {
+                    d[0] = decay(i0.sum - j0.sum) * n0, d[1] = decay(i0.sum - j1.sum) * n1;
+                    d[2] = decay(i1.sum - j0.sum) * n0, d[3] = decay(i1.sum - j1.sum) * n1;
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int i = lane / 4 + 8 * (x / 2), j = col + x % 2;
+                    v[x] = slot == 0 && j > i ? 0.0f : d[x] * (x < 2 ? q0 : q1) * qk[e][x];
+                    a[x] = slot == 0 && j >= i ? 0.0f : d[x] * (x < 2 ? k0 : k1) * kk[e][x];
+                }
+                P[slot][e][0] = pack(v[0], v[1]);
+                P[slot][e][1] = pack(v[2], v[3]);
+                if constexpr (kBack) {
+                    P2[slot][e][0] = pack_rest(v[0], v[1], P[slot][e][0]);
+                    P2[slot][e][1] = pack_rest(v[2], v[3], P[slot][e][1]);
+                }
+                if (slot > 0) {
+                    const int o = slot > 0 ? slot - 1 : 0;
+                    A[o][e][0] = pack(-a[0], -a[1]);
+                    A[o][e][1] = pack(-a[2], -a[3]);
+                    B[o][e][0] = pack_rest(-a[0], -a[1], A[o][e][0]);
+                    B[o][e][1] = pack_rest(-a[2], -a[3], A[o][e][1]);
+                } else {
+                    const float b0 = betas[row], b1 = betas[row + 8];
+                    scratch[20 * col + lane / 4] = b0 * a[0];
+                    scratch[20 * (col + 1) + lane / 4] = b0 * a[1];
+                    scratch[20 * col + lane / 4 + 8] = b1 * a[2];
+                    scratch[20 * (col + 1) + lane / 4 + 8] = b1 * a[3];
+                }
+            }
+            if (slot == 0) {
+                // lanes below 16 keep the first part of their column of the inverse times beta, the others the second
+                __syncwarp();
+                float t[16];
+                invert16(scratch, t);
+                const float bc = betas[16 * warp + lane % 16];
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const uint32_t high = pack(t[i] * bc, t[i + 1] * bc);
+                    T[i / 2] = lane < 16 ? high : pack_rest(t[i] * bc, t[i + 1] * bc, high);
+                }
+            }
+        }
+        if (n >= 1) bar_sync(kBarFree, all);  // the last chunk is through with its blocks
+        const uint32_t hi = base + L::kLOff, lo = hi + L::kSquare, ps = lo + L::kSquare;
+#pragma unroll
+        for (int slot = 0; slot < 3; ++slot) {
+            if (slot == 2 && warp >= 2) break;
+            const uint32_t at = rows_a<L::kPitch>(0, 16 * bi[slot], 2 * bj[slot]);
+            stsm(ps + at, P[slot][0][0], P[slot][0][1], P[slot][1][0], P[slot][1][1]);
+            if constexpr (kBack) stsm(ps + L::kSquare + at, P2[slot][0][0], P2[slot][0][1], P2[slot][1][0], P2[slot][1][1]);
+            if (slot > 0) {
+                const int o = slot > 0 ? slot - 1 : 0;
+                stsm(hi + at, A[o][0][0], A[o][0][1], A[o][1][0], A[o][1][1]);
+                stsm(lo + at, B[o][0][0], B[o][0][1], B[o][1][0], B[o][1][1]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)  // the inverse lies transposed: a lane has a row of it
+            store16(unit_at<L::kPitch>(lane < 16 ? hi : lo, 16 * warp + lane % 16, 2 * warp + u),
+                    make_uint4(T[4 * u], T[4 * u + 1], T[4 * u + 2], T[4 * u + 3]));
+        bar_arrive(kBarFull, all);
+        if (n + 1 < chunks) tokens(n + 1);
+    }
+}
+
+// Packed pairs of a strip to rows of memory: token (or state row) r of `n` goes to to + r stride.
+__device__ __forceinline__ void put_strip(uint32_t strip, __nv_bfloat16* to, int64_t stride, int n, int columns) {
+    __syncwarp();
+    const int lane = threadIdx.x % 32, u = lane % 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 16 * i + lane / 2;
+        if (r < n && 8 * u < columns) *reinterpret_cast<uint4*>(to + r * stride + 8 * u) = load16(strip_at(strip, r, u));
+    }
+    __syncwarp();
+}
+
+}  // namespace delta
+}  // namespace block
+}  // namespace ssdc

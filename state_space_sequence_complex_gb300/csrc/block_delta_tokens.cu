@@ -1,4 +1,4 @@
-// The delta rule token by token in fp32: forward, gradients, and one token for serving.
+// The delta rule token by token: forward and gradients of fp32 inputs, and one token of either type for serving.
 //
 // A state's columns are independent of each other: u_t = beta (v_t - c S^T k_t) takes a column's
 // dot product with k_t, and S = c S + k_t u_t^T adds to it. So a warp holds 16 columns in registers,
@@ -31,18 +31,16 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
 }
 
 // A tile of tokens from t0 into shared memory in fp32, zeros behind the last token and feature.
-template <typename T>
 __device__ void stage(float (*to)[kMaxDim], const Heads& a, int b, int64_t t0, int64_t end, int h, int n) {
     for (int i = threadIdx.x; i < kTile * kMaxDim; i += blockDim.x) {
         const int t = i / kMaxDim, d = i % kMaxDim;
-        to[t][d] = t0 + t < end && d < n ? to_f32(row<T>(a, b, t0 + t, h)[d]) : 0.0f;
+        to[t][d] = t0 + t < end && d < n ? row<float>(a, b, t0 + t, h)[d] : 0.0f;
     }
 }
 // The same from a dense (B, T, H, n) array.
-template <typename T>
 __device__ void stage_dense(float (*to)[kMaxDim], const void* p, const Delta& d, int b, int64_t t0, int64_t end, int h, int n) {
     const Heads a = {p, d.T * d.H * n, (int64_t)d.H * n, n};
-    stage<T>(to, a, b, t0, end, h, n);
+    stage(to, a, b, t0, end, h, n);
 }
 
 // Rows divided by their lengths: each warp takes every n-th token.
@@ -56,13 +54,12 @@ __device__ void unit(float (*x)[kMaxDim], float scale) {
 }
 
 // The decay and beta of a tile's tokens: {c, 1 - a, beta, 1 - beta}.
-template <typename T>
 __device__ void stage_gates(float4* to, const Delta& p, int b, int64_t t0, int64_t end, int h) {
     const int t = threadIdx.x;
     if (t < kTile) {
         float4 g = make_float4(1.0f, 0.0f, 0.0f, 1.0f);
         if (t0 + t < end) {
-            const float2 a = gate(to_f32(*row<T>(p.f, b, t0 + t, h))), be = gate(to_f32(*row<T>(p.beta, b, t0 + t, h)));
+            const float2 a = gate(*row<float>(p.f, b, t0 + t, h)), be = gate(*row<float>(p.beta, b, t0 + t, h));
             const bool first = p.reset != nullptr && p.reset[b * p.T + t0 + t] != 0;
             g = make_float4(first ? 0.0f : a.x, first ? 0.0f : a.y, be.x, be.y);
         }
@@ -75,21 +72,19 @@ struct Columns {  // a lane's part of a warp's 16 columns: rows 32 (i / 4) + 4 (
     float s[KR][4];
     __device__ __forceinline__ static int row(int i) { return (i / 4) * 32 + (threadIdx.x & 7) * 4 + i % 4; }
     __device__ __forceinline__ static int col() { return (threadIdx.x / 32) * 16 + ((threadIdx.x >> 3) & 3) * 4; }
-    template <typename T>
-    __device__ __forceinline__ void load(const T* p, int K, int V) {
+    __device__ __forceinline__ void load(const float* p, int K, int V) {
 #pragma unroll
         for (int i = 0; i < KR; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                s[i][j] = p != nullptr && row(i) < K && col() < V ? to_f32(p[(int64_t)row(i) * V + col() + j]) : 0.0f;
+                s[i][j] = p != nullptr && row(i) < K && col() < V ? p[(int64_t)row(i) * V + col() + j] : 0.0f;
     }
-    template <typename T>
-    __device__ __forceinline__ void store(T* p, int K, int V) const {
+    __device__ __forceinline__ void store(float* p, int K, int V) const {
 #pragma unroll
         for (int i = 0; i < KR; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (row(i) < K && col() < V) p[(int64_t)row(i) * V + col() + j] = from_f32<T>(s[i][j]);
+                if (row(i) < K && col() < V) p[(int64_t)row(i) * V + col() + j] = s[i][j];
     }
     __device__ __forceinline__ static void vec(float* x, const float* from) {
 #pragma unroll
@@ -129,11 +124,10 @@ struct Columns {  // a lane's part of a warp's 16 columns: rows 32 (i / 4) + 4 (
 };
 
 // A tile's rows of `n` values to a dense (B, T, H, n) array.
-template <typename T>
 __device__ void flush(void* p, float (*from)[kMaxDim], const Delta& d, int b, int64_t t0, int64_t end, int h, int n) {
     for (int i = threadIdx.x; i < kTile * n; i += blockDim.x) {
         const int t = i / n, c = i % n;
-        if (t0 + t < end) static_cast<T*>(p)[((b * d.T + t0 + t) * d.H + h) * n + c] = from_f32<T>(from[t][c]);
+        if (t0 + t < end) static_cast<float*>(p)[((b * d.T + t0 + t) * d.H + h) * n + c] = from[t][c];
     }
 }
 
@@ -141,7 +135,7 @@ __device__ __forceinline__ void write4(float* to, const float* v) {
     if ((threadIdx.x & 7) == 0) *reinterpret_cast<float4*>(to + Columns<4>::col()) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
-template <typename T, int KR>
+template <int KR>
 __global__ void __launch_bounds__(256) delta_tokens_fwd(const Delta p) {
     __shared__ float q[kTile][kMaxDim], k[kTile][kMaxDim], v[kTile][kMaxDim], o[kTile][kMaxDim], u[kTile][kMaxDim];
     __shared__ float4 gates[kTile];
@@ -151,10 +145,10 @@ __global__ void __launch_bounds__(256) delta_tokens_fwd(const Delta p) {
     S.load(p.h0 ? p.h0 + seq * size : nullptr, p.K, p.V);
     for (int64_t t0 = 0; t0 < p.T; t0 += kTile) {
         __syncthreads();
-        stage<T>(q, p.q, b, t0, p.T, g, p.K);
-        stage<T>(k, p.k, b, t0, p.T, g, p.K);
-        stage<T>(v, p.v, b, t0, p.T, h, p.V);
-        stage_gates<T>(gates, p, b, t0, p.T, h);
+        stage(q, p.q, b, t0, p.T, g, p.K);
+        stage(k, p.k, b, t0, p.T, g, p.K);
+        stage(v, p.v, b, t0, p.T, h, p.V);
+        stage_gates(gates, p, b, t0, p.T, h);
         __syncthreads();
         if (p.normalize) {
             unit(q, rsqrtf((float)p.K));
@@ -162,7 +156,7 @@ __global__ void __launch_bounds__(256) delta_tokens_fwd(const Delta p) {
             __syncthreads();
         }
         if (p.states != nullptr && t0 % kDeltaChunk == 0)
-            S.store(static_cast<T*>(p.states) + (seq * chunks + t0 / kDeltaChunk) * size, p.K, p.V);
+            S.store(static_cast<float*>(p.states) + (seq * chunks + t0 / kDeltaChunk) * size, p.K, p.V);
         const int n = (int)min((int64_t)kTile, p.T - t0);
         for (int t = 0; t < n; ++t) {
             const float4 gt = gates[t];
@@ -181,8 +175,8 @@ __global__ void __launch_bounds__(256) delta_tokens_fwd(const Delta p) {
             write4(o[t], d);
         }
         __syncthreads();
-        flush<T>(p.o, o, p, b, t0, p.T, h, p.V);
-        if (p.updates != nullptr) flush<T>(p.updates, u, p, b, t0, p.T, h, p.V);
+        flush(p.o, o, p, b, t0, p.T, h, p.V);
+        if (p.updates != nullptr) flush(p.updates, u, p, b, t0, p.T, h, p.V);
     }
     S.store(p.h_last + seq * size, p.K, p.V);
 }
@@ -205,7 +199,7 @@ __host__ __device__ inline Between between(const Delta& p) {
 
 // From the last token to the first, with dS the gradient of the state behind a token:
 //   dS += q do^T, du = dS^T k, dv = z = beta du, dk = dS u (so far), dS = c (dS - k z^T).
-template <typename T, int KR>
+template <int KR>
 __global__ void __launch_bounds__(256) delta_tokens_bwd_reverse(const Delta p) {
     extern __shared__ float sums[];  // [warps][kTile][kMaxDim]
     __shared__ float q[kTile][kMaxDim], k[kTile][kMaxDim], d_o[kTile][kMaxDim], u[kTile][kMaxDim], z[kTile][kMaxDim];
@@ -219,11 +213,11 @@ __global__ void __launch_bounds__(256) delta_tokens_bwd_reverse(const Delta p) {
     dS.load(p.dh_last ? p.dh_last + seq * size : nullptr, p.K, p.V);
     for (int64_t t0 = (p.T - 1) / kTile * kTile; t0 >= 0; t0 -= kTile) {
         __syncthreads();
-        stage<T>(q, p.q, b, t0, p.T, g, p.K);
-        stage<T>(k, p.k, b, t0, p.T, g, p.K);
-        stage<T>(d_o, p.d_o, b, t0, p.T, h, p.V);
-        stage_dense<T>(u, p.in_updates, p, b, t0, p.T, h, p.V);
-        stage_gates<T>(gates, p, b, t0, p.T, h);
+        stage(q, p.q, b, t0, p.T, g, p.K);
+        stage(k, p.k, b, t0, p.T, g, p.K);
+        stage(d_o, p.d_o, b, t0, p.T, h, p.V);
+        stage_dense(u, p.in_updates, p, b, t0, p.T, h, p.V);
+        stage_gates(gates, p, b, t0, p.T, h);
         __syncthreads();
         if (p.normalize) {
             unit(q, rsqrtf((float)p.K));
@@ -263,7 +257,7 @@ __global__ void __launch_bounds__(256) delta_tokens_bwd_reverse(const Delta p) {
                 for (int i = 0; i < KR; ++i) dS.s[i][j] = gt.x * fmaf(-x[i], d[j], dS.s[i][j]);
         }
         __syncthreads();
-        flush<T>(p.dv, z, p, b, t0, p.T, h, p.V);
+        flush(p.dv, z, p, b, t0, p.T, h, p.V);
         for (int i = threadIdx.x; i < n * p.K; i += blockDim.x) {
             const int t = i / p.K, c = i % p.K;
             float s = 0.0f;
@@ -280,7 +274,7 @@ __global__ void __launch_bounds__(256) delta_tokens_bwd_reverse(const Delta p) {
 }
 
 // Forward again through every chunk from its kept state: dq = S_t do, dk -= c S_{t-1} z.
-template <typename T, int KR>
+template <int KR>
 __global__ void __launch_bounds__(256) delta_tokens_bwd_forward(const Delta p) {
     extern __shared__ float sums[];  // [2][warps][kTile][kMaxDim]
     __shared__ float q[kTile][kMaxDim], k[kTile][kMaxDim], d_o[kTile][kMaxDim], u[kTile][kMaxDim], z[kTile][kMaxDim];
@@ -292,15 +286,15 @@ __global__ void __launch_bounds__(256) delta_tokens_bwd_forward(const Delta p) {
     const Between w = between(p);
     float* sums_q = sums + warps * kTile * kMaxDim;
     Columns<KR> S;
-    S.load(static_cast<const T*>(p.in_states) + (seq * chunks + c0) * size, p.K, p.V);
+    S.load(static_cast<const float*>(p.in_states) + (seq * chunks + c0) * size, p.K, p.V);
     for (int64_t t0 = c0 * kDeltaChunk; t0 < end; t0 += kTile) {
         __syncthreads();
-        stage<T>(q, p.q, b, t0, end, g, p.K);
-        stage<T>(k, p.k, b, t0, end, g, p.K);
-        stage<T>(d_o, p.d_o, b, t0, end, h, p.V);
-        stage_dense<T>(u, p.in_updates, p, b, t0, end, h, p.V);
-        stage_dense<T>(z, p.dv, p, b, t0, end, h, p.V);
-        stage_gates<T>(gates, p, b, t0, end, h);
+        stage(q, p.q, b, t0, end, g, p.K);
+        stage(k, p.k, b, t0, end, g, p.K);
+        stage(d_o, p.d_o, b, t0, end, h, p.V);
+        stage_dense(u, p.in_updates, p, b, t0, end, h, p.V);
+        stage_dense(z, p.dv, p, b, t0, end, h, p.V);
+        stage_gates(gates, p, b, t0, end, h);
         __syncthreads();
         if (p.normalize) {
             unit(q, rsqrtf((float)p.K));
@@ -348,7 +342,7 @@ __global__ void __launch_bounds__(256) delta_tokens_bwd_forward(const Delta p) {
 //   in front:   exp(G_i) (do_i.S0^T q_i - z_i.S0^T k_i)
 //   behind:     exp(G_C - G_j) u_j.dS^T k_j,  both: exp(G_C) <S0, dS>
 constexpr int kPitch = kMaxDim + 4;
-template <typename T, int KR>
+template <int KR>
 __global__ void __launch_bounds__(256) delta_tokens_bwd_gates(const Delta p) {
     extern __shared__ float rows[];  // [5][kDeltaChunk][kPitch]: q, k, do, u, z
     __shared__ float pair[kDeltaChunk][kDeltaChunk + 1], front[kDeltaChunk], behind[kDeltaChunk], part[2][8][kDeltaChunk];
@@ -366,13 +360,13 @@ __global__ void __launch_bounds__(256) delta_tokens_bwd_gates(const Delta p) {
     const Heads from[5] = {p.q, p.k, p.d_o, {p.in_updates, p.T * dense, dense, p.V}, {p.dv, p.T * dense, dense, p.V}};
     for (int i = threadIdx.x; i < 5 * kDeltaChunk * kMaxDim; i += blockDim.x) {
         const int a = i / (kDeltaChunk * kMaxDim), t = i / kMaxDim % kDeltaChunk, d = i % kMaxDim;
-        rows[a * kRows + t * kPitch + d] = t < n && d < (a < 2 ? p.K : p.V) ? to_f32(row<T>(from[a], b, t0 + t, a < 2 ? g : h)[d]) : 0.0f;
+        rows[a * kRows + t * kPitch + d] = t < n && d < (a < 2 ? p.K : p.V) ? row<float>(from[a], b, t0 + t, a < 2 ? g : h)[d] : 0.0f;
     }
     if (threadIdx.x == 0) {
         double s = 0.0;
         int r = 0;
         for (int t = 0; t < n; ++t) {
-            const double f = to_f32(*row<T>(p.f, b, t0 + t, h));
+            const double f = *row<float>(p.f, b, t0 + t, h);
             s -= f > 0.0 ? log1p(exp(-f)) : log1p(exp(f)) - f;  // log sigmoid(f)
             r += p.reset != nullptr && p.reset[b * p.T + t0 + t] != 0;
             sum[t] = s;
@@ -398,7 +392,7 @@ __global__ void __launch_bounds__(256) delta_tokens_bwd_gates(const Delta p) {
         return s + __shfl_xor_sync(0xffffffffu, s, 16);
     };
     float x[KR], d[4];
-    S.load(static_cast<const T*>(p.in_states) + (seq * chunks + c0) * size, p.K, p.V);
+    S.load(static_cast<const float*>(p.in_states) + (seq * chunks + c0) * size, p.K, p.V);
     for (int t = 0; t < n; ++t) {
         S.vec(x, q + t * kPitch);
         S.dots(x, d);
@@ -468,13 +462,12 @@ __global__ void __launch_bounds__(256) delta_tokens_bwd_gates(const Delta p) {
         }
         const int64_t at = (b * p.T + t0 + r) * p.H + h;
         const bool first = p.reset != nullptr && p.reset[b * p.T + t0 + r] != 0;
-        static_cast<T*>(p.df)[at] = from_f32<T>(first ? 0.0f : s * gate(to_f32(*row<T>(p.f, b, t0 + r, h))).y);
-        static_cast<T*>(p.db)[at] = from_f32<T>(w.e[at] * gate(to_f32(*row<T>(p.beta, b, t0 + r, h))).y);
+        static_cast<float*>(p.df)[at] = first ? 0.0f : s * gate(*row<float>(p.f, b, t0 + r, h)).y;
+        static_cast<float*>(p.db)[at] = w.e[at] * gate(*row<float>(p.beta, b, t0 + r, h)).y;
     }
 }
 
 // A key head's gradients: its value heads' summed, taken back through the division by the length.
-template <typename T>
 __global__ void __launch_bounds__(128) delta_tokens_bwd_finish(const Delta p) {
     const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / 32, rows = p.B * p.T * p.G;
     if (at >= rows) return;
@@ -482,16 +475,16 @@ __global__ void __launch_bounds__(128) delta_tokens_bwd_finish(const Delta p) {
     const int64_t bt = at / p.G, b = bt / p.T, t = bt % p.T;
     const Between w = between(p);
     for (int side = 0; side < 2; ++side) {
-        const T* x = row<T>(side ? p.k : p.q, b, t, g);
+        const float* x = row<float>(side ? p.k : p.q, b, t, g);
         const float* d = (side ? w.dk : w.dq) + (bt * p.H + g * R) * p.K;
-        T* to = static_cast<T*>(side ? p.dk : p.dq) + at * p.K;
+        float* to = static_cast<float*>(side ? p.dk : p.dq) + at * p.K;
         float v[4], s[4], xx = 0.0f, xs = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int c = lane + 32 * i;
             v[i] = s[i] = 0.0f;
             if (c < p.K) {
-                v[i] = to_f32(x[c]);
+                v[i] = x[c];
                 for (int r = 0; r < R; ++r) s[i] += d[(int64_t)r * p.K + c];
             }
             xx = fmaf(v[i], v[i], xx);
@@ -505,7 +498,7 @@ __global__ void __launch_bounds__(128) delta_tokens_bwd_finish(const Delta p) {
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < p.K) to[lane + 32 * i] = from_f32<T>(scale * fmaf(-along, v[i], s[i]));
+            if (lane + 32 * i < p.K) to[lane + 32 * i] = scale * fmaf(-along, v[i], s[i]);
     }
 }
 
@@ -612,28 +605,28 @@ void step_launch(const Delta& p, cudaStream_t stream) {
     else step_launch<T, 8>(p, stream);
 }
 
-template <typename T, int KR>
+template <int KR>
 int fwd_launch(const Delta& p, cudaStream_t stream) {
-    delta_tokens_fwd<T, KR><<<p.B * p.H, 32 * ((p.V + 15) / 16), 0, stream>>>(p);
+    delta_tokens_fwd<KR><<<p.B * p.H, 32 * ((p.V + 15) / 16), 0, stream>>>(p);
     return 1;
 }
 
-template <typename T, int KR>
+template <int KR>
 int bwd_launch(const Delta& p, cudaStream_t stream) {
     const int warps = (p.V + 15) / 16;
     const int64_t chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk, rows = p.B * p.T * p.G;
     const size_t one = (size_t)warps * kTile * kMaxDim * sizeof(float);
     constexpr int kGates = 5 * kDeltaChunk * kPitch * 4;
     static std::atomic<uint64_t> first{0}, second{0}, third{0};
-    if (allow_smem(delta_tokens_bwd_reverse<T, KR>, 8 * kTile * kMaxDim * 4, first) != cudaSuccess ||
-        allow_smem(delta_tokens_bwd_forward<T, KR>, 16 * kTile * kMaxDim * 4, second) != cudaSuccess ||
-        allow_smem(delta_tokens_bwd_gates<T, KR>, kGates, third) != cudaSuccess)
+    if (allow_smem(delta_tokens_bwd_reverse<KR>, 8 * kTile * kMaxDim * 4, first) != cudaSuccess ||
+        allow_smem(delta_tokens_bwd_forward<KR>, 16 * kTile * kMaxDim * 4, second) != cudaSuccess ||
+        allow_smem(delta_tokens_bwd_gates<KR>, kGates, third) != cudaSuccess)
         return SSDC_ERR_CUDA;
     if (p.B * p.H * chunks > INT32_MAX || rows / 4 >= INT32_MAX) return SSDC_ERR_UNSUPPORTED;
-    delta_tokens_bwd_reverse<T, KR><<<p.B * p.H, 32 * warps, one, stream>>>(p);
-    delta_tokens_bwd_forward<T, KR><<<(unsigned)(p.B * p.H * chunks), 32 * warps, 2 * one, stream>>>(p);
-    delta_tokens_bwd_gates<T, KR><<<(unsigned)(p.B * p.H * chunks), 32 * warps, kGates, stream>>>(p);
-    delta_tokens_bwd_finish<T><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(p);
+    delta_tokens_bwd_reverse<KR><<<p.B * p.H, 32 * warps, one, stream>>>(p);
+    delta_tokens_bwd_forward<KR><<<(unsigned)(p.B * p.H * chunks), 32 * warps, 2 * one, stream>>>(p);
+    delta_tokens_bwd_gates<KR><<<(unsigned)(p.B * p.H * chunks), 32 * warps, kGates, stream>>>(p);
+    delta_tokens_bwd_finish<<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(p);
     return 4;
 }
 
@@ -646,17 +639,16 @@ int delta_step_launch(const Delta& p, cudaStream_t stream) {
 }
 
 int delta_tokens_fwd_launch(const Delta& p, cudaStream_t stream) {
-    if (p.bf16) return p.K > 64 ? fwd_launch<__nv_bfloat16, 16>(p, stream) : fwd_launch<__nv_bfloat16, 8>(p, stream);
-    return p.K > 64 ? fwd_launch<float, 16>(p, stream) : fwd_launch<float, 8>(p, stream);
+    return p.K > 64 ? fwd_launch<16>(p, stream) : fwd_launch<8>(p, stream);
 }
 
 int delta_tokens_bwd_launch(const Delta& p, cudaStream_t stream) {
-    if (p.bf16) return p.K > 64 ? bwd_launch<__nv_bfloat16, 16>(p, stream) : bwd_launch<__nv_bfloat16, 8>(p, stream);
-    return p.K > 64 ? bwd_launch<float, 16>(p, stream) : bwd_launch<float, 8>(p, stream);
+    return p.K > 64 ? bwd_launch<16>(p, stream) : bwd_launch<8>(p, stream);
 }
 
 size_t delta_bwd_workspace(const Delta& p) {
     const int64_t rows = p.B * p.T * p.H, chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk;
+    if (p.bf16) return (size_t)(p.B * p.H * chunks * p.K * p.V) * 2;  // the states' gradients
     return (size_t)(rows * (2 * p.K + 1) + p.B * p.H * chunks * p.K * p.V) * sizeof(float);
 }
 

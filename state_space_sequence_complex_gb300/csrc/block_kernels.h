@@ -174,7 +174,9 @@ struct Delta {
 };
 constexpr int kDeltaChunk = SSD_DELTA_STATE_TOKENS;
 int delta_step_launch(const Delta& p, cudaStream_t stream);
-int delta_tokens_fwd_launch(const Delta& p, cudaStream_t stream);
+int delta_fwd_launch(const Delta& p, cudaStream_t stream);  // bfloat16, in chunks
+int delta_tokens_fwd_launch(const Delta& p, cudaStream_t stream);  // fp32, token by token
+int delta_bwd_launch(const Delta& p, cudaStream_t stream);
 int delta_tokens_bwd_launch(const Delta& p, cudaStream_t stream);
 size_t delta_bwd_workspace(const Delta& p);
 
