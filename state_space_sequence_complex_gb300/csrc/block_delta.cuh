@@ -82,30 +82,24 @@ template <int kPitch>
 __device__ __forceinline__ uint32_t unit_at(uint32_t tile, int r, int u) {
     return tile + r * kPitch + ((u ^ (r & 7)) << 4);
 }
-// Lane addresses of four 8 x 8 matrices. rows_k: B operand from rows n with k along them, two n-tiles
-// from row n0 and 16 values of k from unit u. cols_k: B operand from rows k (16 from k0) with n along them, units
-// u and u + 1. rows_a: A operand, 16 rows from r0. cols_a: A operand of the transposed tile, 16 columns from unit u as
-// its rows and 16 rows from k0 as its k.
+// Lane offsets of four 8 x 8 matrices within a tile, for rows that start at a multiple of 16 and units that start at an
+// even one, 2 i: to be added to the tile and 16-row offset, so that one register serves every tile of this pitch.
+//   across[i]  the matrices lie rows first: an A operand's 16 rows by units 2 i, 2 i + 1 (ldsm); the B operand whose k are
+//              the rows and whose n are the columns of both units (ldsm_t)
+//   down[i]    units first: the B operand of 16 rows n with k along them (ldsm); the A operand of the transposed
+//              tile, whose rows are the columns of both units (ldsm_t)
 template <int kPitch>
-__device__ __forceinline__ uint32_t rows_k(uint32_t tile, int n0, int u) {
-    const int l = threadIdx.x % 32, m = l / 8;
-    return unit_at<kPitch>(tile, n0 + 8 * (m / 2) + l % 8, u + m % 2);
-}
-template <int kPitch>
-__device__ __forceinline__ uint32_t cols_k(uint32_t tile, int k0, int u) {
-    const int l = threadIdx.x % 32, m = l / 8;
-    return unit_at<kPitch>(tile, k0 + 8 * (m % 2) + l % 8, u + m / 2);
-}
-template <int kPitch>
-__device__ __forceinline__ uint32_t rows_a(uint32_t tile, int r0, int u) {
-    const int l = threadIdx.x % 32, m = l / 8;
-    return unit_at<kPitch>(tile, r0 + 8 * (m % 2) + l % 8, u + m / 2);
-}
-template <int kPitch>
-__device__ __forceinline__ uint32_t cols_a(uint32_t tile, int k0, int u) {
-    const int l = threadIdx.x % 32, m = l / 8;
-    return unit_at<kPitch>(tile, k0 + 8 * (m / 2) + l % 8, u + m % 2);
-}
+struct Lanes {
+    uint32_t across[kPitch / 32], down[kPitch / 32];
+    __device__ __forceinline__ explicit Lanes(uint32_t base) {
+        const int l = threadIdx.x % 32, m = l / 8, r = l % 8;
+#pragma unroll
+        for (int i = 0; i < kPitch / 32; ++i) {
+            across[i] = base + (8 * (m % 2) + r) * kPitch + (((2 * i + m / 2) ^ r) << 4);
+            down[i] = base + (8 * (m / 2) + r) * kPitch + (((2 * i + m % 2) ^ r) << 4);
+        }
+    }
+};
 
 // A strip of 16 columns, rows of 32 bytes: unit u (0, 1) of row r.
 __device__ __forceinline__ uint32_t strip_at(uint32_t strip, int r, int u) { return strip + r * 32 + ((u ^ ((r >> 2) & 1)) << 4); }
@@ -175,9 +169,10 @@ constexpr float kUnit = 1099511627776.0f, kPerUnit = 9.094947018e-13f;  // 2^40,
 
 __device__ __forceinline__ float decay(long long log2_units) { return exp2_fast(__ll2float_rn(log2_units) * kPerUnit); }
 
-// 16 lanes: the entries of a group's tokens, one to a lane. Sums are in units of 2^-40 (they are at most 2^14),
+// The entries of a group's tokens, one to a lane of the first 16, or of each half of the warp a group of its own (kBoth). Sums are in units of 2^-40 (they are at most 2^14),
 // which takes integer additions only and rounds nothing but each token's own term; differences keep
 // their digits however large the sums are.
+template <bool kBoth>
 __device__ __forceinline__ void scan_group(float lg, Token* tab) {
     const int lane = threadIdx.x % 32;
     long long s = __float2ll_rn(lg * kUnit);
@@ -187,7 +182,7 @@ __device__ __forceinline__ void scan_group(float lg, Token* tab) {
         if (lane % 16 >= o) s += t;
     }
     const long long end = __shfl_sync(0xffffffffu, s, 15, 16);
-    if (lane < 16) tab[lane] = {s, decay(s), decay(end - s)};
+    if (kBoth || lane < 16) tab[lane % 16] = {s, decay(s), decay(end - s)};
 }
 
 // The sum of squares of a tile's row.

@@ -32,6 +32,8 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
     const int columns = min(16, p.V - col0);
     const int64_t chunks = (p.T + C - 1) / C, seq = (int64_t)b * p.H + h;
     const uint32_t strips = base + L::kStripOff + w * 2 * L::kStrip;
+    const Lanes<L::kKeyPitch> key_lanes(base);
+    const Lanes<L::kPitch> lanes(base);
     const int fetch_u = lane % 2, fetch_r = lane / 2;
     const bool has_unit = 8 * fetch_u < columns;
     const __nv_bfloat16* row = bf16(p.d_o.p) + b * p.d_o.b + h * p.d_o.h + ((chunks - 1) * C + fetch_r) * p.d_o.t + col0 + (has_unit ? 8 * fetch_u : 0);
@@ -73,7 +75,7 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         if (n + 1 < chunks) fetch_do(n + 1);
         else ptx::cp_async_commit();
         bar_sync(kBarKeys + turn, all);
-        const uint32_t keys = base + (int)(n % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
+        const uint32_t keys = (int)(n % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
         float X[8][4] = {};
 #pragma unroll
         for (int s = 0; s < KP / 16; ++s) {
@@ -82,7 +84,7 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 uint32_t kb[4];
-                ldsm(kb, rows_k<L::kKeyPitch>(keys, 16 * m, 2 * s));
+                ldsm(kb, keys + 16 * m * L::kKeyPitch + key_lanes.down[s]);
                 mma(X[2 * m], a.hi, kb[0], kb[1]);
                 mma(X[2 * m + 1], a.hi, kb[2], kb[3]);
                 mma(X[2 * m], a.lo, kb[0], kb[1]);
@@ -93,7 +95,7 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         __syncwarp();
         bar_sync(kBarFull, all);
         const Factors* factors = reinterpret_cast<const Factors*>(smem + L::kFactorsOff) + turn * C;
-        const uint32_t hi = base + L::kLOff, lo = hi + L::kSquare, ps = lo + L::kSquare, ps2 = ps + L::kSquare;
+        constexpr uint32_t hi = L::kLOff, lo = hi + L::kSquare, ps = lo + L::kSquare, ps2 = ps + L::kSquare;
         const float gam = reinterpret_cast<const float*>(smem + L::kGamOff)[turn];
 #pragma unroll
         for (int m = 0; m < 8; ++m)
@@ -112,8 +114,8 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
 #pragma unroll
             for (int j = 0; j <= i; ++j) {
                 uint32_t ph[4], pl[4];
-                ldsm_t(ph, cols_k<L::kPitch>(ps, 16 * i, 2 * j));
-                ldsm_t(pl, cols_k<L::kPitch>(ps2, 16 * i, 2 * j));
+                ldsm_t(ph, ps + 16 * i * L::kPitch + lanes.across[j]);
+                ldsm_t(pl, ps2 + 16 * i * L::kPitch + lanes.across[j]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mma(X[2 * j + e], d_o[i], pl[2 * e], pl[2 * e + 1]);
@@ -126,8 +128,8 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
             Split a;
             uint32_t bh[4], bl[4];
             a.set(X[2 * r], X[2 * r + 1]);
-            ldsm(bh, rows_k<L::kPitch>(hi, 16 * r, 2 * r));
-            ldsm(bl, rows_k<L::kPitch>(lo, 16 * r, 2 * r));
+            ldsm(bh, hi + 16 * r * L::kPitch + lanes.down[r]);
+            ldsm(bl, lo + 16 * r * L::kPitch + lanes.down[r]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 X[2 * r + e][0] = X[2 * r + e][1] = X[2 * r + e][2] = X[2 * r + e][3] = 0.0f;
@@ -138,8 +140,8 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
             a.set(X[2 * r], X[2 * r + 1]);  // Z of this block
 #pragma unroll
             for (int j = 0; j < r; ++j) {
-                ldsm_t(bh, cols_k<L::kPitch>(hi, 16 * r, 2 * j));
-                ldsm_t(bl, cols_k<L::kPitch>(lo, 16 * r, 2 * j));
+                ldsm_t(bh, hi + 16 * r * L::kPitch + lanes.across[j]);
+                ldsm_t(bl, lo + 16 * r * L::kPitch + lanes.across[j]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mma(X[2 * j + e], a.hi, bh[2 * e], bh[2 * e + 1]);
@@ -184,8 +186,8 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
 #pragma unroll
             for (int i = 0; i < KT; i += 2) {
                 uint32_t qb[4], kb[4];
-                ldsm_t(qb, cols_k<L::kKeyPitch>(queries, 16 * s, i));
-                ldsm_t(kb, cols_k<L::kKeyPitch>(keys, 16 * s, i));
+                ldsm_t(qb, queries + 16 * s * L::kKeyPitch + key_lanes.across[i / 2]);
+                ldsm_t(kb, keys + 16 * s * L::kKeyPitch + key_lanes.across[i / 2]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mma(S[i + e], a.hi, qb[2 * e], qb[2 * e + 1]);
@@ -227,54 +229,58 @@ __global__ void __launch_bounds__(kPrep + 32 * NW, KP == 64 && NW == 4 ? 2 : 1) 
 
 // ---- the second kernel
 
-// A tile of rows of `units` 16-byte units (a power of two), kPitch bytes apart.
 template <int KP, int VP>
 struct Tiles {
     static constexpr int kKeyPitch = KP * 2, kPitch = VP * 2, kSquarePitch = C * 2;
     static constexpr int kK = 0, kQ = kK + C * kKeyPitch;
     static constexpr int kDo = kQ + C * kKeyPitch, kZ = kDo + C * kPitch, kU = kZ + C * kPitch;
     static constexpr int kS = kU + C * kPitch, kDs = kS + KP * kPitch;
-    // M1 and M2, transposed as they are read, over the states, which have been read by then
+    // M1 and M2 over the states, which have been read by then
     static constexpr int kM1 = kS, kM2 = kM1 + C * kSquarePitch;
     static constexpr int kSmall = kDs + KP * kPitch;
 };
 struct Small {
     Token tab[C];
-    Factors factors[C];
-    float2 lengths[C];
+    float2 lengths[C];                 // rk, rq
+    float into[C], out_of[C], beta_rest[C], rest[C];  // Gam, gam, exp(-b), 1 - a
     float columns[4][C], rows[C], diagonal[C], front[2][C], behind[2][C];
-    float both[8], gate[C], gam, pad[3];
+    float both[8], gam;
 };
 
-template <int kPitch>
-__device__ __forceinline__ void fetch_rows(uint32_t tile, const __nv_bfloat16* from, int64_t stride, int rows, int have, int n, bool units) {
-    const int per = kPitch / 16;
-    for (int i = threadIdx.x; i < rows * per; i += blockDim.x) {
-        const int r = i / per, u = i % per;
-        const bool valid = r < have && 8 * u < n;
-        const __nv_bfloat16* at = valid ? from + r * stride + 8 * u : from;
-        if (units) fetch<true>(unit_at<kPitch>(tile, r, u), at, valid);
-        else fetch<false>(unit_at<kPitch>(tile, r, u), at, valid);
+// `rows` rows of a tile, a unit of 16 bytes to a thread at a time, zeros from row `have` and column n on.
+template <int kPitch, int kRows, int kThreads, bool kUnitRows>
+__device__ __forceinline__ void fetch_rows(uint32_t tile, const void* array, int64_t first, int64_t stride, int have, int n) {
+    constexpr int kUnits = kPitch / 16, kAtOnce = kThreads / kUnits;
+    const int u = threadIdx.x % kUnits, r = threadIdx.x / kUnits;
+    const bool has_unit = 8 * u < n;
+    const __nv_bfloat16* from = bf16(array) + first + r * stride + (has_unit ? 8 * u : 0);
+#pragma unroll
+    for (int i = 0; i < kRows / kAtOnce; ++i) {
+        fetch<kUnitRows>(unit_at<kPitch>(tile, r + i * kAtOnce, u), from, has_unit && r + i * kAtOnce < have);
+        from += kAtOnce * stride;
     }
 }
 
 // KP / 64 groups of four warps: warp w % 4 has 16 tokens' rows, and of the features of q and k 64 of its group's.
-template <int KP, int VP>
-__global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bwd_chunks(const __grid_constant__ Delta p, bool q_units, bool k_units,
-                                                                                         bool do_units) {
+template <int KP, int VP, bool kUnitRows>
+__global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bwd_chunks(const __grid_constant__ Delta p) {
     using L = Tiles<KP, VP>;
+    constexpr int kThreads = 2 * KP;
     extern __shared__ __align__(128) char smem[];
     const uint32_t base = ptx::smem_addr(smem);
     Small& sm = *reinterpret_cast<Small*>(smem + L::kSmall);
-    const int tid = threadIdx.x, lane = tid % 32, w = tid / 32 % 4, half = tid / 128;
-    const int64_t chunks = (p.T + C - 1) / C;
-    const int64_t c = blockIdx.x % chunks, bg = blockIdx.x / chunks;
+    const int tid = threadIdx.x, lane = tid % 32, w = tid / 32 % 4, half = KP > 64 ? tid / 128 : 0;
+    const int64_t chunks = (p.T + C - 1) / C, c = blockIdx.x % chunks, bg = blockIdx.x / chunks;
     const int b = (int)(bg / p.G), g = (int)(bg % p.G), R = p.H / p.G;
     const int64_t t0 = c * C;
     const int n_tokens = (int)min((int64_t)C, p.T - t0);
     const float q_scale = p.normalize ? rsqrtf((float)p.K) : 1.0f;
-    fetch_rows<L::kKeyPitch>(base + L::kK, bf16(p.k.p) + b * p.k.b + t0 * p.k.t + g * p.k.h, p.k.t, C, n_tokens, p.K, k_units);
-    fetch_rows<L::kKeyPitch>(base + L::kQ, bf16(p.q.p) + b * p.q.b + t0 * p.q.t + g * p.q.h, p.q.t, C, n_tokens, p.K, q_units);
+    fetch_rows<L::kKeyPitch, C, kThreads, kUnitRows>(base + L::kK, p.k.p, b * p.k.b + t0 * p.k.t + g * p.k.h, p.k.t, n_tokens, p.K);
+    fetch_rows<L::kKeyPitch, C, kThreads, kUnitRows>(base + L::kQ, p.q.p, b * p.q.b + t0 * p.q.t + g * p.q.h, p.q.t, n_tokens, p.K);
+    const Lanes<L::kKeyPitch> key_lanes(base);
+    const Lanes<L::kPitch> lanes(base);
+    // (units from the 8th on are 128 bytes further, as only an offset's low three bits of the unit are moved)
+    const uint32_t half_key = 128 * half, own_key = 16 * w * L::kKeyPitch, own = 16 * w * L::kPitch, feature_rows = 64 * half * L::kPitch;
     // rows lane / 4 and 8 more of the warp's 16, features 64 half + 8 i + 2 (lane % 4) and the next
     float dq[8][4] = {}, dk[8][4] = {};
     const int row0 = 16 * w + lane / 4;
@@ -282,43 +288,32 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
         const int h = g * R + r;
         const int64_t seq = (int64_t)b * p.H + h, dense = (int64_t)p.H * p.V, at = ((b * p.T + t0) * p.H + h) * p.V;
         const int64_t state = (seq * chunks + c) * p.K * p.V;
-        __syncthreads();  // the head before is through with the tiles
-        fetch_rows<L::kPitch>(base + L::kDo, bf16(p.d_o.p) + b * p.d_o.b + t0 * p.d_o.t + h * p.d_o.h, p.d_o.t, C, n_tokens, p.V, do_units);
-        fetch_rows<L::kPitch>(base + L::kZ, bf16(p.dv) + at, dense, C, n_tokens, p.V, true);
-        fetch_rows<L::kPitch>(base + L::kU, bf16(p.in_updates) + at, dense, C, n_tokens, p.V, true);
-        fetch_rows<L::kPitch>(base + L::kS, bf16(p.in_states) + state, p.V, KP, p.K, p.V, true);
-        fetch_rows<L::kPitch>(base + L::kDs, bf16(p.ws) + state, p.V, KP, p.K, p.V, true);
-        ptx::cp_async_commit();
-        float beta_rest = 0.0f;  // exp(-b)
-        if (tid < C) {
+        uint16_t f_raw = 0, b_raw = 0;
+        uint8_t mark = 0;
+        if (tid < n_tokens) {
             const int64_t t = t0 + tid;
-            float lg = 0.0f, rest = 0.0f;
-            if (tid < n_tokens) {
-                const float f = to_f32(bf16(p.f.p)[b * p.f.b + t * p.f.t + h * p.f.h]), e = expf(-fabsf(f));
-                const float s = log1pf(e), l = f >= 0.0f ? -s : f - s;
-                const bool first = p.reset != nullptr && p.reset[b * p.T + t] != 0;
-                lg = first || l < -177.0f ? -256.0f : l * kLog2e;
-                rest = first ? 0.0f : (f >= 0.0f ? e : 1.0f) / (1.0f + e);  // 1 - a
-                // where beta is below e^-80 so are u and z, and their product is zero
-                beta_rest = expf(fminf(-to_f32(bf16(p.beta.p)[b * p.beta.b + t * p.beta.t + h * p.beta.h]), 80.0f));
-            }
-            sm.gate[tid] = rest;
-            const int l = lane % 16;
-            long long s = __float2ll_rn(lg * kUnit);
-#pragma unroll
-            for (int o = 1; o < 16; o *= 2) {
-                const long long x = __shfl_up_sync(0xffffffffu, s, o, 16);
-                if (l >= o) s += x;
-            }
-            const long long end = __shfl_sync(0xffffffffu, s, 15, 16);
-            sm.tab[tid] = {s, decay(s), decay(end - s)};
+            f_raw = static_cast<const uint16_t*>(p.f.p)[b * p.f.b + t * p.f.t + h * p.f.h];
+            b_raw = static_cast<const uint16_t*>(p.beta.p)[b * p.beta.b + t * p.beta.t + h * p.beta.h];
+            if (p.reset != nullptr) mark = p.reset[b * p.T + t];
+        }
+        __syncthreads();  // the head before is through with the tiles
+        fetch_rows<L::kPitch, C, kThreads, kUnitRows>(base + L::kDo, p.d_o.p, b * p.d_o.b + t0 * p.d_o.t + h * p.d_o.h, p.d_o.t, n_tokens, p.V);
+        fetch_rows<L::kPitch, C, kThreads, true>(base + L::kZ, p.dv, at, dense, n_tokens, p.V);
+        fetch_rows<L::kPitch, C, kThreads, true>(base + L::kU, p.in_updates, at, dense, n_tokens, p.V);
+        fetch_rows<L::kPitch, KP, kThreads, true>(base + L::kS, p.in_states, state, p.V, p.K, p.V);
+        fetch_rows<L::kPitch, KP, kThreads, true>(base + L::kDs, p.ws, state, p.V, p.K, p.V);
+        ptx::cp_async_commit();
+        if (tid < C) {
+            const bool there = tid < n_tokens;
+            const float f = __uint_as_float((uint32_t)f_raw << 16), e = expf(-fabsf(f));
+            const float s = log1pf(e), l = f >= 0.0f ? -s : f - s;
+            const float lg = !there ? 0.0f : mark != 0 || l < -177.0f ? -256.0f : l * kLog2e;
+            sm.rest[tid] = mark != 0 ? 0.0f : (f >= 0.0f ? e : 1.0f) / (1.0f + e);
+            // where beta is below e^-80 so are u and z, and their product is zero
+            sm.beta_rest[tid] = expf(fminf(-__uint_as_float((uint32_t)b_raw << 16), 80.0f));
+            scan_group<true>(lg, sm.tab + 16 * (tid / 16));
         }
         ptx::cp_async_wait<0>();
-        __syncthreads();
-        if (r == 0 && tid < 2 * C) {
-            const float n = p.normalize ? rsqrtf(row_square<L::kKeyPitch>(base + (tid < C ? L::kK : L::kQ), tid % C) + kUnitEps) : 1.0f;
-            reinterpret_cast<float*>(&sm.lengths[tid % C])[tid / C] = tid < C ? n : n * q_scale;
-        }
         __syncthreads();
         if (tid < C) {
             const int group = tid / 16;
@@ -330,26 +325,30 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
                 mine += m < group ? of_m : 0;
             }
             const float into = decay(mine);
-            sm.factors[tid] = {into, 0.0f, decay(whole - mine), beta_rest};
+            sm.into[tid] = into;
+            sm.out_of[tid] = decay(whole - mine);
             if (tid == C - 1) sm.gam = into;
+        }
+        if (r == 0 && tid < 2 * C) {
+            const float n = p.normalize ? rsqrtf(row_square<L::kKeyPitch>(base + (tid < C ? L::kK : L::kQ), tid % C) + kUnitEps) : 1.0f;
+            reinterpret_cast<float*>(&sm.lengths[tid % C])[tid / C] = tid < C ? n : n * q_scale;
         }
         __syncthreads();
         // the states' part
-        const Factors f0 = sm.factors[row0], f1 = sm.factors[row0 + 8];
+        const float gam = sm.gam, into0 = sm.into[row0], into1 = sm.into[row0 + 8], out0 = sm.out_of[row0], out1 = sm.out_of[row0 + 8];
         const float2 l0 = sm.lengths[row0], l1 = sm.lengths[row0 + 8];
-        float front[2] = {}, behind[2] = {};
+        float front_q[2] = {}, front_k[2] = {}, behind[2] = {};
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            if (64 * half + 8 * i >= p.K) break;
             float so[2][4] = {}, sz[2][4] = {}, su[2][4] = {};
 #pragma unroll
             for (int s = 0; s < VP / 16; ++s) {
                 uint32_t oa[4], za[4], ua[4], sb[4], db[4];
-                ldsm(oa, rows_a<L::kPitch>(base + L::kDo, 16 * w, 2 * s));
-                ldsm(za, rows_a<L::kPitch>(base + L::kZ, 16 * w, 2 * s));
-                ldsm(ua, rows_a<L::kPitch>(base + L::kU, 16 * w, 2 * s));
-                ldsm(sb, rows_k<L::kPitch>(base + L::kS, 64 * half + 8 * i, 2 * s));
-                ldsm(db, rows_k<L::kPitch>(base + L::kDs, 64 * half + 8 * i, 2 * s));
+                ldsm(oa, L::kDo + own + lanes.across[s]);
+                ldsm(za, L::kZ + own + lanes.across[s]);
+                ldsm(ua, L::kU + own + lanes.across[s]);
+                ldsm(sb, L::kS + feature_rows + 8 * i * L::kPitch + lanes.down[s]);
+                ldsm(db, L::kDs + feature_rows + 8 * i * L::kPitch + lanes.down[s]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mma(so[e], oa, sb[2 * e], sb[2 * e + 1]);
@@ -357,31 +356,36 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
                     mma(su[e], ua, db[2 * e], db[2 * e + 1]);
                 }
             }
+            if (gam == 0.0f) {  // a state that a reset cuts off is left out, whatever it holds
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        if ((x < 2 ? into0 : into1) == 0.0f) so[e][x] = sz[e][x] = 0.0f;
+                        if ((x < 2 ? out0 : out1) == 0.0f) su[e][x] = 0.0f;
+                    }
+            }
             uint32_t qv[4], kv[4];  // q and k where the sums are
-            ldsm(qv, rows_a<L::kKeyPitch>(base + L::kQ, 16 * w, 8 * half + i));
-            ldsm(kv, rows_a<L::kKeyPitch>(base + L::kK, 16 * w, 8 * half + i));
+            ldsm(qv, L::kQ + own_key + half_key + key_lanes.across[i / 2]);
+            ldsm(kv, L::kK + own_key + half_key + key_lanes.across[i / 2]);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const Factors& f = x < 2 ? f0 : f1;
                     const uint32_t qp = qv[2 * e + x / 2], kp = kv[2 * e + x / 2];
                     const float q = x % 2 ? ptx::bf16_hi(qp) : ptx::bf16_lo(qp), k = x % 2 ? ptx::bf16_hi(kp) : ptx::bf16_lo(kp);
-                    // a state that a reset cuts off is left out, whatever it holds
-                    const float o = f.k == 0.0f ? 0.0f : f.k * so[e][x], z = f.k == 0.0f ? 0.0f : f.k * sz[e][x];
-                    const float u = f.s == 0.0f ? 0.0f : f.s * su[e][x];
-                    const float2& l = x < 2 ? l0 : l1;
-                    dq[i + e][x] += o;
-                    dk[i + e][x] += u - z;
-                    front[x / 2] += q * l.y * o - k * l.x * z;
-                    behind[x / 2] += k * l.x * u;
+                    const float into = x < 2 ? into0 : into1, out_of = x < 2 ? out0 : out1;
+                    dq[i + e][x] = fmaf(into, so[e][x], dq[i + e][x]);
+                    dk[i + e][x] = fmaf(out_of, su[e][x], fmaf(-into, sz[e][x], dk[i + e][x]));
+                    front_q[x / 2] = fmaf(q, so[e][x], front_q[x / 2]);
+                    front_k[x / 2] = fmaf(k, sz[e][x], front_k[x / 2]);
+                    behind[x / 2] = fmaf(k, su[e][x], behind[x / 2]);
                 }
         }
         float both = 0.0f;
-        if (sm.gam != 0.0f) {
-            for (int i = tid; i < KP * (VP / 8); i += blockDim.x) {
-                const uint32_t at_i = i * 16;  // the same place of both tiles
-                const uint4 a = load16(base + L::kS + at_i), d = load16(base + L::kDs + at_i);
+        if (gam != 0.0f) {
+            for (int i = tid; i < KP * (VP / 8); i += kThreads) {  // the same places of both tiles
+                const uint4 a = load16(base + L::kS + 16 * i), d = load16(base + L::kDs + 16 * i);
                 const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -392,28 +396,30 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
         if (lane == 0) sm.both[tid / 32] = both;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+            const float2& l = x ? l1 : l0;
+            float front = (x ? into1 : into0) * (l.y * front_q[x] - l.x * front_k[x]), back = (x ? out1 : out0) * l.x * behind[x];
 #pragma unroll
             for (int o = 1; o < 4; o *= 2) {
-                front[x] += __shfl_xor_sync(0xffffffffu, front[x], o);
-                behind[x] += __shfl_xor_sync(0xffffffffu, behind[x], o);
+                front += __shfl_xor_sync(0xffffffffu, front, o);
+                back += __shfl_xor_sync(0xffffffffu, back, o);
             }
-            if (lane % 4 == 0) sm.front[half][row0 + 8 * x] = front[x], sm.behind[half][row0 + 8 * x] = behind[x];
+            if (lane % 4 == 0) sm.front[half][row0 + 8 * x] = front, sm.behind[half][row0 + 8 * x] = back;
         }
         __syncthreads();  // the states have been read: M1 and M2 go there
         // rows of the warp against the tokens up to them
+        const Token i0 = sm.tab[row0], i1 = sm.tab[row0 + 8];
         float rows[2] = {};
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             if (n >= w && half == 0 && lane < 16) sm.columns[w][16 * n + lane] = 0.0f;
             if (n > w) continue;
-            float pairs[2][4];
-            float qk[2][4] = {}, kk[2][4] = {}, ou[2][4] = {}, zu[2][4] = {};
+            float qk[2][4] = {}, kk[2][4] = {}, ou[2][4] = {}, zu[2][4] = {}, pairs[2][4];
 #pragma unroll
             for (int s = 0; s < KP / 16; ++s) {
                 uint32_t qa[4], ka[4], kb[4];
-                ldsm(qa, rows_a<L::kKeyPitch>(base + L::kQ, 16 * w, 2 * s));
-                ldsm(ka, rows_a<L::kKeyPitch>(base + L::kK, 16 * w, 2 * s));
-                ldsm(kb, rows_k<L::kKeyPitch>(base + L::kK, 16 * n, 2 * s));
+                ldsm(qa, L::kQ + own_key + key_lanes.across[s]);
+                ldsm(ka, L::kK + own_key + key_lanes.across[s]);
+                ldsm(kb, L::kK + 16 * n * L::kKeyPitch + key_lanes.down[s]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mma(qk[e], qa, kb[2 * e], kb[2 * e + 1]);
@@ -423,62 +429,69 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
 #pragma unroll
             for (int s = 0; s < VP / 16; ++s) {
                 uint32_t oa[4], za[4], ub[4];
-                ldsm(oa, rows_a<L::kPitch>(base + L::kDo, 16 * w, 2 * s));
-                ldsm(za, rows_a<L::kPitch>(base + L::kZ, 16 * w, 2 * s));
-                ldsm(ub, rows_k<L::kPitch>(base + L::kU, 16 * n, 2 * s));
+                ldsm(oa, L::kDo + own + lanes.across[s]);
+                ldsm(za, L::kZ + own + lanes.across[s]);
+                ldsm(ub, L::kU + 16 * n * L::kPitch + lanes.down[s]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mma(ou[e], oa, ub[2 * e], ub[2 * e + 1]);
                     mma(zu[e], za, ub[2 * e], ub[2 * e + 1]);
                 }
             }
-            const Token i0 = sm.tab[row0], i1 = sm.tab[row0 + 8];
-            long long far = 0;
-            for (int m = n + 1; m < w; ++m) far += sm.tab[16 * m + 15].sum;
-            const float apart = decay(far), in0 = apart * i0.in, in1 = apart * i1.in;
+            float in0 = 1.0f, in1 = 1.0f;
+            if (n < w) {
+                long long far = 0;
+                for (int m = n + 1; m < w; ++m) far += sm.tab[16 * m + 15].sum;
+                const float apart = decay(far);
+                in0 = apart * i0.in, in1 = apart * i1.in;
+            }
             uint32_t a1[4], a2[4], m1[4], m2[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int j = 16 * n + 8 * e + 2 * (lane % 4);
                 const Token j0 = sm.tab[j], j1 = sm.tab[j + 1];
                 const float n0 = sm.lengths[j].x, n1 = sm.lengths[j + 1].x;
-                float d[4], sum[2] = {};
+                float d[4];
                 if (n < w) {
                     d[0] = in0 * j0.out, d[1] = in0 * j1.out, d[2] = in1 * j0.out, d[3] = in1 * j1.out;
                 } else {
                     d[0] = decay(i0.sum - j0.sum), d[1] = decay(i0.sum - j1.sum);
                     d[2] = decay(i1.sum - j0.sum), d[3] = decay(i1.sum - j1.sum);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int i = row0 + 8 * (x / 2), jj = j + x % 2;
+                        if (i == jj && half == 0 && i < n_tokens)
+                            static_cast<__nv_bfloat16*>(p.db)[(b * p.T + t0 + i) * p.H + h] = __float2bfloat16_rn(zu[e][x] * sm.beta_rest[i]);
+                        if (jj > i) ou[e][x] = 0.0f;
+                        if (jj >= i) zu[e][x] = 0.0f, kk[e][x] = 0.0f;
+                        if (jj > i) d[x] = 0.0f;
+                        if (jj >= i) qk[e][x] = 0.0f;
+                    }
                 }
+                float o[4], z[4], oq[4], zk[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const int i = row0 + 8 * (x / 2), jj = j + x % 2;
                     const float2& l = x < 2 ? l0 : l1;
-                    const float nj = x % 2 ? n1 : n0;
-                    if (n == w && i == jj && half == 0 && i < n_tokens)
-                        static_cast<__nv_bfloat16*>(p.db)[(b * p.T + t0 + i) * p.H + h] = __float2bfloat16_rn(zu[e][x] * sm.factors[i].beta);
-                    const float o = jj > i ? 0.0f : d[x] * ou[e][x], z = jj >= i ? 0.0f : d[x] * zu[e][x];
-                    const float pair = jj >= i ? 0.0f : nj * (o * l.y * qk[e][x] - z * l.x * kk[e][x]);
-                    pairs[e][x] = pair;
-                    sum[x % 2] += pair;
-                    ou[e][x] = o;
-                    zu[e][x] = -z;
+                    const float dn = d[x] * (x % 2 ? n1 : n0), dm = d[x];
+                    o[x] = dn * ou[e][x];
+                    z[x] = -dn * zu[e][x];
+                    oq[x] = dm * l.y * ou[e][x];
+                    zk[x] = -dm * l.x * zu[e][x];
+                    pairs[e][x] = l.y * (o[x] * qk[e][x]) + l.x * (z[x] * kk[e][x]);
                 }
-                a1[2 * e] = pack(ou[e][0] * n0, ou[e][1] * n1);
-                a1[2 * e + 1] = pack(ou[e][2] * n0, ou[e][3] * n1);
-                a2[2 * e] = pack(zu[e][0] * n0, zu[e][1] * n1);
-                a2[2 * e + 1] = pack(zu[e][2] * n0, zu[e][3] * n1);
-                m1[2 * e] = pack(ou[e][0] * l0.y, ou[e][1] * l0.y);
-                m1[2 * e + 1] = pack(ou[e][2] * l1.y, ou[e][3] * l1.y);
-                m2[2 * e] = pack(zu[e][0] * l0.x, zu[e][1] * l0.x);
-                m2[2 * e + 1] = pack(zu[e][2] * l1.x, zu[e][3] * l1.x);
+                a1[2 * e] = pack(o[0], o[1]), a1[2 * e + 1] = pack(o[2], o[3]);
+                a2[2 * e] = pack(z[0], z[1]), a2[2 * e + 1] = pack(z[2], z[3]);
+                m1[2 * e] = pack(oq[0], oq[1]), m1[2 * e + 1] = pack(oq[2], oq[3]);
+                m2[2 * e] = pack(zk[0], zk[1]), m2[2 * e + 1] = pack(zk[2], zk[3]);
                 if (n < w) {
                     rows[0] += pairs[e][0] + pairs[e][1];
                     rows[1] += pairs[e][2] + pairs[e][3];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
+                        float s = pairs[e][x] + pairs[e][x + 2];
 #pragma unroll
-                        for (int o = 4; o < 32; o *= 2) sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], o);
-                        if (lane < 4 && half == 0) sm.columns[w][j + x] = sum[x];
+                        for (int o = 4; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+                        if (lane < 4 && half == 0) sm.columns[w][j + x] = s;
                     }
                 }
             }
@@ -504,13 +517,14 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
                 }
             }
             if (half == 0) {
-                stsm(rows_a<L::kSquarePitch>(base + L::kM1, 16 * w, 2 * n), m1[0], m1[1], m1[2], m1[3]);
-                stsm(rows_a<L::kSquarePitch>(base + L::kM2, 16 * w, 2 * n), m2[0], m2[1], m2[2], m2[3]);
+                const uint32_t to = base + unit_at<L::kSquarePitch>(0, 16 * w + lane % 16, 2 * n + lane / 16);
+                stsm(L::kM1 + to, m1[0], m1[1], m1[2], m1[3]);
+                stsm(L::kM2 + to, m2[0], m2[1], m2[2], m2[3]);
             }
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 uint32_t kb[4];
-                ldsm_t(kb, cols_k<L::kKeyPitch>(base + L::kK, 16 * n, 8 * half + i));
+                ldsm_t(kb, L::kK + 16 * n * L::kKeyPitch + half_key + key_lanes.across[i / 2]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mma(dq[i + e], a1, kb[2 * e], kb[2 * e + 1]);
@@ -526,17 +540,19 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
         }
         __syncthreads();
         // the columns of the warp's tokens against those from them on
+        const int lane_row = lane % 8 + 8 * (lane / 16), lane_unit = 2 * w + lane / 8 % 2;  // as Lanes::down
+        const uint32_t transposed = base + lane_row * L::kSquarePitch + ((lane_unit ^ (lane % 8)) << 4);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             if (n < w) continue;
             uint32_t a1[4], a2[4];
-            ldsm_t(a1, cols_a<L::kSquarePitch>(base + L::kM1, 16 * n, 2 * w));
-            ldsm_t(a2, cols_a<L::kSquarePitch>(base + L::kM2, 16 * n, 2 * w));
+            ldsm_t(a1, L::kM1 + 16 * n * L::kSquarePitch + transposed);
+            ldsm_t(a2, L::kM2 + 16 * n * L::kSquarePitch + transposed);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 uint32_t qb[4], kb[4];
-                ldsm_t(qb, cols_k<L::kKeyPitch>(base + L::kQ, 16 * n, 8 * half + i));
-                ldsm_t(kb, cols_k<L::kKeyPitch>(base + L::kK, 16 * n, 8 * half + i));
+                ldsm_t(qb, L::kQ + 16 * n * L::kKeyPitch + half_key + key_lanes.across[i / 2]);
+                ldsm_t(kb, L::kK + 16 * n * L::kKeyPitch + half_key + key_lanes.across[i / 2]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mma(dk[i + e], a1, qb[2 * e], qb[2 * e + 1]);
@@ -569,7 +585,7 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
             const float across = group == 1 ? b20 + b30 : group == 2 ? b30 + b31 : 0.0f;
             float s = 0.0f;
             for (int i = 0; i < KP / 16; ++i) s += sm.both[i];
-            s = sm.gam == 0.0f ? across : fmaf(sm.gam, s, across);
+            s = gam == 0.0f ? across : fmaf(gam, s, across);
             float from = f[0] + f[1], before = o[0] + o[1], rows_from = rows_of[0] + rows_of[1], columns_to = columns_of[0] + columns_of[1];
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
@@ -593,7 +609,7 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
-                if (t < n_tokens) static_cast<__nv_bfloat16*>(p.df)[(b * p.T + t0 + t) * p.H + h] = __float2bfloat16_rn(da[i] * sm.gate[t]);
+                if (t < n_tokens) static_cast<__nv_bfloat16*>(p.df)[(b * p.T + t0 + t) * p.H + h] = __float2bfloat16_rn(da[i] * sm.rest[t]);
             }
         }
     }
@@ -604,8 +620,8 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         uint32_t qv[4], kv[4];
-        ldsm(qv, rows_a<L::kKeyPitch>(base + L::kQ, 16 * w, 8 * half + i));
-        ldsm(kv, rows_a<L::kKeyPitch>(base + L::kK, 16 * w, 8 * half + i));
+        ldsm(qv, L::kQ + own_key + half_key + key_lanes.across[i / 2]);
+        ldsm(kv, L::kK + own_key + half_key + key_lanes.across[i / 2]);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -633,7 +649,7 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         uint32_t qv[4], kv[4];
-        const uint32_t qat = rows_a<L::kKeyPitch>(base + L::kQ, 16 * w, 8 * half + i), kat = qat - L::kQ + L::kK;
+        const uint32_t qat = L::kQ + own_key + half_key + key_lanes.across[i / 2], kat = qat - L::kQ + L::kK;
         ldsm(qv, qat);
         ldsm(kv, kat);
 #pragma unroll
@@ -665,14 +681,15 @@ int launch(const Delta& p, cudaStream_t stream) {
     const auto chain = units ? delta_bwd_chain<KP, NW, true> : delta_bwd_chain<KP, NW, false>;
     using T = Tiles<KP, 16 * NW>;
     constexpr int kBytes = T::kSmall + (int)sizeof(Small);
-    static std::atomic<uint64_t> done[3];
-    if (allow_smem(chain, L::kBytes, done[units]) != cudaSuccess || allow_smem(delta_bwd_chunks<KP, 16 * NW>, kBytes, done[2]) != cudaSuccess)
+    const auto of_chunks = units ? delta_bwd_chunks<KP, 16 * NW, true> : delta_bwd_chunks<KP, 16 * NW, false>;
+    static std::atomic<uint64_t> done[2], done_chunks[2];
+    if (allow_smem(chain, L::kBytes, done[units]) != cudaSuccess || allow_smem(of_chunks, kBytes, done_chunks[units]) != cudaSuccess)
         return SSDC_ERR_CUDA;
     const int64_t ctas = (p.T + C - 1) / C * p.B * p.G;
     if (ctas > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
     const int parts = (p.V + 16 * NW - 1) / (16 * NW);
     chain<<<p.B * p.H * parts, kPrep + 32 * NW, L::kBytes, stream>>>(p);
-    delta_bwd_chunks<KP, 16 * NW><<<(unsigned)ctas, 2 * KP, kBytes, stream>>>(p, whole_units(p.q), whole_units(p.k), whole_units(p.d_o));
+    of_chunks<<<(unsigned)ctas, 2 * KP, kBytes, stream>>>(p);
     return 2;
 }
 

@@ -27,6 +27,8 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
     const int columns = min(16, p.V - col0);
     const int64_t chunks = (p.T + C - 1) / C, seq = (int64_t)b * p.H + h;
     const uint32_t strips = base + L::kStripOff + w * 2 * L::kStrip;
+    const Lanes<L::kKeyPitch> key_lanes(base);
+    const Lanes<L::kPitch> lanes(base);
     const int fetch_u = lane % 2, fetch_r = lane / 2;
     const bool has_unit = 8 * fetch_u < columns;
     const __nv_bfloat16* v_row = bf16(p.v.p) + b * p.v.b + h * p.v.h + fetch_r * p.v.t + col0 + (has_unit ? 8 * fetch_u : 0);
@@ -71,7 +73,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
         if (c + 1 < chunks) fetch_v(c + 1);
         else ptx::cp_async_commit();
         bar_sync(kBarKeys + turn, all);
-        const uint32_t keys = base + (int)(c % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
+        const uint32_t keys = (int)(c % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
         float X[8][4] = {}, O[8][4] = {};
 #pragma unroll
         for (int s = 0; s < KP / 16; ++s) {
@@ -80,8 +82,8 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 uint32_t kb[4], qb[4];
-                ldsm(kb, rows_k<L::kKeyPitch>(keys, 16 * n, 2 * s));
-                ldsm(qb, rows_k<L::kKeyPitch>(queries, 16 * n, 2 * s));
+                ldsm(kb, keys + 16 * n * L::kKeyPitch + key_lanes.down[s]);
+                ldsm(qb, queries + 16 * n * L::kKeyPitch + key_lanes.down[s]);
                 mma(X[2 * n], a.hi, kb[0], kb[1]);
                 mma(X[2 * n + 1], a.hi, kb[2], kb[3]);
                 mma(O[2 * n], a.hi, qb[0], qb[1]);
@@ -94,7 +96,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
         __syncwarp();
         bar_sync(kBarFull, all);
         const Factors* factors = reinterpret_cast<const Factors*>(smem + L::kFactorsOff) + turn * C;
-        const uint32_t hi = base + L::kLOff, lo = hi + L::kSquare, ps = lo + L::kSquare;
+        constexpr uint32_t hi = L::kLOff, lo = hi + L::kSquare, ps = lo + L::kSquare;
         const float gam = reinterpret_cast<const float*>(smem + L::kGamOff)[turn];
         // A chunk that cuts the state off (a reset in it, as a rule): what a token does not take from it is zero,
         // whatever the state holds; an infinity or a NaN of one document stays out of the next.
@@ -126,8 +128,8 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
             Split a;
             uint32_t bh[4], bl[4];
             a.set(X[2 * r], X[2 * r + 1]);
-            ldsm_t(bh, cols_k<L::kPitch>(hi, 16 * r, 2 * r));
-            ldsm_t(bl, cols_k<L::kPitch>(lo, 16 * r, 2 * r));
+            ldsm_t(bh, hi + 16 * r * L::kPitch + lanes.across[r]);
+            ldsm_t(bl, lo + 16 * r * L::kPitch + lanes.across[r]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 X[2 * r + e][0] = X[2 * r + e][1] = X[2 * r + e][2] = X[2 * r + e][3] = 0.0f;
@@ -138,8 +140,8 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
             a.set(X[2 * r], X[2 * r + 1]);  // U of this block
 #pragma unroll
             for (int n = r + 1; n < 4; ++n) {
-                ldsm(bh, rows_k<L::kPitch>(hi, 16 * n, 2 * r));
-                ldsm(bl, rows_k<L::kPitch>(lo, 16 * n, 2 * r));
+                ldsm(bh, hi + 16 * n * L::kPitch + lanes.down[r]);
+                ldsm(bl, lo + 16 * n * L::kPitch + lanes.down[r]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mma(X[2 * n + e], a.hi, bh[2 * e], bh[2 * e + 1]);
@@ -149,7 +151,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
             }
 #pragma unroll
             for (int n = r; n < 4; ++n) {
-                ldsm(bh, rows_k<L::kPitch>(ps, 16 * n, 2 * r));
+                ldsm(bh, ps + 16 * n * L::kPitch + lanes.down[r]);
                 mma(O[2 * n], a.hi, bh[0], bh[1]);
                 mma(O[2 * n + 1], a.hi, bh[2], bh[3]);
                 mma(O[2 * n], a.lo, bh[0], bh[1]);
@@ -193,7 +195,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
 #pragma unroll
             for (int i = 0; i < KT; i += 2) {
                 uint32_t kb[4];
-                ldsm_t(kb, cols_k<L::kKeyPitch>(keys, 16 * s, i));
+                ldsm_t(kb, keys + 16 * s * L::kKeyPitch + key_lanes.across[i / 2]);
                 mma(S[i], a.hi, kb[0], kb[1]);
                 mma(S[i + 1], a.hi, kb[2], kb[3]);
                 mma(S[i], a.lo, kb[0], kb[1]);

@@ -94,19 +94,25 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
         // log2 of sigmoid(f), not below -256
         const float s = log1pf(e), l = v >= 0.0f ? -s : v - s, lg = l < -177.0f ? -256.0f : l * kLog2e;
         if (lane >= 16) betas_of[turn * C + gate_r] = there ? (v >= 0.0f ? 1.0f : e) / (1.0f + e) : 0.0f;
-        scan_group(!there ? 0.0f : mark != 0 ? -256.0f : lg, tabs + turn * C + 16 * warp);
+        scan_group<false>(!there ? 0.0f : mark != 0 ? -256.0f : lg, tabs + turn * C + 16 * warp);
         ptx::cp_async_wait<0>();
     };
 
     // this warp's blocks: rows bi, columns bj
     const int bi[3] = {warp, warp < 2 ? warp + 1 : warp, 3}, bj[3] = {warp, warp < 2 ? 0 : warp - 1, warp};
 
+    const Lanes<L::kKeyPitch> key_lanes(base);
+    auto across = [&](int i) {  // Lanes::across of the squares, for an i that is not known beforehand
+        const int m = lane / 8, r = lane % 8;
+        return base + (8 * (m % 2) + r) * L::kPitch + (((2 * i + m / 2) ^ r) << 4);
+    };
+
     fetch_gates(0);
     fetch_keys(0);
     tokens(0);
     for (int64_t n = 0; n < chunks; ++n) {
         const int turn = (int)(n & 1);
-        const uint32_t keys = base + (int)(n % L::kStages) * L::kStage;
+        const uint32_t keys = (int)(n % L::kStages) * L::kStage;  // from the start of shared memory, as the lanes' offsets are
         const Token* tab = tabs + turn * C;
         const float* betas = betas_of + turn * C;
         if (n >= 2) bar_sync(kBarStage + turn, all);  // the chunk before the last is through with its stage
@@ -127,9 +133,9 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
 #pragma unroll
             for (int s = 0; s < KP / 16; ++s) {
                 uint32_t kb[4], ka[4], qa[4];
-                if (slot > 0) ldsm(kb, rows_k<L::kKeyPitch>(kb_at, 0, 2 * s));
-                ldsm(ka, rows_a<L::kKeyPitch>(ka_at, 0, 2 * s));
-                ldsm(qa, rows_a<L::kKeyPitch>(ka_at + L::kKeyTile, 0, 2 * s));
+                if (slot > 0) ldsm(kb, kb_at + key_lanes.down[s]);
+                ldsm(ka, ka_at + key_lanes.across[s]);
+                ldsm(qa, ka_at + L::kKeyTile + key_lanes.across[s]);
                 // an A operand's registers are a B operand's of the same rows, in another order
                 if (slot == 0) kb[0] = ka[0], kb[1] = ka[2], kb[2] = ka[1], kb[3] = ka[3];
 #pragma unroll
@@ -229,11 +235,11 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
             }
         }
         if (n >= 1) bar_sync(kBarFree, all);  // the last chunk is through with its blocks
-        const uint32_t hi = base + L::kLOff, lo = hi + L::kSquare, ps = lo + L::kSquare;
+        constexpr uint32_t hi = L::kLOff, lo = hi + L::kSquare, ps = lo + L::kSquare;
 #pragma unroll
         for (int slot = 0; slot < 3; ++slot) {
             if (slot == 2 && warp >= 2) break;
-            const uint32_t at = rows_a<L::kPitch>(0, 16 * bi[slot], 2 * bj[slot]);
+            const uint32_t at = 16 * bi[slot] * L::kPitch + across(bj[slot]);
             stsm(ps + at, P[slot][0][0], P[slot][0][1], P[slot][1][0], P[slot][1][1]);
             if constexpr (kBack) stsm(ps + L::kSquare + at, P2[slot][0][0], P2[slot][0][1], P2[slot][1][0], P2[slot][1][1]);
             if (slot > 0) {
@@ -244,7 +250,7 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u)  // the inverse lies transposed: a lane has a row of it
-            store16(unit_at<L::kPitch>(lane < 16 ? hi : lo, 16 * warp + lane % 16, 2 * warp + u),
+            store16(base + unit_at<L::kPitch>(lane < 16 ? hi : lo, 16 * warp + lane % 16, 2 * warp + u),
                     make_uint4(T[4 * u], T[4 * u + 1], T[4 * u + 2], T[4 * u + 3]));
         bar_arrive(kBarFull, all);
         if (n + 1 < chunks) tokens(n + 1);
