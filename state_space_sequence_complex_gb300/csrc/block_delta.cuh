@@ -202,7 +202,7 @@ __device__ __forceinline__ float row_square(uint32_t tile, int r) {
     return s;
 }
 
-// The inverse of I + N for a strictly lower triangular 16 x 16 N, whose column j is at NT + 20 j in shared
+// The inverse of I + N for a strictly lower triangular 16 x 16 N, whose column j is at NT + 16 j in shared
 // memory: lane l has column l % 16 of it in t, by forward substitution, which is as exact as N allows also
 // where powers of N are large. A finished row is taken from all later ones at once: 15 independent steps.
 __device__ __forceinline__ void invert16(const float* NT, float* t) {
@@ -213,7 +213,7 @@ __device__ __forceinline__ void invert16(const float* NT, float* t) {
     for (int j = 0; j < 15; ++j) {
 #pragma unroll
         for (int i = (j + 1) / 4 * 4; i < 16; i += 4) {
-            const float4 n = *reinterpret_cast<const float4*>(NT + 20 * j + i);
+            const float4 n = *reinterpret_cast<const float4*>(NT + 16 * j + i);
             const float e[4] = {n.x, n.y, n.z, n.w};
 #pragma unroll
             for (int r = 0; r < 4; ++r)

@@ -23,9 +23,9 @@ namespace block {
 namespace delta {
 namespace {
 
-template <int KP, int NW, bool kUnitRows>
+template <int KP, int NW, int kGroups, bool kUnitRows>
 __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int h, int w, int col0, int column_threads) {
-    using L = Layout<KP, NW, true>;
+    using L = Layout<KP, NW, true, kGroups>;
     constexpr int KT = KP / 8;
     const uint32_t base = ptx::smem_addr(smem);
     const int lane = threadIdx.x % 32, all = kPrep + column_threads;
@@ -60,7 +60,7 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         }
     for (int64_t n = 0; n < chunks; ++n) {
         const int64_t c = chunks - 1 - n;
-        const int turn = (int)(n & 1);
+        const int turn = (int)(n & 1), set = (int)(n & (L::kSets - 1)), half = (int)(n % kGroups);
         const uint32_t mine = strips + turn * L::kStrip, next = strips + (turn ^ 1) * L::kStrip;
 #pragma unroll
         for (int i = 0; i < KT; i += 2) {
@@ -74,7 +74,7 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         }
         if (n + 1 < chunks) fetch_do(n + 1);
         else ptx::cp_async_commit();
-        bar_sync(kBarKeys + turn, all);
+        bar_sync(kBarKeys + (int)(n & 3), all);
         const uint32_t keys = (int)(n % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
         float X[8][4] = {};
 #pragma unroll
@@ -93,10 +93,10 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         }
         ptx::cp_async_wait<1>();
         __syncwarp();
-        bar_sync(kBarFull, all);
-        const Factors* factors = reinterpret_cast<const Factors*>(smem + L::kFactorsOff) + turn * C;
-        constexpr uint32_t hi = L::kLOff, lo = hi + L::kSquare, ps = lo + L::kSquare, ps2 = ps + L::kSquare;
-        const float gam = reinterpret_cast<const float*>(smem + L::kGamOff)[turn];
+        bar_sync(kBarFull + half, all);
+        const Factors* factors = reinterpret_cast<const Factors*>(smem + L::kFactorsOff) + set * C;
+        const uint32_t hi = L::kLOff + half * L::kBlocks, lo = hi + L::kSquare, ps = lo + L::kSquare, ps2 = ps + L::kSquare;
+        const float gam = reinterpret_cast<const float*>(smem + L::kGamOff)[set];
 #pragma unroll
         for (int m = 0; m < 8; ++m)
 #pragma unroll
@@ -124,20 +124,30 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
             }
         }
 #pragma unroll
+        for (int i = 0; i < KT; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[i][e] *= gam;
+            if (gam == 0.0f) S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.0f;
+        }
+        // Block by block from the last: what a block adds to dS keeps the instructions coming while the one before it,
+        // which waits for each of its products, is solved.
+#pragma unroll
         for (int r = 3; r >= 0; --r) {
             Split a;
             uint32_t bh[4], bl[4];
-            a.set(X[2 * r], X[2 * r + 1]);
+            float *x0 = X[2 * r], *x1 = X[2 * r + 1];
+            a.set(x0, x1);
             ldsm(bh, hi + 16 * r * L::kPitch + lanes.down[r]);
             ldsm(bl, lo + 16 * r * L::kPitch + lanes.down[r]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                X[2 * r + e][0] = X[2 * r + e][1] = X[2 * r + e][2] = X[2 * r + e][3] = 0.0f;
-                mma(X[2 * r + e], a.lo, bh[2 * e], bh[2 * e + 1]);
-                mma(X[2 * r + e], a.hi, bl[2 * e], bl[2 * e + 1]);
-                mma(X[2 * r + e], a.hi, bh[2 * e], bh[2 * e + 1]);
+                float* x = X[2 * r + e];
+                x[0] = x[1] = x[2] = x[3] = 0.0f;
+                mma(x, a.lo, bh[2 * e], bh[2 * e + 1]);
+                mma(x, a.hi, bl[2 * e], bl[2 * e + 1]);
+                mma(x, a.hi, bh[2 * e], bh[2 * e + 1]);
             }
-            a.set(X[2 * r], X[2 * r + 1]);  // Z of this block
+            a.set(x0, x1);  // Z of this block
 #pragma unroll
             for (int j = 0; j < r; ++j) {
                 ldsm_t(bh, hi + 16 * r * L::kPitch + lanes.across[j]);
@@ -149,45 +159,29 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
                     mma(X[2 * j + e], a.hi, bl[2 * e], bl[2 * e + 1]);
                 }
             }
-        }
-        if (n + 1 < chunks) bar_arrive(kBarFree, all);
-#pragma unroll
-        for (int m = 0; m < 8; m += 2)
-            stsm_t(strip_rows(mine, 8 * m), pack(X[m][0], X[m][1]), pack(X[m][2], X[m][3]), pack(X[m + 1][0], X[m + 1][1]),
-                   pack(X[m + 1][2], X[m + 1][3]));
-        const int64_t left = p.T - c * C;
-        put_strip(mine, static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + c * C) * p.H + h) * p.V + col0, (int64_t)p.H * p.V,
-                  left < C ? (int)left : C, columns);
-#pragma unroll
-        for (int i = 0; i < KT; ++i) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[i][e] *= gam;
-            if (gam == 0.0f) S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.0f;
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
+            stsm_t(strip_rows(mine, 16 * r), a.hi[0], a.hi[1], a.hi[2], a.hi[3]);
             float g[2][4];  // do of 16 tokens times Gam rq
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int j = 16 * s + 8 * e + 2 * (lane % 4);
-                const Factors f0 = factors[j], f1 = factors[j + 1];
-                g[e][0] = ptx::bf16_lo(d_o[s][2 * e]) * f0.q; g[e][1] = ptx::bf16_hi(d_o[s][2 * e]) * f1.q;
-                g[e][2] = ptx::bf16_lo(d_o[s][2 * e + 1]) * f0.q; g[e][3] = ptx::bf16_hi(d_o[s][2 * e + 1]) * f1.q;
-                float* x = X[2 * s + e];
-                x[0] *= -f0.k; x[1] *= -f1.k; x[2] *= -f0.k; x[3] *= -f1.k;
+                const int j = 16 * r + 8 * e + 2 * (lane % 4);
+                const float2 f0 = *reinterpret_cast<const float2*>(&factors[j]), f1 = *reinterpret_cast<const float2*>(&factors[j + 1]);
+                g[e][0] = ptx::bf16_lo(d_o[r][2 * e]) * f0.y; g[e][1] = ptx::bf16_hi(d_o[r][2 * e]) * f1.y;
+                g[e][2] = ptx::bf16_lo(d_o[r][2 * e + 1]) * f0.y; g[e][3] = ptx::bf16_hi(d_o[r][2 * e + 1]) * f1.y;
+                float* x = X[2 * r + e];
+                x[0] *= -f0.x; x[1] *= -f1.x; x[2] *= -f0.x; x[3] *= -f1.x;
                 if (gam == 0.0f) {
-                    if (f0.k == 0.0f) g[e][0] = g[e][2] = x[0] = x[2] = 0.0f;
-                    if (f1.k == 0.0f) g[e][1] = g[e][3] = x[1] = x[3] = 0.0f;
+                    if (f0.x == 0.0f) g[e][0] = g[e][2] = x[0] = x[2] = 0.0f;
+                    if (f1.x == 0.0f) g[e][1] = g[e][3] = x[1] = x[3] = 0.0f;
                 }
             }
-            Split a, z;
+            Split z;
             a.set(g[0], g[1]);
-            z.set(X[2 * s], X[2 * s + 1]);
+            z.set(x0, x1);
 #pragma unroll
             for (int i = 0; i < KT; i += 2) {
                 uint32_t qb[4], kb[4];
-                ldsm_t(qb, queries + 16 * s * L::kKeyPitch + key_lanes.across[i / 2]);
-                ldsm_t(kb, keys + 16 * s * L::kKeyPitch + key_lanes.across[i / 2]);
+                ldsm_t(qb, queries + 16 * r * L::kKeyPitch + key_lanes.across[i / 2]);
+                ldsm_t(kb, keys + 16 * r * L::kKeyPitch + key_lanes.across[i / 2]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mma(S[i + e], a.hi, qb[2 * e], qb[2 * e + 1]);
@@ -197,7 +191,11 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
                 }
             }
         }
-        if (n + 2 < chunks) bar_arrive(kBarStage + turn, all);
+        if (n + kGroups < chunks) bar_arrive(kBarFree + half, all);
+        if (n + 2 * kGroups < chunks) bar_arrive(kBarStage + (int)(n & 3), all);
+        const int64_t left = p.T - c * C;
+        put_strip(mine, static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + c * C) * p.H + h) * p.V + col0, (int64_t)p.H * p.V,
+                  left < C ? (int)left : C, columns);
     }
     if (p.dh0 != nullptr) {
 #pragma unroll
@@ -210,20 +208,19 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
     }
 }
 
-template <int KP, int NW, bool kUnitRows>
-__global__ void __launch_bounds__(kPrep + 32 * NW, KP == 64 && NW == 4 ? 2 : 1) delta_bwd_chain(const __grid_constant__ Delta p) {
+template <int KP, int NW, int kGroups, bool kUnitRows>
+__global__ void __launch_bounds__(kGroups * kPrep + 32 * NW, KP == 64 && NW == 4 && kGroups == 1 ? 2 : 1) delta_bwd_chain(const __grid_constant__ Delta p) {
     extern __shared__ __align__(128) char smem[];
     const int parts = (p.V + 16 * NW - 1) / (16 * NW), item = blockIdx.x / parts, col0 = blockIdx.x % parts * 16 * NW;
     const int b = item / p.H, h = item % p.H;
     const int warps = min(NW, (p.V - col0 + 15) / 16);
-    constexpr bool kSplit = KP == 64 || NW == 8;
-    if (threadIdx.x < kPrep) {
-        if constexpr (kSplit) ptx::regs_dec<NW == 8 ? 104 : 96>();
-        prepare_chunks<KP, NW, true, kUnitRows>(p, smem, b, h, 32 * warps);
+    if (threadIdx.x < kGroups * kPrep) {
+        Registers<KP, NW, kGroups>::prepare();
+        prepare_chunks<KP, NW, true, kGroups, kUnitRows>(p, smem, b, h, 32 * warps);
     } else {
-        if constexpr (kSplit) ptx::regs_inc<NW == 8 ? 200 : 160>();
-        const int w = threadIdx.x / 32 - kPrep / 32;
-        if (w < warps) walk_back<KP, NW, kUnitRows>(p, smem, b, h, w, col0 + 16 * w, 32 * warps);
+        Registers<KP, NW, kGroups>::walk();
+        const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
+        if (w < warps) walk_back<KP, NW, kGroups, kUnitRows>(p, smem, b, h, w, col0 + 16 * w, 32 * warps);
     }
 }
 
@@ -674,23 +671,27 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
     }
 }
 
-template <int KP, int NW>
-int launch(const Delta& p, cudaStream_t stream) {
-    using L = Layout<KP, NW, true>;
+template <int KP, int NW, int kGroups>
+int launch_chain(const Delta& p, cudaStream_t stream) {
+    using L = Layout<KP, NW, true, kGroups>;
     const bool units = whole_units(p.k) && whole_units(p.q) && whole_units(p.d_o);
-    const auto chain = units ? delta_bwd_chain<KP, NW, true> : delta_bwd_chain<KP, NW, false>;
-    using T = Tiles<KP, 16 * NW>;
-    constexpr int kBytes = T::kSmall + (int)sizeof(Small);
-    const auto of_chunks = units ? delta_bwd_chunks<KP, 16 * NW, true> : delta_bwd_chunks<KP, 16 * NW, false>;
-    static std::atomic<uint64_t> done[2], done_chunks[2];
-    if (allow_smem(chain, L::kBytes, done[units]) != cudaSuccess || allow_smem(of_chunks, kBytes, done_chunks[units]) != cudaSuccess)
-        return SSDC_ERR_CUDA;
-    const int64_t ctas = (p.T + C - 1) / C * p.B * p.G;
-    if (ctas > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
+    const auto kernel = units ? delta_bwd_chain<KP, NW, kGroups, true> : delta_bwd_chain<KP, NW, kGroups, false>;
+    static std::atomic<uint64_t> done[2];
+    if (allow_smem(kernel, L::kBytes, done[units]) != cudaSuccess) return SSDC_ERR_CUDA;
     const int parts = (p.V + 16 * NW - 1) / (16 * NW);
-    chain<<<p.B * p.H * parts, kPrep + 32 * NW, L::kBytes, stream>>>(p);
-    of_chunks<<<(unsigned)ctas, 2 * KP, kBytes, stream>>>(p);
-    return 2;
+    kernel<<<p.B * p.H * parts, kGroups * kPrep + 32 * NW, L::kBytes, stream>>>(p);
+    return 1;
+}
+
+template <int KP, int VP>
+int launch_chunks(const Delta& p, cudaStream_t stream) {
+    const bool units = whole_units(p.k) && whole_units(p.q) && whole_units(p.d_o);
+    const auto kernel = units ? delta_bwd_chunks<KP, VP, true> : delta_bwd_chunks<KP, VP, false>;
+    constexpr int kBytes = Tiles<KP, VP>::kSmall + (int)sizeof(Small);
+    static std::atomic<uint64_t> done[2];
+    if (allow_smem(kernel, kBytes, done[units]) != cudaSuccess) return SSDC_ERR_CUDA;
+    kernel<<<(unsigned)((p.T + C - 1) / C * p.B * p.G), 2 * KP, kBytes, stream>>>(p);
+    return 1;
 }
 
 }  // namespace
@@ -698,8 +699,15 @@ int launch(const Delta& p, cudaStream_t stream) {
 
 int delta_bwd_launch(const Delta& p, cudaStream_t stream) {
     using namespace delta;
-    if (p.K <= 64) return p.V <= 64 ? launch<64, 4>(p, stream) : launch<64, 8>(p, stream);
-    return p.V <= 64 ? launch<128, 4>(p, stream) : launch<128, 8>(p, stream);
+    if ((p.T + C - 1) / C * p.B * p.G > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
+    int chain, chunks;
+    if (few_states(p)) chain = p.K <= 64 ? launch_chain<64, 4, 2>(p, stream) : launch_chain<128, 4, 2>(p, stream);
+    else if (p.K <= 64) chain = p.V <= 64 ? launch_chain<64, 4, 1>(p, stream) : launch_chain<64, 8, 1>(p, stream);
+    else chain = p.V <= 64 ? launch_chain<128, 4, 1>(p, stream) : launch_chain<128, 8, 1>(p, stream);
+    if (chain < 0) return chain;
+    if (p.K <= 64) chunks = p.V <= 64 ? launch_chunks<64, 64>(p, stream) : launch_chunks<64, 128>(p, stream);
+    else chunks = p.V <= 64 ? launch_chunks<128, 64>(p, stream) : launch_chunks<128, 128>(p, stream);
+    return chunks < 0 ? chunks : chain + chunks;
 }
 
 }  // namespace block

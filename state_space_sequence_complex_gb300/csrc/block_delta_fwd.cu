@@ -18,9 +18,9 @@ namespace block {
 namespace delta {
 namespace {
 
-template <int KP, int NW, bool kUnitRows>
+template <int KP, int NW, int kGroups, bool kUnitRows>
 __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, int w, int col0, int column_threads) {
-    using L = Layout<KP, NW, false>;
+    using L = Layout<KP, NW, false, kGroups>;
     constexpr int KT = KP / 8;  // 8-row tiles of the state
     const uint32_t base = ptx::smem_addr(smem);
     const int lane = threadIdx.x % 32, all = kPrep + column_threads;
@@ -55,7 +55,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
             S[i][e] = p.h0 != nullptr && r < p.K && cl < columns ? p.h0[state + (int64_t)r * p.V + cl] : 0.0f;
         }
     for (int64_t c = 0; c < chunks; ++c) {
-        const int turn = (int)(c & 1);
+        const int turn = (int)(c & 1), set = (int)(c & (L::kSets - 1)), half = (int)(c % kGroups);
         // the strip of the next chunk is free until it is fetched, that of this one when v has been read
         const uint32_t mine = strips + turn * L::kStrip, next = strips + (turn ^ 1) * L::kStrip;
         if (p.states != nullptr) {
@@ -72,7 +72,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
         }
         if (c + 1 < chunks) fetch_v(c + 1);
         else ptx::cp_async_commit();
-        bar_sync(kBarKeys + turn, all);
+        bar_sync(kBarKeys + (int)(c & 3), all);
         const uint32_t keys = (int)(c % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
         float X[8][4] = {}, O[8][4] = {};
 #pragma unroll
@@ -94,10 +94,10 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
         }
         ptx::cp_async_wait<1>();
         __syncwarp();
-        bar_sync(kBarFull, all);
-        const Factors* factors = reinterpret_cast<const Factors*>(smem + L::kFactorsOff) + turn * C;
-        constexpr uint32_t hi = L::kLOff, lo = hi + L::kSquare, ps = lo + L::kSquare;
-        const float gam = reinterpret_cast<const float*>(smem + L::kGamOff)[turn];
+        bar_sync(kBarFull + half, all);
+        const Factors* factors = reinterpret_cast<const Factors*>(smem + L::kFactorsOff) + set * C;
+        const uint32_t hi = L::kLOff + half * L::kBlocks, lo = hi + L::kSquare, ps = lo + L::kSquare;
+        const float gam = reinterpret_cast<const float*>(smem + L::kGamOff)[set];
         // A chunk that cuts the state off (a reset in it, as a rule): what a token does not take from it is zero,
         // whatever the state holds; an infinity or a NaN of one document stays out of the next.
         if (gam == 0.0f) {
@@ -124,20 +124,34 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
             }
         }
 #pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[i][e] *= gam;
+        if (gam == 0.0f) {
+#pragma unroll
+            for (int i = 0; i < KT; ++i) S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.0f;
+        }
+        const int64_t left = p.T - c * C;
+        const int n_tokens = left < C ? (int)left : C;
+        // Block by block: what a block adds to O and S keeps the instructions coming while the next one, which
+        // waits for each of its products, is solved.
+#pragma unroll
         for (int r = 0; r < 4; ++r) {
             Split a;
             uint32_t bh[4], bl[4];
-            a.set(X[2 * r], X[2 * r + 1]);
+            float *x0 = X[2 * r], *x1 = X[2 * r + 1];
+            a.set(x0, x1);
             ldsm_t(bh, hi + 16 * r * L::kPitch + lanes.across[r]);
             ldsm_t(bl, lo + 16 * r * L::kPitch + lanes.across[r]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                X[2 * r + e][0] = X[2 * r + e][1] = X[2 * r + e][2] = X[2 * r + e][3] = 0.0f;
-                mma(X[2 * r + e], a.lo, bh[2 * e], bh[2 * e + 1]);
-                mma(X[2 * r + e], a.hi, bl[2 * e], bl[2 * e + 1]);
-                mma(X[2 * r + e], a.hi, bh[2 * e], bh[2 * e + 1]);
+                float* x = X[2 * r + e];
+                x[0] = x[1] = x[2] = x[3] = 0.0f;
+                mma(x, a.lo, bh[2 * e], bh[2 * e + 1]);
+                mma(x, a.hi, bl[2 * e], bl[2 * e + 1]);
+                mma(x, a.hi, bh[2 * e], bh[2 * e + 1]);
             }
-            a.set(X[2 * r], X[2 * r + 1]);  // U of this block
+            a.set(x0, x1);  // U of this block
 #pragma unroll
             for (int n = r + 1; n < 4; ++n) {
                 ldsm(bh, hi + 16 * n * L::kPitch + lanes.down[r]);
@@ -149,6 +163,8 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
                     mma(X[2 * n + e], a.hi, bl[2 * e], bl[2 * e + 1]);
                 }
             }
+            if (p.updates != nullptr)
+                stsm_t(strip_rows(mine, 16 * r), a.hi[0], a.hi[1], a.hi[2], a.hi[3]);
 #pragma unroll
             for (int n = r; n < 4; ++n) {
                 ldsm(bh, ps + 16 * n * L::kPitch + lanes.down[r]);
@@ -157,52 +173,33 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
                 mma(O[2 * n], a.lo, bh[0], bh[1]);
                 mma(O[2 * n + 1], a.lo, bh[2], bh[3]);
             }
-        }
-        if (c + 1 < chunks) bar_arrive(kBarFree, all);
-#pragma unroll
-        for (int i = 0; i < KT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[i][e] *= gam;
-        if (gam == 0.0f) {
-#pragma unroll
-            for (int i = 0; i < KT; ++i) S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.0f;
-        }
-        const int64_t left = p.T - c * C;
-        const int n_tokens = left < C ? (int)left : C;
-        if (p.updates != nullptr) {
-#pragma unroll
-            for (int n = 0; n < 8; n += 2)
-                stsm_t(strip_rows(mine, 8 * n), pack(X[n][0], X[n][1]), pack(X[n][2], X[n][3]), pack(X[n + 1][0], X[n + 1][1]),
-                       pack(X[n + 1][2], X[n + 1][3]));
-            put_strip(mine, static_cast<__nv_bfloat16*>(p.updates) + ((b * p.T + c * C) * p.H + h) * p.V + col0, (int64_t)p.H * p.V,
-                      n_tokens, columns);
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int j = 16 * s + 8 * e + 2 * (lane % 4);
+                const int j = 16 * r + 8 * e + 2 * (lane % 4);
                 const float f0 = factors[j].s, f1 = factors[j + 1].s;
-                float* x = X[2 * s + e];
+                float* x = X[2 * r + e];
                 x[0] *= f0; x[1] *= f1; x[2] *= f0; x[3] *= f1;
                 if (gam == 0.0f) {  // what a reset keeps from the next chunk is left out, too
                     if (f0 == 0.0f) x[0] = x[2] = 0.0f;
                     if (f1 == 0.0f) x[1] = x[3] = 0.0f;
                 }
             }
-            Split a;
-            a.set(X[2 * s], X[2 * s + 1]);
+            a.set(x0, x1);
 #pragma unroll
             for (int i = 0; i < KT; i += 2) {
                 uint32_t kb[4];
-                ldsm_t(kb, keys + 16 * s * L::kKeyPitch + key_lanes.across[i / 2]);
+                ldsm_t(kb, keys + 16 * r * L::kKeyPitch + key_lanes.across[i / 2]);
                 mma(S[i], a.hi, kb[0], kb[1]);
                 mma(S[i + 1], a.hi, kb[2], kb[3]);
                 mma(S[i], a.lo, kb[0], kb[1]);
                 mma(S[i + 1], a.lo, kb[2], kb[3]);
             }
         }
-        if (c + 2 < chunks) bar_arrive(kBarStage + turn, all);
+        if (c + kGroups < chunks) bar_arrive(kBarFree + half, all);
+        if (c + 2 * kGroups < chunks) bar_arrive(kBarStage + (int)(c & 3), all);
+        if (p.updates != nullptr)
+            put_strip(mine, static_cast<__nv_bfloat16*>(p.updates) + ((b * p.T + c * C) * p.H + h) * p.V + col0, (int64_t)p.H * p.V,
+                      n_tokens, columns);
 #pragma unroll
         for (int n = 0; n < 8; n += 2)
             stsm_t(strip_rows(mine, 8 * n), pack(O[n][0], O[n][1]), pack(O[n][2], O[n][3]), pack(O[n + 1][0], O[n + 1][1]),
@@ -219,32 +216,31 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
         }
 }
 
-template <int KP, int NW, bool kUnitRows>
-__global__ void __launch_bounds__(kPrep + 32 * NW, KP == 64 && NW == 4 ? 2 : 1) delta_fwd(const __grid_constant__ Delta p) {
+template <int KP, int NW, int kGroups, bool kUnitRows>
+__global__ void __launch_bounds__(kGroups * kPrep + 32 * NW, KP == 64 && NW == 4 && kGroups == 1 ? 2 : 1) delta_fwd(const __grid_constant__ Delta p) {
     extern __shared__ __align__(128) char smem[];
     const int parts = (p.V + 16 * NW - 1) / (16 * NW), item = blockIdx.x / parts, col0 = blockIdx.x % parts * 16 * NW;
     const int b = item / p.H, h = item % p.H;
     const int warps = min(NW, (p.V - col0 + 15) / 16);  // that have columns
-    constexpr bool kSplit = KP == 64 || NW == 8;        // registers: fewer to prepare, more for the columns
-    if (threadIdx.x < kPrep) {
-        if constexpr (kSplit) ptx::regs_dec<NW == 8 ? 104 : 96>();
-        prepare_chunks<KP, NW, false, kUnitRows>(p, smem, b, h, 32 * warps);
+    if (threadIdx.x < kGroups * kPrep) {
+        Registers<KP, NW, kGroups>::prepare();
+        prepare_chunks<KP, NW, false, kGroups, kUnitRows>(p, smem, b, h, 32 * warps);
     } else {
-        if constexpr (kSplit) ptx::regs_inc<NW == 8 ? 200 : 160>();
-        const int w = threadIdx.x / 32 - kPrep / 32;
-        if (w < warps) walk<KP, NW, kUnitRows>(p, smem, b, h, w, col0 + 16 * w, 32 * warps);
+        Registers<KP, NW, kGroups>::walk();
+        const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
+        if (w < warps) walk<KP, NW, kGroups, kUnitRows>(p, smem, b, h, w, col0 + 16 * w, 32 * warps);
     }
 }
 
-template <int KP, int NW>
+template <int KP, int NW, int kGroups>
 int launch(const Delta& p, cudaStream_t stream) {
-    using L = Layout<KP, NW, false>;
+    using L = Layout<KP, NW, false, kGroups>;
     const bool units = whole_units(p.k) && whole_units(p.q) && whole_units(p.v);
-    const auto kernel = units ? delta_fwd<KP, NW, true> : delta_fwd<KP, NW, false>;
+    const auto kernel = units ? delta_fwd<KP, NW, kGroups, true> : delta_fwd<KP, NW, kGroups, false>;
     static std::atomic<uint64_t> done[2];
     if (allow_smem(kernel, L::kBytes, done[units]) != cudaSuccess) return SSDC_ERR_CUDA;
     const int parts = (p.V + 16 * NW - 1) / (16 * NW);
-    kernel<<<p.B * p.H * parts, kPrep + 32 * NW, L::kBytes, stream>>>(p);
+    kernel<<<p.B * p.H * parts, kGroups * kPrep + 32 * NW, L::kBytes, stream>>>(p);
     return 1;
 }
 
@@ -253,8 +249,9 @@ int launch(const Delta& p, cudaStream_t stream) {
 
 int delta_fwd_launch(const Delta& p, cudaStream_t stream) {
     using namespace delta;
-    if (p.K <= 64) return p.V <= 64 ? launch<64, 4>(p, stream) : launch<64, 8>(p, stream);
-    return p.V <= 64 ? launch<128, 4>(p, stream) : launch<128, 8>(p, stream);
+    if (few_states(p)) return p.K <= 64 ? launch<64, 4, 2>(p, stream) : launch<128, 4, 2>(p, stream);
+    if (p.K <= 64) return p.V <= 64 ? launch<64, 4, 1>(p, stream) : launch<64, 8, 1>(p, stream);
+    return p.V <= 64 ? launch<128, 4, 1>(p, stream) : launch<128, 8, 1>(p, stream);
 }
 
 }  // namespace block

@@ -7,47 +7,54 @@ namespace ssdc {
 namespace block {
 namespace delta {
 
-enum : int { kBarPrep = 1, kBarKeys = 2 /* and 3 */, kBarStage = 4 /* and 5 */, kBarFull = 6, kBarFree = 7 };
+// Barriers by number: kBarPrep and the next, one for each group that prepares chunks; four each for a chunk's keys and its
+// stage, by the chunk's number; two each for its blocks, there and used.
+enum : int { kBarPrep = 1, kBarKeys = 3, kBarStage = 7, kBarFull = 11, kBarFree = 13 };
 
-// kBack: from the last chunk to the first, and P in two parts.
-template <int KP, int NW, bool kBack>
+// kBack: from the last chunk to the first, and P in two parts. kGroups: of four warps that prepare chunks, in turn.
+template <int KP, int NW, bool kBack, int kGroups>
 struct Layout {
     static constexpr int kKeyPitch = KP * 2, kKeyTile = C * kKeyPitch;
     static constexpr int kStage = 2 * kKeyTile;          // k and q
-    static constexpr int kStages = 3;
+    static constexpr int kStages = kGroups == 2 ? 4 : 3;
+    static constexpr int kSets = 2 * kGroups;            // of what the tokens of a chunk have
     static constexpr int kStrip = C * 32;                // 64 tokens of 16 columns
     static constexpr int kPitch = C * 2, kSquare = C * kPitch;
+    static constexpr int kBlocks = (kBack ? 4 : 3) * kSquare;  // blocks of -A and (T beta)^T, two parts; P
     static constexpr int kStripOff = kStages * kStage;   // [warp][2] strips of v or do
-    static constexpr int kLOff = kStripOff + NW * 2 * kStrip;  // blocks of -A and (T beta)^T, two parts; P
-    static constexpr int kTabOff = kLOff + (kBack ? 4 : 3) * kSquare;  // [2] Token[64]
-    static constexpr int kFactorsOff = kTabOff + 2 * C * 16; // [2] Factors[64], then [2] Gam_C
-    static constexpr int kGamOff = kFactorsOff + 2 * C * 16;
-    static constexpr int kBetaOff = kGamOff + 16;        // [2] beta of the 64 tokens
-    static constexpr int kLengthOff = kBetaOff + 2 * C * 4;  // rk, rq of the 64 tokens
-    static constexpr int kScratchOff = kLengthOff + C * 8;     // [4 warps] 16 x 20 floats
-    static constexpr int kBytes = kScratchOff + 4 * 16 * 20 * 4;
+    static constexpr int kLOff = kStripOff + NW * 2 * kStrip;  // [kGroups] blocks
+    static constexpr int kTabOff = kLOff + kGroups * kBlocks;  // [kSets] Token[64]
+    static constexpr int kFactorsOff = kTabOff + kSets * C * 16;  // [kSets] Factors[64], then [kSets] Gam_C
+    static constexpr int kGamOff = kFactorsOff + kSets * C * 16;
+    static constexpr int kBetaOff = kGamOff + 16;        // [kSets] beta of the 64 tokens
+    static constexpr int kLengthOff = kBetaOff + kSets * C * 4;  // [kGroups] rk, rq of the 64 tokens
+    static constexpr int kScratchOff = kLengthOff + kGroups * C * 8;  // [warps] 16 x 16 floats
+    static constexpr int kBytes = kScratchOff + kGroups * 4 * 16 * 16 * 4;
 };
 
 // What prepares chunks: each of four warps fetches 16 rows of a chunk's keys and queries and takes their lengths,
 // and computes two or three of the ten 16 x 16 blocks on and below the diagonal, one of them on it. While it
-// works on one chunk, the next one's rows are on their way.
-template <int KP, int NW, bool kBack, bool kUnitRows>
+// works on one chunk, the next one's rows are on their way. Two groups of four warps take chunks in turn: where there is
+// one CTA to an SM, the preparation of a chunk takes longer than its way along the chain.
+template <int KP, int NW, bool kBack, int kGroups, bool kUnitRows>
 __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b, int h, int column_threads) {
-    using L = Layout<KP, NW, kBack>;
+    using L = Layout<KP, NW, kBack, kGroups>;
     constexpr int kUnits = KP / 8, kRows = 32 / kUnits;  // of a row; rows a warp fetches at once
     const uint32_t base = ptx::smem_addr(smem);
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = h / (p.H / p.G), all = kPrep + column_threads;
+    const int mine = kGroups == 2 ? threadIdx.x / kPrep : 0;  // group
+    const int tid = threadIdx.x % kPrep, warp = tid / 32, lane = tid % 32, g = h / (p.H / p.G), all = kPrep + column_threads;
     const int64_t chunks = (p.T + C - 1) / C;
     Token* const tabs = reinterpret_cast<Token*>(smem + L::kTabOff);
     float* const betas_of = reinterpret_cast<float*>(smem + L::kBetaOff);
-    float* const scratch = reinterpret_cast<float*>(smem + L::kScratchOff) + warp * 320;
+    float* const scratch = reinterpret_cast<float*>(smem + L::kScratchOff) + (mine * 4 + warp) * 256;
     const float q_scale = p.normalize ? rsqrtf((float)p.K) : 1.0f;
 
     const int fetch_u = lane % kUnits, fetch_r = 16 * warp + lane / kUnits;
     const bool has_unit = fetch_u * 8 < p.K;
     // chunks are counted in the order they are taken: the n-th has the tokens from first_token(n)
-    const int64_t step = kBack ? -C : C, first = kBack ? (chunks - 1) * C : 0;
-    auto first_token = [&](int64_t n) { return first + n * step; };
+    const int64_t chunk_step = kBack ? -C : C;
+    auto first_token = [&](int64_t n) { return (kBack ? (chunks - 1) * C : 0) + n * chunk_step; };
+    const int64_t step = kGroups * chunk_step, first = first_token(mine);
     const __nv_bfloat16* k_row = bf16(p.k.p) + b * p.k.b + g * p.k.h + (first + fetch_r) * p.k.t + (has_unit ? fetch_u * 8 : 0);
     const __nv_bfloat16* q_row = bf16(p.q.p) + b * p.q.b + g * p.q.h + (first + fetch_r) * p.q.t + (has_unit ? fetch_u * 8 : 0);
     auto fetch_keys = [&](int64_t n) {  // in order
@@ -88,13 +95,13 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
     };
     // the entries of the warp's tokens of the n-th chunk
     auto tokens = [&](int64_t n) {
-        const int turn = (int)(n & 1);
+        const int set = (int)(n & (L::kSets - 1));
         const bool there = first_token(n) + gate_r < p.T;
         const float v = __uint_as_float((uint32_t)gate << 16), e = expf(-fabsf(v));
         // log2 of sigmoid(f), not below -256
         const float s = log1pf(e), l = v >= 0.0f ? -s : v - s, lg = l < -177.0f ? -256.0f : l * kLog2e;
-        if (lane >= 16) betas_of[turn * C + gate_r] = there ? (v >= 0.0f ? 1.0f : e) / (1.0f + e) : 0.0f;
-        scan_group<false>(!there ? 0.0f : mark != 0 ? -256.0f : lg, tabs + turn * C + 16 * warp);
+        if (lane >= 16) betas_of[set * C + gate_r] = there ? (v >= 0.0f ? 1.0f : e) / (1.0f + e) : 0.0f;
+        scan_group<false>(!there ? 0.0f : mark != 0 ? -256.0f : lg, tabs + set * C + 16 * warp);
         ptx::cp_async_wait<0>();
     };
 
@@ -107,24 +114,28 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
         return base + (8 * (m % 2) + r) * L::kPitch + (((2 * i + m / 2) ^ r) << 4);
     };
 
-    fetch_gates(0);
-    fetch_keys(0);
-    tokens(0);
-    for (int64_t n = 0; n < chunks; ++n) {
-        const int turn = (int)(n & 1);
+    if (mine < chunks) {
+        fetch_gates(mine);
+        fetch_keys(mine);
+        tokens(mine);
+    }
+    for (int64_t n = mine; n < chunks; n += kGroups) {
+        const int set = (int)(n & (L::kSets - 1));
         const uint32_t keys = (int)(n % L::kStages) * L::kStage;  // from the start of shared memory, as the lanes' offsets are
-        const Token* tab = tabs + turn * C;
-        const float* betas = betas_of + turn * C;
-        if (n >= 2) bar_sync(kBarStage + turn, all);  // the chunk before the last is through with its stage
-        if (n + 1 < chunks) {
-            fetch_gates(n + 1);
-            fetch_keys(n + 1);
+        const Token* tab = tabs + set * C;
+        const float* betas = betas_of + set * C;
+        if constexpr (kGroups == 1) {
+            if (n >= 2) bar_sync(kBarStage + (int)((n - 2) & 3), all);  // that chunk is through with its stage
+            if (n + 1 < chunks) {
+                fetch_gates(n + 1);
+                fetch_keys(n + 1);
+            }
         }
-        bar_sync(kBarPrep, kPrep);
-        bar_arrive(kBarKeys + turn, all);
+        bar_sync(kBarPrep + mine, kPrep);
+        bar_arrive(kBarKeys + (int)(n & 3), all);
         // pairs of the blocks' entries, rows lane / 4 and 8 more: P, and -A in two parts
         uint32_t P[3][2][2], P2[3][2][2], A[2][2][2], B[2][2][2], T[8];
-        float2* lengths = reinterpret_cast<float2*>(smem + L::kLengthOff);
+        float2* lengths = reinterpret_cast<float2*>(smem + L::kLengthOff) + mine * C;
 #pragma unroll
         for (int slot = 0; slot < 3; ++slot) {
             if (slot == 2 && warp >= 2) break;
@@ -155,20 +166,20 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
                             lengths[16 * warp + 8 * e + lane / 4] =
                                 p.normalize ? make_float2(rsqrtf(kk[e][2 * e + x] + kUnitEps), rsqrtf(qq[e][2 * e + x] + kUnitEps) * q_scale)
                                             : make_float2(1.0f, 1.0f);
-                bar_sync(kBarPrep, kPrep);
+                bar_sync(kBarPrep + mine, kPrep);
                 if (tid >= kPrep - C) {
                     const int i = tid - (kPrep - C), group = i / 16;
-                    long long mine = tab[i].sum, all_of_it = 0;
+                    long long sum = tab[i].sum, all_of_it = 0;
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
                         const long long of_m = tab[16 * m + 15].sum;
                         all_of_it += of_m;
-                        mine += m < group ? of_m : 0;
+                        sum += m < group ? of_m : 0;
                     }
-                    const float into = decay(mine);
+                    const float into = decay(sum);
                     const float2 n = lengths[i];
-                    reinterpret_cast<Factors*>(smem + L::kFactorsOff)[turn * C + i] = {into * n.x, into * n.y, decay(all_of_it - mine) * n.x, betas[i]};
-                    if (i == C - 1) reinterpret_cast<float*>(smem + L::kGamOff)[turn] = into;
+                    reinterpret_cast<Factors*>(smem + L::kFactorsOff)[set * C + i] = {into * n.x, into * n.y, decay(all_of_it - sum) * n.x, betas[i]};
+                    if (i == C - 1) reinterpret_cast<float*>(smem + L::kGamOff)[set] = into;
                 }
             }
             const int row = 16 * bi[slot] + lane / 4;
@@ -215,10 +226,10 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
                     B[o][e][1] = pack_rest(-a[2], -a[3], A[o][e][1]);
                 } else {
                     const float b0 = betas[row], b1 = betas[row + 8];
-                    scratch[20 * col + lane / 4] = b0 * a[0];
-                    scratch[20 * (col + 1) + lane / 4] = b0 * a[1];
-                    scratch[20 * col + lane / 4 + 8] = b1 * a[2];
-                    scratch[20 * (col + 1) + lane / 4 + 8] = b1 * a[3];
+                    scratch[16 * col + lane / 4] = b0 * a[0];
+                    scratch[16 * (col + 1) + lane / 4] = b0 * a[1];
+                    scratch[16 * col + lane / 4 + 8] = b1 * a[2];
+                    scratch[16 * (col + 1) + lane / 4 + 8] = b1 * a[3];
                 }
             }
             if (slot == 0) {
@@ -234,8 +245,8 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
                 }
             }
         }
-        if (n >= 1) bar_sync(kBarFree, all);  // the last chunk is through with its blocks
-        constexpr uint32_t hi = L::kLOff, lo = hi + L::kSquare, ps = lo + L::kSquare;
+        if (n >= kGroups) bar_sync(kBarFree + mine, all);  // the chunk before is through with its blocks
+        const uint32_t hi = L::kLOff + mine * L::kBlocks, lo = hi + L::kSquare, ps = lo + L::kSquare;
 #pragma unroll
         for (int slot = 0; slot < 3; ++slot) {
             if (slot == 2 && warp >= 2) break;
@@ -252,10 +263,36 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
         for (int u = 0; u < 2; ++u)  // the inverse lies transposed: a lane has a row of it
             store16(base + unit_at<L::kPitch>(lane < 16 ? hi : lo, 16 * warp + lane % 16, 2 * warp + u),
                     make_uint4(T[4 * u], T[4 * u + 1], T[4 * u + 2], T[4 * u + 3]));
-        bar_arrive(kBarFull, all);
-        if (n + 1 < chunks) tokens(n + 1);
+        bar_arrive(kBarFull + mine, all);
+        if (n + kGroups < chunks) {
+            if constexpr (kGroups == 2) {
+                fetch_gates(n + 2);
+                if (n >= 2) bar_sync(kBarStage + (int)((n - 2) & 3), all);
+                fetch_keys(n + 2);
+            }
+            tokens(n + kGroups);
+        }
     }
 }
+
+// A CTA's registers: fewer to the warps that prepare, more to those with columns, within what it was launched with (128
+// to a thread where two CTAs share an SM, 168 with 12 warps).
+template <int KP, int NW, int kGroups>
+struct Registers {
+    static constexpr int kPrepare = kGroups == 2 ? 120 : NW == 8 ? 104 : 96;
+    static constexpr int kWalk = kGroups == 2 ? 232 : NW == 8 ? 200 : 160;
+    static constexpr bool kSplit = KP == 64 || NW == 8 || kGroups == 2;  // else 255 to every thread
+    static_assert(!kSplit || kGroups * 4 * kPrepare + NW * kWalk <= (kGroups * 4 + NW) * (kGroups * 4 + NW == 8 ? 128 : 168), "");
+    __device__ __forceinline__ static void prepare() {
+        if constexpr (kSplit) ptx::regs_dec<kPrepare>();
+    }
+    __device__ __forceinline__ static void walk() {
+        if constexpr (kSplit) ptx::regs_inc<kWalk>();
+    }
+};
+
+// Whether every SM has one CTA of 64 columns at most: then two groups prepare its chunks.
+inline bool few_states(const Delta& p) { return (int64_t)p.B * p.H * ((p.V + 63) / 64) <= device_sms(); }
 
 // Packed pairs of a strip to rows of memory: token (or state row) r of `n` goes to to + r stride.
 __device__ __forceinline__ void put_strip(uint32_t strip, __nv_bfloat16* to, int64_t stride, int n, int columns) {
