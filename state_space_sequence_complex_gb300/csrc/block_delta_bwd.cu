@@ -76,7 +76,7 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         else ptx::cp_async_commit();
         bar_sync(kBarKeys + (int)(n & 3), all);
         const uint32_t keys = (int)(n % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
-        float X[8][4] = {};
+        float X[8][4];
 #pragma unroll
         for (int s = 0; s < KP / 16; ++s) {
             Split a;
@@ -85,8 +85,8 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
             for (int m = 0; m < 4; ++m) {
                 uint32_t kb[4];
                 ldsm(kb, keys + 16 * m * L::kKeyPitch + key_lanes.down[s]);
-                mma(X[2 * m], a.hi, kb[0], kb[1]);
-                mma(X[2 * m + 1], a.hi, kb[2], kb[3]);
+                mma_at(s, X[2 * m], a.hi, kb[0], kb[1]);
+                mma_at(s, X[2 * m + 1], a.hi, kb[2], kb[3]);
                 mma(X[2 * m], a.lo, kb[0], kb[1]);
                 mma(X[2 * m + 1], a.lo, kb[2], kb[3]);
             }
@@ -142,8 +142,7 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float* x = X[2 * r + e];
-                x[0] = x[1] = x[2] = x[3] = 0.0f;
-                mma(x, a.lo, bh[2 * e], bh[2 * e + 1]);
+                mma0(x, a.lo, bh[2 * e], bh[2 * e + 1]);
                 mma(x, a.hi, bl[2 * e], bl[2 * e + 1]);
                 mma(x, a.hi, bh[2 * e], bh[2 * e + 1]);
             }
@@ -337,7 +336,7 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
         float front_q[2] = {}, front_k[2] = {}, behind[2] = {};
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            float so[2][4] = {}, sz[2][4] = {}, su[2][4] = {};
+            float so[2][4], sz[2][4], su[2][4];
 #pragma unroll
             for (int s = 0; s < VP / 16; ++s) {
                 uint32_t oa[4], za[4], ua[4], sb[4], db[4];
@@ -348,9 +347,9 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
                 ldsm(db, L::kDs + feature_rows + 8 * i * L::kPitch + lanes.down[s]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    mma(so[e], oa, sb[2 * e], sb[2 * e + 1]);
-                    mma(sz[e], za, sb[2 * e], sb[2 * e + 1]);
-                    mma(su[e], ua, db[2 * e], db[2 * e + 1]);
+                    mma_at(s, so[e], oa, sb[2 * e], sb[2 * e + 1]);
+                    mma_at(s, sz[e], za, sb[2 * e], sb[2 * e + 1]);
+                    mma_at(s, su[e], ua, db[2 * e], db[2 * e + 1]);
                 }
             }
             if (gam == 0.0f) {  // a state that a reset cuts off is left out, whatever it holds
@@ -410,7 +409,7 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
         for (int n = 0; n < 4; ++n) {
             if (n >= w && half == 0 && lane < 16) sm.columns[w][16 * n + lane] = 0.0f;
             if (n > w) continue;
-            float qk[2][4] = {}, kk[2][4] = {}, ou[2][4] = {}, zu[2][4] = {}, pairs[2][4];
+            float qk[2][4], kk[2][4], ou[2][4], zu[2][4], pairs[2][4];
 #pragma unroll
             for (int s = 0; s < KP / 16; ++s) {
                 uint32_t qa[4], ka[4], kb[4];
@@ -419,8 +418,8 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
                 ldsm(kb, L::kK + 16 * n * L::kKeyPitch + key_lanes.down[s]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    mma(qk[e], qa, kb[2 * e], kb[2 * e + 1]);
-                    mma(kk[e], ka, kb[2 * e], kb[2 * e + 1]);
+                    mma_at(s, qk[e], qa, kb[2 * e], kb[2 * e + 1]);
+                    mma_at(s, kk[e], ka, kb[2 * e], kb[2 * e + 1]);
                 }
             }
 #pragma unroll
@@ -431,8 +430,8 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
                 ldsm(ub, L::kU + 16 * n * L::kPitch + lanes.down[s]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    mma(ou[e], oa, ub[2 * e], ub[2 * e + 1]);
-                    mma(zu[e], za, ub[2 * e], ub[2 * e + 1]);
+                    mma_at(s, ou[e], oa, ub[2 * e], ub[2 * e + 1]);
+                    mma_at(s, zu[e], za, ub[2 * e], ub[2 * e + 1]);
                 }
             }
             float in0 = 1.0f, in1 = 1.0f;
@@ -500,8 +499,8 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
                 for (int e = 0; e < 2; ++e) {
                     const int t = 8 * e + lane / 4, j = 2 * (lane % 4);
                     auto ones = [&](int k) { return (k < t ? 0x3F80u : 0u) | (k + 1 < t ? 0x3F800000u : 0u); };
-                    float sum[4] = {};
-                    mma(sum, a.hi, ones(j), ones(j + 8));
+                    float sum[4];
+                    mma0(sum, a.hi, ones(j), ones(j + 8));
                     mma(sum, a.lo, ones(j), ones(j + 8));
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {

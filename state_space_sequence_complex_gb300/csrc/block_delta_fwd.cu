@@ -74,7 +74,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
         else ptx::cp_async_commit();
         bar_sync(kBarKeys + (int)(c & 3), all);
         const uint32_t keys = (int)(c % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
-        float X[8][4] = {}, O[8][4] = {};
+        float X[8][4], O[8][4];
 #pragma unroll
         for (int s = 0; s < KP / 16; ++s) {
             Split a;
@@ -84,10 +84,10 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
                 uint32_t kb[4], qb[4];
                 ldsm(kb, keys + 16 * n * L::kKeyPitch + key_lanes.down[s]);
                 ldsm(qb, queries + 16 * n * L::kKeyPitch + key_lanes.down[s]);
-                mma(X[2 * n], a.hi, kb[0], kb[1]);
-                mma(X[2 * n + 1], a.hi, kb[2], kb[3]);
-                mma(O[2 * n], a.hi, qb[0], qb[1]);
-                mma(O[2 * n + 1], a.hi, qb[2], qb[3]);
+                mma_at(s, X[2 * n], a.hi, kb[0], kb[1]);
+                mma_at(s, X[2 * n + 1], a.hi, kb[2], kb[3]);
+                mma_at(s, O[2 * n], a.hi, qb[0], qb[1]);
+                mma_at(s, O[2 * n + 1], a.hi, qb[2], qb[3]);
                 mma(X[2 * n], a.lo, kb[0], kb[1]);
                 mma(X[2 * n + 1], a.lo, kb[2], kb[3]);
             }
@@ -146,8 +146,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float* x = X[2 * r + e];
-                x[0] = x[1] = x[2] = x[3] = 0.0f;
-                mma(x, a.lo, bh[2 * e], bh[2 * e + 1]);
+                mma0(x, a.lo, bh[2 * e], bh[2 * e + 1]);
                 mma(x, a.hi, bl[2 * e], bl[2 * e + 1]);
                 mma(x, a.hi, bh[2 * e], bh[2 * e + 1]);
             }

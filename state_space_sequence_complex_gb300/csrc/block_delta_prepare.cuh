@@ -139,7 +139,7 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
 #pragma unroll
         for (int slot = 0; slot < 3; ++slot) {
             if (slot == 2 && warp >= 2) break;
-            float kk[2][4] = {}, qk[2][4] = {}, qq[2][4] = {};
+            float kk[2][4], qk[2][4], qq[2][4];
             const uint32_t kb_at = keys + 16 * bj[slot] * L::kKeyPitch, ka_at = keys + 16 * bi[slot] * L::kKeyPitch;
 #pragma unroll
             for (int s = 0; s < KP / 16; ++s) {
@@ -151,9 +151,9 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
                 if (slot == 0) kb[0] = ka[0], kb[1] = ka[2], kb[2] = ka[1], kb[3] = ka[3];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    mma(qk[e], qa, kb[2 * e], kb[2 * e + 1]);
-                    mma(kk[e], ka, kb[2 * e], kb[2 * e + 1]);
-                    if (slot == 0) mma(qq[e], qa, qa[e], qa[e + 2]);
+                    mma_at(s, qk[e], qa, kb[2 * e], kb[2 * e + 1]);
+                    mma_at(s, kk[e], ka, kb[2 * e], kb[2 * e + 1]);
+                    if (slot == 0) mma_at(s, qq[e], qa, qa[e], qa[e + 2]);
                 }
             }
             if (slot == 0) {
