@@ -6,6 +6,7 @@
 // inside a tile of them; a CTA has all columns of one state, as the gradients of q and k sum over them.
 #include "block_common.cuh"
 #include "block_kernels.h"
+#include "ssdc_kernels.h"
 
 namespace ssdc {
 namespace block {
@@ -508,6 +509,8 @@ __global__ void __launch_bounds__(128) delta_tokens_bwd_finish(const Delta p) {
 template <typename T, int CG, int R>
 __global__ void __launch_bounds__(256) delta_step(const Delta p) {
     constexpr int RG = 256 / CG;  // groups of rows; thread = group * CG + columns / 4
+    launch_dependents();
+    grid_dependency_wait();
     __shared__ float q[kMaxDim], k[kMaxDim], norms[2];
     __shared__ float4 part[8][CG];
     const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, g = h / (p.H / p.G);
@@ -587,22 +590,24 @@ __global__ void __launch_bounds__(256) delta_step(const Delta p) {
 }
 
 template <typename T, int CG>
-void step_launch(const Delta& p, cudaStream_t stream) {
+int step_launch(const Delta& p, cudaStream_t stream) {
     constexpr int RG = 256 / CG;
-    const int grid = p.B * p.H, rows = (p.K + RG - 1) / RG;
+    const int rows = (p.K + RG - 1) / RG;
+    auto go = [&](auto kernel) {
+        return launch_dependent(kernel, dim3(p.B * p.H), dim3(256), 0, stream, p) == cudaSuccess ? 1 : SSDC_ERR_CUDA;
+    };
     if constexpr (128 / RG >= 16)
-        if (rows > 8) return delta_step<T, CG, 16><<<grid, 256, 0, stream>>>(p);
+        if (rows > 8) return go(delta_step<T, CG, 16>);
     if constexpr (128 / RG >= 8)
-        if (rows > 4) return delta_step<T, CG, 8><<<grid, 256, 0, stream>>>(p);
+        if (rows > 4) return go(delta_step<T, CG, 8>);
     if constexpr (128 / RG >= 4)
-        if (rows > 2) return delta_step<T, CG, 4><<<grid, 256, 0, stream>>>(p);
-    delta_step<T, CG, 2><<<grid, 256, 0, stream>>>(p);
+        if (rows > 2) return go(delta_step<T, CG, 4>);
+    return go(delta_step<T, CG, 2>);
 }
 template <typename T>
-void step_launch(const Delta& p, cudaStream_t stream) {
-    if (p.V > 64) step_launch<T, 32>(p, stream);
-    else if (p.V > 32) step_launch<T, 16>(p, stream);
-    else step_launch<T, 8>(p, stream);
+int step_launch(const Delta& p, cudaStream_t stream) {
+    if (p.V > 64) return step_launch<T, 32>(p, stream);
+    return p.V > 32 ? step_launch<T, 16>(p, stream) : step_launch<T, 8>(p, stream);
 }
 
 template <int KR>
@@ -633,9 +638,7 @@ int bwd_launch(const Delta& p, cudaStream_t stream) {
 }  // namespace
 
 int delta_step_launch(const Delta& p, cudaStream_t stream) {
-    if (p.bf16) step_launch<__nv_bfloat16>(p, stream);
-    else step_launch<float>(p, stream);
-    return 1;
+    return p.bf16 ? step_launch<__nv_bfloat16>(p, stream) : step_launch<float>(p, stream);
 }
 
 int delta_tokens_fwd_launch(const Delta& p, cudaStream_t stream) {

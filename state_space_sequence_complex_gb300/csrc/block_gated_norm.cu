@@ -9,6 +9,7 @@
 
 #include "block_common.cuh"
 #include "block_kernels.h"
+#include "ssdc_kernels.h"
 
 namespace ssdc {
 namespace block {
@@ -90,54 +91,87 @@ __device__ __forceinline__ Place place(int piece, int per_piece, int D, int N) {
     return a;
 }
 
-template <typename T, int kOut, bool kWarp, bool kAligned>
-__global__ void __launch_bounds__(512) gated_norm_fwd(const GatedNorm p, int pieces, int per_piece) {
+// Two values a thread at a time where an instruction does two: a row's instructions were as long as its memory.
+template <typename T, int kOut, bool kWarp, bool kAligned, int kRows>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarps : 512) gated_norm_fwd(const GatedNorm p, int per_piece) {
     __shared__ float buffer[kWarp ? 1 : 512];
+    launch_dependents();
+    grid_dependency_wait();
     const int N = p.H * p.D;
-    const int64_t item = kWarp ? (int64_t)blockIdx.x * kWarps + threadIdx.x / 32 : blockIdx.x;
-    const int64_t m = item / pieces;
-    if (m >= p.M) return;  // whole warps, or the whole CTA
-    const Place a = place<kWarp>((int)(item % pieces), per_piece, p.D, N);
+    const Place a = place<kWarp>(blockIdx.y, per_piece, p.D, N);
     const bool mine = a.feature < N;
-    float u[kVec] = {}, z[kVec] = {};
-    if (mine) {
-        load8<T, kAligned>(u, p.x, m * p.x_ld + a.feature);
-        load8<T, kAligned>(z, p.z, m * p.z_ld + a.feature);
-        if (p.v != nullptr) {
-            float v[kVec];
-            load8<T, kAligned>(v, p.v, m * p.v_ld + a.feature);
-            const float s = p.s[a.head];
+    const int64_t m0 = kWarp ? ((int64_t)blockIdx.x * kWarps + threadIdx.x / 32) * kRows : blockIdx.x;
+    float2 u[kRows][4], z[kRows][4];
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) u[i] = fmaf(s, v[i], u[i]);
+    for (int r = 0; r < kRows; ++r) {
+        const bool there = mine && m0 + r < p.M;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[r][i] = z[r][i] = make_float2(0.0f, 0.0f);
+        if (there) {
+            load8<T, kAligned>(&u[r][0].x, p.x, (m0 + r) * p.x_ld + a.feature);
+            load8<T, kAligned>(&z[r][0].x, p.z, (m0 + r) * p.z_ld + a.feature);
         }
     }
-    float ss = 0.0f;
+    if (p.v != nullptr && mine) {
+        const float s = p.s[a.head];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) ss = fmaf(u[i], u[i], ss);
-    ss = head_sum<kWarp>(ss, a.lanes, a.first, buffer);
-    const float rstd = 1.0f / sqrtf(ss / (float)p.D + p.eps);
-    float y[kVec];
+        for (int r = 0; r < kRows; ++r) {
+            if (m0 + r >= p.M) break;
+            float2 v[4];
+            load8<T, kAligned>(&v[0].x, p.v, (m0 + r) * p.v_ld + a.feature);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        const float w = p.w != nullptr && mine ? p.w[a.feature + i] : 1.0f;
-        y[i] = u[i] * rstd * w * (z[i] * sigmoid(z[i]));
-    }
-    if constexpr (kOut == SSD_TYPE_E4M3) {
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) amax = fmaxf(amax, mine ? fabsf(y[i]) : 0.0f);
-        amax = warp_max<16>(amax);
-        const Scale scale(amax);
-        if (mine) {
-            if (a.feature % SSD_FP8_GROUP == 0) p.scale[(int64_t)(a.feature / SSD_FP8_GROUP) * p.M + m] = scale.s;
-            float q[kVec];
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) q[i] = scale.quotient(y[i]);
-            store_e4m3<kVec>(static_cast<uint8_t*>(p.y) + m * p.y_ld + a.feature, q);
+            for (int i = 0; i < 4; ++i) u[r][i] = ptx::fma2(make_float2(s, s), v[i], u[r][i]);
         }
-    } else if (mine) {
-        if constexpr (kOut == SSD_TYPE_BF16) store8<__nv_bfloat16, kAligned>(p.y, m * p.y_ld + a.feature, y);
-        else store8<float, kAligned>(p.y, m * p.y_ld + a.feature, y);
+    }
+    float2 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = make_float2(1.0f, 1.0f);
+    if (p.w != nullptr && mine) {
+        if ((reinterpret_cast<uintptr_t>(p.w) & 15) == 0) {
+            const float4 lo = *reinterpret_cast<const float4*>(p.w + a.feature), hi = *reinterpret_cast<const float4*>(p.w + a.feature + 4);
+            w[0] = make_float2(lo.x, lo.y), w[1] = make_float2(lo.z, lo.w), w[2] = make_float2(hi.x, hi.y), w[3] = make_float2(hi.z, hi.w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = make_float2(p.w[a.feature + 2 * i], p.w[a.feature + 2 * i + 1]);
+        }
+    }
+    const float mean = 1.0f / (float)p.D;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        if (m0 + r >= p.M) break;  // whole warps, or the whole CTA
+        float2 ss2 = ptx::mul2(u[r][0], u[r][0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) ss2 = ptx::fma2(u[r][i], u[r][i], ss2);
+        const float ss = head_sum<kWarp>(ss2.x + ss2.y, a.lanes, a.first, buffer);
+        const float rstd = rsqrtf(fmaf(ss, mean, p.eps));
+        float2 y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 e = ptx::mul2(z[r][i], make_float2(-1.44269504f, -1.44269504f));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+            e = ptx::fma2(e, make_float2(1.0f, 1.0f), make_float2(1.0f, 1.0f));
+            asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+            asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+            y[i] = ptx::mul2(ptx::mul2(ptx::mul2(u[r][i], make_float2(rstd, rstd)), w[i]), ptx::mul2(z[r][i], e));
+        }
+        const int64_t m = m0 + r;
+        if constexpr (kOut == SSD_TYPE_E4M3) {
+            float amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
+            amax = warp_max<16>(mine ? amax : 0.0f);
+            const Scale scale(amax);
+            if (mine) {
+                if (a.feature % SSD_FP8_GROUP == 0) p.scale[(int64_t)(a.feature / SSD_FP8_GROUP) * p.M + m] = scale.s;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = scale.quotient(y[i]);
+                store_e4m3<kVec>(static_cast<uint8_t*>(p.y) + m * p.y_ld + a.feature, &y[0].x);
+            }
+        } else if (mine) {
+            if constexpr (kOut == SSD_TYPE_BF16) store8<__nv_bfloat16, kAligned>(p.y, m * p.y_ld + a.feature, &y[0].x);
+            else store8<float, kAligned>(p.y, m * p.y_ld + a.feature, &y[0].x);
+        }
     }
 }
 
@@ -147,6 +181,8 @@ __global__ void __launch_bounds__(512) gated_norm_fwd(const GatedNorm p, int pie
 template <typename T, bool kWarp, bool kAligned, bool kSkip>
 __global__ void __launch_bounds__(kWarp ? 256 : 512) gated_norm_bwd(const GatedNorm p, int pieces, int per_piece, int parts) {
     __shared__ float buffer[kWarp ? 1 : 4 * 512], sums[kWarp ? kWarps : 1][32][kVec + 1];
+    launch_dependents();
+    grid_dependency_wait();
     const int N = p.H * p.D, piece = blockIdx.x % pieces, part = blockIdx.x / pieces;
     const Place a = place<kWarp>(piece, per_piece, p.D, N);
     const bool mine = a.feature < N;
@@ -229,18 +265,22 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512) gated_norm_bwd(const GatedN
     }
 }
 
-// dw and ds from the CTAs' shares, 8 warps to 32 columns.
+// dw and ds from the CTAs' shares: 32 groups of 8 columns' threads take every 32nd share.
 __global__ void __launch_bounds__(256) gated_norm_dw(const GatedNorm p, int parts) {
-    __shared__ float sums[8][32];
-    const int N = p.H * p.D, lane = threadIdx.x % 32, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+    __shared__ float sums[32][9];
+    grid_dependency_wait();
+    const int N = p.H * p.D, lane = threadIdx.x % 8, group = threadIdx.x / 8, c = blockIdx.x * 8 + lane;
     float s = 0.0f;
-    if (c < N + p.H)
-        for (int r = warp; r < parts; r += 8) s += p.partial[(int64_t)r * (N + p.H) + c];
-    sums[warp][lane] = s;
+    if (c < N + p.H) {
+#pragma unroll 4
+        for (int r = group; r < parts; r += 32) s += p.partial[(int64_t)r * (N + p.H) + c];
+    }
+    sums[group][lane] = s;
     __syncthreads();
-    if (warp == 0) {
+    if (threadIdx.x < 8) {
+        s = 0.0f;
 #pragma unroll
-        for (int r = 1; r < 8; ++r) s += sums[r][lane];
+        for (int r = 0; r < 32; ++r) s += sums[r][lane];
         if (c < N) {
             if (p.dw != nullptr) p.dw[c] = s;
         } else if (c < N + p.H && p.ds != nullptr) {
@@ -280,12 +320,15 @@ Split split(int H, int D, bool groups) {
 template <typename T, int kOut>
 int fwd_launch(const GatedNorm& p, bool aligned, cudaStream_t stream) {
     const Split s = split(p.H, p.D, kOut == SSD_TYPE_E4M3);
-    const int64_t items = p.M * s.pieces, ctas = s.warp ? (items + kWarps - 1) / kWarps : items;
-    if (ctas > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
-    auto go = [&](auto kernel) { kernel<<<(unsigned)ctas, s.threads, 0, stream>>>(p, s.pieces, s.per_piece); };
-    if (s.warp) aligned ? go(gated_norm_fwd<T, kOut, true, true>) : go(gated_norm_fwd<T, kOut, true, false>);
-    else aligned ? go(gated_norm_fwd<T, kOut, false, true>) : go(gated_norm_fwd<T, kOut, false, false>);
-    return 1;
+    auto go = [&](auto kernel, int64_t rows) {
+        const dim3 grid((unsigned)((p.M + rows - 1) / rows), s.pieces);
+        return launch_dependent(kernel, grid, dim3(s.threads), 0, stream, p, s.per_piece) == cudaSuccess ? 1 : SSDC_ERR_CUDA;
+    };
+    if (!s.warp) return aligned ? go(gated_norm_fwd<T, kOut, false, true, 1>, 1) : go(gated_norm_fwd<T, kOut, false, false, 1>, 1);
+    // two rows a warp where that leaves every SM its 64 warps twice: more loads on their way, weights read once
+    const bool two = p.M * s.pieces >= (int64_t)4 * 64 * device_sms();
+    if (two) return aligned ? go(gated_norm_fwd<T, kOut, true, true, 2>, 2 * kWarps) : go(gated_norm_fwd<T, kOut, true, false, 2>, 2 * kWarps);
+    return aligned ? go(gated_norm_fwd<T, kOut, true, true, 1>, kWarps) : go(gated_norm_fwd<T, kOut, true, false, 1>, kWarps);
 }
 template <typename T>
 int fwd_launch(const GatedNorm& p, cudaStream_t stream) {
@@ -301,12 +344,15 @@ template <typename T, bool kSkip>
 int bwd_launch(const GatedNorm& p, bool aligned, cudaStream_t stream) {
     const Split s = split(p.H, p.D, false);
     const int parts = gated_norm_bwd_parts(p.M, p.H, p.D);
-    auto go = [&](auto kernel) { kernel<<<(unsigned)(s.pieces * parts), s.threads, 0, stream>>>(p, s.pieces, s.per_piece, parts); };
-    if (s.warp) aligned ? go(gated_norm_bwd<T, true, true, kSkip>) : go(gated_norm_bwd<T, true, false, kSkip>);
-    else aligned ? go(gated_norm_bwd<T, false, true, kSkip>) : go(gated_norm_bwd<T, false, false, kSkip>);
+    auto go = [&](auto kernel) {
+        return launch_dependent(kernel, dim3(s.pieces * parts), dim3(s.threads), 0, stream, p, s.pieces, s.per_piece, parts);
+    };
+    cudaError_t e;
+    if (s.warp) e = aligned ? go(gated_norm_bwd<T, true, true, kSkip>) : go(gated_norm_bwd<T, true, false, kSkip>);
+    else e = aligned ? go(gated_norm_bwd<T, false, true, kSkip>) : go(gated_norm_bwd<T, false, false, kSkip>);
+    if (e != cudaSuccess) return SSDC_ERR_CUDA;
     if (p.partial == nullptr) return 1;
-    gated_norm_dw<<<(p.H * p.D + p.H + 31) / 32, 256, 0, stream>>>(p, parts);
-    return 2;
+    return launch_dependent(gated_norm_dw, dim3((p.H * p.D + p.H + 7) / 8), dim3(256), 0, stream, p, parts) == cudaSuccess ? 2 : SSDC_ERR_CUDA;
 }
 template <typename T>
 int bwd_launch(const GatedNorm& p, cudaStream_t stream) {
