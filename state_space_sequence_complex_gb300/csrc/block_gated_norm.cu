@@ -77,21 +77,59 @@ __device__ __forceinline__ float head_sum(float v, int n, int first, float* buff
 
 // The features of a thread and its head: `piece` counts the row's parts (256 features, or a CTA's heads).
 struct Place {
-    int feature;  // first of the 8; at least N: none
+    int feature;  // first of the 8; of a thread without features the row's first, which it reads and leaves
     int head, lanes, first;
+    bool mine;
 };
 template <bool kWarp>
 __device__ __forceinline__ Place place(int piece, int per_piece, int D, int N) {
     Place a;
     const int t = kWarp ? threadIdx.x % 32 : threadIdx.x;
-    a.feature = t < per_piece ? (piece * per_piece + t) * kVec : N;
-    a.head = a.feature < N ? a.feature / D : 0;
+    a.feature = (piece * per_piece + t) * kVec;
+    a.mine = t < per_piece && a.feature < N;
+    if (!a.mine) a.feature = 0;
+    a.head = a.feature / D;
     a.lanes = D / kVec;
     a.first = t < per_piece ? t / a.lanes * a.lanes : 0;
     return a;
 }
 
-// Two values a thread at a time where an instruction does two: a row's instructions were as long as its memory.
+// A thread's weights.
+__device__ __forceinline__ void load_weights(float2* w, const float* p, int feature) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = make_float2(1.0f, 1.0f);
+    if (p == nullptr) return;
+    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        const float4 lo = *reinterpret_cast<const float4*>(p + feature), hi = *reinterpret_cast<const float4*>(p + feature + 4);
+        w[0] = make_float2(lo.x, lo.y), w[1] = make_float2(lo.z, lo.w), w[2] = make_float2(hi.x, hi.y), w[3] = make_float2(hi.z, hi.w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = make_float2(p[feature + 2 * i], p[feature + 2 * i + 1]);
+    }
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// sigmoid of two values, to zero where the exponential overflows.
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+    float2 e = ptx::mul2(z, both(-1.44269504f));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    e = ptx::fma2(e, both(1.0f), both(1.0f));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    return e;
+}
+
+__device__ __forceinline__ float sum8(const float2* a, const float2* b) {
+    float2 s = ptx::mul2(a[0], b[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s = ptx::fma2(a[i], b[i], s);
+    return s.x + s.y;
+}
+
+// Two values at a time where an instruction does two, and no branch for what a thread does not have: a row's
+// instructions were as long as its memory.
 template <typename T, int kOut, bool kWarp, bool kAligned, int kRows>
 __global__ void __launch_bounds__(kWarp ? 32 * kWarps : 512) gated_norm_fwd(const GatedNorm p, int per_piece) {
     __shared__ float buffer[kWarp ? 1 : 512];
@@ -99,76 +137,50 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarps : 512) gated_norm_fwd(cons
     grid_dependency_wait();
     const int N = p.H * p.D;
     const Place a = place<kWarp>(blockIdx.y, per_piece, p.D, N);
-    const bool mine = a.feature < N;
     const int64_t m0 = kWarp ? ((int64_t)blockIdx.x * kWarps + threadIdx.x / 32) * kRows : blockIdx.x;
-    float2 u[kRows][4], z[kRows][4];
+    if (m0 >= p.M) return;  // whole warps, or the whole CTA
+    float2 u[kRows][4], z[kRows][4], w[4];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        const bool there = mine && m0 + r < p.M;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[r][i] = z[r][i] = make_float2(0.0f, 0.0f);
-        if (there) {
-            load8<T, kAligned>(&u[r][0].x, p.x, (m0 + r) * p.x_ld + a.feature);
-            load8<T, kAligned>(&z[r][0].x, p.z, (m0 + r) * p.z_ld + a.feature);
-        }
+        const int64_t m = kRows == 1 ? m0 : min(m0 + r, p.M - 1);
+        load8<T, kAligned>(&u[r][0].x, p.x, m * p.x_ld + a.feature);
+        load8<T, kAligned>(&z[r][0].x, p.z, m * p.z_ld + a.feature);
     }
-    if (p.v != nullptr && mine) {
-        const float s = p.s[a.head];
+    load_weights(w, p.w, a.feature);
+    if (p.v != nullptr) {
+        const float2 s = both(p.s[a.head]);
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            if (m0 + r >= p.M) break;
             float2 v[4];
-            load8<T, kAligned>(&v[0].x, p.v, (m0 + r) * p.v_ld + a.feature);
+            load8<T, kAligned>(&v[0].x, p.v, (kRows == 1 ? m0 : min(m0 + r, p.M - 1)) * p.v_ld + a.feature);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) u[r][i] = ptx::fma2(make_float2(s, s), v[i], u[r][i]);
-        }
-    }
-    float2 w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = make_float2(1.0f, 1.0f);
-    if (p.w != nullptr && mine) {
-        if ((reinterpret_cast<uintptr_t>(p.w) & 15) == 0) {
-            const float4 lo = *reinterpret_cast<const float4*>(p.w + a.feature), hi = *reinterpret_cast<const float4*>(p.w + a.feature + 4);
-            w[0] = make_float2(lo.x, lo.y), w[1] = make_float2(lo.z, lo.w), w[2] = make_float2(hi.x, hi.y), w[3] = make_float2(hi.z, hi.w);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = make_float2(p.w[a.feature + 2 * i], p.w[a.feature + 2 * i + 1]);
+            for (int i = 0; i < 4; ++i) u[r][i] = ptx::fma2(s, v[i], u[r][i]);
         }
     }
     const float mean = 1.0f / (float)p.D;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        if (m0 + r >= p.M) break;  // whole warps, or the whole CTA
-        float2 ss2 = ptx::mul2(u[r][0], u[r][0]);
-#pragma unroll
-        for (int i = 1; i < 4; ++i) ss2 = ptx::fma2(u[r][i], u[r][i], ss2);
-        const float ss = head_sum<kWarp>(ss2.x + ss2.y, a.lanes, a.first, buffer);
-        const float rstd = rsqrtf(fmaf(ss, mean, p.eps));
+        const int64_t m = m0 + r;
+        const bool there = a.mine && (kRows == 1 || m < p.M);
+        const float ss = head_sum<kWarp>(sum8(u[r], u[r]), a.lanes, a.first, buffer);
+        const float2 rstd = both(rsqrtf(fmaf(ss, mean, p.eps)));
         float2 y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float2 e = ptx::mul2(z[r][i], make_float2(-1.44269504f, -1.44269504f));
-            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
-            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-            e = ptx::fma2(e, make_float2(1.0f, 1.0f), make_float2(1.0f, 1.0f));
-            asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
-            asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-            y[i] = ptx::mul2(ptx::mul2(ptx::mul2(u[r][i], make_float2(rstd, rstd)), w[i]), ptx::mul2(z[r][i], e));
-        }
-        const int64_t m = m0 + r;
+        for (int i = 0; i < 4; ++i)
+            y[i] = ptx::mul2(ptx::mul2(ptx::mul2(u[r][i], rstd), w[i]), ptx::mul2(z[r][i], sigmoid2(z[r][i])));
         if constexpr (kOut == SSD_TYPE_E4M3) {
             float amax = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
-            amax = warp_max<16>(mine ? amax : 0.0f);
+            amax = warp_max<16>(a.mine ? amax : 0.0f);
             const Scale scale(amax);
-            if (mine) {
+            if (there) {
                 if (a.feature % SSD_FP8_GROUP == 0) p.scale[(int64_t)(a.feature / SSD_FP8_GROUP) * p.M + m] = scale.s;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = scale.quotient(y[i]);
                 store_e4m3<kVec>(static_cast<uint8_t*>(p.y) + m * p.y_ld + a.feature, &y[0].x);
             }
-        } else if (mine) {
+        } else if (there) {
             if constexpr (kOut == SSD_TYPE_BF16) store8<__nv_bfloat16, kAligned>(p.y, m * p.y_ld + a.feature, &y[0].x);
             else store8<float, kAligned>(p.y, m * p.y_ld + a.feature, &y[0].x);
         }
@@ -179,70 +191,66 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarps : 512) gated_norm_fwd(cons
 // (of u u and of n u) are taken at once; dw and ds stay in registers over a thread's rows and are added up
 // in a fixed order: rows of a thread, warps of a CTA, CTAs by gated_norm_dw.
 template <typename T, bool kWarp, bool kAligned, bool kSkip>
-__global__ void __launch_bounds__(kWarp ? 256 : 512) gated_norm_bwd(const GatedNorm p, int pieces, int per_piece, int parts) {
+__global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : 1) gated_norm_bwd(const GatedNorm p, int pieces, int per_piece, int parts) {
     __shared__ float buffer[kWarp ? 1 : 4 * 512], sums[kWarp ? kWarps : 1][32][kVec + 1];
     launch_dependents();
     grid_dependency_wait();
     const int N = p.H * p.D, piece = blockIdx.x % pieces, part = blockIdx.x / pieces;
     const Place a = place<kWarp>(piece, per_piece, p.D, N);
-    const bool mine = a.feature < N;
-    float w[kVec], dw[kVec] = {}, ds = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) w[i] = !mine ? 0.0f : p.w != nullptr ? p.w[a.feature + i] : 1.0f;
-    const float s = kSkip && mine ? p.s[a.head] : 0.0f, mean = 1.0f / (float)p.D;
+    float2 w[4], dw[4] = {}, ds = {};
+    load_weights(w, p.w, a.feature);
+    const float s = kSkip ? p.s[a.head] : 0.0f, mean = 1.0f / (float)p.D;
     int turn = 0;
     for (int64_t m = kWarp ? (int64_t)part * kWarps + threadIdx.x / 32 : part; m < p.M; m += (int64_t)parts * (kWarp ? kWarps : 1)) {
-        float u[kVec] = {}, z[kVec] = {}, dy[kVec] = {}, v[kVec] = {};
-        if (mine) {
-            load8<T, kAligned>(u, p.x, m * p.x_ld + a.feature);
-            load8<T, kAligned>(z, p.z, m * p.z_ld + a.feature);
-            load8<T, kAligned>(dy, p.dy, m * p.dy_ld + a.feature);
-            if constexpr (kSkip) {
-                load8<T, kAligned>(v, p.v, m * p.v_ld + a.feature);
+        float2 u[4], z[4], dy[4], v[4], n[4];
+        load8<T, kAligned>(&u[0].x, p.x, m * p.x_ld + a.feature);
+        load8<T, kAligned>(&z[0].x, p.z, m * p.z_ld + a.feature);
+        load8<T, kAligned>(&dy[0].x, p.dy, m * p.dy_ld + a.feature);
+        if constexpr (kSkip) {
+            load8<T, kAligned>(&v[0].x, p.v, m * p.v_ld + a.feature);
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) u[i] = fmaf(s, v[i], u[i]);
-            }
+            for (int i = 0; i < 4; ++i) u[i] = ptx::fma2(both(s), v[i], u[i]);
         }
-        float uu = 0.0f, nu = 0.0f, n[kVec];
+        float uu = sum8(u, u);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            float sg, rest;
-            sigmoid_pair(z[i], sg, rest);
-            const float g = z[i] * sg, t = dy[i] * u[i];
-            n[i] = dy[i] * g;                      // times w later
-            z[i] = t * w[i] * fmaf(g, rest, sg);   // dz / rstd
-            dy[i] = t * g;                         // dw's term / rstd
-            uu = fmaf(u[i], u[i], uu);
-            n[i] *= w[i];
-            nu = fmaf(n[i], u[i], nu);
+        for (int i = 0; i < 4; ++i) {
+            const float2 sg = sigmoid2(z[i]), g = ptx::mul2(z[i], sg), t = ptx::mul2(dy[i], u[i]);
+            // the gate's slope sg (1 + z (1 - sg)); 1 - sg is off by 2^-24, and so is the slope, which is near one there
+            const float2 slope = ptx::fma2(g, ptx::fma2(sg, both(-1.0f), both(1.0f)), sg);
+            n[i] = ptx::mul2(ptx::mul2(dy[i], g), w[i]);
+            z[i] = ptx::mul2(ptx::mul2(t, w[i]), slope);  // dz / rstd
+            dy[i] = ptx::mul2(t, g);                      // dw's term / rstd
         }
+        float nu = sum8(n, u);
         uu = head_sum<kWarp>(uu, a.lanes, a.first, buffer + (turn & 1) * 1024);
         nu = head_sum<kWarp>(nu, a.lanes, a.first, buffer + (turn & 1) * 1024 + (kWarp ? 0 : 512));
         ++turn;
-        const float rstd = 1.0f / sqrtf(fmaf(uu, mean, p.eps)), along = nu * mean * rstd * rstd;
+        const float r = rsqrtf(fmaf(uu, mean, p.eps));
+        const float2 rstd = both(r), along = both(-nu * mean * r * r);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            dw[i] = fmaf(dy[i], rstd, dw[i]);
-            z[i] *= rstd;
-            u[i] = rstd * fmaf(-along, u[i], n[i]);
+        for (int i = 0; i < 4; ++i) {
+            dw[i] = ptx::fma2(dy[i], rstd, dw[i]);
+            z[i] = ptx::mul2(z[i], rstd);
+            u[i] = ptx::mul2(rstd, ptx::fma2(along, u[i], n[i]));
             if constexpr (kSkip) {
-                ds = fmaf(u[i], v[i], ds);
-                v[i] = s * u[i];
+                ds = ptx::fma2(u[i], v[i], ds);
+                v[i] = ptx::mul2(both(s), u[i]);
             }
         }
-        if (mine) {
-            store8<T, kAligned>(p.dx, m * p.dx_ld + a.feature, u);
-            store8<T, kAligned>(p.dz, m * p.dz_ld + a.feature, z);
-            if constexpr (kSkip) store8<T, kAligned>(p.dv, m * p.dv_ld + a.feature, v);
+        if (a.mine) {
+            store8<T, kAligned>(p.dx, m * p.dx_ld + a.feature, &u[0].x);
+            store8<T, kAligned>(p.dz, m * p.dz_ld + a.feature, &z[0].x);
+            if constexpr (kSkip) store8<T, kAligned>(p.dv, m * p.dv_ld + a.feature, &v[0].x);
         }
     }
     if (p.partial == nullptr) return;
     float* to = p.partial + (int64_t)part * (N + p.H);
+    const float* dw1 = &dw[0].x;
     if constexpr (kWarp) {
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sums[warp][lane][i] = dw[i];
-        sums[warp][lane][kVec] = head_sum<true>(ds, a.lanes, a.first, buffer);
+        for (int i = 0; i < kVec; ++i) sums[warp][lane][i] = dw1[i];
+        sums[warp][lane][kVec] = head_sum<true>(ds.x + ds.y, a.lanes, a.first, buffer);
         __syncthreads();
         for (int i = threadIdx.x; i < 32 * (kVec + 1); i += blockDim.x) {
             const int l = i / (kVec + 1), e = i % (kVec + 1), feature = (piece * per_piece + l) * kVec;
@@ -256,11 +264,11 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512) gated_norm_bwd(const GatedN
         }
     } else {
         __syncthreads();
-        ds = head_sum<false>(ds, a.lanes, a.first, buffer);
-        if (mine) {
+        const float of_head = head_sum<false>(ds.x + ds.y, a.lanes, a.first, buffer);
+        if (a.mine) {
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) to[a.feature + i] = dw[i];
-            if (a.feature % p.D == 0) to[N + a.head] = ds;
+            for (int i = 0; i < kVec; ++i) to[a.feature + i] = dw1[i];
+            if (a.feature % p.D == 0) to[N + a.head] = of_head;
         }
     }
 }
@@ -371,8 +379,8 @@ int gated_norm_fwd_launch(const GatedNorm& p, cudaStream_t stream) {
 
 int gated_norm_bwd_parts(int64_t M, int64_t H, int64_t D) {
     const Split s = split((int)H, (int)D, false);
-    // about three CTAs of 256 threads an SM
-    const int64_t want = std::max<int64_t>(1, 456 * 256 / ((int64_t)s.threads * s.pieces));
+    // as many CTAs as have room at once: three of 256 threads an SM, or two of those that need more registers
+    const int64_t want = std::max<int64_t>(1, (s.warp ? 456 : 304) * 256 / ((int64_t)s.threads * s.pieces));
     return (int)std::min(want, s.warp ? (M + kWarps - 1) / kWarps : M);
 }
 
