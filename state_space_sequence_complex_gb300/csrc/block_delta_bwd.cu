@@ -58,29 +58,24 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
             const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
             S[i][e] = p.dh_last != nullptr && r < p.K && cl < columns ? p.dh_last[state + (int64_t)r * p.V + cl] : 0.0f;
         }
+    const int64_t z_stride = (int64_t)p.H * p.V, z_step = C * z_stride;
+    __nv_bfloat16* z_rows = static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + (chunks - 1) * C) * p.H + h) * p.V + col0;
     for (int64_t n = 0; n < chunks; ++n) {
         const int64_t c = chunks - 1 - n;
         const int turn = (int)(n & 1), set = (int)(n & (L::kSets - 1)), half = (int)(n % kGroups);
-        const uint32_t mine = strips + turn * L::kStrip, next = strips + (turn ^ 1) * L::kStrip;
-#pragma unroll
-        for (int i = 0; i < KT; i += 2) {
-            stsm_t(strip_rows(next, 8 * i % C), pack(S[i][0], S[i][1]), pack(S[i][2], S[i][3]), pack(S[i + 1][0], S[i + 1][1]),
-                   pack(S[i + 1][2], S[i + 1][3]));
-            if ((i + 2) % 8 == 0) {
-                const int first = 8 * i / C * C;
-                put_strip(next, static_cast<__nv_bfloat16*>(p.ws) + (seq * chunks + c) * p.K * p.V + (int64_t)first * p.V + col0, p.V,
-                          p.K - first, columns);
-            }
-        }
-        if (n + 1 < chunks) fetch_do(n + 1);
-        else ptx::cp_async_commit();
+        // This chunk's strip has its do, and when that has been read its z. The other one has the last chunk's z,
+        // which goes to memory beside the first products; then dS; then the next do.
+        const uint32_t mine = strips + turn * L::kStrip, other = strips + (turn ^ 1) * L::kStrip;
         bar_sync(kBarKeys + (int)(n & 3), all);
         const uint32_t keys = (int)(n % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
+        StripRows rows;
+        rows.take(other);
         float X[8][4];
 #pragma unroll
         for (int s = 0; s < KP / 16; ++s) {
             Split a;
             a.set(S[2 * s], S[2 * s + 1]);
+            stsm_t(strip_rows(other, 16 * s % C), a.hi[0], a.hi[1], a.hi[2], a.hi[3]);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 uint32_t kb[4];
@@ -90,7 +85,16 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
                 mma(X[2 * m], a.lo, kb[0], kb[1]);
                 mma(X[2 * m + 1], a.lo, kb[2], kb[3]);
             }
+            if (s == 0 && n > 0) rows.give(z_rows + z_step, z_stride, n == 1 ? (int)(p.T - (chunks - 1) * C) : C, columns);
+            if (s % 4 == 3) {
+                const int first = s / 4 * C;
+                rows.take(other);
+                rows.give(static_cast<__nv_bfloat16*>(p.ws) + (seq * chunks + c) * p.K * p.V + (int64_t)first * p.V + col0, p.V,
+                          p.K - first, columns);
+            }
         }
+        if (n + 1 < chunks) fetch_do(n + 1);
+        else ptx::cp_async_commit();
         ptx::cp_async_wait<1>();
         __syncwarp();
         bar_sync(kBarFull + half, all);
@@ -192,10 +196,11 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         }
         if (n + kGroups < chunks) bar_arrive(kBarFree + half, all);
         if (n + 2 * kGroups < chunks) bar_arrive(kBarStage + (int)(n & 3), all);
-        const int64_t left = p.T - c * C;
-        put_strip(mine, static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + c * C) * p.H + h) * p.V + col0, (int64_t)p.H * p.V,
-                  left < C ? (int)left : C, columns);
+        z_rows -= z_step;
     }
+    StripRows rows;
+    rows.take(strips + (int)((chunks - 1) & 1) * L::kStrip);
+    rows.give(z_rows + z_step, z_stride, chunks == 1 ? (int)p.T : C, columns);
     if (p.dh0 != nullptr) {
 #pragma unroll
         for (int i = 0; i < KT; ++i)

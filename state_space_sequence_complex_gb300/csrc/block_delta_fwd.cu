@@ -54,31 +54,24 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
             const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
             S[i][e] = p.h0 != nullptr && r < p.K && cl < columns ? p.h0[state + (int64_t)r * p.V + cl] : 0.0f;
         }
+    const int64_t o_stride = (int64_t)p.H * p.V, o_step = C * o_stride, o_first = (b * p.T * p.H + h) * p.V + col0;
+    __nv_bfloat16* o_rows = static_cast<__nv_bfloat16*>(p.o) + o_first;
+    __nv_bfloat16* u_rows = static_cast<__nv_bfloat16*>(p.updates) + o_first;
     for (int64_t c = 0; c < chunks; ++c) {
         const int turn = (int)(c & 1), set = (int)(c & (L::kSets - 1)), half = (int)(c % kGroups);
-        // the strip of the next chunk is free until it is fetched, that of this one when v has been read
-        const uint32_t mine = strips + turn * L::kStrip, next = strips + (turn ^ 1) * L::kStrip;
-        if (p.states != nullptr) {
-#pragma unroll
-            for (int i = 0; i < KT; i += 2) {
-                stsm_t(strip_rows(next, 8 * i % C), pack(S[i][0], S[i][1]), pack(S[i][2], S[i][3]), pack(S[i + 1][0], S[i + 1][1]),
-                       pack(S[i + 1][2], S[i + 1][3]));
-                if ((i + 2) % 8 == 0) {
-                    const int first = 8 * i / C * C;
-                    put_strip(next, static_cast<__nv_bfloat16*>(p.states) + (seq * chunks + c) * p.K * p.V + (int64_t)first * p.V + col0,
-                              p.V, p.K - first, columns);
-                }
-            }
-        }
-        if (c + 1 < chunks) fetch_v(c + 1);
-        else ptx::cp_async_commit();
+        // The strip of this chunk has its v, and when that has been read its u and o. The other one has the last
+        // chunk's o, which goes to memory beside the first products; then the state, where it is kept; then the next v.
+        const uint32_t mine = strips + turn * L::kStrip, other = strips + (turn ^ 1) * L::kStrip;
         bar_sync(kBarKeys + (int)(c & 3), all);
         const uint32_t keys = (int)(c % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
+        StripRows rows;
+        rows.take(other);
         float X[8][4], O[8][4];
 #pragma unroll
         for (int s = 0; s < KP / 16; ++s) {
             Split a;
             a.set(S[2 * s], S[2 * s + 1]);
+            if (p.states != nullptr) stsm_t(strip_rows(other, 16 * s % C), a.hi[0], a.hi[1], a.hi[2], a.hi[3]);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 uint32_t kb[4], qb[4];
@@ -91,7 +84,16 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
                 mma(X[2 * n], a.lo, kb[0], kb[1]);
                 mma(X[2 * n + 1], a.lo, kb[2], kb[3]);
             }
+            if (s == 0 && c > 0) rows.give(o_rows - o_step, o_stride, C, columns);
+            if (p.states != nullptr && s % 4 == 3) {
+                const int first = s / 4 * C;
+                rows.take(other);
+                rows.give(static_cast<__nv_bfloat16*>(p.states) + (seq * chunks + c) * p.K * p.V + (int64_t)first * p.V + col0, p.V,
+                          p.K - first, columns);
+            }
         }
+        if (c + 1 < chunks) fetch_v(c + 1);
+        else ptx::cp_async_commit();
         ptx::cp_async_wait<1>();
         __syncwarp();
         bar_sync(kBarFull + half, all);
@@ -196,16 +198,20 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
         }
         if (c + kGroups < chunks) bar_arrive(kBarFree + half, all);
         if (c + 2 * kGroups < chunks) bar_arrive(kBarStage + (int)(c & 3), all);
-        if (p.updates != nullptr)
-            put_strip(mine, static_cast<__nv_bfloat16*>(p.updates) + ((b * p.T + c * C) * p.H + h) * p.V + col0, (int64_t)p.H * p.V,
-                      n_tokens, columns);
+        if (p.updates != nullptr) {
+            rows.take(mine);
+            rows.give(u_rows, o_stride, n_tokens, columns);
+            u_rows += o_step;
+        }
 #pragma unroll
         for (int n = 0; n < 8; n += 2)
             stsm_t(strip_rows(mine, 8 * n), pack(O[n][0], O[n][1]), pack(O[n][2], O[n][3]), pack(O[n + 1][0], O[n + 1][1]),
                    pack(O[n + 1][2], O[n + 1][3]));
-        put_strip(mine, static_cast<__nv_bfloat16*>(p.o) + ((b * p.T + c * C) * p.H + h) * p.V + col0, (int64_t)p.H * p.V, n_tokens,
-                  columns);
+        o_rows += o_step;
     }
+    StripRows rows;
+    rows.take(strips + (int)((chunks - 1) & 1) * L::kStrip);
+    rows.give(o_rows - o_step, o_stride, (int)(p.T - (chunks - 1) * C), columns);
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll

@@ -294,17 +294,27 @@ struct Registers {
 // Whether every SM has one CTA of 64 columns at most: then two groups prepare its chunks.
 inline bool few_states(const Delta& p) { return (int64_t)p.B * p.H * ((p.V + 63) / 64) <= device_sms(); }
 
-// Packed pairs of a strip to rows of memory: token (or state row) r of `n` goes to to + r stride.
-__device__ __forceinline__ void put_strip(uint32_t strip, __nv_bfloat16* to, int64_t stride, int n, int columns) {
-    __syncwarp();
-    const int lane = threadIdx.x % 32, u = lane % 2;
+// A strip's rows on their way to memory: read here, row r of the first n goes to to + r stride. What is between the
+// two hides the reading.
+struct StripRows {
+    uint4 v[4];
+    __device__ __forceinline__ void take(uint32_t strip) {
+        __syncwarp();
+        const int lane = threadIdx.x % 32;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 16 * i + lane / 2;
-        if (r < n && 8 * u < columns) *reinterpret_cast<uint4*>(to + r * stride + 8 * u) = load16(strip_at(strip, r, u));
+        for (int i = 0; i < 4; ++i) v[i] = load16(strip_at(strip, 16 * i + lane / 2, lane % 2));
+        __syncwarp();
     }
-    __syncwarp();
-}
+    __device__ __forceinline__ void give(__nv_bfloat16* to, int64_t stride, int n, int columns) const {
+        const int lane = threadIdx.x % 32, u = lane % 2;
+        __nv_bfloat16* at = to + lane / 2 * stride + 8 * u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (16 * i + lane / 2 < n && 8 * u < columns) *reinterpret_cast<uint4*>(at) = v[i];
+            at += 16 * stride;
+        }
+    }
+};
 
 }  // namespace delta
 }  // namespace block
