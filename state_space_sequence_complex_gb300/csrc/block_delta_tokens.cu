@@ -136,48 +136,145 @@ __device__ __forceinline__ void write4(float* to, const float* v) {
     if ((threadIdx.x & 7) == 0) *reinterpret_cast<float4*>(to + Columns<4>::col()) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
+// Forward. A token waits for the one before, so its way through a warp is what counts: S^T k and S^T q are both taken from
+// the state in front of the token, o = c S^T q + (q.k) u, which leaves one round of sums across lanes, and the next
+// token's keys and queries are on their way to registers meanwhile. Tiles of tokens are copied ahead.
+constexpr int kFwdTile = 16;
+struct FwdTile {
+    float q[kFwdTile][kMaxDim], k[kFwdTile][kMaxDim], v[kFwdTile][kMaxDim];
+};
+struct FwdShared {
+    FwdTile tile[2];
+    float o[kFwdTile][kMaxDim], u[kFwdTile][kMaxDim];
+    float4 gates[kFwdTile];  // c, beta, and what q and k are multiplied by
+    float products[kFwdTile];  // q.k
+};
+
+__device__ __forceinline__ void copy4(float* to, const float* from, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_addr(to)), "l"(from), "r"(valid ? 4 : 0) : "memory");
+}
+
 template <int KR>
-__global__ void __launch_bounds__(256) delta_tokens_fwd(const Delta p) {
-    __shared__ float q[kTile][kMaxDim], k[kTile][kMaxDim], v[kTile][kMaxDim], o[kTile][kMaxDim], u[kTile][kMaxDim];
-    __shared__ float4 gates[kTile];
-    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, g = h / (p.H / p.G);
+__global__ void __launch_bounds__(256) delta_tokens_fwd(const __grid_constant__ Delta p) {
+    extern __shared__ __align__(16) char smem[];
+    FwdShared& sm = *reinterpret_cast<FwdShared*>(smem);
+    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, g = h / (p.H / p.G), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk, seq = (int64_t)b * p.H + h, size = (int64_t)p.K * p.V;
+    const float q_scale = p.normalize ? rsqrtf((float)p.K) : 1.0f;
+    const float *q0 = row<float>(p.q, b, 0, g), *k0 = row<float>(p.k, b, 0, g), *v0 = row<float>(p.v, b, 0, h);
+    const int warps = blockDim.x / 32;
+    auto fetch = [&](int64_t t0) {  // a warp to a token's row at a time
+        FwdTile& to = sm.tile[t0 / kFwdTile & 1];
+        const float *q = q0 + (t0 + warp) * p.q.t + lane, *k = k0 + (t0 + warp) * p.k.t + lane, *v = v0 + (t0 + warp) * p.v.t + lane;
+        const int64_t q_step = warps * p.q.t, k_step = warps * p.k.t, v_step = warps * p.v.t;
+        for (int i = warp; i < kFwdTile; i += warps) {
+            const bool there = t0 + i < p.T;
+#pragma unroll
+            for (int d = 0; d < 8 * KR; d += 32) {
+                copy4(&to.q[i][lane + d], q + d, there && lane + d < p.K);
+                copy4(&to.k[i][lane + d], k + d, there && lane + d < p.K);
+            }
+            for (int d = 0; d < 16 * warps; d += 32) copy4(&to.v[i][lane + d], v + d, there && lane + d < p.V);
+            q += q_step, k += k_step, v += v_step;
+        }
+        ptx::cp_async_commit();
+    };
+    fetch(0);
     Columns<KR> S;
     S.load(p.h0 ? p.h0 + seq * size : nullptr, p.K, p.V);
-    for (int64_t t0 = 0; t0 < p.T; t0 += kTile) {
-        __syncthreads();
-        stage(q, p.q, b, t0, p.T, g, p.K);
-        stage(k, p.k, b, t0, p.T, g, p.K);
-        stage(v, p.v, b, t0, p.T, h, p.V);
-        stage_gates(gates, p, b, t0, p.T, h);
-        __syncthreads();
-        if (p.normalize) {
-            unit(q, rsqrtf((float)p.K));
-            unit(k, 1.0f);
-            __syncthreads();
+    for (int64_t t0 = 0; t0 < p.T; t0 += kFwdTile) {
+        FwdTile& tile = sm.tile[t0 / kFwdTile & 1];
+        ptx::cp_async_wait<0>();
+        __syncthreads();  // this tile is there, and the last one is through
+        if (t0 + kFwdTile < p.T) fetch(t0 + kFwdTile);
+        const int n = (int)min((int64_t)kFwdTile, p.T - t0);
+        // lengths, q.k and gates: eight lanes to a token
+        for (int t = 4 * warp + lane / 8; t - lane / 8 < n; t += 4 * warps) {
+            const int there = min(t, kFwdTile - 1);
+            float qs[KR], ks[KR], qq = 0.0f, kk = 0.0f, qk = 0.0f;
+            Columns<KR>::vec(qs, tile.q[there]);
+            Columns<KR>::vec(ks, tile.k[there]);
+#pragma unroll
+            for (int i = 0; i < KR; ++i) qq = fmaf(qs[i], qs[i], qq), kk = fmaf(ks[i], ks[i], kk), qk = fmaf(qs[i], ks[i], qk);
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) {
+                qq += __shfl_xor_sync(0xffffffffu, qq, o);
+                kk += __shfl_xor_sync(0xffffffffu, kk, o);
+                qk += __shfl_xor_sync(0xffffffffu, qk, o);
+            }
+            if (lane % 8 == 0 && t < n) {
+                const float sq = p.normalize ? q_scale / sqrtf(qq + kUnitEps) : 1.0f, sk = p.normalize ? 1.0f / sqrtf(kk + kUnitEps) : 1.0f;
+                const bool first = p.reset != nullptr && p.reset[b * p.T + t0 + t] != 0;
+                sm.gates[t] = make_float4(first ? 0.0f : gate(*row<float>(p.f, b, t0 + t, h)).x, gate(*row<float>(p.beta, b, t0 + t, h)).x, sq, sk);
+                sm.products[t] = qk * sq * sk;
+            }
         }
+        __syncthreads();
         if (p.states != nullptr && t0 % kDeltaChunk == 0)
             S.store(static_cast<float*>(p.states) + (seq * chunks + t0 / kDeltaChunk) * size, p.K, p.V);
-        const int n = (int)min((int64_t)kTile, p.T - t0);
+        float k[KR], q[KR];
+        S.vec(k, tile.k[0]);
+        S.vec(q, tile.q[0]);
+        float4 gt = sm.gates[0], v = *reinterpret_cast<const float4*>(&tile.v[0][S.col()]);
+        float qk = sm.products[0];
         for (int t = 0; t < n; ++t) {
-            const float4 gt = gates[t];
-            float x[KR], d[4];
-            S.vec(x, k[t]);
-            S.dots(x, d);
+            const int next = min(t + 1, n - 1);
+            float2 dk[2][2], dq[2][2];  // pairs of columns; rows in two sums
+#pragma unroll
+            for (int j = 0; j < 2; ++j) dk[j][0] = dk[j][1] = dq[j][0] = dq[j][1] = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < KR; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 s = make_float2(S.s[i][2 * j], S.s[i][2 * j + 1]);
+                    dk[j][i % 2] = ptx::fma2(s, make_float2(k[i], k[i]), dk[j][i % 2]);
+                    dq[j][i % 2] = ptx::fma2(s, make_float2(q[i], q[i]), dq[j][i % 2]);
+                }
+            S.vec(q, tile.q[next]);
+            float kn[KR];
+            S.vec(kn, tile.k[next]);
+            const float4 next_gt = sm.gates[next], next_v = *reinterpret_cast<const float4*>(&tile.v[next][S.col()]);
+            const float next_qk = sm.products[next];
+            float sums[8];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                sums[2 * j] = dk[j][0].x + dk[j][1].x, sums[2 * j + 1] = dk[j][0].y + dk[j][1].y;
+                sums[4 + 2 * j] = dq[j][0].x + dq[j][1].x, sums[4 + 2 * j + 1] = dq[j][0].y + dq[j][1].y;
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], o);
+            const float vs[4] = {v.x, v.y, v.z, v.w}, keep_k = gt.x * gt.w, keep_q = gt.x * gt.z;
+            float u[4], o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                d[j] = gt.z * fmaf(-gt.x, d[j], v[t][S.col() + j]);
-#pragma unroll
-                for (int i = 0; i < KR; ++i) S.s[i][j] = fmaf(x[i], d[j], gt.x * S.s[i][j]);
+                u[j] = gt.y * fmaf(-keep_k, sums[j], vs[j]);
+                o[j] = fmaf(qk, u[j], keep_q * sums[4 + j]);
             }
-            if (p.updates != nullptr) write4(u[t], d);
-            S.vec(x, q[t]);
-            S.dots(x, d);
-            write4(o[t], d);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float2 ku = make_float2(gt.w * u[2 * j], gt.w * u[2 * j + 1]);
+#pragma unroll
+                for (int i = 0; i < KR; ++i) {
+                    const float2 s = ptx::mul2(make_float2(S.s[i][2 * j], S.s[i][2 * j + 1]), make_float2(gt.x, gt.x));
+                    const float2 r = ptx::fma2(make_float2(k[i], k[i]), ku, s);
+                    S.s[i][2 * j] = r.x, S.s[i][2 * j + 1] = r.y;
+                }
+            }
+            if (p.updates != nullptr) write4(sm.u[t], u);
+            write4(sm.o[t], o);
+#pragma unroll
+            for (int i = 0; i < KR; ++i) k[i] = kn[i];
+            gt = next_gt, v = next_v, qk = next_qk;
         }
         __syncthreads();
-        flush(p.o, o, p, b, t0, p.T, h, p.V);
-        if (p.updates != nullptr) flush(p.updates, u, p, b, t0, p.T, h, p.V);
+        const int64_t at = (b * p.T + t0) * p.H + h;
+        for (int t = warp; t < n; t += blockDim.x / 32)
+            for (int d = lane; d < p.V; d += 32) {
+                static_cast<float*>(p.o)[(at + (int64_t)t * p.H) * p.V + d] = sm.o[t][d];
+                if (p.updates != nullptr) static_cast<float*>(p.updates)[(at + (int64_t)t * p.H) * p.V + d] = sm.u[t][d];
+            }
     }
     S.store(p.h_last + seq * size, p.K, p.V);
 }
@@ -511,7 +608,7 @@ __global__ void __launch_bounds__(256) delta_step(const Delta p) {
     constexpr int RG = 256 / CG;  // groups of rows; thread = group * CG + columns / 4
     launch_dependents();
     grid_dependency_wait();
-    __shared__ float q[kMaxDim], k[kMaxDim], norms[2];
+    __shared__ float q[kMaxDim], k[kMaxDim];
     __shared__ float4 part[8][CG];
     const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, g = h / (p.H / p.G);
     const int c = threadIdx.x % CG, rg = threadIdx.x / CG, col = 4 * c;
@@ -612,7 +709,9 @@ int step_launch(const Delta& p, cudaStream_t stream) {
 
 template <int KR>
 int fwd_launch(const Delta& p, cudaStream_t stream) {
-    delta_tokens_fwd<KR><<<p.B * p.H, 32 * ((p.V + 15) / 16), 0, stream>>>(p);
+    static std::atomic<uint64_t> done{0};
+    if (allow_smem(delta_tokens_fwd<KR>, sizeof(FwdShared), done) != cudaSuccess) return SSDC_ERR_CUDA;
+    delta_tokens_fwd<KR><<<p.B * p.H, 32 * ((p.V + 15) / 16), sizeof(FwdShared), stream>>>(p);
     return 1;
 }
 
