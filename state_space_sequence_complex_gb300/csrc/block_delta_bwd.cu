@@ -30,19 +30,20 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
     const uint32_t base = ptx::smem_addr(smem);
     const int lane = threadIdx.x % 32, all = kPrep + column_threads;
     const int columns = min(16, p.V - col0);
-    const int64_t chunks = (p.T + C - 1) / C, seq = (int64_t)b * p.H + h;
+    const int chunks = (int)((p.T + C - 1) / C);
+    const int64_t seq = (int64_t)b * p.H + h;
     const uint32_t strips = base + L::kStripOff + w * 2 * L::kStrip;
     const Lanes<L::kKeyPitch> key_lanes(base);
     const Lanes<L::kPitch> lanes(base);
     const int fetch_u = lane % 2, fetch_r = lane / 2;
     const bool has_unit = 8 * fetch_u < columns;
-    const __nv_bfloat16* row = bf16(p.d_o.p) + b * p.d_o.b + h * p.d_o.h + ((chunks - 1) * C + fetch_r) * p.d_o.t + col0 + (has_unit ? 8 * fetch_u : 0);
-    auto fetch_do = [&](int64_t n) {  // chunks from the last to the first
-        const int left = (int)min((int64_t)C, p.T - (chunks - 1 - n) * C) - fetch_r;
+    const __nv_bfloat16* row = bf16(p.d_o.p) + b * p.d_o.b + h * p.d_o.h + ((int64_t)(chunks - 1) * C + fetch_r) * p.d_o.t + col0 + (has_unit ? 8 * fetch_u : 0);
+    auto fetch_do = [&](int n) {  // chunks from the last to the first
+        const int left = (int)min((int64_t)C, p.T - (int64_t)(chunks - 1 - n) * C) - fetch_r;
         const __nv_bfloat16* r = row;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            fetch<kUnitRows>(strip_at(strips + (int)(n & 1) * L::kStrip, fetch_r + 16 * i, fetch_u), r, has_unit && 16 * i < left);
+            fetch<kUnitRows>(strip_at(strips + (n & 1) * L::kStrip, fetch_r + 16 * i, fetch_u), r, has_unit && 16 * i < left);
             r += 16 * p.d_o.t;
         }
         ptx::cp_async_commit();
@@ -59,15 +60,16 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
             S[i][e] = p.dh_last != nullptr && r < p.K && cl < columns ? p.dh_last[state + (int64_t)r * p.V + cl] : 0.0f;
         }
     const int64_t z_stride = (int64_t)p.H * p.V, z_step = C * z_stride;
-    __nv_bfloat16* z_rows = static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + (chunks - 1) * C) * p.H + h) * p.V + col0;
-    for (int64_t n = 0; n < chunks; ++n) {
-        const int64_t c = chunks - 1 - n;
-        const int turn = (int)(n & 1), set = (int)(n & (L::kSets - 1)), half = (int)(n % kGroups);
+    __nv_bfloat16* z_rows = static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + (int64_t)(chunks - 1) * C) * p.H + h) * p.V + col0;
+    int stage = 0;
+    for (int n = 0; n < chunks; ++n, stage = L::next_stage(stage, 1)) {
+        const int c = chunks - 1 - n;
+        const int turn = n & 1, set = n & (L::kSets - 1), half = n % kGroups;
         // This chunk's strip has its do, and when that has been read its z. The other one has the last chunk's z,
         // which goes to memory beside the first products; then dS; then the next do.
         const uint32_t mine = strips + turn * L::kStrip, other = strips + (turn ^ 1) * L::kStrip;
-        bar_sync(kBarKeys + (int)(n & 3), all);
-        const uint32_t keys = (int)(n % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
+        bar_sync(kBarKeys + (n & 3), all);
+        const uint32_t keys = stage * L::kStage, queries = keys + L::kKeyTile;
         StripRows rows;
         rows.take(other);
         float X[8][4];
@@ -85,7 +87,7 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
                 mma(X[2 * m], a.lo, kb[0], kb[1]);
                 mma(X[2 * m + 1], a.lo, kb[2], kb[3]);
             }
-            if (s == 0 && n > 0) rows.give(z_rows + z_step, z_stride, n == 1 ? (int)(p.T - (chunks - 1) * C) : C, columns);
+            if (s == 0 && n > 0) rows.give(z_rows + z_step, z_stride, n == 1 ? (int)(p.T - (int64_t)(chunks - 1) * C) : C, columns);
             if (s % 4 == 3) {
                 const int first = s / 4 * C;
                 rows.take(other);
@@ -195,11 +197,11 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
             }
         }
         if (n + kGroups < chunks) bar_arrive(kBarFree + half, all);
-        if (n + 2 * kGroups < chunks) bar_arrive(kBarStage + (int)(n & 3), all);
+        if (n + 2 * kGroups < chunks) bar_arrive(kBarStage + (n & 3), all);
         z_rows -= z_step;
     }
     StripRows rows;
-    rows.take(strips + (int)((chunks - 1) & 1) * L::kStrip);
+    rows.take(strips + ((chunks - 1) & 1) * L::kStrip);
     rows.give(z_rows + z_step, z_stride, chunks == 1 ? (int)p.T : C, columns);
     if (p.dh0 != nullptr) {
 #pragma unroll

@@ -25,19 +25,20 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
     const uint32_t base = ptx::smem_addr(smem);
     const int lane = threadIdx.x % 32, all = kPrep + column_threads;
     const int columns = min(16, p.V - col0);
-    const int64_t chunks = (p.T + C - 1) / C, seq = (int64_t)b * p.H + h;
+    const int chunks = (int)((p.T + C - 1) / C);
+    const int64_t seq = (int64_t)b * p.H + h;
     const uint32_t strips = base + L::kStripOff + w * 2 * L::kStrip;
     const Lanes<L::kKeyPitch> key_lanes(base);
     const Lanes<L::kPitch> lanes(base);
     const int fetch_u = lane % 2, fetch_r = lane / 2;
     const bool has_unit = 8 * fetch_u < columns;
     const __nv_bfloat16* v_row = bf16(p.v.p) + b * p.v.b + h * p.v.h + fetch_r * p.v.t + col0 + (has_unit ? 8 * fetch_u : 0);
-    auto fetch_v = [&](int64_t c) {  // chunks in order
-        const int left = (int)min((int64_t)C, p.T - c * C) - fetch_r;
+    auto fetch_v = [&](int c) {  // chunks in order
+        const int left = (int)min((int64_t)C, p.T - (int64_t)c * C) - fetch_r;
         const __nv_bfloat16* v = v_row;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            fetch<kUnitRows>(strip_at(strips + (int)(c & 1) * L::kStrip, fetch_r + 16 * i, fetch_u), v, has_unit && 16 * i < left);
+            fetch<kUnitRows>(strip_at(strips + (c & 1) * L::kStrip, fetch_r + 16 * i, fetch_u), v, has_unit && 16 * i < left);
             v += 16 * p.v.t;
         }
         ptx::cp_async_commit();
@@ -57,13 +58,14 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
     const int64_t o_stride = (int64_t)p.H * p.V, o_step = C * o_stride, o_first = (b * p.T * p.H + h) * p.V + col0;
     __nv_bfloat16* o_rows = static_cast<__nv_bfloat16*>(p.o) + o_first;
     __nv_bfloat16* u_rows = static_cast<__nv_bfloat16*>(p.updates) + o_first;
-    for (int64_t c = 0; c < chunks; ++c) {
-        const int turn = (int)(c & 1), set = (int)(c & (L::kSets - 1)), half = (int)(c % kGroups);
+    int stage = 0;
+    for (int c = 0; c < chunks; ++c, stage = L::next_stage(stage, 1)) {
+        const int turn = c & 1, set = c & (L::kSets - 1), half = c % kGroups;
         // The strip of this chunk has its v, and when that has been read its u and o. The other one has the last
         // chunk's o, which goes to memory beside the first products; then the state, where it is kept; then the next v.
         const uint32_t mine = strips + turn * L::kStrip, other = strips + (turn ^ 1) * L::kStrip;
-        bar_sync(kBarKeys + (int)(c & 3), all);
-        const uint32_t keys = (int)(c % L::kStages) * L::kStage, queries = keys + L::kKeyTile;
+        bar_sync(kBarKeys + (c & 3), all);
+        const uint32_t keys = stage * L::kStage, queries = keys + L::kKeyTile;
         StripRows rows;
         rows.take(other);
         float X[8][4], O[8][4];
@@ -133,7 +135,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
 #pragma unroll
             for (int i = 0; i < KT; ++i) S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.0f;
         }
-        const int64_t left = p.T - c * C;
+        const int64_t left = p.T - (int64_t)c * C;
         const int n_tokens = left < C ? (int)left : C;
         // Block by block: what a block adds to O and S keeps the instructions coming while the next one, which
         // waits for each of its products, is solved.
@@ -197,7 +199,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
             }
         }
         if (c + kGroups < chunks) bar_arrive(kBarFree + half, all);
-        if (c + 2 * kGroups < chunks) bar_arrive(kBarStage + (int)(c & 3), all);
+        if (c + 2 * kGroups < chunks) bar_arrive(kBarStage + (c & 3), all);
         if (p.updates != nullptr) {
             rows.take(mine);
             rows.give(u_rows, o_stride, n_tokens, columns);
@@ -210,8 +212,8 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
         o_rows += o_step;
     }
     StripRows rows;
-    rows.take(strips + (int)((chunks - 1) & 1) * L::kStrip);
-    rows.give(o_rows - o_step, o_stride, (int)(p.T - (chunks - 1) * C), columns);
+    rows.take(strips + ((chunks - 1) & 1) * L::kStrip);
+    rows.give(o_rows - o_step, o_stride, (int)(p.T - (int64_t)(chunks - 1) * C), columns);
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll

@@ -17,6 +17,7 @@ struct Layout {
     static constexpr int kKeyPitch = KP * 2, kKeyTile = C * kKeyPitch;
     static constexpr int kStage = 2 * kKeyTile;          // k and q
     static constexpr int kStages = kGroups == 2 ? 4 : 3;
+    __host__ __device__ static constexpr int next_stage(int s, int by) { return s + by >= kStages ? s + by - kStages : s + by; }
     static constexpr int kSets = 2 * kGroups;            // of what the tokens of a chunk have
     static constexpr int kStrip = C * 32;                // 64 tokens of 16 columns
     static constexpr int kPitch = C * 2, kSquare = C * kPitch;
@@ -43,7 +44,7 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
     const uint32_t base = ptx::smem_addr(smem);
     const int mine = kGroups == 2 ? threadIdx.x / kPrep : 0;  // group
     const int tid = threadIdx.x % kPrep, warp = tid / 32, lane = tid % 32, g = h / (p.H / p.G), all = kPrep + column_threads;
-    const int64_t chunks = (p.T + C - 1) / C;
+    const int chunks = (int)((p.T + C - 1) / C);
     Token* const tabs = reinterpret_cast<Token*>(smem + L::kTabOff);
     float* const betas_of = reinterpret_cast<float*>(smem + L::kBetaOff);
     float* const scratch = reinterpret_cast<float*>(smem + L::kScratchOff) + (mine * 4 + warp) * 256;
@@ -53,12 +54,14 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
     const bool has_unit = fetch_u * 8 < p.K;
     // chunks are counted in the order they are taken: the n-th has the tokens from first_token(n)
     const int64_t chunk_step = kBack ? -C : C;
-    auto first_token = [&](int64_t n) { return (kBack ? (chunks - 1) * C : 0) + n * chunk_step; };
+    auto first_token = [&](int n) { return (kBack ? (int64_t)(chunks - 1) * C : 0) + n * chunk_step; };
     const int64_t step = kGroups * chunk_step, first = first_token(mine);
     const __nv_bfloat16* k_row = bf16(p.k.p) + b * p.k.b + g * p.k.h + (first + fetch_r) * p.k.t + (has_unit ? fetch_u * 8 : 0);
     const __nv_bfloat16* q_row = bf16(p.q.p) + b * p.q.b + g * p.q.h + (first + fetch_r) * p.q.t + (has_unit ? fetch_u * 8 : 0);
-    auto fetch_keys = [&](int64_t n) {  // in order
-        const uint32_t stage = base + (int)(n % L::kStages) * L::kStage;
+    int stage_of_next = mine;  // counted along: a division takes as long as a product of a block
+    auto fetch_keys = [&](int n) {  // in order
+        const uint32_t stage = base + stage_of_next * L::kStage;
+        stage_of_next = L::next_stage(stage_of_next, kGroups);
         const int left = (int)min((int64_t)C, p.T - first_token(n)) - fetch_r;
         const __nv_bfloat16 *k = k_row, *q = q_row;
 #pragma unroll
@@ -84,7 +87,7 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
     const uint8_t* marks = p.reset != nullptr && lane < 16 ? p.reset + b * p.T + gate_0 : nullptr;
     uint16_t gate;
     uint8_t mark;
-    auto fetch_gates = [&](int64_t n) {  // in order
+    auto fetch_gates = [&](int n) {  // in order
         gate = 0, mark = 0;
         if (first_token(n) + gate_r < p.T) {
             gate = *gates;
@@ -94,8 +97,8 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
         if (marks != nullptr) marks += step;
     };
     // the entries of the warp's tokens of the n-th chunk
-    auto tokens = [&](int64_t n) {
-        const int set = (int)(n & (L::kSets - 1));
+    auto tokens = [&](int n) {
+        const int set = n & (L::kSets - 1);
         const bool there = first_token(n) + gate_r < p.T;
         const float v = __uint_as_float((uint32_t)gate << 16), e = expf(-fabsf(v));
         // log2 of sigmoid(f), not below -256
@@ -119,20 +122,21 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
         fetch_keys(mine);
         tokens(mine);
     }
-    for (int64_t n = mine; n < chunks; n += kGroups) {
-        const int set = (int)(n & (L::kSets - 1));
-        const uint32_t keys = (int)(n % L::kStages) * L::kStage;  // from the start of shared memory, as the lanes' offsets are
+    int stage = mine;
+    for (int n = mine; n < chunks; n += kGroups, stage = L::next_stage(stage, kGroups)) {
+        const int set = n & (L::kSets - 1);
+        const uint32_t keys = stage * L::kStage;  // from the start of shared memory, as the lanes' offsets are
         const Token* tab = tabs + set * C;
         const float* betas = betas_of + set * C;
         if constexpr (kGroups == 1) {
-            if (n >= 2) bar_sync(kBarStage + (int)((n - 2) & 3), all);  // that chunk is through with its stage
+            if (n >= 2) bar_sync(kBarStage + ((n - 2) & 3), all);  // that chunk is through with its stage
             if (n + 1 < chunks) {
                 fetch_gates(n + 1);
                 fetch_keys(n + 1);
             }
         }
         bar_sync(kBarPrep + mine, kPrep);
-        bar_arrive(kBarKeys + (int)(n & 3), all);
+        bar_arrive(kBarKeys + (n & 3), all);
         // pairs of the blocks' entries, rows lane / 4 and 8 more: P, and -A in two parts
         uint32_t P[3][2][2], P2[3][2][2], A[2][2][2], B[2][2][2], T[8];
         float2* lengths = reinterpret_cast<float2*>(smem + L::kLengthOff) + mine * C;
@@ -267,7 +271,7 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
         if (n + kGroups < chunks) {
             if constexpr (kGroups == 2) {
                 fetch_gates(n + 2);
-                if (n >= 2) bar_sync(kBarStage + (int)((n - 2) & 3), all);
+                if (n >= 2) bar_sync(kBarStage + ((n - 2) & 3), all);
                 fetch_keys(n + 2);
             }
             tokens(n + kGroups);
