@@ -221,10 +221,10 @@ __global__ void __launch_bounds__(kGroups * kPrep + 32 * NW, KP == 64 && NW == 4
     const int b = item / p.H, h = item % p.H;
     const int warps = min(NW, (p.V - col0 + 15) / 16);
     if (threadIdx.x < kGroups * kPrep) {
-        Registers<KP, NW, kGroups>::prepare();
+        Registers<KP, NW, true, kGroups>::prepare();
         prepare_chunks<KP, NW, true, kGroups, kUnitRows>(p, smem, b, h, 32 * warps);
     } else {
-        Registers<KP, NW, kGroups>::walk();
+        Registers<KP, NW, true, kGroups>::walk();
         const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
         if (w < warps) walk_back<KP, NW, kGroups, kUnitRows>(p, smem, b, h, w, col0 + 16 * w, 32 * warps);
     }
@@ -247,7 +247,7 @@ struct Small {
     float2 lengths[C];                 // rk, rq
     float into[C], out_of[C], beta_rest[C], rest[C];  // Gam, gam, exp(-b), 1 - a
     float columns[4][C], rows[C], diagonal[C], front[2][C], behind[2][C];
-    float both[8], gam;
+    float both[8], gam, apart[4][4];   // apart[i][j]: the decay across the whole groups between groups i and j
 };
 
 // `rows` rows of a tile, a unit of 16 bytes to a thread at a time, zeros from row `have` and column n on.
@@ -331,6 +331,13 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
             sm.into[tid] = into;
             sm.out_of[tid] = decay(whole - mine);
             if (tid == C - 1) sm.gam = into;
+            if (tid < 16) {
+                long long s = 0;
+#pragma unroll
+                for (int m = 1; m < 3; ++m)
+                    if (tid / 4 < m && m < tid % 4) s += sm.tab[16 * m + 15].sum;
+                sm.apart[tid / 4][tid % 4] = decay(s);
+            }
         }
         if (r == 0 && tid < 2 * C) {
             const float n = p.normalize ? rsqrtf(row_square<L::kKeyPitch>(base + (tid < C ? L::kK : L::kQ), tid % C) + kUnitEps) : 1.0f;
@@ -443,9 +450,7 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
             }
             float in0 = 1.0f, in1 = 1.0f;
             if (n < w) {
-                long long far = 0;
-                for (int m = n + 1; m < w; ++m) far += sm.tab[16 * m + 15].sum;
-                const float apart = decay(far);
+                const float apart = sm.apart[n][w];
                 in0 = apart * i0.in, in1 = apart * i1.in;
             }
             uint32_t a1[4], a2[4], m1[4], m2[4];

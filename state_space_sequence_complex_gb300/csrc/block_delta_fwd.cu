@@ -230,10 +230,10 @@ __global__ void __launch_bounds__(kGroups * kPrep + 32 * NW, KP == 64 && NW == 4
     const int b = item / p.H, h = item % p.H;
     const int warps = min(NW, (p.V - col0 + 15) / 16);  // that have columns
     if (threadIdx.x < kGroups * kPrep) {
-        Registers<KP, NW, kGroups>::prepare();
+        Registers<KP, NW, false, kGroups>::prepare();
         prepare_chunks<KP, NW, false, kGroups, kUnitRows>(p, smem, b, h, 32 * warps);
     } else {
-        Registers<KP, NW, kGroups>::walk();
+        Registers<KP, NW, false, kGroups>::walk();
         const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
         if (w < warps) walk<KP, NW, kGroups, kUnitRows>(p, smem, b, h, w, col0 + 16 * w, 32 * warps);
     }

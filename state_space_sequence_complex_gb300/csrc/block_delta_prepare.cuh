@@ -280,11 +280,13 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
 }
 
 // A CTA's registers: fewer to the warps that prepare, more to those with columns, within what it was launched with (128
-// to a thread where two CTAs share an SM, 168 with 12 warps).
-template <int KP, int NW, int kGroups>
+// to a thread where two CTAs share an SM, 168 with 12 warps). Spilled registers cost the most where two CTAs share an SM:
+// 112 and 144 against 96 and 160 took the forward pass of 256 states from 202 to 194 us, 104 and 152 the backward
+// one from 217 to 189.
+template <int KP, int NW, bool kBack, int kGroups>
 struct Registers {
-    static constexpr int kPrepare = kGroups == 2 ? 120 : NW == 8 ? 104 : 96;
-    static constexpr int kWalk = kGroups == 2 ? 232 : NW == 8 ? 200 : 160;
+    static constexpr int kPrepare = kGroups == 2 ? 136 : NW == 8 || kBack ? 104 : 112;
+    static constexpr int kWalk = kGroups == 2 ? 232 : NW == 8 ? 200 : kBack ? 152 : 144;
     static constexpr bool kSplit = KP == 64 || NW == 8 || kGroups == 2;  // else 255 to every thread
     static_assert(!kSplit || kGroups * 4 * kPrepare + NW * kWalk <= (kGroups * 4 + NW) * (kGroups * 4 + NW == 8 ? 128 : 168), "");
     __device__ __forceinline__ static void prepare() {
