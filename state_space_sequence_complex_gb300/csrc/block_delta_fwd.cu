@@ -69,26 +69,32 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
         StripRows rows;
         rows.take(other);
         float X[8][4], O[8][4];
+        Split a;
+        uint32_t kb[2][4], qb[2][4];  // the next products' operands are read before this one's are used
+        ldsm(kb[0], keys + key_lanes.down[0]);
+        ldsm(qb[0], queries + key_lanes.down[0]);
 #pragma unroll
-        for (int s = 0; s < KP / 16; ++s) {
-            Split a;
-            a.set(S[2 * s], S[2 * s + 1]);
-            if (p.states != nullptr) stsm_t(strip_rows(other, 16 * s % C), a.hi[0], a.hi[1], a.hi[2], a.hi[3]);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                uint32_t kb[4], qb[4];
-                ldsm(kb, keys + 16 * n * L::kKeyPitch + key_lanes.down[s]);
-                ldsm(qb, queries + 16 * n * L::kKeyPitch + key_lanes.down[s]);
-                mma_at(s, X[2 * n], a.hi, kb[0], kb[1]);
-                mma_at(s, X[2 * n + 1], a.hi, kb[2], kb[3]);
-                mma_at(s, O[2 * n], a.hi, qb[0], qb[1]);
-                mma_at(s, O[2 * n + 1], a.hi, qb[2], qb[3]);
-                mma(X[2 * n], a.lo, kb[0], kb[1]);
-                mma(X[2 * n + 1], a.lo, kb[2], kb[3]);
+        for (int it = 0; it < KP / 4; ++it) {
+            const int s = it / 4, n = it % 4, now = it % 2;
+            if (n == 0) {
+                a.set(S[2 * s], S[2 * s + 1]);
+                if (p.states != nullptr) stsm_t(strip_rows(other, 16 * s % C), a.hi[0], a.hi[1], a.hi[2], a.hi[3]);
             }
-            if (s == 0 && c > 0) rows.give(o_rows - o_step, o_stride, C, columns);
-            if (p.states != nullptr && s % 4 == 3) {
-                const int first = s / 4 * C;
+            if (it + 1 < KP / 4) {
+                const int s1 = (it + 1) / 4, n1 = (it + 1) % 4;
+                ldsm(kb[1 - now], keys + 16 * n1 * L::kKeyPitch + key_lanes.down[s1]);
+                ldsm(qb[1 - now], queries + 16 * n1 * L::kKeyPitch + key_lanes.down[s1]);
+            }
+            const uint32_t *k = kb[now], *q = qb[now];
+            mma_at(s, X[2 * n], a.hi, k[0], k[1]);
+            mma_at(s, X[2 * n + 1], a.hi, k[2], k[3]);
+            mma_at(s, O[2 * n], a.hi, q[0], q[1]);
+            mma_at(s, O[2 * n + 1], a.hi, q[2], q[3]);
+            mma(X[2 * n], a.lo, k[0], k[1]);
+            mma(X[2 * n + 1], a.lo, k[2], k[3]);
+            if (it == 3 && c > 0) rows.give(o_rows - o_step, o_stride, C, columns);
+            if (p.states != nullptr && it % 16 == 15) {
+                const int first = it / 16 * C;
                 rows.take(other);
                 rows.give(static_cast<__nv_bfloat16*>(p.states) + (seq * chunks + c) * p.K * p.V + (int64_t)first * p.V + col0, p.V,
                           p.K - first, columns);
