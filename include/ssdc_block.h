@@ -234,6 +234,9 @@ int ssd_fp8_matmul(ssd_rows_in a, const float *a_scale, ssd_rows_in b, const flo
  * outside the span of every input. Outputs, states and updates are 16-byte aligned.
  * K and V are multiples of 8 up to 128, G divides H.
  *
+ * Nothing passes a reset, an infinity or a NaN neither, with F32, and with BF16 where the reset is at a multiple of
+ * 64 tokens; elsewhere one of BF16 reaches the other documents that share a chunk of 64 tokens with its own.
+ *
  * BF16: chunks of 64 tokens on the tensor cores, products with operands in one or two bf16
  * parts and fp32 sums; states are within 1e-5 of exact ones (relative to their norm)
  * where |k|^2 beta <= 2, which normalised keys always meet: beyond that the recurrence itself grows
@@ -336,11 +339,11 @@ int ssd_gated_norm_bwd(ssd_rows_in dy, ssd_rows_in x, ssd_rows_in z, const float
 #define SSD_CALL_FP8_QUANTIZE 5        /* 12 words */
 #define SSD_CALL_FP8_MATMUL 6          /* 15 words */
 #define SSD_CALL_GATED_SCAN_FWD_WS 7   /* 23 words */
-#define SSD_CALL_DELTA_RULE_FWD 8      /* 34 words */
-#define SSD_CALL_DELTA_RULE_STEP 9     /* 31 words */
-#define SSD_CALL_DELTA_RULE_BWD 10     /* 40 words */
-#define SSD_CALL_GATED_NORM_FWD 11     /* 17 words */
-#define SSD_CALL_GATED_NORM_BWD 12     /* 25 words */
+#define SSD_CALL_DELTA_RULE_FWD 9      /* 34 words */
+#define SSD_CALL_DELTA_RULE_STEP 10    /* 31 words */
+#define SSD_CALL_DELTA_RULE_BWD 11     /* 40 words */
+#define SSD_CALL_GATED_NORM_FWD 12     /* 17 words */
+#define SSD_CALL_GATED_NORM_BWD 13     /* 25 words */
 int ssd_block_call(int32_t call, const int64_t *words, cudaStream_t stream);
 
 #ifdef __cplusplus

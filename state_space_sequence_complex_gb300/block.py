@@ -594,7 +594,7 @@ class DeltaRule:
         self._marks = torch.uint8, torch.Size((B, T)), index
         self._out = (self.o.data_ptr(), self.h_last.data_ptr(),
                      *((self.states.data_ptr(), self.updates.data_ptr()) if keep else (0, 0)))
-        self._call = _Call("ssd_delta_rule_fwd", 8, 34, index)
+        self._call = _Call("ssd_delta_rule_fwd", 9, 34, index)
 
     def __call__(self, q, k, v, f, b, h0=None, reset=None, stream=None):
         self._call(stream, *_heads("q", q, self._qk), *_heads("k", k, self._qk), *_heads("v", v, self._v),
@@ -623,7 +623,7 @@ class DeltaRuleBackward:
         self._states = self.dtype, torch.Size((B, heads, -(-T // STATE_TOKENS), K, V)), index
         self._marks = torch.uint8, torch.Size((B, T)), index
         self._out = (*(g[n].data_ptr() for n in ("dq", "dk", "dv", "df", "db", "dh0")), self.workspace.data_ptr(), nbytes)
-        self._call = _Call("ssd_delta_rule_bwd", 10, 40, index)
+        self._call = _Call("ssd_delta_rule_bwd", 11, 40, index)
 
     def __call__(self, q, k, f, b, states, updates, do, dh_last=None, reset=None, stream=None):
         self._call(stream, *_heads("q", q, self._qk), *_heads("k", k, self._qk), *_gate("f", f, self._fb),
@@ -647,7 +647,7 @@ class DeltaRuleStep:
         self._qk, self._v = (self.dtype, torch.Size((B, key_heads, K)), index), (self.dtype, self.o.shape, index)
         self._fb, self._state = (self.dtype, torch.Size((B, heads)), index), (torch.float32, self.state.shape, index)
         self._rest, self._own = (*self._dims, self.o.data_ptr()), self.state.data_ptr()
-        self._call = _Call("ssd_delta_rule_step", 9, 31, index)
+        self._call = _Call("ssd_delta_rule_step", 10, 31, index)
 
     def __call__(self, q, k, v, f, b, state, state_out=None, stream=None):
         to = self._own if state_out is None else _dense("state_out", state_out, self._state)
@@ -711,7 +711,7 @@ class GatedNorm:
         self._rest = (_float_bits(self.eps), M, heads, D, self.type, _TYPES[out], self.y.data_ptr(), self.y.stride(0),
                       0 if self.scale is None else self.scale.data_ptr())
         self._result = self.y if self.scale is None else (self.y, self.scale)
-        self._call = _Call("ssd_gated_norm_fwd", 11, 17, index)
+        self._call = _Call("ssd_gated_norm_fwd", 12, 17, index)
 
     def __call__(self, x, z, w=None, v=None, s=None, stream=None):
         if (v is not None) != self.skip or (s is not None) != self.skip:
@@ -745,7 +745,7 @@ class GatedNormBackward:
         self._dims = (_float_bits(self.eps), M, heads, D, self.type)
         self._out = (*_rows("dx", g["dx"], self._like), *_rows("dz", g["dz"], self._like), *_rows("dv", g.get("dv"), self._like),
                      g["dw"].data_ptr(), g["ds"].data_ptr() if skip else 0, self.workspace.data_ptr(), nbytes)
-        self._call = _Call("ssd_gated_norm_bwd", 12, 25, index)
+        self._call = _Call("ssd_gated_norm_bwd", 13, 25, index)
 
     def __call__(self, dy, x, z, w=None, v=None, s=None, stream=None):
         if (v is not None) != self.skip or (s is not None) != self.skip:

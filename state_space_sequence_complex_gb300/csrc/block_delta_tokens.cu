@@ -73,6 +73,10 @@ struct Columns {  // a lane's part of a warp's 16 columns: rows 32 (i / 4) + 4 (
     float s[KR][4];
     __device__ __forceinline__ static int row(int i) { return (i / 4) * 32 + (threadIdx.x & 7) * 4 + i % 4; }
     __device__ __forceinline__ static int col() { return (threadIdx.x / 32) * 16 + ((threadIdx.x >> 3) & 3) * 4; }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < KR; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+    }
     __device__ __forceinline__ void load(const float* p, int K, int V) {
 #pragma unroll
         for (int i = 0; i < KR; ++i)
@@ -245,6 +249,11 @@ __global__ void __launch_bounds__(256) delta_tokens_fwd(const __grid_constant__ 
             for (int o = 1; o < 8; o *= 2)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], o);
+            if (gt.x == 0.0f) {  // the state ends here, whatever it holds
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sums[j] = 0.0f;
+                S.clear();
+            }
             const float vs[4] = {v.x, v.y, v.z, v.w}, keep_k = gt.x * gt.w, keep_q = gt.x * gt.z;
             float u[4], o[4];
 #pragma unroll
@@ -353,6 +362,7 @@ __global__ void __launch_bounds__(256) delta_tokens_bwd_reverse(const Delta p) {
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < KR; ++i) dS.s[i][j] = gt.x * fmaf(-x[i], d[j], dS.s[i][j]);
+            if (gt.x == 0.0f) dS.clear();  // nothing is owed to the tokens before, whatever the later ones hold
         }
         __syncthreads();
         flush(p.dv, z, p, b, t0, p.T, h, p.V);
@@ -405,6 +415,7 @@ __global__ void __launch_bounds__(256) delta_tokens_bwd_forward(const Delta p) {
             float x[KR], y[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[j] = -gt.x * z[t][S.col() + j];
+            if (gt.x == 0.0f) S.clear();
             S.sums(y, sums + (warp * kTile + t) * kMaxDim);
             S.vec(x, k[t]);
 #pragma unroll

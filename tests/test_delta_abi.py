@@ -1,0 +1,204 @@
+"""Host-only checks of the delta rule and the gated norm: the arguments that each entry point refuses before anything
+reaches a GPU. Every call here fails a host check, so the addresses are never used."""
+import ctypes
+
+import pytest
+
+from state_space_sequence_complex_gb300 import block, ssdc
+
+INVALID, UNSUPPORTED, ALIGN, WORKSPACE = (ssdc.SSDC_ERR_INVALID, ssdc.SSDC_ERR_UNSUPPORTED, ssdc.SSDC_ERR_ALIGN,
+                                          ssdc.SSDC_ERR_WORKSPACE)
+BASE = 1 << 40
+
+
+def at(k):
+    """Addresses 64 GB apart."""
+    return BASE + (k << 36)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from state_space_sequence_complex_gb300 import build
+    build.build()
+    return block.load()
+
+
+HEADS = lambda p, h=2, d=64, T=100: block.ssd_heads(p, T * h * d, h * d, d)
+DIMS = dict(B=2, T=100, H=4, G=2, K=64, V=32, type=1, normalize=1)
+
+
+def dims(**k):
+    d = {**DIMS, **k}
+    return block.ssd_delta_dims(*(d[n] for n in ("B", "T", "H", "G", "K", "V", "type", "normalize")))
+
+
+def fwd(lib, **k):
+    a = dict(q=HEADS(at(1)), k=HEADS(at(2)), v=HEADS(at(3), 4, 32), f=HEADS(at(4), 4, 1), b=HEADS(at(5), 4, 1), h0=at(6), reset=at(7),
+             o=at(8), h_last=at(9), states=at(10), updates=at(11), **DIMS)
+    a.update(k)
+    return lib.ssd_delta_rule_fwd(a["q"], a["k"], a["v"], a["f"], a["b"], a["h0"], a["reset"], dims(**{n: a[n] for n in DIMS}),
+                                  a["o"], a["h_last"], a["states"], a["updates"], None)
+
+
+BAD_DIMS = [
+    (dict(B=0), INVALID), (dict(T=0), INVALID), (dict(H=0), INVALID), (dict(G=0), INVALID), (dict(K=0), INVALID), (dict(V=-8), INVALID),
+    (dict(type=2), INVALID), (dict(type=-1), INVALID), (dict(normalize=2), INVALID), (dict(G=3), INVALID), (dict(G=8), INVALID),
+    (dict(K=60), UNSUPPORTED), (dict(V=36), UNSUPPORTED), (dict(K=136), UNSUPPORTED), (dict(V=256), UNSUPPORTED),
+    (dict(B=(1 << 20) + 1), UNSUPPORTED), (dict(B=1 << 19, H=4), UNSUPPORTED), (dict(T=(1 << 31) - 1), UNSUPPORTED),
+    (dict(B=1 << 10, T=1 << 30), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("change,want", BAD_DIMS)
+def test_dims_refused(lib, change, want):
+    assert fwd(lib, **change) == want
+    assert lib.ssd_delta_rule_bwd_workspace_bytes(dims(**change)) == 0
+    assert bwd(lib, **change) == want
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(q=HEADS(None)), INVALID), (dict(k=HEADS(None)), INVALID), (dict(v=HEADS(None)), INVALID), (dict(f=HEADS(None)), INVALID),
+    (dict(b=HEADS(None)), INVALID), (dict(o=None), INVALID), (dict(h_last=None), INVALID),
+    (dict(states=None), INVALID), (dict(updates=None), INVALID),               # one without the other
+    (dict(q=HEADS(at(1) + 1)), ALIGN), (dict(o=at(8) + 8), ALIGN), (dict(h0=at(6) + 4), ALIGN), (dict(h_last=at(9) + 8), ALIGN),
+    (dict(states=at(10) + 2), ALIGN), (dict(updates=at(11) + 8), ALIGN),
+    (dict(q=block.ssd_heads(at(1), -1, 64, 64)), INVALID), (dict(k=block.ssd_heads(at(2), 64, -64, 64)), INVALID),
+    (dict(v=block.ssd_heads(at(3), 64, 64, -1)), INVALID), (dict(v=block.ssd_heads(at(3), 1 << 41, 64, 64)), INVALID),
+    (dict(v=block.ssd_heads(at(3), 1 << 40, 1 << 34, 1)), INVALID),
+    (dict(o=at(3)), INVALID), (dict(o=at(1) + 16), INVALID), (dict(h_last=at(6) + 16), INVALID), (dict(h_last=at(8)), INVALID),
+    (dict(states=at(9)), INVALID), (dict(updates=at(8)), INVALID), (dict(updates=at(7)), INVALID),
+    # between the rows of a wider input: inside its span
+    (dict(v=block.ssd_heads(at(3), 100 * 512, 512, 32), o=at(3) + 512), INVALID)])
+def test_forward_refuses(lib, change, want):
+    assert fwd(lib, **change) == want
+
+
+def bwd(lib, **k):
+    a = dict(q=HEADS(at(1)), k=HEADS(at(2)), f=HEADS(at(3), 4, 1), b=HEADS(at(4), 4, 1), states=at(5), updates=at(6), reset=None,
+             do=HEADS(at(7), 4, 32), dh_last=at(8), dq=at(9), dk=at(10), dv=at(11), df=at(12), db=at(13), dh0=at(14), ws=at(15),
+             ws_bytes=1 << 34, **DIMS)
+    a.update(k)
+    return lib.ssd_delta_rule_bwd(a["q"], a["k"], a["f"], a["b"], a["states"], a["updates"], a["reset"], a["do"], a["dh_last"],
+                                  dims(**{n: a[n] for n in DIMS}), a["dq"], a["dk"], a["dv"], a["df"], a["db"], a["dh0"], a["ws"],
+                                  a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(ws=None), WORKSPACE), (dict(ws=at(15) + 128), WORKSPACE), (dict(ws_bytes=16), WORKSPACE), (dict(states=None), INVALID),
+    (dict(updates=None), INVALID), (dict(do=HEADS(None)), INVALID), (dict(dq=None), INVALID), (dict(dk=None), INVALID),
+    (dict(dv=None), INVALID), (dict(df=None), INVALID), (dict(db=None), INVALID), (dict(dq=at(1)), INVALID), (dict(dk=at(9)), INVALID),
+    (dict(dv=at(7)), INVALID), (dict(dv=at(6)), INVALID), (dict(df=at(3)), INVALID), (dict(dh0=at(8) + 16), INVALID),
+    (dict(dh0=at(5)), INVALID), (dict(ws=at(5)), INVALID), (dict(dq=at(9) + 8), ALIGN), (dict(states=at(5) + 4), ALIGN)])
+def test_backward_refuses(lib, change, want):
+    assert bwd(lib, **change) == want
+
+
+def test_workspace_sizes(lib):
+    size = lib.ssd_delta_rule_bwd_workspace_bytes
+    assert size(dims()) == 2 * 4 * 2 * 64 * 32 * 2           # the states' gradients, two chunks, in bfloat16
+    assert size(dims(type=0)) > 2 * 2 * 100 * 4 * 64 * 4     # fp32: gradients of q and k for each value head too
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(T=2), INVALID), (dict(state=None), INVALID), (dict(out=None), INVALID), (dict(out=at(6) + 16), INVALID), (dict(o=at(6)), INVALID),
+    (dict(state=at(6) + 4), ALIGN), (dict(K=20), UNSUPPORTED)])
+def test_step_refuses(lib, change, want):
+    a = dict(state=at(6), out=at(7), o=at(8), T=1, K=64)
+    a.update(change)
+    h = lambda p, n, d: block.ssd_heads(p, n * d, 0, d)
+    assert lib.ssd_delta_rule_step(h(at(1), 2, 64), h(at(2), 2, 64), h(at(3), 4, 32), h(at(4), 4, 1), h(at(5), 4, 1), a["state"],
+                                   dims(T=a["T"], K=a["K"]), a["o"], a["out"], None) == want
+
+
+ROWS = lambda p, ld=256: block.ssd_rows(p, ld)
+
+
+def norm(lib, **k):
+    a = dict(x=ROWS(at(1)), z=ROWS(at(2)), w=at(3), v=ROWS(at(4)), s=at(5), eps=1e-5, M=10, H=4, D=64, type=1, out=2, y=ROWS(at(6)), scale=at(7))
+    a.update(k)
+    return lib.ssd_gated_norm_fwd(a["x"], a["z"], a["w"], a["v"], a["s"], a["eps"], a["M"], a["H"], a["D"], a["type"], a["out"],
+                                  a["y"], a["scale"], None)
+
+
+BAD_SIZES = [(dict(M=0), INVALID), (dict(H=0), INVALID), (dict(D=-8), INVALID), (dict(type=2), INVALID), (dict(D=12), UNSUPPORTED),
+             (dict(D=264), UNSUPPORTED), (dict(H=600), UNSUPPORTED), (dict(M=1 << 31), UNSUPPORTED), (dict(H=1 << 40), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("change,want", BAD_SIZES + [
+    (dict(out=3), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(x=ROWS(None)), INVALID),
+    (dict(z=ROWS(None)), INVALID), (dict(y=ROWS(None)), INVALID), (dict(s=None), INVALID), (dict(v=ROWS(None)), INVALID),
+    (dict(scale=None), INVALID), (dict(out=1), INVALID), (dict(y=ROWS(at(6), 255)), INVALID), (dict(y=ROWS(at(6), 264)), ALIGN),
+    (dict(y=ROWS(at(6) + 8)), ALIGN), (dict(x=ROWS(at(1) + 1)), ALIGN), (dict(w=at(3) + 2), ALIGN), (dict(y=ROWS(at(1))), INVALID),
+    (dict(scale=at(5)), INVALID), (dict(x=ROWS(at(1), -1)), INVALID),
+    (dict(out=1, scale=None, y=ROWS(at(1), 512)), INVALID), (dict(out=1, scale=None, y=ROWS(at(1) + 2)), INVALID)])
+def test_norm_refuses(lib, change, want):
+    assert norm(lib, **change) == want
+
+
+def norm_bwd(lib, **k):
+    a = dict(dy=ROWS(at(1)), x=ROWS(at(2)), z=ROWS(at(3)), w=at(4), v=ROWS(at(5)), s=at(6), eps=1e-5, M=10, H=4, D=64, type=1, dx=ROWS(at(7)),
+             dz=ROWS(at(8)), dv=ROWS(at(9)), dw=at(10), ds=at(11), ws=at(12), ws_bytes=1 << 30)
+    a.update(k)
+    return lib.ssd_gated_norm_bwd(*(a[n] for n in ("dy", "x", "z", "w", "v", "s", "eps", "M", "H", "D", "type", "dx", "dz", "dv", "dw", "ds",
+                                                   "ws", "ws_bytes")), None)
+
+
+@pytest.mark.parametrize("change,want", BAD_SIZES + [
+    (dict(ws=None), WORKSPACE), (dict(ws=at(12) + 64), WORKSPACE), (dict(ws_bytes=64), WORKSPACE), (dict(eps=-1.0), INVALID),
+    (dict(dy=ROWS(None)), INVALID), (dict(dx=ROWS(None)), INVALID), (dict(dz=ROWS(None)), INVALID), (dict(dv=ROWS(None)), INVALID),
+    (dict(ds=None), INVALID), (dict(s=None), INVALID), (dict(dx=ROWS(at(1))), INVALID), (dict(dz=ROWS(at(7))), INVALID),
+    (dict(dw=at(4)), INVALID), (dict(ds=at(10)), INVALID), (dict(dx=ROWS(at(7), 255)), INVALID)])
+def test_norm_backward_refuses(lib, change, want):
+    assert norm_bwd(lib, **change) == want
+    if "M" in change or "H" in change or "D" in change:
+        assert lib.ssd_gated_norm_bwd_workspace_bytes(*(change.get(n, d) for n, d in (("M", 10), ("H", 4), ("D", 64)))) == 0
+
+
+@pytest.mark.parametrize("call,words", [(9, 34), (10, 31), (11, 40), (12, 17), (13, 25)])
+def test_word_block_calls_refuse_what_the_calls_refuse(lib, call, words):
+    none = (ctypes.c_int64 * words)()      # null addresses, zero sizes
+    assert lib.ssd_block_call(call, none, None) == INVALID
+    assert lib.ssd_block_call(call, None, None) == INVALID
+
+
+def test_strides_never_taken_are_not_checked(lib):
+    """Of a single row, token or head: each call still fails, but by its last check."""
+    one = dict(B=1, T=1, H=1, G=1)
+    odd = lambda p: block.ssd_heads(p, -5, 1 << 50, -1)
+    assert fwd(lib, **one, q=odd(at(1)), k=odd(at(2)), v=odd(at(3)), f=odd(at(4)), b=odd(at(5)), updates=at(10)) == INVALID
+    assert fwd(lib, **one, q=odd(at(1)), k=odd(at(2)), v=odd(at(3)), f=odd(at(4)), b=odd(at(5)), updates=at(11) + 8) == ALIGN
+
+
+def test_plans_refuse(lib):
+    for make in (lambda: block.DeltaRule(0, 4, 2, 8, 8, device="cpu"), lambda: block.DeltaRule(1, 4, 3, 8, 8, key_heads=2, device="cpu"),
+                 lambda: block.DeltaRule(1, 4, 2, 8, 8, "fp16", device="cpu"), lambda: block.DeltaRuleStep(1, 2, -8, 8, device="cpu"),
+                 lambda: block.DeltaRuleBackward(1, 0, 2, 8, 8, device="cpu"), lambda: block.GatedNorm(4, 0, 8, device="cpu"),
+                 lambda: block.GatedNorm(4, 2, 8, out="int8", device="cpu"), lambda: block.GatedNormBackward(4, 2, 8, "fp8", device="cpu")):
+        with pytest.raises(ValueError):
+            make()
+    for make in (lambda: block.DeltaRule(1, 4, 2, 12, 8, device="cpu"), lambda: block.DeltaRuleStep(1, 2, 8, 136, device="cpu"),
+                 lambda: block.GatedNorm(4, 2, 12, device="cpu"), lambda: block.GatedNormBackward(4, 200, 256, device="cpu")):
+        with pytest.raises(ssdc.SSDCError):
+            make()
+
+
+def test_calls_check_their_tensors(lib):
+    import torch
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    rule = block.DeltaRule(2, 3, 4, 16, 8, key_heads=2, device="cpu")
+    q, v, f = bf(2, 3, 2, 16), bf(2, 3, 4, 8), bf(2, 3, 4)
+    with pytest.raises(TypeError, match="q must be"):
+        rule(q.float(), q, v, f, f)
+    with pytest.raises(ValueError, match="k must have shape"):
+        rule(q, bf(2, 3, 4, 16), v, f, f)
+    with pytest.raises(ValueError, match="contiguous features"):
+        rule(q, q, bf(2, 3, 8, 4).transpose(2, 3), f, f)
+    with pytest.raises(ValueError, match="h0 must be contiguous"):
+        rule(q, q, v, f, f, h0=torch.zeros(2, 4, 16, 16)[..., ::2])
+    with pytest.raises(TypeError, match="reset"):
+        rule(q, q, v, f, f, reset=torch.zeros(2, 3))
+    step = block.DeltaRuleStep(2, 4, 16, 8, device="cpu")
+    with pytest.raises(ValueError, match="state"):
+        step(bf(2, 4, 16), bf(2, 4, 16), bf(2, 4, 8), bf(2, 4), bf(2, 4), torch.zeros(2, 4, 8, 16))
+    norm_ = block.GatedNorm(4, 2, 8, device="cpu")
+    with pytest.raises(ValueError, match="w must have"):
+        norm_(bf(4, 16), bf(4, 16), torch.zeros(8))

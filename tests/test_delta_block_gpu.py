@@ -1,0 +1,236 @@
+"""The delta rule and the gated norm at the sizes where another kernel is taken, in guarded arrays, and one after
+another as a layer has them. Tolerances as in test_delta_gpu and test_gated_norm_gpu."""
+import pytest
+import torch
+
+from state_space_sequence_complex_gb300 import block
+from tests.test_delta_gpu import DT, NAMES, check, close, cuda, make, randn, reference, run, sizes
+
+pytestmark = pytest.mark.gpu
+GUARD = 7.25
+
+# more states than SMs, as many CTAs as SMs, and fewer, for every padded size of K and V
+MANY = [(20, 130, 8, 4, 64, 64), (10, 130, 8, 8, 64, 128), (20, 70, 8, 8, 128, 64), (10, 129, 8, 4, 128, 128), (40, 65, 4, 2, 24, 40),
+        (20, 200, 8, 8, 40, 72), (22, 66, 8, 8, 104, 16), (19, 64, 8, 8, 64, 64), (19, 193, 8, 1, 64, 64), (1, 700, 3, 3, 64, 64),
+        (1, 700, 2, 1, 128, 128)]
+
+
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("docs", [0.0, 0.03])
+def test_many_and_few_states(shape, docs):
+    check(make(*shape, docs=docs, seed=sum(shape)), "bf16")
+
+
+@pytest.mark.parametrize("shape", MANY[:5] + MANY[-2:], ids=lambda s: "x".join(map(str, s)))
+def test_rows_that_start_anywhere(shape):
+    """Rows of one projection that start two bytes past a unit of 16, and have no whole number of them."""
+    B, T, H, G, K, V = shape
+    wide = randn(B, T, 2 * G * K + 2 * H * V + 2 * H + 3, seed=3, dtype=torch.bfloat16).cuda()
+    y, at = cuda(make(*shape, seed=4)), 1
+    for n, h, d in (("q", G, K), ("k", G, K), ("v", H, V), ("do", H, V)):
+        y[n] = wide[..., at:at + h * d].unflatten(-1, (h, d))
+        at += h * d
+    y["f"], y["b"] = wide[..., at:at + H], wide[..., at + H:at + 2 * H]
+    want, got = reference({n: None if t is None else t.cpu() for n, t in y.items()}), run(y, "bf16")
+    for n in want:
+        close(got[n], want[n], n, "bf16")
+
+
+def guarded(*shape, dtype):
+    """A dense array with 64 guard values behind it, and the guard."""
+    n = 1
+    for k in shape:
+        n *= k
+    store = torch.full((n + 64,), GUARD, device="cuda", dtype=dtype)
+    return store[:n].view(*shape), store[n:]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", [(2, 70, 3, 1, 40, 24), (20, 65, 8, 8, 64, 64), (1, 1, 1, 1, 8, 8), (2, 129, 2, 2, 128, 120)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_nothing_is_written_behind_an_output(shape, dtype):
+    B, T, H, G, K, V = shape
+    dt, lib, st = DT[dtype], block.load(), torch.cuda.current_stream().cuda_stream
+    x = make(*shape, dtype=dtype, seed=8)
+    want, y = reference(x), cuda(x)
+    d, NC = block.ssd_delta_dims(B, T, H, G, K, V, block._TYPES[dtype], 1), -(-T // 64)
+    hd = lambda t: block.ssd_heads(t.data_ptr(), *(t.stride()[:3] if t.dim() == 4 else t.stride()))
+    outs = {n: guarded(*s, dtype=t) for n, s, t in (
+        ("o", (B, T, H, V), dt), ("h_last", (B, H, K, V), torch.float32), ("states", (B, H, NC, K, V), dt), ("updates", (B, T, H, V), dt),
+        ("dq", (B, T, G, K), dt), ("dk", (B, T, G, K), dt), ("dv", (B, T, H, V), dt), ("df", (B, T, H), dt), ("db", (B, T, H), dt),
+        ("dh0", (B, H, K, V), torch.float32))}
+    nbytes = lib.ssd_delta_rule_bwd_workspace_bytes(d)
+    outs["ws"] = guarded(nbytes, dtype=torch.uint8)
+    p = {n: t.data_ptr() for n, (t, _) in outs.items()}
+    assert lib.ssd_delta_rule_fwd(*(hd(y[n]) for n in NAMES), y["h0"].data_ptr(), None, d, p["o"], p["h_last"], p["states"], p["updates"], st) == 0
+    assert lib.ssd_delta_rule_bwd(hd(y["q"]), hd(y["k"]), hd(y["f"]), hd(y["b"]), p["states"], p["updates"], None, hd(y["do"]),
+                                  y["dh_last"].data_ptr(), d, *(p[n] for n in ("dq", "dk", "dv", "df", "db", "dh0", "ws")), nbytes, st) == 0
+    torch.cuda.synchronize()
+    for n, (t, end) in outs.items():
+        assert (end == (7 if n == "ws" else GUARD)).all(), n
+        if n in want:
+            close(t, want[n], n, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradient_of_the_state_in_place_and_left_out(dtype):
+    """dh0 over dh_last, and no dh0 at all, through the C ABI."""
+    B, T, H, K = 2, 66, 2, 32
+    x = cuda(make(B, T, H, H, K, K, dtype=dtype, seed=12))
+    want = run(x, dtype)
+    plan = block.DeltaRuleBackward(B, T, H, K, K, dtype)
+    fwd = block.DeltaRule(B, T, H, K, K, dtype, keep=True)
+    fwd(*(x[n] for n in NAMES), h0=x["h0"])
+    lib, st = block.load(), torch.cuda.current_stream().cuda_stream
+    hd = lambda t: block.ssd_heads(t.data_ptr(), *(t.stride()[:3] if t.dim() == 4 else t.stride()))
+    for dh0 in (x["dh_last"].clone(), None):
+        last = x["dh_last"] if dh0 is None else dh0
+        g = plan.grads
+        assert lib.ssd_delta_rule_bwd(hd(x["q"]), hd(x["k"]), hd(x["f"]), hd(x["b"]), fwd.states.data_ptr(), fwd.updates.data_ptr(), None,
+                                      hd(x["do"]), last.data_ptr(), plan.dims, *(g[n].data_ptr() for n in ("dq", "dk", "dv", "df", "db")),
+                                      None if dh0 is None else dh0.data_ptr(), plan.workspace.data_ptr(), plan.workspace.numel(), st) == 0
+        for n in ("dq", "dk", "dv", "df", "db"):
+            assert torch.equal(g[n], want[n]), n
+        if dh0 is not None:
+            assert torch.equal(dh0, want["dh0"])
+
+
+def test_two_streams_at_once():
+    """Two plans at the same time on streams of their own."""
+    xs = [cuda(make(4, 300, 4, 4, 64, 64, seed=s)) for s in (20, 21)]
+    want = [{n: t.clone() for n, t in run(x, "bf16").items()} for x in xs]
+    plans = [(block.DeltaRule(*sizes(x), keep=True), block.DeltaRuleBackward(*sizes(x))) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for x, (plan, back), s in zip(xs, plans, streams):
+            plan(*(x[n] for n in NAMES), h0=x["h0"], stream=s)
+            back(x["q"], x["k"], x["f"], x["b"], plan.states, plan.updates, x["do"], dh_last=x["dh_last"], stream=s)
+    torch.cuda.synchronize()
+    for (plan, back), w in zip(plans, want):
+        assert torch.equal(plan.o, w["o"]) and torch.equal(plan.h_last, w["h_last"])
+        for n, t in back.grads.items():
+            assert torch.equal(t, w[n]), n
+
+
+@pytest.mark.parametrize("dtype,at", [("bf16", 128), ("bf16", 192), ("fp32", 128), ("fp32", 100), ("fp32", 1), ("fp32", 255)])
+@pytest.mark.parametrize("bad", ["v", "k", "h0"])
+def test_nothing_passes_a_reset(dtype, at, bad):
+    """Not an infinity or a NaN either, in either direction: in fp32 at any reset, in bfloat16 at those that begin a chunk."""
+    x = make(1, 256, 2, 2, 64, 64, dtype=dtype, seed=30)
+    x["reset"] = torch.zeros(1, 256, dtype=torch.uint8)
+    x["reset"][0, at] = 1
+    clean = {n: t.clone() for n, t in run(cuda(x), dtype).items()}
+    worse = {n: None if t is None else t.clone() for n, t in x.items()}
+    if bad == "h0":
+        worse["h0"][0, 1, 3, 5] = float("inf")
+    else:
+        worse[bad][0, at // 2, 1, 3] = float("nan")
+    got = run(cuda(worse), dtype)
+    assert not torch.isfinite(got["o"][0, at // 2:at, 1]).all()
+    for n in ("o", "dq", "dk", "dv", "df", "db"):
+        assert torch.equal(got[n][:, at:], clean[n][:, at:]), n
+    assert torch.equal(got["h_last"], clean["h_last"])
+    # backwards: a NaN in the later document's gradient stays there
+    worse = {n: None if t is None else t.clone() for n, t in x.items()}
+    worse["do"][0, (at + 256) // 2, 1, 3] = float("nan")
+    worse["dh_last"][0, 0, 2, 2] = float("inf")
+    got = run(cuda(worse), dtype)
+    assert not torch.isfinite(got["dv"][0, at:, 1]).all()
+    for n in ("dq", "dk", "dv", "df", "db"):
+        assert torch.equal(got[n][:, :at], clean[n][:, :at]), n
+    assert torch.equal(got["dh0"], clean["dh0"])
+
+
+class Layer:
+    """residual norm -> 8-bit product (q | k | v | f | b | z) -> delta rule -> gated norm in 8 bits -> 8-bit product"""
+
+    def __init__(self, width, H, K, V, seed):
+        self.width, self.H, self.K, self.V = width, H, K, V
+        self.cuts = [H * K, H * K, H * V, H, H, H * V]
+        self.w_in = randn(sum(self.cuts), width, seed=seed, dtype=torch.bfloat16, std=width ** -0.5).cuda()
+        self.w_out = randn(width, H * V, seed=seed + 1, dtype=torch.bfloat16, std=(H * V) ** -0.5).cuda()
+        self.norm, self.gate = (randn(n, seed=seed + 2, mean=1.0, std=0.1).cuda() for n in (width, H * V))
+        self.w_in8 = [t.clone() for t in block.Fp8Quantize(*self.w_in.shape, scales="blocks")(self.w_in)]
+        self.w_out8 = [t.clone() for t in block.Fp8Quantize(*self.w_out.shape, scales="blocks")(self.w_out)]
+
+    def plans(self, B, T):
+        M, HV = B * T, self.H * self.V
+        return dict(norm=block.ResidualNorm(M, self.width), to_in=block.Fp8Product(M, sum(self.cuts), self.width),
+                    rule=block.DeltaRuleStep(B, self.H, self.K, self.V) if T == 1 else block.DeltaRule(B, T, self.H, self.K, self.V),
+                    gate=block.GatedNorm(M, self.H, self.V), to_out=block.Fp8Product(M, self.width, HV), sizes=(B, T))
+
+    def __call__(self, p, x, stream, state):
+        """(stream, add, state) of B T rows."""
+        B, T = p["sizes"]
+        r, q8, s8 = p["norm"](x, stream, self.norm)
+        parts = p["to_in"](q8, s8, *self.w_in8).split(self.cuts, dim=1)
+        dims = (self.K, self.K, self.V, 0, 0)
+        view = [t.unflatten(1, (self.H, d)) if d else t for t, d in zip(parts, dims)]
+        if T == 1:
+            o, state = p["rule"](*view, state, state_out=state)
+        else:
+            o, last = p["rule"](*(t.unflatten(0, (B, T)) for t in view), h0=state)
+            state.copy_(last)
+        y8, ys8 = p["gate"](o.reshape(B * T, -1), parts[5], self.gate)
+        return r, p["to_out"](y8, ys8, *self.w_out8), state
+
+
+def test_a_layer_over_a_prompt_and_token_by_token():
+    """The same rows in one pass and token by token, the tokens captured in a graph: the sums' order alone differs. A
+    bfloat16 value then is a step (2^-8) off at most, and about one in 2^5 of the e4m3 values made from those by a step of theirs
+    (2^-3): 2^-5.5 of the norm for each of the two products' operands: sqrt(2) 2^-5.5 = 0.032."""
+    B, T, width, H, K, V = 3, 80, 256, 4, 32, 48
+    layer = Layer(width, H, K, V, seed=40)
+    x, res = (randn(B, T, width, seed=50 + i, dtype=torch.bfloat16).cuda() for i in range(2))
+    p, state = layer.plans(B, T), torch.zeros(B, H, K, V, device="cuda")
+    r, add, state = layer(p, x.flatten(0, 1), res.flatten(0, 1), state)
+    r, add = r.unflatten(0, (B, T)), add.unflatten(0, (B, T))
+    one, token, stream, carried = layer.plans(B, 1), torch.empty_like(x[:, 0]), torch.empty_like(x[:, 0]), torch.zeros_like(state)
+    token.copy_(x[:, 0]), stream.copy_(res[:, 0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(one, token, stream, carried)
+    torch.cuda.current_stream().wait_stream(side)
+    carried.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r1, add1, _ = layer(one, token, stream, carried)
+    carried.zero_()
+    for t in range(T):
+        token.copy_(x[:, t]), stream.copy_(res[:, t])
+        graph.replay()
+        assert torch.equal(r1, r[:, t])
+        e = float((add1.double() - add[:, t].double()).norm() / add[:, t].double().norm())
+        assert e <= 0.032, (t, e)
+    e = float((carried.double() - state.double()).norm() / state.double().norm())
+    assert e <= 0.032, e
+
+
+def test_a_layer_s_gradients():
+    """Delta rule and gated norm with a skip connection, differentiated together in fp32, against the same in 64 bits."""
+    B, T, H, K, V = 2, 70, 3, 16, 24
+    x = make(B, T, H, H, K, V, dtype="fp32", seed=60, state=False)
+    z, w, s = randn(B * T, H * V, seed=61), randn(H * V, seed=62, mean=1.0, std=0.2), randn(H, seed=63)
+    dy = randn(B * T, H * V, seed=64)
+    d = {n: x[n].double().requires_grad_() for n in NAMES}
+    extra = [t.double().requires_grad_() for t in (z, w, s)]
+    q = d["q"] / (d["q"].square().sum(-1, keepdim=True) + 1e-6).sqrt() / K ** 0.5
+    k = d["k"] / (d["k"].square().sum(-1, keepdim=True) + 1e-6).sqrt()
+    S, rows = torch.zeros(B, H, K, V, dtype=torch.float64), []
+    for t in range(T):
+        S = torch.sigmoid(d["f"][:, t])[..., None, None] * S
+        u = torch.sigmoid(d["b"][:, t])[..., None] * (d["v"][:, t] - torch.einsum("bhk,bhkv->bhv", k[:, t], S))
+        S = S + k[:, t, :, :, None] * u[:, :, None]
+        rows.append(torch.einsum("bhk,bhkv->bhv", q[:, t], S))
+    u = torch.stack(rows, 1) + extra[2][:, None] * d["v"]
+    y = (u / (u.square().mean(-1, keepdim=True) + 1e-5).sqrt()).reshape(B * T, -1) * extra[1] * extra[0] * torch.sigmoid(extra[0])
+    want = torch.autograd.grad((y * dy.double()).sum(), list(d.values()) + extra)
+    leaves = [x[n].cuda().requires_grad_() for n in NAMES] + [t.cuda().requires_grad_() for t in (z, w, s)]
+    o, _ = block.delta_rule(*leaves[:5])
+    got = block.gated_norm(o.reshape(B * T, -1), leaves[5], leaves[6], leaves[2].reshape(B * T, -1), leaves[7], heads=H)
+    close(got, y, "y", "fp32")
+    # the norm divides by the length of o, whose heads are up to ten times smaller here than v: errors grow by that
+    for n, a, b in zip(("dq", "dk", "dv", "df", "db", "dz", "dw", "ds"), torch.autograd.grad(got, leaves, dy.cuda()), want):
+        close(a, b, n, "fp32", scale=10.0)

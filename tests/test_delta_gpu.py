@@ -24,7 +24,7 @@ def tolerance(name, dtype):
 
 
 def close(got, want, name, dtype, scale=1.0):
-    got, want = got.double().cpu(), want.detach().double().cpu()
+    got, want = got.detach().double().cpu(), want.detach().double().cpu()
     assert got.shape == want.shape, name
     assert torch.isfinite(got).all(), name
     norm = float(want.norm())
