@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
             const bool there = tid < n_tokens;
             const float f = __uint_as_float((uint32_t)f_raw << 16), e = expf(-fabsf(f));
             const float s = log1pf(e), l = f >= 0.0f ? -s : f - s;
-            const float lg = !there ? 0.0f : mark != 0 || l < -177.0f ? -256.0f : l * kLog2e;
+            // (a NaN comes back in `rest`, u and z)
+            const float lg = !there || (mark == 0 && f != f) ? 0.0f : mark != 0 || l < -177.0f ? -256.0f : l * kLog2e;
             sm.rest[tid] = mark != 0 ? 0.0f : (f >= 0.0f ? e : 1.0f) / (1.0f + e);
             // where beta is below e^-80 so are u and z, and their product is zero
             sm.beta_rest[tid] = expf(fminf(-__uint_as_float((uint32_t)b_raw << 16), 80.0f));

@@ -103,8 +103,11 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
         const float v = __uint_as_float((uint32_t)gate << 16), e = expf(-fabsf(v));
         // log2 of sigmoid(f), not below -256
         const float s = log1pf(e), l = v >= 0.0f ? -s : v - s, lg = l < -177.0f ? -256.0f : l * kLog2e;
-        if (lane >= 16) betas_of[set * C + gate_r] = there ? (v >= 0.0f ? 1.0f : e) / (1.0f + e) : 0.0f;
-        scan_group<false>(!there ? 0.0f : mark != 0 ? -256.0f : lg, tabs + set * C + 16 * warp);
+        // Sums of integers hold no NaN: one in f, of a token without a mark, is handed on in its beta.
+        const bool bad = there && mark == 0 && v != v;
+        const bool bad_f = __shfl_sync(0xffffffffu, bad, lane % 16);
+        if (lane >= 16) betas_of[set * C + gate_r] = !there ? 0.0f : bad_f ? __int_as_float(0x7fffffff) : (v >= 0.0f ? 1.0f : e) / (1.0f + e);
+        scan_group<false>(!there || bad ? 0.0f : mark != 0 ? -256.0f : lg, tabs + set * C + 16 * warp);
         ptx::cp_async_wait<0>();
     };
 

@@ -476,8 +476,10 @@ __global__ void __launch_bounds__(256) delta_tokens_bwd_gates(const Delta p) {
         int r = 0;
         for (int t = 0; t < n; ++t) {
             const double f = *row<float>(p.f, b, t0 + t, h);
-            s -= f > 0.0 ? log1p(exp(-f)) : log1p(exp(f)) - f;  // log sigmoid(f)
-            r += p.reset != nullptr && p.reset[b * p.T + t0 + t] != 0;
+            const bool first = p.reset != nullptr && p.reset[b * p.T + t0 + t] != 0;
+            // log sigmoid(f), at least -10^4: exp is zero there, and the difference of two infinities would be a NaN
+            if (!first) s += fmax(f > 0.0 ? -log1p(exp(-f)) : f - log1p(exp(f)), -1e4);
+            r += first;
             sum[t] = s;
             doc[t] = r;
         }

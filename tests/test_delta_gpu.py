@@ -375,6 +375,40 @@ def test_infinities_and_nans_stay_in_their_head(dtype):
     assert torch.equal(got["o"][0, :64, 1], clean["o"][0, :64, 1])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("gate", ["f", "b"])
+def test_a_nan_gate_is_not_lost(gate, dtype):
+    """Results behind it are NaN, and gradients of what is in front of it; under a reset f is not looked at."""
+    x = make(1, 200, 2, 2, 32, 24, dtype=dtype, seed=64)
+    clean = {n: t.clone() for n, t in run(cuda(x), dtype).items()}
+    x[gate][0, 70, 1] = float("nan")
+    got = run(cuda(x), dtype)
+    assert torch.isnan(got["o"][0, 70:, 1]).all() and torch.isnan(got["h_last"][0, 1]).all()
+    assert torch.isnan(got["dv"][0, :70, 1]).all() and torch.isnan(got["dh0"][0, 1]).all()
+    assert torch.isnan(got["d" + gate][0, 70, 1])
+    assert torch.equal(got["o"][0, :64, 1], clean["o"][0, :64, 1])
+    for n in clean:
+        head = 1 if n in ("h_last", "dh0") else 2
+        assert torch.equal(got[n].select(head, 0), clean[n].select(head, 0)), n
+    if gate == "f":
+        x["reset"] = torch.zeros(1, 200, dtype=torch.uint8)
+        x["reset"][0, 70] = 1
+        got, x["f"][0, 70, 1] = {n: t.clone() for n, t in run(cuda(x), dtype).items()}, 3.0
+        want = run(cuda(x), dtype)
+        for n in want:
+            assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_infinite_gates(dtype):
+    """f = -inf lets nothing through, as a reset does, and has no gradient; f = inf lets everything through."""
+    x = make(1, 150, 2, 2, 32, 24, dtype=dtype, seed=65)
+    x["f"][0, (3, 40, 41, 100), 1] = -float("inf")
+    x["f"][0, (5, 64, 130), 1] = float("inf")
+    x["b"][0, 20, 1], x["b"][0, 21, 1] = -float("inf"), float("inf")
+    check(x, dtype)
+
+
 def test_long_row_past_2_31_elements():
     """Tokens whose offset from the row's first is past 2^31 elements."""
     if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
