@@ -261,12 +261,16 @@ typedef struct {
  *   states, updates   outputs for the backward pass, or both NULL: the state that
  *             enters every SSD_DELTA_STATE_TOKENS-th token,
  *             (B, H, ceil(T / that), K, V), and u (B, T, H, V), both of `type`
- * One launch.
+ *   workspace ssd_delta_rule_fwd_workspace_bytes() bytes, 256-byte aligned, its contents
+ *             need not be kept; NULL where that is 0
+ * One launch; BF16 sequences much longer than the states are many: three, with a workspace, in segments that are
+ * taken at once and joined.
  */
 #define SSD_DELTA_STATE_TOKENS 64
+size_t ssd_delta_rule_fwd_workspace_bytes(ssd_delta_dims dims);
 int ssd_delta_rule_fwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in v, ssd_heads_in f, ssd_heads_in b, const float *h0,
                        const uint8_t *reset, ssd_delta_dims dims, void *o, float *h_last, void *states, void *updates,
-                       cudaStream_t stream);
+                       void *workspace, size_t ws_bytes, cudaStream_t stream);
 
 /*
  * One token for every batch row (the forward pass at T = 1, for generation), on
@@ -285,7 +289,7 @@ int ssd_delta_rule_step(ssd_heads_in q, ssd_heads_in k, ssd_heads_in v, ssd_head
  *   dh0       output (B, H, K, V) fp32, or NULL; it may be dh_last
  *   workspace ssd_delta_rule_bwd_workspace_bytes() bytes, 256-byte aligned, its
  *             contents need not be kept
- * df is 0 at a reset. Sums run in a fixed order. Two launches (F32: four).
+ * df is 0 at a reset. Sums run in a fixed order. Two launches (in segments four, F32 four).
  */
 size_t ssd_delta_rule_bwd_workspace_bytes(ssd_delta_dims dims);
 int ssd_delta_rule_bwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in f, ssd_heads_in b, const void *states,
@@ -339,7 +343,7 @@ int ssd_gated_norm_bwd(ssd_rows_in dy, ssd_rows_in x, ssd_rows_in z, const float
 #define SSD_CALL_FP8_QUANTIZE 5        /* 12 words */
 #define SSD_CALL_FP8_MATMUL 6          /* 15 words */
 #define SSD_CALL_GATED_SCAN_FWD_WS 7   /* 23 words */
-#define SSD_CALL_DELTA_RULE_FWD 9      /* 34 words */
+#define SSD_CALL_DELTA_RULE_FWD 9      /* 36 words */
 #define SSD_CALL_DELTA_RULE_STEP 10    /* 31 words */
 #define SSD_CALL_DELTA_RULE_BWD 11     /* 40 words */
 #define SSD_CALL_GATED_NORM_FWD 12     /* 17 words */

@@ -43,7 +43,8 @@ _DTYPES = {"fp32": torch.float32, "bf16": torch.bfloat16}
 EXPORTS = ("ssd_gated_scan_states_bytes", "ssd_gated_scan_fwd", "ssd_gated_scan_workspace_bytes", "ssd_gated_scan_fwd_ws", "ssd_gated_scan_step", "ssd_gated_scan_bwd",
            "ssd_residual_norm_fwd", "ssd_residual_norm_bwd_workspace_bytes", "ssd_residual_norm_bwd",
            "ssd_fp8_quantize", "ssd_fp8_matmul_workspace_bytes", "ssd_fp8_matmul", "ssd_block_call",
-           "ssd_delta_rule_fwd", "ssd_delta_rule_step", "ssd_delta_rule_bwd_workspace_bytes", "ssd_delta_rule_bwd",
+           "ssd_delta_rule_fwd_workspace_bytes", "ssd_delta_rule_fwd", "ssd_delta_rule_step",
+           "ssd_delta_rule_bwd_workspace_bytes", "ssd_delta_rule_bwd",
            "ssd_gated_norm_fwd", "ssd_gated_norm_bwd_workspace_bytes", "ssd_gated_norm_bwd")
 
 
@@ -91,7 +92,8 @@ def load() -> ctypes.CDLL:
             ("ssd_fp8_quantize", i32, [r, i64, i64, i32, i32, r, vp, r, vp, vp]),
             ("ssd_fp8_matmul_workspace_bytes", sz, [i64, i64, i64]),
             ("ssd_fp8_matmul", i32, [r, vp, r, vp, i32, i64, i64, i64, i32, r, vp, sz, vp]),
-            ("ssd_delta_rule_fwd", i32, [hd, hd, hd, hd, hd, vp, vp, dd, vp, vp, vp, vp, vp]),
+            ("ssd_delta_rule_fwd_workspace_bytes", sz, [dd]),
+            ("ssd_delta_rule_fwd", i32, [hd, hd, hd, hd, hd, vp, vp, dd, vp, vp, vp, vp, vp, sz, vp]),
             ("ssd_delta_rule_step", i32, [hd, hd, hd, hd, hd, vp, dd, vp, vp, vp]),
             ("ssd_delta_rule_bwd_workspace_bytes", sz, [dd]),
             ("ssd_delta_rule_bwd", i32, [hd, hd, hd, hd, vp, vp, vp, hd, vp, dd, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
@@ -592,9 +594,12 @@ class DeltaRule:
         self._qk, self._v = (self.dtype, torch.Size((B, T, key_heads, K)), index), (self.dtype, self.o.shape, index)
         self._fb, self._state = (self.dtype, torch.Size((B, T, heads)), index), (torch.float32, self.h_last.shape, index)
         self._marks = torch.uint8, torch.Size((B, T)), index
+        nbytes = load().ssd_delta_rule_fwd_workspace_bytes(self.dims)
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
         self._out = (self.o.data_ptr(), self.h_last.data_ptr(),
-                     *((self.states.data_ptr(), self.updates.data_ptr()) if keep else (0, 0)))
-        self._call = _Call("ssd_delta_rule_fwd", 9, 34, index)
+                     *((self.states.data_ptr(), self.updates.data_ptr()) if keep else (0, 0)),
+                     self.workspace.data_ptr() if nbytes else 0, nbytes)
+        self._call = _Call("ssd_delta_rule_fwd", 9, 36, index)
 
     def __call__(self, q, k, v, f, b, h0=None, reset=None, stream=None):
         self._call(stream, *_heads("q", q, self._qk), *_heads("k", k, self._qk), *_heads("v", v, self._v),

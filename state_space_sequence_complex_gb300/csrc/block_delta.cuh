@@ -19,6 +19,7 @@
 
 #include "block_common.cuh"
 #include "block_kernels.h"
+#include "ssdc_kernels.h"
 
 namespace ssdc {
 namespace block {

@@ -23,23 +23,25 @@ namespace block {
 namespace delta {
 namespace {
 
+// out: with dv and the states' gradients; else only the gradient of the state in front of the chunks.
 template <int KP, int NW, int kGroups, bool kUnitRows>
-__device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int h, int w, int col0, int column_threads) {
+__device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int h, const Way& way, bool out, int w, int col0, int column_threads) {
     using L = Layout<KP, NW, true, kGroups>;
     constexpr int KT = KP / 8;
     const uint32_t base = ptx::smem_addr(smem);
     const int lane = threadIdx.x % 32, all = kPrep + column_threads;
-    const int columns = min(16, p.V - col0);
-    const int chunks = (int)((p.T + C - 1) / C);
+    const int columns = min(16, (way.unit ? p.K : p.V) - col0);
+    const int chunks = way.span.chunks, last = chunk_count(p) - 1 - way.span.first;  // the first that is taken
+    auto tokens_of = [&](int c) { return (int)min((int64_t)C, p.T - (int64_t)c * C); };
     const int64_t seq = (int64_t)b * p.H + h;
     const uint32_t strips = base + L::kStripOff + w * 2 * L::kStrip;
     const Lanes<L::kKeyPitch> key_lanes(base);
     const Lanes<L::kPitch> lanes(base);
     const int fetch_u = lane % 2, fetch_r = lane / 2;
-    const bool has_unit = 8 * fetch_u < columns;
-    const __nv_bfloat16* row = bf16(p.d_o.p) + b * p.d_o.b + h * p.d_o.h + ((int64_t)(chunks - 1) * C + fetch_r) * p.d_o.t + col0 + (has_unit ? 8 * fetch_u : 0);
+    const bool has_unit = !way.unit && 8 * fetch_u < columns;
+    const __nv_bfloat16* row = bf16(p.d_o.p) + b * p.d_o.b + h * p.d_o.h + ((int64_t)last * C + fetch_r) * p.d_o.t + (has_unit ? col0 + 8 * fetch_u : 0);
     auto fetch_do = [&](int n) {  // chunks from the last to the first
-        const int left = (int)min((int64_t)C, p.T - (int64_t)(chunks - 1 - n) * C) - fetch_r;
+        const int left = tokens_of(last - n) - fetch_r;
         const __nv_bfloat16* r = row;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -51,19 +53,20 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
     };
     fetch_do(0);
     float S[KT][4];  // dS, as the forward kernel holds S
-    const int64_t state = seq * p.K * p.V + col0;
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
-            S[i][e] = p.dh_last != nullptr && r < p.K && cl < columns ? p.dh_last[state + (int64_t)r * p.V + cl] : 0.0f;
+            S[i][e] = way.start != nullptr && r < p.K && cl < columns ? way.start[r * p.V + col0 + cl]
+                      : way.unit && r == col0 + cl                    ? 1.0f
+                                                                      : 0.0f;
         }
     const int64_t z_stride = (int64_t)p.H * p.V, z_step = C * z_stride;
-    __nv_bfloat16* z_rows = static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + (int64_t)(chunks - 1) * C) * p.H + h) * p.V + col0;
+    __nv_bfloat16* z_rows = static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + (int64_t)last * C) * p.H + h) * p.V + col0;
     int stage = 0;
     for (int n = 0; n < chunks; ++n, stage = L::next_stage(stage, 1)) {
-        const int c = chunks - 1 - n;
+        const int c = last - n;
         const int turn = n & 1, set = n & (L::kSets - 1), half = n % kGroups;
         // This chunk's strip has its do, and when that has been read its z. The other one has the last chunk's z,
         // which goes to memory beside the first products; then dS; then the next do.
@@ -71,13 +74,13 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         bar_sync(kBarKeys + (n & 3), all);
         const uint32_t keys = stage * L::kStage, queries = keys + L::kKeyTile;
         StripRows rows;
-        rows.take(other);
+        if (out) rows.take(other);
         float X[8][4];
 #pragma unroll
         for (int s = 0; s < KP / 16; ++s) {
             Split a;
             a.set(S[2 * s], S[2 * s + 1]);
-            stsm_t(strip_rows(other, 16 * s % C), a.hi[0], a.hi[1], a.hi[2], a.hi[3]);
+            if (out) stsm_t(strip_rows(other, 16 * s % C), a.hi[0], a.hi[1], a.hi[2], a.hi[3]);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 uint32_t kb[4];
@@ -87,11 +90,11 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
                 mma(X[2 * m], a.lo, kb[0], kb[1]);
                 mma(X[2 * m + 1], a.lo, kb[2], kb[3]);
             }
-            if (s == 0 && n > 0) rows.give(z_rows + z_step, z_stride, n == 1 ? (int)(p.T - (int64_t)(chunks - 1) * C) : C, columns);
-            if (s % 4 == 3) {
+            if (out && s == 0 && n > 0) rows.give(z_rows + z_step, z_stride, tokens_of(c + 1), columns);
+            if (out && s % 4 == 3) {
                 const int first = s / 4 * C;
                 rows.take(other);
-                rows.give(static_cast<__nv_bfloat16*>(p.ws) + (seq * chunks + c) * p.K * p.V + (int64_t)first * p.V + col0, p.V,
+                rows.give(static_cast<__nv_bfloat16*>(p.ws) + (seq * chunk_count(p) + c) * p.K * p.V + (int64_t)first * p.V + col0, p.V,
                           p.K - first, columns);
             }
         }
@@ -200,33 +203,60 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         if (n + 2 * kGroups < chunks) bar_arrive(kBarStage + (n & 3), all);
         z_rows -= z_step;
     }
-    StripRows rows;
-    rows.take(strips + ((chunks - 1) & 1) * L::kStrip);
-    rows.give(z_rows + z_step, z_stride, chunks == 1 ? (int)p.T : C, columns);
-    if (p.dh0 != nullptr) {
+    if (out) {
+        StripRows rows;
+        rows.take(strips + ((chunks - 1) & 1) * L::kStrip);
+        rows.give(z_rows + z_step, z_stride, tokens_of(last - chunks + 1), columns);
+    }
+    if (way.end != nullptr) {
 #pragma unroll
         for (int i = 0; i < KT; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
-                if (r < p.K && cl < columns) p.dh0[state + (int64_t)r * p.V + cl] = S[i][e];
+                if (r < p.K && cl < columns) way.end[r * way.end_row + (col0 + cl) * way.end_column] = S[i][e];
             }
     }
 }
 
-template <int KP, int NW, int kGroups, bool kUnitRows>
+template <int KP, int NW, int kGroups, bool kUnitRows, bool kSegments>
 __global__ void __launch_bounds__(kGroups * kPrep + 32 * NW, KP == 64 && NW == 4 && kGroups == 1 ? 2 : 1) delta_bwd_chain(const __grid_constant__ Delta p) {
     extern __shared__ __align__(128) char smem[];
-    const int parts = (p.V + 16 * NW - 1) / (16 * NW), item = blockIdx.x / parts, col0 = blockIdx.x % parts * 16 * NW;
-    const int b = item / p.H, h = item % p.H;
+    const int parts = (p.V + 16 * NW - 1) / (16 * NW), col0 = blockIdx.x % parts * 16 * NW;
+    const int segment = kSegments ? 1 + blockIdx.x / parts % (p.segments - 1) : 0;
+    const int seq = kSegments ? blockIdx.x / parts / (p.segments - 1) : blockIdx.x / parts, b = seq / p.H, h = seq % p.H;
+    const int64_t state = (int64_t)seq * p.K * p.V;
+    const bool all = !kSegments || segment == p.segments - 1;  // up to the first token
+    const Span span = kSegments ? segment_span(p, segment) : Span{0, chunk_count(p)};
+    const Way way = {span, kSegments ? carry_state(p, seq, segment) : p.dh_last != nullptr ? p.dh_last + state : nullptr,
+                     all && p.dh0 != nullptr ? p.dh0 + state : nullptr, p.V, 1, false};
     const int warps = min(NW, (p.V - col0 + 15) / 16);
     if (threadIdx.x < kGroups * kPrep) {
         Registers<KP, NW, true, kGroups>::prepare();
-        prepare_chunks<KP, NW, true, kGroups, kUnitRows>(p, smem, b, h, 32 * warps);
+        prepare_chunks<KP, NW, true, kGroups, kUnitRows>(p, smem, b, h, span, 32 * warps);
     } else {
         Registers<KP, NW, true, kGroups>::walk();
         const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
-        if (w < warps) walk_back<KP, NW, kGroups, kUnitRows>(p, smem, b, h, w, col0 + 16 * w, 32 * warps);
+        if (kSegments) grid_dependency_wait();  // chunks are prepared meanwhile
+        if (w < warps) walk_back<KP, NW, kGroups, kUnitRows>(p, smem, b, h, way, true, w, col0 + 16 * w, 32 * warps);
+    }
+}
+
+// The first pass over segments, as the forward one; its segments are numbered from the last.
+template <int KP, int kGroups, bool kUnitRows>
+__global__ void __launch_bounds__(kGroups * kPrep + 256, 1) delta_bwd_carry(const __grid_constant__ Delta p) {
+    extern __shared__ __align__(128) char smem[];
+    const Carry c(p);
+    if (c.warps() == 0) return;
+    if (threadIdx.x < kGroups * kPrep) {
+        Registers<KP, 8, true, kGroups>::prepare();
+        prepare_chunks<KP, 8, true, kGroups, kUnitRows>(p, smem, c.b, c.h, c.span, 32 * c.warps());
+        launch_dependents();
+    } else {
+        Registers<KP, 8, true, kGroups>::walk();
+        const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
+        if (c.has_columns(w))
+            walk_back<KP, 8, kGroups, kUnitRows>(p, smem, c.b, c.h, c.way(p, w, p.dh_last), c.segment == 0, w, c.column(w), 32 * c.warps());
     }
 }
 
@@ -683,16 +713,30 @@ __global__ void __launch_bounds__(2 * KP, KP == 64 && VP == 64 ? 3 : 1) delta_bw
     }
 }
 
-template <int KP, int NW, int kGroups>
+template <int KP, int NW, int kGroups, bool kSegments = false>
 int launch_chain(const Delta& p, cudaStream_t stream) {
     using L = Layout<KP, NW, true, kGroups>;
     const bool units = whole_units(p.k) && whole_units(p.q) && whole_units(p.d_o);
-    const auto kernel = units ? delta_bwd_chain<KP, NW, kGroups, true> : delta_bwd_chain<KP, NW, kGroups, false>;
+    const auto kernel = units ? delta_bwd_chain<KP, NW, kGroups, true, kSegments> : delta_bwd_chain<KP, NW, kGroups, false, kSegments>;
     static std::atomic<uint64_t> done[2];
     if (allow_smem(kernel, L::kBytes, done[units]) != cudaSuccess) return SSDC_ERR_CUDA;
     const int parts = (p.V + 16 * NW - 1) / (16 * NW);
-    kernel<<<p.B * p.H * parts, kGroups * kPrep + 32 * NW, L::kBytes, stream>>>(p);
+    const int grid = p.B * p.H * parts * (kSegments ? p.segments - 1 : 1), threads = kGroups * kPrep + 32 * NW;
+    if (!kSegments) kernel<<<grid, threads, L::kBytes, stream>>>(p);
+    else if (launch_dependent(kernel, grid, threads, L::kBytes, stream, p) != cudaSuccess) return SSDC_ERR_CUDA;
     return 1;
+}
+
+template <int KP, int kGroups>
+int launch_segments(const Delta& p, cudaStream_t stream) {
+    using L = Layout<KP, 8, true, kGroups>;
+    const bool units = whole_units(p.k) && whole_units(p.q) && whole_units(p.d_o);
+    const auto kernel = units ? delta_bwd_carry<KP, kGroups, true> : delta_bwd_carry<KP, kGroups, false>;
+    static std::atomic<uint64_t> done[2];
+    if (allow_smem(kernel, L::kBytes, done[units]) != cudaSuccess) return SSDC_ERR_CUDA;
+    kernel<<<Carry::grid(p), kGroups * kPrep + 256, L::kBytes, stream>>>(p);
+    const int joined = join_launch(p, stream), second = joined < 0 ? joined : launch_chain<KP, 4, 2, true>(p, stream);
+    return second < 0 ? second : 1 + joined + second;
 }
 
 template <int KP, int VP>
@@ -713,7 +757,8 @@ int delta_bwd_launch(const Delta& p, cudaStream_t stream) {
     using namespace delta;
     if ((p.T + C - 1) / C * p.B * p.G > INT32_MAX) return SSDC_ERR_UNSUPPORTED;
     int chain, chunks;
-    if (few_states(p)) chain = p.K <= 64 ? launch_chain<64, 4, 2>(p, stream) : launch_chain<128, 4, 2>(p, stream);
+    if (p.segments > 1) chain = p.K <= 64 ? launch_segments<64, 2>(p, stream) : launch_segments<128, 1>(p, stream);
+    else if (few_states(p)) chain = p.K <= 64 ? launch_chain<64, 4, 2>(p, stream) : launch_chain<128, 4, 2>(p, stream);
     else if (p.K <= 64) chain = p.V <= 64 ? launch_chain<64, 4, 1>(p, stream) : launch_chain<64, 8, 1>(p, stream);
     else chain = p.V <= 64 ? launch_chain<128, 4, 1>(p, stream) : launch_chain<128, 8, 1>(p, stream);
     if (chain < 0) return chain;

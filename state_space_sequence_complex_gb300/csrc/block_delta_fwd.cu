@@ -18,23 +18,24 @@ namespace block {
 namespace delta {
 namespace {
 
-template <int KP, int NW, int kGroups, bool kUnitRows>
-__device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, int w, int col0, int column_threads) {
+// kOut: with o, and states and updates where they are asked for; else only the state behind the chunks.
+template <int KP, int NW, int kGroups, bool kUnitRows, bool kOut>
+__device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, const Way& way, int w, int col0, int column_threads) {
     using L = Layout<KP, NW, false, kGroups>;
     constexpr int KT = KP / 8;  // 8-row tiles of the state
     const uint32_t base = ptx::smem_addr(smem);
     const int lane = threadIdx.x % 32, all = kPrep + column_threads;
-    const int columns = min(16, p.V - col0);
-    const int chunks = (int)((p.T + C - 1) / C);
-    const int64_t seq = (int64_t)b * p.H + h;
+    const int columns = min(16, (way.unit ? p.K : p.V) - col0);
+    const int chunks = way.span.chunks;
+    const int64_t seq = (int64_t)b * p.H + h, token0 = (int64_t)way.span.first * C;
     const uint32_t strips = base + L::kStripOff + w * 2 * L::kStrip;
     const Lanes<L::kKeyPitch> key_lanes(base);
     const Lanes<L::kPitch> lanes(base);
     const int fetch_u = lane % 2, fetch_r = lane / 2;
-    const bool has_unit = 8 * fetch_u < columns;
-    const __nv_bfloat16* v_row = bf16(p.v.p) + b * p.v.b + h * p.v.h + fetch_r * p.v.t + col0 + (has_unit ? 8 * fetch_u : 0);
+    const bool has_unit = !way.unit && 8 * fetch_u < columns;
+    const __nv_bfloat16* v_row = bf16(p.v.p) + b * p.v.b + h * p.v.h + (token0 + fetch_r) * p.v.t + (has_unit ? col0 + 8 * fetch_u : 0);
     auto fetch_v = [&](int c) {  // chunks in order
-        const int left = (int)min((int64_t)C, p.T - (int64_t)c * C) - fetch_r;
+        const int left = (int)min((int64_t)C, p.T - token0 - (int64_t)c * C) - fetch_r;
         const __nv_bfloat16* v = v_row;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -47,15 +48,16 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
     fetch_v(0);
     // state[row 8 i + 2 (lane % 4) + e % 2][column lane / 4 + 8 (e / 2)]
     float S[KT][4];
-    const int64_t state = seq * p.K * p.V + col0;
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
-            S[i][e] = p.h0 != nullptr && r < p.K && cl < columns ? p.h0[state + (int64_t)r * p.V + cl] : 0.0f;
+            S[i][e] = way.start != nullptr && r < p.K && cl < columns ? way.start[r * p.V + col0 + cl]
+                      : !kOut && way.unit && r == col0 + cl           ? 1.0f
+                                                                      : 0.0f;
         }
-    const int64_t o_stride = (int64_t)p.H * p.V, o_step = C * o_stride, o_first = (b * p.T * p.H + h) * p.V + col0;
+    const int64_t o_stride = (int64_t)p.H * p.V, o_step = C * o_stride, o_first = ((b * p.T + token0) * p.H + h) * p.V + col0;
     __nv_bfloat16* o_rows = static_cast<__nv_bfloat16*>(p.o) + o_first;
     __nv_bfloat16* u_rows = static_cast<__nv_bfloat16*>(p.updates) + o_first;
     int stage = 0;
@@ -67,37 +69,39 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
         bar_sync(kBarKeys + (c & 3), all);
         const uint32_t keys = stage * L::kStage, queries = keys + L::kKeyTile;
         StripRows rows;
-        rows.take(other);
+        if (kOut) rows.take(other);
         float X[8][4], O[8][4];
         Split a;
         uint32_t kb[2][4], qb[2][4];  // the next products' operands are read before this one's are used
         ldsm(kb[0], keys + key_lanes.down[0]);
-        ldsm(qb[0], queries + key_lanes.down[0]);
+        if (kOut) ldsm(qb[0], queries + key_lanes.down[0]);
 #pragma unroll
         for (int it = 0; it < KP / 4; ++it) {
             const int s = it / 4, n = it % 4, now = it % 2;
             if (n == 0) {
                 a.set(S[2 * s], S[2 * s + 1]);
-                if (p.states != nullptr) stsm_t(strip_rows(other, 16 * s % C), a.hi[0], a.hi[1], a.hi[2], a.hi[3]);
+                if (kOut && p.states != nullptr) stsm_t(strip_rows(other, 16 * s % C), a.hi[0], a.hi[1], a.hi[2], a.hi[3]);
             }
             if (it + 1 < KP / 4) {
                 const int s1 = (it + 1) / 4, n1 = (it + 1) % 4;
                 ldsm(kb[1 - now], keys + 16 * n1 * L::kKeyPitch + key_lanes.down[s1]);
-                ldsm(qb[1 - now], queries + 16 * n1 * L::kKeyPitch + key_lanes.down[s1]);
+                if (kOut) ldsm(qb[1 - now], queries + 16 * n1 * L::kKeyPitch + key_lanes.down[s1]);
             }
             const uint32_t *k = kb[now], *q = qb[now];
             mma_at(s, X[2 * n], a.hi, k[0], k[1]);
             mma_at(s, X[2 * n + 1], a.hi, k[2], k[3]);
-            mma_at(s, O[2 * n], a.hi, q[0], q[1]);
-            mma_at(s, O[2 * n + 1], a.hi, q[2], q[3]);
+            if (kOut) {
+                mma_at(s, O[2 * n], a.hi, q[0], q[1]);
+                mma_at(s, O[2 * n + 1], a.hi, q[2], q[3]);
+            }
             mma(X[2 * n], a.lo, k[0], k[1]);
             mma(X[2 * n + 1], a.lo, k[2], k[3]);
-            if (it == 3 && c > 0) rows.give(o_rows - o_step, o_stride, C, columns);
-            if (p.states != nullptr && it % 16 == 15) {
+            if (kOut && it == 3 && c > 0) rows.give(o_rows - o_step, o_stride, C, columns);
+            if (kOut && p.states != nullptr && it % 16 == 15) {
                 const int first = it / 16 * C;
                 rows.take(other);
-                rows.give(static_cast<__nv_bfloat16*>(p.states) + (seq * chunks + c) * p.K * p.V + (int64_t)first * p.V + col0, p.V,
-                          p.K - first, columns);
+                rows.give(static_cast<__nv_bfloat16*>(p.states) + (seq * chunk_count(p) + way.span.first + c) * p.K * p.V + (int64_t)first * p.V + col0,
+                          p.V, p.K - first, columns);
             }
         }
         if (c + 1 < chunks) fetch_v(c + 1);
@@ -115,7 +119,10 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
             for (int n = 0; n < 8; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (factors[8 * n + 2 * (lane % 4) + e % 2].k == 0.0f) X[n][e] = O[n][e] = 0.0f;
+                    if (factors[8 * n + 2 * (lane % 4) + e % 2].k == 0.0f) {
+                        X[n][e] = 0.0f;
+                        if (kOut) O[n][e] = 0.0f;
+                    }
         }
 #pragma unroll
         for (int n = 0; n < 8; n += 2) {
@@ -125,12 +132,15 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
             for (int e = 0; e < 2; ++e) {
                 const int j = 8 * (n + e) + 2 * (lane % 4);
                 const float2 f0 = *reinterpret_cast<const float2*>(&factors[j]), f1 = *reinterpret_cast<const float2*>(&factors[j + 1]);
-                float *x = X[n + e], *o = O[n + e];
+                float* x = X[n + e];
                 x[0] = fmaf(-f0.x, x[0], ptx::bf16_lo(r[2 * e]));
                 x[1] = fmaf(-f1.x, x[1], ptx::bf16_hi(r[2 * e]));
                 x[2] = fmaf(-f0.x, x[2], ptx::bf16_lo(r[2 * e + 1]));
                 x[3] = fmaf(-f1.x, x[3], ptx::bf16_hi(r[2 * e + 1]));
-                o[0] *= f0.y; o[1] *= f1.y; o[2] *= f0.y; o[3] *= f1.y;
+                if (kOut) {
+                    float* o = O[n + e];
+                    o[0] *= f0.y; o[1] *= f1.y; o[2] *= f0.y; o[3] *= f1.y;
+                }
             }
         }
 #pragma unroll
@@ -141,7 +151,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
 #pragma unroll
             for (int i = 0; i < KT; ++i) S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.0f;
         }
-        const int64_t left = p.T - (int64_t)c * C;
+        const int64_t left = p.T - token0 - (int64_t)c * C;
         const int n_tokens = left < C ? (int)left : C;
         // Block by block: what a block adds to O and S keeps the instructions coming while the next one, which
         // waits for each of its products, is solved.
@@ -172,10 +182,10 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
                     mma(X[2 * n + e], a.hi, bl[2 * e], bl[2 * e + 1]);
                 }
             }
-            if (p.updates != nullptr)
+            if (kOut && p.updates != nullptr)
                 stsm_t(strip_rows(mine, 16 * r), a.hi[0], a.hi[1], a.hi[2], a.hi[3]);
 #pragma unroll
-            for (int n = r; n < 4; ++n) {
+            for (int n = r; n < (kOut ? 4 : 0); ++n) {
                 ldsm(bh, ps + 16 * n * L::kPitch + lanes.down[r]);
                 mma(O[2 * n], a.hi, bh[0], bh[1]);
                 mma(O[2 * n + 1], a.hi, bh[2], bh[3]);
@@ -206,62 +216,200 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, i
         }
         if (c + kGroups < chunks) bar_arrive(kBarFree + half, all);
         if (c + 2 * kGroups < chunks) bar_arrive(kBarStage + (c & 3), all);
-        if (p.updates != nullptr) {
+        if (kOut && p.updates != nullptr) {
             rows.take(mine);
             rows.give(u_rows, o_stride, n_tokens, columns);
             u_rows += o_step;
         }
 #pragma unroll
-        for (int n = 0; n < 8; n += 2)
+        for (int n = 0; n < (kOut ? 8 : 0); n += 2)
             stsm_t(strip_rows(mine, 8 * n), pack(O[n][0], O[n][1]), pack(O[n][2], O[n][3]), pack(O[n + 1][0], O[n + 1][1]),
                    pack(O[n + 1][2], O[n + 1][3]));
         o_rows += o_step;
     }
-    StripRows rows;
-    rows.take(strips + ((chunks - 1) & 1) * L::kStrip);
-    rows.give(o_rows - o_step, o_stride, (int)(p.T - (int64_t)(chunks - 1) * C), columns);
+    if (kOut) {
+        StripRows rows;
+        rows.take(strips + ((chunks - 1) & 1) * L::kStrip);
+        rows.give(o_rows - o_step, o_stride, (int)min((int64_t)C, p.T - token0 - (int64_t)(chunks - 1) * C), columns);
+    }
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
-            if (r < p.K && cl < columns) p.h_last[state + (int64_t)r * p.V + cl] = S[i][e];
+            if (way.end != nullptr && r < p.K && cl < columns) way.end[r * way.end_row + (col0 + cl) * way.end_column] = S[i][e];
         }
 }
 
-template <int KP, int NW, int kGroups, bool kUnitRows>
+// kSegments: the second pass over segments, else whole sequences.
+template <int KP, int NW, int kGroups, bool kUnitRows, bool kSegments>
 __global__ void __launch_bounds__(kGroups * kPrep + 32 * NW, KP == 64 && NW == 4 && kGroups == 1 ? 2 : 1) delta_fwd(const __grid_constant__ Delta p) {
     extern __shared__ __align__(128) char smem[];
-    const int parts = (p.V + 16 * NW - 1) / (16 * NW), item = blockIdx.x / parts, col0 = blockIdx.x % parts * 16 * NW;
-    const int b = item / p.H, h = item % p.H;
+    const int parts = (p.V + 16 * NW - 1) / (16 * NW), col0 = blockIdx.x % parts * 16 * NW;
+    const int segment = kSegments ? 1 + blockIdx.x / parts % (p.segments - 1) : 0;
+    const int seq = kSegments ? blockIdx.x / parts / (p.segments - 1) : blockIdx.x / parts, b = seq / p.H, h = seq % p.H;
+    const int64_t state = (int64_t)seq * p.K * p.V;
+    const bool last = !kSegments || segment == p.segments - 1;
+    const Span span = kSegments ? segment_span(p, segment) : Span{0, chunk_count(p)};
+    // (the states between segments are there already)
+    const Way way = {span, kSegments ? carry_state(p, seq, segment) : p.h0 != nullptr ? p.h0 + state : nullptr,
+                     last ? p.h_last + state : nullptr, p.V, 1, false};
     const int warps = min(NW, (p.V - col0 + 15) / 16);  // that have columns
     if (threadIdx.x < kGroups * kPrep) {
         Registers<KP, NW, false, kGroups>::prepare();
-        prepare_chunks<KP, NW, false, kGroups, kUnitRows>(p, smem, b, h, 32 * warps);
+        prepare_chunks<KP, NW, false, kGroups, kUnitRows>(p, smem, b, h, span, 32 * warps);
     } else {
         Registers<KP, NW, false, kGroups>::walk();
         const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
-        if (w < warps) walk<KP, NW, kGroups, kUnitRows>(p, smem, b, h, w, col0 + 16 * w, 32 * warps);
+        if (kSegments) grid_dependency_wait();  // chunks are prepared meanwhile
+        if (w < warps) walk<KP, NW, kGroups, kUnitRows, true>(p, smem, b, h, way, w, col0 + 16 * w, 32 * warps);
     }
 }
 
-template <int KP, int NW, int kGroups>
-int launch(const Delta& p, cudaStream_t stream) {
-    using L = Layout<KP, NW, false, kGroups>;
-    const bool units = whole_units(p.k) && whole_units(p.q) && whole_units(p.v);
-    const auto kernel = units ? delta_fwd<KP, NW, kGroups, true> : delta_fwd<KP, NW, kGroups, false>;
-    static std::atomic<uint64_t> done[2];
-    if (allow_smem(kernel, L::kBytes, done[units]) != cudaSuccess) return SSDC_ERR_CUDA;
-    const int parts = (p.V + 16 * NW - 1) / (16 * NW);
-    kernel<<<p.B * p.H * parts, kGroups * kPrep + 32 * NW, L::kBytes, stream>>>(p);
+// The first pass over segments: 64 columns of the state, and 64 of the transition, to a CTA.
+template <int KP, int kGroups, bool kUnitRows>
+__global__ void __launch_bounds__(kGroups * kPrep + 256, 1) delta_fwd_carry(const __grid_constant__ Delta p) {
+    extern __shared__ __align__(128) char smem[];
+    const Carry c(p);
+    if (c.warps() == 0) return;
+    if (threadIdx.x < kGroups * kPrep) {
+        Registers<KP, 8, false, kGroups>::prepare();
+        prepare_chunks<KP, 8, false, kGroups, kUnitRows>(p, smem, c.b, c.h, c.span, 32 * c.warps());
+        launch_dependents();
+    } else {
+        Registers<KP, 8, false, kGroups>::walk();
+        const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
+        if (!c.has_columns(w)) return;
+        const Way way = c.way(p, w, p.h0);
+        if (c.segment == 0) walk<KP, 8, kGroups, kUnitRows, true>(p, smem, c.b, c.h, way, w, c.column(w), 32 * c.warps());
+        else walk<KP, 8, kGroups, kUnitRows, false>(p, smem, c.b, c.h, way, w, c.column(w), 32 * c.warps());
+    }
+}
+
+// The states between segments, 8 columns to a CTA: a thread has a row and 4 of them. A step reads the transition
+// and the segment's own part, which are fetched some steps ahead, from shared memory; its sums are in fp32.
+template <int KP>
+struct Join {
+    static constexpr int kThreads = 2 * KP, kStages = KP == 64 ? 4 : 3;
+    static constexpr int kStage = KP * KP * 4 + KP * 32;  // the transition; the own part, rows of 8 columns
+    static constexpr int kBytes = kStages * kStage;
+};
+template <int KP>
+__global__ void __launch_bounds__(2 * KP) delta_join(const __grid_constant__ Delta p) {
+    using J = Join<KP>;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ __align__(16) float states[2][KP][12];
+    const int parts = p.V / 8, seq = blockIdx.x / parts, col0 = blockIdx.x % parts * 8;
+    const int r = threadIdx.x % KP, c0 = threadIdx.x / KP * 4, steps = p.segments - 2;
+    const bool mine = r < p.K;
+    const uint32_t base = ptx::smem_addr(smem);
+    launch_dependents();
+    grid_dependency_wait();
+    auto at = [&](int m) { return carry_state(p, seq, m) + r * p.V + col0 + c0; };
+    auto fetch_step = [&](int m) {  // the m-th, from 1 on
+        if (m <= steps) {
+            const uint32_t to = base + m % J::kStages * J::kStage;
+            const float* from = carry_move(p, seq, m);
+            for (int i = threadIdx.x; i < p.K * p.K / 4; i += J::kThreads) copy16(to + 16 * i, from + 4 * i, true);
+            copy16(to + KP * KP * 4 + 32 * r + 4 * c0, mine ? at(m + 1) : p.carry, mine);
+        }
+        ptx::cp_async_commit();
+    };
+#pragma unroll
+    for (int m = 1; m < J::kStages; ++m) fetch_step(m);
+    float4 own = mine ? *reinterpret_cast<const float4*>(at(1)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int m = 1; m <= steps; ++m) {
+        float(&S)[KP][12] = states[m & 1];
+        *reinterpret_cast<float4*>(&S[r][c0]) = own;
+        ptx::cp_async_wait<J::kStages - 2>();
+        __syncthreads();
+        fetch_step(m + J::kStages - 1);
+        const float* stage = reinterpret_cast<const float*>(smem + m % J::kStages * J::kStage);
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        bool any = false;
+        if (mine) {
+#pragma unroll 8
+            for (int j = 0; j < p.K; ++j) {
+                const float v = stage[j * p.K + r];
+                const float4 s = *reinterpret_cast<const float4*>(&S[j][c0]);
+                any = any || v != 0.0f;
+                sum.x = fmaf(v, s.x, sum.x), sum.y = fmaf(v, s.y, sum.y), sum.z = fmaf(v, s.z, sum.z), sum.w = fmaf(v, s.w, sum.w);
+            }
+        }
+        own = *reinterpret_cast<const float4*>(stage + KP * KP + 8 * r + c0);
+        // a row that takes nothing (behind a reset) stays as it is, whatever the state holds
+        if (any) own.x += sum.x, own.y += sum.y, own.z += sum.z, own.w += sum.w;
+        if (mine) *reinterpret_cast<float4*>(at(m + 1)) = own;
+    }
+}
+
+template <int KP>
+int launch_join(const Delta& p, cudaStream_t stream) {
+    using J = Join<KP>;
+    static std::atomic<uint64_t> done;
+    if (allow_smem(delta_join<KP>, J::kBytes, done) != cudaSuccess) return SSDC_ERR_CUDA;
+    if (launch_dependent(delta_join<KP>, p.B * p.H * (p.V / 8), J::kThreads, J::kBytes, stream, p) != cudaSuccess) return SSDC_ERR_CUDA;
     return 1;
 }
 
+template <int KP, int NW, int kGroups, bool kSegments = false>
+int launch(const Delta& p, cudaStream_t stream) {
+    using L = Layout<KP, NW, false, kGroups>;
+    const bool units = whole_units(p.k) && whole_units(p.q) && whole_units(p.v);
+    const auto kernel = units ? delta_fwd<KP, NW, kGroups, true, kSegments> : delta_fwd<KP, NW, kGroups, false, kSegments>;
+    static std::atomic<uint64_t> done[2];
+    if (allow_smem(kernel, L::kBytes, done[units]) != cudaSuccess) return SSDC_ERR_CUDA;
+    const int parts = (p.V + 16 * NW - 1) / (16 * NW);
+    const int grid = p.B * p.H * parts * (kSegments ? p.segments - 1 : 1), threads = kGroups * kPrep + 32 * NW;
+    if (!kSegments) kernel<<<grid, threads, L::kBytes, stream>>>(p);
+    else if (launch_dependent(kernel, grid, threads, L::kBytes, stream, p) != cudaSuccess) return SSDC_ERR_CUDA;
+    return 1;
+}
+
+template <int KP, int kGroups>
+int launch_segments(const Delta& p, cudaStream_t stream) {
+    using L = Layout<KP, 8, false, kGroups>;
+    const bool units = whole_units(p.k) && whole_units(p.q) && whole_units(p.v);
+    const auto kernel = units ? delta_fwd_carry<KP, kGroups, true> : delta_fwd_carry<KP, kGroups, false>;
+    static std::atomic<uint64_t> done[2];
+    if (allow_smem(kernel, L::kBytes, done[units]) != cudaSuccess) return SSDC_ERR_CUDA;
+    kernel<<<Carry::grid(p), kGroups * kPrep + 256, L::kBytes, stream>>>(p);
+    const int joined = join_launch(p, stream), second = joined < 0 ? joined : launch<KP, 4, 2, true>(p, stream);
+    return second < 0 ? second : 1 + joined + second;
+}
+
 }  // namespace
+
+int join_launch(const Delta& p, cudaStream_t stream) { return p.K <= 64 ? launch_join<64>(p, stream) : launch_join<128>(p, stream); }
+
 }  // namespace delta
+
+// In chunks' times (2.85 us up to 64 rows, 3.85 above): both passes, whose chunks cost 1 each (above 64 rows, where
+// the first pass prepares them in one group, 1.3 there); the join's steps; and what two more launches cost, their
+// code's way from memory included. Measured, forward, whole and as chosen here: B 2 T 2048 H 16 K V 64
+// 100 / 70 us, B 1 T 65536 H 8 2,905 / 381, B 1 T 2048 H 2 98 / 52; K V 128: B 1 T 4096 H 16 258 / 176, B 1
+// T 16384 H 4 994 / 210, and not chosen B 4 T 2048 H 8 135 / 152.
+DeltaSegments delta_segments(const Delta& p) {
+    const int chunks = delta::chunk_count(p), sms = 152;
+    const int64_t most = p.bf16 ? sms / ((int64_t)p.B * p.H * delta::Carry::wide(p)) + 1 : 1;
+    DeltaSegments best = {1, chunks};
+    double least = chunks;
+    for (int n = 3; n <= most && n <= chunks; ++n) {
+        const int each = (chunks + n - 1) / n;
+        if ((chunks + each - 1) / each != n) continue;
+        const double cost = p.K > 64 ? 2.3 * each + 0.45 * (n - 2) + 12.0 : 2.0 * each + 0.4 * (n - 2) + 6.5;
+        if (cost < least) least = cost, best = {n, each};
+    }
+    return best;
+}
+size_t delta_carry_bytes(const Delta& p) {
+    const int64_t n = delta_segments(p).n;
+    return n == 1 ? 0 : (size_t)p.B * p.H * ((n - 1) * p.K * p.V + (n - 2) * p.K * p.K) * sizeof(float);
+}
 
 int delta_fwd_launch(const Delta& p, cudaStream_t stream) {
     using namespace delta;
+    if (p.segments > 1) return p.K <= 64 ? launch_segments<64, 2>(p, stream) : launch_segments<128, 1>(p, stream);
     if (few_states(p)) return p.K <= 64 ? launch<64, 4, 2>(p, stream) : launch<128, 4, 2>(p, stream);
     if (p.K <= 64) return p.V <= 64 ? launch<64, 4, 1>(p, stream) : launch<64, 8, 1>(p, stream);
     return p.V <= 64 ? launch<128, 4, 1>(p, stream) : launch<128, 8, 1>(p, stream);

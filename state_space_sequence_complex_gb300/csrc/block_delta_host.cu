@@ -77,6 +77,12 @@ Delta problem(const ssd_delta_dims& d) {
     return p;
 }
 
+// How a call takes its sequences (bfloat16).
+void segments(Delta& p, void* carry) {
+    const DeltaSegments s = delta_segments(p);
+    p.segments = s.n; p.segment_chunks = s.chunks; p.carry = static_cast<float*>(carry);
+}
+
 int check_gated_norm(int64_t M, int64_t H, int64_t D, int type) {
     if (M <= 0 || H <= 0 || D <= 0) return SSDC_ERR_INVALID;
     if (type != SSD_TYPE_F32 && type != SSD_TYPE_BF16) return SSDC_ERR_INVALID;
@@ -88,16 +94,23 @@ int check_gated_norm(int64_t M, int64_t H, int64_t D, int type) {
 
 extern "C" {
 
+size_t ssd_delta_rule_fwd_workspace_bytes(ssd_delta_dims d) {
+    if (check_delta(d) != SSDC_OK) return 0;
+    return delta_carry_bytes(problem(d));
+}
+
 int ssd_delta_rule_fwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in v, ssd_heads_in f, ssd_heads_in b, const float* h0,
                        const uint8_t* reset, ssd_delta_dims d, void* o, float* h_last, void* states, void* updates,
-                       cudaStream_t stream) {
+                       void* workspace, size_t ws_bytes, cudaStream_t stream) {
     int rc = check_delta(d);
     if (rc != SSDC_OK) return rc;
     if ((states == nullptr) != (updates == nullptr)) return SSDC_ERR_INVALID;
+    Delta p = problem(d);
+    const size_t need = delta_carry_bytes(p);
+    if (need != 0 && (workspace == nullptr || !aligned_to(workspace, 256) || ws_bytes < need)) return SSDC_ERR_WORKSPACE;
     const size_t e = type_bytes(d.type);
     const int64_t state = d.B * d.H * d.K * d.V, rows = d.B * d.T * d.H;
     Spans a;
-    Delta p = problem(d);
     p.q = a.heads(q, d, d.G, d.K); p.k = a.heads(k, d, d.G, d.K); p.v = a.heads(v, d, d.H, d.V);
     p.f = a.heads(f, d, d.H, 1); p.beta = a.heads(b, d, d.H, 1);
     a.dense_in(h0, state, 4, 16);
@@ -106,8 +119,10 @@ int ssd_delta_rule_fwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in v, ssd_heads
     a.output(h_last, state, 4, true, h0);
     a.output(states, state * chunks(d), e, false);
     a.output(updates, rows * d.V, e, false);
+    if (need != 0) a.output(workspace, (int64_t)need, 1);
     if (a.rc == SSDC_OK) a.rc = check_device();
     if (a.rc != SSDC_OK) return a.rc;
+    segments(p, workspace);
     p.h0 = h0; p.reset = reset; p.o = o; p.h_last = h_last; p.states = states; p.updates = updates;
     (void)cudaGetLastError();
     return done(p.bf16 ? delta_fwd_launch(p, stream) : delta_tokens_fwd_launch(p, stream));
@@ -143,11 +158,11 @@ int ssd_delta_rule_bwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in f, ssd_heads
                        void* dv, void* df, void* db, float* dh0, void* workspace, size_t ws_bytes, cudaStream_t stream) {
     int rc = check_delta(d);
     if (rc != SSDC_OK) return rc;
-    const size_t need = delta_bwd_workspace(problem(d)), e = type_bytes(d.type);
+    Delta p = problem(d);
+    const size_t need = delta_bwd_workspace(p), e = type_bytes(d.type);
     if (workspace == nullptr || !aligned_to(workspace, 256) || ws_bytes < need) return SSDC_ERR_WORKSPACE;
     const int64_t state = d.B * d.H * d.K * d.V, rows = d.B * d.T * d.H, key_rows = d.B * d.T * d.G;
     Spans a;
-    Delta p = problem(d);
     p.q = a.heads(q, d, d.G, d.K); p.k = a.heads(k, d, d.G, d.K);
     p.f = a.heads(f, d, d.H, 1); p.beta = a.heads(b, d, d.H, 1);
     p.d_o = a.heads(d_o, d, d.H, d.V);
@@ -164,6 +179,7 @@ int ssd_delta_rule_bwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in f, ssd_heads
     a.output(workspace, (int64_t)need, 1);
     if (a.rc == SSDC_OK) a.rc = check_device();
     if (a.rc != SSDC_OK) return a.rc;
+    segments(p, static_cast<char*>(workspace) + delta_kept_bytes(p));
     p.in_states = states; p.in_updates = updates; p.reset = reset; p.dh_last = dh_last;
     p.dq = dq; p.dk = dk; p.dv = dv; p.df = df; p.db = db; p.dh0 = dh0; p.ws = workspace;
     (void)cudaGetLastError();
@@ -277,8 +293,8 @@ int ssdc::block::delta_call(int32_t call, const int64_t* words, cudaStream_t str
             const ssd_delta_dims d = dims();
             void* o = ptr();
             float* h_last = f32();
-            void* states = ptr();
-            return ssd_delta_rule_fwd(q, k, v, f, b, h0, reset, d, o, h_last, states, ptr(), stream);
+            void *states = ptr(), *updates = ptr(), *ws = ptr();
+            return ssd_delta_rule_fwd(q, k, v, f, b, h0, reset, d, o, h_last, states, updates, ws, (size_t)i64(), stream);
         }
         case SSD_CALL_DELTA_RULE_STEP: {
             const ssd_heads_in q = heads(), k = heads(), v = heads(), f = heads(), b = heads();

@@ -33,18 +33,35 @@ struct Layout {
     static constexpr int kBytes = kScratchOff + kGroups * 4 * 16 * 16 * 4;
 };
 
+// Chunks of a sequence in the order they are taken, from the first-th on.
+struct Span {
+    int first, chunks;
+};
+__host__ __device__ __forceinline__ int chunk_count(const Delta& p) { return (int)((p.T + C - 1) / C); }
+
+// What column warps do with the chunks: from a state (null: zero) to the one behind them, whose rows and
+// columns are so far apart. Of a segment's transition, which is what becomes of the unit matrix: it
+// has no values of its own.
+struct Way {
+    Span span;
+    const float* start;
+    float* end;
+    int end_row, end_column;
+    bool unit;
+};
+
 // What prepares chunks: each of four warps fetches 16 rows of a chunk's keys and queries and takes their lengths,
 // and computes two or three of the ten 16 x 16 blocks on and below the diagonal, one of them on it. While it
 // works on one chunk, the next one's rows are on their way. Two groups of four warps take chunks in turn: where there is
 // one CTA to an SM, the preparation of a chunk takes longer than its way along the chain.
 template <int KP, int NW, bool kBack, int kGroups, bool kUnitRows>
-__device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b, int h, int column_threads) {
+__device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b, int h, const Span& span, int column_threads) {
     using L = Layout<KP, NW, kBack, kGroups>;
     constexpr int kUnits = KP / 8, kRows = 32 / kUnits;  // of a row; rows a warp fetches at once
     const uint32_t base = ptx::smem_addr(smem);
     const int mine = kGroups == 2 ? threadIdx.x / kPrep : 0;  // group
     const int tid = threadIdx.x % kPrep, warp = tid / 32, lane = tid % 32, g = h / (p.H / p.G), all = kPrep + column_threads;
-    const int chunks = (int)((p.T + C - 1) / C);
+    const int chunks = span.chunks;
     Token* const tabs = reinterpret_cast<Token*>(smem + L::kTabOff);
     float* const betas_of = reinterpret_cast<float*>(smem + L::kBetaOff);
     float* const scratch = reinterpret_cast<float*>(smem + L::kScratchOff) + (mine * 4 + warp) * 256;
@@ -54,7 +71,8 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
     const bool has_unit = fetch_u * 8 < p.K;
     // chunks are counted in the order they are taken: the n-th has the tokens from first_token(n)
     const int64_t chunk_step = kBack ? -C : C;
-    auto first_token = [&](int n) { return (kBack ? (int64_t)(chunks - 1) * C : 0) + n * chunk_step; };
+    const int64_t origin = (int64_t)(kBack ? chunk_count(p) - 1 - span.first : span.first) * C;
+    auto first_token = [&](int n) { return origin + n * chunk_step; };
     const int64_t step = kGroups * chunk_step, first = first_token(mine);
     const __nv_bfloat16* k_row = bf16(p.k.p) + b * p.k.b + g * p.k.h + (first + fetch_r) * p.k.t + (has_unit ? fetch_u * 8 : 0);
     const __nv_bfloat16* q_row = bf16(p.q.p) + b * p.q.b + g * p.q.h + (first + fetch_r) * p.q.t + (has_unit ? fetch_u * 8 : 0);
@@ -288,10 +306,10 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
 // one from 217 to 189.
 template <int KP, int NW, bool kBack, int kGroups>
 struct Registers {
-    static constexpr int kPrepare = kGroups == 2 ? 136 : NW == 8 || kBack ? 104 : 112;
-    static constexpr int kWalk = kGroups == 2 ? 232 : NW == 8 ? 200 : kBack ? 152 : 144;
+    static constexpr int kPrepare = kGroups == 2 && NW == 4 ? 136 : NW == 8 || kBack ? 104 : 112;
+    static constexpr int kWalk = kGroups == 2 ? (NW == 4 ? 232 : 152) : NW == 8 ? 200 : kBack ? 152 : 144;
     static constexpr bool kSplit = KP == 64 || NW == 8 || kGroups == 2;  // else 255 to every thread
-    static_assert(!kSplit || kGroups * 4 * kPrepare + NW * kWalk <= (kGroups * 4 + NW) * (kGroups * 4 + NW == 8 ? 128 : 168), "");
+    static_assert(!kSplit || kGroups * 4 * kPrepare + NW * kWalk <= (kGroups * 4 + NW) * (kGroups * 4 + NW == 12 ? 168 : 128), "");
     __device__ __forceinline__ static void prepare() {
         if constexpr (kSplit) ptx::regs_dec<kPrepare>();
     }
@@ -302,6 +320,51 @@ struct Registers {
 
 // Whether every SM has one CTA of 64 columns at most: then two groups prepare its chunks.
 inline bool few_states(const Delta& p) { return (int64_t)p.B * p.H * ((p.V + 63) / 64) <= device_sms(); }
+
+// A sequence in segments, where there are so few states that most SMs would have none. The update is linear in the
+// state: a segment maps it to M S + E, with M what becomes of the unit matrix without values. So
+//   first   segment 0 is taken as a whole sequence is; of the others but the last, E and M, from 64 columns of
+//           each to a CTA
+//   joined  the states between the segments, one after the other: S <- M S + E
+//   second  segments 1 and on are taken from their states
+// Backwards the same, from the last segment to the first. `carry` has for each state the n - 1 states between
+// segments ([K][V]), then the n - 2 transitions, transposed.
+__host__ __device__ __forceinline__ float* carry_state(const Delta& p, int64_t seq, int segment) {  // 1 and on: what enters it
+    return p.carry + (seq * (p.segments - 1) + segment - 1) * p.K * p.V;
+}
+__host__ __device__ __forceinline__ float* carry_move(const Delta& p, int64_t seq, int segment) {  // 1 to n - 2
+    return p.carry + (int64_t)p.B * p.H * (p.segments - 1) * p.K * p.V + (seq * (p.segments - 2) + segment - 1) * p.K * p.K;
+}
+__device__ __forceinline__ Span segment_span(const Delta& p, int segment) {
+    const int first = segment * p.segment_chunks;
+    return {first, min(p.segment_chunks, chunk_count(p) - first)};
+}
+int join_launch(const Delta& p, cudaStream_t stream);
+
+// A CTA of the first pass. Column warps 0 to 3 have columns of the state, 4 to 7 of the transition.
+struct Carry {
+    int b, h, seq, segment, part, value_warps, unit_warps;
+    Span span;
+    __device__ __forceinline__ explicit Carry(const Delta& p) {
+        const int parts = wide(p);
+        part = blockIdx.x % parts, segment = blockIdx.x / parts % (p.segments - 1), seq = blockIdx.x / parts / (p.segments - 1);
+        b = seq / p.H, h = seq % p.H;
+        value_warps = count(p.V), unit_warps = segment == 0 ? 0 : count(p.K);
+        span = segment_span(p, segment);
+    }
+    __device__ __forceinline__ int count(int columns) const { return min(4, max(0, (columns - 64 * part + 15) / 16)); }
+    __device__ __forceinline__ int warps() const { return value_warps + unit_warps; }
+    __device__ __forceinline__ bool has_columns(int w) const { return w < 4 ? w < value_warps : w - 4 < unit_warps; }
+    __device__ __forceinline__ int column(int w) const { return 64 * part + 16 * (w % 4); }
+    // `start`: the first segment's states
+    __device__ __forceinline__ Way way(const Delta& p, int w, const float* start) const {
+        const bool unit = w >= 4;
+        return {span, segment == 0 && start != nullptr ? start + (int64_t)seq * p.K * p.V : nullptr,
+                unit ? carry_move(p, seq, segment) : carry_state(p, seq, segment + 1), unit ? 1 : p.V, unit ? p.K : 1, unit};
+    }
+    __host__ __device__ __forceinline__ static int wide(const Delta& p) { return ((p.K > p.V ? p.K : p.V) + 63) / 64; }
+    __host__ static int grid(const Delta& p) { return p.B * p.H * wide(p) * (p.segments - 1); }
+};
 
 // A strip's rows on their way to memory: read here, row r of the first n goes to to + r stride. What is between the
 // two hides the reading.

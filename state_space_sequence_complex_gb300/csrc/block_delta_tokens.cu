@@ -763,7 +763,7 @@ int delta_tokens_bwd_launch(const Delta& p, cudaStream_t stream) {
 
 size_t delta_bwd_workspace(const Delta& p) {
     const int64_t rows = p.B * p.T * p.H, chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk;
-    if (p.bf16) return (size_t)(p.B * p.H * chunks * p.K * p.V) * 2;  // the states' gradients
+    if (p.bf16) return delta_kept_bytes(p) + delta_carry_bytes(p);
     return (size_t)(rows * (2 * p.K + 1) + p.B * p.H * chunks * p.K * p.V) * sizeof(float);
 }
 

@@ -171,8 +171,20 @@ struct Delta {
     void *dq, *dk, *dv, *df, *db;
     float* dh0;
     void* ws;
+    // segments of a sequence, and their chunks (block_delta_prepare.cuh): their states and transitions, or null
+    int segments, segment_chunks;
+    float* carry;
 };
+struct DeltaSegments {
+    int n, chunks;
+};
+DeltaSegments delta_segments(const Delta& p);
+size_t delta_carry_bytes(const Delta& p);  // that `carry` holds
 constexpr int kDeltaChunk = SSD_DELTA_STATE_TOKENS;
+// bfloat16: the states' gradients, with which a backward call's workspace begins; `carry` follows
+inline size_t delta_kept_bytes(const Delta& p) {
+    return ((size_t)p.B * p.H * ((p.T + kDeltaChunk - 1) / kDeltaChunk) * p.K * p.V * 2 + 255) / 256 * 256;
+}
 int delta_step_launch(const Delta& p, cudaStream_t stream);
 int delta_fwd_launch(const Delta& p, cudaStream_t stream);  // bfloat16, in chunks
 int delta_tokens_fwd_launch(const Delta& p, cudaStream_t stream);  // fp32, token by token

@@ -34,10 +34,10 @@ def dims(**k):
 
 def fwd(lib, **k):
     a = dict(q=HEADS(at(1)), k=HEADS(at(2)), v=HEADS(at(3), 4, 32), f=HEADS(at(4), 4, 1), b=HEADS(at(5), 4, 1), h0=at(6), reset=at(7),
-             o=at(8), h_last=at(9), states=at(10), updates=at(11), **DIMS)
+             o=at(8), h_last=at(9), states=at(10), updates=at(11), ws=None, ws_bytes=0, **DIMS)
     a.update(k)
     return lib.ssd_delta_rule_fwd(a["q"], a["k"], a["v"], a["f"], a["b"], a["h0"], a["reset"], dims(**{n: a[n] for n in DIMS}),
-                                  a["o"], a["h_last"], a["states"], a["updates"], None)
+                                  a["o"], a["h_last"], a["states"], a["updates"], a["ws"], a["ws_bytes"], None)
 
 
 BAD_DIMS = [
@@ -52,6 +52,7 @@ BAD_DIMS = [
 def test_dims_refused(lib, change, want):
     assert fwd(lib, **change) == want
     assert lib.ssd_delta_rule_bwd_workspace_bytes(dims(**change)) == 0
+    assert lib.ssd_delta_rule_fwd_workspace_bytes(dims(**change)) == 0
     assert bwd(lib, **change) == want
 
 
@@ -70,6 +71,17 @@ def test_dims_refused(lib, change, want):
     (dict(v=block.ssd_heads(at(3), 100 * 512, 512, 32), o=at(3) + 512), INVALID)])
 def test_forward_refuses(lib, change, want):
     assert fwd(lib, **change) == want
+
+
+LONG = dict(B=1, T=4096, H=2, G=2, v=HEADS(at(3), 2, 32, 4096))
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(), WORKSPACE), (dict(ws=at(12), ws_bytes=4096), WORKSPACE), (dict(ws=at(12) + 128, ws_bytes=1 << 30), WORKSPACE),
+    (dict(ws=at(11), ws_bytes=1 << 30), INVALID), (dict(ws=at(1), ws_bytes=1 << 30), INVALID),
+    (dict(ws=at(12), ws_bytes=1 << 30, o=at(8) + 8), ALIGN)])
+def test_forward_in_segments_refuses(lib, change, want):
+    assert fwd(lib, **LONG, **change) == want
 
 
 def bwd(lib, **k):
@@ -96,6 +108,13 @@ def test_workspace_sizes(lib):
     size = lib.ssd_delta_rule_bwd_workspace_bytes
     assert size(dims()) == 2 * 4 * 2 * 64 * 32 * 2           # the states' gradients, two chunks, in bfloat16
     assert size(dims(type=0)) > 2 * 2 * 100 * 4 * 64 * 4     # fp32: gradients of q and k for each value head too
+    # in segments: their states and transitions; whole sequences and fp32 have none
+    carry = lib.ssd_delta_rule_fwd_workspace_bytes
+    assert carry(dims()) == carry(dims(T=1)) == carry(dims(B=64, T=4096)) == carry(dims(type=0, T=1 << 16)) == 0
+    for K, V in ((64, 32), (8, 8), (128, 128), (128, 8), (72, 104)):
+        d = dims(B=1, T=4096, K=K, V=V)
+        n = (carry(d) // 16 + K * V + 2 * K * K) / (K * V + K * K)        # (n - 1) K V + (n - 2) K K floats for 4 heads
+        assert n == int(n) >= 3 and size(d) == 4 * 64 * K * V * 2 + carry(d)
 
 
 @pytest.mark.parametrize("change,want", [
@@ -153,7 +172,7 @@ def test_norm_backward_refuses(lib, change, want):
         assert lib.ssd_gated_norm_bwd_workspace_bytes(*(change.get(n, d) for n, d in (("M", 10), ("H", 4), ("D", 64)))) == 0
 
 
-@pytest.mark.parametrize("call,words", [(9, 34), (10, 31), (11, 40), (12, 17), (13, 25)])
+@pytest.mark.parametrize("call,words", [(9, 36), (10, 31), (11, 40), (12, 17), (13, 25)])
 def test_word_block_calls_refuse_what_the_calls_refuse(lib, call, words):
     none = (ctypes.c_int64 * words)()      # null addresses, zero sizes
     assert lib.ssd_block_call(call, none, None) == INVALID

@@ -36,6 +36,41 @@ def test_rows_that_start_anywhere(shape):
         close(got[n], want[n], n, "bf16")
 
 
+# few states of many tokens, which are taken in segments: a last one of a single token, of a few chunks less than the
+# others, sizes below the tiles', two parts of the state with one of the transition, and the other way round
+LONG = [(1, 2049, 2, 1, 64, 64), (1, 1500, 1, 1, 8, 128), (1, 1999, 3, 3, 128, 40), (2, 1700, 5, 5, 72, 104), (1, 3001, 1, 1, 128, 128)]
+
+
+@pytest.mark.parametrize("docs", [0.0, 0.001])
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_few_states_in_segments(shape, docs):
+    x = make(*shape, seed=sum(shape), docs=docs, state=docs == 0.0)
+    assert block.DeltaRule(*sizes(x), key_heads=shape[3]).workspace is not None
+    check(x, "bf16")
+
+
+def test_segments_without_lengths_of_one():
+    """Keys of their own length, rows that start anywhere, and the state passed on in place."""
+    B, T, H, K = 1, 1200, 2, 64
+    x = make(B, T, H, H, K, K, seed=41)
+    x["k"], x["q"] = (x["k"].float() / 8).bfloat16(), (x["q"].float() / 8).bfloat16()
+    check(x, "bf16", normalize=False)
+    y = cuda(x)
+    for n in ("q", "k", "v", "do"):
+        wide = torch.zeros(B, T, H * K + 3, dtype=torch.bfloat16, device="cuda")
+        wide[..., 1:1 + H * K] = y[n].flatten(2)
+        y[n] = wide[..., 1:1 + H * K].unflatten(-1, (H, K))
+    want = {n: t.clone() for n, t in run(cuda(x), "bf16", normalize=False).items()}
+    got = run(y, "bf16", normalize=False)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    y = cuda(x)
+    plan = block.DeltaRule(B, T, H, K, K, normalize=False)
+    plan.h_last.copy_(y["h0"])
+    o, last = plan(*(y[n] for n in NAMES), h0=plan.h_last)
+    assert torch.equal(o, want["o"]) and torch.equal(last, want["h_last"])
+
+
 def guarded(*shape, dtype):
     """A dense array with 64 guard values behind it, and the guard."""
     n = 1
@@ -46,7 +81,8 @@ def guarded(*shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("shape", [(2, 70, 3, 1, 40, 24), (20, 65, 8, 8, 64, 64), (1, 1, 1, 1, 8, 8), (2, 129, 2, 2, 128, 120)],
+@pytest.mark.parametrize("shape", [(2, 70, 3, 1, 40, 24), (20, 65, 8, 8, 64, 64), (1, 1, 1, 1, 8, 8), (2, 129, 2, 2, 128, 120),
+                                   (1, 1500, 2, 1, 40, 24)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_nothing_is_written_behind_an_output(shape, dtype):
     B, T, H, G, K, V = shape
@@ -61,13 +97,16 @@ def test_nothing_is_written_behind_an_output(shape, dtype):
         ("dh0", (B, H, K, V), torch.float32))}
     nbytes = lib.ssd_delta_rule_bwd_workspace_bytes(d)
     outs["ws"] = guarded(nbytes, dtype=torch.uint8)
+    carry = lib.ssd_delta_rule_fwd_workspace_bytes(d)
+    outs["carry"] = guarded(carry, dtype=torch.uint8)
     p = {n: t.data_ptr() for n, (t, _) in outs.items()}
-    assert lib.ssd_delta_rule_fwd(*(hd(y[n]) for n in NAMES), y["h0"].data_ptr(), None, d, p["o"], p["h_last"], p["states"], p["updates"], st) == 0
+    assert lib.ssd_delta_rule_fwd(*(hd(y[n]) for n in NAMES), y["h0"].data_ptr(), None, d, p["o"], p["h_last"], p["states"], p["updates"],
+                                  p["carry"] if carry else None, carry, st) == 0
     assert lib.ssd_delta_rule_bwd(hd(y["q"]), hd(y["k"]), hd(y["f"]), hd(y["b"]), p["states"], p["updates"], None, hd(y["do"]),
                                   y["dh_last"].data_ptr(), d, *(p[n] for n in ("dq", "dk", "dv", "df", "db", "dh0", "ws")), nbytes, st) == 0
     torch.cuda.synchronize()
     for n, (t, end) in outs.items():
-        assert (end == (7 if n == "ws" else GUARD)).all(), n
+        assert (end == (7 if n in ("ws", "carry") else GUARD)).all(), n
         if n in want:
             close(t, want[n], n, dtype)
 
@@ -113,12 +152,15 @@ def test_two_streams_at_once():
             assert torch.equal(t, w[n]), n
 
 
-@pytest.mark.parametrize("dtype,at", [("bf16", 128), ("bf16", 192), ("fp32", 128), ("fp32", 100), ("fp32", 1), ("fp32", 255)])
+@pytest.mark.parametrize("dtype,at,T", [("bf16", 128, 256), ("bf16", 192, 256), ("fp32", 128, 256), ("fp32", 100, 256), ("fp32", 1, 256),
+                                        ("fp32", 255, 256), ("bf16", 1024, 2048), ("bf16", 960, 2048), ("bf16", 64, 2048),
+                                        ("bf16", 1984, 2048)])
 @pytest.mark.parametrize("bad", ["v", "k", "h0"])
-def test_nothing_passes_a_reset(dtype, at, bad):
-    """Not an infinity or a NaN either, in either direction: in fp32 at any reset, in bfloat16 at those that begin a chunk."""
-    x = make(1, 256, 2, 2, 64, 64, dtype=dtype, seed=30)
-    x["reset"] = torch.zeros(1, 256, dtype=torch.uint8)
+def test_nothing_passes_a_reset(dtype, at, T, bad):
+    """Not an infinity or a NaN either, in either direction: in fp32 at any reset, in bfloat16 at those that begin a chunk.
+    At T 2048 in segments."""
+    x = make(1, T, 2, 2, 64, 64, dtype=dtype, seed=30)
+    x["reset"] = torch.zeros(1, T, dtype=torch.uint8)
     x["reset"][0, at] = 1
     clean = {n: t.clone() for n, t in run(cuda(x), dtype).items()}
     worse = {n: None if t is None else t.clone() for n, t in x.items()}
@@ -133,7 +175,7 @@ def test_nothing_passes_a_reset(dtype, at, bad):
     assert torch.equal(got["h_last"], clean["h_last"])
     # backwards: a NaN in the later document's gradient stays there
     worse = {n: None if t is None else t.clone() for n, t in x.items()}
-    worse["do"][0, (at + 256) // 2, 1, 3] = float("nan")
+    worse["do"][0, (at + T) // 2, 1, 3] = float("nan")
     worse["dh_last"][0, 0, 2, 2] = float("inf")
     got = run(cuda(worse), dtype)
     assert not torch.isfinite(got["dv"][0, at:, 1]).all()
