@@ -24,21 +24,23 @@ namespace delta {
 namespace {
 
 // out: with dv and the states' gradients; else only the gradient of the state in front of the chunks.
-template <int KP, int NW, int kGroups, bool kUnitRows>
+template <int KP, int NW, int kGroups, bool kUnitRows, int kPass>
 __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int h, const Way& way, bool out, int w, int col0, int column_threads) {
     using L = Layout<KP, NW, true, kGroups>;
     constexpr int KT = KP / 8;
+    const bool unit = kPass == kFirst && way.unit;
     const uint32_t base = ptx::smem_addr(smem);
     const int lane = threadIdx.x % 32, all = kPrep + column_threads;
-    const int columns = min(16, (way.unit ? p.K : p.V) - col0);
+    const int columns = min(16, (unit ? p.K : p.V) - col0);
     const int chunks = way.span.chunks, last = chunk_count(p) - 1 - way.span.first;  // the first that is taken
     auto tokens_of = [&](int c) { return (int)min((int64_t)C, p.T - (int64_t)c * C); };
+    const bool ends = kPass == kWhole || (kPass == kFirst && way.segment == 0);  // its first chunk is the sequence's last
     const int64_t seq = (int64_t)b * p.H + h;
     const uint32_t strips = base + L::kStripOff + w * 2 * L::kStrip;
     const Lanes<L::kKeyPitch> key_lanes(base);
     const Lanes<L::kPitch> lanes(base);
     const int fetch_u = lane % 2, fetch_r = lane / 2;
-    const bool has_unit = !way.unit && 8 * fetch_u < columns;
+    const bool has_unit = !unit && 8 * fetch_u < columns;
     const __nv_bfloat16* row = bf16(p.d_o.p) + b * p.d_o.b + h * p.d_o.h + ((int64_t)last * C + fetch_r) * p.d_o.t + (has_unit ? col0 + 8 * fetch_u : 0);
     auto fetch_do = [&](int n) {  // chunks from the last to the first
         const int left = tokens_of(last - n) - fetch_r;
@@ -53,14 +55,15 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
     };
     fetch_do(0);
     float S[KT][4];  // dS, as the forward kernel holds S
+    const float* from = state_in<kPass>(p, p.dh_last, seq, way);
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
-            S[i][e] = way.start != nullptr && r < p.K && cl < columns ? way.start[r * p.V + col0 + cl]
-                      : way.unit && r == col0 + cl                    ? 1.0f
-                                                                      : 0.0f;
+            S[i][e] = from != nullptr && r < p.K && cl < columns ? from[r * p.V + col0 + cl]
+                      : unit && r == col0 + cl                   ? 1.0f
+                                                                 : 0.0f;
         }
     const int64_t z_stride = (int64_t)p.H * p.V, z_step = C * z_stride;
     __nv_bfloat16* z_rows = static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + (int64_t)last * C) * p.H + h) * p.V + col0;
@@ -90,11 +93,11 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
                 mma(X[2 * m], a.lo, kb[0], kb[1]);
                 mma(X[2 * m + 1], a.lo, kb[2], kb[3]);
             }
-            if (out && s == 0 && n > 0) rows.give(z_rows + z_step, z_stride, tokens_of(c + 1), columns);
+            if (out && s == 0 && n > 0) rows.give(z_rows + z_step, z_stride, n == 1 && ends ? tokens_of(last) : C, columns);
             if (out && s % 4 == 3) {
                 const int first = s / 4 * C;
                 rows.take(other);
-                rows.give(static_cast<__nv_bfloat16*>(p.ws) + (seq * chunk_count(p) + c) * p.K * p.V + (int64_t)first * p.V + col0, p.V,
+                rows.give(static_cast<__nv_bfloat16*>(p.ws) + ((kPass == kWhole ? seq * chunks : seq * chunk_count(p)) + c) * p.K * p.V + (int64_t)first * p.V + col0, p.V,
                           p.K - first, columns);
             }
         }
@@ -208,15 +211,15 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         rows.take(strips + ((chunks - 1) & 1) * L::kStrip);
         rows.give(z_rows + z_step, z_stride, tokens_of(last - chunks + 1), columns);
     }
-    if (way.end != nullptr) {
+    float* to = state_out<kPass>(p, p.dh0, seq, way);
+    if (to == nullptr) return;
 #pragma unroll
-        for (int i = 0; i < KT; ++i)
+    for (int i = 0; i < KT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
-                if (r < p.K && cl < columns) way.end[r * way.end_row + (col0 + cl) * way.end_column] = S[i][e];
-            }
-    }
+        for (int e = 0; e < 4; ++e) {
+            const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = col0 + lane / 4 + 8 * (e / 2);
+            if (r < p.K && cl < col0 + columns) to[unit ? cl * p.K + r : r * p.V + cl] = S[i][e];
+        }
 }
 
 template <int KP, int NW, int kGroups, bool kUnitRows, bool kSegments>
@@ -225,11 +228,8 @@ __global__ void __launch_bounds__(kGroups * kPrep + 32 * NW, KP == 64 && NW == 4
     const int parts = (p.V + 16 * NW - 1) / (16 * NW), col0 = blockIdx.x % parts * 16 * NW;
     const int segment = kSegments ? 1 + blockIdx.x / parts % (p.segments - 1) : 0;
     const int seq = kSegments ? blockIdx.x / parts / (p.segments - 1) : blockIdx.x / parts, b = seq / p.H, h = seq % p.H;
-    const int64_t state = (int64_t)seq * p.K * p.V;
-    const bool all = !kSegments || segment == p.segments - 1;  // up to the first token
     const Span span = kSegments ? segment_span(p, segment) : Span{0, chunk_count(p)};
-    const Way way = {span, kSegments ? carry_state(p, seq, segment) : p.dh_last != nullptr ? p.dh_last + state : nullptr,
-                     all && p.dh0 != nullptr ? p.dh0 + state : nullptr, p.V, 1, false};
+    const Way way = {span, segment, false};
     const int warps = min(NW, (p.V - col0 + 15) / 16);
     if (threadIdx.x < kGroups * kPrep) {
         Registers<KP, NW, true, kGroups>::prepare();
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kGroups * kPrep + 32 * NW, KP == 64 && NW == 4
         Registers<KP, NW, true, kGroups>::walk();
         const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
         if (kSegments) grid_dependency_wait();  // chunks are prepared meanwhile
-        if (w < warps) walk_back<KP, NW, kGroups, kUnitRows>(p, smem, b, h, way, true, w, col0 + 16 * w, 32 * warps);
+        if (w < warps) walk_back<KP, NW, kGroups, kUnitRows, kSegments ? kSecond : kWhole>(p, smem, b, h, way, true, w, col0 + 16 * w, 32 * warps);
     }
 }
 
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kGroups * kPrep + 256, 1) delta_bwd_carry(cons
         Registers<KP, 8, true, kGroups>::walk();
         const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
         if (c.has_columns(w))
-            walk_back<KP, 8, kGroups, kUnitRows>(p, smem, c.b, c.h, c.way(p, w, p.dh_last), c.segment == 0, w, c.column(w), 32 * c.warps());
+            walk_back<KP, 8, kGroups, kUnitRows, kFirst>(p, smem, c.b, c.h, c.way(w), c.segment == 0, w, c.column(w), 32 * c.warps());
     }
 }
 

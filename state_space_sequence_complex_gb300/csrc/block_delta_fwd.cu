@@ -19,20 +19,21 @@ namespace delta {
 namespace {
 
 // kOut: with o, and states and updates where they are asked for; else only the state behind the chunks.
-template <int KP, int NW, int kGroups, bool kUnitRows, bool kOut>
+template <int KP, int NW, int kGroups, bool kUnitRows, int kPass, bool kOut>
 __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, const Way& way, int w, int col0, int column_threads) {
     using L = Layout<KP, NW, false, kGroups>;
     constexpr int KT = KP / 8;  // 8-row tiles of the state
+    const bool unit = kPass == kFirst && !kOut && way.unit;
     const uint32_t base = ptx::smem_addr(smem);
     const int lane = threadIdx.x % 32, all = kPrep + column_threads;
-    const int columns = min(16, (way.unit ? p.K : p.V) - col0);
+    const int columns = min(16, (unit ? p.K : p.V) - col0);
     const int chunks = way.span.chunks;
     const int64_t seq = (int64_t)b * p.H + h, token0 = (int64_t)way.span.first * C;
     const uint32_t strips = base + L::kStripOff + w * 2 * L::kStrip;
     const Lanes<L::kKeyPitch> key_lanes(base);
     const Lanes<L::kPitch> lanes(base);
     const int fetch_u = lane % 2, fetch_r = lane / 2;
-    const bool has_unit = !way.unit && 8 * fetch_u < columns;
+    const bool has_unit = !unit && 8 * fetch_u < columns;
     const __nv_bfloat16* v_row = bf16(p.v.p) + b * p.v.b + h * p.v.h + (token0 + fetch_r) * p.v.t + (has_unit ? col0 + 8 * fetch_u : 0);
     auto fetch_v = [&](int c) {  // chunks in order
         const int left = (int)min((int64_t)C, p.T - token0 - (int64_t)c * C) - fetch_r;
@@ -48,14 +49,15 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, c
     fetch_v(0);
     // state[row 8 i + 2 (lane % 4) + e % 2][column lane / 4 + 8 (e / 2)]
     float S[KT][4];
+    const float* from = state_in<kPass>(p, p.h0, seq, way);
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
-            S[i][e] = way.start != nullptr && r < p.K && cl < columns ? way.start[r * p.V + col0 + cl]
-                      : !kOut && way.unit && r == col0 + cl           ? 1.0f
-                                                                      : 0.0f;
+            S[i][e] = from != nullptr && r < p.K && cl < columns ? from[r * p.V + col0 + cl]
+                      : unit && r == col0 + cl                   ? 1.0f
+                                                                 : 0.0f;
         }
     const int64_t o_stride = (int64_t)p.H * p.V, o_step = C * o_stride, o_first = ((b * p.T + token0) * p.H + h) * p.V + col0;
     __nv_bfloat16* o_rows = static_cast<__nv_bfloat16*>(p.o) + o_first;
@@ -100,7 +102,8 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, c
             if (kOut && p.states != nullptr && it % 16 == 15) {
                 const int first = it / 16 * C;
                 rows.take(other);
-                rows.give(static_cast<__nv_bfloat16*>(p.states) + (seq * chunk_count(p) + way.span.first + c) * p.K * p.V + (int64_t)first * p.V + col0,
+                const int64_t at = kPass == kWhole ? seq * chunks + c : seq * chunk_count(p) + way.span.first + c;
+                rows.give(static_cast<__nv_bfloat16*>(p.states) + at * p.K * p.V + (int64_t)first * p.V + col0,
                           p.V, p.K - first, columns);
             }
         }
@@ -232,12 +235,14 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, c
         rows.take(strips + ((chunks - 1) & 1) * L::kStrip);
         rows.give(o_rows - o_step, o_stride, (int)min((int64_t)C, p.T - token0 - (int64_t)(chunks - 1) * C), columns);
     }
+    float* to = state_out<kPass>(p, p.h_last, seq, way);
+    if (to == nullptr) return;
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = lane / 4 + 8 * (e / 2);
-            if (way.end != nullptr && r < p.K && cl < columns) way.end[r * way.end_row + (col0 + cl) * way.end_column] = S[i][e];
+            const int r = 8 * i + 2 * (lane % 4) + e % 2, cl = col0 + lane / 4 + 8 * (e / 2);
+            if (r < p.K && cl < col0 + columns) to[unit ? cl * p.K + r : r * p.V + cl] = S[i][e];
         }
 }
 
@@ -248,12 +253,8 @@ __global__ void __launch_bounds__(kGroups * kPrep + 32 * NW, KP == 64 && NW == 4
     const int parts = (p.V + 16 * NW - 1) / (16 * NW), col0 = blockIdx.x % parts * 16 * NW;
     const int segment = kSegments ? 1 + blockIdx.x / parts % (p.segments - 1) : 0;
     const int seq = kSegments ? blockIdx.x / parts / (p.segments - 1) : blockIdx.x / parts, b = seq / p.H, h = seq % p.H;
-    const int64_t state = (int64_t)seq * p.K * p.V;
-    const bool last = !kSegments || segment == p.segments - 1;
     const Span span = kSegments ? segment_span(p, segment) : Span{0, chunk_count(p)};
-    // (the states between segments are there already)
-    const Way way = {span, kSegments ? carry_state(p, seq, segment) : p.h0 != nullptr ? p.h0 + state : nullptr,
-                     last ? p.h_last + state : nullptr, p.V, 1, false};
+    const Way way = {span, segment, false};
     const int warps = min(NW, (p.V - col0 + 15) / 16);  // that have columns
     if (threadIdx.x < kGroups * kPrep) {
         Registers<KP, NW, false, kGroups>::prepare();
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kGroups * kPrep + 32 * NW, KP == 64 && NW == 4
         Registers<KP, NW, false, kGroups>::walk();
         const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
         if (kSegments) grid_dependency_wait();  // chunks are prepared meanwhile
-        if (w < warps) walk<KP, NW, kGroups, kUnitRows, true>(p, smem, b, h, way, w, col0 + 16 * w, 32 * warps);
+        if (w < warps) walk<KP, NW, kGroups, kUnitRows, kSegments ? kSecond : kWhole, true>(p, smem, b, h, way, w, col0 + 16 * w, 32 * warps);
     }
 }
 
@@ -280,9 +281,8 @@ __global__ void __launch_bounds__(kGroups * kPrep + 256, 1) delta_fwd_carry(cons
         Registers<KP, 8, false, kGroups>::walk();
         const int w = threadIdx.x / 32 - kGroups * kPrep / 32;
         if (!c.has_columns(w)) return;
-        const Way way = c.way(p, w, p.h0);
-        if (c.segment == 0) walk<KP, 8, kGroups, kUnitRows, true>(p, smem, c.b, c.h, way, w, c.column(w), 32 * c.warps());
-        else walk<KP, 8, kGroups, kUnitRows, false>(p, smem, c.b, c.h, way, w, c.column(w), 32 * c.warps());
+        if (c.segment == 0) walk<KP, 8, kGroups, kUnitRows, kFirst, true>(p, smem, c.b, c.h, c.way(w), w, c.column(w), 32 * c.warps());
+        else walk<KP, 8, kGroups, kUnitRows, kFirst, false>(p, smem, c.b, c.h, c.way(w), w, c.column(w), 32 * c.warps());
     }
 }
 

@@ -39,14 +39,12 @@ struct Span {
 };
 __host__ __device__ __forceinline__ int chunk_count(const Delta& p) { return (int)((p.T + C - 1) / C); }
 
-// What column warps do with the chunks: from a state (null: zero) to the one behind them, whose rows and
-// columns are so far apart. Of a segment's transition, which is what becomes of the unit matrix: it
-// has no values of its own.
+// Where column warps walk: whole sequences, or segments in the first or the second pass over them; then which one, and
+// whether they carry columns of its transition, which is what becomes of the unit matrix without values.
+enum : int { kWhole, kFirst, kSecond };
 struct Way {
     Span span;
-    const float* start;
-    float* end;
-    int end_row, end_column;
+    int segment;
     bool unit;
 };
 
@@ -121,11 +119,10 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
         const float v = __uint_as_float((uint32_t)gate << 16), e = expf(-fabsf(v));
         // log2 of sigmoid(f), not below -256
         const float s = log1pf(e), l = v >= 0.0f ? -s : v - s, lg = l < -177.0f ? -256.0f : l * kLog2e;
-        // Sums of integers hold no NaN: one in f, of a token without a mark, is handed on in its beta.
-        const bool bad = there && mark == 0 && v != v;
-        const bool bad_f = __shfl_sync(0xffffffffu, bad, lane % 16);
-        if (lane >= 16) betas_of[set * C + gate_r] = !there ? 0.0f : bad_f ? __int_as_float(0x7fffffff) : (v >= 0.0f ? 1.0f : e) / (1.0f + e);
-        scan_group<false>(!there || bad ? 0.0f : mark != 0 ? -256.0f : lg, tabs + set * C + 16 * warp);
+        if (lane >= 16) betas_of[set * C + gate_r] = there ? (v >= 0.0f ? 1.0f : e) / (1.0f + e) : 0.0f;
+        // Sums of integers hold no NaN: with 10^5 of log2 for one in f every decay across its token is infinite, and
+        // what is made of that in two parts is a NaN.
+        scan_group<false>(!there ? 0.0f : mark != 0 ? -256.0f : fminf(lg, 1e5f), tabs + set * C + 16 * warp);
         ptx::cp_async_wait<0>();
     };
 
@@ -302,12 +299,12 @@ __device__ __forceinline__ void prepare_chunks(const Delta& p, char* smem, int b
 
 // A CTA's registers: fewer to the warps that prepare, more to those with columns, within what it was launched with (128
 // to a thread where two CTAs share an SM, 168 with 12 warps). Spilled registers cost the most where two CTAs share an SM:
-// 112 and 144 against 96 and 160 took the forward pass of 256 states from 202 to 194 us, 104 and 152 the backward
-// one from 217 to 189.
+// 112 and 144 against 96 and 160 took the forward pass of 256 states from 202 to 194 us; against 104 and 152 the
+// backward one from 205 to 187.
 template <int KP, int NW, bool kBack, int kGroups>
 struct Registers {
-    static constexpr int kPrepare = kGroups == 2 && NW == 4 ? 136 : NW == 8 || kBack ? 104 : 112;
-    static constexpr int kWalk = kGroups == 2 ? (NW == 4 ? 232 : 152) : NW == 8 ? 200 : kBack ? 152 : 144;
+    static constexpr int kPrepare = kGroups == 2 && NW == 4 ? 136 : NW == 8 ? 104 : 112;
+    static constexpr int kWalk = kGroups == 2 ? (NW == 4 ? 232 : 152) : NW == 8 ? 200 : 144;
     static constexpr bool kSplit = KP == 64 || NW == 8 || kGroups == 2;  // else 255 to every thread
     static_assert(!kSplit || kGroups * 4 * kPrepare + NW * kWalk <= (kGroups * 4 + NW) * (kGroups * 4 + NW == 12 ? 168 : 128), "");
     __device__ __forceinline__ static void prepare() {
@@ -335,6 +332,17 @@ __host__ __device__ __forceinline__ float* carry_state(const Delta& p, int64_t s
 __host__ __device__ __forceinline__ float* carry_move(const Delta& p, int64_t seq, int segment) {  // 1 to n - 2
     return p.carry + (int64_t)p.B * p.H * (p.segments - 1) * p.K * p.V + (seq * (p.segments - 2) + segment - 1) * p.K * p.K;
 }
+// The states that a walk begins from (or null: zero) and leaves (or null), of those in front of and behind the sequences.
+template <int kPass>
+__device__ __forceinline__ const float* state_in(const Delta& p, const float* front, int64_t seq, const Way& way) {
+    if (kPass == kSecond) return carry_state(p, seq, way.segment);
+    return front != nullptr && (kPass == kWhole || way.segment == 0) ? front + seq * p.K * p.V : nullptr;
+}
+template <int kPass>
+__device__ __forceinline__ float* state_out(const Delta& p, float* behind, int64_t seq, const Way& way) {
+    if (kPass == kFirst) return way.unit ? carry_move(p, seq, way.segment) : carry_state(p, seq, way.segment + 1);
+    return behind != nullptr && (kPass == kWhole || way.segment == p.segments - 1) ? behind + seq * p.K * p.V : nullptr;
+}
 __device__ __forceinline__ Span segment_span(const Delta& p, int segment) {
     const int first = segment * p.segment_chunks;
     return {first, min(p.segment_chunks, chunk_count(p) - first)};
@@ -356,12 +364,7 @@ struct Carry {
     __device__ __forceinline__ int warps() const { return value_warps + unit_warps; }
     __device__ __forceinline__ bool has_columns(int w) const { return w < 4 ? w < value_warps : w - 4 < unit_warps; }
     __device__ __forceinline__ int column(int w) const { return 64 * part + 16 * (w % 4); }
-    // `start`: the first segment's states
-    __device__ __forceinline__ Way way(const Delta& p, int w, const float* start) const {
-        const bool unit = w >= 4;
-        return {span, segment == 0 && start != nullptr ? start + (int64_t)seq * p.K * p.V : nullptr,
-                unit ? carry_move(p, seq, segment) : carry_state(p, seq, segment + 1), unit ? 1 : p.V, unit ? p.K : 1, unit};
-    }
+    __device__ __forceinline__ Way way(int w) const { return {span, segment, w >= 4}; }
     __host__ __device__ __forceinline__ static int wide(const Delta& p) { return ((p.K > p.V ? p.K : p.V) + 63) / 64; }
     __host__ static int grid(const Delta& p) { return p.B * p.H * wide(p) * (p.segments - 1); }
 };
