@@ -263,8 +263,7 @@ typedef struct {
  *             (B, H, ceil(T / that), K, V), and u (B, T, H, V), both of `type`
  *   workspace ssd_delta_rule_fwd_workspace_bytes() bytes, 256-byte aligned, its contents
  *             need not be kept; NULL where that is 0
- * One launch; BF16 sequences much longer than the states are many: three, with a workspace, in segments that are
- * taken at once and joined.
+ * One launch; few long sequences: three, with a workspace, in segments that are taken at once and joined.
  */
 #define SSD_DELTA_STATE_TOKENS 64
 size_t ssd_delta_rule_fwd_workspace_bytes(ssd_delta_dims dims);
@@ -289,7 +288,7 @@ int ssd_delta_rule_step(ssd_heads_in q, ssd_heads_in k, ssd_heads_in v, ssd_head
  *   dh0       output (B, H, K, V) fp32, or NULL; it may be dh_last
  *   workspace ssd_delta_rule_bwd_workspace_bytes() bytes, 256-byte aligned, its
  *             contents need not be kept
- * df is 0 at a reset. Sums run in a fixed order. Two launches (in segments four, F32 four).
+ * df is 0 at a reset. Sums run in a fixed order. Two launches (BF16 in segments four; F32 four).
  */
 size_t ssd_delta_rule_bwd_workspace_bytes(ssd_delta_dims dims);
 int ssd_delta_rule_bwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in f, ssd_heads_in b, const void *states,

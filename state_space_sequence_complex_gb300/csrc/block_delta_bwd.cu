@@ -735,7 +735,7 @@ int launch_segments(const Delta& p, cudaStream_t stream) {
     static std::atomic<uint64_t> done[2];
     if (allow_smem(kernel, L::kBytes, done[units]) != cudaSuccess) return SSDC_ERR_CUDA;
     kernel<<<Carry::grid(p), kGroups * kPrep + 256, L::kBytes, stream>>>(p);
-    const int joined = join_launch(p, stream), second = joined < 0 ? joined : launch_chain<KP, 4, 2, true>(p, stream);
+    const int joined = delta_join_launch(p, stream), second = joined < 0 ? joined : launch_chain<KP, 4, 2, true>(p, stream);
     return second < 0 ? second : 1 + joined + second;
 }
 

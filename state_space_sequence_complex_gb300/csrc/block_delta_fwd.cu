@@ -374,30 +374,34 @@ int launch_segments(const Delta& p, cudaStream_t stream) {
     static std::atomic<uint64_t> done[2];
     if (allow_smem(kernel, L::kBytes, done[units]) != cudaSuccess) return SSDC_ERR_CUDA;
     kernel<<<Carry::grid(p), kGroups * kPrep + 256, L::kBytes, stream>>>(p);
-    const int joined = join_launch(p, stream), second = joined < 0 ? joined : launch<KP, 4, 2, true>(p, stream);
+    const int joined = delta_join_launch(p, stream), second = joined < 0 ? joined : launch<KP, 4, 2, true>(p, stream);
     return second < 0 ? second : 1 + joined + second;
 }
 
 }  // namespace
 
-int join_launch(const Delta& p, cudaStream_t stream) { return p.K <= 64 ? launch_join<64>(p, stream) : launch_join<128>(p, stream); }
-
 }  // namespace delta
+
+int delta_join_launch(const Delta& p, cudaStream_t stream) {
+    return p.K <= 64 ? delta::launch_join<64>(p, stream) : delta::launch_join<128>(p, stream);
+}
 
 // In chunks' times (2.85 us up to 64 rows, 3.85 above): both passes, whose chunks cost 1 each (above 64 rows, where
 // the first pass prepares them in one group, 1.3 there); the join's steps; and what two more launches cost, their
 // code's way from memory included. Measured, forward, whole and as chosen here: B 2 T 2048 H 16 K V 64
 // 100 / 70 us, B 1 T 65536 H 8 2,905 / 381, B 1 T 2048 H 2 98 / 52; K V 128: B 1 T 4096 H 16 258 / 176, B 1
 // T 16384 H 4 994 / 210, and not chosen B 4 T 2048 H 8 135 / 152.
+// fp32: a chunk's 64 tokens take 29 us, also where an SM has two CTAs (registers leave room for one above 64 rows).
 DeltaSegments delta_segments(const Delta& p) {
     const int chunks = delta::chunk_count(p), sms = 152;
-    const int64_t most = p.bf16 ? sms / ((int64_t)p.B * p.H * delta::Carry::wide(p)) + 1 : 1;
+    const int64_t states = (int64_t)p.B * p.H;
+    const int64_t most = p.bf16 ? sms / (states * delta::Carry::wide(p)) + 1 : (sms * (p.K > 64 ? 1 : 2) / states + 3) / 2;
     DeltaSegments best = {1, chunks};
     double least = chunks;
     for (int n = 3; n <= most && n <= chunks; ++n) {
         const int each = (chunks + n - 1) / n;
         if ((chunks + each - 1) / each != n) continue;
-        const double cost = p.K > 64 ? 2.3 * each + 0.45 * (n - 2) + 12.0 : 2.0 * each + 0.4 * (n - 2) + 6.5;
+        const double cost = !p.bf16 ? 2.0 * each + 0.05 * (n - 2) + 0.5 : p.K > 64 ? 2.3 * each + 0.45 * (n - 2) + 12.0 : 2.0 * each + 0.4 * (n - 2) + 6.5;
         if (cost < least) least = cost, best = {n, each};
     }
     return best;

@@ -77,7 +77,7 @@ Delta problem(const ssd_delta_dims& d) {
     return p;
 }
 
-// How a call takes its sequences (bfloat16).
+// How a call takes its sequences.
 void segments(Delta& p, void* carry) {
     const DeltaSegments s = delta_segments(p);
     p.segments = s.n; p.segment_chunks = s.chunks; p.carry = static_cast<float*>(carry);
@@ -179,7 +179,7 @@ int ssd_delta_rule_bwd(ssd_heads_in q, ssd_heads_in k, ssd_heads_in f, ssd_heads
     a.output(workspace, (int64_t)need, 1);
     if (a.rc == SSDC_OK) a.rc = check_device();
     if (a.rc != SSDC_OK) return a.rc;
-    segments(p, static_cast<char*>(workspace) + delta_kept_bytes(p));
+    if (p.bf16) segments(p, static_cast<char*>(workspace) + delta_kept_bytes(p));
     p.in_states = states; p.in_updates = updates; p.reset = reset; p.dh_last = dh_last;
     p.dq = dq; p.dk = dk; p.dv = dv; p.df = df; p.db = db; p.dh0 = dh0; p.ws = workspace;
     (void)cudaGetLastError();

@@ -39,9 +39,7 @@ struct Span {
 };
 __host__ __device__ __forceinline__ int chunk_count(const Delta& p) { return (int)((p.T + C - 1) / C); }
 
-// Where column warps walk: whole sequences, or segments in the first or the second pass over them; then which one, and
-// whether they carry columns of its transition, which is what becomes of the unit matrix without values.
-enum : int { kWhole, kFirst, kSecond };
+// Where column warps walk: which segment, and whether they carry columns of its transition.
 struct Way {
     Span span;
     int segment;
@@ -318,20 +316,6 @@ struct Registers {
 // Whether every SM has one CTA of 64 columns at most: then two groups prepare its chunks.
 inline bool few_states(const Delta& p) { return (int64_t)p.B * p.H * ((p.V + 63) / 64) <= device_sms(); }
 
-// A sequence in segments, where there are so few states that most SMs would have none. The update is linear in the
-// state: a segment maps it to M S + E, with M what becomes of the unit matrix without values. So
-//   first   segment 0 is taken as a whole sequence is; of the others but the last, E and M, from 64 columns of
-//           each to a CTA
-//   joined  the states between the segments, one after the other: S <- M S + E
-//   second  segments 1 and on are taken from their states
-// Backwards the same, from the last segment to the first. `carry` has for each state the n - 1 states between
-// segments ([K][V]), then the n - 2 transitions, transposed.
-__host__ __device__ __forceinline__ float* carry_state(const Delta& p, int64_t seq, int segment) {  // 1 and on: what enters it
-    return p.carry + (seq * (p.segments - 1) + segment - 1) * p.K * p.V;
-}
-__host__ __device__ __forceinline__ float* carry_move(const Delta& p, int64_t seq, int segment) {  // 1 to n - 2
-    return p.carry + (int64_t)p.B * p.H * (p.segments - 1) * p.K * p.V + (seq * (p.segments - 2) + segment - 1) * p.K * p.K;
-}
 // The states that a walk begins from (or null: zero) and leaves (or null), of those in front of and behind the sequences.
 template <int kPass>
 __device__ __forceinline__ const float* state_in(const Delta& p, const float* front, int64_t seq, const Way& way) {
@@ -347,8 +331,6 @@ __device__ __forceinline__ Span segment_span(const Delta& p, int segment) {
     const int first = segment * p.segment_chunks;
     return {first, min(p.segment_chunks, chunk_count(p) - first)};
 }
-int join_launch(const Delta& p, cudaStream_t stream);
-
 // A CTA of the first pass. Column warps 0 to 3 have columns of the state, 4 to 7 of the transition.
 struct Carry {
     int b, h, seq, segment, part, value_warps, unit_warps;

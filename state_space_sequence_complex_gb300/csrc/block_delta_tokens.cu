@@ -4,6 +4,8 @@
 // dot product with k_t, and S = c S + k_t u_t^T adds to it. So a warp holds 16 columns in registers,
 // 8 lanes to a column that have every 8th group of 4 rows each, and walks the tokens without a barrier
 // inside a tile of them; a CTA has all columns of one state, as the gradients of q and k sum over them.
+#include <algorithm>
+
 #include "block_common.cuh"
 #include "block_kernels.h"
 #include "ssdc_kernels.h"
@@ -91,6 +93,19 @@ struct Columns {  // a lane's part of a warp's 16 columns: rows 32 (i / 4) + 4 (
             for (int j = 0; j < 4; ++j)
                 if (row(i) < K && col() < V) p[(int64_t)row(i) * V + col() + j] = s[i][j];
     }
+    __device__ __forceinline__ void store_transposed(float* p, int K) const {
+#pragma unroll
+        for (int i = 0; i < KR; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (row(i) < K && col() < K) p[(col() + j) * K + row(i)] = s[i][j];
+    }
+    __device__ __forceinline__ void unit() {
+#pragma unroll
+        for (int i = 0; i < KR; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = row(i) == col() + j ? 1.0f : 0.0f;
+    }
     __device__ __forceinline__ static void vec(float* x, const float* from) {
 #pragma unroll
         for (int i = 0; i < KR; i += 4) {
@@ -158,12 +173,21 @@ __device__ __forceinline__ void copy4(float* to, const float* from, bool valid) 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_addr(to)), "l"(from), "r"(valid ? 4 : 0) : "memory");
 }
 
-template <int KR>
+// kPass: whole sequences, or the first or second pass over segments. In the first one there are, for a state, segment 0
+// and then of each other segment but the last the transition and the state from zero.
+template <int KR, int kPass>
 __global__ void __launch_bounds__(256) delta_tokens_fwd(const __grid_constant__ Delta p) {
     extern __shared__ __align__(16) char smem[];
     FwdShared& sm = *reinterpret_cast<FwdShared*>(smem);
-    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, g = h / (p.H / p.G), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk, seq = (int64_t)b * p.H + h, size = (int64_t)p.K * p.V;
+    const int each = kPass == kWhole ? 1 : kPass == kFirst ? 2 * p.segments - 3 : p.segments - 1, item = blockIdx.x % each;
+    const int segment = kPass == kWhole ? 0 : kPass == kFirst ? (item + 1) / 2 : item + 1;
+    const bool unit = kPass == kFirst && item % 2 == 1, out = kPass != kFirst || item == 0;
+    const int64_t seq = blockIdx.x / each;
+    const int b = (int)(seq / p.H), h = (int)(seq % p.H), g = h / (p.H / p.G), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t chunks = (p.T + kDeltaChunk - 1) / kDeltaChunk, size = (int64_t)p.K * p.V;
+    const int64_t begin = kPass == kWhole ? 0 : (int64_t)segment * p.segment_chunks * kDeltaChunk;
+    const int64_t end = kPass == kWhole ? p.T : min(p.T, begin + (int64_t)p.segment_chunks * kDeltaChunk);
+    const int values = unit ? 0 : p.V;  // of a token
     const float q_scale = p.normalize ? rsqrtf((float)p.K) : 1.0f;
     const float *q0 = row<float>(p.q, b, 0, g), *k0 = row<float>(p.k, b, 0, g), *v0 = row<float>(p.v, b, 0, h);
     const int warps = blockDim.x / 32;
@@ -172,26 +196,33 @@ __global__ void __launch_bounds__(256) delta_tokens_fwd(const __grid_constant__ 
         const float *q = q0 + (t0 + warp) * p.q.t + lane, *k = k0 + (t0 + warp) * p.k.t + lane, *v = v0 + (t0 + warp) * p.v.t + lane;
         const int64_t q_step = warps * p.q.t, k_step = warps * p.k.t, v_step = warps * p.v.t;
         for (int i = warp; i < kFwdTile; i += warps) {
-            const bool there = t0 + i < p.T;
+            const bool there = t0 + i < end;
 #pragma unroll
             for (int d = 0; d < 8 * KR; d += 32) {
                 copy4(&to.q[i][lane + d], q + d, there && lane + d < p.K);
                 copy4(&to.k[i][lane + d], k + d, there && lane + d < p.K);
             }
-            for (int d = 0; d < 16 * warps; d += 32) copy4(&to.v[i][lane + d], v + d, there && lane + d < p.V);
+            for (int d = 0; d < 16 * warps; d += 32) copy4(&to.v[i][lane + d], v + d, there && lane + d < values);
             q += q_step, k += k_step, v += v_step;
         }
         ptx::cp_async_commit();
     };
-    fetch(0);
+    if (kPass == kFirst) launch_dependents();
+    fetch(begin);
     Columns<KR> S;
-    S.load(p.h0 ? p.h0 + seq * size : nullptr, p.K, p.V);
-    for (int64_t t0 = 0; t0 < p.T; t0 += kFwdTile) {
+    if (kPass == kSecond) {
+        grid_dependency_wait();
+        S.load(carry_state(p, seq, segment), p.K, p.V);
+    } else {
+        S.load(segment == 0 && p.h0 ? p.h0 + seq * size : nullptr, p.K, p.V);
+        if (unit) S.unit();
+    }
+    for (int64_t t0 = begin; t0 < end; t0 += kFwdTile) {
         FwdTile& tile = sm.tile[t0 / kFwdTile & 1];
         ptx::cp_async_wait<0>();
         __syncthreads();  // this tile is there, and the last one is through
-        if (t0 + kFwdTile < p.T) fetch(t0 + kFwdTile);
-        const int n = (int)min((int64_t)kFwdTile, p.T - t0);
+        if (t0 + kFwdTile < end) fetch(t0 + kFwdTile);
+        const int n = (int)min((int64_t)kFwdTile, end - t0);
         // lengths, q.k and gates: eight lanes to a token
         for (int t = 4 * warp + lane / 8; t - lane / 8 < n; t += 4 * warps) {
             const int there = min(t, kFwdTile - 1);
@@ -214,7 +245,7 @@ __global__ void __launch_bounds__(256) delta_tokens_fwd(const __grid_constant__ 
             }
         }
         __syncthreads();
-        if (p.states != nullptr && t0 % kDeltaChunk == 0)
+        if (out && p.states != nullptr && t0 % kDeltaChunk == 0)
             S.store(static_cast<float*>(p.states) + (seq * chunks + t0 / kDeltaChunk) * size, p.K, p.V);
         float k[KR], q[KR];
         S.vec(k, tile.k[0]);
@@ -279,13 +310,15 @@ __global__ void __launch_bounds__(256) delta_tokens_fwd(const __grid_constant__ 
         }
         __syncthreads();
         const int64_t at = (b * p.T + t0) * p.H + h;
-        for (int t = warp; t < n; t += blockDim.x / 32)
+        for (int t = warp; t < (out ? n : 0); t += blockDim.x / 32)
             for (int d = lane; d < p.V; d += 32) {
                 static_cast<float*>(p.o)[(at + (int64_t)t * p.H) * p.V + d] = sm.o[t][d];
                 if (p.updates != nullptr) static_cast<float*>(p.updates)[(at + (int64_t)t * p.H) * p.V + d] = sm.u[t][d];
             }
     }
-    S.store(p.h_last + seq * size, p.K, p.V);
+    if (unit) S.store_transposed(carry_move(p, seq, segment), p.K);
+    else if (kPass == kFirst) S.store(carry_state(p, seq, segment + 1), p.K, p.V);
+    else if (kPass == kWhole || segment == p.segments - 1) S.store(p.h_last + seq * size, p.K, p.V);
 }
 
 // What the launches of the backward pass leave for each other, in fp32.
@@ -720,12 +753,24 @@ int step_launch(const Delta& p, cudaStream_t stream) {
     return p.V > 32 ? step_launch<T, 16>(p, stream) : step_launch<T, 8>(p, stream);
 }
 
+template <int KR, int kPass>
+int fwd_pass(const Delta& p, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = delta_tokens_fwd<KR, kPass>;
+    if (allow_smem(kernel, sizeof(FwdShared), done) != cudaSuccess) return SSDC_ERR_CUDA;
+    const int each = kPass == kWhole ? 1 : kPass == kFirst ? 2 * p.segments - 3 : p.segments - 1;
+    const int columns = kPass == kFirst ? std::max(p.K, p.V) : p.V;
+    const dim3 grid(p.B * p.H * each), block(32 * ((columns + 15) / 16));
+    if (kPass != kSecond) kernel<<<grid, block, sizeof(FwdShared), stream>>>(p);
+    else if (launch_dependent(kernel, grid, block, sizeof(FwdShared), stream, p) != cudaSuccess) return SSDC_ERR_CUDA;
+    return 1;
+}
 template <int KR>
 int fwd_launch(const Delta& p, cudaStream_t stream) {
-    static std::atomic<uint64_t> done{0};
-    if (allow_smem(delta_tokens_fwd<KR>, sizeof(FwdShared), done) != cudaSuccess) return SSDC_ERR_CUDA;
-    delta_tokens_fwd<KR><<<p.B * p.H, 32 * ((p.V + 15) / 16), sizeof(FwdShared), stream>>>(p);
-    return 1;
+    if (p.segments == 1) return fwd_pass<KR, kWhole>(p, stream);
+    const int first = fwd_pass<KR, kFirst>(p, stream), joined = first < 0 ? first : delta_join_launch(p, stream);
+    const int second = joined < 0 ? joined : fwd_pass<KR, kSecond>(p, stream);
+    return second < 0 ? second : first + joined + second;
 }
 
 template <int KR>

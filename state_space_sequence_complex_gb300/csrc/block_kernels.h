@@ -171,7 +171,7 @@ struct Delta {
     void *dq, *dk, *dv, *df, *db;
     float* dh0;
     void* ws;
-    // segments of a sequence, and their chunks (block_delta_prepare.cuh): their states and transitions, or null
+    // segments of a sequence, and their chunks; their states and transitions, or null
     int segments, segment_chunks;
     float* carry;
 };
@@ -185,6 +185,23 @@ constexpr int kDeltaChunk = SSD_DELTA_STATE_TOKENS;
 inline size_t delta_kept_bytes(const Delta& p) {
     return ((size_t)p.B * p.H * ((p.T + kDeltaChunk - 1) / kDeltaChunk) * p.K * p.V * 2 + 255) / 256 * 256;
 }
+
+// A sequence in segments, where there are so few states that most SMs would have none. The update is linear in the
+// state: a segment maps it to M S + E, with M what becomes of the unit matrix without values. So
+//   first   segment 0 is taken as a whole sequence is; of the others but the last, E and M
+//   joined  the states between the segments, one after the other: S <- M S + E
+//   second  segments 1 and on are taken from their states
+// Backwards the same, from the last segment to the first. `carry` has for each state the n - 1 states between
+// segments ([K][V]), then the n - 2 transitions, transposed.
+enum : int { kWhole, kFirst, kSecond };  // sequences as they are, or a pass over segments
+__host__ __device__ inline float* carry_state(const Delta& p, int64_t seq, int segment) {  // 1 and on: what enters it
+    return p.carry + (seq * (p.segments - 1) + segment - 1) * p.K * p.V;
+}
+__host__ __device__ inline float* carry_move(const Delta& p, int64_t seq, int segment) {  // 1 to n - 2
+    return p.carry + (int64_t)p.B * p.H * (p.segments - 1) * p.K * p.V + (seq * (p.segments - 2) + segment - 1) * p.K * p.K;
+}
+int delta_join_launch(const Delta& p, cudaStream_t stream);
+
 int delta_step_launch(const Delta& p, cudaStream_t stream);
 int delta_fwd_launch(const Delta& p, cudaStream_t stream);  // bfloat16, in chunks
 int delta_tokens_fwd_launch(const Delta& p, cudaStream_t stream);  // fp32, token by token

@@ -108,9 +108,10 @@ def test_workspace_sizes(lib):
     size = lib.ssd_delta_rule_bwd_workspace_bytes
     assert size(dims()) == 2 * 4 * 2 * 64 * 32 * 2           # the states' gradients, two chunks, in bfloat16
     assert size(dims(type=0)) > 2 * 2 * 100 * 4 * 64 * 4     # fp32: gradients of q and k for each value head too
-    # in segments: their states and transitions; whole sequences and fp32 have none
+    # in segments: their states and transitions; whole sequences have none
     carry = lib.ssd_delta_rule_fwd_workspace_bytes
-    assert carry(dims()) == carry(dims(T=1)) == carry(dims(B=64, T=4096)) == carry(dims(type=0, T=1 << 16)) == 0
+    assert carry(dims()) == carry(dims(T=1)) == carry(dims(B=64, T=4096)) == carry(dims(type=0)) == carry(dims(B=64, type=0, T=4096)) == 0
+    assert carry(dims(type=0, T=4096)) > 0
     for K, V in ((64, 32), (8, 8), (128, 128), (128, 8), (72, 104)):
         d = dims(B=1, T=4096, K=K, V=V)
         n = (carry(d) // 16 + K * V + 2 * K * K) / (K * V + K * K)        # (n - 1) K V + (n - 2) K K floats for 4 heads

@@ -41,31 +41,33 @@ def test_rows_that_start_anywhere(shape):
 LONG = [(1, 2049, 2, 1, 64, 64), (1, 1500, 1, 1, 8, 128), (1, 1999, 3, 3, 128, 40), (2, 1700, 5, 5, 72, 104), (1, 3001, 1, 1, 128, 128)]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("docs", [0.0, 0.001])
 @pytest.mark.parametrize("shape", LONG, ids=lambda s: "x".join(map(str, s)))
-def test_few_states_in_segments(shape, docs):
-    x = make(*shape, seed=sum(shape), docs=docs, state=docs == 0.0)
-    assert block.DeltaRule(*sizes(x), key_heads=shape[3]).workspace is not None
-    check(x, "bf16")
+def test_few_states_in_segments(shape, docs, dtype):
+    x = make(*shape, dtype=dtype, seed=sum(shape), docs=docs, state=docs == 0.0)
+    assert block.DeltaRule(*sizes(x), dtype=dtype, key_heads=shape[3]).workspace is not None
+    check(x, dtype)
 
 
-def test_segments_without_lengths_of_one():
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_segments_without_lengths_of_one(dtype):
     """Keys of their own length, rows that start anywhere, and the state passed on in place."""
     B, T, H, K = 1, 1200, 2, 64
-    x = make(B, T, H, H, K, K, seed=41)
-    x["k"], x["q"] = (x["k"].float() / 8).bfloat16(), (x["q"].float() / 8).bfloat16()
-    check(x, "bf16", normalize=False)
+    x = make(B, T, H, H, K, K, dtype=dtype, seed=41)
+    x["k"], x["q"] = (x["k"].float() / 8).to(DT[dtype]), (x["q"].float() / 8).to(DT[dtype])
+    check(x, dtype, normalize=False)
     y = cuda(x)
     for n in ("q", "k", "v", "do"):
-        wide = torch.zeros(B, T, H * K + 3, dtype=torch.bfloat16, device="cuda")
+        wide = torch.zeros(B, T, H * K + 3, dtype=DT[dtype], device="cuda")
         wide[..., 1:1 + H * K] = y[n].flatten(2)
         y[n] = wide[..., 1:1 + H * K].unflatten(-1, (H, K))
-    want = {n: t.clone() for n, t in run(cuda(x), "bf16", normalize=False).items()}
-    got = run(y, "bf16", normalize=False)
+    want = {n: t.clone() for n, t in run(cuda(x), dtype, normalize=False).items()}
+    got = run(y, dtype, normalize=False)
     for n in want:
         assert torch.equal(got[n], want[n]), n
     y = cuda(x)
-    plan = block.DeltaRule(B, T, H, K, K, normalize=False)
+    plan = block.DeltaRule(B, T, H, K, K, dtype, normalize=False)
     plan.h_last.copy_(y["h0"])
     o, last = plan(*(y[n] for n in NAMES), h0=plan.h_last)
     assert torch.equal(o, want["o"]) and torch.equal(last, want["h_last"])
@@ -153,7 +155,7 @@ def test_two_streams_at_once():
 
 
 @pytest.mark.parametrize("dtype,at,T", [("bf16", 128, 256), ("bf16", 192, 256), ("fp32", 128, 256), ("fp32", 100, 256), ("fp32", 1, 256),
-                                        ("fp32", 255, 256), ("bf16", 1024, 2048), ("bf16", 960, 2048), ("bf16", 64, 2048),
+                                        ("fp32", 255, 256), ("bf16", 1024, 2048), ("fp32", 1000, 2048), ("bf16", 960, 2048), ("bf16", 64, 2048),
                                         ("bf16", 1984, 2048)])
 @pytest.mark.parametrize("bad", ["v", "k", "h0"])
 def test_nothing_passes_a_reset(dtype, at, T, bad):
