@@ -238,9 +238,9 @@ int ssd_fp8_matmul(ssd_rows_in a, const float *a_scale, ssd_rows_in b, const flo
  * 64 tokens; elsewhere one of BF16 reaches the other documents that share a chunk of 64 tokens with its own.
  *
  * BF16: chunks of 64 tokens on the tensor cores, products with operands in one or two bf16
- * parts and fp32 sums; states are within 1e-5 of exact ones (relative to their norm)
- * where |k|^2 beta <= 2, which normalised keys always meet: beyond that the recurrence itself grows
- * without bound. F32: token by token in fp32. Fastest: BF16, first elements and strides in whole 16 bytes.
+ * parts and fp32 sums; states are within 1e-5 of exact ones, relative to the norm of the terms k u^T of
+ * a chunk that they are summed from (their own norm, but where like keys make the terms cancel), where
+ * |k|^2 beta <= 2, which normalised keys always meet: beyond that the recurrence itself grows without bound. F32: token by token in fp32. Fastest: BF16, first elements and strides in whole 16 bytes.
  */
 typedef struct {
     const void *p;

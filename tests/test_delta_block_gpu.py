@@ -73,6 +73,87 @@ def test_segments_without_lengths_of_one(dtype):
     assert torch.equal(o, want["o"]) and torch.equal(last, want["h_last"])
 
 
+def term_norms(x):
+    """The norms of what o, h_last and dq are summed from in their chunk of 64 tokens: what enters from the state in
+    front, and each token's own term. A term's roundings are relative to the term (those of u in do_i.u_j to |do_i| |u_j|),
+    independent of each other, and stay when the terms cancel: with keys all alike u_j is nearly v_j - v_{j-1}, and
+    64 of them add up to one v."""
+    B, T, H, V = x["v"].shape
+    q, k, v, f, b, do = (x[n].double() for n in NAMES + ("do",))
+    scale = 1 / (q.square().sum(-1, keepdim=True) + 1e-6).sqrt() / q.shape[3] ** 0.5  # dq is taken back through it
+    q, k = q * scale, k / (k.square().sum(-1, keepdim=True) + 1e-6).sqrt()
+    a, beta, S = torch.sigmoid(f), torch.sigmoid(b), x["h0"].double()
+    total = dict.fromkeys(("o", "h_last", "dq"), 0.0)
+    for t in range(T):
+        if t % 64 == 0:
+            front, into, us, ks = S, torch.ones(B, H, dtype=torch.float64), [], []
+        S = S * a[:, t, :, None, None]
+        into = into * a[:, t]
+        us = [u * a[:, t, :, None] for u in us]  # decayed to this token
+        us.append(beta[:, t, :, None] * (v[:, t] - torch.einsum("bhk,bhkv->bhv", k[:, t], S)))
+        ks.append(k[:, t])
+        S = S + k[:, t, :, :, None] * us[-1][:, :, None]
+        size = torch.stack(us).norm(dim=-1)
+        d = do[:, t].norm(dim=-1)
+        state = into * front.flatten(2).norm(dim=-1)
+        pairs = torch.einsum("bhk,jbhk->jbh", q[:, t], torch.stack(ks))
+        total["o"] += float(((pairs * size).square().sum(0) + (into * torch.einsum("bhk,bhkv->bhv", q[:, t], front).norm(dim=-1)) ** 2).sum())
+        total["dq"] += float(((d ** 2 * (size.square().sum(0) + state ** 2)) * scale[:, t, :, 0] ** 2).sum())
+    total["h_last"] = float((size.square().sum(0) + state ** 2).sum())
+    return {n: t ** 0.5 for n, t in total.items()}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", ["the same key", "nothing kept", "all kept"])
+def test_segments_at_their_ends(case, dtype):
+    """Transitions that are one direction's projection again and again, zero, and products of reflections."""
+    T = 1300
+    x = make(1, T, 2, 2, 64, 64, dtype=dtype, seed=43, decay=8.0)
+    if case == "the same key":
+        x["k"] = x["k"][:, :1].expand(-1, T, -1, -1).contiguous()
+        x["b"] = torch.full_like(x["b"], 6.0)
+    else:
+        x["f"] = torch.full_like(x["f"], -40.0 if case == "nothing kept" else 20.0)
+    assert block.DeltaRule(*sizes(x), dtype=dtype).workspace is not None
+    want, got = reference(x), run(cuda(x), dtype)
+    terms = term_norms(x) if case == "the same key" and dtype == "bf16" else {}
+    for n in want:
+        if n != "df":  # where nothing is kept its values are below the smallest numbers
+            close(got[n], want[n], n, dtype, max(1.0, terms.get(n, 0.0) / float(want[n].norm())))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_segments_captured_and_at_once(dtype):
+    """Graphs of two plans replayed on two streams at once, over and over: the same values every time."""
+    B, T, H, K = 1, 1500, 3, 64
+    xs = [cuda(make(B, T, H, H, K, K, dtype=dtype, seed=s)) for s in (44, 45)]
+    want = [{n: t.clone() for n, t in run(x, dtype).items()} for x in xs]
+    graphs, outs = [], []
+    for x in xs:
+        plan, back = block.DeltaRule(B, T, H, K, K, dtype, keep=True), block.DeltaRuleBackward(B, T, H, K, K, dtype)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o, last = plan(*(x[n] for n in NAMES), h0=x["h0"])
+            g = back(x["q"], x["k"], x["f"], x["b"], plan.states, plan.updates, x["do"], dh_last=x["dh_last"])
+        graphs.append((graph, plan, back))
+        outs.append(dict(o=o, h_last=last, **g))
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(4):
+        for o in outs:
+            for t in o.values():
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for s, (graph, plan, back) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                for p in (plan, back):  # nothing of an earlier call is looked at
+                    p.workspace.fill_(0xFF)
+                graph.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            for n in w:
+                assert torch.equal(o[n], w[n]), n
+
+
 def guarded(*shape, dtype):
     """A dense array with 64 guard values behind it, and the guard."""
     n = 1
