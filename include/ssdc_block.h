@@ -236,6 +236,7 @@ int ssd_fp8_matmul(ssd_rows_in a, const float *a_scale, ssd_rows_in b, const flo
  *
  * Nothing passes a reset, an infinity or a NaN neither, with F32, and with BF16 where the reset is at a multiple of
  * 64 tokens; elsewhere one of BF16 reaches the other documents that share a chunk of 64 tokens with its own.
+ * (BF16: a chunk whose tokens together decay below 2^-126 is a reset to what is in front of it.)
  *
  * BF16: chunks of 64 tokens on the tensor cores, products with operands in one or two bf16
  * parts and fp32 sums; states are within 1e-5 of exact ones, relative to the norm of the terms k u^T of

@@ -9,6 +9,8 @@ call at the same time need a plan each.
 (``torch.autograd``, first derivatives) and allocate their outputs. They do not
 read the status of a wait between CTAs that gave up, which a plan's ``status()``
 does: that waits for the GPU.
+Where a backward pass is captured in a CUDA graph, no graph of the same leaves made outside the capture may
+be alive: autograd adds a leaf's gradient up on the stream that it first met the leaf on.
 
 A plan's tensors belong to the device it was made for; a call runs there, on that
 device's current stream or on ``stream``, whichever device is current. Tensors made on another stream have to be ordered with
@@ -21,6 +23,9 @@ it by the caller, as for any kernel.
     y = block.Fp8Product(M, N, D)(q, scale, w_q, w_s)   # y = norm(r) weight^T
     scan = block.GatedScan(B, T, C, "bf16")
     h, h_last = scan(x, f, i, h0=state)                 # slices of y work: strides are taken from the tensors
+    rule = block.DeltaRule(B, T, H, K, V, key_heads=G)
+    o, state = rule(q, k, v, f, b)                      # (B, T, heads, features) slices; state: what DeltaRuleStep continues
+    q8, scale = block.GatedNorm(B * T, H, V)(o.flatten(2).flatten(0, 1), z, w)
 """
 from __future__ import annotations
 
@@ -580,7 +585,8 @@ class DeltaRule:
     takes q, k (B, T, key_heads, K), v (B, T, heads, V) with contiguous features, f, b (B, T, heads), an optional
     state (B, heads, K, V) float32 (this object's own ``h_last`` continues the last call in place) and optional
     marks (B, T) uint8, and returns ``(o, h_last)``. With ``keep`` a call also fills ``states`` and ``updates``,
-    which the backward pass takes. K and V are multiples of 8 up to 128."""
+    which the backward pass takes. K and V are multiples of 8 up to 128. Few long sequences are taken in segments, for which a
+    plan has a ``workspace`` (else None)."""
 
     def __init__(self, B, T, heads, K, V, dtype="bf16", key_heads=None, normalize=True, keep=False, device="cuda"):
         self.dims, self._dims = _delta_dims(B, T, heads, K, V, dtype, key_heads, normalize, "DeltaRule")

@@ -71,6 +71,7 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
     const int64_t z_stride = (int64_t)p.H * p.V, z_step = C * z_stride;
     __nv_bfloat16* z_rows = static_cast<__nv_bfloat16*>(p.dv) + ((b * p.T + (int64_t)last * C) * p.H + h) * p.V + col0;
     int stage = 0;
+    bool cut = false;
     for (int n = 0; n < chunks; ++n, stage = L::next_stage(stage, 1)) {
         const int c = last - n;
         const int turn = n & 1, set = n & (L::kSets - 1), half = n % kGroups;
@@ -112,6 +113,7 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         const Factors* factors = reinterpret_cast<const Factors*>(smem + L::kFactorsOff) + set * C;
         const uint32_t hi = L::kLOff + half * L::kBlocks, lo = hi + L::kSquare, ps = lo + L::kSquare, ps2 = ps + L::kSquare;
         const float gam = reinterpret_cast<const float*>(smem + L::kGamOff)[set];
+        cut = cut || gam == 0.0f;
 #pragma unroll
         for (int m = 0; m < 8; ++m)
 #pragma unroll
@@ -214,6 +216,7 @@ __device__ __forceinline__ void walk_back(const Delta& p, char* smem, int b, int
         rows.take(strips + ((chunks - 1) & 1) * L::kStrip);
         rows.give(z_rows + z_step, z_stride, tokens_of(last - chunks + 1), columns);
     }
+    if (unit && col0 == 0 && lane == 0) *carry_cut(p, seq, way.segment) = cut ? 1.0f : 0.0f;
     float* to = state_out<kPass>(p, p.dh0, seq, way);
     if (to == nullptr) return;
 #pragma unroll

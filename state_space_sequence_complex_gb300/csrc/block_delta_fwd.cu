@@ -66,6 +66,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, c
     __nv_bfloat16* o_rows = static_cast<__nv_bfloat16*>(p.o) + o_first;
     __nv_bfloat16* u_rows = static_cast<__nv_bfloat16*>(p.updates) + o_first;
     int stage = 0;
+    bool cut = false;
     for (int c = 0; c < chunks; ++c, stage = L::next_stage(stage, 1)) {
         const int turn = c & 1, set = c & (L::kSets - 1), half = c % kGroups;
         // The strip of this chunk has its v, and when that has been read its u and o. The other one has the last
@@ -121,6 +122,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, c
         // A chunk that cuts the state off (a reset in it, as a rule): what a token does not take from it is zero,
         // whatever the state holds; an infinity or a NaN of one document stays out of the next.
         if (gam == 0.0f) {
+            cut = true;
 #pragma unroll
             for (int n = 0; n < 8; ++n)
 #pragma unroll
@@ -238,6 +240,7 @@ __device__ __forceinline__ void walk(const Delta& p, char* smem, int b, int h, c
         rows.take(strips + ((chunks - 1) & 1) * L::kStrip);
         rows.give(o_rows - o_step, o_stride, (int)min((int64_t)C, p.T - token0 - (int64_t)(chunks - 1) * C), columns);
     }
+    if (unit && col0 == 0 && lane == 0) *carry_cut(p, seq, way.segment) = cut ? 1.0f : 0.0f;
     float* to = state_out<kPass>(p, p.h_last, seq, way);
     if (to == nullptr) return;
 #pragma unroll
@@ -329,19 +332,17 @@ __global__ void __launch_bounds__(2 * KP) delta_join(const __grid_constant__ Del
         fetch_step(m + J::kStages - 1);
         const float* stage = reinterpret_cast<const float*>(smem + m % J::kStages * J::kStage);
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        bool any = false;
+        const bool cut = *carry_cut(p, seq, m) != 0.0f;
         if (mine) {
 #pragma unroll 8
             for (int j = 0; j < p.K; ++j) {
                 const float v = stage[j * p.K + r];
                 const float4 s = *reinterpret_cast<const float4*>(&S[j][c0]);
-                any = any || v != 0.0f;
                 sum.x = fmaf(v, s.x, sum.x), sum.y = fmaf(v, s.y, sum.y), sum.z = fmaf(v, s.z, sum.z), sum.w = fmaf(v, s.w, sum.w);
             }
         }
         own = *reinterpret_cast<const float4*>(stage + KP * KP + 8 * r + c0);
-        // a row that takes nothing (behind a reset) stays as it is, whatever the state holds
-        if (any) own.x += sum.x, own.y += sum.y, own.z += sum.z, own.w += sum.w;
+        if (!cut) own.x += sum.x, own.y += sum.y, own.z += sum.z, own.w += sum.w;
         if (mine) *reinterpret_cast<float4*>(at(m + 1)) = own;
     }
 }
@@ -411,7 +412,7 @@ DeltaSegments delta_segments(const Delta& p) {
 }
 size_t delta_carry_bytes(const Delta& p) {
     const int64_t n = delta_segments(p).n;
-    return n == 1 ? 0 : (size_t)p.B * p.H * ((n - 1) * p.K * p.V + (n - 2) * p.K * p.K) * sizeof(float);
+    return n == 1 ? 0 : (size_t)p.B * p.H * ((n - 1) * p.K * p.V + (n - 2) * (p.K * p.K + 1)) * sizeof(float);
 }
 
 int delta_fwd_launch(const Delta& p, cudaStream_t stream) {

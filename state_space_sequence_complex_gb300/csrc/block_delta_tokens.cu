@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(256) delta_tokens_fwd(const __grid_constant__ 
         S.load(segment == 0 && p.h0 ? p.h0 + seq * size : nullptr, p.K, p.V);
         if (unit) S.unit();
     }
+    bool cut = false;
     for (int64_t t0 = begin; t0 < end; t0 += kFwdTile) {
         FwdTile& tile = sm.tile[t0 / kFwdTile & 1];
         ptx::cp_async_wait<0>();
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(256) delta_tokens_fwd(const __grid_constant__ 
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], o);
             if (gt.x == 0.0f) {  // the state ends here, whatever it holds
+                cut = true;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sums[j] = 0.0f;
                 S.clear();
@@ -317,6 +319,7 @@ __global__ void __launch_bounds__(256) delta_tokens_fwd(const __grid_constant__ 
                 if (p.updates != nullptr) static_cast<float*>(p.updates)[(at + (int64_t)t * p.H) * p.V + d] = sm.u[t][d];
             }
     }
+    if (unit && threadIdx.x == 0) *carry_cut(p, seq, segment) = cut ? 1.0f : 0.0f;
     if (unit) S.store_transposed(carry_move(p, seq, segment), p.K);
     else if (kPass == kFirst) S.store(carry_state(p, seq, segment + 1), p.K, p.V);
     else if (kPass == kWhole || segment == p.segments - 1) S.store(p.h_last + seq * size, p.K, p.V);

@@ -192,13 +192,18 @@ inline size_t delta_kept_bytes(const Delta& p) {
 //   joined  the states between the segments, one after the other: S <- M S + E
 //   second  segments 1 and on are taken from their states
 // Backwards the same, from the last segment to the first. `carry` has for each state the n - 1 states between
-// segments ([K][V]), then the n - 2 transitions, transposed.
+// segments ([K][V]), then the n - 2 transitions, transposed, and for each of them a mark.
 enum : int { kWhole, kFirst, kSecond };  // sequences as they are, or a pass over segments
 __host__ __device__ inline float* carry_state(const Delta& p, int64_t seq, int segment) {  // 1 and on: what enters it
     return p.carry + (seq * (p.segments - 1) + segment - 1) * p.K * p.V;
 }
 __host__ __device__ inline float* carry_move(const Delta& p, int64_t seq, int segment) {  // 1 to n - 2
     return p.carry + (int64_t)p.B * p.H * (p.segments - 1) * p.K * p.V + (seq * (p.segments - 2) + segment - 1) * p.K * p.K;
+}
+// 1 to n - 2: whether the segment cuts off what enters it, a NaN or an infinity too: its transition is zero also where
+// decays are just too small, and then they pass, as they do where the sequence is taken as it is.
+__host__ __device__ inline float* carry_cut(const Delta& p, int64_t seq, int segment) {
+    return carry_move(p, (int64_t)p.B * p.H, 1) + seq * (p.segments - 2) + segment - 1;
 }
 int delta_join_launch(const Delta& p, cudaStream_t stream);
 

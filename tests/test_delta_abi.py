@@ -114,7 +114,7 @@ def test_workspace_sizes(lib):
     assert carry(dims(type=0, T=4096)) > 0
     for K, V in ((64, 32), (8, 8), (128, 128), (128, 8), (72, 104)):
         d = dims(B=1, T=4096, K=K, V=V)
-        n = (carry(d) // 16 + K * V + 2 * K * K) / (K * V + K * K)        # (n - 1) K V + (n - 2) K K floats for 4 heads
+        n = (carry(d) // 16 + K * V + 2 * (K * K + 1)) / (K * V + K * K + 1)  # (n - 1) K V + (n - 2) (K K + 1) floats for 4 heads
         assert n == int(n) >= 3 and size(d) == 4 * 64 * K * V * 2 + carry(d)
 
 

@@ -122,6 +122,22 @@ def test_segments_at_their_ends(case, dtype):
             close(got[n], want[n], n, dtype, max(1.0, terms.get(n, 0.0) / float(want[n].norm())))
 
 
+@pytest.mark.parametrize("dtype,f", [("bf16", 0.0), ("fp32", 0.0), ("fp32", -3.0)])
+def test_a_nan_stays_where_decays_are_small(dtype, f):
+    """2^-64 to 2^-280 a chunk: transitions of a segment are zero, but a NaN or an infinity decays to no number."""
+    T = 1500
+    x = make(1, T, 2, 2, 64, 64, dtype=dtype, seed=46)
+    x["f"] = torch.full_like(x["f"], f)
+    assert block.DeltaRule(*sizes(x), dtype=dtype).workspace is not None
+    clean = {n: t.clone() for n, t in run(cuda(x), dtype).items()}
+    x["v"][0, 10, 1, 3], x["h0"][0, 1, 0, 5] = float("nan"), float("inf")
+    x["do"][0, T - 10, 0, 7] = float("nan")
+    got = run(cuda(x), dtype)
+    assert not torch.isfinite(got["o"][0, 10:, 1, 3]).any() and not torch.isfinite(got["h_last"][0, 1, :, 3]).any()
+    assert not torch.isfinite(got["o"][0, :, 1, 5]).any() and not torch.isfinite(got["dv"][0, :T - 10, 0, 7]).any()
+    assert torch.equal(got["o"][0, :, 0], clean["o"][0, :, 0]) and torch.equal(got["dv"][0, :, 1], clean["dv"][0, :, 1])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_segments_captured_and_at_once(dtype):
     """Graphs of two plans replayed on two streams at once, over and over: the same values every time."""
