@@ -4,7 +4,9 @@
 // Bound by memory: every value is read once and kept in registers, a thread has 8 features in a row.
 // Where D is a power of two, a warp's 256 features hold whole heads and whole groups of 128 (the groups
 // of the 8-bit scales), and both are reduced by shuffles. For other D a CTA has whole heads (and whole
-// groups, where it writes 8 bits), and a head's sum goes through shared memory. 32,768 rows of 16 heads of 64 in
+// groups, where it writes 8 bits), and a head's sum goes through shared memory. Narrow rows lie side by side in a warp or
+// a CTA: 524,288 rows of one head of 64 take 37 us forward and 70 back, with a warp to each 100 and 195, and 300,000 of
+// 72 37 and 69, with a CTA to each 305 and 162. 32,768 rows of 16 heads of 64 in
 // bfloat16: forward to 8 bits 35 us (4.8 TB/s; 27 instructions a value take 68 % of the issue slots as well), gradients with
 // the skip 81 us (5.8 TB/s, of it 6 for the sum of dw's shares).
 #include <algorithm>
@@ -77,22 +79,31 @@ __device__ __forceinline__ float head_sum(float v, int n, int first, float* buff
     }
 }
 
+// How rows are dealt out: pieces of a row with whole heads, of `vecs` threads each; narrow rows (one piece) side by side,
+// `rows` of them in a warp or a CTA, `slot` threads apart.
+struct Split {
+    bool warp;
+    int pieces, vecs, rows, slot, threads;
+};
+
 // The features of a thread and its head: `piece` counts the row's parts (256 features, or a CTA's heads).
 struct Place {
     int feature;  // first of the 8; of a thread without features the row's first, which it reads and leaves
-    int head, lanes, first;
+    int head, lanes, first, row;  // row: of those side by side
     bool mine;
 };
-template <bool kWarp>
-__device__ __forceinline__ Place place(int piece, int per_piece, int D, int N) {
+template <bool kWarp, bool kNarrow>
+__device__ __forceinline__ Place place(int piece, const Split& s, int D, int N) {
     Place a;
     const int t = kWarp ? threadIdx.x % 32 : threadIdx.x;
-    a.feature = (piece * per_piece + t) * kVec;
-    a.mine = t < per_piece && a.feature < N;
+    a.row = kNarrow && s.rows > 1 ? t / s.slot : 0;
+    const int in_row = kNarrow ? t - a.row * s.slot : t, vecs = kWarp && !kNarrow ? 32 : s.vecs;
+    a.feature = (piece * vecs + in_row) * kVec;
+    a.mine = (!kNarrow || a.row < s.rows) && in_row < vecs && a.feature < N;
     if (!a.mine) a.feature = 0;
     a.head = a.feature / D;
     a.lanes = D / kVec;
-    a.first = t < per_piece ? t / a.lanes * a.lanes : 0;
+    a.first = a.mine ? a.row * s.slot + in_row / a.lanes * a.lanes : 0;
     return a;
 }
 
@@ -132,19 +143,24 @@ __device__ __forceinline__ float sum8(const float2* a, const float2* b) {
 
 // Two values at a time where an instruction does two, and no branch for what a thread does not have: a row's
 // instructions were as long as its memory.
-template <typename T, int kOut, bool kWarp, bool kAligned, int kRows>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarps : 512) gated_norm_fwd(const GatedNorm p, int per_piece) {
+// kNarrow: rows side by side.
+template <typename T, int kOut, bool kWarp, bool kAligned, int kRows, bool kNarrow>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarps : 512) gated_norm_fwd(const GatedNorm p, const Split split) {
     __shared__ float buffer[kWarp ? 1 : 512];
     launch_dependents();
     grid_dependency_wait();
     const int N = p.H * p.D;
-    const Place a = place<kWarp>(blockIdx.y, per_piece, p.D, N);
-    const int64_t m0 = kWarp ? ((int64_t)blockIdx.x * kWarps + threadIdx.x / 32) * kRows : blockIdx.x;
-    if (m0 >= p.M) return;  // whole warps, or the whole CTA
+    const Place a = place<kWarp, kNarrow>(blockIdx.y, split, p.D, N);
+    const int side = kNarrow ? split.rows : 1;
+    const int64_t first = (kWarp ? ((int64_t)blockIdx.x * kWarps + threadIdx.x / 32) * kRows : blockIdx.x) * side;
+    if (first >= p.M) return;  // whole warps, or the whole CTA
+    auto row = [&](int r) { return first + (kNarrow ? a.row : 0) + r * side; };
+    constexpr bool kAll = kRows == 1 && !kNarrow;  // else rows behind the last one are that one, read again
+    auto read = [&](int r) { return kAll ? row(r) : min(row(r), p.M - 1); };
     float2 u[kRows][4], z[kRows][4], w[4];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        const int64_t m = kRows == 1 ? m0 : min(m0 + r, p.M - 1);
+        const int64_t m = read(r);
         load8<T, kAligned>(&u[r][0].x, p.x, m * p.x_ld + a.feature);
         load8<T, kAligned>(&z[r][0].x, p.z, m * p.z_ld + a.feature);
     }
@@ -154,7 +170,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarps : 512) gated_norm_fwd(cons
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
             float2 v[4];
-            load8<T, kAligned>(&v[0].x, p.v, (kRows == 1 ? m0 : min(m0 + r, p.M - 1)) * p.v_ld + a.feature);
+            load8<T, kAligned>(&v[0].x, p.v, read(r) * p.v_ld + a.feature);
 #pragma unroll
             for (int i = 0; i < 4; ++i) u[r][i] = ptx::fma2(s, v[i], u[r][i]);
         }
@@ -162,8 +178,8 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarps : 512) gated_norm_fwd(cons
     const float mean = 1.0f / (float)p.D;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        const int64_t m = m0 + r;
-        const bool there = a.mine && (kRows == 1 || m < p.M);
+        const int64_t m = row(r);
+        const bool there = a.mine && (kAll || m < p.M);
         const float ss = head_sum<kWarp>(sum8(u[r], u[r]), a.lanes, a.first, buffer);
         const float2 rstd = both(rsqrtf(fmaf(ss, mean, p.eps)));
         float2 y[4];
@@ -174,7 +190,9 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarps : 512) gated_norm_fwd(cons
             float amax = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
-            amax = warp_max<16>(a.mine ? amax : 0.0f);
+            amax = a.mine ? amax : 0.0f;
+            if constexpr (!kNarrow) amax = warp_max<16>(amax);
+            else for (int o = 1; o < min(16, split.slot); o *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             const Scale scale(amax);
             if (there) {
                 if (a.feature % SSD_FP8_GROUP == 0) p.scale[(int64_t)(a.feature / SSD_FP8_GROUP) * p.M + m] = scale.s;
@@ -192,18 +210,22 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarps : 512) gated_norm_fwd(cons
 // Gradients. With g = z sigmoid(z), n = dy g w: du = rstd (n - u rstd^2 mean(n u)), so both sums of a head
 // (of u u and of n u) are taken at once; dw and ds stay in registers over a thread's rows and are added up
 // in a fixed order: rows of a thread, warps of a CTA, CTAs by gated_norm_dw.
-template <typename T, bool kWarp, bool kAligned, bool kSkip>
-__global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : 1) gated_norm_bwd(const GatedNorm p, int pieces, int per_piece, int parts) {
+// kNarrow: rows side by side.
+template <typename T, bool kWarp, bool kAligned, bool kSkip, bool kNarrow>
+__global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : 1) gated_norm_bwd(const GatedNorm p, const Split split, int parts) {
     __shared__ float buffer[kWarp ? 1 : 4 * 512], sums[kWarp ? kWarps : 1][32][kVec + 1];
     launch_dependents();
     grid_dependency_wait();
-    const int N = p.H * p.D, piece = blockIdx.x % pieces, part = blockIdx.x / pieces;
-    const Place a = place<kWarp>(piece, per_piece, p.D, N);
+    const int N = p.H * p.D, piece = blockIdx.x % split.pieces, part = blockIdx.x / split.pieces, rows = kNarrow ? split.rows : 1;
+    const Place a = place<kWarp, kNarrow>(piece, split, p.D, N);
     float2 w[4], dw[4] = {}, ds = {};
     load_weights(w, p.w, a.feature);
     const float s = kSkip ? p.s[a.head] : 0.0f, mean = 1.0f / (float)p.D;
     int turn = 0;
-    for (int64_t m = kWarp ? (int64_t)part * kWarps + threadIdx.x / 32 : part; m < p.M; m += (int64_t)parts * (kWarp ? kWarps : 1)) {
+    const int64_t step = (int64_t)parts * (kWarp ? kWarps : 1) * rows;
+    for (int64_t m0 = (kWarp ? (int64_t)part * kWarps + threadIdx.x / 32 : part) * rows; m0 < p.M; m0 += step) {
+        const bool there = !kNarrow || m0 + a.row < p.M;  // what is behind the last row reads that, and adds nothing
+        const int64_t m = kNarrow ? min(m0 + a.row, p.M - 1) : m0;
         float2 u[4], z[4], dy[4], v[4], n[4];
         load8<T, kAligned>(&u[0].x, p.x, m * p.x_ld + a.feature);
         load8<T, kAligned>(&z[0].x, p.z, m * p.z_ld + a.feature);
@@ -231,15 +253,15 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : 1) gated_norm_b
         const float2 rstd = both(r), along = both(-nu * mean * r * r);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            dw[i] = ptx::fma2(dy[i], rstd, dw[i]);
+            if (there) dw[i] = ptx::fma2(dy[i], rstd, dw[i]);
             z[i] = ptx::mul2(z[i], rstd);
             u[i] = ptx::mul2(rstd, ptx::fma2(along, u[i], n[i]));
             if constexpr (kSkip) {
-                ds = ptx::fma2(u[i], v[i], ds);
+                if (there) ds = ptx::fma2(u[i], v[i], ds);
                 v[i] = ptx::mul2(both(s), u[i]);
             }
         }
-        if (a.mine) {
+        if (a.mine && there) {
             store8<T, kAligned>(p.dx, m * p.dx_ld + a.feature, &u[0].x);
             store8<T, kAligned>(p.dz, m * p.dz_ld + a.feature, &z[0].x);
             if constexpr (kSkip) store8<T, kAligned>(p.dv, m * p.dv_ld + a.feature, &v[0].x);
@@ -255,22 +277,36 @@ __global__ void __launch_bounds__(kWarp ? 256 : 512, kWarp ? 3 : 1) gated_norm_b
         sums[warp][lane][kVec] = head_sum<true>(ds.x + ds.y, a.lanes, a.first, buffer);
         __syncthreads();
         for (int i = threadIdx.x; i < 32 * (kVec + 1); i += blockDim.x) {
-            const int l = i / (kVec + 1), e = i % (kVec + 1), feature = (piece * per_piece + l) * kVec;
-            float t = 0.0f;
-#pragma unroll
-            for (int r = 0; r < kWarps; ++r) t += sums[r][l][e];
+            const int l = i / (kVec + 1), e = i % (kVec + 1), feature = (piece * split.vecs + l) * kVec;
             if (feature < N) {
+                float t = 0.0f;
+                for (int side = 0; side < rows; ++side)
+#pragma unroll
+                    for (int r = 0; r < kWarps; ++r) t += sums[r][side * split.slot + l][e];
                 if (e < kVec) to[feature + e] = t;
                 else if (feature % p.D == 0) to[N + feature / p.D] = t;
             }
         }
     } else {
         __syncthreads();
-        const float of_head = head_sum<false>(ds.x + ds.y, a.lanes, a.first, buffer);
-        if (a.mine) {
+        float share[kVec + 1];
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) to[a.feature + i] = dw1[i];
-            if (a.feature % p.D == 0) to[N + a.head] = of_head;
+        for (int i = 0; i < kVec; ++i) share[i] = dw1[i];
+        share[kVec] = head_sum<false>(ds.x + ds.y, a.lanes, a.first, buffer);
+        if constexpr (kNarrow) {
+#pragma unroll
+            for (int i = 0; i <= kVec; ++i) {
+                __syncthreads();
+                buffer[threadIdx.x] = share[i];
+                __syncthreads();
+                if (a.mine && a.row == 0)
+                    for (int side = 1; side < rows; ++side) share[i] += buffer[threadIdx.x + side * split.slot];
+            }
+        }
+        if (a.mine && a.row == 0) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) to[a.feature + i] = share[i];
+            if (a.feature % p.D == 0) to[N + a.head] = share[kVec];
         }
     }
 }
@@ -305,25 +341,33 @@ bool rows_aligned(const void* p, int64_t ld, size_t elem) {
     return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)elem % 16 == 0);
 }
 
-// How a row is dealt out: features of 8 per thread, whole heads to a piece, and with `groups` whole groups of 128.
-struct Split {
-    bool warp;
-    int per_piece, pieces, threads;
-};
+// Whole heads to a piece, and with `groups` whole groups of 128. A row of at most half a warp's (a CTA's) threads shares
+// it with others: the shuffles want a power of two of threads to a row of a warp, groups multiples of 16 or such a power.
 Split split(int H, int D, bool groups) {
     const int N = H * D, vecs = N / kVec, head = D / kVec;
-    Split s;
+    auto up = [](int v) {
+        int n = 1;
+        while (n < v) n *= 2;
+        return n;
+    };
+    Split s = {};
     s.warp = power_of_two(D);
     if (s.warp) {
-        s.per_piece = 32;
+        s.vecs = 32;
     } else {
         int unit = head;
         if (groups)
             while (unit % 16 != 0) unit += head;  // at most 31 * 16 = 496
-        s.per_piece = unit * (unit <= 256 ? 256 / unit : 1);
+        s.vecs = unit * (unit <= 256 ? 256 / unit : 1);
     }
-    s.pieces = (vecs + s.per_piece - 1) / s.per_piece;
-    s.threads = s.warp ? 32 * kWarps : (std::min(s.per_piece, vecs) + 31) / 32 * 32;
+    s.pieces = (vecs + s.vecs - 1) / s.vecs;
+    s.threads = s.warp ? 32 * kWarps : (std::min(s.vecs, vecs) + 31) / 32 * 32;
+    const int room = s.warp ? 32 : 256, slot = s.warp || (groups && vecs < 16) ? up(vecs) : groups ? (vecs + 15) / 16 * 16 : vecs;
+    s.rows = 1, s.slot = room;
+    if (2 * slot <= room) {
+        s.rows = room / slot, s.slot = slot, s.vecs = vecs;
+        if (!s.warp) s.threads = (s.rows * slot + 31) / 32 * 32;
+    }
     return s;
 }
 
@@ -331,15 +375,20 @@ template <typename T, int kOut>
 int fwd_launch(const GatedNorm& p, bool aligned, cudaStream_t stream) {
     const Split s = split(p.H, p.D, kOut == SSD_TYPE_E4M3);
     auto go = [&](auto kernel, int64_t rows) {
+        rows *= s.rows;
         const dim3 grid((unsigned)((p.M + rows - 1) / rows), s.pieces);
-        return launch_dependent(kernel, grid, dim3(s.threads), 0, stream, p, s.per_piece) == cudaSuccess ? 1 : SSDC_ERR_CUDA;
+        return launch_dependent(kernel, grid, dim3(s.threads), 0, stream, p, s) == cudaSuccess ? 1 : SSDC_ERR_CUDA;
     };
-    if (!s.warp) return aligned ? go(gated_norm_fwd<T, kOut, false, true, 1>, 1) : go(gated_norm_fwd<T, kOut, false, false, 1>, 1);
+    if (!s.warp) return aligned ? go(gated_norm_fwd<T, kOut, false, true, 1, true>, 1) : go(gated_norm_fwd<T, kOut, false, false, 1, true>, 1);
     // two rows a warp where that leaves every SM its 64 warps twice: more loads on their way, weights read once (35.5 us
     // at 32,768 x 1,024 to 8 bits, 38.0 with one); with fewer rows one leaves no SM without warps
-    const bool two = p.M * s.pieces >= (int64_t)4 * 64 * device_sms();
-    if (two) return aligned ? go(gated_norm_fwd<T, kOut, true, true, 2>, 2 * kWarps) : go(gated_norm_fwd<T, kOut, true, false, 2>, 2 * kWarps);
-    return aligned ? go(gated_norm_fwd<T, kOut, true, true, 1>, kWarps) : go(gated_norm_fwd<T, kOut, true, false, 1>, kWarps);
+    const bool two = p.M * s.pieces >= (int64_t)4 * 64 * device_sms() * s.rows;
+    if (s.rows > 1) {
+        if (two) return aligned ? go(gated_norm_fwd<T, kOut, true, true, 2, true>, 2 * kWarps) : go(gated_norm_fwd<T, kOut, true, false, 2, true>, 2 * kWarps);
+        return aligned ? go(gated_norm_fwd<T, kOut, true, true, 1, true>, kWarps) : go(gated_norm_fwd<T, kOut, true, false, 1, true>, kWarps);
+    }
+    if (two) return aligned ? go(gated_norm_fwd<T, kOut, true, true, 2, false>, 2 * kWarps) : go(gated_norm_fwd<T, kOut, true, false, 2, false>, 2 * kWarps);
+    return aligned ? go(gated_norm_fwd<T, kOut, true, true, 1, false>, kWarps) : go(gated_norm_fwd<T, kOut, true, false, 1, false>, kWarps);
 }
 template <typename T>
 int fwd_launch(const GatedNorm& p, cudaStream_t stream) {
@@ -356,11 +405,12 @@ int bwd_launch(const GatedNorm& p, bool aligned, cudaStream_t stream) {
     const Split s = split(p.H, p.D, false);
     const int parts = gated_norm_bwd_parts(p.M, p.H, p.D);
     auto go = [&](auto kernel) {
-        return launch_dependent(kernel, dim3(s.pieces * parts), dim3(s.threads), 0, stream, p, s.pieces, s.per_piece, parts);
+        return launch_dependent(kernel, dim3(s.pieces * parts), dim3(s.threads), 0, stream, p, s, parts);
     };
     cudaError_t e;
-    if (s.warp) e = aligned ? go(gated_norm_bwd<T, true, true, kSkip>) : go(gated_norm_bwd<T, true, false, kSkip>);
-    else e = aligned ? go(gated_norm_bwd<T, false, true, kSkip>) : go(gated_norm_bwd<T, false, false, kSkip>);
+    if (s.warp && s.rows == 1) e = aligned ? go(gated_norm_bwd<T, true, true, kSkip, false>) : go(gated_norm_bwd<T, true, false, kSkip, false>);
+    else if (s.warp) e = aligned ? go(gated_norm_bwd<T, true, true, kSkip, true>) : go(gated_norm_bwd<T, true, false, kSkip, true>);
+    else e = aligned ? go(gated_norm_bwd<T, false, true, kSkip, true>) : go(gated_norm_bwd<T, false, false, kSkip, true>);
     if (e != cudaSuccess) return SSDC_ERR_CUDA;
     if (p.partial == nullptr) return 1;
     return launch_dependent(gated_norm_dw, dim3((p.H * p.D + p.H + 7) / 8), dim3(256), 0, stream, p, parts) == cudaSuccess ? 2 : SSDC_ERR_CUDA;
@@ -384,7 +434,8 @@ int gated_norm_bwd_parts(int64_t M, int64_t H, int64_t D) {
     const Split s = split((int)H, (int)D, false);
     // as many CTAs as have room at once: three of 256 threads an SM, or two of those that need more registers
     const int64_t want = std::max<int64_t>(1, (s.warp ? 456 : 304) * 256 / ((int64_t)s.threads * s.pieces));
-    return (int)std::min(want, s.warp ? (M + kWarps - 1) / kWarps : M);
+    const int64_t rows = (int64_t)s.rows * (s.warp ? kWarps : 1);
+    return (int)std::min(want, (M + rows - 1) / rows);
 }
 
 int gated_norm_bwd_launch(const GatedNorm& p, cudaStream_t stream) {

@@ -84,6 +84,57 @@ def test_8_bits(shape, dtype, skip):
     assert float((q.double() - ref).norm() / ref.norm().clamp_min(1e-300)) <= 4e-3
 
 
+# narrow rows, which lie side by side in a warp or a CTA: rows that fill the last one, and one more; slots that are
+# wider than a row, groups of 8 bits that end inside a slot, more rows than one round of CTAs
+NARROW = [(64, 1, 64), (65, 1, 64), (33, 2, 8), (100, 1, 24), (257, 3, 16), (19, 1, 72), (86, 1, 24), (41, 5, 24), (35, 1, 128),
+          (50, 1, 136), (51, 3, 40), (200001, 1, 8), (90001, 1, 24), (30001, 3, 32)]
+
+
+@pytest.mark.parametrize("skip", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", NARROW, **ids)
+def test_narrow_rows(shape, dtype, skip):
+    """ds of a single head is one number, the sum of M D terms of either sign, du v: each term has its own roundings, in
+    proportion to itself and independent of the others', so ds is off in proportion to the root of the sum of the terms'
+    squares, however little of them is left."""
+    M, H, D = shape
+    x = make(*shape, dtype, skip, seed=sum(shape))
+    want, grads = reference(x, H)
+    for out in ("bf16", "fp32"):
+        close(block.GatedNorm(M, H, D, dtype, out=out, skip=skip)(x["x"], x["z"], x["w"], x["v"], x["s"]), want, out)
+    got = block.GatedNormBackward(M, H, D, dtype, skip=skip)(x["dy"], x["x"], x["z"], x["w"], x["v"], x["s"])
+    assert sorted(got) == sorted(grads)
+    for n in grads:
+        if n == "ds":
+            terms = float((grads["dx"] * x["v"].double()).norm())
+            assert float((got[n].double() - grads[n]).norm()) <= TOL[torch.float32] * max(terms, float(grads[n].norm()))
+        else:
+            close(got[n], grads[n], n)
+    test_8_bits(shape, dtype, skip)
+
+
+def test_narrow_rows_one_by_one():
+    """A row's results do not depend on those beside it, nor a NaN in one on the others, but for the sums over rows."""
+    for H, D in ((1, 64), (3, 16), (1, 24), (3, 24)):
+        M = 75
+        x = make(M, H, D, "bf16", True, seed=9)
+        one = {n: block.GatedNorm(1, H, D, out=n, skip=True) for n in ("bf16", "fp8")}
+        back1 = block.GatedNormBackward(1, H, D, skip=True)
+        x["x"][10, 3] = float("nan")
+        y = block.GatedNorm(M, H, D, out="bf16", skip=True)(x["x"], x["z"], x["w"], x["v"], x["s"])
+        q, scale = block.GatedNorm(M, H, D, skip=True)(x["x"], x["z"], x["w"], x["v"], x["s"])
+        g = block.GatedNormBackward(M, H, D, skip=True)(x["dy"], x["x"], x["z"], x["w"], x["v"], x["s"])
+        for m in (0, 9, 10, 11, 31, 32, 74):
+            r = {n: x[n][m:m + 1] for n in ("x", "z", "v", "dy")}
+            bits = lambda t: t.contiguous().view(torch.uint8 if t.element_size() == 1 else torch.int16)
+            assert torch.equal(bits(one["bf16"](r["x"], r["z"], x["w"], r["v"], x["s"])), bits(y[m:m + 1]))
+            q1, s1 = one["fp8"](r["x"], r["z"], x["w"], r["v"], x["s"])
+            assert torch.equal(bits(q1), bits(q[m:m + 1])) and torch.equal(s1.view(torch.int32), scale[:, m:m + 1].contiguous().view(torch.int32))
+            g1 = back1(r["dy"], r["x"], r["z"], x["w"], r["v"], x["s"])
+            for n in ("dx", "dz", "dv"):
+                assert torch.equal(bits(g1[n]), bits(g[n][m:m + 1])), (H, D, m, n)
+
+
 def test_no_weights():
     x = make(10, 3, 72, "bf16", False)
     x["w"] = None
